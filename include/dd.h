@@ -17,8 +17,10 @@
  * Extensions of the same step: Quest-style min/max landmarks and coverage
  * budgets for the selection, the step's own tokens as causal tail rows of
  * the attention, a capped LRU residency update of per-(request, KV head) hot
- * pools after a step, and a predictive prefetch of a layer's predicted
- * chunks ahead of its step (each documented at its entry point below).
+ * pools after a step, a predictive prefetch of a layer's predicted chunks
+ * ahead of its step, and beside the step rotary positions, appending rows to
+ * the cache, and a cache held in 4 bits with the gather and the attention
+ * that read it (each documented at its entry point below).
  *
  * Notation: B requests, Hq query heads, Hkv KV heads, G = Hq/Hkv (query head h
  * reads KV head floor(h/G)), d head dimension, L context tokens, cs tokens per
@@ -364,6 +366,147 @@ dd_status dd_update_residency(dd_ctx *ctx, int32_t step, int32_t cap, int32_t sl
                               const int32_t *miss_count, const void *Kst, const void *Vst,
                               int32_t *resident_slot, int32_t *slot_chunk, int32_t *last_used, void *Khot,
                               void *Vhot, int32_t *admitted, dd_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions, appending to the cache, and a cache held in 4 bits
+ *
+ * These calls take a context like every other one.  They run on the current
+ * device, which has to be the context's (DD_ERR_INVALID_ARG otherwise), write
+ * nothing on the host, and may all be captured into a CUDA graph.
+ *
+ * The 4-bit cache.  A row of 128 values is 64 bytes of e2m1 codes (byte i: value
+ * 2i in the low nibble, value 2i+1 in the high nibble) and eight e4m3 scales,
+ * one for each 16 consecutive values: value = code * scale * 2^e, where e is the
+ * exponent of the KV head (k_exp / v_exp, int32 [Hkv] device, |e| <= 64, NULL =
+ * all zero).  The product of code and scale has at most six significant bits, so
+ * every value is exact in bf16 (2^e apart from its range).  Rows are stored in blocks of 16
+ * (16 x 64 bytes of codes, then 16 x 8 bytes of scales: 1152 bytes), a chunk of
+ * cs rows is cs/16 blocks, so a 4-bit pool or staging buffer is uint8
+ * [slots, cs*72] and a 4-bit home cache uint8 [B,Hkv,C,cs*72], K and V apart,
+ * chunk numbers and slots as in bf16.
+ * ------------------------------------------------------------------------- */
+#define DD_KV4_ROW_BYTES 72
+
+typedef enum { DD_KV_BF16 = 0, DD_KV_4BIT = 1 } dd_kv_format;
+
+/* Rotary positions: of each row's first rot_dim values, pair i (i < rot_dim/2)
+ * is turned by the angle position * f_i.  DD_ROPE_HALF pairs values i and i +
+ * rot_dim/2, DD_ROPE_INTERLEAVED values 2i and 2i+1; the other 128 - rot_dim
+ * values pass through.  rot_dim is 32, 64, 96 or 128. */
+typedef enum { DD_ROPE_HALF = 0, DD_ROPE_INTERLEAVED = 1 } dd_rope_layout;
+
+/* Radians per position, f_i = base^(-2i/rot_dim), scaled for long contexts:
+ *   PLAIN          f_i
+ *   LINEAR         f_i / factor
+ *   NTK            f_i of the base  base * factor^(rot_dim/(rot_dim-2))
+ *   BY_PARTS       f_i * (1 - r_i) + f_i / factor * r_i with the ramp r_i = clamp((i - lo)
+ *                  / (hi - lo), 0, 1), lo = max(floor(a(beta_fast)), 0), hi =
+ *                  min(ceil(a(beta_slow)), rot_dim - 1) (hi - lo at least 0.001), a(x) = rot_dim *
+ *                  ln(orig_len / (2 pi x)) / (2 ln base): pairs that turn more than beta_fast
+ *                  times in orig_len positions stay, those below beta_slow are divided
+ *   BY_WAVELENGTH  f_i * s_i + f_i / factor * (1 - s_i) with s_i = clamp((orig_len * f_i /
+ *                  (2 pi) - beta_slow) / (beta_fast - beta_slow), 0, 1)                        */
+typedef enum {
+  DD_ROPE_PLAIN = 0,
+  DD_ROPE_LINEAR = 1,
+  DD_ROPE_NTK = 2,
+  DD_ROPE_BY_PARTS = 3,
+  DD_ROPE_BY_WAVELENGTH = 4
+} dd_rope_scaling;
+
+typedef struct {
+  int32_t rot_dim;
+  dd_rope_scaling scaling;
+  double base;                    /* > 1 */
+  double factor;                  /* >= 1 (not used by PLAIN) */
+  double orig_len;                /* > 0, the BY_ scalings only */
+  double beta_fast, beta_slow;    /* beta_fast > beta_slow > 0, the BY_ scalings only */
+  double gain;                    /* factor on the rotated values; <= 0: 0.1 ln(factor) + 1 for BY_PARTS, else 1 */
+} dd_rope_params;
+
+/* Fill `table` (host memory, DD_ROPE_TABLE_BYTES) with what the calls below read
+ * from device memory: each pair's frequency as a 64-bit fraction of a turn, so
+ * that position * frequency is exact modulo one turn at any position, and 512
+ * sines and cosines to 48 bits.  Host only: no device call. */
+#define DD_ROPE_TABLE_BYTES 8704
+dd_status dd_rope_table(const dd_rope_params *params, void *table);
+
+typedef struct {
+  const void *table;       /* device copy of dd_rope_table's output, 16-byte aligned */
+  int32_t rot_dim;         /* as in its dd_rope_params */
+  dd_rope_layout layout;
+} dd_rope;
+
+/* Rotate rows: x bf16 [B,T,H,128] and out (may be x), each with the strides (in
+ * elements, multiples of 8; the last dimension dense) of request, token and head.
+ * Row t of request b has position start_pos[b] + t, start_pos int32 [B] device,
+ * positions >= 0; new_len int32 [B] device or NULL (= T): rows t >= new_len[b]
+ * are padding and neither read nor written.  B is the context's; T and H are this
+ * call's.  Each output is the exact rotation of its pair, taken to about 2^-36 of the
+ * larger of the two values, rounded once to bf16. */
+dd_status dd_rope_rows(dd_ctx *ctx, const dd_rope *rope, const void *x, const int64_t x_stride[3], void *out,
+                       const int64_t out_stride[3], int32_t T, int32_t H, const int32_t *start_pos,
+                       const int32_t *new_len, dd_stream_t stream);
+
+/* Append keys and values to the cache, the keys rotated on the way.  Row t <
+ * new_len[b] of request b goes to position start_pos[b] + t of its KV heads, i.e.
+ * to row pos mod cs of chunk pos / cs:
+ *   - of the home cache Kh/Vh (bf16 [B,Hkv,L,128] or 4-bit [B,Hkv,C,cs*72], pinned
+ *     host or device; both NULL: not written), and
+ *   - of the chunk's resident copy in Khot/Vhot (bf16 [hot_slots,cs,128] or 4-bit
+ *     [hot_slots,cs*72]; both NULL: not written) where resident_slot (int32
+ *     [B,Hkv,C]) is not -1.
+ * k, v: bf16 [B,T,Hkv,128] with strides as in dd_rope_rows.  Every other row keeps
+ * its bytes.  A position outside [0, L), a length outside [0, T] or a slot outside
+ * [-1, hot_slots) sets DD_ERR_DEVICE_CHECK and its rows are left out.  Two resident
+ * chunks must not share a slot.
+ * 4 bits: a rotated key is rounded to bf16 first (so a cache of either format is
+ * built from the same keys), the values of a head are divided by 2^e, a group's
+ * scale is the e4m3 number nearest to its largest magnitude / 6 (at most 448) and
+ * a code the e2m1 number nearest to value / scale, ties to even in both, beyond
+ * +-6 the largest code.  An infinite value gives the largest value there is, a NaN
+ * makes its group of 16 NaN. */
+typedef struct {
+  const void *k, *v;
+  int64_t k_stride[3], v_stride[3];
+  int32_t T;
+  dd_kv_format format;
+  const int32_t *start_pos, *new_len;   /* int32 [B] device; new_len NULL: T */
+  const dd_rope *rope;                  /* NULL: keys as they are */
+  void *Kh, *Vh;
+  void *Khot, *Vhot;
+  const int32_t *resident_slot;
+  const int32_t *k_exp, *v_exp;         /* 4 bits only */
+} dd_append_args;
+
+dd_status dd_append_kv(dd_ctx *ctx, const dd_append_args *args, dd_stream_t stream);
+
+/* dd_gather_kv for a 4-bit home cache Kh/Vh (pinned host, or device), by a kernel
+ * that loads over the host link.  expand = 0: chunk m of the list is copied as it
+ * is into staging slot m of Kst/Vst, uint8 [max_misses,cs*72].  expand != 0: it is
+ * written as bf16 values, Kst/Vst bf16 [max_misses,cs,128], for the calls that take
+ * bf16 chunks (a value below bf16's normal range rounds). */
+dd_status dd_gather_kv4(dd_ctx *ctx, const void *Kh, const void *Vh, const int32_t *miss_list,
+                        const int32_t *miss_count, void *Kst, void *Vst, int32_t expand, const int32_t *k_exp,
+                        const int32_t *v_exp, dd_stream_t stream);
+
+/* dd_sparse_attn_decode over 4-bit pages: Khot/Vhot uint8 [hot_slots,cs*72], Kst/Vst
+ * uint8 [max_misses,cs*72], tails in bf16.  What is more:
+ *   union_qmask  may be NULL: every query attends to every chunk of the union;
+ *   miss_count   may be NULL: every staging slot below max_misses is filled;
+ *   kv_len       int32 [B] device or NULL: rows at positions >= kv_len[b] are left
+ *                out, whatever they hold (a chunk that is not full yet, chunks behind
+ *                the end).  The position of row t of union chunk i is
+ *                union_idx[b,g,i]*cs + t; union_idx int32 [B,Hkv,Umax] as written by
+ *                dd_resolve_union, needed with kv_len.
+ * Attention over a whole cache: k = C, union_cnt = the chunks in use, union_idx =
+ * 0, 1, ..., union_slot = their pages.  A query without a row gets zeros. */
+dd_status dd_sparse_attn_decode_kv4(dd_ctx *ctx, const void *q, const void *Khot, const void *Vhot,
+                                    const void *Kst, const void *Vst, const int32_t *k_exp, const int32_t *v_exp,
+                                    const void *K_tail, const void *V_tail, const int32_t *union_idx,
+                                    const int32_t *union_slot, const uint8_t *union_qmask,
+                                    const int32_t *union_cnt, const int32_t *miss_count, const int32_t *kv_len,
+                                    float softmax_scale, float *out, dd_stream_t stream);
 
 /* Diagnostics for failure detection: runs one of the library's bounded
  * device waits on something that nothing will ever signal -- kind 0: an

@@ -25,4 +25,5 @@ Every function is pinned by the tests in ``tests/test_oracle_pins.py``
 against closed forms, library routines for special cases, brute force on
 tiny inputs and the worked numbers printed on the pages.
 """
+from .kv_cache import *  # noqa: F401,F403
 from .sparse_kv import *  # noqa: F401,F403

@@ -649,4 +649,106 @@ dd_status dd_step(dd_ctx *c, const dd_step_args *a, dd_stream_t stream) {
   return DD_OK;
 }
 
+// ------------------------------------------------ rotary positions, appends, 4-bit cache
+
+// The calls below run on the current device: it has to be the context's.
+static dd_status on_device(const dd_ctx *c) {
+  int dev = -1;
+  DD_CUDA(cudaGetDevice(&dev));
+  return dev == c->device ? DD_OK : DD_ERR_INVALID_ARG;
+}
+
+static bool rope_ok(const dd_rope *r) {
+  return r && r->table && aligned16(r->table) && r->rot_dim >= 32 && r->rot_dim <= kD && r->rot_dim % 32 == 0 &&
+         (r->layout == DD_ROPE_HALF || r->layout == DD_ROPE_INTERLEAVED);
+}
+
+// rows of 128 bf16 read in 16-byte pieces
+static bool rows_ok(const void *p, const int64_t *stride) {
+  return p && stride && aligned16(p) && stride[0] % 8 == 0 && stride[1] % 8 == 0 && stride[2] % 8 == 0;
+}
+
+dd_status dd_rope_rows(dd_ctx *c, const dd_rope *rope, const void *x, const int64_t x_stride[3], void *out,
+                       const int64_t out_stride[3], int32_t T, int32_t H, const int32_t *start_pos,
+                       const int32_t *new_len, dd_stream_t stream) {
+  if (!c || T < 0 || H < 0 || H > 65535) return DD_ERR_INVALID_ARG;
+  if (c->dims.B == 0 || T == 0 || H == 0) return DD_OK;
+  if (!rope_ok(rope) || !rows_ok(x, x_stride) || !rows_ok(out, out_stride) || !start_pos) return DD_ERR_INVALID_ARG;
+  DD_TRY(on_device(c));
+  c->launches += 1;
+  return cuda_ok(dd::launch_rope_rows(rope, x, x_stride, out, out_stride, c->dims.B, T, H, start_pos, new_len,
+                                      c->sm_count, c->status, (cudaStream_t)stream));
+}
+
+dd_status dd_append_kv(dd_ctx *c, const dd_append_args *a, dd_stream_t stream) {
+  if (!c || !a || a->T < 0 || c->dims.Hkv > 65535) return DD_ERR_INVALID_ARG;
+  if (a->format != DD_KV_BF16 && a->format != DD_KV_4BIT) return DD_ERR_INVALID_ARG;
+  if (c->units == 0 || a->T == 0) return DD_OK;
+  if (!rows_ok(a->k, a->k_stride) || !rows_ok(a->v, a->v_stride) || !a->start_pos) return DD_ERR_INVALID_ARG;
+  if (a->rope && !rope_ok(a->rope)) return DD_ERR_INVALID_ARG;
+  if ((a->Kh == nullptr) != (a->Vh == nullptr) || (a->Khot == nullptr) != (a->Vhot == nullptr))
+    return DD_ERR_INVALID_ARG;
+  if (!a->Kh && !a->Khot) return DD_ERR_INVALID_ARG;
+  if (a->Khot && (!a->resident_slot || !aligned16(a->Khot) || !aligned16(a->Vhot))) return DD_ERR_INVALID_ARG;
+  if (a->format == DD_KV_BF16 && (a->k_exp || a->v_exp)) return DD_ERR_INVALID_ARG;
+  DD_TRY(on_device(c));
+  const void *kd = nullptr, *vd = nullptr;
+  if (a->Kh) {
+    if (!aligned16(a->Kh) || !aligned16(a->Vh)) return DD_ERR_INVALID_ARG;
+    DD_TRY(host_kv_views(c, a->Kh, a->Vh, &kd, &vd));
+  }
+  c->launches += 1;
+  return cuda_ok(dd::launch_append(a, const_cast<void *>(kd), const_cast<void *>(vd), c->dims.B, c->dims.Hkv, c->C,
+                                   c->dims.cs, c->hot_slots, c->sm_count, c->status, (cudaStream_t)stream));
+}
+
+dd_status dd_gather_kv4(dd_ctx *c, const void *Kh, const void *Vh, const int32_t *miss_list,
+                        const int32_t *miss_count, void *Kst, void *Vst, int32_t expand, const int32_t *k_exp,
+                        const int32_t *v_exp, dd_stream_t stream) {
+  if (!c || (!expand && (k_exp || v_exp))) return DD_ERR_INVALID_ARG;
+  if (c->units == 0) return DD_OK;
+  if (!Kh || !Vh || !miss_list || !miss_count || !aligned16(Kh) || !aligned16(Vh)) return DD_ERR_INVALID_ARG;
+  if (c->max_misses > 0 && (!Kst || !Vst || !aligned16(Kst) || !aligned16(Vst))) return DD_ERR_INVALID_ARG;
+  if (c->max_misses == 0) return DD_OK;
+  DD_TRY(on_device(c));
+  const void *kd, *vd;
+  DD_TRY(host_kv_views(c, Kh, Vh, &kd, &vd));
+  c->launches += 1;
+  return cuda_ok(dd::launch_gather4(static_cast<const uint8_t *>(kd), static_cast<const uint8_t *>(vd), miss_list,
+                                    miss_count, Kst, Vst, expand != 0, k_exp, v_exp, c->max_misses, c->units,
+                                    c->dims.Hkv, c->C, c->dims.cs, c->status, c->sm_count, (cudaStream_t)stream));
+}
+
+dd_status dd_sparse_attn_decode_kv4(dd_ctx *c, const void *q, const void *Khot, const void *Vhot, const void *Kst,
+                                    const void *Vst, const int32_t *k_exp, const int32_t *v_exp, const void *K_tail,
+                                    const void *V_tail, const int32_t *union_idx, const int32_t *union_slot,
+                                    const uint8_t *union_qmask, const int32_t *union_cnt, const int32_t *miss_count,
+                                    const int32_t *kv_len, float softmax_scale, float *out, dd_stream_t stream) {
+  if (!c) return DD_ERR_INVALID_ARG;
+  if (c->units == 0) return DD_OK;
+  if ((K_tail == nullptr) != (V_tail == nullptr) || (kv_len && !union_idx)) return DD_ERR_INVALID_ARG;
+  if (K_tail && (!aligned16(K_tail) || !aligned16(V_tail))) return DD_ERR_INVALID_ARG;
+  if (!q || !union_slot || !union_cnt || !out || !aligned16(q) || !aligned16(out)) return DD_ERR_INVALID_ARG;
+  if (c->hot_slots > 0 && (!Khot || !Vhot || !aligned16(Khot) || !aligned16(Vhot))) return DD_ERR_INVALID_ARG;
+  if (c->max_misses > 0 && (!Kst || !Vst || !aligned16(Kst) || !aligned16(Vst))) return DD_ERR_INVALID_ARG;
+  DD_TRY(on_device(c));
+  const dd_dims &d = c->dims;
+  dd::Attn4Args a{};
+  a.q = q;
+  a.Khot = static_cast<const uint8_t *>(Khot), a.Vhot = static_cast<const uint8_t *>(Vhot);
+  a.Kst = static_cast<const uint8_t *>(Kst), a.Vst = static_cast<const uint8_t *>(Vst);
+  a.k_exp = k_exp, a.v_exp = v_exp;
+  a.k_tail = K_tail, a.v_tail = V_tail;
+  a.union_idx = union_idx, a.union_slot = union_slot, a.union_qmask = union_qmask, a.union_cnt = union_cnt;
+  a.miss_count = miss_count, a.kv_len = kv_len;
+  a.softmax_scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kD);
+  a.out = out;
+  a.B = d.B, a.n_q = d.n_q, a.Hq = d.Hq, a.Hkv = d.Hkv, a.cs = d.cs, a.umax = c->umax;
+  a.hot_slots = c->hot_slots, a.max_misses = c->max_misses;
+  a.status = c->status;
+  a.sm_count = c->sm_count;
+  c->launches += 1;
+  return cuda_ok(dd::launch_attn4(a, (cudaStream_t)stream));
+}
+
 }  // extern "C"

@@ -379,4 +379,30 @@ cudaError_t launch_gather(const uint4 *Kh, const uint4 *Vh, const int32_t *miss_
                           const int32_t *miss_count, uint4 *Kst, uint4 *Vst, int64_t max_misses,
                           int64_t n_chunks_total, int cs, int32_t *status, int sm_count, cudaStream_t s,
                           int32_t *map_out = nullptr, int ctas_per_sm = 8);
+cudaError_t launch_gather4(const uint8_t *Kh, const uint8_t *Vh, const int32_t *miss_list, const int32_t *miss_count,
+                           void *Kst, void *Vst, bool expand, const int32_t *k_exp, const int32_t *v_exp,
+                           int64_t max_misses, int units, int Hkv, int C, int cs, int32_t *status, int sm_count,
+                           cudaStream_t s);
+cudaError_t launch_rope_rows(const dd_rope *r, const void *x, const int64_t *xs, void *out, const int64_t *os, int B,
+                             int T, int H, const int32_t *start_pos, const int32_t *new_len, int sm_count,
+                             int32_t *status, cudaStream_t s);
+cudaError_t launch_append(const dd_append_args *a, void *kh_dev, void *vh_dev, int B, int Hkv, int C, int cs,
+                          int64_t hot_slots, int sm_count, int32_t *status, cudaStream_t s);
+// attention over 4-bit pages (dd_attn4.cu)
+struct Attn4Args {
+  const void *q;
+  const uint8_t *Khot, *Vhot, *Kst, *Vst;
+  const int32_t *k_exp, *v_exp;
+  const void *k_tail, *v_tail;
+  const int32_t *union_idx, *union_slot;
+  const uint8_t *union_qmask;
+  const int32_t *union_cnt, *miss_count, *kv_len;
+  float softmax_scale;
+  float *out;
+  int B, n_q, Hq, Hkv, cs, umax;
+  int64_t hot_slots, max_misses;
+  int32_t *status;
+  int sm_count;
+};
+cudaError_t launch_attn4(const Attn4Args &a, cudaStream_t s);
 }  // namespace dd

@@ -1,0 +1,89 @@
+// The 4-bit cache format shared by the append, the gather and the attention:
+// blocks of 16 rows, 16 x 64 bytes of e2m1 codes then 16 x 8 e4m3 scales.
+//
+// e2m1 has two significant bits and e4m3 four, so code * scale has at most six:
+// exact in bf16 and in fp16 (2^-10 .. 2688), which lets the attention feed the
+// matrix instructions with 16-bit operands without rounding what is stored.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "dd_common.cuh"
+
+namespace dd {
+
+constexpr int kRow4 = DD_KV4_ROW_BYTES;
+constexpr int kBlk4 = 16 * kRow4;         // bytes of a block of 16 rows
+constexpr int kBlk4Scales = 16 * 64;      // offset of its scales
+constexpr int kMaxExp4 = 64;              // |e| of a head's 2^e
+
+// 2^e for |e| <= 126, from the exponent's bits
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// The head's exponent, checked: one outside +-64 is reported and clamped.
+__device__ __forceinline__ int head_exp(const int32_t *exps, int g, int32_t *status) {
+  if (!exps) return 0;
+  const int e = exps[g];
+  if (e < -kMaxExp4 || e > kMaxExp4) {
+    set_status(status, DD_ERR_DEVICE_CHECK);
+    return e < 0 ? -kMaxExp4 : kMaxExp4;
+  }
+  return e;
+}
+
+// four bytes of codes -> four half2 (byte i: low nibble in .x, high nibble in .y)
+__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// two e4m3 scales (bytes of s) -> half2
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t s) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)s));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// e4m3 nearest to amax / 6, at most 448 (0x7F, NaN, for a NaN group)
+__device__ __forceinline__ uint32_t group_scale(float amax, bool nan) {
+  uint16_t s;
+  const float v = __fdiv_rn(amax, 6.f);   // a tie of e4m3 times 6 is representable: the quotient of one is exact
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(0.f), "f"(v));
+  return nan ? 0x7Fu : (uint32_t)(s & 0xFF);
+}
+
+// 1 / scale for the encoder (0 for a zero scale: all codes zero)
+__device__ __forceinline__ float scale_inverse(uint32_t s8) {
+  const float s = __half2float(__ushort_as_half((uint16_t)(e4m3x2_to_half2(s8) & 0xFFFFu)));
+  return s > 0.f ? __frcp_rn(s) : 0.f;
+}
+
+// Eight values (bf16 values times a power of two) -> four bytes of codes.
+// value * (1/scale) is within 2^-23 of the quotient.  The quotient of two
+// numbers of 8 and 4 significant bits is either one of e2m1's ties (at most
+// three significant bits) or at least 2^-9 of it away, so rounding the product
+// to 16 significant bits first puts every tie back in its place.
+__device__ __forceinline__ uint32_t encode8(const float (&x)[8], float inv) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = __uint_as_float((__float_as_uint(x[i] * inv) + 0x80u) & ~0xFFu);
+  uint32_t r;
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n mov.b32 %0, {b0, b1, b2, b3};\n}\n"
+      : "=r"(r)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return r;
+}
+
+}  // namespace dd

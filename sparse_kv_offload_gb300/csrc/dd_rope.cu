@@ -1,0 +1,434 @@
+// Rotary positions, and appending rows to the cache with the rotation on the way.
+//
+// The cache is read back by every later step and, in 4 bits, rounded again, so
+// the rotation is made independent of how it is computed: the result is the
+// bf16 nearest to the exact rotation.  fp32 alone is off where it matters: the
+// angle of position 10^5 loses 17 of its 24 bits, and a product rounded to fp32
+// falls on the other side of a bf16 tie once in some ten thousand values.  So
+//   - a frequency is a 64-bit fraction of a turn: position * frequency wraps
+//     modulo a turn by itself, exactly, at any position;
+//   - sine and cosine come from 512 stored angles (hi + lo floats) and the angle
+//     sum formulas with the remainder |r| <= pi/512, whose series end after
+//     r^5 and r^4;
+//   - products and sums keep their rounding errors (fma, two-sum), and the last
+//     rounding sees them as a sticky bit.
+//
+// A row is 8 lanes x 16 values: lane i turns pairs 8i..8i+7 (two 16-byte pieces
+// of the row), so a token's sines and cosines are computed once per lane and
+// serve all the heads that the warp goes through.  Bound by HBM.
+#include <math.h>
+
+#include "dd_kv4.cuh"
+
+namespace dd {
+
+namespace {
+
+constexpr int kRopeThreads = 128;
+constexpr int kLut = 512;               // stored angles of a turn
+constexpr int kLutOff = 64 * 8;         // table: 64 frequencies, then the stored angles
+
+struct Rope {
+  const uint64_t *freq;                 // turns per position * 2^64
+  const float4 *lut;                    // {cos hi, sin hi, cos lo, sin lo} * gain
+  int rot_dim;                          // 0: no rotation
+  bool half;
+};
+
+// The eight pairs' cosines and sines at one position, hi + lo.
+struct Turn {
+  float ch[8], cl[8], sh[8], sl[8];
+};
+
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
+  s = a + b;
+  const float t = s - a;
+  e = (a - (s - t)) + (b - t);
+}
+
+// gain * (cos, sin) of phase / 2^64 turns
+__device__ __forceinline__ void cos_sin(uint64_t phase, const float4 *lut, float &ch, float &cl, float &sh,
+                                        float &sl) {
+  const uint32_t idx = (uint32_t)((phase + (1ull << 54)) >> 55);        // nearest stored angle, 0..512
+  const int32_t rem = (int32_t)((int64_t)(phase - ((uint64_t)idx << 55)) >> 23);   // |rem| <= 2^31 - 1: units of 2^-41 turns
+  const float rf = (float)rem;
+  const float rr = (float)(rem - (int32_t)rf);
+  // 2 pi * 2^-41 in two floats
+  constexpr double kStep = 6.283185307179586476925286766559 / 2199023255552.0;
+  constexpr float kHi = (float)kStep, kLo = (float)(kStep - (double)kHi);
+  const float d = rf * kHi;
+  const float dl = fmaf(rf, kHi, -d) + fmaf(rf, kLo, rr * kHi);
+  const float d2 = d * d;
+  const float t = fmaf(d * d2, fmaf(d2, 1.f / 120.f, -1.f / 6.f), dl);     // sin r - d
+  const float u = fmaf(d2 * d2, 1.f / 24.f, fmaf(d2, -0.5f, -d * dl));     // cos r - 1
+  const float4 a = __ldg(lut + (idx & (kLut - 1)));
+  {
+    const float p = a.x * d, e = fmaf(a.x, d, -p);
+    const float q = fmaf(a.y, u, fmaf(a.x, t, fmaf(a.z, d, e))) + a.w;
+    float s, r;
+    two_sum(a.y, p, s, r);
+    r += q;
+    sh = s + r;
+    sl = r - (sh - s);
+  }
+  {
+    const float p = -a.y * d, e = fmaf(-a.y, d, -p);
+    const float q = fmaf(a.x, u, fmaf(-a.y, t, fmaf(-a.w, d, e))) + a.z;
+    float s, r;
+    two_sum(a.x, p, s, r);
+    r += q;
+    ch = s + r;
+    cl = r - (ch - s);
+  }
+}
+
+// bf16 bits of x1 * (ch + cl) + x2 * (sh + sl), x1 and x2 bf16 values: one rounding
+__device__ __forceinline__ uint32_t dot2_bf16(float x1, float ch, float cl, float x2, float sh, float sl) {
+  const float a = x1 * ch, b = x2 * sh;
+  float s, e;
+  two_sum(a, b, s, e);
+  e += (fmaf(x1, ch, -a) + fmaf(x2, sh, -b)) + fmaf(x1, cl, x2 * sl);
+  const float hi = s + e, rest = e - (hi - s);
+  uint32_t w = __float_as_uint(hi);
+  if (!(fabsf(hi) < INFINITY)) {
+    w = __float_as_uint(a + b);     // infinities and NaN: the error terms say nothing
+  } else if (rest != 0.f) {
+    w -= (rest < 0.f) != (hi < 0.f);    // truncate towards zero, ...
+    w |= 1u;                            // ... sticky
+  }
+  return f2bf(__uint_as_float(w));
+}
+
+// The two 16-byte pieces (0..15) of a row that lane i (0..7) holds: with halves
+// paired the pieces i and i + rot_dim/16 of a lane that turns, else 2i, 2i + 1.
+__device__ __forceinline__ void pieces(const Rope &r, int i, bool rotated, int &pa, int &pb) {
+  const bool apart = rotated && r.half && i < r.rot_dim / 16;
+  pa = apart ? i : 2 * i;
+  pb = apart ? i + r.rot_dim / 16 : 2 * i + 1;
+}
+
+__device__ __forceinline__ void make_turn(const Rope &r, int i, int64_t pos, Turn &t) {
+  if (i >= r.rot_dim / 16) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) cos_sin((uint64_t)pos * __ldg(r.freq + 8 * i + e), r.lut, t.ch[e], t.cl[e], t.sh[e], t.sl[e]);
+}
+
+// Rotate the lane's two pieces in place.
+__device__ __forceinline__ void rotate(const Rope &r, int i, const Turn &t, uint4 &va, uint4 &vb) {
+  if (i >= r.rot_dim / 16) return;
+  float a[8], b[8];
+  unpack8(va, a);
+  unpack8(vb, b);
+  uint32_t oa[8], ob[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // interleaved: pairs 0..3 lie in a, 4..7 in b
+    const float x = r.half ? a[e] : (e < 4 ? a[2 * (e & 3)] : b[2 * (e & 3)]);
+    const float y = r.half ? b[e] : (e < 4 ? a[2 * (e & 3) + 1] : b[2 * (e & 3) + 1]);
+    oa[e] = dot2_bf16(x, t.ch[e], t.cl[e], -y, t.sh[e], t.sl[e]);
+    ob[e] = dot2_bf16(y, t.ch[e], t.cl[e], x, t.sh[e], t.sl[e]);
+  }
+  if (r.half) {
+    va = make_uint4(oa[0] | oa[1] << 16, oa[2] | oa[3] << 16, oa[4] | oa[5] << 16, oa[6] | oa[7] << 16);
+    vb = make_uint4(ob[0] | ob[1] << 16, ob[2] | ob[3] << 16, ob[4] | ob[5] << 16, ob[6] | ob[7] << 16);
+  } else {
+    va = make_uint4(oa[0] | ob[0] << 16, oa[1] | ob[1] << 16, oa[2] | ob[2] << 16, oa[3] | ob[3] << 16);
+    vb = make_uint4(oa[4] | ob[4] << 16, oa[5] | ob[5] << 16, oa[6] | ob[6] << 16, oa[7] | ob[7] << 16);
+  }
+}
+
+struct Rows {          // where the rows of a call lie, in elements
+  int64_t b, t, h;
+};
+
+// The new rows' token of a lane's row group: its request, row and position.
+struct Token {
+  bool ok;
+  int b;
+  int64_t t, pos;
+};
+
+__device__ __forceinline__ Token token_of(int64_t n, int B, int T, const int32_t *start_pos, const int32_t *new_len,
+                                          int64_t L, int32_t *status) {
+  Token k;
+  k.ok = n < (int64_t)B * T;
+  k.b = k.ok ? (int)(n / T) : 0;
+  k.t = k.ok ? n - (int64_t)k.b * T : 0;
+  const int len = new_len ? new_len[k.b] : T;
+  k.pos = (int64_t)start_pos[k.b] + k.t;
+  if (k.ok && (len < 0 || len > T)) {
+    set_status(status, DD_ERR_DEVICE_CHECK);
+    k.ok = false;
+  }
+  k.ok = k.ok && k.t < len;
+  if (k.ok && (start_pos[k.b] < 0 || k.pos >= L)) {
+    set_status(status, DD_ERR_DEVICE_CHECK);
+    k.ok = false;
+  }
+  return k;
+}
+
+__global__ void __launch_bounds__(kRopeThreads) k_rope_rows(Rope r, const uint16_t *__restrict__ x, Rows xs,
+                                                            uint16_t *out, Rows os, int B, int T, int H, int heads,
+                                                            const int32_t *__restrict__ start_pos,
+                                                            const int32_t *__restrict__ new_len, int32_t *status) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = threadIdx.x & 7;
+  const Token k = token_of(((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 3, B, T, start_pos, new_len,
+                           INT64_MAX, status);
+  if (!k.ok) return;
+  Turn t;
+  make_turn(r, i, k.pos, t);
+  int pa, pb;
+  pieces(r, i, true, pa, pb);
+  const int h1 = min(H, (int)(blockIdx.y + 1) * heads);
+  for (int h = blockIdx.y * heads; h < h1; ++h) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(x + k.b * xs.b + k.t * xs.t + h * xs.h);
+    uint4 *dst = reinterpret_cast<uint4 *>(out + k.b * os.b + k.t * os.t + h * os.h);
+    uint4 va = src[pa], vb = src[pb];
+    rotate(r, i, t, va, vb);
+    dst[pa] = va;
+    dst[pb] = vb;
+  }
+}
+
+struct AppendP {
+  Rope r;
+  const uint16_t *k, *v;
+  Rows ks, vs;
+  int B, T, H, heads, C, cs, shift;       // cs = 1 << shift
+  const int32_t *start_pos, *new_len;
+  uint8_t *Kh, *Vh, *Khot, *Vhot;
+  const int32_t *slot;
+  int64_t hot_slots;
+  const int32_t *k_exp, *v_exp;
+  int32_t *status;
+};
+
+// codes and scales of the lane's two pieces into row `row` of the page
+__device__ __forceinline__ void store4(uint8_t *page, int row, int pa, int pb, int i, bool apart, uint32_t ca,
+                                       uint32_t cb, uint32_t sa, uint32_t sb) {
+  uint8_t *blk = page + (row >> 4) * kBlk4;
+  uint8_t *codes = blk + (row & 15) * 64;
+  uint8_t *scales = blk + kBlk4Scales + (row & 15) * 8;
+  *reinterpret_cast<uint32_t *>(codes + pa * 4) = ca;
+  *reinterpret_cast<uint32_t *>(codes + pb * 4) = cb;
+  if (!apart) {
+    scales[i] = (uint8_t)sa;
+  } else if ((i & 1) == 0) {   // lanes i, i + 1 hold the halves of groups pa/2 and pb/2
+    scales[pa >> 1] = (uint8_t)sa;
+    scales[pb >> 1] = (uint8_t)sb;
+  }
+}
+
+__device__ __forceinline__ float group_max(const float (&x)[8], bool &nan) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    m = fmaxf(m, fabsf(x[e]));
+    nan = nan || x[e] != x[e];
+  }
+  return m;
+}
+
+// Quantise the lane's two pieces.  `apart`: the other half of each piece's group of 16
+// is the neighbour lane's, else the two pieces are one group.  Every lane of the
+// eight takes part.
+__device__ __forceinline__ void quantise(const uint4 &va, const uint4 &vb, float mul, bool apart, unsigned lanes,
+                                         uint32_t &ca, uint32_t &cb, uint32_t &sa, uint32_t &sb) {
+  float a[8], b[8];
+  unpack8(va, a);
+  unpack8(vb, b);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) a[e] *= mul, b[e] *= mul;
+  bool na = false, nb = false;
+  const float ma = group_max(a, na), mb = group_max(b, nb);
+  // a NaN travels through the maxima as a NaN
+  const float qa = na ? NAN : ma, qb = nb ? NAN : mb;
+  const float oa = __shfl_xor_sync(lanes, qa, 1), ob = __shfl_xor_sync(lanes, qb, 1);
+  const float xa = apart ? oa : qb, xb = apart ? ob : qa;
+  sa = group_scale(fmaxf(qa, xa), qa != qa || xa != xa);
+  sb = group_scale(fmaxf(qb, xb), qb != qb || xb != xb);
+  ca = encode8(a, scale_inverse(sa));
+  cb = encode8(b, scale_inverse(sb));
+}
+
+template <bool kFour>
+__global__ void __launch_bounds__(kRopeThreads) k_append(AppendP p) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = threadIdx.x & 7;
+  const unsigned lanes = 0xFFu << (threadIdx.x & 24);      // the eight lanes of this row
+  const Token k = token_of(((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 3, p.B, p.T, p.start_pos, p.new_len,
+                           (int64_t)p.C << p.shift, p.status);
+  if (!k.ok) return;
+  Turn t;
+  make_turn(p.r, i, k.pos, t);
+  int pa, pb;
+  pieces(p.r, i, true, pa, pb);
+  const bool apart = pb != pa + 1;
+  const int c = (int)(k.pos >> p.shift), row = (int)(k.pos & (p.cs - 1));
+  const int64_t page_bytes = (int64_t)p.cs * (kFour ? kRow4 : 2 * kD);
+  const int h1 = min(p.H, (int)(blockIdx.y + 1) * p.heads);
+  for (int h = blockIdx.y * p.heads; h < h1; ++h) {
+    const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k + k.b * p.ks.b + k.t * p.ks.t + h * p.ks.h);
+    const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v + k.b * p.vs.b + k.t * p.vs.t + h * p.vs.h);
+    uint4 ka = ksrc[pa], kb = ksrc[pb];
+    const uint4 va = vsrc[2 * i], vb = vsrc[2 * i + 1];
+    const int64_t chunk = ((int64_t)k.b * p.H + h) * p.C + c;
+    int64_t slot = -1;
+    if (p.Khot) {
+      slot = p.slot[chunk];
+      if (slot < -1 || slot >= p.hot_slots) {
+        set_status(p.status, DD_ERR_DEVICE_CHECK);
+        slot = -1;
+      }
+    }
+    rotate(p.r, i, t, ka, kb);
+    if (kFour) {
+      uint32_t kca, kcb, ksa, ksb, vca, vcb, vsa, vsb;
+      quantise(ka, kb, pow2i(-head_exp(p.k_exp, h, p.status)), apart, lanes, kca, kcb, ksa, ksb);
+      quantise(va, vb, pow2i(-head_exp(p.v_exp, h, p.status)), false, lanes, vca, vcb, vsa, vsb);
+      if (p.Kh) {
+        store4(p.Kh + chunk * page_bytes, row, pa, pb, i, apart, kca, kcb, ksa, ksb);
+        store4(p.Vh + chunk * page_bytes, row, 2 * i, 2 * i + 1, i, false, vca, vcb, vsa, vsb);
+      }
+      if (slot >= 0) {
+        store4(p.Khot + slot * page_bytes, row, pa, pb, i, apart, kca, kcb, ksa, ksb);
+        store4(p.Vhot + slot * page_bytes, row, 2 * i, 2 * i + 1, i, false, vca, vcb, vsa, vsb);
+      }
+    } else {
+      if (p.Kh) {
+        uint4 *kd = reinterpret_cast<uint4 *>(p.Kh + chunk * page_bytes + row * 2 * kD);
+        uint4 *vd = reinterpret_cast<uint4 *>(p.Vh + chunk * page_bytes + row * 2 * kD);
+        kd[pa] = ka, kd[pb] = kb;
+        vd[2 * i] = va, vd[2 * i + 1] = vb;
+      }
+      if (slot >= 0) {
+        uint4 *kd = reinterpret_cast<uint4 *>(p.Khot + slot * page_bytes + row * 2 * kD);
+        uint4 *vd = reinterpret_cast<uint4 *>(p.Vhot + slot * page_bytes + row * 2 * kD);
+        kd[pa] = ka, kd[pb] = kb;
+        vd[2 * i] = va, vd[2 * i + 1] = vb;
+      }
+    }
+  }
+}
+
+Rope rope_of(const dd_rope *r) {
+  Rope k{};
+  if (r) {
+    k.freq = static_cast<const uint64_t *>(r->table);
+    k.lut = reinterpret_cast<const float4 *>(static_cast<const uint8_t *>(r->table) + kLutOff);
+    k.rot_dim = r->rot_dim;
+    k.half = r->layout == DD_ROPE_HALF;
+  }
+  return k;
+}
+
+// Heads per warp: all of them while the tokens alone give every SM its 16 warps of
+// 4 tokens, else as few as it takes to fill them (a step of a few tokens has one
+// head per warp, so its latency is one row's).
+int heads_per_warp(int64_t tokens, int H, int sm_count) {
+  const int64_t warps = (tokens + 3) / 4;
+  const int64_t want = (int64_t)sm_count * 16;
+  const int64_t groups = warps >= want ? 1 : (want + warps - 1) / warps;
+  return groups >= H ? 1 : (int)((H + groups - 1) / groups);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_rows(const dd_rope *r, const void *x, const int64_t *xs, void *out, const int64_t *os, int B,
+                             int T, int H, const int32_t *start_pos, const int32_t *new_len, int sm_count,
+                             int32_t *status, cudaStream_t s) {
+  const int64_t tokens = (int64_t)B * T;
+  const int heads = heads_per_warp(tokens, H, sm_count);
+  const int64_t gx = (tokens * 8 + kRopeThreads - 1) / kRopeThreads;
+  return launch_k(k_rope_rows, dim3((unsigned)gx, (H + heads - 1) / heads), dim3(kRopeThreads), 0, s, rope_of(r),
+                  static_cast<const uint16_t *>(x), Rows{xs[0], xs[1], xs[2]}, static_cast<uint16_t *>(out),
+                  Rows{os[0], os[1], os[2]}, B, T, H, heads, start_pos, new_len, status);
+}
+
+cudaError_t launch_append(const dd_append_args *a, void *kh_dev, void *vh_dev, int B, int Hkv, int C, int cs,
+                          int64_t hot_slots, int sm_count, int32_t *status, cudaStream_t s) {
+  AppendP p{};
+  p.r = rope_of(a->rope);
+  p.k = static_cast<const uint16_t *>(a->k);
+  p.v = static_cast<const uint16_t *>(a->v);
+  p.ks = Rows{a->k_stride[0], a->k_stride[1], a->k_stride[2]};
+  p.vs = Rows{a->v_stride[0], a->v_stride[1], a->v_stride[2]};
+  p.B = B, p.T = a->T, p.H = Hkv, p.C = C, p.cs = cs;
+  p.shift = cs == 16 ? 4 : cs == 32 ? 5 : 6;
+  const int64_t tokens = (int64_t)B * a->T;
+  p.heads = heads_per_warp(tokens, Hkv, sm_count);
+  p.start_pos = a->start_pos, p.new_len = a->new_len;
+  p.Kh = static_cast<uint8_t *>(kh_dev), p.Vh = static_cast<uint8_t *>(vh_dev);
+  p.Khot = static_cast<uint8_t *>(a->Khot), p.Vhot = static_cast<uint8_t *>(a->Vhot);
+  p.slot = a->resident_slot;
+  p.hot_slots = hot_slots;
+  p.k_exp = a->k_exp, p.v_exp = a->v_exp;
+  p.status = status;
+  const dim3 grid((unsigned)((tokens * 8 + kRopeThreads - 1) / kRopeThreads), (Hkv + p.heads - 1) / p.heads);
+  return a->format == DD_KV_4BIT ? launch_k(k_append<true>, grid, dim3(kRopeThreads), 0, s, p)
+                                 : launch_k(k_append<false>, grid, dim3(kRopeThreads), 0, s, p);
+}
+
+}  // namespace dd
+
+// --------------------------------------------------------------------- host table
+static bool rope_params_ok(const dd_rope_params *p) {
+  if (!p || p->rot_dim < 32 || p->rot_dim > dd::kD || p->rot_dim % 32) return false;
+  if (!(p->base > 1.0) || !isfinite(p->base) || !isfinite(p->gain)) return false;
+  if (p->scaling < DD_ROPE_PLAIN || p->scaling > DD_ROPE_BY_WAVELENGTH) return false;
+  if (p->scaling != DD_ROPE_PLAIN && !(p->factor >= 1.0 && isfinite(p->factor))) return false;
+  if (p->scaling >= DD_ROPE_BY_PARTS &&
+      !(p->orig_len > 0.0 && isfinite(p->orig_len) && p->beta_slow > 0.0 && p->beta_fast > p->beta_slow &&
+        isfinite(p->beta_fast)))
+    return false;
+  return true;
+}
+
+extern "C" dd_status dd_rope_table(const dd_rope_params *p, void *table) {
+  if (!rope_params_ok(p) || !table) return DD_ERR_INVALID_ARG;
+  const double pi2 = 6.283185307179586476925286766559;
+  const int n = p->rot_dim / 2;
+  const double base = p->scaling == DD_ROPE_NTK ? p->base * pow(p->factor, p->rot_dim / (p->rot_dim - 2.0)) : p->base;
+  double lo = 0, hi = 0;
+  if (p->scaling == DD_ROPE_BY_PARTS) {
+    const double a = p->rot_dim * log(p->orig_len / (p->beta_fast * pi2)) / (2.0 * log(p->base));
+    const double b = p->rot_dim * log(p->orig_len / (p->beta_slow * pi2)) / (2.0 * log(p->base));
+    lo = floor(a) > 0.0 ? floor(a) : 0.0;
+    hi = ceil(b) < p->rot_dim - 1.0 ? ceil(b) : p->rot_dim - 1.0;
+  }
+  uint64_t *freq = static_cast<uint64_t *>(table);
+  for (int i = 0; i < 64; ++i) {
+    freq[i] = 0;
+    if (i >= n) continue;
+    double f = pow(base, -2.0 * i / p->rot_dim);
+    if (p->scaling == DD_ROPE_LINEAR) f /= p->factor;
+    if (p->scaling == DD_ROPE_BY_PARTS) {
+      const double span = hi - lo > 1e-3 ? hi - lo : 1e-3;
+      const double r = fmin(fmax((i - lo) / span, 0.0), 1.0);
+      f = f / p->factor * r + f * (1.0 - r);
+    } else if (p->scaling == DD_ROPE_BY_WAVELENGTH) {
+      const double r = fmin(fmax((p->orig_len * f / pi2 - p->beta_slow) / (p->beta_fast - p->beta_slow), 0.0), 1.0);
+      f = f * r + f / p->factor * (1.0 - r);
+    }
+    // f / (2 pi) in two doubles, times 2^64 (f <= 1, so below 2^62)
+    const double inv = 0.15915494309189535, inv_lo = -9.839338337591243e-18;
+    const double t = f * inv, e = fma(f, inv, -t) + f * inv_lo;
+    const double th = floor(ldexp(t, 64)), tl = floor((ldexp(t, 64) - th) + ldexp(e, 64) + 0.5);
+    freq[i] = (uint64_t)th + (uint64_t)(int64_t)tl;
+  }
+  const double gain =
+      p->gain > 0.0 ? p->gain : p->scaling == DD_ROPE_BY_PARTS ? 0.1 * log(p->factor) + 1.0 : 1.0;
+  float *lut = reinterpret_cast<float *>(static_cast<uint8_t *>(table) + dd::kLutOff);
+  for (int i = 0; i < dd::kLut; ++i) {
+    const double c = gain * cos(pi2 * i / dd::kLut), s = gain * sin(pi2 * i / dd::kLut);
+    lut[4 * i + 0] = (float)c;
+    lut[4 * i + 1] = (float)s;
+    lut[4 * i + 2] = (float)(c - (double)(float)c);
+    lut[4 * i + 3] = (float)(s - (double)(float)s);
+  }
+  return DD_OK;
+}

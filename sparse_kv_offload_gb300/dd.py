@@ -22,6 +22,12 @@ DD_OK, DD_ERR_INVALID_ARG, DD_ERR_CUDA, DD_ERR_CAPACITY, DD_ERR_TIMEOUT, DD_ERR_
 GATHER_ZEROCOPY, GATHER_MEMCPY, GATHER_KERNEL, GATHER_AUTO = 0, 1, 2, 3
 TRACE_SLOTS = 256          # per-SM slots of a step's timing words (DD_TRACE_SLOTS)
 LM_MEAN, LM_MINMAX = 0, 1
+D_HEAD = 128               # head dimension of the library
+KV_BF16, KV_4BIT = 0, 1
+KV4_ROW_BYTES = 72         # bytes of a 4-bit row of 128 values (DD_KV4_ROW_BYTES)
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BY_PARTS, ROPE_BY_WAVELENGTH = range(5)
+ROPE_TABLE_BYTES = 8704
 
 EXPORTED = (
     "dd_create", "dd_destroy", "dd_build_landmarks", "dd_score_landmarks", "dd_select_topk",
@@ -29,6 +35,7 @@ EXPORTED = (
     "dd_launch_count", "dd_status_str", "dd_last_cuda_error", "dd_synth_kv", "dd_synth_queries", "dd_sparse_attn_decode_noalloc",
     "dd_build_landmarks_minmax", "dd_score_landmarks_minmax", "dd_update_residency",
     "dd_prefetch_kv", "dd_select_topk_mass", "dd_selftest_bounded_wait", "dd_step_folds_scoring",
+    "dd_rope_table", "dd_rope_rows", "dd_append_kv", "dd_gather_kv4", "dd_sparse_attn_decode_kv4",
 )
 
 
@@ -66,6 +73,28 @@ class StepArgs(ctypes.Structure):
     ]
 
 
+class RopeParams(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("orig_len", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("gain", ctypes.c_double)]
+
+
+class RopeRef(ctypes.Structure):
+    _fields_ = [("table", _vp), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int)]
+
+
+_stride3 = ctypes.c_int64 * 3
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("k", _vp), ("v", _vp), ("k_stride", _stride3), ("v_stride", _stride3), ("T", ctypes.c_int32),
+        ("format", ctypes.c_int), ("start_pos", _vp), ("new_len", _vp), ("rope", ctypes.POINTER(RopeRef)),
+        ("Kh", _vp), ("Vh", _vp), ("Khot", _vp), ("Vhot", _vp), ("resident_slot", _vp), ("k_exp", _vp),
+        ("v_exp", _vp),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libdd.so is not built ({LIB_PATH}); run sparse_kv_offload_gb300.build.build()")
@@ -87,6 +116,12 @@ def _load():
         "dd_selftest_bounded_wait": (i32, [_vp, i32, _vp]),
         "dd_select_topk_mass": (i32, [_vp, _vp, _vp, _vp, f32, i32, f32, _vp]),
         "dd_prefetch_kv": (i32, [_vp, _vp, i32, i32, i32, _vp, _vp, _vp, _vp, _vp, _vp, i32, _vp]),
+        "dd_rope_table": (i32, [ctypes.POINTER(RopeParams), _vp]),
+        "dd_rope_rows": (i32, [_vp, ctypes.POINTER(RopeRef), _vp, ctypes.POINTER(i64), _vp, ctypes.POINTER(i64), i32,
+                               i32, _vp, _vp, _vp]),
+        "dd_append_kv": (i32, [_vp, ctypes.POINTER(AppendArgs), _vp]),
+        "dd_gather_kv4": (i32, [_vp] * 7 + [i32] + [_vp] * 3),
+        "dd_sparse_attn_decode_kv4": (i32, [_vp] * 16 + [f32, _vp, _vp]),
         "dd_get_status": (i32, [_vp, ctypes.POINTER(i32)]),
         "dd_launch_count": (i64, [_vp]),
         "dd_step_folds_scoring": (i32, [ctypes.POINTER(Dims), i32, ctypes.c_int, f32]),
@@ -141,6 +176,71 @@ def _ptr(t, dtype=None, numel=None, device=True, name="tensor", allow_none=False
     if numel is not None and t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} elements, needs {numel}")
     return t.data_ptr()
+
+
+def _rows(t, shape, name, writable=False):
+    """Address and (request, token, head) strides of bf16 rows [B, T, H, 128]: any strides
+    that are multiples of 8 elements (16 bytes), the last dimension dense."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+    st = t.stride()
+    if t.numel() and st[3] != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    st = tuple(s if n > 1 else 0 for s, n in zip(st[:3], shape[:3]))   # a dimension of one has no stride
+    if any(s % 8 for s in st):
+        raise ValueError(f"{name}: strides must be multiples of 8 elements")
+    if writable:
+        extent = D_HEAD
+        for s, n in sorted((s, n) for s, n in zip(st, shape[:3]) if n > 1):
+            if s < extent:
+                raise ValueError(f"{name}: rows overlap")
+            extent += s * (n - 1)
+    return t.data_ptr(), _stride3(*st)
+
+
+def _i32(t, numel, name, allow_none=False):
+    return _ptr(t, torch.int32, numel, name=name, allow_none=allow_none)
+
+
+def _either(t, dtype, numel, name, allow_none=False):
+    """Address of a tensor in device or in pinned host memory."""
+    on_gpu = t is None or not isinstance(t, torch.Tensor) or t.is_cuda
+    return _ptr(t, dtype, numel, device=on_gpu, name=name, allow_none=allow_none)
+
+
+class Rope:
+    """Rotary positions: dd_rope_table's table on the device and the pairs' layout."""
+
+    def __init__(self, table, rot_dim, layout):
+        self.table = table
+        self.rot_dim = int(rot_dim)
+        self.layout = int(layout)
+        self._ref = RopeRef(_ptr(table, torch.uint8, ROPE_TABLE_BYTES, name="table"), self.rot_dim, self.layout)
+
+
+def rope_host_table(rot_dim, base=10000.0, scaling=0, factor=1.0, orig_len=0.0, beta_fast=32.0, beta_slow=1.0,
+                    gain=0.0) -> torch.Tensor:
+    """dd_rope_table's output as a uint8 host tensor (no GPU needed; see dd.h)."""
+    t = torch.zeros(ROPE_TABLE_BYTES, dtype=torch.uint8)
+    p = RopeParams(int(rot_dim), int(scaling), float(base), float(factor), float(orig_len), float(beta_fast),
+                   float(beta_slow), float(gain))
+    _chk(_lib.dd_rope_table(ctypes.byref(p), t.data_ptr()), "dd_rope_table")
+    return t
+
+
+def rope_table(rot_dim, base=10000.0, layout=0, scaling=0, device="cuda", **scaling_params) -> Rope:
+    """Rotary positions for Context.rope and Context.append_kv, made once: ``layout``
+    ROPE_HALF or ROPE_INTERLEAVED, ``scaling`` one of ROPE_PLAIN .. ROPE_BY_WAVELENGTH
+    with its factor, orig_len, beta_fast, beta_slow and gain (see dd.h)."""
+    if layout not in (ROPE_HALF, ROPE_INTERLEAVED):
+        raise ValueError(f"layout must be ROPE_HALF or ROPE_INTERLEAVED, got {layout}")
+    return Rope(rope_host_table(rot_dim, base=base, scaling=scaling, **scaling_params).to(device), rot_dim, layout)
 
 
 @dataclass(frozen=True)
@@ -290,6 +390,83 @@ class Context:
             _ptr(miss_count, torch.int32, 1, name="miss_count"), float(softmax_scale),
             _ptr(out, torch.float32, s.B * s.n_q * s.Hq * s.d, name="out"), _stream(stream)),
             "dd_sparse_attn_decode")
+
+    # ------------------------------------------- rotary positions, appends, 4-bit cache
+    def rope(self, rope, x, out, start_pos, new_len=None, stream=None):
+        """Rotate rows x bf16 [B, T, H, 128] into ``out`` (may be x): row t of request b at
+        position start_pos[b] + t, rows t >= new_len[b] left out (see dd.h)."""
+        if x.dim() != 4:
+            raise ValueError("x must be [B, T, H, 128]")
+        B, T, H = self.shape.B, x.shape[1], x.shape[2]
+        xp, xs = _rows(x, (B, T, H, D_HEAD), "x")
+        op, os_ = _rows(out, (B, T, H, D_HEAD), "out", writable=True)
+        _chk(_lib.dd_rope_rows(self._h, ctypes.byref(rope._ref), xp, xs, op, os_, T, H, _i32(start_pos, B, "start_pos"),
+                               _i32(new_len, B, "new_len", True), _stream(stream)), "dd_rope_rows")
+
+    def append_kv(self, k, v, start_pos, new_len=None, rope=None, Kh=None, Vh=None, Khot=None, Vhot=None,
+                  resident_slot=None, kv_format=KV_BF16, k_exp=None, v_exp=None, stream=None):
+        """Append rows k, v bf16 [B, T, Hkv, 128] to the home cache Kh/Vh (pinned host or
+        device) and to the resident copies in Khot/Vhot, keys rotated by ``rope`` on the
+        way; kv_format KV_BF16 or KV_4BIT (see dd.h)."""
+        s = self.shape
+        if k.dim() != 4:
+            raise ValueError("k must be [B, T, Hkv, 128]")
+        T = k.shape[1]
+        four = kv_format == KV_4BIT
+        dt = torch.uint8 if four else torch.bfloat16
+        row = KV4_ROW_BYTES if four else s.d
+        nh, nr = s.B * s.Hkv * s.L * row, self.hot_slots * s.cs * row
+        a = AppendArgs()
+        a.k, a.k_stride = _rows(k, (s.B, T, s.Hkv, D_HEAD), "k")
+        a.v, a.v_stride = _rows(v, (s.B, T, s.Hkv, D_HEAD), "v")
+        a.T, a.format = T, int(kv_format)
+        a.start_pos, a.new_len = _i32(start_pos, s.B, "start_pos"), _i32(new_len, s.B, "new_len", True)
+        if rope is not None:
+            a.rope = ctypes.pointer(rope._ref)
+        a.Kh, a.Vh = _either(Kh, dt, nh, "Kh", True), _either(Vh, dt, nh, "Vh", True)
+        a.Khot, a.Vhot = _ptr(Khot, dt, nr, name="Khot", allow_none=True), _ptr(Vhot, dt, nr, name="Vhot", allow_none=True)
+        a.resident_slot = _i32(resident_slot, s.B * s.Hkv * s.C, "resident_slot", True)
+        a.k_exp, a.v_exp = _i32(k_exp, s.Hkv, "k_exp", True), _i32(v_exp, s.Hkv, "v_exp", True)
+        _chk(_lib.dd_append_kv(self._h, ctypes.byref(a), _stream(stream)), "dd_append_kv")
+
+    def gather_kv4(self, Kh, Vh, miss_list, miss_count, Kst, Vst, expand=False, k_exp=None, v_exp=None, stream=None):
+        """Missing chunks of a 4-bit home cache (pinned host or device) into staging, as they
+        are or, with ``expand``, as bf16 values (see dd.h)."""
+        s = self.shape
+        n = s.B * s.Hkv * s.L * KV4_ROW_BYTES
+        dt, row = (torch.bfloat16, s.d) if expand else (torch.uint8, KV4_ROW_BYTES)
+        ns = self.max_misses * s.cs * row
+        _chk(_lib.dd_gather_kv4(
+            self._h, _either(Kh, torch.uint8, n, "Kh"), _either(Vh, torch.uint8, n, "Vh"),
+            _i32(miss_list, 1, "miss_list"), _i32(miss_count, 1, "miss_count"), _ptr(Kst, dt, ns, name="Kst"),
+            _ptr(Vst, dt, ns, name="Vst"), 1 if expand else 0, _i32(k_exp, s.Hkv, "k_exp", True),
+            _i32(v_exp, s.Hkv, "v_exp", True), _stream(stream)), "dd_gather_kv4")
+
+    def sparse_attn_decode_kv4(self, q, Khot, Vhot, Kst, Vst, union_slot, union_cnt, out, union_qmask=None,
+                               union_idx=None, kv_len=None, miss_count=None, k_exp=None, v_exp=None, K_tail=None,
+                               V_tail=None, softmax_scale=0.0, stream=None):
+        """sparse_attn_decode over 4-bit pages (uint8 [slots, cs*72]); rows at positions >=
+        kv_len[b] are left out (see dd.h)."""
+        s = self.shape
+        page = s.cs * KV4_ROW_BYTES
+        nh, ns = self.hot_slots * page, self.max_misses * page
+        units = s.B * s.Hkv
+        nu, nt = units * s.umax, s.B * s.n_q * s.Hkv * s.d
+        nq = s.B * s.n_q * s.Hq * s.d
+        _chk(_lib.dd_sparse_attn_decode_kv4(
+            self._h, _ptr(q, torch.bfloat16, nq, name="q"),
+            _ptr(Khot, torch.uint8, nh, name="Khot", allow_none=True),
+            _ptr(Vhot, torch.uint8, nh, name="Vhot", allow_none=True),
+            _ptr(Kst, torch.uint8, ns, name="Kst", allow_none=True),
+            _ptr(Vst, torch.uint8, ns, name="Vst", allow_none=True),
+            _i32(k_exp, s.Hkv, "k_exp", True), _i32(v_exp, s.Hkv, "v_exp", True),
+            _ptr(K_tail, torch.bfloat16, nt, name="K_tail", allow_none=True),
+            _ptr(V_tail, torch.bfloat16, nt, name="V_tail", allow_none=True),
+            _i32(union_idx, nu, "union_idx", True), _i32(union_slot, nu, "union_slot"),
+            _ptr(union_qmask, torch.uint8, nu, name="union_qmask", allow_none=True),
+            _i32(union_cnt, units, "union_cnt"), _i32(miss_count, 1, "miss_count", True),
+            _i32(kv_len, s.B, "kv_len", True), float(softmax_scale),
+            _ptr(out, torch.float32, nq, name="out"), _stream(stream)), "dd_sparse_attn_decode_kv4")
 
     def selftest_bounded_wait(self, kind, stream=None):
         """Run a bounded device wait that nothing signals (see dd.h); the status

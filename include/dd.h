@@ -498,9 +498,10 @@ dd_status dd_gather_kv4(dd_ctx *ctx, const void *Kh, const void *Vh, const int32
  *                out, whatever they hold (a chunk that is not full yet, chunks behind
  *                the end).  The position of row t of union chunk i is
  *                union_idx[b,g,i]*cs + t; union_idx int32 [B,Hkv,Umax] as written by
- *                dd_resolve_union, needed with kv_len.
+ *                dd_resolve_union (ascending, no chunk twice), needed with kv_len.
  * Attention over a whole cache: k = C, union_cnt = the chunks in use, union_idx =
- * 0, 1, ..., union_slot = their pages.  A query without a row gets zeros. */
+ * 0, 1, ..., union_slot = their pages.  A query without a row gets zeros.
+ * B*Hkv*(Umax*cs/16 + 1) has to stay below 2^29 (DD_ERR_INVALID_ARG). */
 dd_status dd_sparse_attn_decode_kv4(dd_ctx *ctx, const void *q, const void *Khot, const void *Vhot,
                                     const void *Kst, const void *Vst, const int32_t *k_exp, const int32_t *v_exp,
                                     const void *K_tail, const void *V_tail, const int32_t *union_idx,

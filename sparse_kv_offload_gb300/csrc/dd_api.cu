@@ -7,6 +7,7 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <vector>
 
 #include "dd_tc.cuh"
@@ -31,6 +32,8 @@ struct dd_ctx {
   int32_t *ticket = nullptr;
   void *dummy_pool = nullptr;
   dd::AttnPlan plan;
+  dd::Attn4Plan plan4;
+  int32_t *arrive4 = nullptr;         // 4-bit attention: CTAs done with each unit (zero between calls)
   // host side
   int32_t *h_miss = nullptr;          // pinned: [1 + max_misses]
   cudaStream_t copy_stream = nullptr;
@@ -190,6 +193,10 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   const int64_t B = dims->B, Hkv = dims->Hkv, n_q = dims->n_q, k = dims->k, C = c->C;
   const int64_t units = c->units;
   c->plan = dd::attn_plan(c->units, c->umax, c->NQ, c->sm_count);
+  c->plan4 = dd::attn4_plan(c->units, c->NQ, c->sm_count);
+  // the two attentions share their partial sums (calls on one context do not overlap)
+  const int64_t part_o = std::max(c->plan.part_o_floats, c->plan4.part_o_floats);
+  const int64_t part_ml = std::max(c->plan.part_ml_floats, c->plan4.part_ml_floats);
   int64_t bytes = 0;
   auto add = [&](int64_t n, int64_t sz) { bytes += ((n * sz) + 255) & ~int64_t(255); };
   add(1, 4);                                   // status
@@ -203,8 +210,8 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   add(max_misses > 0 ? max_misses : 1, 4);     // miss_list
   add(1, 4);                                   // miss_count
   add(B * n_q * Hkv * k, 4);                   // attn_slot
-  add(c->plan.part_o_floats, 4);               // part_o
-  add(c->plan.part_ml_floats, 4);              // part_ml
+  add(part_o, 4);                              // part_o
+  add(part_ml, 4);                             // part_ml
   add(2 * units + 1, 4);                       // chunk_off + fix-up counters
   add(c->plan.flat_entries, 16);               // flat chunk table
   add(64 * 128, 2);                            // dummy pool (64 rows)
@@ -212,6 +219,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   add(16 * units, 8);                          // union and miss offsets by the last CTA (a line per unit)
   add(3, 4);                                   // ticket counters + look-back epoch
   add(1, 8);                                   // self-test word
+  add(units * c->plan4.groups, 4);             // 4-bit attention: arrival counters
   if (cudaMalloc(&c->ws, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   uint8_t *cur = static_cast<uint8_t *>(c->ws);
   c->status = carve<int32_t>(cur, 1);
@@ -225,8 +233,8 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   c->miss_list = carve<int32_t>(cur, max_misses > 0 ? max_misses : 1);
   c->miss_count = carve<int32_t>(cur, 1);
   c->attn_slot = carve<int32_t>(cur, B * n_q * Hkv * k);
-  c->part_o = carve<float>(cur, c->plan.part_o_floats);
-  c->part_ml = carve<float>(cur, c->plan.part_ml_floats);
+  c->part_o = carve<float>(cur, part_o);
+  c->part_ml = carve<float>(cur, part_ml);
   c->chunk_off = carve<int32_t>(cur, 2 * units + 1);
   c->flat = carve<int4>(cur, c->plan.flat_entries);
   c->dummy_pool = carve<uint16_t>(cur, 64 * 128);
@@ -234,6 +242,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   c->lb_pref = carve<unsigned long long>(cur, 16 * units);
   c->ticket = carve<int32_t>(cur, 3);
   c->diag_word = carve<unsigned long long>(cur, 1);
+  c->arrive4 = carve<int32_t>(cur, units * c->plan4.groups);
   if (cudaMemset(c->ws, 0, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   const int32_t first_epoch = 1;   // look-back words start zeroed, i.e. with epoch 0
   if (cudaMemcpy(c->ticket + 2, &first_epoch, sizeof(first_epoch), cudaMemcpyHostToDevice) != cudaSuccess)
@@ -731,8 +740,11 @@ dd_status dd_sparse_attn_decode_kv4(dd_ctx *c, const void *q, const void *Khot, 
   if (!q || !union_slot || !union_cnt || !out || !aligned16(q) || !aligned16(out)) return DD_ERR_INVALID_ARG;
   if (c->hot_slots > 0 && (!Khot || !Vhot || !aligned16(Khot) || !aligned16(Vhot))) return DD_ERR_INVALID_ARG;
   if (c->max_misses > 0 && (!Kst || !Vst || !aligned16(Kst) || !aligned16(Vst))) return DD_ERR_INVALID_ARG;
-  DD_TRY(on_device(c));
   const dd_dims &d = c->dims;
+  // blocks of 16 rows are numbered with 32 bits
+  if ((int64_t)c->units * c->plan4.groups * ((int64_t)c->umax * (d.cs / 16) + 1) >= (int64_t(1) << 30))
+    return DD_ERR_INVALID_ARG;
+  DD_TRY(on_device(c));
   dd::Attn4Args a{};
   a.q = q;
   a.Khot = static_cast<const uint8_t *>(Khot), a.Vhot = static_cast<const uint8_t *>(Vhot);
@@ -746,9 +758,8 @@ dd_status dd_sparse_attn_decode_kv4(dd_ctx *c, const void *q, const void *Khot, 
   a.B = d.B, a.n_q = d.n_q, a.Hq = d.Hq, a.Hkv = d.Hkv, a.cs = d.cs, a.umax = c->umax;
   a.hot_slots = c->hot_slots, a.max_misses = c->max_misses;
   a.status = c->status;
-  a.sm_count = c->sm_count;
   c->launches += 1;
-  return cuda_ok(dd::launch_attn4(a, (cudaStream_t)stream));
+  return cuda_ok(dd::launch_attn4(a, c->plan4, c->part_o, c->part_ml, c->arrive4, (cudaStream_t)stream));
 }
 
 }  // extern "C"

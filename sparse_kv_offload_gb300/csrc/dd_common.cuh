@@ -402,7 +402,13 @@ struct Attn4Args {
   int B, n_q, Hq, Hkv, cs, umax;
   int64_t hot_slots, max_misses;
   int32_t *status;
-  int sm_count;
 };
-cudaError_t launch_attn4(const Attn4Args &a, cudaStream_t s);
+struct Attn4Plan {
+  int nt, groups, n_cta;
+  int64_t part_o_floats, part_ml_floats;
+};
+Attn4Plan attn4_plan(int units, int NQ, int sm_count);
+// part_o, part_ml: the plan's floats; arrive: [units * groups] counters, zero (and left zero)
+cudaError_t launch_attn4(const Attn4Args &a, const Attn4Plan &plan, float *part_o, float *part_ml, int32_t *arrive,
+                         cudaStream_t s);
 }  // namespace dd

@@ -31,6 +31,8 @@
 // until the end of a unit, where the warps' sums are joined in shared memory.  A
 // unit cut by a slice's end is joined by whichever of its CTAs comes last.  No
 // plan kernel: every CTA sums the unions' lengths itself.
+#include <limits.h>
+
 #include "dd_attn.cuh"
 #include "dd_kv4.cuh"
 
@@ -38,30 +40,33 @@ namespace dd {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kMaxRuns = 64;             // units of a slice listed at a time
+constexpr int kMaxRuns = 16;             // units of a slice listed at a time
 constexpr int kTileBytes = 4 * kBlk4;    // two blocks of 16 rows: K and V of the first, then of the second
 constexpr int kJoinRow = 132;            // floats of a query vector's sums in the joining buffer (128 + padding)
 constexpr float kLazy = 8.f;             // a score may exceed the reference by 2^kLazy ...
 constexpr float kHead = 6.f;             // ... and weights are held times 2^kHead
 
-// NT tiles of 8 query vectors a warp.  One tile: its query registers fit beside the
-// sums of two CTAs' warps on an SM; more tiles read the queries from shared memory.
-__host__ __device__ constexpr int attn4_ctas_per_sm(int nt) { return nt <= 2 ? 2 : 1; }
-__host__ __device__ constexpr int attn4_stages(int nt) { return nt <= 2 ? 2 : 4; }
+// NT tiles of 8 query vectors a warp, two CTAs on an SM.  Up to 4 query vectors (kPack)
+// the two parts of P share a tile, one in its columns 0-3, one in 4-7, which halves the
+// products with V (whole cache, 8 requests of 128K: 195 -> 179 us).  One tile: eight warps a CTA
+// with the queries in registers (128 registers a thread); two: six warps (168), the
+// queries in shared memory.
+__host__ __device__ constexpr int attn4_warps(int nt) { return nt == 1 ? 8 : 6; }
+constexpr int kStages = 2;               // tiles in flight per warp
 __host__ __device__ constexpr size_t attn4_smem(int nt) {
-  return (size_t)kWarps * attn4_stages(nt) * kTileBytes + (size_t)kWarps * 8 * kJoinRow * 4 +
-         (nt > 1 ? (size_t)nt * 8 * 256 : 0);
+  return (size_t)attn4_warps(nt) * (kStages * kTileBytes + 8 * kJoinRow * 4) + (nt > 1 ? (size_t)nt * 8 * 256 : 0);
 }
 
 struct Run {           // a unit's place in the sequence of tiles
-  int unit, start, end, cnt;
+  int vunit, unit, b, g, q0;       // unit and group of query vectors, request, KV head, first query vector
+  int start, end, cnt, len;        // tiles [start, end) of the sequence; chunks; rows (INT_MAX: no kv_len)
+  int cta0, cta1;                  // the CTAs that share it
+  int ke, ve;
 };
 
 struct Attn4Params {
   Attn4Args a;
-  int NQ, G, bpc_shift, groups, vunits;   // vunits = units * groups of query vectors
+  int NQ, G, bpc_shift, groups, group_q, vunits;   // vunits = units * groups of group_q query vectors
   float *part_o, *part_ml;
   int32_t *arrive;
 };
@@ -114,15 +119,20 @@ __device__ __forceinline__ uint32_t movm(uint32_t a) {
   return r;
 }
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // shared-memory loads by address (asm: the ring is written by bulk copies)
 __device__ __forceinline__ uint4 lds128(uint32_t p) {
   uint4 r;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(p));
   return r;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t p) {
-  uint2 r;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(p));
+__device__ __forceinline__ uint32_t lds32(uint32_t p) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(p));
   return r;
 }
 __device__ __forceinline__ uint32_t lds16(uint32_t p) {
@@ -139,19 +149,41 @@ __device__ __forceinline__ uint32_t lds8(uint32_t p) {
 // Tiles of a unit: pairs of its union's blocks of 16 rows, those wholly behind the
 // end left out (chunk numbers ascend, so block x lies at position 16 x or later),
 // at least one, so that a unit without rows is visited too.
-__device__ __forceinline__ int unit_tiles(const Attn4Params &p, int vunit, int &cnt) {
-  const int unit = vunit / p.groups;
-  cnt = p.a.union_cnt[unit];
-  if (cnt < 0 || cnt > p.a.umax) {
-    set_status(p.a.status, DD_ERR_DEVICE_CHECK);
-    cnt = cnt < 0 ? 0 : p.a.umax;
+struct Lengths {
+  int cnt, len, exps;      // chunks, rows (INT_MAX without kv_len), ke | ve << 16
+};
+__device__ __forceinline__ int unit_tiles(const Attn4Params &p, int vunit, Lengths &r) {
+  const Attn4Args &a = p.a;
+  const int unit = vunit / p.groups, b = unit / a.Hkv, g = unit - b * a.Hkv;
+  r.cnt = a.union_cnt[unit];
+  r.len = a.kv_len ? a.kv_len[b] : INT_MAX;
+  int ke = a.k_exp ? a.k_exp[g] : 0;
+  int ve = a.v_exp ? a.v_exp[g] : 0;
+  if (r.cnt < 0 || r.cnt > a.umax || abs(ke) > kMaxExp4 || abs(ve) > kMaxExp4) {
+    set_status(a.status, DD_ERR_DEVICE_CHECK);
+    r.cnt = r.cnt < 0 ? 0 : min(r.cnt, a.umax);
+    ke = max(-kMaxExp4, min(ke, kMaxExp4));
+    ve = max(-kMaxExp4, min(ve, kMaxExp4));
   }
-  int n = cnt << p.bpc_shift;
-  if (p.a.kv_len) {
-    const int len = max(p.a.kv_len[unit / p.a.Hkv], 0);
-    n = min(n, (len >> 4) + ((len & 15) != 0));
-  }
+  r.exps = (ke & 0xFFFF) | ve << 16;
+  r.len = max(r.len, 0);
+  const int n = min(r.cnt << p.bpc_shift, (r.len >> 4) + ((r.len & 15) != 0));
   return max((n + 1) >> 1, 1);
+}
+
+__device__ __forceinline__ void fill_run(const Attn4Params &p, Run &r, int vunit, int start, int end,
+                                         const Lengths &l) {
+  r.vunit = vunit;
+  r.unit = vunit / p.groups;
+  r.q0 = (vunit - r.unit * p.groups) * p.group_q;
+  r.b = r.unit / p.a.Hkv;
+  r.g = r.unit - r.b * p.a.Hkv;
+  r.start = start;
+  r.end = end;
+  r.cnt = l.cnt;
+  r.len = l.len;
+  r.ke = (int)(int16_t)(l.exps & 0xFFFF);
+  r.ve = l.exps >> 16;
 }
 
 // 2^(a - b) with equal arguments (both -inf among them) giving 1
@@ -168,13 +200,14 @@ __device__ __forceinline__ int64_t out_row(const Attn4Params &p, int unit, int q
   return ((int64_t)(b * p.a.n_q + j) * p.a.Hq + h) * kD;
 }
 
-// Step's own rows (in shared memory: keys, then values), then the division.  The lane
-// holds columns 4 lane .. of the query vector (qw).
-__device__ __forceinline__ void finish(const Attn4Params &p, int unit, int qv, Part s, uint2 qw, const uint2 *tails,
-                                       int lane) {
+// Step's own rows (in shared memory: keys, then values; the query vector too), then
+// the division.  The lane holds columns 4 lane .. of the query vector.
+__device__ __forceinline__ void finish(const Attn4Params &p, int unit, int qv, Part s, const uint2 *query,
+                                       const uint2 *tails, int lane) {
   const Attn4Args &a = p.a;
   if (a.k_tail) {
     const float sl2 = a.softmax_scale * 1.4426950408889634f;
+    const uint2 qw = query[lane];
     const int j = qv / p.G;
     for (int t = 0; t <= j; ++t) {
       const uint2 kw = tails[t * 32 + lane], vw = tails[(kMaxNq + t) * 32 + lane];
@@ -201,20 +234,9 @@ __device__ __forceinline__ void finish(const Attn4Params &p, int unit, int qv, P
   *reinterpret_cast<float4 *>(a.out + out_row(p, unit, qv) + 4 * lane) = r;
 }
 
-// fp16 fragments of NT x 8 query vectors, scaled, and each column's factor back.
-// B fragment of step s: values 32 t4 + 4 s + {0,1} and {2,3} of query vector g8.
-__device__ __forceinline__ void load_query(const Attn4Params &p, int unit, int qv, int t4, uint32_t (&f)[16],
-                                           float &back) {
-  uint4 w[4];
-  if (qv < p.NQ) {
-    const uint4 *src =
-        reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.a.q) + out_row(p, unit, qv) + 32 * t4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = src[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
-  }
+// fp16 fragments of a lane's 32 query values, scaled by a power of two, and the factor back.  B fragment of
+// step s: values 32 t4 + 4 s + {0,1} and {2,3} of query vector g8.
+__device__ __forceinline__ void query_fragments(const uint4 (&w)[4], uint32_t (&f)[16], float &back) {
   const uint32_t v[16] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w,
                           w[2].x, w[2].y, w[2].z, w[2].w, w[3].x, w[3].y, w[3].z, w[3].w};
   uint32_t top = 0;   // largest magnitude, as bits
@@ -230,9 +252,9 @@ __device__ __forceinline__ void load_query(const Attn4Params &p, int unit, int q
   back = pow2i(-sh);
 }
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const __grid_constant__ Attn4Params p) {
-  constexpr int S = attn4_stages(NT);
+template <int NT, bool kPack>
+__global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_constant__ Attn4Params p) {
+  constexpr int S = kStages, kWarps = attn4_warps(NT), kThreads = kWarps * 32;
   constexpr bool kQReg = NT == 1;
   extern __shared__ __align__(128) uint8_t smem[];
   float *join = reinterpret_cast<float *>(smem + kWarps * S * kTileBytes);     // [kWarps][8][kJoinRow]
@@ -243,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
   __shared__ uint4 s_tails[2 * kMaxNq * 16];      // the unit's own new rows: keys, values
   __shared__ float s_back[NT * 8];
   __shared__ int scratch[33];
-  __shared__ int s_first, s_flag;
+  __shared__ int s_first, s_flag, s_lo, s_hi;
+  __shared__ uint4 s_query[NT * 8 * 16];            // the run's query vectors as they are
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t4 = lane & 3, g8 = lane >> 2;
@@ -256,18 +279,57 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
   pdl_trigger();
 
   // ------------------------------------------------------------- the slice
+  // Equal slices of the sequence, in whole rounds of the warps.  A slice that holds the
+  // end of one unit and the start of the next pays for two queries and two joins, two
+  // to three rounds' time, so where the units are no more than the threads (their
+  // lengths are then loaded once) and parts of up to two rounds more than a slice let
+  // every CTA work on one unit, the units are cut into such parts instead.
+  // Llama-3-8B layer, two queries: 21.0 -> 18.8 us; three requests, 21 units: 32.4 -> 20.8 us.
+  const bool one_round = p.vunits <= kThreads;
   if (tid == 0) s_flag = load_status(a.status);
-  int c0, total;
-  {
-    int sum = 0;
-    for (int u = tid; u < p.vunits; u += kThreads) sum += unit_tiles(p, u, c0);
-    total = block_sum(sum, scratch);
+  const int64_t staged = a.miss_count ? min((int64_t)*a.miss_count, a.max_misses) : a.max_misses;
+  Lengths mine{};
+  int my_tiles = 0, my_start, total;
+  if (one_round) {
+    if (tid < p.vunits) my_tiles = unit_tiles(p, tid, mine);
+    my_start = block_excl_scan(my_tiles, scratch, &total);
+  } else {
+    for (int u = tid; u < p.vunits; u += kThreads) my_tiles += unit_tiles(p, u, mine);
+    total = block_sum(my_tiles, scratch);
   }
   const bool dead = s_flag != 0;       // an error is pending: no work (the counts below still go on)
-  const int per = max((total + (int)gridDim.x - 1) / (int)gridDim.x, kWarps);
-  const int lo = (int)min((int64_t)total, (int64_t)blockIdx.x * per), hi = min(total, lo + per);
+  const int n_cta = (int)gridDim.x;
+  int per = ((total + n_cta - 1) / n_cta + kWarps - 1) / kWarps * kWarps;
+  int lo = (int)min((int64_t)total, (int64_t)blockIdx.x * per), hi = min(total, lo + per);
+  bool parts = false;
+  if (one_round && n_cta + kThreads < 1024) {
+    // the number of parts for three part lengths, 10 bits each (at most n_cta + units)
+    int mine3 = 0, all3;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) mine3 |= (my_tiles + per + k * kWarps - 1) / (per + k * kWarps) << (10 * k);
+    const int before3 = block_excl_scan(mine3, scratch, &all3);
+#pragma unroll
+    for (int k = 2; k >= 0; --k) {
+      if ((all3 >> (10 * k) & 1023) > n_cta) continue;
+      parts = true;
+      const int n = mine3 >> (10 * k) & 1023, first = before3 >> (10 * k) & 1023;
+      const int part = (int)blockIdx.x - first;
+      if (k == 0 || (all3 >> (10 * (k - 1)) & 1023) > n_cta) {      // the shortest that fits
+        hi = (int)blockIdx.x < (all3 >> (10 * k) & 1023);           // does this CTA have a part?
+        lo = 0;
+        if (n && part >= 0 && part < n) {
+          const int len = (my_tiles + n - 1) / n;
+          fill_run(p, runs[0], tid, my_start, my_start + my_tiles, mine);
+          runs[0].cta0 = first;
+          runs[0].cta1 = first + n - 1;
+          s_lo = my_start + part * len;
+          s_hi = min(my_start + my_tiles, s_lo + len);
+        }
+        break;
+      }
+    }
+  }
   if (lo >= hi) return;
-  const int64_t staged = a.miss_count ? min((int64_t)*a.miss_count, a.max_misses) : a.max_misses;
   const int64_t page = (int64_t)16 * kRow4 << p.bpc_shift;
   const uint32_t all_q = (1u << a.n_q) - 1u;
   const float sl2 = a.softmax_scale * 1.4426950408889634f;
@@ -276,30 +338,65 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
   bool alive = true;
 
   for (int w0 = 0;; w0 += kMaxRuns) {
-    // the slice's units number w0 .. w0 + kMaxRuns - 1
+    // the slice's units number w0 .. w0 + kMaxRuns - 1; the barrier is for what this list
+    // and s_lo, s_hi held before, and for the part written above
     __syncthreads();
-    int base = 0, n_seen = 0;          // tiles of the units before this round, units of the slice seen
-    for (int u0 = 0; u0 < p.vunits && base < hi; u0 += kThreads) {
-      int cnt = 0;
-      const int u = u0 + tid;
-      const int v = u < p.vunits ? unit_tiles(p, u, cnt) : 0;
-      int all;
-      const int start = base + block_excl_scan(v, scratch, &all);
-      if (v && start <= lo && lo < start + v) s_first = u;
-      __syncthreads();
-      if (base + all > lo) {
-        const int rank = u - s_first - w0;
-        if (v && start < hi && start + v > lo && rank >= 0 && rank < kMaxRuns)
-          runs[rank] = Run{u, start, start + v, cnt};
-        n_seen += __syncthreads_count(v && start < hi && start + v > lo);
+    int n_seen = 0;                    // units of the slice seen
+    if (parts) {
+      n_seen = 1;
+      lo = s_lo;
+      hi = s_hi;
+    } else {
+      int base = 0;                    // tiles of the units before this round
+      for (int u0 = 0; u0 < p.vunits && base < hi; u0 += kThreads) {
+        int all = total, start = my_start;
+        if (!one_round) {
+          const int u = u0 + tid;
+          my_tiles = u < p.vunits ? unit_tiles(p, u, mine) : 0;
+          start = base + block_excl_scan(my_tiles, scratch, &all);
+        }
+        const bool in = my_tiles && start < hi && start + my_tiles > lo;
+        if (in && start <= lo) s_first = u0 + tid;
+        const int n = __syncthreads_count(in);
+        if (n) {
+          const int rank = u0 + tid - s_first - w0;
+          if (in && rank >= 0 && rank < kMaxRuns) {
+            fill_run(p, runs[rank], u0 + tid, start, start + my_tiles, mine);
+            runs[rank].cta0 = start / per;
+            runs[rank].cta1 = (start + my_tiles - 1) / per;
+          }
+          n_seen += n;
+        }
+        base += all;
       }
-      base += all;
+      __syncthreads();
     }
     const int n_runs = min(n_seen - w0, kMaxRuns);
     const int wlo = max(lo, runs[0].start), whi = min(hi, runs[n_runs - 1].end);
 
     // --------------------------------------- this warp's tiles: wlo + warp + i * kWarps
     const int n_tiles = whi - wlo > warp ? (whi - wlo - warp + kWarps - 1) / kWarps : 0;
+    // the first run's query vectors are on their way while the tiles are looked up
+    // a run's query vectors and its own new rows come by asynchronous copies, the first
+    // run's while its tiles are looked up
+    auto stage_run = [&](const Run &r) {
+      for (int e = tid; e < NT * 8 * 16; e += kThreads) {
+        const int qv = r.q0 + (e >> 4);
+        if (qv < p.NQ)
+          cp_async16(s_query + e, reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + out_row(p, r.unit, qv)) + (e & 15));
+        else
+          s_query[e] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (a.k_tail) {
+        for (int i = tid; i < 2 * a.n_q * 16; i += kThreads) {
+          const int kv = i >= a.n_q * 16, e = kv ? i - a.n_q * 16 : i;
+          const uint16_t *src = static_cast<const uint16_t *>(kv ? a.v_tail : a.k_tail);
+          cp_async16(s_tails + kv * kMaxNq * 16 + e, reinterpret_cast<const uint4 *>(
+              src + ((int64_t)(r.b * a.n_q + (e >> 4)) * a.Hkv + r.g) * kD) + (e & 15));
+        }
+      }
+    };
+    stage_run(runs[0]);
     // lane 2 t + h holds block h of tile i0 + t: its slot, and {query mask, rows in use << 8, block of the chunk << 13}
     auto entry = [&](int i, int &slot, uint32_t &meta) {
       slot = 0;
@@ -313,13 +410,12 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
       const int blk = 2 * (x - runs[r].start) + (lane & 1);
       const int ci = blk >> p.bpc_shift, sub = blk & ((1 << p.bpc_shift) - 1);
       if (ci >= runs[r].cnt) return;
-      const int unit = runs[r].unit / p.groups;
-      const int64_t e = (int64_t)unit * a.umax + ci;
+      const int64_t e = (int64_t)runs[r].unit * a.umax + ci;
       slot = a.union_slot[e];
       const uint32_t qm = a.union_qmask ? a.union_qmask[e] & all_q : all_q;
       int rows = 16;
       if (a.kv_len) {
-        const int64_t left = (int64_t)a.kv_len[unit / a.Hkv] - ((int64_t)a.union_idx[e] * a.cs + sub * 16);
+        const int64_t left = runs[r].len - ((int64_t)a.union_idx[e] * a.cs + sub * 16);
         rows = left < 0 ? 0 : left > 16 ? 16 : (int)left;
       }
       if (slot >= 0 ? slot >= a.hot_slots : -1 - (int64_t)slot >= staged) {
@@ -328,10 +424,9 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
       }
       if (qm && rows) meta = qm | (uint32_t)rows << 8 | (uint32_t)sub << 13;
     };
-    int cur_slot, nxt_slot, i0 = 0;
-    uint32_t cur_meta, nxt_meta;
+    int cur_slot, nxt_slot = 0, i0 = 0;
+    uint32_t cur_meta, nxt_meta = 0;
     entry(lane >> 1, cur_slot, cur_meta);
-    entry(16 + (lane >> 1), nxt_slot, nxt_meta);
 
     // the two lanes that hold tile i ask for its blocks (an empty block just arrives)
     auto issue = [&](int i) {
@@ -353,33 +448,34 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
     };
 #pragma unroll 1
     for (int i = 0; i < S; ++i) issue(i);
+    entry(16 + (lane >> 1), nxt_slot, nxt_meta);
 
     int i = 0;
 #pragma unroll 1
     for (int r = 0; r < n_runs; ++r) {
-      const Run run = runs[r];
-      const int unit = run.unit / p.groups, qg0 = (run.unit - unit * p.groups) * NT * 8;
-      const int b = unit / a.Hkv, g = unit - b * a.Hkv;
-      const float kmul = sl2 * pow2i(head_exp(a.k_exp, g, a.status));
+      const int unit = runs[r].unit, q0 = runs[r].q0, run_end = runs[r].end;
+      const float kmul = sl2 * pow2i(runs[r].ke);
       uint32_t qf[16];            // one tile: its fragments
       float mul[NT][2];           // score units of columns 2 t4 and 2 t4 + 1
       int jq[NT][2];              // their queries (31: no such query vector)
-      if (a.k_tail && tid < 2 * a.n_q * 16) {
-        const int kv = tid >= a.n_q * 16, e = kv ? tid - a.n_q * 16 : tid;
-        const uint16_t *src = static_cast<const uint16_t *>(kv ? a.v_tail : a.k_tail);
-        s_tails[kv * kMaxNq * 16 + e] = reinterpret_cast<const uint4 *>(
-            src + ((int64_t)(b * a.n_q + (e >> 4)) * a.Hkv + g) * kD)[e & 15];
-      }
+      cp_async_wait_all();
+      __syncthreads();
       if constexpr (kQReg) {
+        uint4 w[4];
         float back;
-        load_query(p, unit, qg0 + g8, t4, qf, back);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = s_query[(kPack ? g8 & 3 : g8) * 16 + t4 * 4 + e];
+        query_fragments(w, qf, back);
         mul[0][0] = __shfl_sync(0xffffffffu, back, t4 * 8) * kmul;
         mul[0][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4) * kmul;
       } else {
         if (warp < NT) {
+          uint4 w[4];
           uint32_t f[16];
           float back;
-          load_query(p, unit, qg0 + warp * 8 + g8, t4, f, back);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = s_query[(warp * 8 + g8) * 16 + t4 * 4 + e];
+          query_fragments(w, f, back);
 #pragma unroll
           for (int s = 0; s < 8; ++s)
             *reinterpret_cast<uint2 *>(qsm + ((warp * 8 + s) * 32 + lane) * 8) = make_uint2(f[2 * s], f[2 * s + 1]);
@@ -396,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int qv = qg0 + n * 8 + 2 * t4 + c;
+          const int qv = q0 + n * 8 + (kPack ? (2 * t4 + c) & 3 : 2 * t4 + c);
           jq[n][c] = qv < p.NQ ? qv / p.G : 31;
         }
 
@@ -410,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
       }
 
 #pragma unroll 1
-      for (; i < n_tiles && wlo + warp + i * kWarps < run.end; ++i) {
+      for (; i < n_tiles && wlo + warp + i * kWarps < run_end; ++i) {
         // a block that was not asked for (0) is computed with all its rows masked
         const uint32_t meta0 = __shfl_sync(0xffffffffu, cur_meta, 2 * (i & 15));
         const uint32_t meta1 = __shfl_sync(0xffffffffu, cur_meta, 2 * (i & 15) + 1);
@@ -514,10 +610,16 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
               const uint32_t h0 = cvt_f16x2(p0, p1), h1 = cvt_f16x2(p2, p3);
               const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
               const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
-              ph[h][n][0] = movm(h0);
-              ph[h][n][1] = movm(h1);
-              pl[h][n][0] = movm(cvt_f16x2(p0 - f0.x, p1 - f0.y));
-              pl[h][n][1] = movm(cvt_f16x2(p2 - f1.x, p3 - f1.y));
+              const uint32_t l0 = cvt_f16x2(p0 - f0.x, p1 - f0.y), l1 = cvt_f16x2(p2 - f1.x, p3 - f1.y);
+              if constexpr (kPack) {   // columns 0-3: the first part, 4-7: the second
+                ph[h][n][0] = movm(t4 < 2 ? h0 : l0);
+                ph[h][n][1] = movm(t4 < 2 ? h1 : l1);
+              } else {
+                ph[h][n][0] = movm(h0);
+                ph[h][n][1] = movm(h1);
+                pl[h][n][0] = movm(l0);
+                pl[h][n][1] = movm(l1);
+              }
             }
           }
 
@@ -560,13 +662,6 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
             }
             const uint32_t s01[2] = {e4m3x2_to_half2(sc[0]), e4m3x2_to_half2(sc[1])};
             const uint32_t s23[2] = {e4m3x2_to_half2(sc[0] >> 16), e4m3x2_to_half2(sc[1] >> 16)};
-            uint2 v[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t vb = tile + (2 * h + 1) * kBlk4 + g8 * 8;
-              v[h][0] = lds64(vb + ra * 64), v[h][1] = lds64(vb + rb * 64);
-              v[h][2] = lds64(vb + (ra + 8) * 64), v[h][3] = lds64(vb + (rb + 8) * 64);
-            }
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               // even columns of two rows side by side, then the odd ones
@@ -575,26 +670,39 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
               for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const uint32_t xa = w ? v[h][2 * e].y : v[h][2 * e].x, xb = w ? v[h][2 * e + 1].y : v[h][2 * e + 1].x;
+                  const uint32_t vb = tile + (2 * h + 1) * kBlk4 + g8 * 8 + 4 * w + e * 512;
+                  const uint32_t xa = lds32(vb + ra * 64), xb = lds32(vb + rb * 64);
                   x[h][2 * e] = (xa & 0x0F0F0F0Fu) | ((xb << 4) & 0xF0F0F0F0u);
                   x[h][2 * e + 1] = ((xa >> 4) & 0x0F0F0F0Fu) | (xb & 0xF0F0F0F0u);
                 }
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                uint32_t af[2][4];
+              for (int t2 = 0; t2 < 4; t2 += 2) {
+                uint32_t af[2][2][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) af[h][e] = hmul2_u32(e2m1_byte(x[h][e], t), e < 2 ? s01[h] : s23[h]);
+                  for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      af[q][h][e] = hmul2_u32(e2m1_byte(x[h][e], t2 + q), e < 2 ? s01[h] : s23[h]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                  float d[4];
-                  mma_f16_first(d, af[0], pl[0][n][0], pl[0][n][1]);
-                  mma_f16(d, af[1], pl[1][n][0], pl[1][n][1]);
-                  mma_f16(d, af[0], ph[0][n][0], ph[0][n][1]);
-                  mma_f16(d, af[1], ph[1][n][0], ph[1][n][1]);
+                  float d[2][4];
+                  // two sums at a time: a product waits for the one before it in its sum
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) o[n][4 * w + t][e] += d[e];
+                  for (int q = 0; q < 2; ++q) mma_f16_first(d[q], af[q][0], ph[0][n][0], ph[0][n][1]);
+#pragma unroll
+                  for (int q = 0; q < 2; ++q) mma_f16(d[q], af[q][1], ph[1][n][0], ph[1][n][1]);
+                  if constexpr (!kPack) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) mma_f16(d[q], af[q][0], pl[0][n][0], pl[0][n][1]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) mma_f16(d[q], af[q][1], pl[1][n][0], pl[1][n][1]);
+                  }
+#pragma unroll
+                  for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][4 * w + t2 + q][e] += d[q][e];
                 }
               }
             }
@@ -611,18 +719,11 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
       }
 
       // ------------------------------------------------ join the warps, 8 query vectors at a time
-      const int cta0 = run.start / per, cta1 = (run.end - 1) / per;
+      const int vunit = runs[r].vunit;
+      const int cta0 = runs[r].cta0, cta1 = runs[r].cta1;
       const bool shared = cta0 != cta1;
-      const float vmul = pow2i(head_exp(a.v_exp, g, a.status));
+      const float vmul = pow2i(runs[r].ve);
       const uint2 *tails = reinterpret_cast<const uint2 *>(s_tails);
-      uint2 qw[NT];                // columns 4 lane .. of this warp's query vectors, for the tails
-      if (a.k_tail) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int qv = min(qg0 + n * 8 + warp, p.NQ - 1);
-          qw[n] = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + out_row(p, unit, qv) + 4 * lane);
-        }
-      }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float l0 = l[n][0], l1 = l[n][1];
@@ -644,16 +745,22 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
                                                                    o[n][2 * t + 1][cc], o[n][2 * t + 1][2 + cc]);
         }
         __syncthreads();
-        const int qv = qg0 + n * 8 + warp;      // this warp's query vector
-        if (qv < p.NQ && !dead) {
+#pragma unroll 1
+        for (int k = warp; k < (kPack ? 4 : 8); k += kWarps) {
+          const int qv = q0 + n * 8 + k;        // this warp's query vector
+          if (qv >= p.NQ || dead) break;
           Part s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) s.m = fmaxf(s.m, s_m[w][warp]);
+          for (int w = 0; w < kWarps; ++w) s.m = fmaxf(s.m, s_m[w][k]);
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
-            const float wt = weight_of(s_m[w][warp], s.m);
-            const float4 v = *reinterpret_cast<const float4 *>(join + (w * 8 + warp) * kJoinRow + 4 * lane);
-            s.l = fmaf(wt, s_l[w][warp], s.l);
+            const float wt = weight_of(s_m[w][k], s.m);
+            float4 v = *reinterpret_cast<const float4 *>(join + (w * 8 + k) * kJoinRow + 4 * lane);
+            if constexpr (kPack) {
+              const float4 v2 = *reinterpret_cast<const float4 *>(join + (w * 8 + 4 + k) * kJoinRow + 4 * lane);
+              v.x += v2.x, v.y += v2.y, v.z += v2.z, v.w += v2.w;
+            }
+            s.l = fmaf(wt, s_l[w][k], s.l);
             s.o.x = fmaf(wt, v.x, s.o.x);
             s.o.y = fmaf(wt, v.y, s.o.y);
             s.o.z = fmaf(wt, v.z, s.o.z);
@@ -661,11 +768,11 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
           }
           s.o.x *= vmul, s.o.y *= vmul, s.o.z *= vmul, s.o.w *= vmul;
           if (!shared) {
-            finish(p, unit, qv, s, qw[n], tails, lane);
+            finish(p, unit, qv, s, reinterpret_cast<const uint2 *>(s_query + (n * 8 + k) * 16), tails, lane);
           } else {
-            const int64_t k = ((int64_t)blockIdx.x + run.unit) * (NT * 8) + n * 8 + warp;
-            *reinterpret_cast<float4 *>(p.part_o + k * kD + 4 * lane) = s.o;
-            if (lane == 0) *reinterpret_cast<float2 *>(p.part_ml + 2 * k) = make_float2(s.m, s.l);
+            const int64_t at = ((int64_t)blockIdx.x + vunit) * (NT * 8) + n * 8 + k;
+            *reinterpret_cast<float4 *>(p.part_o + at * kD + 4 * lane) = s.o;
+            if (lane == 0) *reinterpret_cast<float2 *>(p.part_ml + 2 * at) = make_float2(s.m, s.l);
           }
         }
         __syncthreads();
@@ -673,64 +780,75 @@ __global__ void __launch_bounds__(kThreads, attn4_ctas_per_sm(NT)) k_attn4(const
       if (shared) {
         // the barrier above orders the CTA's parts before the count, the one below the count before the reads
         if (tid == 0) {
-          const bool last = atom_add_acq_rel_gpu(p.arrive + run.unit, 1) == cta1 - cta0;
-          if (last) p.arrive[run.unit] = 0;     // for the next call
+          const bool last = atom_add_acq_rel_gpu(p.arrive + vunit, 1) == cta1 - cta0;
+          if (last) p.arrive[vunit] = 0;        // for the next call
           s_flag = last;
         }
         __syncthreads();
         const bool last = s_flag != 0;
         if (last && !dead) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const int qv = qg0 + n * 8 + warp;
+#pragma unroll 1
+          for (int k = warp; k < NT * 8; k += kWarps) {
+            const int qv = q0 + k;
             if (qv >= p.NQ) break;
+            // 32 parts at a time: a lane holds one's reference and weight, the sums of eight are in flight
             Part s = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-            for (int k0 = cta0; k0 <= cta1; k0 += 4) {
-              float2 ml[4];
-              float4 v[4];
+            for (int k0 = cta0; k0 <= cta1; k0 += 32) {
+              const int np = min(32, cta1 - k0 + 1);
+              const int64_t at0 = ((int64_t)k0 + vunit) * (NT * 8) + k;
+              float2 ml = make_float2(-INFINITY, 0.f);
+              if (lane < np) ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + 2 * (at0 + (int64_t)lane * (NT * 8))));
+              float mn = fmaxf(s.m, ml.x);
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const int64_t k = ((int64_t)min(k0 + t, cta1) + run.unit) * (NT * 8) + n * 8 + warp;
-                ml[t] = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + 2 * k));
-                v[t] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + k * kD + 4 * lane));
-              }
+              for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+              const float wa = weight_of(s.m, mn), wt = weight_of(ml.x, mn);
+              float lw = lane < np ? wt * ml.y : 0.f;
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                if (k0 + t > cta1) break;
-                const float mn = fmaxf(s.m, ml[t].x);
-                const float wa = weight_of(s.m, mn), wt = weight_of(ml[t].x, mn);
-                s.l = s.l * wa + wt * ml[t].y;
-                s.o.x = s.o.x * wa + wt * v[t].x;
-                s.o.y = s.o.y * wa + wt * v[t].y;
-                s.o.z = s.o.z * wa + wt * v[t].z;
-                s.o.w = s.o.w * wa + wt * v[t].w;
-                s.m = mn;
+              for (int d = 16; d > 0; d >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, d);
+              s.l = s.l * wa + lw;
+              s.o.x *= wa, s.o.y *= wa, s.o.z *= wa, s.o.w *= wa;
+              for (int t0 = 0; t0 < np; t0 += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+                  v[t] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + (at0 + (int64_t)min(t0 + t, np - 1) * (NT * 8)) * kD + 4 * lane));
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                  const float f = __shfl_sync(0xffffffffu, wt, (t0 + t) & 31);
+                  if (t0 + t < np) {
+                    s.o.x = fmaf(f, v[t].x, s.o.x);
+                    s.o.y = fmaf(f, v[t].y, s.o.y);
+                    s.o.z = fmaf(f, v[t].z, s.o.z);
+                    s.o.w = fmaf(f, v[t].w, s.o.w);
+                  }
+                }
               }
+              s.m = mn;
             }
-            finish(p, unit, qv, s, qw[n], tails, lane);
+            finish(p, unit, qv, s, reinterpret_cast<const uint2 *>(s_query + k * 16), tails, lane);
           }
         }
-        __syncthreads();   // s_flag is read
+        __syncthreads();   // s_flag, the tails and the query vectors are read
       }
+      if (r + 1 < n_runs) stage_run(runs[r + 1]);
     }
     seq += (uint32_t)n_tiles;
     if (whi >= hi) return;
   }
 }
 
-// Tiles of 8 query vectors per warp: up to 5 (their sums are 160 registers); more are
-// split into two groups, each of which goes through the pages itself.
+// Up to 8 query vectors: one tile a warp; more: groups of up to 16, each of which goes
+// through the unit's pages by itself.
 void attn4_tiles(int NQ, int &nt, int &groups) {
-  const int tiles = (NQ + 7) / 8;
-  groups = (tiles + 4) / 5;
-  nt = (tiles + groups - 1) / groups;
+  nt = NQ <= 8 ? 1 : 2;
+  groups = (NQ + nt * 8 - 1) / (nt * 8);
 }
 
-template <int NT>
+template <int NT, bool kPack>
 cudaError_t launch_t(int grid, const Attn4Params &p, cudaStream_t s) {
-  cudaError_t e = set_dyn_smem((const void *)k_attn4<NT>, attn4_smem(NT));
+  cudaError_t e = set_dyn_smem((const void *)k_attn4<NT, kPack>, attn4_smem(NT));
   if (e != cudaSuccess) return e;
-  return launch_k(k_attn4<NT>, dim3(grid), dim3(kThreads), attn4_smem(NT), s, p);
+  return launch_k(k_attn4<NT, kPack>, dim3(grid), dim3(attn4_warps(NT) * 32), attn4_smem(NT), s, p);
 }
 
 }  // namespace
@@ -738,7 +856,7 @@ cudaError_t launch_t(int grid, const Attn4Params &p, cudaStream_t s) {
 Attn4Plan attn4_plan(int units, int NQ, int sm_count) {
   Attn4Plan pl;
   attn4_tiles(NQ, pl.nt, pl.groups);
-  pl.n_cta = sm_count > 0 ? sm_count * attn4_ctas_per_sm(pl.nt) : 1;
+  pl.n_cta = sm_count > 0 ? sm_count * 2 : 1;
   const int64_t slots = (int64_t)pl.n_cta + (int64_t)units * pl.groups;
   pl.part_o_floats = slots * pl.nt * 8 * kD;
   pl.part_ml_floats = slots * pl.nt * 8 * 2;
@@ -753,19 +871,15 @@ cudaError_t launch_attn4(const Attn4Args &a, const Attn4Plan &pl, float *part_o,
   p.NQ = a.n_q * p.G;
   p.bpc_shift = a.cs == 16 ? 0 : a.cs == 32 ? 1 : 2;
   p.groups = pl.groups;
+  p.group_q = pl.nt * 8;
   p.vunits = a.B * a.Hkv * pl.groups;
   p.part_o = part_o, p.part_ml = part_ml, p.arrive = arrive;
-  // no more CTAs than slices of kWarps tiles there can be
+  // no more CTAs than slices of a tile per warp there can be
+  const int kWarps = attn4_warps(pl.nt);
   const int64_t most = ((int64_t)p.vunits * ((((int64_t)a.umax << p.bpc_shift) + 1) / 2 + 1) + kWarps - 1) / kWarps;
   const int grid = (int)(most < pl.n_cta ? most : pl.n_cta);
-  switch (pl.nt) {
-    case 1: return launch_t<1>(grid, p, s);
-    case 2: return launch_t<2>(grid, p, s);
-    case 3: return launch_t<3>(grid, p, s);
-    case 4: return launch_t<4>(grid, p, s);
-    case 5: return launch_t<5>(grid, p, s);
-  }
-  return cudaErrorInvalidValue;
+  if (pl.nt == 2) return launch_t<2, false>(grid, p, s);
+  return p.NQ <= 4 ? launch_t<1, true>(grid, p, s) : launch_t<1, false>(grid, p, s);
 }
 
 }  // namespace dd

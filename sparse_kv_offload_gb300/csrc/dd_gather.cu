@@ -7,6 +7,7 @@
 // K or V (cs rows x 256 bytes, contiguous in both the host tensor and the
 // staging slot) with 16-byte loads issued over the host link, eight in
 // flight per lane before the stores.
+#include "dd_attn.cuh"
 #include "dd_kv4.cuh"
 
 namespace dd {
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(kGatherThreads) k_expand4(
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
-        o[e] = pack_bf2(v.x * s, v.y * s);
+        o[e] = cvt_bf16x2(v.x * s, v.y * s);
       }
       dst[i * 32] = make_uint4(o[0], o[1], o[2], o[3]);
     }

@@ -68,7 +68,7 @@ __device__ __forceinline__ float scale_inverse(uint32_t s8) {
   return s > 0.f ? __frcp_rn(s) : 0.f;
 }
 
-// Eight values (bf16 values times a power of two) -> four bytes of codes.
+// Eight bf16 values and 1/scale (times a power of two) -> four bytes of codes.
 // value * (1/scale) is within 2^-23 of the quotient.  The quotient of two
 // numbers of 8 and 4 significant bits is either one of e2m1's ties (at most
 // three significant bits) or at least 2^-9 of it away, so rounding the product

@@ -12,12 +12,17 @@
 //     r^5 and r^4;
 //   - products and sums keep their rounding errors (fma, two-sum), and the last
 //     rounding sees them as a sticky bit.
+// All of that is needed only next to a tie: a value is first computed in plain fp32
+// with a bound on its error, and where both ends of the interval round to the same
+// bf16 number that is the answer.  One lane in some 500 has to go on (26 operations a
+// value instead of 7).
 //
 // A row is 8 lanes x 16 values: lane i turns pairs 8i..8i+7 (two 16-byte pieces
 // of the row), so a token's sines and cosines are computed once per lane and
 // serve all the heads that the warp goes through.  Bound by HBM.
 #include <math.h>
 
+#include "dd_attn.cuh"
 #include "dd_kv4.cuh"
 
 namespace dd {
@@ -35,9 +40,9 @@ struct Rope {
   bool half;
 };
 
-// The eight pairs' cosines and sines at one position, hi + lo.
+// The eight pairs' cosines and sines at one position (fp32, within 2^-24 of the gain).
 struct Turn {
-  float ch[8], cl[8], sh[8], sl[8];
+  float c[8], s[8];
 };
 
 __device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
@@ -110,23 +115,31 @@ __device__ __forceinline__ void pieces(const Rope &r, int i, bool rotated, int &
 __device__ __forceinline__ void make_turn(const Rope &r, int i, int64_t pos, Turn &t) {
   if (i >= r.rot_dim / 16) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) cos_sin((uint64_t)pos * __ldg(r.freq + 8 * i + e), r.lut, t.ch[e], t.cl[e], t.sh[e], t.sl[e]);
+  for (int e = 0; e < 8; ++e) {
+    float cl, sl;
+    cos_sin((uint64_t)pos * __ldg(r.freq + 8 * i + e), r.lut, t.c[e], cl, t.s[e], sl);
+  }
 }
 
-// Rotate the lane's two pieces in place.
-__device__ __forceinline__ void rotate(const Rope &r, int i, const Turn &t, uint4 &va, uint4 &vb) {
-  if (i >= r.rot_dim / 16) return;
+// interleaved: pairs 0..3 lie in a, 4..7 in b
+__device__ __forceinline__ void pair_of(bool half, const float (&a)[8], const float (&b)[8], int e, float &x, float &y) {
+  x = half ? a[e] : (e < 4 ? a[2 * (e & 3)] : b[2 * (e & 3)]);
+  y = half ? b[e] : (e < 4 ? a[2 * (e & 3) + 1] : b[2 * (e & 3) + 1]);
+}
+
+// The lane's pieces rotated with every rounding error kept.
+__device__ __noinline__ void rotate_exactly(const Rope &r, int i, int64_t pos, uint4 &va, uint4 &vb) {
   float a[8], b[8];
   unpack8(va, a);
   unpack8(vb, b);
   uint32_t oa[8], ob[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    // interleaved: pairs 0..3 lie in a, 4..7 in b
-    const float x = r.half ? a[e] : (e < 4 ? a[2 * (e & 3)] : b[2 * (e & 3)]);
-    const float y = r.half ? b[e] : (e < 4 ? a[2 * (e & 3) + 1] : b[2 * (e & 3) + 1]);
-    oa[e] = dot2_bf16(x, t.ch[e], t.cl[e], -y, t.sh[e], t.sl[e]);
-    ob[e] = dot2_bf16(y, t.ch[e], t.cl[e], x, t.sh[e], t.sl[e]);
+    float x, y, ch, cl, sh, sl;
+    pair_of(r.half, a, b, e, x, y);
+    cos_sin((uint64_t)pos * __ldg(r.freq + 8 * i + e), r.lut, ch, cl, sh, sl);
+    oa[e] = dot2_bf16(x, ch, cl, -y, sh, sl);
+    ob[e] = dot2_bf16(y, ch, cl, x, sh, sl);
   }
   if (r.half) {
     va = make_uint4(oa[0] | oa[1] << 16, oa[2] | oa[3] << 16, oa[4] | oa[5] << 16, oa[6] | oa[7] << 16);
@@ -135,6 +148,47 @@ __device__ __forceinline__ void rotate(const Rope &r, int i, const Turn &t, uint
     va = make_uint4(oa[0] | ob[0] << 16, oa[1] | ob[1] << 16, oa[2] | ob[2] << 16, oa[3] | ob[3] << 16);
     vb = make_uint4(oa[4] | ob[4] << 16, oa[5] | ob[5] << 16, oa[6] | ob[6] << 16, oa[7] | ob[7] << 16);
   }
+}
+
+// Rotate the lane's two pieces in place.
+__device__ __forceinline__ void rotate(const Rope &r, int i, int64_t pos, const Turn &t, float gain, uint4 &va,
+                                       uint4 &vb) {
+  if (i >= r.rot_dim / 16) return;
+  float a[8], b[8];
+  unpack8(va, a);
+  unpack8(vb, b);
+  float ox[8], oy[8], err[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float x, y;
+    pair_of(r.half, a, b, e, x, y);
+    ox[e] = fmaf(x, t.c[e], -(y * t.s[e]));
+    oy[e] = fmaf(y, t.c[e], x * t.s[e]);
+    // cosine and sine are off by 2^-24 of the gain each, the product and the sum round by 2^-24 of
+    // (|x| + |y|) gain at most each: four times 2^-24 of that cover all, and the roundings of +- err with it
+    err[e] = (fabsf(x) + fabsf(y)) * gain;
+  }
+  uint32_t up[8], diff = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // neighbouring halves of the output: two x (or two y) with halves paired, x and y of a pair interleaved
+    const float p = r.half ? (e < 4 ? ox[2 * (e & 3)] : oy[2 * (e & 3)]) : ox[e];
+    const float q = r.half ? (e < 4 ? ox[2 * (e & 3) + 1] : oy[2 * (e & 3) + 1]) : oy[e];
+    const float ep = r.half ? err[2 * (e & 3)] : err[e], eq = r.half ? err[2 * (e & 3) + 1] : err[e];
+    up[e] = cvt_bf16x2(p + ep, q + eq);
+    diff |= up[e] ^ cvt_bf16x2(p - ep, q - eq);
+  }
+  if (diff) {
+    rotate_exactly(r, i, pos, va, vb);
+  } else {
+    va = make_uint4(up[0], up[1], up[2], up[3]);
+    vb = make_uint4(up[4], up[5], up[6], up[7]);
+  }
+}
+
+// the bound on an fp32 rotation's error, of (|x| + |y|): a little over 2^-22 of the gain (the cosine of angle 0)
+__device__ __forceinline__ float bound_of(const Rope &r) {
+  return r.rot_dim ? __ldg(r.lut).x * 2.5e-7f : 0.f;
 }
 
 struct Rows {          // where the rows of a call lie, in elements
@@ -178,18 +232,27 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_rows(Rope r, const uint16
   const Token k = token_of(((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 3, B, T, start_pos, new_len,
                            INT64_MAX, status);
   if (!k.ok) return;
-  Turn t;
-  make_turn(r, i, k.pos, t);
   int pa, pb;
   pieces(r, i, true, pa, pb);
-  const int h1 = min(H, (int)(blockIdx.y + 1) * heads);
-  for (int h = blockIdx.y * heads; h < h1; ++h) {
-    const uint4 *src = reinterpret_cast<const uint4 *>(x + k.b * xs.b + k.t * xs.t + h * xs.h);
-    uint4 *dst = reinterpret_cast<uint4 *>(out + k.b * os.b + k.t * os.t + h * os.h);
-    uint4 va = src[pa], vb = src[pb];
-    rotate(r, i, t, va, vb);
-    dst[pa] = va;
-    dst[pb] = vb;
+  const int h0 = blockIdx.y * heads, h1 = min(H, h0 + heads);
+  const uint4 *src = reinterpret_cast<const uint4 *>(x + k.b * xs.b + k.t * xs.t + h0 * xs.h);
+  uint4 *dst = reinterpret_cast<uint4 *>(out + k.b * os.b + k.t * os.t + h0 * os.h);
+  const int64_t xstep = xs.h / 8, ostep = os.h / 8;
+  // the next two heads' pieces are on their way while one is turned
+  uint4 a0 = src[pa], b0 = src[pb], a1 = a0, b1 = b0;
+  if (h0 + 1 < h1) a1 = src[xstep + pa], b1 = src[xstep + pb];
+  Turn t;
+  make_turn(r, i, k.pos, t);
+  const float gain = bound_of(r);
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    uint4 a2 = a1, b2 = b1;
+    if (h + 2 < h1) a2 = src[2 * xstep + pa], b2 = src[2 * xstep + pb];
+    rotate(r, i, k.pos, t, gain, a0, b0);
+    dst[pa] = a0;
+    dst[pb] = b0;
+    src += xstep, dst += ostep;
+    a0 = a1, b0 = b1, a1 = a2, b1 = b2;
   }
 }
 
@@ -222,36 +285,31 @@ __device__ __forceinline__ void store4(uint8_t *page, int row, int pa, int pb, i
   }
 }
 
-__device__ __forceinline__ float group_max(const float (&x)[8], bool &nan) {
-  float m = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    m = fmaxf(m, fabsf(x[e]));
-    nan = nan || x[e] != x[e];
-  }
-  return m;
+// The largest magnitude of eight bf16 values, as bf16 bits (a NaN's are above infinity's).
+__device__ __forceinline__ uint32_t top8(const uint4 &v) {
+  const uint32_t m = 0x7FFF7FFFu;
+  const uint32_t t = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+  return max(t & 0xFFFFu, t >> 16);
 }
 
-// Quantise the lane's two pieces.  `apart`: the other half of each piece's group of 16
-// is the neighbour lane's, else the two pieces are one group.  Every lane of the
-// eight takes part.
+// Quantise the lane's two pieces, values divided by 2^e (mul = 2^-e).  `apart`: the other
+// half of each piece's group of 16 is the neighbour lane's, else the two pieces are one
+// group.  Every lane of the eight takes part.
 __device__ __forceinline__ void quantise(const uint4 &va, const uint4 &vb, float mul, bool apart, unsigned lanes,
                                          uint32_t &ca, uint32_t &cb, uint32_t &sa, uint32_t &sb) {
+  uint32_t ta = top8(va), tb = top8(vb);
+  const uint32_t both = __shfl_xor_sync(lanes, ta | tb << 16, 1);
+  const uint32_t oa = apart ? both & 0xFFFFu : tb, ob = apart ? both >> 16 : ta;
+  ta = max(ta, oa);
+  tb = max(tb, ob);
+  // (mul is a power of two: the largest value scaled is the largest of the scaled values)
+  sa = group_scale(__uint_as_float(ta << 16) * mul, ta > 0x7F80u);
+  sb = group_scale(__uint_as_float(tb << 16) * mul, tb > 0x7F80u);
   float a[8], b[8];
   unpack8(va, a);
   unpack8(vb, b);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) a[e] *= mul, b[e] *= mul;
-  bool na = false, nb = false;
-  const float ma = group_max(a, na), mb = group_max(b, nb);
-  // a NaN travels through the maxima as a NaN
-  const float qa = na ? NAN : ma, qb = nb ? NAN : mb;
-  const float oa = __shfl_xor_sync(lanes, qa, 1), ob = __shfl_xor_sync(lanes, qb, 1);
-  const float xa = apart ? oa : qb, xb = apart ? ob : qa;
-  sa = group_scale(fmaxf(qa, xa), qa != qa || xa != xa);
-  sb = group_scale(fmaxf(qb, xb), qb != qb || xb != xb);
-  ca = encode8(a, scale_inverse(sa));
-  cb = encode8(b, scale_inverse(sb));
+  ca = encode8(a, scale_inverse(sa) * mul);
+  cb = encode8(b, scale_inverse(sb) * mul);
 }
 
 template <bool kFour>
@@ -263,19 +321,26 @@ __global__ void __launch_bounds__(kRopeThreads) k_append(AppendP p) {
   const Token k = token_of(((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 3, p.B, p.T, p.start_pos, p.new_len,
                            (int64_t)p.C << p.shift, p.status);
   if (!k.ok) return;
-  Turn t;
-  make_turn(p.r, i, k.pos, t);
   int pa, pb;
   pieces(p.r, i, true, pa, pb);
   const bool apart = pb != pa + 1;
   const int c = (int)(k.pos >> p.shift), row = (int)(k.pos & (p.cs - 1));
   const int64_t page_bytes = (int64_t)p.cs * (kFour ? kRow4 : 2 * kD);
-  const int h1 = min(p.H, (int)(blockIdx.y + 1) * p.heads);
-  for (int h = blockIdx.y * p.heads; h < h1; ++h) {
-    const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k + k.b * p.ks.b + k.t * p.ks.t + h * p.ks.h);
-    const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v + k.b * p.vs.b + k.t * p.vs.t + h * p.vs.h);
-    uint4 ka = ksrc[pa], kb = ksrc[pb];
-    const uint4 va = vsrc[2 * i], vb = vsrc[2 * i + 1];
+  const int h0 = blockIdx.y * p.heads, h1 = min(p.H, h0 + p.heads);
+  const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k + k.b * p.ks.b + k.t * p.ks.t + h0 * p.ks.h);
+  const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v + k.b * p.vs.b + k.t * p.vs.t + h0 * p.vs.h);
+  uint4 nka = ksrc[pa], nkb = ksrc[pb], nva = vsrc[2 * i], nvb = vsrc[2 * i + 1];
+  Turn t;
+  make_turn(p.r, i, k.pos, t);
+  const float gain = bound_of(p.r);
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    uint4 ka = nka, kb = nkb;
+    const uint4 va = nva, vb = nvb;
+    if (h + 1 < h1) {          // the next head's rows are on their way
+      ksrc += p.ks.h / 8, vsrc += p.vs.h / 8;
+      nka = ksrc[pa], nkb = ksrc[pb], nva = vsrc[2 * i], nvb = vsrc[2 * i + 1];
+    }
     const int64_t chunk = ((int64_t)k.b * p.H + h) * p.C + c;
     int64_t slot = -1;
     if (p.Khot) {
@@ -285,7 +350,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_append(AppendP p) {
         slot = -1;
       }
     }
-    rotate(p.r, i, t, ka, kb);
+    rotate(p.r, i, k.pos, t, gain, ka, kb);
     if (kFour) {
       uint32_t kca, kcb, ksa, ksb, vca, vcb, vsa, vsb;
       quantise(ka, kb, pow2i(-head_exp(p.k_exp, h, p.status)), apart, lanes, kca, kcb, ksa, ksb);
@@ -326,13 +391,13 @@ Rope rope_of(const dd_rope *r) {
   return k;
 }
 
-// Heads per warp: all of them while the tokens alone give every SM its 16 warps of
-// 4 tokens, else as few as it takes to fill them (a step of a few tokens has one
-// head per warp, so its latency is one row's).
+// Heads per warp: one while that does not give every SM 16 warps (of 4 tokens), so
+// that a step of a few tokens takes one row's time; else 16 at most (by then a token's
+// sines and cosines are a tenth of the work), in groups of one size.
 int heads_per_warp(int64_t tokens, int H, int sm_count) {
-  const int64_t warps = (tokens + 3) / 4;
-  const int64_t want = (int64_t)sm_count * 16;
-  const int64_t groups = warps >= want ? 1 : (want + warps - 1) / warps;
+  const int64_t warps = (tokens + 3) / 4, want = (int64_t)sm_count * 16;
+  int64_t groups = (H + 15) / 16;
+  if (groups * warps < want) groups = (want + warps - 1) / warps;
   return groups >= H ? 1 : (int)((H + groups - 1) / groups);
 }
 

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -83,16 +84,10 @@ class RopeRef(ctypes.Structure):
     _fields_ = [("table", _vp), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int)]
 
 
-_stride3 = ctypes.c_int64 * 3
-
-
-class AppendArgs(ctypes.Structure):
-    _fields_ = [
-        ("k", _vp), ("v", _vp), ("k_stride", _stride3), ("v_stride", _stride3), ("T", ctypes.c_int32),
-        ("format", ctypes.c_int), ("start_pos", _vp), ("new_len", _vp), ("rope", ctypes.POINTER(RopeRef)),
-        ("Kh", _vp), ("Vh", _vp), ("Khot", _vp), ("Vhot", _vp), ("resident_slot", _vp), ("k_exp", _vp),
-        ("v_exp", _vp),
-    ]
+# dd_append_args: k, v; their strides; T, format; start_pos, new_len, rope, Kh, Vh, Khot,
+# Vhot, resident_slot, k_exp, v_exp
+_append_args = struct.Struct("@2P6q2i10P")
+_strides = struct.Struct("@3q")
 
 
 def _load():
@@ -117,9 +112,8 @@ def _load():
         "dd_select_topk_mass": (i32, [_vp, _vp, _vp, _vp, f32, i32, f32, _vp]),
         "dd_prefetch_kv": (i32, [_vp, _vp, i32, i32, i32, _vp, _vp, _vp, _vp, _vp, _vp, i32, _vp]),
         "dd_rope_table": (i32, [ctypes.POINTER(RopeParams), _vp]),
-        "dd_rope_rows": (i32, [_vp, ctypes.POINTER(RopeRef), _vp, ctypes.POINTER(i64), _vp, ctypes.POINTER(i64), i32,
-                               i32, _vp, _vp, _vp]),
-        "dd_append_kv": (i32, [_vp, ctypes.POINTER(AppendArgs), _vp]),
+        "dd_rope_rows": (i32, [_vp, _vp, _vp, ctypes.c_char_p, _vp, ctypes.c_char_p, i32, i32, _vp, _vp, _vp]),
+        "dd_append_kv": (i32, [_vp, ctypes.c_char_p, _vp]),
         "dd_gather_kv4": (i32, [_vp] * 7 + [i32] + [_vp] * 3),
         "dd_sparse_attn_decode_kv4": (i32, [_vp] * 16 + [f32, _vp, _vp]),
         "dd_get_status": (i32, [_vp, ctypes.POINTER(i32)]),
@@ -183,12 +177,15 @@ def _rows(t, shape, name, writable=False):
     that are multiples of 8 elements (16 bytes), the last dimension dense."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {shape}")
+    B, T, H, _ = shape
+    if t.is_contiguous():      # dense rows: nothing more to look at
+        return t.data_ptr(), T * H * D_HEAD, H * D_HEAD, D_HEAD
     st = t.stride()
     if t.numel() and st[3] != 1:
         raise ValueError(f"{name}: the last dimension must be dense")
@@ -201,11 +198,26 @@ def _rows(t, shape, name, writable=False):
             if s < extent:
                 raise ValueError(f"{name}: rows overlap")
             extent += s * (n - 1)
-    return t.data_ptr(), _stride3(*st)
+    return t.data_ptr(), *st
+
+
+def _dev(t, dtype, numel, name):
+    """_ptr of a device tensor, None allowed: one test when all is well (a step's calls
+    take a dozen tensors each, and the host runs just ahead of the GPU)."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, dtype, numel, name=name)
 
 
 def _i32(t, numel, name, allow_none=False):
-    return _ptr(t, torch.int32, numel, name=name, allow_none=allow_none)
+    if t is None and not allow_none:
+        raise ValueError(f"{name} is required")
+    return _dev(t, torch.int32, numel, name)
 
 
 def _either(t, dtype, numel, name, allow_none=False):
@@ -222,6 +234,7 @@ class Rope:
         self.rot_dim = int(rot_dim)
         self.layout = int(layout)
         self._ref = RopeRef(_ptr(table, torch.uint8, ROPE_TABLE_BYTES, name="table"), self.rot_dim, self.layout)
+        self._addr = ctypes.addressof(self._ref)
 
 
 def rope_host_table(rot_dim, base=10000.0, scaling=0, factor=1.0, orig_len=0.0, beta_fast=32.0, beta_slow=1.0,
@@ -397,11 +410,14 @@ class Context:
         position start_pos[b] + t, rows t >= new_len[b] left out (see dd.h)."""
         if x.dim() != 4:
             raise ValueError("x must be [B, T, H, 128]")
-        B, T, H = self.shape.B, x.shape[1], x.shape[2]
-        xp, xs = _rows(x, (B, T, H, D_HEAD), "x")
-        op, os_ = _rows(out, (B, T, H, D_HEAD), "out", writable=True)
-        _chk(_lib.dd_rope_rows(self._h, ctypes.byref(rope._ref), xp, xs, op, os_, T, H, _i32(start_pos, B, "start_pos"),
-                               _i32(new_len, B, "new_len", True), _stream(stream)), "dd_rope_rows")
+        B = self.shape.B
+        _, T, H, _ = x.shape
+        shape = (B, T, H, D_HEAD)
+        xp, *xs = _rows(x, shape, "x")
+        op, *os_ = _rows(out, shape, "out", writable=True)
+        _chk(_lib.dd_rope_rows(self._h, rope._addr, xp, _strides.pack(*xs), op, _strides.pack(*os_), T, H,
+                               _i32(start_pos, B, "start_pos"), _dev(new_len, torch.int32, B, "new_len"),
+                               _stream(stream)), "dd_rope_rows")
 
     def append_kv(self, k, v, start_pos, new_len=None, rope=None, Kh=None, Vh=None, Khot=None, Vhot=None,
                   resident_slot=None, kv_format=KV_BF16, k_exp=None, v_exp=None, stream=None):
@@ -413,21 +429,19 @@ class Context:
             raise ValueError("k must be [B, T, Hkv, 128]")
         T = k.shape[1]
         four = kv_format == KV_4BIT
-        dt = torch.uint8 if four else torch.bfloat16
-        row = KV4_ROW_BYTES if four else s.d
+        dt, row = (torch.uint8, KV4_ROW_BYTES) if four else (torch.bfloat16, s.d)
         nh, nr = s.B * s.Hkv * s.L * row, self.hot_slots * s.cs * row
-        a = AppendArgs()
-        a.k, a.k_stride = _rows(k, (s.B, T, s.Hkv, D_HEAD), "k")
-        a.v, a.v_stride = _rows(v, (s.B, T, s.Hkv, D_HEAD), "v")
-        a.T, a.format = T, int(kv_format)
-        a.start_pos, a.new_len = _i32(start_pos, s.B, "start_pos"), _i32(new_len, s.B, "new_len", True)
-        if rope is not None:
-            a.rope = ctypes.pointer(rope._ref)
-        a.Kh, a.Vh = _either(Kh, dt, nh, "Kh", True), _either(Vh, dt, nh, "Vh", True)
-        a.Khot, a.Vhot = _ptr(Khot, dt, nr, name="Khot", allow_none=True), _ptr(Vhot, dt, nr, name="Vhot", allow_none=True)
-        a.resident_slot = _i32(resident_slot, s.B * s.Hkv * s.C, "resident_slot", True)
-        a.k_exp, a.v_exp = _i32(k_exp, s.Hkv, "k_exp", True), _i32(v_exp, s.Hkv, "v_exp", True)
-        _chk(_lib.dd_append_kv(self._h, ctypes.byref(a), _stream(stream)), "dd_append_kv")
+        shape = (s.B, T, s.Hkv, D_HEAD)
+        kp, *ks = _rows(k, shape, "k")
+        vp, *vs = _rows(v, shape, "v")
+        i32 = torch.int32
+        a = _append_args.pack(
+            kp, vp, *ks, *vs, T, int(kv_format), _i32(start_pos, s.B, "start_pos"),
+            _dev(new_len, i32, s.B, "new_len") or 0, rope._addr if rope is not None else 0,
+            _either(Kh, dt, nh, "Kh", True) or 0, _either(Vh, dt, nh, "Vh", True) or 0, _dev(Khot, dt, nr, "Khot") or 0,
+            _dev(Vhot, dt, nr, "Vhot") or 0, _dev(resident_slot, i32, s.B * s.Hkv * s.C, "resident_slot") or 0,
+            _dev(k_exp, i32, s.Hkv, "k_exp") or 0, _dev(v_exp, i32, s.Hkv, "v_exp") or 0)
+        _chk(_lib.dd_append_kv(self._h, a, _stream(stream)), "dd_append_kv")
 
     def gather_kv4(self, Kh, Vh, miss_list, miss_count, Kst, Vst, expand=False, k_exp=None, v_exp=None, stream=None):
         """Missing chunks of a 4-bit home cache (pinned host or device) into staging, as they
@@ -438,8 +452,8 @@ class Context:
         ns = self.max_misses * s.cs * row
         _chk(_lib.dd_gather_kv4(
             self._h, _either(Kh, torch.uint8, n, "Kh"), _either(Vh, torch.uint8, n, "Vh"),
-            _i32(miss_list, 1, "miss_list"), _i32(miss_count, 1, "miss_count"), _ptr(Kst, dt, ns, name="Kst"),
-            _ptr(Vst, dt, ns, name="Vst"), 1 if expand else 0, _i32(k_exp, s.Hkv, "k_exp", True),
+            _i32(miss_list, 1, "miss_list"), _i32(miss_count, 1, "miss_count"), _dev(Kst, dt, ns, "Kst"),
+            _dev(Vst, dt, ns, "Vst"), 1 if expand else 0, _i32(k_exp, s.Hkv, "k_exp", True),
             _i32(v_exp, s.Hkv, "v_exp", True), _stream(stream)), "dd_gather_kv4")
 
     def sparse_attn_decode_kv4(self, q, Khot, Vhot, Kst, Vst, union_slot, union_cnt, out, union_qmask=None,
@@ -453,20 +467,17 @@ class Context:
         units = s.B * s.Hkv
         nu, nt = units * s.umax, s.B * s.n_q * s.Hkv * s.d
         nq = s.B * s.n_q * s.Hq * s.d
+        u8, bf, i32 = torch.uint8, torch.bfloat16, torch.int32
+        if q is None or out is None:
+            raise ValueError("q and out are required")
         _chk(_lib.dd_sparse_attn_decode_kv4(
-            self._h, _ptr(q, torch.bfloat16, nq, name="q"),
-            _ptr(Khot, torch.uint8, nh, name="Khot", allow_none=True),
-            _ptr(Vhot, torch.uint8, nh, name="Vhot", allow_none=True),
-            _ptr(Kst, torch.uint8, ns, name="Kst", allow_none=True),
-            _ptr(Vst, torch.uint8, ns, name="Vst", allow_none=True),
-            _i32(k_exp, s.Hkv, "k_exp", True), _i32(v_exp, s.Hkv, "v_exp", True),
-            _ptr(K_tail, torch.bfloat16, nt, name="K_tail", allow_none=True),
-            _ptr(V_tail, torch.bfloat16, nt, name="V_tail", allow_none=True),
-            _i32(union_idx, nu, "union_idx", True), _i32(union_slot, nu, "union_slot"),
-            _ptr(union_qmask, torch.uint8, nu, name="union_qmask", allow_none=True),
-            _i32(union_cnt, units, "union_cnt"), _i32(miss_count, 1, "miss_count", True),
-            _i32(kv_len, s.B, "kv_len", True), float(softmax_scale),
-            _ptr(out, torch.float32, nq, name="out"), _stream(stream)), "dd_sparse_attn_decode_kv4")
+            self._h, _dev(q, bf, nq, "q"), _dev(Khot, u8, nh, "Khot"), _dev(Vhot, u8, nh, "Vhot"),
+            _dev(Kst, u8, ns, "Kst"), _dev(Vst, u8, ns, "Vst"), _dev(k_exp, i32, s.Hkv, "k_exp"),
+            _dev(v_exp, i32, s.Hkv, "v_exp"), _dev(K_tail, bf, nt, "K_tail"), _dev(V_tail, bf, nt, "V_tail"),
+            _dev(union_idx, i32, nu, "union_idx"), _i32(union_slot, nu, "union_slot"),
+            _dev(union_qmask, u8, nu, "union_qmask"), _i32(union_cnt, units, "union_cnt"),
+            _dev(miss_count, i32, 1, "miss_count"), _dev(kv_len, i32, s.B, "kv_len"), float(softmax_scale),
+            _dev(out, torch.float32, nq, "out"), _stream(stream)), "dd_sparse_attn_decode_kv4")
 
     def selftest_bounded_wait(self, kind, stream=None):
         """Run a bounded device wait that nothing signals (see dd.h); the status

@@ -54,29 +54,36 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
   return r;
 }
 
-// e4m3 nearest to amax / 6, at most 448 (0x7F, NaN, for a NaN group)
-__device__ __forceinline__ uint32_t group_scale(float amax, bool nan) {
+// A product with the reciprocal of a number is within 2^-22 of the quotient.  Where the
+// numbers have 8 and 4 significant bits, the quotient is either a tie of the format that
+// it is rounded to (at most five significant bits) or at least 2^-9 of it away, so
+// rounding the product to 16 significant bits first puts every tie back in its place.
+__device__ __forceinline__ float to_16_bits(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x80u) & ~0xFFu);
+}
+
+// Two groups' scales, the e4m3 numbers nearest to top / 6, at most 448 (0x7F, NaN, for a
+// NaN group), and mul / scale (0 for a zero scale: all codes zero).  top: the largest
+// magnitudes as bf16 bits, mul: a power of two that they are multiplied by first.
+__device__ __forceinline__ void group_scales(uint32_t top_a, uint32_t top_b, float mul, uint32_t &sa, uint32_t &sb,
+                                             float &inv_a, float &inv_b) {
+  const float a = to_16_bits(__uint_as_float(top_a << 16) * mul * (1.f / 6.f));
+  const float b = to_16_bits(__uint_as_float(top_b << 16) * mul * (1.f / 6.f));
   uint16_t s;
-  const float v = __fdiv_rn(amax, 6.f);   // a tie of e4m3 times 6 is representable: the quotient of one is exact
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(0.f), "f"(v));
-  return nan ? 0x7Fu : (uint32_t)(s & 0xFF);
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s) : "f"(b), "f"(a));
+  sa = top_a > 0x7F80u ? 0x7Fu : (uint32_t)(s & 0xFF);
+  sb = top_b > 0x7F80u ? 0x7Fu : (uint32_t)(s >> 8);
+  const uint32_t h = e4m3x2_to_half2(s);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+  inv_a = f.x > 0.f ? __fdividef(1.f, f.x) * mul : 0.f;
+  inv_b = f.y > 0.f ? __fdividef(1.f, f.y) * mul : 0.f;
 }
 
-// 1 / scale for the encoder (0 for a zero scale: all codes zero)
-__device__ __forceinline__ float scale_inverse(uint32_t s8) {
-  const float s = __half2float(__ushort_as_half((uint16_t)(e4m3x2_to_half2(s8) & 0xFFFFu)));
-  return s > 0.f ? __frcp_rn(s) : 0.f;
-}
-
-// Eight bf16 values and 1/scale (times a power of two) -> four bytes of codes.
-// value * (1/scale) is within 2^-23 of the quotient.  The quotient of two
-// numbers of 8 and 4 significant bits is either one of e2m1's ties (at most
-// three significant bits) or at least 2^-9 of it away, so rounding the product
-// to 16 significant bits first puts every tie back in its place.
+// Eight bf16 values and mul / scale -> four bytes of codes.
 __device__ __forceinline__ uint32_t encode8(const float (&x)[8], float inv) {
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __uint_as_float((__float_as_uint(x[i] * inv) + 0x80u) & ~0xFFu);
+  for (int i = 0; i < 8; ++i) y[i] = to_16_bits(x[i] * inv);
   uint32_t r;
   asm("{\n .reg .b8 b0, b1, b2, b3;\n cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
       " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"

@@ -12,10 +12,11 @@
 //     r^5 and r^4;
 //   - products and sums keep their rounding errors (fma, two-sum), and the last
 //     rounding sees them as a sticky bit.
-// All of that is needed only next to a tie: a value is first computed in plain fp32
-// with a bound on its error, and where both ends of the interval round to the same
-// bf16 number that is the answer.  One lane in some 500 has to go on (26 operations a
-// value instead of 7).
+// The sticky bit is needed only next to a tie: a value is first added up to within 2^-22
+// of itself, and where both ends of that interval round to the same bf16 number, that is
+// the answer.  One lane in a thousand has to go on (26 operations a value instead of 10).
+// (With the sines and cosines in fp32 alone the interval is as wide as the larger value's
+// error, and a third of the warps had a lane that went on.)
 //
 // A row is 8 lanes x 16 values: lane i turns pairs 8i..8i+7 (two 16-byte pieces
 // of the row), so a token's sines and cosines are computed once per lane and
@@ -40,9 +41,9 @@ struct Rope {
   bool half;
 };
 
-// The eight pairs' cosines and sines at one position (fp32, within 2^-24 of the gain).
+// The eight pairs' cosines and sines at one position, hi + lo.
 struct Turn {
-  float c[8], s[8];
+  float ch[8], cl[8], sh[8], sl[8];
 };
 
 __device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
@@ -115,10 +116,7 @@ __device__ __forceinline__ void pieces(const Rope &r, int i, bool rotated, int &
 __device__ __forceinline__ void make_turn(const Rope &r, int i, int64_t pos, Turn &t) {
   if (i >= r.rot_dim / 16) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float cl, sl;
-    cos_sin((uint64_t)pos * __ldg(r.freq + 8 * i + e), r.lut, t.c[e], cl, t.s[e], sl);
-  }
+  for (int e = 0; e < 8; ++e) cos_sin((uint64_t)pos * __ldg(r.freq + 8 * i + e), r.lut, t.ch[e], t.cl[e], t.sh[e], t.sl[e]);
 }
 
 // interleaved: pairs 0..3 lie in a, 4..7 in b
@@ -127,68 +125,55 @@ __device__ __forceinline__ void pair_of(bool half, const float (&a)[8], const fl
   y = half ? b[e] : (e < 4 ? a[2 * (e & 3) + 1] : b[2 * (e & 3) + 1]);
 }
 
-// The lane's pieces rotated with every rounding error kept.
-__device__ __noinline__ void rotate_exactly(const Rope &r, int i, int64_t pos, uint4 &va, uint4 &vb) {
-  float a[8], b[8];
-  unpack8(va, a);
-  unpack8(vb, b);
-  uint32_t oa[8], ob[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float x, y, ch, cl, sh, sl;
-    pair_of(r.half, a, b, e, x, y);
-    cos_sin((uint64_t)pos * __ldg(r.freq + 8 * i + e), r.lut, ch, cl, sh, sl);
-    oa[e] = dot2_bf16(x, ch, cl, -y, sh, sl);
-    ob[e] = dot2_bf16(y, ch, cl, x, sh, sl);
-  }
-  if (r.half) {
-    va = make_uint4(oa[0] | oa[1] << 16, oa[2] | oa[3] << 16, oa[4] | oa[5] << 16, oa[6] | oa[7] << 16);
-    vb = make_uint4(ob[0] | ob[1] << 16, ob[2] | ob[3] << 16, ob[4] | ob[5] << 16, ob[6] | ob[7] << 16);
-  } else {
-    va = make_uint4(oa[0] | ob[0] << 16, oa[1] | ob[1] << 16, oa[2] | ob[2] << 16, oa[3] | ob[3] << 16);
-    vb = make_uint4(oa[4] | ob[4] << 16, oa[5] | ob[5] << 16, oa[6] | ob[6] << 16, oa[7] | ob[7] << 16);
-  }
+// The pair's rotation with every rounding error kept.  (A function of its own: the common
+// path stays short.)
+__device__ __noinline__ uint32_t rotate_exactly(float x, float y, float ch, float cl, float sh, float sl) {
+  return dot2_bf16(x, ch, cl, -y, sh, sl) | dot2_bf16(y, ch, cl, x, sh, sl) << 16;
+}
+
+// x * (ch + cl) + y * (sh + sl), within 2^-23 of itself and 2^-36 of the larger product
+__device__ __forceinline__ float dot2_near(float x, float ch, float cl, float y, float sh, float sl) {
+  const float p = y * sh;
+  return fmaf(x, ch, p) + fmaf(x, cl, fmaf(y, sl, fmaf(y, sh, -p)));
 }
 
 // Rotate the lane's two pieces in place.
-__device__ __forceinline__ void rotate(const Rope &r, int i, int64_t pos, const Turn &t, float gain, uint4 &va,
-                                       uint4 &vb) {
+__device__ __forceinline__ void rotate(const Rope &r, int i, const Turn &t, uint4 &va, uint4 &vb) {
   if (i >= r.rot_dim / 16) return;
+  constexpr float kUp = 1.f + 2.384185791015625e-07f, kDown = 1.f - 2.384185791015625e-07f;   // 1 +- 2^-22
   float a[8], b[8];
   unpack8(va, a);
   unpack8(vb, b);
-  float ox[8], oy[8], err[8];
+  uint32_t o[8], near = 0;      // pairs {x, y}; bit e: pair e is next to a tie
+  float finite = 0.f;           // NaN once a value is infinite or NaN
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float x, y;
     pair_of(r.half, a, b, e, x, y);
-    ox[e] = fmaf(x, t.c[e], -(y * t.s[e]));
-    oy[e] = fmaf(y, t.c[e], x * t.s[e]);
-    // cosine and sine are off by 2^-24 of the gain each, the product and the sum round by 2^-24 of
-    // (|x| + |y|) gain at most each: four times 2^-24 of that cover all, and the roundings of +- err with it
-    err[e] = (fabsf(x) + fabsf(y)) * gain;
+    const float p = dot2_near(x, t.ch[e], t.cl[e], -y, t.sh[e], t.sl[e]);
+    const float q = dot2_near(y, t.ch[e], t.cl[e], x, t.sh[e], t.sl[e]);
+    o[e] = cvt_bf16x2(p * kUp, q * kUp);
+    if (o[e] != cvt_bf16x2(p * kDown, q * kDown)) near |= 1u << e;
+    finite = fmaf(p, 0.f, fmaf(q, 0.f, finite));
   }
-  uint32_t up[8], diff = 0;
+  if (finite != finite) near = 0xFFu;      // the error terms of infinities say nothing
+  if (near) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // neighbouring halves of the output: two x (or two y) with halves paired, x and y of a pair interleaved
-    const float p = r.half ? (e < 4 ? ox[2 * (e & 3)] : oy[2 * (e & 3)]) : ox[e];
-    const float q = r.half ? (e < 4 ? ox[2 * (e & 3) + 1] : oy[2 * (e & 3) + 1]) : oy[e];
-    const float ep = r.half ? err[2 * (e & 3)] : err[e], eq = r.half ? err[2 * (e & 3) + 1] : err[e];
-    up[e] = cvt_bf16x2(p + ep, q + eq);
-    diff |= up[e] ^ cvt_bf16x2(p - ep, q - eq);
+    for (int e = 0; e < 8; ++e) {
+      float x, y;
+      pair_of(r.half, a, b, e, x, y);
+      if (near >> e & 1u) o[e] = rotate_exactly(x, y, t.ch[e], t.cl[e], t.sh[e], t.sl[e]);
+    }
   }
-  if (diff) {
-    rotate_exactly(r, i, pos, va, vb);
+  if (r.half) {
+    va = make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410), __byte_perm(o[4], o[5], 0x5410),
+                    __byte_perm(o[6], o[7], 0x5410));
+    vb = make_uint4(__byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632), __byte_perm(o[4], o[5], 0x7632),
+                    __byte_perm(o[6], o[7], 0x7632));
   } else {
-    va = make_uint4(up[0], up[1], up[2], up[3]);
-    vb = make_uint4(up[4], up[5], up[6], up[7]);
+    va = make_uint4(o[0], o[1], o[2], o[3]);
+    vb = make_uint4(o[4], o[5], o[6], o[7]);
   }
-}
-
-// the bound on an fp32 rotation's error, of (|x| + |y|): a little over 2^-22 of the gain (the cosine of angle 0)
-__device__ __forceinline__ float bound_of(const Rope &r) {
-  return r.rot_dim ? __ldg(r.lut).x * 2.5e-7f : 0.f;
 }
 
 struct Rows {          // where the rows of a call lie, in elements
@@ -243,12 +228,11 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_rows(Rope r, const uint16
   if (h0 + 1 < h1) a1 = src[xstep + pa], b1 = src[xstep + pb];
   Turn t;
   make_turn(r, i, k.pos, t);
-  const float gain = bound_of(r);
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
     uint4 a2 = a1, b2 = b1;
     if (h + 2 < h1) a2 = src[2 * xstep + pa], b2 = src[2 * xstep + pb];
-    rotate(r, i, k.pos, t, gain, a0, b0);
+    rotate(r, i, t, a0, b0);
     dst[pa] = a0;
     dst[pb] = b0;
     src += xstep, dst += ostep;
@@ -303,13 +287,13 @@ __device__ __forceinline__ void quantise(const uint4 &va, const uint4 &vb, float
   ta = max(ta, oa);
   tb = max(tb, ob);
   // (mul is a power of two: the largest value scaled is the largest of the scaled values)
-  sa = group_scale(__uint_as_float(ta << 16) * mul, ta > 0x7F80u);
-  sb = group_scale(__uint_as_float(tb << 16) * mul, tb > 0x7F80u);
+  float ia, ib;
+  group_scales(ta, tb, mul, sa, sb, ia, ib);
   float a[8], b[8];
   unpack8(va, a);
   unpack8(vb, b);
-  ca = encode8(a, scale_inverse(sa) * mul);
-  cb = encode8(b, scale_inverse(sb) * mul);
+  ca = encode8(a, ia);
+  cb = encode8(b, ib);
 }
 
 template <bool kFour>
@@ -332,7 +316,6 @@ __global__ void __launch_bounds__(kRopeThreads) k_append(AppendP p) {
   uint4 nka = ksrc[pa], nkb = ksrc[pb], nva = vsrc[2 * i], nvb = vsrc[2 * i + 1];
   Turn t;
   make_turn(p.r, i, k.pos, t);
-  const float gain = bound_of(p.r);
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
     uint4 ka = nka, kb = nkb;
@@ -350,7 +333,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_append(AppendP p) {
         slot = -1;
       }
     }
-    rotate(p.r, i, k.pos, t, gain, ka, kb);
+    rotate(p.r, i, t, ka, kb);
     if (kFour) {
       uint32_t kca, kcb, ksa, ksb, vca, vcb, vsa, vsb;
       quantise(ka, kb, pow2i(-head_exp(p.k_exp, h, p.status)), apart, lanes, kca, kcb, ksa, ksb);

@@ -219,7 +219,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   add(16 * units, 8);                          // union and miss offsets by the last CTA (a line per unit)
   add(3, 4);                                   // ticket counters + look-back epoch
   add(1, 8);                                   // self-test word
-  add(units * c->plan4.groups, 4);             // 4-bit attention: arrival counters
+  add(units, 4);             // 4-bit attention: arrival counters
   if (cudaMalloc(&c->ws, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   uint8_t *cur = static_cast<uint8_t *>(c->ws);
   c->status = carve<int32_t>(cur, 1);
@@ -242,7 +242,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   c->lb_pref = carve<unsigned long long>(cur, 16 * units);
   c->ticket = carve<int32_t>(cur, 3);
   c->diag_word = carve<unsigned long long>(cur, 1);
-  c->arrive4 = carve<int32_t>(cur, units * c->plan4.groups);
+  c->arrive4 = carve<int32_t>(cur, units);
   if (cudaMemset(c->ws, 0, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   const int32_t first_epoch = 1;   // look-back words start zeroed, i.e. with epoch 0
   if (cudaMemcpy(c->ticket + 2, &first_epoch, sizeof(first_epoch), cudaMemcpyHostToDevice) != cudaSuccess)
@@ -742,7 +742,7 @@ dd_status dd_sparse_attn_decode_kv4(dd_ctx *c, const void *q, const void *Khot, 
   if (c->max_misses > 0 && (!Kst || !Vst || !aligned16(Kst) || !aligned16(Vst))) return DD_ERR_INVALID_ARG;
   const dd_dims &d = c->dims;
   // blocks of 16 rows are numbered with 32 bits
-  if ((int64_t)c->units * c->plan4.groups * ((int64_t)c->umax * (d.cs / 16) + 1) >= (int64_t(1) << 30))
+  if ((int64_t)c->units * ((int64_t)c->umax * (d.cs / 16) + 1) >= (int64_t(1) << 30))
     return DD_ERR_INVALID_ARG;
   DD_TRY(on_device(c));
   dd::Attn4Args a{};

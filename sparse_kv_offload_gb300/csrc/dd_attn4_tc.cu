@@ -1,0 +1,463 @@
+// Attention over 4-bit pages on the fifth-generation tensor cores, for more than 16
+// query vectors per KV head.
+//
+// With many query vectors the products, not the bytes, bound the mma.sync kernel
+// (dd_attn4.cu), and its groups of 16 decode a unit's pages once each.  Here a page is
+// decoded once, into shared memory, for up to 64 query vectors, and the accumulators
+// live in tensor memory.  One CTA per SM; a tile is 64 rows (four blocks):
+//   warp 12     asks for a tile's blocks (bulk copies into a ring of four tiles)
+//   warps 8-11  decode one block each: fp16 K and V (a code times its scale is exact), in
+//               the 128-byte-swizzled layout that the products read, three tiles deep
+//   warp 13     S = Q K^T (M = 64 query vectors, N = 64 rows, K = 128), double-buffered in
+//               tensor memory, and O += P V (N = 128 columns, K = 64 rows)
+//   warps 0-7   softmax, four threads a query vector (the M = 64 layout: row r in lane 32 (r
+//               / 16) + r % 16); P goes to shared memory as two fp16 parts (22 bits)
+// The tensor cores add up at most kFold tiles: then, and where a score exceeds the
+// softmax's reference by 2^8, the softmax threads take O over into fp32 registers, where
+// additions round to nearest, and the next product overwrites it.
+//
+// Bound by the softmax threads' chain per tile (about 1000 cycles, of which the products
+// take 770); the decoding (16 KB written a tile) and the loads hide behind it.
+#include "dd_attn4.cuh"
+
+namespace dd {
+
+namespace {
+
+constexpr int kSoft = 8;                            // softmax warps
+constexpr int kDecode = 4;                          // decoding warps, one per block of a tile
+constexpr int kTcThreads = (kSoft + kDecode + 2) * 32;
+constexpr int kTcM = 64;
+constexpr int kRaw = 4, kKv = 3;                    // tiles: as they are, and decoded
+constexpr int kRawBytes = 4 * 2 * kBlk4;
+constexpr int kHalf = 64 * 128;                     // 64 rows of 64 fp16 values
+constexpr int kKvBytes = 4 * kHalf;                 // K lo, K hi, V lo, V hi
+constexpr int kMeta = 16;                           // tiles' records
+constexpr int kFold = 8;
+constexpr int kTcJoinRow = 132;
+constexpr uint32_t kTmemCols = 256;                 // S: 2 x 64 columns, O: 128
+constexpr size_t kTcSmem = 1024 + (size_t)kKv * kKvBytes + 2 * kHalf + 4 * kHalf + (size_t)kRaw * kRawBytes +
+                           (size_t)kTcM * kTcJoinRow * 4;
+
+// kind::f16 instruction descriptor with fp16 A and B: fp32 accumulator, B's major-ness, N, M
+constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+  return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft * 32) : "memory"); }
+
+// A block's 16 rows of 128 values -> fp16, 16-byte pieces of 8 values: a lane takes piece c
+// of rows 2 it + lane / 16.  dst: the tile's lo half at the block's first row.
+template <bool kV>
+__device__ __forceinline__ uint32_t decode_block(uint32_t raw, uint32_t dst, int rows, int lane) {
+  const int c = lane & 15, half = lane >> 4;
+  uint32_t nan = 0;      // rows' groups that are NaN (this lane's group, one bit)
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int row = 2 * it + half;
+    uint32_t s = lds8(raw + kBlk4Scales + row * 8 + (c >> 1));
+    const uint32_t w = lds32(raw + row * 64 + c * 4);
+    if (kV) {
+      if (row >= rows) s = 0;                       // rows behind the end may hold anything
+      if ((s & 0x7Fu) == 0x7Fu) s = 0, nan = 1;     // 0 * NaN would reach every query
+    }
+    const uint32_t s2 = e4m3x2_to_half2(s | s << 8);
+    uint32_t h[4];
+    e2m1x8_to_half2(w, h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = hmul2_u32(h[e], s2);
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)((c >> 3) * kHalf + row * 128 +
+                                                                              (((c & 7) ^ (row & 7)) << 4))),
+                 "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                 : "memory");
+  }
+  return nan;
+}
+
+__global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constant__ Attn4Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  // the swizzle pattern is anchored at 1024-byte boundaries
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t kv0 = smem_u32(smem);                               // [kKv][kKvBytes]
+  const uint32_t q0s = kv0 + kKv * kKvBytes;                         // [2 halves][64 rows][128 B]
+  const uint32_t p0 = q0s + 2 * kHalf;                               // [2 tiles][2 parts][64 rows][128 B]
+  const uint32_t raw0 = p0 + 4 * kHalf;                              // [kRaw][4 blocks][K, V]
+  float *join = reinterpret_cast<float *>(smem + (raw0 - kv0) + kRaw * kRawBytes);   // [kTcM][kTcJoinRow]
+  __shared__ PlanSmem plan;
+  __shared__ __align__(8) uint64_t bars[2 * kRaw + 2 * kKv + 7];
+  __shared__ uint4 s_tails[2 * kMaxNq * 16];
+  __shared__ uint32_t s_meta[kMeta][4], s_nan[kMeta];
+  __shared__ float s_back[kTcM], s_m[kTcM], s_l[kTcM], s_red[2][kTcM];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_over[2], s_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Attn4Args &a = p.a;
+  const uint32_t raw_full = smem_u32(bars), raw_empty = raw_full + 8 * kRaw;
+  const uint32_t kv_full = raw_empty + 8 * kRaw, kv_empty = kv_full + 8 * kKv;
+  const uint32_t s_full = kv_empty + 8 * kKv, pv_done = s_full + 16, p_ready = pv_done + 16, q_full = p_ready + 8;
+  const uint32_t mma_done = q_full + 8;
+  if (tid == 0) {
+    for (int i = 0; i < kRaw; ++i) mbar_init(raw_full + 8 * i, 4), mbar_init(raw_empty + 8 * i, kDecode);
+    for (int i = 0; i < kKv; ++i) mbar_init(kv_full + 8 * i, kDecode), mbar_init(kv_empty + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(pv_done + 8 * i, 1);
+    mbar_init(p_ready, 1);
+    mbar_init(q_full, 1);
+    mbar_init(mma_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  pdl_trigger();
+  Slice<kTcThreads, 1, 2> slice;
+  if (!slice.open(p, plan)) return;
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * kTcM;
+  const uint32_t all_q = (1u << a.n_q) - 1u;
+
+  // Every role walks the same tiles and numbers them alike.  A wait that runs out (2 s)
+  // only ends that thread's waiting: the barriers below are still met by all.
+  int t = 0, run_no = 0;
+  bool alive = true;
+  auto wait = [&](uint32_t bar, int parity) {
+    if (alive && !mbar_wait(bar, (uint32_t)parity & 1u, a.status)) alive = false;
+  };
+
+  for (int w0 = 0;; w0 += kMaxRuns) {
+    int wlo, whi;
+    const int n_runs = slice.list(p, plan, w0, wlo, whi);
+    const Run *runs = plan.runs;
+    const int n_tiles = whi - wlo;
+
+    if (slice.dead) {
+      // an error is pending: no work, but the counts of shared units go on
+      if (tid == 0)
+        for (int r = 0; r < n_runs; ++r)
+          if (runs[r].cta0 != runs[r].cta1 &&
+              atom_add_acq_rel_gpu(p.arrive + runs[r].unit, 1) == runs[r].cta1 - runs[r].cta0)
+            p.arrive[runs[r].unit] = 0;
+    } else if (warp == kSoft + kDecode) {
+      // ------------------------------------------------------------- loads
+      for (int i0 = 0; i0 < n_tiles; i0 += 8) {
+        // lane 4 k + h: block h of tile i0 + k
+        BlockRef ref = {0, 0u};
+        const int x = wlo + i0 + (lane >> 2);
+        if (x < whi) {
+          int r = 0;
+#pragma unroll
+          for (int step = kMaxRuns / 2; step > 0; step >>= 1)
+            if (r + step < n_runs && runs[r + step].start <= x) r += step;
+          ref = look_up(p, runs[r], 4 * (x - runs[r].start) + (lane & 3), slice.staged, all_q);
+        }
+        for (int k = 0; k < 8 && i0 + k < n_tiles; ++k, ++t) {
+          const int st = t % kRaw;
+          if (t >= kRaw) wait(raw_empty + 8 * st, t / kRaw - 1);
+          __syncwarp();
+          if ((lane >> 2) == k) {
+            s_meta[t % kMeta][lane & 3] = ref.meta;
+            if ((lane & 3) == 0) s_nan[t % kMeta] = 0u;
+            __threadfence_block();
+          }
+          __syncwarp();
+          if ((lane >> 2) == k) {
+            if (ref.meta && alive)
+              load_block(p, ref, raw0 + st * kRawBytes + (lane & 3) * 2 * kBlk4, raw_full + 8 * st);
+            else
+              mbar_arrive(raw_full + 8 * st);
+          }
+        }
+      }
+    } else if (warp >= kSoft && warp < kSoft + kDecode) {
+      // ------------------------------------------------------------ decoding
+      const int blk = warp - kSoft;
+      for (int i = 0; i < n_tiles; ++i, ++t) {
+        const int st = t % kRaw, b = t % kKv;
+        wait(raw_full + 8 * st, t / kRaw);
+        if (t >= kKv) wait(kv_empty + 8 * b, t / kKv - 1);
+        const uint32_t meta = s_meta[t % kMeta][blk];
+        const uint32_t raw = raw0 + st * kRawBytes + blk * 2 * kBlk4, dst = kv0 + b * kKvBytes + blk * 16 * 128;
+        decode_block<false>(raw, dst, 16, lane);
+        const uint32_t nan = decode_block<true>(raw + kBlk4, dst + 2 * kHalf, (int)(meta >> 8) & 31, lane);
+        if (nan) atomicOr(&s_nan[t % kMeta], 1u << (blk * 8 + ((lane & 15) >> 1)));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(raw_empty + 8 * st);
+          mbar_arrive(kv_full + 8 * b);
+        }
+      }
+    } else if (warp == kSoft + kDecode + 1) {
+      // ------------------------------------------------------------ products
+      if (lane == 0) {
+        constexpr uint32_t id_s = idesc_f16(kTcM, 64, 0), id_o = idesc_f16(kTcM, 128, 1);
+        auto issue_pv = [&](int u) {
+          wait(p_ready, u);
+          tc_fence_after();
+          if (!alive) return;
+          const uint32_t pa = p0 + (u & 1) * 2 * kHalf, vb = kv0 + (u % kKv) * kKvBytes + 2 * kHalf;
+          const bool over = s_over[u & 1] != 0;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t b = smem_desc_sw128(vb + ks * 16 * 128, kHalf, 1024);
+            tc_mma(tmem_o, smem_desc_sw128(pa + ks * 32, 16, 1024), b, id_o, !(over && ks == 0));
+            tc_mma(tmem_o, smem_desc_sw128(pa + kHalf + ks * 32, 16, 1024), b, id_o, 1);
+          }
+          tc_commit(kv_empty + 8 * (u % kKv));
+          tc_commit(pv_done + 8 * (u & 1));
+        };
+        int x = wlo;
+        for (int r = 0; r < n_runs; ++r, ++run_no) {
+          const int end = min(whi, runs[r].end);
+          wait(q_full, run_no);
+          for (; x < end; ++x, ++t) {
+            wait(kv_full + 8 * (t % kKv), t / kKv);
+            tc_fence_after();
+            if (alive) {
+              // the softmax threads are done with S(t - 2): P(t - 2) was ready
+              const uint32_t kb = kv0 + (t % kKv) * kKvBytes;
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                tc_mma(tmem + (t & 1) * kTcM, smem_desc_sw128(q0s + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024),
+                       smem_desc_sw128(kb + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024), id_s, ks > 0);
+              tc_commit(s_full + 8 * (t & 1));
+            }
+            // S of this tile runs beside the softmax of the one before, its P V comes after it
+            if (x > max(wlo, runs[r].start)) issue_pv(t - 1);
+            if (x + 1 == end) issue_pv(t);
+          }
+        }
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------- softmax
+      const int wq = warp & 3, wc = warp >> 2, sub = lane >> 4;
+      const int row = 16 * wq + (lane & 15);             // query vector
+      const int bi = 2 * wc + sub;                       // block of the tile: 16 columns of S
+      const int ocol = 32 * bi;                          // and 32 of O
+      const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
+      const bool active = row < p.NQ;
+      const int j = active ? row / p.G : 31;
+      const float sl2 = a.softmax_scale * 1.4426950408889634f;
+      for (int r = 0; r < n_runs; ++r) {
+        const Run &run = runs[r];
+        const int n = min(whi, run.end) - max(wlo, run.start);
+        stage_tails(p, run, s_tails, tid, kSoft * 32);
+        {
+          // the queries: four threads a query vector, 32 values each
+          const int qv = tid >> 2, part = tid & 3;
+          uint4 w[4];
+          if (qv < p.NQ) {
+            const uint4 *src =
+                reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + out_row(p, run.unit, qv) + 32 * part);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = src[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          uint32_t f[16];
+          float back;
+          query_fragments(w, f, back);
+          if (part == 0) s_back[qv] = back * (sl2 * pow2i(run.ke));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = 4 * part + e;
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                             q0s + (uint32_t)((c >> 3) * kHalf + qv * 128 + (((c & 7) ^ (qv & 7)) << 4))),
+                         "r"(f[4 * e]), "r"(f[4 * e + 1]), "r"(f[4 * e + 2]), "r"(f[4 * e + 3])
+                         : "memory");
+          }
+        }
+        cp_async_wait_all();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        soft_barrier();
+        if (tid == 0) mbar_arrive(q_full);
+
+        const float mul = s_back[row];
+        float m = -INFINITY, l = 0.f, oacc[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) oacc[e] = 0.f;
+        int since = 0;                                   // tiles in O since it was taken over
+        for (int i = 0; i < n; ++i, ++t) {
+          wait(s_full + 8 * (t & 1), t >> 1);
+          __syncwarp();
+          tc_fence_after();
+          float x[16];
+          tmem_ld16_split<16>(tmem + lane_base + (t & 1) * kTcM + 32 * wc, x);
+          const uint32_t meta = s_meta[t % kMeta][bi];
+          const int rows = (meta & 255u) >> j & 1u ? (int)(meta >> 8) & 31 : 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = e < rows ? x[e] * mul : -INFINITY;
+          float pm = x[0];
+#pragma unroll
+          for (int e = 1; e < 16; ++e) pm = fmaxf(pm, x[e]);
+          pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 16));
+          if (sub == 0) s_red[wc][row] = pm;
+          // one barrier exchanges the halves' maxima and votes on a new reference
+          uint32_t any;
+          asm volatile(
+              "{\n .reg .pred q, r;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred r, 1, %2, q;\n selp.u32 %0, 1, 0, r;\n}\n"
+              : "=r"(any)
+              : "r"((uint32_t)(pm > m + (kLazy + kHead))), "n"(kSoft * 32)
+              : "memory");
+          const float mx = fmaxf(s_red[0][row], s_red[1][row]);
+          float factor = 1.f;
+          if (mx > m + (kLazy + kHead)) {
+            const float nm = mx - kHead;
+            factor = weight_of(m, nm);
+            m = nm;
+          }
+          const bool fold = i > 0 && (any || since == kFold);
+          // P's buffer: its last reader is PV(t - 2); O: PV(t - 1)
+          const int before = fold ? t - 1 : t - 2;
+          if (before >= 0) wait(pv_done + 8 * (before & 1), before >> 1);
+          if (fold) {
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float o[16];
+              tmem_ld16_split<32>(tmem_o + lane_base + 64 * wc + 16 * h, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) oacc[16 * h + e] = (oacc[16 * h + e] + o[e]) * factor;
+            }
+            l *= factor;
+            since = 0;
+          }
+          const uint32_t nan = s_nan[t % kMeta];
+          if (nan) {
+            // NaN groups of V: NaN for the queries that see their block
+#pragma unroll 1
+            for (int blk = 0; blk < 4; ++blk) {
+              if (!((s_meta[t % kMeta][blk] & 255u) >> j & 1u)) continue;
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (nan >> (blk * 8 + 2 * bi + h) & 1u) {
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) oacc[16 * h + e] = NAN;
+                }
+            }
+          }
+          if (active) {
+            // a query without a row so far: -inf - 0 gives weight 0, and a NaN passes
+            const float base = m == -INFINITY ? 0.f : m;
+            const uint32_t ph = p0 + (t & 1) * 2 * kHalf + row * 128;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t hi[4], lo[4];
+              float sum = 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float u = ex2_approx(x[8 * c + 2 * e] - base), v = ex2_approx(x[8 * c + 2 * e + 1] - base);
+                sum += u + v;
+                hi[e] = cvt_f16x2(u, v);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi[e]));
+                lo[e] = cvt_f16x2(u - f.x, v - f.y);
+              }
+              l += sum;
+              const uint32_t off = (uint32_t)(((2 * bi + c) ^ (row & 7)) << 4);
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(ph + off), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
+                           "r"(hi[3])
+                           : "memory");
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(ph + kHalf + off), "r"(lo[0]), "r"(lo[1]),
+                           "r"(lo[2]), "r"(lo[3])
+                           : "memory");
+            }
+          }
+          if (tid == 0) s_over[t & 1] = i == 0 || fold;
+          ++since;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          tc_fence_before();
+          soft_barrier();
+          if (tid == 0) mbar_arrive(p_ready);
+        }
+
+        // ------------------------------------------------- the run's sums
+        wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1);
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float o[16];
+          tmem_ld16_split<32>(tmem_o + lane_base + 64 * wc + 16 * h, o);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) oacc[16 * h + e] += o[e];
+        }
+        tc_fence_before();      // O is read before the next run's first product overwrites it
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (sub == 0) s_red[wc][row] = l;
+        if (bi == 0) s_m[row] = m;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<float4 *>(join + row * kTcJoinRow + ocol + 4 * e) =
+              make_float4(oacc[4 * e], oacc[4 * e + 1], oacc[4 * e + 2], oacc[4 * e + 3]);
+        soft_barrier();
+        if (tid < kTcM) s_l[tid] = s_red[0][tid] + s_red[1][tid];
+        soft_barrier();
+        const bool shared = run.cta0 != run.cta1;
+        const float vmul = pow2i(run.ve);
+        const uint2 *tails = reinterpret_cast<const uint2 *>(s_tails);
+        auto query_of = [&](int k) {
+          return a.k_tail ? *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) +
+                                                             out_row(p, run.unit, k) + 4 * lane)
+                          : make_uint2(0u, 0u);
+        };
+#pragma unroll 2
+        for (int k = warp; k < p.NQ; k += kSoft) {
+          const float4 v = *reinterpret_cast<const float4 *>(join + k * kTcJoinRow + 4 * lane);
+          const Part s = {s_m[k], s_l[k], make_float4(v.x * vmul, v.y * vmul, v.z * vmul, v.w * vmul)};
+          if (!shared) {
+            finish(p, run.unit, k, s, query_of(k), tails, lane);
+          } else {
+            const int64_t at = ((int64_t)blockIdx.x + run.unit) * p.group_q + k;
+            *reinterpret_cast<float4 *>(p.part_o + at * kD + 4 * lane) = s.o;
+            if (lane == 0) *reinterpret_cast<float2 *>(p.part_ml + 2 * at) = make_float2(s.m, s.l);
+          }
+        }
+        soft_barrier();
+        if (shared) {
+          // the barrier above orders the CTA's parts before the count, the one below the count before the reads
+          if (tid == 0) {
+            const bool last = atom_add_acq_rel_gpu(p.arrive + run.unit, 1) == run.cta1 - run.cta0;
+            if (last) p.arrive[run.unit] = 0;        // for the next call
+            s_last = last;
+          }
+          soft_barrier();
+          if (s_last)
+            for (int k = warp; k < p.NQ; k += kSoft)
+              finish(p, run.unit, k, combine_parts(p, run, k, lane), query_of(k), tails, lane);
+          soft_barrier();       // s_last and the tails are read
+        }
+      }
+    }
+    if (whi >= slice.hi) break;
+  }
+  // every product issued is done before the tensor memory is freed
+  if (warp == kSoft + kDecode + 1 && lane == 0) {
+    tc_commit(mma_done);
+    mbar_wait(mma_done, 0, a.status);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attn4_tc(int grid, const Attn4Params &p, cudaStream_t s) {
+  cudaError_t e = set_dyn_smem((const void *)k_attn4_tc, kTcSmem);
+  if (e != cudaSuccess) return e;
+  return launch_k(k_attn4_tc, dim3(grid), dim3(kTcThreads), kTcSmem, s, p);
+}
+
+}  // namespace dd

@@ -404,11 +404,11 @@ struct Attn4Args {
   int32_t *status;
 };
 struct Attn4Plan {
-  int nt, groups, n_cta;
+  int nt, group_q, n_cta;
   int64_t part_o_floats, part_ml_floats;
 };
 Attn4Plan attn4_plan(int units, int NQ, int sm_count);
-// part_o, part_ml: the plan's floats; arrive: [units * groups] counters, zero (and left zero)
+// part_o, part_ml: the plan's floats; arrive: [units] counters, zero (and left zero)
 cudaError_t launch_attn4(const Attn4Args &a, const Attn4Plan &plan, float *part_o, float *part_ml, int32_t *arrive,
                          cudaStream_t s);
 }  // namespace dd

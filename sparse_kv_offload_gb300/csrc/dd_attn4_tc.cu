@@ -51,22 +51,25 @@ __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" 
 template <bool kV>
 __device__ __forceinline__ uint32_t decode_block(uint32_t raw, uint32_t dst, int rows, int lane) {
   const int c = lane & 15, half = lane >> 4;
+  const uint32_t codes = raw + half * 64 + c * 4, scales = raw + kBlk4Scales + half * 8 + (c >> 1);
+  dst += (uint32_t)((c >> 3) * kHalf + half * 128);
   uint32_t nan = 0;      // rows' groups that are NaN (this lane's group, one bit)
+  uint32_t w[8], s[8];   // all loads first: the eight pieces' chains then overlap
+#pragma unroll
+  for (int it = 0; it < 8; ++it) s[it] = lds8(scales + it * 16), w[it] = lds32(codes + it * 128);
 #pragma unroll
   for (int it = 0; it < 8; ++it) {
     const int row = 2 * it + half;
-    uint32_t s = lds8(raw + kBlk4Scales + row * 8 + (c >> 1));
-    const uint32_t w = lds32(raw + row * 64 + c * 4);
     if (kV) {
-      if (row >= rows) s = 0;                       // rows behind the end may hold anything
-      if ((s & 0x7Fu) == 0x7Fu) s = 0, nan = 1;     // 0 * NaN would reach every query
+      if (row >= rows) s[it] = 0;                           // rows behind the end may hold anything
+      if ((s[it] & 0x7Fu) == 0x7Fu) s[it] = 0, nan = 1;     // 0 * NaN would reach every query
     }
-    const uint32_t s2 = e4m3x2_to_half2(s | s << 8);
+    const uint32_t s2 = e4m3x2_to_half2(s[it] * 0x101u);
     uint32_t h[4];
-    e2m1x8_to_half2(w, h);
+    e2m1x8_to_half2(w[it], h);
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = hmul2_u32(h[e], s2);
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)((c >> 3) * kHalf + row * 128 +
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)(it * 256 +
                                                                               (((c & 7) ^ (row & 7)) << 4))),
                  "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                  : "memory");
@@ -196,18 +199,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
     } else if (warp == kSoft + kDecode + 1) {
       // ------------------------------------------------------------ products
       if (lane == 0) {
+        // (descriptors hold addresses in 16-byte units: a step adds a constant)
         constexpr uint32_t id_s = idesc_f16(kTcM, 64, 0), id_o = idesc_f16(kTcM, 128, 1);
+        const uint64_t q_desc = smem_desc_sw128(q0s, 16, 1024), k_desc = smem_desc_sw128(kv0, 16, 1024);
+        const uint64_t p_desc = smem_desc_sw128(p0, 16, 1024), v_desc = smem_desc_sw128(kv0 + 2 * kHalf, kHalf, 1024);
         auto issue_pv = [&](int u) {
           wait(p_ready, u);
           tc_fence_after();
           if (!alive) return;
-          const uint32_t pa = p0 + (u & 1) * 2 * kHalf, vb = kv0 + (u % kKv) * kKvBytes + 2 * kHalf;
+          const uint64_t pa = p_desc + (uint32_t)((u & 1) * (2 * kHalf / 16));
+          const uint64_t vb = v_desc + (uint32_t)((u % kKv) * (kKvBytes / 16));
           const bool over = s_over[u & 1] != 0;
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t b = smem_desc_sw128(vb + ks * 16 * 128, kHalf, 1024);
-            tc_mma(tmem_o, smem_desc_sw128(pa + ks * 32, 16, 1024), b, id_o, !(over && ks == 0));
-            tc_mma(tmem_o, smem_desc_sw128(pa + kHalf + ks * 32, 16, 1024), b, id_o, 1);
+            const uint64_t b = vb + ks * 16 * 128 / 16;
+            tc_mma(tmem_o, pa + ks * 32 / 16, b, id_o, !(over && ks == 0));
+            tc_mma(tmem_o, pa + (kHalf + ks * 32) / 16, b, id_o, 1);
           }
           tc_commit(kv_empty + 8 * (u % kKv));
           tc_commit(pv_done + 8 * (u & 1));
@@ -221,11 +228,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
             tc_fence_after();
             if (alive) {
               // the softmax threads are done with S(t - 2): P(t - 2) was ready
-              const uint32_t kb = kv0 + (t % kKv) * kKvBytes;
+              const uint64_t kb = k_desc + (uint32_t)((t % kKv) * (kKvBytes / 16));
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                tc_mma(tmem + (t & 1) * kTcM, smem_desc_sw128(q0s + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024),
-                       smem_desc_sw128(kb + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024), id_s, ks > 0);
+              for (int ks = 0; ks < 8; ++ks) {
+                const int off = ((ks >> 2) * kHalf + (ks & 3) * 32) / 16;
+                tc_mma(tmem + (t & 1) * kTcM, q_desc + off, kb + off, id_s, ks > 0);
+              }
               tc_commit(s_full + 8 * (t & 1));
             }
             // S of this tile runs beside the softmax of the one before, its P V comes after it
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
       const int bi = 2 * wc + sub;                       // block of the tile: 16 columns of S
       const int ocol = 32 * bi;                          // and 32 of O
       const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-      const bool active = row < p.NQ;
+      const bool active = row < p.NQ, some = 16 * wq < p.NQ;     // some: of this warp's query vectors
       const int j = active ? row / p.G : 31;
       const float sl2 = a.softmax_scale * 1.4426950408889634f;
       for (int r = 0; r < n_runs; ++r) {
@@ -289,17 +297,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           wait(s_full + 8 * (t & 1), t >> 1);
           __syncwarp();
           tc_fence_after();
-          float x[16];
-          tmem_ld16_split<16>(tmem + lane_base + (t & 1) * kTcM + 32 * wc, x);
-          const uint32_t meta = s_meta[t % kMeta][bi];
-          const int rows = (meta & 255u) >> j & 1u ? (int)(meta >> 8) & 31 : 0;
+          float x[16], pm = -INFINITY;
+          if (some) {
+            tmem_ld16_split<16>(tmem + lane_base + (t & 1) * kTcM + 32 * wc, x);
+            const uint32_t meta = s_meta[t % kMeta][bi];
+            const int rows = (meta & 255u) >> j & 1u ? (int)(meta >> 8) & 31 : 0;
+            if (rows < 16) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = e < rows ? x[e] * mul : -INFINITY;
-          float pm = x[0];
+              for (int e = 0; e < 16; ++e)
+                if (e >= rows) x[e] = -INFINITY;
+            }
 #pragma unroll
-          for (int e = 1; e < 16; ++e) pm = fmaxf(pm, x[e]);
-          pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 16));
-          if (sub == 0) s_red[wc][row] = pm;
+            for (int e = 0; e < 16; ++e) x[e] *= mul;
+            float m8[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m8[e] = fmaxf(x[e], x[e + 8]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m8[e] = fmaxf(m8[e], m8[e + 4]);
+            pm = fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3]));
+            pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, 16));
+            if (sub == 0) s_red[wc][row] = pm;
+          }
           // one barrier exchanges the halves' maxima and votes on a new reference
           uint32_t any;
           asm volatile(
@@ -307,7 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
               : "=r"(any)
               : "r"((uint32_t)(pm > m + (kLazy + kHead))), "n"(kSoft * 32)
               : "memory");
-          const float mx = fmaxf(s_red[0][row], s_red[1][row]);
+          const float mx = some ? fmaxf(s_red[0][row], s_red[1][row]) : -INFINITY;
           float factor = 1.f;
           if (mx > m + (kLazy + kHead)) {
             const float nm = mx - kHead;
@@ -318,7 +336,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           // P's buffer: its last reader is PV(t - 2); O: PV(t - 1)
           const int before = fold ? t - 1 : t - 2;
           if (before >= 0) wait(pv_done + 8 * (before & 1), before >> 1);
-          if (fold) {
+          if (fold && some) {
             __syncwarp();
             tc_fence_after();
 #pragma unroll
@@ -329,8 +347,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
               for (int e = 0; e < 16; ++e) oacc[16 * h + e] = (oacc[16 * h + e] + o[e]) * factor;
             }
             l *= factor;
-            since = 0;
           }
+          if (fold) since = 0;
           const uint32_t nan = s_nan[t % kMeta];
           if (nan) {
             // NaN groups of V: NaN for the queries that see their block

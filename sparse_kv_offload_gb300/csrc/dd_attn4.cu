@@ -557,7 +557,7 @@ cudaError_t launch_attn4(const Attn4Args &a, const Attn4Plan &pl, float *part_o,
   p.units = a.B * a.Hkv;
   p.part_o = part_o, p.part_ml = part_ml, p.arrive = arrive;
   // no more CTAs than slices of a tile per warp (tcgen05: of a tile) there can be
-  const int tile_blocks = pl.nt ? 2 : 4, quantum = pl.nt ? attn4_warps(pl.nt) : 1;
+  const int tile_blocks = pl.nt ? 2 : 8, quantum = pl.nt ? attn4_warps(pl.nt) : 1;
   const int64_t blocks = (int64_t)a.umax << p.bpc_shift;
   const int64_t most = ((int64_t)p.units * ((blocks + tile_blocks - 1) / tile_blocks + 1) + quantum - 1) / quantum;
   const int grid = (int)(most < pl.n_cta ? most : pl.n_cta);

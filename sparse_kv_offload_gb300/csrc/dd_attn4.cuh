@@ -366,7 +366,7 @@ struct Slice {
   }
 };
 
-// dd_attn4_tc.cu: one CTA per SM, tiles of 64 rows, all query vectors of a unit at once
+// dd_attn4_tc.cu: one CTA per SM, tiles of 128 rows, all query vectors of a unit at once
 cudaError_t launch_attn4_tc(int grid, const Attn4Params &p, cudaStream_t s);
 
 }  // namespace dd

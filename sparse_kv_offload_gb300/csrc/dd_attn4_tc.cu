@@ -4,20 +4,23 @@
 // With many query vectors the products, not the bytes, bound the mma.sync kernel
 // (dd_attn4.cu), and its groups of 16 decode a unit's pages once each.  Here a page is
 // decoded once, into shared memory, for up to 64 query vectors, and the accumulators
-// live in tensor memory.  One CTA per SM; a tile is 64 rows (four blocks):
-//   warp 12     asks for a tile's blocks (bulk copies into a ring of four tiles)
-//   warps 8-11  decode one block each: fp16 K and V (a code times its scale is exact), in
-//               the 128-byte-swizzled layout that the products read, three tiles deep
-//   warp 13     S = Q K^T (M = 64 query vectors, N = 64 rows, K = 128), double-buffered in
-//               tensor memory, and O += P V (N = 128 columns, K = 64 rows)
+// live in tensor memory.  One CTA per SM; a tile is 128 rows (eight blocks), so that a
+// tile's fixed costs (barriers, waits, the vote) are paid half as often as with 64:
+//   warp 12     asks for a tile's blocks (bulk copies into a ring of two tiles)
+//   warps 8-11  decode two blocks each: fp16 K and V (a code times its scale is exact), in
+//               the 128-byte-swizzled layout that the products read, two tiles deep; K's
+//               buffer is free again after S, V's after O += P V
+//   warp 13     S = Q K^T (M = 64 query vectors, N = 128 rows, K = 128), double-buffered in
+//               tensor memory, and O += P V (N = 128 columns, K = 128 rows)
 //   warps 0-7   softmax, four threads a query vector (the M = 64 layout: row r in lane 32 (r
 //               / 16) + r % 16); P goes to shared memory as two fp16 parts (22 bits)
 // The tensor cores add up at most kFold tiles: then, and where a score exceeds the
 // softmax's reference by 2^8, the softmax threads take O over into fp32 registers, where
 // additions round to nearest, and the next product overwrites it.
 //
-// Bound by the softmax threads' chain per tile (about 1000 cycles, of which the products
-// take 770); the decoding (16 KB written a tile) and the loads hide behind it.
+// Bound by the softmax threads' chain per tile; the products (1536 cycles), the decoding
+// and the loads run beside it.  32B-class layer, five queries: 64-row tiles 182 us, these
+// 149 us.
 #include "dd_attn4.cuh"
 
 namespace dd {
@@ -25,19 +28,19 @@ namespace dd {
 namespace {
 
 constexpr int kSoft = 8;                            // softmax warps
-constexpr int kDecode = 4;                          // decoding warps, one per block of a tile
+constexpr int kDecode = 4;                          // decoding warps
 constexpr int kTcThreads = (kSoft + kDecode + 2) * 32;
 constexpr int kTcM = 64;
-constexpr int kRaw = 4, kKv = 3;                    // tiles: as they are, and decoded
-constexpr int kRawBytes = 4 * 2 * kBlk4;
-constexpr int kHalf = 64 * 128;                     // 64 rows of 64 fp16 values
-constexpr int kKvBytes = 4 * kHalf;                 // K lo, K hi, V lo, V hi
-constexpr int kMeta = 16;                           // tiles' records
-constexpr int kFold = 8;
-constexpr int kTcJoinRow = 132;
-constexpr uint32_t kTmemCols = 256;                 // S: 2 x 64 columns, O: 128
-constexpr size_t kTcSmem = 1024 + (size_t)kKv * kKvBytes + 2 * kHalf + 4 * kHalf + (size_t)kRaw * kRawBytes +
-                           (size_t)kTcM * kTcJoinRow * 4;
+constexpr int kBlocks = 8;                          // blocks of a tile
+constexpr int kRaw = 2, kKv = 2;                    // tiles: as they are, and decoded
+constexpr int kRawBytes = kBlocks * 2 * kBlk4;
+constexpr int kHalf = 64 * 128;                     // 64 rows of 64 fp16 values (queries, P)
+constexpr int kTileHalf = 128 * 128;                // 128 rows of 64 fp16 values (K, V)
+constexpr int kKvBytes = 4 * kTileHalf;             // K lo, K hi, V lo, V hi
+constexpr int kMeta = 8;                            // tiles' records
+constexpr int kFold = 4;
+constexpr uint32_t kTmemCols = 512;                 // S: 2 x 128 columns, O: 128
+constexpr size_t kTcSmem = 1024 + (size_t)kKv * kKvBytes + 2 * kHalf + 4 * kHalf + (size_t)kRaw * kRawBytes;
 
 // kind::f16 instruction descriptor with fp16 A and B: fp32 accumulator, B's major-ness, N, M
 constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
@@ -47,23 +50,21 @@ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
 __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft * 32) : "memory"); }
 
 // A block's 16 rows of 128 values -> fp16, 16-byte pieces of 8 values: a lane takes piece c
-// of rows 2 it + lane / 16.  dst: the tile's lo half at the block's first row.
+// of rows 2 it + lane / 16.  dst: the tile's lo half at the block's first row.  Scales of V's
+// rows behind the end, which may hold anything, and NaN ones (0 * NaN would reach every
+// query) count as 0.
 template <bool kV>
-__device__ __forceinline__ uint32_t decode_block(uint32_t raw, uint32_t dst, int rows, int lane) {
+__device__ __forceinline__ void decode_block(uint32_t raw, uint32_t dst, int rows, int lane) {
   const int c = lane & 15, half = lane >> 4;
   const uint32_t codes = raw + half * 64 + c * 4, scales = raw + kBlk4Scales + half * 8 + (c >> 1);
-  dst += (uint32_t)((c >> 3) * kHalf + half * 128);
-  uint32_t nan = 0;      // rows' groups that are NaN (this lane's group, one bit)
+  dst += (uint32_t)((c >> 3) * kTileHalf + half * 128);
   uint32_t w[8], s[8];   // all loads first: the eight pieces' chains then overlap
 #pragma unroll
   for (int it = 0; it < 8; ++it) s[it] = lds8(scales + it * 16), w[it] = lds32(codes + it * 128);
 #pragma unroll
   for (int it = 0; it < 8; ++it) {
     const int row = 2 * it + half;
-    if (kV) {
-      if (row >= rows) s[it] = 0;                           // rows behind the end may hold anything
-      if ((s[it] & 0x7Fu) == 0x7Fu) s[it] = 0, nan = 1;     // 0 * NaN would reach every query
-    }
+    if (kV && (row >= rows || (s[it] & 0x7Fu) == 0x7Fu)) s[it] = 0;
     const uint32_t s2 = e4m3x2_to_half2(s[it] * 0x101u);
     uint32_t h[4];
     e2m1x8_to_half2(w[it], h);
@@ -74,7 +75,17 @@ __device__ __forceinline__ uint32_t decode_block(uint32_t raw, uint32_t dst, int
                  "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                  : "memory");
   }
-  return nan;
+}
+
+// Groups of 16 columns (bits) in which one of V's first `rows` rows is NaN: the warp's 16
+// bytes x 8 of scales, a word a lane.
+__device__ __forceinline__ uint32_t nan_groups(uint32_t raw_v, int rows, int lane) {
+  const uint32_t w = lds32(raw_v + kBlk4Scales + lane * 4);      // row lane / 2, groups 4 (lane & 1) ..
+  const uint32_t n = (lane >> 1) < rows ? (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) : 0u;
+  if (!__any_sync(0xffffffffu, n != 0u)) return 0u;
+  uint32_t bits = (n >> 7 & 1u) | (n >> 14 & 2u) | (n >> 21 & 4u) | (n >> 28 & 8u);
+  bits <<= 4 * (lane & 1);
+  return __reduce_or_sync(0xffffffffu, bits);
 }
 
 __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constant__ Attn4Params p) {
@@ -83,27 +94,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t kv0 = smem_u32(smem);                               // [kKv][kKvBytes]
   const uint32_t q0s = kv0 + kKv * kKvBytes;                         // [2 halves][64 rows][128 B]
-  const uint32_t p0 = q0s + 2 * kHalf;                               // [2 tiles][2 parts][64 rows][128 B]
-  const uint32_t raw0 = p0 + 4 * kHalf;                              // [kRaw][4 blocks][K, V]
-  float *join = reinterpret_cast<float *>(smem + (raw0 - kv0) + kRaw * kRawBytes);   // [kTcM][kTcJoinRow]
+  const uint32_t p0 = q0s + 2 * kHalf;                               // [2 parts][2 halves][64 rows][128 B]
+  const uint32_t raw0 = p0 + 4 * kHalf;                              // [kRaw][kBlocks][K, V]
+  // a run's sums, in P's place once its last product is done: [64 rows][32 pieces of 4
+  // columns], piece c of row r at c ^ (r & 31)
+  float4 *join = reinterpret_cast<float4 *>(smem + (p0 - kv0));
   __shared__ PlanSmem plan;
-  __shared__ __align__(8) uint64_t bars[2 * kRaw + 2 * kKv + 7];
+  __shared__ __align__(8) uint64_t bars[2 * kRaw + 4 * kKv + 6];
   __shared__ uint4 s_tails[2 * kMaxNq * 16];
-  __shared__ uint32_t s_meta[kMeta][4], s_nan[kMeta];
+  __shared__ __align__(16) uint32_t s_meta[kMeta][kBlocks], s_nan[kMeta][kBlocks];
   __shared__ float s_back[kTcM], s_m[kTcM], s_l[kTcM], s_red[2][kTcM];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_over[2], s_last;
+  __shared__ int s_over, s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Attn4Args &a = p.a;
   const uint32_t raw_full = smem_u32(bars), raw_empty = raw_full + 8 * kRaw;
-  const uint32_t kv_full = raw_empty + 8 * kRaw, kv_empty = kv_full + 8 * kKv;
-  const uint32_t s_full = kv_empty + 8 * kKv, pv_done = s_full + 16, p_ready = pv_done + 16, q_full = p_ready + 8;
+  const uint32_t k_full = raw_empty + 8 * kRaw, k_empty = k_full + 8 * kKv, v_full = k_empty + 8 * kKv,
+                 v_empty = v_full + 8 * kKv;
+  const uint32_t s_full = v_empty + 8 * kKv, pv_done = s_full + 16, p_ready = pv_done + 8, q_full = p_ready + 8;
   const uint32_t mma_done = q_full + 8;
   if (tid == 0) {
-    for (int i = 0; i < kRaw; ++i) mbar_init(raw_full + 8 * i, 4), mbar_init(raw_empty + 8 * i, kDecode);
-    for (int i = 0; i < kKv; ++i) mbar_init(kv_full + 8 * i, kDecode), mbar_init(kv_empty + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(s_full + 8 * i, 1), mbar_init(pv_done + 8 * i, 1);
+    for (int i = 0; i < kRaw; ++i) mbar_init(raw_full + 8 * i, kBlocks), mbar_init(raw_empty + 8 * i, kDecode);
+    for (int i = 0; i < kKv; ++i) {
+      mbar_init(k_full + 8 * i, kDecode), mbar_init(v_full + 8 * i, kDecode);
+      mbar_init(k_empty + 8 * i, 1), mbar_init(v_empty + 8 * i, 1);
+    }
+    mbar_init(s_full, 1), mbar_init(s_full + 8, 1);
+    mbar_init(pv_done, 1);
     mbar_init(p_ready, 1);
     mbar_init(q_full, 1);
     mbar_init(mma_done, 1);
@@ -111,7 +129,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
   }
   pdl_wait();
   pdl_trigger();
-  Slice<kTcThreads, 1, 2> slice;
+  Slice<kTcThreads, 1, 3> slice;
   if (!slice.open(p, plan)) return;
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
@@ -122,7 +140,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * kTcM;
+  const uint32_t tmem = s_tmem, tmem_o = tmem + 256;
   const uint32_t all_q = (1u << a.n_q) - 1u;
 
   // Every role walks the same tiles and numbers them alike.  A wait that runs out (2 s)
@@ -148,30 +166,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
             p.arrive[runs[r].unit] = 0;
     } else if (warp == kSoft + kDecode) {
       // ------------------------------------------------------------- loads
-      for (int i0 = 0; i0 < n_tiles; i0 += 8) {
-        // lane 4 k + h: block h of tile i0 + k
+      for (int i0 = 0; i0 < n_tiles; i0 += 4) {
+        // lane 8 k + h: block h of tile i0 + k
         BlockRef ref = {0, 0u};
-        const int x = wlo + i0 + (lane >> 2);
+        const int x = wlo + i0 + (lane >> 3);
         if (x < whi) {
           int r = 0;
 #pragma unroll
           for (int step = kMaxRuns / 2; step > 0; step >>= 1)
             if (r + step < n_runs && runs[r + step].start <= x) r += step;
-          ref = look_up(p, runs[r], 4 * (x - runs[r].start) + (lane & 3), slice.staged, all_q);
+          ref = look_up(p, runs[r], kBlocks * (x - runs[r].start) + (lane & 7), slice.staged, all_q);
         }
-        for (int k = 0; k < 8 && i0 + k < n_tiles; ++k, ++t) {
+        for (int k = 0; k < 4 && i0 + k < n_tiles; ++k, ++t) {
           const int st = t % kRaw;
           if (t >= kRaw) wait(raw_empty + 8 * st, t / kRaw - 1);
           __syncwarp();
-          if ((lane >> 2) == k) {
-            s_meta[t % kMeta][lane & 3] = ref.meta;
-            if ((lane & 3) == 0) s_nan[t % kMeta] = 0u;
-            __threadfence_block();
-          }
-          __syncwarp();
-          if ((lane >> 2) == k) {
+          if ((lane >> 3) == k) {
+            s_meta[t % kMeta][lane & 7] = ref.meta;      // (the arrival below releases it)
             if (ref.meta && alive)
-              load_block(p, ref, raw0 + st * kRawBytes + (lane & 3) * 2 * kBlk4, raw_full + 8 * st);
+              load_block(p, ref, raw0 + st * kRawBytes + (lane & 7) * 2 * kBlk4, raw_full + 8 * st);
             else
               mbar_arrive(raw_full + 8 * st);
           }
@@ -179,62 +192,79 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
       }
     } else if (warp >= kSoft && warp < kSoft + kDecode) {
       // ------------------------------------------------------------ decoding
-      const int blk = warp - kSoft;
+      const int w = warp - kSoft;
       for (int i = 0; i < n_tiles; ++i, ++t) {
         const int st = t % kRaw, b = t % kKv;
         wait(raw_full + 8 * st, t / kRaw);
-        if (t >= kKv) wait(kv_empty + 8 * b, t / kKv - 1);
-        const uint32_t meta = s_meta[t % kMeta][blk];
-        const uint32_t raw = raw0 + st * kRawBytes + blk * 2 * kBlk4, dst = kv0 + b * kKvBytes + blk * 16 * 128;
-        decode_block<false>(raw, dst, 16, lane);
-        const uint32_t nan = decode_block<true>(raw + kBlk4, dst + 2 * kHalf, (int)(meta >> 8) & 31, lane);
-        if (nan) atomicOr(&s_nan[t % kMeta], 1u << (blk * 8 + ((lane & 15) >> 1)));
+        if (t >= kKv) wait(k_empty + 8 * b, t / kKv - 1);
+        __syncwarp();
+#pragma unroll 1
+        for (int blk = w; blk < kBlocks; blk += kDecode) {
+          const uint32_t raw = raw0 + st * kRawBytes + blk * 2 * kBlk4;
+          const int rows = (int)(s_meta[t % kMeta][blk] >> 8) & 31;
+          const uint32_t nan = nan_groups(raw + kBlk4, rows, lane);
+          if (lane == 0) s_nan[t % kMeta][blk] = nan;
+          decode_block<false>(raw, kv0 + b * kKvBytes + blk * 16 * 128, 16, lane);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + 8 * b);
+        if (t >= kKv) wait(v_empty + 8 * b, t / kKv - 1);
+        __syncwarp();
+#pragma unroll 1
+        for (int blk = w; blk < kBlocks; blk += kDecode) {
+          const uint32_t raw = raw0 + st * kRawBytes + (blk * 2 + 1) * kBlk4;
+          const int rows = (int)(s_meta[t % kMeta][blk] >> 8) & 31;
+          decode_block<true>(raw, kv0 + b * kKvBytes + 2 * kTileHalf + blk * 16 * 128, rows, lane);
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
+          mbar_arrive(v_full + 8 * b);
           mbar_arrive(raw_empty + 8 * st);
-          mbar_arrive(kv_full + 8 * b);
         }
       }
     } else if (warp == kSoft + kDecode + 1) {
       // ------------------------------------------------------------ products
       if (lane == 0) {
         // (descriptors hold addresses in 16-byte units: a step adds a constant)
-        constexpr uint32_t id_s = idesc_f16(kTcM, 64, 0), id_o = idesc_f16(kTcM, 128, 1);
+        constexpr uint32_t id_s = idesc_f16(kTcM, 128, 0), id_o = idesc_f16(kTcM, 128, 1);
         const uint64_t q_desc = smem_desc_sw128(q0s, 16, 1024), k_desc = smem_desc_sw128(kv0, 16, 1024);
-        const uint64_t p_desc = smem_desc_sw128(p0, 16, 1024), v_desc = smem_desc_sw128(kv0 + 2 * kHalf, kHalf, 1024);
+        const uint64_t p_desc = smem_desc_sw128(p0, 16, 1024);
+        const uint64_t v_desc = smem_desc_sw128(kv0 + 2 * kTileHalf, kTileHalf, 1024);
         auto issue_pv = [&](int u) {
+          wait(v_full + 8 * (u % kKv), u / kKv);
           wait(p_ready, u);
           tc_fence_after();
           if (!alive) return;
-          const uint64_t pa = p_desc + (uint32_t)((u & 1) * (2 * kHalf / 16));
           const uint64_t vb = v_desc + (uint32_t)((u % kKv) * (kKvBytes / 16));
-          const bool over = s_over[u & 1] != 0;
+          const bool over = s_over != 0;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
+          for (int ks = 0; ks < 8; ++ks) {
             const uint64_t b = vb + ks * 16 * 128 / 16;
-            tc_mma(tmem_o, pa + ks * 32 / 16, b, id_o, !(over && ks == 0));
-            tc_mma(tmem_o, pa + (kHalf + ks * 32) / 16, b, id_o, 1);
+            const int off = ((ks >> 2) * kHalf + (ks & 3) * 32) / 16;
+            tc_mma(tmem_o, p_desc + off, b, id_o, !(over && ks == 0));
+            tc_mma(tmem_o, p_desc + 2 * kHalf / 16 + off, b, id_o, 1);
           }
-          tc_commit(kv_empty + 8 * (u % kKv));
-          tc_commit(pv_done + 8 * (u & 1));
+          tc_commit(v_empty + 8 * (u % kKv));
+          tc_commit(pv_done);
         };
         int x = wlo;
         for (int r = 0; r < n_runs; ++r, ++run_no) {
           const int end = min(whi, runs[r].end);
           wait(q_full, run_no);
           for (; x < end; ++x, ++t) {
-            wait(kv_full + 8 * (t % kKv), t / kKv);
+            wait(k_full + 8 * (t % kKv), t / kKv);
             tc_fence_after();
             if (alive) {
               // the softmax threads are done with S(t - 2): P(t - 2) was ready
               const uint64_t kb = k_desc + (uint32_t)((t % kKv) * (kKvBytes / 16));
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks) {
-                const int off = ((ks >> 2) * kHalf + (ks & 3) * 32) / 16;
-                tc_mma(tmem + (t & 1) * kTcM, q_desc + off, kb + off, id_s, ks > 0);
-              }
+              for (int ks = 0; ks < 8; ++ks)
+                tc_mma(tmem + (t & 1) * 128, q_desc + ((ks >> 2) * kHalf + (ks & 3) * 32) / 16,
+                       kb + ((ks >> 2) * kTileHalf + (ks & 3) * 32) / 16, id_s, ks > 0);
               tc_commit(s_full + 8 * (t & 1));
+              tc_commit(k_empty + 8 * (t % kKv));
             }
             // S of this tile runs beside the softmax of the one before, its P V comes after it
             if (x > max(wlo, runs[r].start)) issue_pv(t - 1);
@@ -247,8 +277,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
       // ------------------------------------------------------------- softmax
       const int wq = warp & 3, wc = warp >> 2, sub = lane >> 4;
       const int row = 16 * wq + (lane & 15);             // query vector
-      const int bi = 2 * wc + sub;                       // block of the tile: 16 columns of S
-      const int ocol = 32 * bi;                          // and 32 of O
+      const int bi = 2 * wc + sub;                       // 32 columns of S (blocks 2 bi, 2 bi + 1) and of O
       const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
       const bool active = row < p.NQ, some = 16 * wq < p.NQ;     // some: of this warp's query vectors
       const int j = active ? row / p.G : 31;
@@ -297,21 +326,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           wait(s_full + 8 * (t & 1), t >> 1);
           __syncwarp();
           tc_fence_after();
-          float x[16], pm = -INFINITY;
+          float x[32], pm = -INFINITY;
           if (some) {
-            tmem_ld16_split<16>(tmem + lane_base + (t & 1) * kTcM + 32 * wc, x);
-            const uint32_t meta = s_meta[t % kMeta][bi];
-            const int rows = (meta & 255u) >> j & 1u ? (int)(meta >> 8) & 31 : 0;
-            if (rows < 16) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (e >= rows) x[e] = -INFINITY;
+            for (int h = 0; h < 2; ++h) {
+              tmem_ld16_split<32>(tmem + lane_base + (t & 1) * 128 + 64 * wc + 16 * h, x + 16 * h);
+              const uint32_t meta = s_meta[t % kMeta][2 * bi + h];
+              const int rows = (meta & 255u) >> j & 1u ? (int)(meta >> 8) & 31 : 0;
+              if (rows < 16) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (e >= rows) x[16 * h + e] = -INFINITY;
+              }
             }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] *= mul;
+            for (int e = 0; e < 32; ++e) x[e] *= mul;
             float m8[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m8[e] = fmaxf(x[e], x[e + 8]);
+            for (int e = 0; e < 8; ++e) m8[e] = fmaxf(fmaxf(x[e], x[e + 8]), fmaxf(x[e + 16], x[e + 24]));
 #pragma unroll
             for (int e = 0; e < 4; ++e) m8[e] = fmaxf(m8[e], m8[e + 4]);
             pm = fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3]));
@@ -333,9 +365,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
             m = nm;
           }
           const bool fold = i > 0 && (any || since == kFold);
-          // P's buffer: its last reader is PV(t - 2); O: PV(t - 1)
-          const int before = fold ? t - 1 : t - 2;
-          if (before >= 0) wait(pv_done + 8 * (before & 1), before >> 1);
+          // P's and O's last reader and writer: PV(t - 1)
+          if (t > 0) wait(pv_done, t - 1);
           if (fold && some) {
             __syncwarp();
             tc_fence_after();
@@ -349,26 +380,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
             l *= factor;
           }
           if (fold) since = 0;
-          const uint32_t nan = s_nan[t % kMeta];
-          if (nan) {
-            // NaN groups of V: NaN for the queries that see their block
+          {
+            const uint4 n0 = *reinterpret_cast<const uint4 *>(s_nan[t % kMeta]);
+            const uint4 n1 = *reinterpret_cast<const uint4 *>(s_nan[t % kMeta] + 4);
+            if ((n0.x | n0.y | n0.z | n0.w | n1.x | n1.y | n1.z | n1.w) != 0u) {
+              // NaN groups of V: NaN for the queries that see their block
 #pragma unroll 1
-            for (int blk = 0; blk < 4; ++blk) {
-              if (!((s_meta[t % kMeta][blk] & 255u) >> j & 1u)) continue;
+              for (int blk = 0; blk < kBlocks; ++blk) {
+                const uint32_t nan = s_nan[t % kMeta][blk];
+                if (!((s_meta[t % kMeta][blk] & 255u) >> j & 1u)) continue;
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (nan >> (blk * 8 + 2 * bi + h) & 1u) {
+                for (int h = 0; h < 2; ++h)
+                  if (nan >> (2 * bi + h) & 1u) {
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) oacc[16 * h + e] = NAN;
-                }
+                    for (int e = 0; e < 16; ++e) oacc[16 * h + e] = NAN;
+                  }
+              }
             }
           }
           if (active) {
             // a query without a row so far: -inf - 0 gives weight 0, and a NaN passes
             const float base = m == -INFINITY ? 0.f : m;
-            const uint32_t ph = p0 + (t & 1) * 2 * kHalf + row * 128;
+            const uint32_t ph = p0 + (bi >> 1) * kHalf + row * 128;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t hi[4], lo[4];
               float sum = 0.f;
 #pragma unroll
@@ -380,16 +415,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
                 lo[e] = cvt_f16x2(u - f.x, v - f.y);
               }
               l += sum;
-              const uint32_t off = (uint32_t)(((2 * bi + c) ^ (row & 7)) << 4);
+              const uint32_t off = (uint32_t)((((bi & 1) * 4 + c) ^ (row & 7)) << 4);
               asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(ph + off), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
                            "r"(hi[3])
                            : "memory");
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(ph + kHalf + off), "r"(lo[0]), "r"(lo[1]),
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(ph + 2 * kHalf + off), "r"(lo[0]), "r"(lo[1]),
                            "r"(lo[2]), "r"(lo[3])
                            : "memory");
             }
           }
-          if (tid == 0) s_over[t & 1] = i == 0 || fold;
+          if (tid == 0) s_over = i == 0 || fold;
           ++since;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           tc_fence_before();
@@ -398,7 +433,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
         }
 
         // ------------------------------------------------- the run's sums
-        wait(pv_done + 8 * ((t - 1) & 1), (t - 1) >> 1);
+        wait(pv_done, t - 1);
         __syncwarp();
         tc_fence_after();
 #pragma unroll
@@ -414,7 +449,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
         if (bi == 0) s_m[row] = m;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<float4 *>(join + row * kTcJoinRow + ocol + 4 * e) =
+          join[row * 32 + ((8 * bi + e) ^ (row & 31))] =
               make_float4(oacc[4 * e], oacc[4 * e + 1], oacc[4 * e + 2], oacc[4 * e + 3]);
         soft_barrier();
         if (tid < kTcM) s_l[tid] = s_red[0][tid] + s_red[1][tid];
@@ -429,7 +464,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
         };
 #pragma unroll 2
         for (int k = warp; k < p.NQ; k += kSoft) {
-          const float4 v = *reinterpret_cast<const float4 *>(join + k * kTcJoinRow + 4 * lane);
+          const float4 v = join[k * 32 + (lane ^ (k & 31))];
           const Part s = {s_m[k], s_l[k], make_float4(v.x * vmul, v.y * vmul, v.z * vmul, v.w * vmul)};
           if (!shared) {
             finish(p, run.unit, k, s, query_of(k), tails, lane);

@@ -223,6 +223,11 @@ __device__ __forceinline__ Part combine_parts(const Attn4Params &p, const Run &r
   for (int k0 = r.cta0; k0 <= r.cta1; k0 += 32) {
     const int np = min(32, r.cta1 - k0 + 1);
     const int64_t at0 = ((int64_t)k0 + r.unit) * group_q + k;
+    const float4 *src = reinterpret_cast<const float4 *>(p.part_o + at0 * kD) + lane;
+    const int64_t step = (int64_t)group_q * (kD / 4);
+    float4 v[8];     // on their way while the weights are worked out
+#pragma unroll
+    for (int t = 0; t < 8; ++t) v[t] = __ldcg(src + min(t, np - 1) * step);
     float2 ml = make_float2(-INFINITY, 0.f);
     if (lane < np) ml = __ldcg(reinterpret_cast<const float2 *>(p.part_ml + 2 * (at0 + (int64_t)lane * group_q)));
     float mn = fmaxf(s.m, ml.x);
@@ -235,10 +240,10 @@ __device__ __forceinline__ Part combine_parts(const Attn4Params &p, const Run &r
     s.l = s.l * wa + lw;
     s.o.x *= wa, s.o.y *= wa, s.o.z *= wa, s.o.w *= wa;
     for (int t0 = 0; t0 < np; t0 += 8) {
-      float4 v[8];
+      if (t0 > 0) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-        v[t] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + (at0 + (int64_t)min(t0 + t, np - 1) * group_q) * kD + 4 * lane));
+        for (int t = 0; t < 8; ++t) v[t] = __ldcg(src + min(t0 + t, np - 1) * step);
+      }
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         const float f = __shfl_sync(0xffffffffu, wt, (t0 + t) & 31);

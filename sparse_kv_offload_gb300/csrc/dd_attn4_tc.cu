@@ -6,21 +6,26 @@
 // decoded once, into shared memory, for up to 64 query vectors, and the accumulators
 // live in tensor memory.  One CTA per SM; a tile is 128 rows (eight blocks), so that a
 // tile's fixed costs (barriers, waits, the vote) are paid half as often as with 64:
-//   warp 12     asks for a tile's blocks (bulk copies into a ring of two tiles)
+//   warp 12     asks for a tile's blocks (bulk copies into a ring of three tiles)
 //   warps 8-11  decode two blocks each: fp16 K and V (a code times its scale is exact), in
-//               the 128-byte-swizzled layout that the products read, two tiles deep; K's
-//               buffer is free again after S, V's after O += P V
+//               the 128-byte-swizzled layout that the products read; K has one buffer,
+//               free again after S, V two
 //   warp 13     S = Q K^T (M = 64 query vectors, N = 128 rows, K = 128), double-buffered in
-//               tensor memory, and O += P V (N = 128 columns, K = 128 rows)
+//               tensor memory, and O += P V (N = 128 columns, K = 128 rows) with both parts
+//               of P as one operand of 128 rows, which takes no longer than 64
 //   warps 0-7   softmax, four threads a query vector (the M = 64 layout: row r in lane 32 (r
 //               / 16) + r % 16); P goes to shared memory as two fp16 parts (22 bits)
-// The tensor cores add up at most kFold tiles: then, and where a score exceeds the
-// softmax's reference by 2^8, the softmax threads take O over into fp32 registers, where
-// additions round to nearest, and the next product overwrites it.
+// The tensor cores truncate when they add (the sums of 8,192 tiles are off by 1.5e-5): they
+// add up at most kFold tiles (1e-6); then, and where a score exceeds the softmax's reference
+// by 2^8, the softmax threads take O over into fp32 registers, where additions round to
+// nearest, and the next product overwrites it.
 //
-// Bound by the softmax threads' chain per tile; the products (1536 cycles), the decoding
-// and the loads run beside it.  32B-class layer, five queries: 64-row tiles 182 us, these
-// 149 us.
+// Bound by the softmax threads' chain per tile (some 3,000 cycles; the products take 1,024,
+// the decoding 2,000, and both run beside it).  32B-class layer, five queries: the
+// mma.sync kernel in groups of 16 215 us, 64-row tiles 182, 128-row tiles 151, both parts
+// of P in one operand and O taken over every eight tiles instead of two 143.  Sixteen softmax
+// warps (80 registers) gain 1-3% with 40 or more query vectors and lose 5% with 20; eight
+// decoding warps (96 registers) lose 10%.
 #include "dd_attn4.cuh"
 
 namespace dd {
@@ -32,15 +37,15 @@ constexpr int kDecode = 4;                          // decoding warps
 constexpr int kTcThreads = (kSoft + kDecode + 2) * 32;
 constexpr int kTcM = 64;
 constexpr int kBlocks = 8;                          // blocks of a tile
-constexpr int kRaw = 2, kKv = 2;                    // tiles: as they are, and decoded
+constexpr int kRaw = 3, kK = 1, kV = 2;             // tiles: as they are, and decoded (K's buffer is free after S)
 constexpr int kRawBytes = kBlocks * 2 * kBlk4;
 constexpr int kHalf = 64 * 128;                     // 64 rows of 64 fp16 values (queries, P)
 constexpr int kTileHalf = 128 * 128;                // 128 rows of 64 fp16 values (K, V)
-constexpr int kKvBytes = 4 * kTileHalf;             // K lo, K hi, V lo, V hi
+constexpr int kKvBytes = 2 * kTileHalf;             // lo, hi
 constexpr int kMeta = 8;                            // tiles' records
-constexpr int kFold = 4;
+constexpr int kFold = 8;
 constexpr uint32_t kTmemCols = 512;                 // S: 2 x 128 columns, O: 128
-constexpr size_t kTcSmem = 1024 + (size_t)kKv * kKvBytes + 2 * kHalf + 4 * kHalf + (size_t)kRaw * kRawBytes;
+constexpr size_t kTcSmem = 1024 + (size_t)(kK + kV) * kKvBytes + 2 * kHalf + 4 * kHalf + (size_t)kRaw * kRawBytes;
 
 // kind::f16 instruction descriptor with fp16 A and B: fp32 accumulator, B's major-ness, N, M
 constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
@@ -49,11 +54,47 @@ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
 
 __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft * 32) : "memory"); }
 
+// A thread's 32 columns of S (two loads, one wait): threads 0-15 of the warp at c, 16-31 at
+// c + 32, of lanes 0-15 of the warp's quarter.
+__device__ __forceinline__ void tmem_ld_s(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 32;"
+        : "=r"(r[16 * h]), "=r"(r[16 * h + 1]), "=r"(r[16 * h + 2]), "=r"(r[16 * h + 3]), "=r"(r[16 * h + 4]),
+          "=r"(r[16 * h + 5]), "=r"(r[16 * h + 6]), "=r"(r[16 * h + 7]), "=r"(r[16 * h + 8]), "=r"(r[16 * h + 9]),
+          "=r"(r[16 * h + 10]), "=r"(r[16 * h + 11]), "=r"(r[16 * h + 12]), "=r"(r[16 * h + 13]),
+          "=r"(r[16 * h + 14]), "=r"(r[16 * h + 15])
+        : "r"(taddr + 16 * h));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// acc = (acc + a thread's 32 columns of O) * factor.  Lanes 0-15 of the quarter hold the sums
+// of P's first part, lanes 16-31 those of its second: a thread reads 64 columns of its
+// lane, 16 at a time, and gives half of them away.
+__device__ __forceinline__ void tmem_add_o(uint32_t taddr, float (&acc)[32], float factor, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float a[16], b[16];
+    tmem_ld32x32b_x16(taddr + 16 * h, a);
+    tmem_ld32x32b_x16(taddr + 32 + 16 * h, b);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float keep = lane < 16 ? a[e] : b[e], give = lane < 16 ? b[e] : a[e];
+      acc[16 * h + e] = (acc[16 * h + e] + (keep + __shfl_xor_sync(0xffffffffu, give, 16))) * factor;
+    }
+  }
+}
+
 // A block's 16 rows of 128 values -> fp16, 16-byte pieces of 8 values: a lane takes piece c
 // of rows 2 it + lane / 16.  dst: the tile's lo half at the block's first row.  Scales of V's
 // rows behind the end, which may hold anything, and NaN ones (0 * NaN would reach every
 // query) count as 0.
-template <bool kV>
+template <bool kValues>
 __device__ __forceinline__ void decode_block(uint32_t raw, uint32_t dst, int rows, int lane) {
   const int c = lane & 15, half = lane >> 4;
   const uint32_t codes = raw + half * 64 + c * 4, scales = raw + kBlk4Scales + half * 8 + (c >> 1);
@@ -64,7 +105,7 @@ __device__ __forceinline__ void decode_block(uint32_t raw, uint32_t dst, int row
 #pragma unroll
   for (int it = 0; it < 8; ++it) {
     const int row = 2 * it + half;
-    if (kV && (row >= rows || (s[it] & 0x7Fu) == 0x7Fu)) s[it] = 0;
+    if (kValues && (row >= rows || (s[it] & 0x7Fu) == 0x7Fu)) s[it] = 0;
     const uint32_t s2 = e4m3x2_to_half2(s[it] * 0x101u);
     uint32_t h[4];
     e2m1x8_to_half2(w[it], h);
@@ -92,15 +133,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   // the swizzle pattern is anchored at 1024-byte boundaries
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const uint32_t kv0 = smem_u32(smem);                               // [kKv][kKvBytes]
-  const uint32_t q0s = kv0 + kKv * kKvBytes;                         // [2 halves][64 rows][128 B]
-  const uint32_t p0 = q0s + 2 * kHalf;                               // [2 parts][2 halves][64 rows][128 B]
+  const uint32_t kv0 = smem_u32(smem), v0 = kv0 + kK * kKvBytes;     // [kK][kKvBytes], [kV][kKvBytes]
+  const uint32_t q0s = v0 + kV * kKvBytes;                           // [2 halves][64 rows][128 B]
+  const uint32_t p0 = q0s + 2 * kHalf;                               // [2 halves][128 rows][128 B]
   const uint32_t raw0 = p0 + 4 * kHalf;                              // [kRaw][kBlocks][K, V]
   // a run's sums, in P's place once its last product is done: [64 rows][32 pieces of 4
   // columns], piece c of row r at c ^ (r & 31)
   float4 *join = reinterpret_cast<float4 *>(smem + (p0 - kv0));
   __shared__ PlanSmem plan;
-  __shared__ __align__(8) uint64_t bars[2 * kRaw + 4 * kKv + 6];
+  __shared__ __align__(8) uint64_t bars[2 * kRaw + 2 * kK + 2 * kV + 6];
   __shared__ uint4 s_tails[2 * kMaxNq * 16];
   __shared__ __align__(16) uint32_t s_meta[kMeta][kBlocks], s_nan[kMeta][kBlocks];
   __shared__ float s_back[kTcM], s_m[kTcM], s_l[kTcM], s_red[2][kTcM];
@@ -110,16 +151,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Attn4Args &a = p.a;
   const uint32_t raw_full = smem_u32(bars), raw_empty = raw_full + 8 * kRaw;
-  const uint32_t k_full = raw_empty + 8 * kRaw, k_empty = k_full + 8 * kKv, v_full = k_empty + 8 * kKv,
-                 v_empty = v_full + 8 * kKv;
-  const uint32_t s_full = v_empty + 8 * kKv, pv_done = s_full + 16, p_ready = pv_done + 8, q_full = p_ready + 8;
+  const uint32_t k_full = raw_empty + 8 * kRaw, k_empty = k_full + 8 * kK, v_full = k_empty + 8 * kK,
+                 v_empty = v_full + 8 * kV;
+  const uint32_t s_full = v_empty + 8 * kV, pv_done = s_full + 16, p_ready = pv_done + 8, q_full = p_ready + 8;
   const uint32_t mma_done = q_full + 8;
   if (tid == 0) {
     for (int i = 0; i < kRaw; ++i) mbar_init(raw_full + 8 * i, kBlocks), mbar_init(raw_empty + 8 * i, kDecode);
-    for (int i = 0; i < kKv; ++i) {
-      mbar_init(k_full + 8 * i, kDecode), mbar_init(v_full + 8 * i, kDecode);
-      mbar_init(k_empty + 8 * i, 1), mbar_init(v_empty + 8 * i, 1);
-    }
+    for (int i = 0; i < kK; ++i) mbar_init(k_full + 8 * i, kDecode), mbar_init(k_empty + 8 * i, 1);
+    for (int i = 0; i < kV; ++i) mbar_init(v_full + 8 * i, kDecode), mbar_init(v_empty + 8 * i, 1);
     mbar_init(s_full, 1), mbar_init(s_full + 8, 1);
     mbar_init(pv_done, 1);
     mbar_init(p_ready, 1);
@@ -194,9 +233,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
       // ------------------------------------------------------------ decoding
       const int w = warp - kSoft;
       for (int i = 0; i < n_tiles; ++i, ++t) {
-        const int st = t % kRaw, b = t % kKv;
+        const int st = t % kRaw, kb = t % kK, vb = t % kV;
         wait(raw_full + 8 * st, t / kRaw);
-        if (t >= kKv) wait(k_empty + 8 * b, t / kKv - 1);
+        if (t >= kK) wait(k_empty + 8 * kb, t / kK - 1);
         __syncwarp();
 #pragma unroll 1
         for (int blk = w; blk < kBlocks; blk += kDecode) {
@@ -204,23 +243,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           const int rows = (int)(s_meta[t % kMeta][blk] >> 8) & 31;
           const uint32_t nan = nan_groups(raw + kBlk4, rows, lane);
           if (lane == 0) s_nan[t % kMeta][blk] = nan;
-          decode_block<false>(raw, kv0 + b * kKvBytes + blk * 16 * 128, 16, lane);
+          decode_block<false>(raw, kv0 + kb * kKvBytes + blk * 16 * 128, 16, lane);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + 8 * b);
-        if (t >= kKv) wait(v_empty + 8 * b, t / kKv - 1);
+        if (lane == 0) mbar_arrive(k_full + 8 * kb);
+        if (t >= kV) wait(v_empty + 8 * vb, t / kV - 1);
         __syncwarp();
 #pragma unroll 1
         for (int blk = w; blk < kBlocks; blk += kDecode) {
           const uint32_t raw = raw0 + st * kRawBytes + (blk * 2 + 1) * kBlk4;
           const int rows = (int)(s_meta[t % kMeta][blk] >> 8) & 31;
-          decode_block<true>(raw, kv0 + b * kKvBytes + 2 * kTileHalf + blk * 16 * 128, rows, lane);
+          decode_block<true>(raw, v0 + vb * kKvBytes + blk * 16 * 128, rows, lane);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(v_full + 8 * b);
+          mbar_arrive(v_full + 8 * vb);
           mbar_arrive(raw_empty + 8 * st);
         }
       }
@@ -228,25 +267,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
       // ------------------------------------------------------------ products
       if (lane == 0) {
         // (descriptors hold addresses in 16-byte units: a step adds a constant)
-        constexpr uint32_t id_s = idesc_f16(kTcM, 128, 0), id_o = idesc_f16(kTcM, 128, 1);
+        constexpr uint32_t id_s = idesc_f16(kTcM, 128, 0), id_o = idesc_f16(128, 128, 1);
         const uint64_t q_desc = smem_desc_sw128(q0s, 16, 1024), k_desc = smem_desc_sw128(kv0, 16, 1024);
         const uint64_t p_desc = smem_desc_sw128(p0, 16, 1024);
-        const uint64_t v_desc = smem_desc_sw128(kv0 + 2 * kTileHalf, kTileHalf, 1024);
+        const uint64_t v_desc = smem_desc_sw128(v0, kTileHalf, 1024);
         auto issue_pv = [&](int u) {
-          wait(v_full + 8 * (u % kKv), u / kKv);
+          wait(v_full + 8 * (u % kV), u / kV);
           wait(p_ready, u);
           tc_fence_after();
           if (!alive) return;
-          const uint64_t vb = v_desc + (uint32_t)((u % kKv) * (kKvBytes / 16));
+          const uint64_t vb = v_desc + (uint32_t)((u % kV) * (kKvBytes / 16));
           const bool over = s_over != 0;
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
-            const uint64_t b = vb + ks * 16 * 128 / 16;
-            const int off = ((ks >> 2) * kHalf + (ks & 3) * 32) / 16;
-            tc_mma(tmem_o, p_desc + off, b, id_o, !(over && ks == 0));
-            tc_mma(tmem_o, p_desc + 2 * kHalf / 16 + off, b, id_o, 1);
+            tc_mma(tmem_o, p_desc + ((ks >> 2) * kTileHalf + (ks & 3) * 32) / 16, vb + ks * 16 * 128 / 16, id_o,
+                   !(over && ks == 0));
           }
-          tc_commit(v_empty + 8 * (u % kKv));
+          tc_commit(v_empty + 8 * (u % kV));
           tc_commit(pv_done);
         };
         int x = wlo;
@@ -254,17 +291,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           const int end = min(whi, runs[r].end);
           wait(q_full, run_no);
           for (; x < end; ++x, ++t) {
-            wait(k_full + 8 * (t % kKv), t / kKv);
+            wait(k_full + 8 * (t % kK), t / kK);
             tc_fence_after();
             if (alive) {
               // the softmax threads are done with S(t - 2): P(t - 2) was ready
-              const uint64_t kb = k_desc + (uint32_t)((t % kKv) * (kKvBytes / 16));
+              const uint64_t kb = k_desc + (uint32_t)((t % kK) * (kKvBytes / 16));
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
                 tc_mma(tmem + (t & 1) * 128, q_desc + ((ks >> 2) * kHalf + (ks & 3) * 32) / 16,
                        kb + ((ks >> 2) * kTileHalf + (ks & 3) * 32) / 16, id_s, ks > 0);
               tc_commit(s_full + 8 * (t & 1));
-              tc_commit(k_empty + 8 * (t % kKv));
+              tc_commit(k_empty + 8 * (t % kK));
             }
             // S of this tile runs beside the softmax of the one before, its P V comes after it
             if (x > max(wlo, runs[r].start)) issue_pv(t - 1);
@@ -328,9 +365,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           tc_fence_after();
           float x[32], pm = -INFINITY;
           if (some) {
+            tmem_ld_s(tmem + lane_base + (t & 1) * 128 + 64 * wc, x);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              tmem_ld16_split<32>(tmem + lane_base + (t & 1) * 128 + 64 * wc + 16 * h, x + 16 * h);
               const uint32_t meta = s_meta[t % kMeta][2 * bi + h];
               const int rows = (meta & 255u) >> j & 1u ? (int)(meta >> 8) & 31 : 0;
               if (rows < 16) {
@@ -370,13 +407,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           if (fold && some) {
             __syncwarp();
             tc_fence_after();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float o[16];
-              tmem_ld16_split<32>(tmem_o + lane_base + 64 * wc + 16 * h, o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) oacc[16 * h + e] = (oacc[16 * h + e] + o[e]) * factor;
-            }
+            tmem_add_o(tmem_o + lane_base + 64 * wc, oacc, factor, lane);
             l *= factor;
           }
           if (fold) since = 0;
@@ -401,7 +432,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           if (active) {
             // a query without a row so far: -inf - 0 gives weight 0, and a NaN passes
             const float base = m == -INFINITY ? 0.f : m;
-            const uint32_t ph = p0 + (bi >> 1) * kHalf + row * 128;
+            const uint32_t ph = p0 + (bi >> 1) * kTileHalf + (32 * wq + (lane & 15)) * 128;     // the second part 16 rows on
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t hi[4], lo[4];
@@ -419,7 +450,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
               asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(ph + off), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
                            "r"(hi[3])
                            : "memory");
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(ph + 2 * kHalf + off), "r"(lo[0]), "r"(lo[1]),
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(ph + 16 * 128 + off), "r"(lo[0]), "r"(lo[1]),
                            "r"(lo[2]), "r"(lo[3])
                            : "memory");
             }
@@ -436,13 +467,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
         wait(pv_done, t - 1);
         __syncwarp();
         tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float o[16];
-          tmem_ld16_split<32>(tmem_o + lane_base + 64 * wc + 16 * h, o);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) oacc[16 * h + e] += o[e];
-        }
+        tmem_add_o(tmem_o + lane_base + 64 * wc, oacc, 1.f, lane);
         tc_fence_before();      // O is read before the next run's first product overwrites it
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         if (sub == 0) s_red[wc][row] = l;

@@ -222,8 +222,9 @@ def _i32(t, numel, name, allow_none=False):
 
 def _either(t, dtype, numel, name, allow_none=False):
     """Address of a tensor in device or in pinned host memory."""
-    on_gpu = t is None or not isinstance(t, torch.Tensor) or t.is_cuda
-    return _ptr(t, dtype, numel, device=on_gpu, name=name, allow_none=allow_none)
+    if isinstance(t, torch.Tensor):
+        return _dev(t, dtype, numel, name) if t.is_cuda else _ptr(t, dtype, numel, device=False, name=name)
+    return _ptr(t, dtype, numel, name=name, allow_none=allow_none)
 
 
 class Rope:

@@ -437,8 +437,9 @@ typedef struct {
   dd_rope_layout layout;
 } dd_rope;
 
-/* Rotate rows: x bf16 [B,T,H,128] and out (may be x), each with the strides (in
- * elements, multiples of 8; the last dimension dense) of request, token and head.
+/* Rotate rows: x bf16 [B,T,H,128] and out, each with the strides (in elements,
+ * multiples of 8; the last dimension dense) of request, token and head.  out is x with
+ * the same strides, or does not overlap it.
  * Row t of request b has position start_pos[b] + t, start_pos int32 [B] device,
  * positions >= 0; new_len int32 [B] device or NULL (= T): rows t >= new_len[b]
  * are padding and neither read nor written.  B is the context's; T and H are this

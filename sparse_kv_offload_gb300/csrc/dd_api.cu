@@ -683,6 +683,7 @@ dd_status dd_rope_rows(dd_ctx *c, const dd_rope *rope, const void *x, const int6
   if (!c || T < 0 || H < 0 || H > 65535) return DD_ERR_INVALID_ARG;
   if (c->dims.B == 0 || T == 0 || H == 0) return DD_OK;
   if (!rope_ok(rope) || !rows_ok(x, x_stride) || !rows_ok(out, out_stride) || !start_pos) return DD_ERR_INVALID_ARG;
+  if (x == out && memcmp(x_stride, out_stride, 3 * sizeof(int64_t)) != 0) return DD_ERR_INVALID_ARG;
   DD_TRY(on_device(c));
   c->launches += 1;
   return cuda_ok(dd::launch_rope_rows(rope, x, x_stride, out, out_stride, c->dims.B, T, H, start_pos, new_len,

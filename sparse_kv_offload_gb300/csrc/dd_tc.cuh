@@ -77,22 +77,6 @@ __device__ __forceinline__ void tmem_ld32x32b_x16(uint32_t taddr, float *v) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 16x32bx2 tensor-memory load, 16 columns: threads 0-15 of the warp read lanes 0-15 of its
-// lane quarter at columns [c, c + 16), threads 16-31 the same lanes at [c + kSplit, c +
-// kSplit + 16).
-template <int kSplit>
-__device__ __forceinline__ void tmem_ld16_split(uint32_t taddr, float *v) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], %17;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr), "n"(kSplit));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // host: tensor maps (bf16, 128-byte swizzle), cached by their arguments
 // A [rows, 128] bf16 pool viewed as 2-D, boxes of box_rows rows x 64 columns.
 bool make_pool_map(CUtensorMap *map, const void *base, int64_t rows, int box_rows);

@@ -169,9 +169,10 @@ def test_large_scores(dd):
     assert small.all() or x["cnt"].min() == 0
 
 
-def test_rows_behind_the_end_may_hold_anything(dd):
+@pytest.mark.parametrize("G", [2, 4, 16], ids=["nq4", "nq8", "nq32"])
+def test_rows_behind_the_end_may_hold_anything(dd, G):
     """NaN scales and random codes behind kv_len, in chunks that end inside and in chunks wholly behind."""
-    x = make_case(31, 3, 2, 4, 2, 32, 12, 8, empty=0.0)
+    x = make_case(31, 3, 2, G, 2, 32, 12, 8, empty=0.0)
     x["length"] = np.array([0, 5, 200])
     want, tol = want_of(x, False)
     rng = np.random.default_rng(1)
@@ -196,11 +197,12 @@ def test_rows_behind_the_end_may_hold_anything(dd):
     assert not got[0].any()                                       # no row at all: zeros
 
 
-def test_nan_stays_with_the_queries_that_see_it(dd):
+@pytest.mark.parametrize("G", [1, 2, 4, 8], ids=["nq3", "nq6", "nq12", "nq24"])
+def test_nan_stays_with_the_queries_that_see_it(dd, G):
     """A NaN scale in a chunk: the queries that picked the chunk get NaN (in the columns of a V group, everywhere for
     K), the others their own result."""
     for which in ("V", "K"):
-        x = make_case(41, 1, 1, 4, 3, 16, 30, 10, p_hot=1.0, empty=0.0, ragged=False)
+        x = make_case(41, 1, 1, G, 3, 16, 30, 10, p_hot=1.0, empty=0.0, ragged=False)
         want, tol = want_of(x, True)
         i = int(np.flatnonzero((x["qmask"][0, 0, :x["cnt"][0, 0]] & 7) < 7)[0])
         x[which + "hot"].reshape(len(x[which + "hot"]), -1, 1152)[x["slot"][0, 0, i], 0, 1024 + 3 * 8 + 2] = 0x7F
@@ -258,16 +260,18 @@ def test_refusals(dd):
         assert ctx.launch_count() == 0 and ctx.status() == 0
 
 
-def test_same_result_every_time_and_in_graphs(dd):
+@pytest.mark.parametrize("n_heads", [4, 16, 64], ids=["nq4", "nq16", "nq64"])
+def test_same_result_every_time_and_in_graphs(dd, n_heads):
     """Repeated, captured (two graphs of one context, replayed in turn) and run on another stream: the same bits."""
     import torch
-    x = make_case(71, 2, 2, 8, 2, 16, 400, 150, ragged=True)
+    x = make_case(71, 2, 2, n_heads // 2, 2, 16, 400, 150, ragged=True)
+    Hq = n_heads
     p = [torch.from_numpy(x[n]).cuda() for n in ("Khot", "Vhot", "Kst", "Vst")]
     q, slot, cnt = tl.to_bf16(x["q"]), tl.to_i32(x["slot"]), tl.to_i32(x["cnt"])
     kw = dict(union_qmask=torch.from_numpy(x["qmask"].reshape(-1)).cuda(), kv_len=tl.to_i32(x["length"]),
               union_idx=tl.to_i32(x["idx"]), K_tail=tl.to_bf16(x["Kt"]), V_tail=tl.to_bf16(x["Vt"]))
-    with dd.Context(dd.Shape(2, 16, 2, D, 6400, 16, 150, 2), max_misses=x["n_st"], hot_slots=x["n_hot"]) as ctx:
-        outs = [torch.zeros(2, 2, 16, D, device="cuda") for _ in range(4)]
+    with dd.Context(dd.Shape(2, Hq, 2, D, 6400, 16, 150, 2), max_misses=x["n_st"], hot_slots=x["n_hot"]) as ctx:
+        outs = [torch.zeros(2, 2, Hq, D, device="cuda") for _ in range(4)]
         ctx.sparse_attn_decode_kv4(q, *p, slot, cnt, outs[0], **kw)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
@@ -308,6 +312,88 @@ def test_offsets_past_32_bits(dd):
         assert ctx.status() == 0
     want, tol = want_of(x, False, mask=False)
     assert (np.abs(out.cpu().numpy() - want) <= tol).all()
+
+
+# more units than a CTA has threads, and more units per CTA than it lists at a time
+@pytest.mark.parametrize("B,Hkv,G", [(80, 8, 3), (96, 6, 20), (1280, 8, 4), (512, 8, 20), (512, 8, 12)])
+def test_many_small_units(dd, B, Hkv, G):
+    import torch
+    cs, units, n = 16, B * Hkv, 64
+    rng = np.random.default_rng(B)
+    K, V = pages(rng, n, cs), pages(rng, n, cs)
+    cnt = rng.integers(0, 3, units)
+    slot = rng.integers(0, n, (units, 2))
+    length = rng.integers(0, 2 * cs + 1, B)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    q = torch.randn(B, 1, Hkv * G, D, generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.full((B, 1, Hkv * G, D), float("nan"), device="cuda")
+    with dd.Context(dd.Shape(B, Hkv * G, Hkv, D, 2 * cs, cs, 2, 1), max_misses=0, hot_slots=n) as ctx:
+        idx = tl.to_i32(np.tile([0, 1], (units, 1)))
+        for _ in range(2):
+            ctx.sparse_attn_decode_kv4(q, torch.from_numpy(K).cuda(), torch.from_numpy(V).cuda(), None, None, tl.to_i32(slot),
+                                       tl.to_i32(cnt), out, union_idx=idx, kv_len=tl.to_i32(length))
+            assert ctx.status() == 0
+    dev64 = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()       # noqa: E731
+    Kv, Vv = (dev64(oracle.kv4_values(p, np.zeros(n)))[dev64(slot)].flatten(1, 2) for p in (K, V))      # [units, 32, D]
+    pos = torch.arange(2 * cs, device="cuda")
+    seen = (pos < dev64(cnt)[:, None] * cs) & (pos < dev64(np.repeat(length, Hkv))[:, None])
+    qd = q.double().view(units, G, D)
+    x = (qd @ Kv.transpose(1, 2) * D ** -0.5).masked_fill(~seen[:, None], -np.inf)
+    w = torch.nan_to_num(torch.softmax(x, -1), nan=0.0)
+    want = w @ Vv
+    # scores off by 128 * 2^-23 of the sum of magnitudes, twice in a weight, and 2^-18 for the rest (as above)
+    dx = 128 * 2.0 ** -23 * (qd.abs() @ Kv.abs().transpose(1, 2)).amax(-1, keepdim=True) * D ** -0.5
+    assert ((out.double().view(units, G, D) - want).abs() <= (2 * dx + 2.0 ** -18) * Vv.abs().max()).all()
+
+
+@pytest.mark.parametrize("G", [4, 12, 30])
+def test_pending_errors_stop_the_work_and_nothing_else(dd, G):
+    """While the status word is set the call leaves its output alone, also where CTAs share units; then all is as before."""
+    import torch
+    x = make_case(91, 2, 2, G, 1, 16, 500, 400, p_hot=1.0, empty=0.0, ragged=False)
+    p = [torch.from_numpy(x[n]).cuda() for n in ("Khot", "Vhot")]
+    kw = dict(k_exp=tl.to_i32(x["ke"]), v_exp=tl.to_i32(x["ve"]))
+    q, slot, cnt = tl.to_bf16(x["q"]), tl.to_i32(x["slot"]), tl.to_i32(x["cnt"])
+    want, tol = want_of(x, False, mask=False)
+    with dd.Context(dd.Shape(2, 2 * G, 2, D, 8000, 16, 400, 1), max_misses=0, hot_slots=x["n_hot"]) as ctx:
+        for _ in range(2):
+            bad = slot.clone()
+            bad[0, 0, 3] = x["n_hot"]
+            trash = torch.zeros(2, 1, 2 * G, D, device="cuda")
+            ctx.sparse_attn_decode_kv4(q, *p, None, None, bad, cnt, trash, **kw)
+            out = torch.full((2, 1, 2 * G, D), 7.0, device="cuda")
+            ctx.sparse_attn_decode_kv4(q, *p, None, None, slot, cnt, out, **kw)
+            assert ctx.status() == dd.DD_ERR_DEVICE_CHECK and (out == 7.0).all()
+            ctx.sparse_attn_decode_kv4(q, *p, None, None, slot, cnt, out, **kw)
+            assert ctx.status() == 0
+            assert (np.abs(out.cpu().numpy() - want) <= tol).all()
+
+
+def test_two_contexts_at_once(dd):
+    """Calls of two contexts on two streams, overlapping: each context has its own workspace."""
+    import torch
+    cases = [make_case(95, 2, 2, 4, 1, 16, 300, 250), make_case(96, 2, 2, 20, 1, 16, 300, 250)]
+    wants = [want_of(x, False) for x in cases]
+    ctxs, args, outs, streams = [], [], [], []
+    for x in cases:
+        G = x["G"]
+        ctxs.append(dd.Context(dd.Shape(2, 2 * G, 2, D, 4800, 16, 250, 1), max_misses=x["n_st"], hot_slots=x["n_hot"]))
+        args.append(([tl.to_bf16(x["q"])] + [torch.from_numpy(x[n]).cuda() for n in ("Khot", "Vhot", "Kst", "Vst")]
+                     + [tl.to_i32(x["slot"]), tl.to_i32(x["cnt"])],
+                     dict(union_qmask=torch.from_numpy(x["qmask"].reshape(-1)).cuda(), kv_len=tl.to_i32(x["length"]),
+                          union_idx=tl.to_i32(x["idx"]), miss_count=tl.to_i32([x["n_st"]]), k_exp=tl.to_i32(x["ke"]),
+                          v_exp=tl.to_i32(x["ve"]))))
+        outs.append(torch.zeros(2, 1, 2 * G, D, device="cuda"))
+        streams.append(torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, (a, kw), o, s in zip(ctxs, args, outs, streams):
+            c.sparse_attn_decode_kv4(*a, o, stream=s, **kw)
+    for c, o, (want, tol) in zip(ctxs, outs, wants):
+        assert c.status() == 0
+        assert (np.abs(o.cpu().numpy() - want) <= tol).all()
+        c.close()
 
 
 @pytest.mark.parametrize("cs,host", [(16, True), (64, False)])

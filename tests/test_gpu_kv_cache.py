@@ -110,7 +110,7 @@ def test_rope_of_special_values(dd):
     top = np.isinf(want) | (np.abs(want) > 3.38e38)              # next to overflow: infinite or the largest number
     assert np.array_equal(np.sign(got[top]), np.sign(want[top])) and (np.abs(got[top]) > 3.3e38).all()
     fine = ~np.isnan(want) & ~top
-    assert (np.abs(got - want)[fine] <= np.abs(want[fine]) * 2.0 ** -8 + 2.0 ** -133).all()
+    assert (np.abs(got[fine] - want[fine]) <= np.abs(want[fine]) * 2.0 ** -8 + 2.0 ** -133).all()
 
 
 class Cache:
@@ -352,7 +352,9 @@ def test_refusals(dd):
             with pytest.raises((ValueError, TypeError, dd.DDError)):
                 ctx.append_kv(k, x, start, Kh=home, Vh=home)
         off = torch.zeros(B * T * H * D + 8, **bf)[1:1 + B * T * H * D].view(B, T, H, D)      # not on 16 bytes
-        for x, o in ((off, k), (k, off), (k, k[:, :, :1].expand(B, T, H, D)), (k[:1], k), (k[0], k)):
+        tall = torch.zeros(B, T, 2 * H, D, **bf)       # the same first row, other strides
+        for x, o in ((off, k), (k, off), (k, k[:, :, :1].expand(B, T, H, D)), (k[:1], k), (k[0], k),
+                     (tall[:, :, :H], tall[:, :, ::2])):
             with pytest.raises((ValueError, dd.DDError)):
                 ctx.rope(rope, x, o, start)
         for kw in (dict(), dict(Kh=home), dict(Kh=home, Vh=home, k_exp=start),

@@ -223,20 +223,20 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_rows(Rope r, const uint16
   const uint4 *src = reinterpret_cast<const uint4 *>(x + k.b * xs.b + k.t * xs.t + h0 * xs.h);
   uint4 *dst = reinterpret_cast<uint4 *>(out + k.b * os.b + k.t * os.t + h0 * os.h);
   const int64_t xstep = xs.h / 8, ostep = os.h / 8;
-  // the next two heads' pieces are on their way while one is turned
-  uint4 a0 = src[pa], b0 = src[pb], a1 = a0, b1 = b0;
-  if (h0 + 1 < h1) a1 = src[xstep + pa], b1 = src[xstep + pb];
+  // the next head's pieces are on their way while one is turned
+  uint4 a0 = src[pa], b0 = src[pb];
   Turn t;
   make_turn(r, i, k.pos, t);
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
-    uint4 a2 = a1, b2 = b1;
-    if (h + 2 < h1) a2 = src[2 * xstep + pa], b2 = src[2 * xstep + pb];
+    src += xstep;
+    uint4 a1 = a0, b1 = b0;
+    if (h + 1 < h1) a1 = src[pa], b1 = src[pb];
     rotate(r, i, t, a0, b0);
     dst[pa] = a0;
     dst[pb] = b0;
-    src += xstep, dst += ostep;
-    a0 = a1, b0 = b1, a1 = a2, b1 = b2;
+    dst += ostep;
+    a0 = a1, b0 = b1;
   }
 }
 

@@ -366,6 +366,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           float x[32], pm = -INFINITY;
           if (some) {
             tmem_ld_s(tmem + lane_base + (t & 1) * 128 + 64 * wc, x);
+            // (the mask comes after the factor, which may be 0)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] *= mul;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t meta = s_meta[t % kMeta][2 * bi + h];
@@ -376,8 +379,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
                   if (e >= rows) x[16 * h + e] = -INFINITY;
               }
             }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] *= mul;
             float m8[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) m8[e] = fmaxf(fmaxf(x[e], x[e + 8]), fmaxf(x[e + 16], x[e + 24]));

@@ -218,6 +218,17 @@ def test_nan_stays_with_the_queries_that_see_it(dd, G):
             assert (np.abs(got - want)[0, j][:, ~bad] <= tol[0, j]).all()
 
 
+@pytest.mark.parametrize("G", [1, 4, 8], ids=["nq3", "nq12", "nq24"])
+def test_scores_that_underflow_keep_the_mask(dd, G):
+    """Queries and keys so small that every score is zero in fp32: equal weights for the rows that are seen, none for
+    the others."""
+    x = make_case(61, 2, 2, G, 3, 16, 40, 12, qscale=2.0 ** -126)
+    x["ke"] = np.full(2, -64)
+    want, tol = want_of(x, False)
+    got, st = run(dd, x, False)
+    assert st == 0 and (np.abs(got - want) <= tol).all()
+
+
 def test_bad_pages_are_reported(dd):
     x = make_case(51, 1, 2, 4, 1, 16, 30, 10, empty=0.0, ragged=False)
     for name, value in (("slot", x["n_hot"]), ("slot", -1 - x["n_st"]), ("slot", -2 ** 31), ("cnt", x["U"] + 1), ("cnt", -1),

@@ -132,8 +132,8 @@ __device__ __forceinline__ void finish(const Attn4Params &p, int unit, int qv, P
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
       x *= sl2;
-      const float m = fmaxf(s.m, x);      // a NaN score leaves m: its weight is NaN
-      const float wa = weight_of(s.m, m), wt = weight_of(x, m);
+      const float m = fmaxf(s.m, x);      // a NaN score leaves m: its weight is NaN, ...
+      const float wa = weight_of(s.m, m), wt = exp2f(x - m);      // ... as is that of +inf, and of -inf alone
       s.l = s.l * wa + wt;
       s.o.x = s.o.x * wa + wt * bf_lo(vw.x);
       s.o.y = s.o.y * wa + wt * bf_hi(vw.x);

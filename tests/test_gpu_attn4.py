@@ -229,6 +229,25 @@ def test_scores_that_underflow_keep_the_mask(dd, G):
     assert st == 0 and (np.abs(got - want) <= tol).all()
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("G", [2, 12, 24])
+def test_infinite_scores_of_the_new_rows(dd, G, sign):
+    """A new row whose key is infinite: NaN for the query vectors whose score is +inf, no weight where it is -inf."""
+    for empty in (0.0, 1.0):
+        x = make_case(62, 2, 2, G, 1, 16, 40, 12, empty=empty, ragged=False)
+        x["Kt"] = x["Kt"].copy()
+        x["Kt"][..., 0] = synth.f32_to_bf16(np.full(1, sign * np.inf, np.float32))[0]
+        want, tol = want_of(x, False)
+        got, st = run(dd, x, True)
+        assert st == 0
+        up = oracle.bf16_decode(x["q"])[..., 0] * sign >= 0        # 0 * inf: NaN too
+        assert 0 < up.sum() < up.size
+        if empty:
+            assert np.isnan(got).all()                             # nothing else: -inf - -inf
+        else:
+            assert np.isnan(got[up]).all() and (np.abs(got - want) <= tol)[~up].all()
+
+
 def test_bad_pages_are_reported(dd):
     x = make_case(51, 1, 2, 4, 1, 16, 30, 10, empty=0.0, ragged=False)
     for name, value in (("slot", x["n_hot"]), ("slot", -1 - x["n_st"]), ("slot", -2 ** 31), ("cnt", x["U"] + 1), ("cnt", -1),

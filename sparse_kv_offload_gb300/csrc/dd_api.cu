@@ -667,6 +667,12 @@ static dd_status on_device(const dd_ctx *c) {
   return dev == c->device ? DD_OK : DD_ERR_INVALID_ARG;
 }
 
+// Looked up on every call: what lay at an address before says nothing about what does now.
+static dd_status kv_views(const void *Kh, const void *Vh, const void **kd, const void **vd) {
+  DD_TRY(device_view(Kh, kd));
+  return device_view(Vh, vd);
+}
+
 static bool rope_ok(const dd_rope *r) {
   return r && r->table && aligned16(r->table) && r->rot_dim >= 32 && r->rot_dim <= kD && r->rot_dim % 32 == 0 &&
          (r->layout == DD_ROPE_HALF || r->layout == DD_ROPE_INTERLEAVED);
@@ -705,7 +711,7 @@ dd_status dd_append_kv(dd_ctx *c, const dd_append_args *a, dd_stream_t stream) {
   const void *kd = nullptr, *vd = nullptr;
   if (a->Kh) {
     if (!aligned16(a->Kh) || !aligned16(a->Vh)) return DD_ERR_INVALID_ARG;
-    DD_TRY(host_kv_views(c, a->Kh, a->Vh, &kd, &vd));
+    DD_TRY(kv_views(a->Kh, a->Vh, &kd, &vd));
   }
   c->launches += 1;
   return cuda_ok(dd::launch_append(a, const_cast<void *>(kd), const_cast<void *>(vd), c->dims.B, c->dims.Hkv, c->C,
@@ -722,7 +728,7 @@ dd_status dd_gather_kv4(dd_ctx *c, const void *Kh, const void *Vh, const int32_t
   if (c->max_misses == 0) return DD_OK;
   DD_TRY(on_device(c));
   const void *kd, *vd;
-  DD_TRY(host_kv_views(c, Kh, Vh, &kd, &vd));
+  DD_TRY(kv_views(Kh, Vh, &kd, &vd));
   c->launches += 1;
   return cuda_ok(dd::launch_gather4(static_cast<const uint8_t *>(kd), static_cast<const uint8_t *>(vd), miss_list,
                                     miss_count, Kst, Vst, expand != 0, k_exp, v_exp, c->max_misses, c->units,

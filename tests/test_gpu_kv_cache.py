@@ -408,3 +408,36 @@ def test_append_is_captured_and_replayed(dd):
             ctx.append_kv(k, k, tl.to_i32([i * T] * B), rope=rope, Kh=K2, Vh=V2, kv_format=dd.KV_4BIT)
         assert ctx.status() == 0
         assert torch.equal(K, K2) and torch.equal(V, V2) and K.any()
+
+
+def test_home_memory_is_looked_up_on_every_call(dd):
+    """The C calls refuse host memory that is no longer pinned, although they took the same address before."""
+    import torch
+    B, T, H, cs, C = 1, 2, 1, 16, 2
+    k = torch.ones(B, T, H, D, dtype=torch.bfloat16, device="cuda")
+    start = torch.zeros(B, dtype=torch.int32, device="cuda")
+    lst, n = tl.to_i32([0]), tl.to_i32([1])
+    home = [torch.zeros(1 << 16, dtype=torch.uint8) for _ in range(2)]
+    at = [(t.data_ptr() + 4095) // 4096 * 4096 for t in home]      # a page of its own each
+    st4 = [torch.zeros(1, cs * 72, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    strides = (T * H * D, H * D, D)
+    with dd.Context(dd.Shape(B, H, H, D, C * cs, cs, 1, 1), max_misses=1) as ctx:
+        args = dd._append_args.pack(k.data_ptr(), k.data_ptr(), *strides, *strides, T, dd.KV_4BIT, start.data_ptr(), 0, 0,
+                                    *at, 0, 0, 0, 0, 0)
+
+        def calls():
+            a = dd._lib.dd_append_kv(ctx._h, args, None)
+            g = dd._lib.dd_gather_kv4(ctx._h, *at, lst.data_ptr(), n.data_ptr(), st4[0].data_ptr(), st4[1].data_ptr(), 0,
+                                      None, None, None)
+            torch.cuda.synchronize()
+            return a, g
+        assert calls() == (dd.DD_ERR_INVALID_ARG,) * 2
+        rt = torch.cuda.cudart()
+        for p in at:
+            assert int(rt.cudaHostRegister(p, 4096, 0)) == 0
+        try:
+            assert calls() == (dd.DD_OK,) * 2 and ctx.status() == 0 and st4[0].any()
+        finally:
+            for p in at:
+                assert int(rt.cudaHostUnregister(p)) == 0
+        assert calls() == (dd.DD_ERR_INVALID_ARG,) * 2

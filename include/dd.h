@@ -371,8 +371,9 @@ dd_status dd_update_residency(dd_ctx *ctx, int32_t step, int32_t cap, int32_t sl
  * Rotary positions, appending to the cache, and a cache held in 4 bits
  *
  * These calls take a context like every other one.  They run on the current
- * device, which has to be the context's (DD_ERR_INVALID_ARG otherwise), write
- * nothing on the host, and may all be captured into a CUDA graph.
+ * device, which has to be the context's (DD_ERR_INVALID_ARG otherwise), keep
+ * nothing on the host from one call for the next, and may all be captured into
+ * a CUDA graph.
  *
  * The 4-bit cache.  A row of 128 values is 64 bytes of e2m1 codes (byte i: value
  * 2i in the low nibble, value 2i+1 in the high nibble) and eight e4m3 scales,
@@ -502,7 +503,7 @@ dd_status dd_gather_kv4(dd_ctx *ctx, const void *Kh, const void *Vh, const int32
  *                dd_resolve_union (ascending, no chunk twice), needed with kv_len.
  * Attention over a whole cache: k = C, union_cnt = the chunks in use, union_idx =
  * 0, 1, ..., union_slot = their pages.  A query without a row gets zeros.
- * B*Hkv*(Umax*cs/16 + 1) has to stay below 2^29 (DD_ERR_INVALID_ARG). */
+ * B*Hkv*(Umax*cs/16 + 1) has to stay below 2^30 (DD_ERR_INVALID_ARG). */
 dd_status dd_sparse_attn_decode_kv4(dd_ctx *ctx, const void *q, const void *Khot, const void *Vhot,
                                     const void *Kst, const void *Vst, const int32_t *k_exp, const int32_t *v_exp,
                                     const void *K_tail, const void *V_tail, const int32_t *union_idx,

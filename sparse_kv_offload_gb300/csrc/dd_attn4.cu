@@ -14,6 +14,10 @@
 //     interleaved before they are converted.
 // Query vectors are the narrow side (8 a tile), so the 4 or 8 of a KV head's
 // group are not padded to 16.
+// Whole cache, 8 requests of 128K (842 MB): 179 us, where the copies alone take 131 and
+// everything but the copies 160-176.  A tile of 32 rows takes 748 instructions: 128 conversions
+// and 128 multiplications, 41 to interleave V's rows, 64 additions of sums, the rest loads,
+// softmax and moves.
 //
 // Precision.  A code times its scale is exact in fp16.  A query vector is scaled
 // by a power of two to just below 2^15, where its 8-bit significands are exact in
@@ -534,7 +538,11 @@ cudaError_t launch_t(int grid, const Attn4Params &p, cudaStream_t s) {
 
 }  // namespace
 
-// Up to 8 query vectors: one tile a warp, up to 16: two; more: tcgen05.
+// Up to 8 query vectors: one tile a warp, up to 16: two; more: tcgen05.  Both sides of the
+// second border (us, mma.sync in groups of 16 / tcgen05): 12 query vectors 41 / 66, 16: 79 /
+// 120, 20: 44.3 / 42.3, 24: 17.5 / 17.5, 40: 215 / 141, 64: 87 / 62; and with 4 the whole cache
+// of 8 requests takes 179 / 489.  (The first border is a tile's width: up to it a second tile
+// would hold padding only.)
 Attn4Plan attn4_plan(int units, int NQ, int sm_count) {
   Attn4Plan pl;
   pl.nt = NQ <= 8 ? 1 : NQ <= 16 ? 2 : 0;

@@ -1,5 +1,5 @@
 // Shared device code of the two attentions over 4-bit pages (dd_attn4.cu: mma.sync, up to
-// 16 query vectors a group; dd_attn4_tc.cu: tcgen05): the units and how the CTAs share
+// 16 query vectors a unit; dd_attn4_tc.cu: tcgen05, up to 64): the units and how the CTAs share
 // them, the blocks' look-up and loads, the queries in fp16, the step's own rows and the
 // joining of a unit's parts.
 #pragma once

@@ -2,7 +2,7 @@
 // query vectors per KV head.
 //
 // With many query vectors the products, not the bytes, bound the mma.sync kernel
-// (dd_attn4.cu), and its groups of 16 decode a unit's pages once each.  Here a page is
+// (dd_attn4.cu), and each 16 of them would decode a unit's pages again.  Here a page is
 // decoded once, into shared memory, for up to 64 query vectors, and the accumulators
 // live in tensor memory.  One CTA per SM; a tile is 128 rows (eight blocks), so that a
 // tile's fixed costs (barriers, waits, the vote) are paid half as often as with 64:
@@ -21,9 +21,10 @@
 // nearest, and the next product overwrites it.
 //
 // Bound by the softmax threads' chain per tile (some 3,000 cycles; the products take 1,024,
-// the decoding 2,000, and both run beside it).  32B-class layer, five queries: the
-// mma.sync kernel in groups of 16 215 us, 64-row tiles 182, 128-row tiles 151, both parts
-// of P in one operand and O taken over every eight tiles instead of two 143.  Sixteen softmax
+// the decoding 2,000, and both run beside it).  32B-class layer, five queries
+// (171 MB of pages, floor 25 us): the mma.sync kernel in groups of 16 215 us, 64-row tiles
+// 182, 128-row tiles 151, both parts of P in one operand and O taken over every eight tiles
+// instead of two 141.  Sixteen softmax
 // warps (80 registers) gain 1-3% with 40 or more query vectors and lose 5% with 20; eight
 // decoding warps (96 registers) lose 10%.
 #include "dd_attn4.cuh"

@@ -79,18 +79,25 @@ __device__ __forceinline__ void group_scales(uint32_t top_a, uint32_t top_b, flo
   inv_b = f.y > 0.f ? __fdividef(1.f, f.y) * mul : 0.f;
 }
 
-// Eight bf16 values and mul / scale -> four bytes of codes.
-__device__ __forceinline__ uint32_t encode8(const float (&x)[8], float inv) {
+// Eight bf16 values (x; v as they are) and mul / scale -> four bytes of codes.  The codes'
+// ties are multiples of 1/4 and other quotients at least 2^-11 away from them, so
+// rounding the product to multiples of 2^-13 puts every tie back in its place too, by two
+// instructions of the FMA pipe: 1536 is added and taken away.  That loses the sign of a
+// value that becomes 0, so the signs are taken from v.
+__device__ __forceinline__ uint32_t encode8(const uint4 &v, const float (&x)[8], float inv) {
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = to_16_bits(x[i] * inv);
+  for (int i = 0; i < 8; ++i) y[i] = __fadd_rn(fmaf(x[i], inv, 1536.f), -1536.f);
   uint32_t r;
   asm("{\n .reg .b8 b0, b1, b2, b3;\n cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
       " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
       " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n mov.b32 %0, {b0, b1, b2, b3};\n}\n"
       : "=r"(r)
       : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
-  return r;
+  // value k's sign is bit 7 of byte k; times 17 it lies in bits 3 and 7 of bytes 1 and 3
+  const uint32_t a = (__byte_perm(v.x, v.y, 0x7531) & 0x80808080u) * 17u;
+  const uint32_t b = (__byte_perm(v.z, v.w, 0x7531) & 0x80808080u) * 17u;
+  return r | (__byte_perm(a, b, 0x7531) & 0x88888888u);
 }
 
 }  // namespace dd

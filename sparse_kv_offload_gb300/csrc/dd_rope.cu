@@ -20,7 +20,14 @@
 //
 // A row is 8 lanes x 16 values: lane i turns pairs 8i..8i+7 (two 16-byte pieces
 // of the row), so a token's sines and cosines are computed once per lane and
-// serve all the heads that the warp goes through.  Bound by HBM.
+// serve all the heads that the warp goes through.
+//
+// Bound by loads in flight and issue slots, near HBM: four prompts of 4K with 64 heads (537 MB)
+// 108 us, 73% of the copy rate (every value by the sticky path: 231; the loads of two heads
+// ahead instead of one: 117).  Appending 201 MB to bf16 pages takes 42 us (70%; first form 61).
+// 4 bits are bound by the rounding (a product, an addition, a mask and half a conversion a
+// value): 268 MB of keys and values into 75 MB of pages take 65 us, 5.3 TB/s.  A step's call of
+// a few rows takes 2.6 us (rotation) or 3.1 us (append) on the device, a launch and one row's time.
 #include <math.h>
 
 #include "dd_attn.cuh"
@@ -292,8 +299,8 @@ __device__ __forceinline__ void quantise(const uint4 &va, const uint4 &vb, float
   float a[8], b[8];
   unpack8(va, a);
   unpack8(vb, b);
-  ca = encode8(a, ia);
-  cb = encode8(b, ib);
+  ca = encode8(va, a, ia);
+  cb = encode8(vb, b, ib);
 }
 
 template <bool kFour>

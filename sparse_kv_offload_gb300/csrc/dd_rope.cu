@@ -18,16 +18,20 @@
 // (With the sines and cosines in fp32 alone the interval is as wide as the larger value's
 // error, and a third of the warps had a lane that went on.)
 //
-// A row is 8 lanes x 16 values: lane i turns pairs 8i..8i+7 (two 16-byte pieces
+// A row is 8 lanes x 16 values: lane i turns up to eight pairs (two 16-byte pieces
 // of the row), so a token's sines and cosines are computed once per lane and
 // serve all the heads that the warp goes through.
 //
-// Bound by loads in flight and issue slots, near HBM: four prompts of 4K with 64 heads (537 MB)
-// 108 us, 73% of the copy rate (every value by the sticky path: 231; the loads of two heads
-// ahead instead of one: 117).  Appending 201 MB to bf16 pages takes 42 us (70%; first form 61).
-// 4 bits are bound by the rounding (a product, an addition, a mask and half a conversion a
-// value): 268 MB of keys and values into 75 MB of pages take 65 us, 5.3 TB/s.  A step's call of
-// a few rows takes 2.6 us (rotation) or 3.1 us (append) on the device, a launch and one row's time.
+// The rotation alone is bound by HBM: four prompts of 4K tokens with 64 heads, half of each
+// turned (537 MB), take 84 us, 95% of the copy rate; all of 2K tokens' heads turned (268 MB)
+// 48 us, 82%.  (Every value by the sticky path: 231 us; the next head's pieces in registers
+// instead of four heads' on their way to shared memory 103 and 59; lanes 0-3 turning all of
+// half a row's pairs instead of every lane half of its own 108.)
+// Appending 201 MB to bf16 pages takes 39.5 us, 75% (first form 61), bound by the loads that
+// 16 warps an SM keep in flight; copies to shared memory gain 1 us there, keys and values by
+// blocks of their own lose 4.  4 bits are bound by the issue slots, most of them the
+// rounding's: 201 MB into 57 MB of pages in some 70 us.  A step's call of a few rows takes
+// 2.6 us (rotation) or 3.1 us (append) on the device, a launch and one row's time.
 #include <math.h>
 
 #include "dd_attn.cuh"
@@ -38,6 +42,7 @@ namespace dd {
 namespace {
 
 constexpr int kRopeThreads = 128;
+constexpr int kAhead = 4;               // heads on their way (two: 86 and 53 us, six: 84 and 52)
 constexpr int kLut = 512;               // stored angles of a turn
 constexpr int kLutOff = 64 * 8;         // table: 64 frequencies, then the stored angles
 
@@ -45,7 +50,6 @@ struct Rope {
   const uint64_t *freq;                 // turns per position * 2^64
   const float4 *lut;                    // {cos hi, sin hi, cos lo, sin lo} * gain
   int rot_dim;                          // 0: no rotation
-  bool half;
 };
 
 // The eight pairs' cosines and sines at one position, hi + lo.
@@ -112,24 +116,29 @@ __device__ __forceinline__ uint32_t dot2_bf16(float x1, float ch, float cl, floa
   return f2bf(__uint_as_float(w));
 }
 
-// The two 16-byte pieces (0..15) of a row that lane i (0..7) holds: with halves
-// paired the pieces i and i + rot_dim/16 of a lane that turns, else 2i, 2i + 1.
-__device__ __forceinline__ void pieces(const Rope &r, int i, bool rotated, int &pa, int &pb) {
-  const bool apart = rotated && r.half && i < r.rot_dim / 16;
-  pa = apart ? i : 2 * i;
-  pb = apart ? i + r.rot_dim / 16 : 2 * i + 1;
+// The two 16-byte pieces (0..15) of a row that lane i (0..7) holds.  With halves paired:
+// a piece of the first half and its partner, the lanes behind them sharing what
+// passes through; else pieces i and i + 8, so that a rotation of half the row leaves
+// every lane half the work.  Lanes i and i ^ 1 hold both halves of the same two groups of 16,
+// and eight lanes load and store whole lines.
+template <bool kHalf>
+__device__ __forceinline__ void pieces(const Rope &r, int i, int &pa, int &pb) {
+  const int n = r.rot_dim / 16;          // lanes that turn (halves paired)
+  const bool turns = kHalf && i < n;
+  pa = !kHalf || turns ? i : n + i;
+  pb = turns ? i + n : i + 8;
 }
 
+// The pairs of a lane: 8 i .. of halves, else 4 i .. and 32 + 4 i ..
+template <bool kHalf>
 __device__ __forceinline__ void make_turn(const Rope &r, int i, int64_t pos, Turn &t) {
-  if (i >= r.rot_dim / 16) return;
+  if (kHalf ? i >= r.rot_dim / 16 : i >= r.rot_dim / 8) return;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) cos_sin((uint64_t)pos * __ldg(r.freq + 8 * i + e), r.lut, t.ch[e], t.cl[e], t.sh[e], t.sl[e]);
-}
-
-// interleaved: pairs 0..3 lie in a, 4..7 in b
-__device__ __forceinline__ void pair_of(bool half, const float (&a)[8], const float (&b)[8], int e, float &x, float &y) {
-  x = half ? a[e] : (e < 4 ? a[2 * (e & 3)] : b[2 * (e & 3)]);
-  y = half ? b[e] : (e < 4 ? a[2 * (e & 3) + 1] : b[2 * (e & 3) + 1]);
+  for (int e = 0; e < 8; ++e) {
+    if (!kHalf && e == 4 && i + 8 >= r.rot_dim / 8) return;
+    const int pair = kHalf ? 8 * i + e : 4 * i + (e & 3) + (e >> 2) * 32;
+    cos_sin((uint64_t)pos * __ldg(r.freq + pair), r.lut, t.ch[e], t.cl[e], t.sh[e], t.sl[e]);
+  }
 }
 
 // The pair's rotation with every rounding error kept.  (A function of its own: the common
@@ -144,21 +153,16 @@ __device__ __forceinline__ float dot2_near(float x, float ch, float cl, float y,
   return fmaf(x, ch, p) + fmaf(x, cl, fmaf(y, sl, fmaf(y, sh, -p)));
 }
 
-// Rotate the lane's two pieces in place.
-__device__ __forceinline__ void rotate(const Rope &r, int i, const Turn &t, uint4 &va, uint4 &vb) {
-  if (i >= r.rot_dim / 16) return;
+// N pairs (x, y) turned by t's E0 .., as bf16 pairs
+template <int N, int E0>
+__device__ __forceinline__ void rotate_pairs(const Turn &t, const float (&x)[N], const float (&y)[N], uint32_t (&o)[N]) {
   constexpr float kUp = 1.f + 2.384185791015625e-07f, kDown = 1.f - 2.384185791015625e-07f;   // 1 +- 2^-22
-  float a[8], b[8];
-  unpack8(va, a);
-  unpack8(vb, b);
-  uint32_t o[8], near = 0;      // pairs {x, y}; bit e: pair e is next to a tie
+  uint32_t near = 0;            // bit e: pair e is next to a tie
   float finite = 0.f;           // NaN once a value is infinite or NaN
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float x, y;
-    pair_of(r.half, a, b, e, x, y);
-    const float p = dot2_near(x, t.ch[e], t.cl[e], -y, t.sh[e], t.sl[e]);
-    const float q = dot2_near(y, t.ch[e], t.cl[e], x, t.sh[e], t.sl[e]);
+  for (int e = 0; e < N; ++e) {
+    const float p = dot2_near(x[e], t.ch[E0 + e], t.cl[E0 + e], -y[e], t.sh[E0 + e], t.sl[E0 + e]);
+    const float q = dot2_near(y[e], t.ch[E0 + e], t.cl[E0 + e], x[e], t.sh[E0 + e], t.sl[E0 + e]);
     o[e] = cvt_bf16x2(p * kUp, q * kUp);
     if (o[e] != cvt_bf16x2(p * kDown, q * kDown)) near |= 1u << e;
     finite = fmaf(p, 0.f, fmaf(q, 0.f, finite));
@@ -166,22 +170,65 @@ __device__ __forceinline__ void rotate(const Rope &r, int i, const Turn &t, uint
   if (finite != finite) near = 0xFFu;      // the error terms of infinities say nothing
   if (near) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float x, y;
-      pair_of(r.half, a, b, e, x, y);
-      if (near >> e & 1u) o[e] = rotate_exactly(x, y, t.ch[e], t.cl[e], t.sh[e], t.sl[e]);
-    }
+    for (int e = 0; e < N; ++e)
+      if (near >> e & 1u)
+        o[e] = rotate_exactly(x[e], y[e], t.ch[E0 + e], t.cl[E0 + e], t.sh[E0 + e], t.sl[E0 + e]);
   }
-  if (r.half) {
+}
+
+// A piece of neighbouring pairs
+template <int E0>
+__device__ __forceinline__ void rotate_piece(const Turn &t, uint4 &v) {
+  float a[8], x[4], y[4];
+  unpack8(v, a);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = a[2 * e], y[e] = a[2 * e + 1];
+  uint32_t o[4];
+  rotate_pairs<4, E0>(t, x, y, o);
+  v = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Rotate the lane's two pieces in place.
+template <bool kHalf>
+__device__ __forceinline__ void rotate(const Rope &r, int i, const Turn &t, uint4 &va, uint4 &vb) {
+  if constexpr (kHalf) {
+    if (i >= r.rot_dim / 16) return;
+    float a[8], b[8];
+    unpack8(va, a);
+    unpack8(vb, b);
+    uint32_t o[8];
+    rotate_pairs<8, 0>(t, a, b, o);
     va = make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410), __byte_perm(o[4], o[5], 0x5410),
                     __byte_perm(o[6], o[7], 0x5410));
     vb = make_uint4(__byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632), __byte_perm(o[4], o[5], 0x7632),
                     __byte_perm(o[6], o[7], 0x7632));
   } else {
-    va = make_uint4(o[0], o[1], o[2], o[3]);
-    vb = make_uint4(o[4], o[5], o[6], o[7]);
+    if (i < r.rot_dim / 8) rotate_piece<0>(t, va);
+    if (i + 8 < r.rot_dim / 8) rotate_piece<4>(t, vb);
   }
 }
+
+// A thread's 16-byte pieces of the next kAhead heads, on their way to shared memory: no
+// thread reads another's, so there is no barrier.
+template <int kPieces>
+struct Ahead {
+  uint4 piece[kAhead][kPieces][kRopeThreads];
+
+  // asks for pieces of head n (none behind the last one); the slot's last reader is done
+  template <typename F>
+  __device__ __forceinline__ void ask(int n, int heads, F src) {
+    if (n < heads) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(&piece[n % kAhead][i][threadIdx.x])),
+                     "l"(src(i))
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // the next head's pieces are here, kAhead - 1 later ones may still be on their way
+  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
+};
 
 struct Rows {          // where the rows of a call lie, in elements
   int64_t b, t, h;
@@ -214,6 +261,7 @@ __device__ __forceinline__ Token token_of(int64_t n, int B, int T, const int32_t
   return k;
 }
 
+template <bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads) k_rope_rows(Rope r, const uint16_t *__restrict__ x, Rows xs,
                                                             uint16_t *out, Rows os, int B, int T, int H, int heads,
                                                             const int32_t *__restrict__ start_pos,
@@ -225,25 +273,30 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope_rows(Rope r, const uint16
                            INT64_MAX, status);
   if (!k.ok) return;
   int pa, pb;
-  pieces(r, i, true, pa, pb);
+  pieces<kHalf>(r, i, pa, pb);
   const int h0 = blockIdx.y * heads, h1 = min(H, h0 + heads);
   const uint4 *src = reinterpret_cast<const uint4 *>(x + k.b * xs.b + k.t * xs.t + h0 * xs.h);
   uint4 *dst = reinterpret_cast<uint4 *>(out + k.b * os.b + k.t * os.t + h0 * os.h);
   const int64_t xstep = xs.h / 8, ostep = os.h / 8;
-  // the next head's pieces are on their way while one is turned
-  uint4 a0 = src[pa], b0 = src[pb];
+  const int n = h1 - h0;
+  __shared__ Ahead<2> ahead;
+  uint4 a = src[pa], b = src[pb];
+#pragma unroll
+  for (int m = 1; m < kAhead; ++m)
+    ahead.ask(m, n, [&](int e) { return src + m * xstep + (e ? pb : pa); });
   Turn t;
-  make_turn(r, i, k.pos, t);
+  make_turn<kHalf>(r, i, k.pos, t);
 #pragma unroll 1
-  for (int h = h0; h < h1; ++h) {
-    src += xstep;
-    uint4 a1 = a0, b1 = b0;
-    if (h + 1 < h1) a1 = src[pa], b1 = src[pb];
-    rotate(r, i, t, a0, b0);
-    dst[pa] = a0;
-    dst[pb] = b0;
+  for (int m = 0;;) {
+    rotate<kHalf>(r, i, t, a, b);
+    ahead.ask(m + kAhead, n, [&](int e) { return src + (m + kAhead) * xstep + (e ? pb : pa); });
+    dst[pa] = a;
+    dst[pb] = b;
     dst += ostep;
-    a0 = a1, b0 = b1;
+    if (++m == n) break;
+    ahead.wait();
+    a = ahead.piece[m % kAhead][0][threadIdx.x];
+    b = ahead.piece[m % kAhead][1][threadIdx.x];
   }
 }
 
@@ -261,16 +314,14 @@ struct AppendP {
 };
 
 // codes and scales of the lane's two pieces into row `row` of the page
-__device__ __forceinline__ void store4(uint8_t *page, int row, int pa, int pb, int i, bool apart, uint32_t ca,
-                                       uint32_t cb, uint32_t sa, uint32_t sb) {
+__device__ __forceinline__ void store4(uint8_t *page, int row, int pa, int pb, bool even, uint32_t ca, uint32_t cb,
+                                       uint32_t sa, uint32_t sb) {
   uint8_t *blk = page + (row >> 4) * kBlk4;
   uint8_t *codes = blk + (row & 15) * 64;
   uint8_t *scales = blk + kBlk4Scales + (row & 15) * 8;
   *reinterpret_cast<uint32_t *>(codes + pa * 4) = ca;
   *reinterpret_cast<uint32_t *>(codes + pb * 4) = cb;
-  if (!apart) {
-    scales[i] = (uint8_t)sa;
-  } else if ((i & 1) == 0) {   // lanes i, i + 1 hold the halves of groups pa/2 and pb/2
+  if (even) {      // (the neighbour lane holds the groups' other halves)
     scales[pa >> 1] = (uint8_t)sa;
     scales[pb >> 1] = (uint8_t)sb;
   }
@@ -283,16 +334,14 @@ __device__ __forceinline__ uint32_t top8(const uint4 &v) {
   return max(t & 0xFFFFu, t >> 16);
 }
 
-// Quantise the lane's two pieces, values divided by 2^e (mul = 2^-e).  `apart`: the other
-// half of each piece's group of 16 is the neighbour lane's, else the two pieces are one
-// group.  Every lane of the eight takes part.
-__device__ __forceinline__ void quantise(const uint4 &va, const uint4 &vb, float mul, bool apart, unsigned lanes,
-                                         uint32_t &ca, uint32_t &cb, uint32_t &sa, uint32_t &sb) {
+// Quantise the lane's two pieces, values divided by 2^e (mul = 2^-e); the other half of
+// each piece's group of 16 is the neighbour lane's.  Every lane of the eight takes part.
+__device__ __forceinline__ void quantise(const uint4 &va, const uint4 &vb, float mul, unsigned lanes, uint32_t &ca,
+                                         uint32_t &cb, uint32_t &sa, uint32_t &sb) {
   uint32_t ta = top8(va), tb = top8(vb);
   const uint32_t both = __shfl_xor_sync(lanes, ta | tb << 16, 1);
-  const uint32_t oa = apart ? both & 0xFFFFu : tb, ob = apart ? both >> 16 : ta;
-  ta = max(ta, oa);
-  tb = max(tb, ob);
+  ta = max(ta, both & 0xFFFFu);
+  tb = max(tb, both >> 16);
   // (mul is a power of two: the largest value scaled is the largest of the scaled values)
   float ia, ib;
   group_scales(ta, tb, mul, sa, sb, ia, ib);
@@ -303,7 +352,24 @@ __device__ __forceinline__ void quantise(const uint4 &va, const uint4 &vb, float
   cb = encode8(vb, b, ib);
 }
 
-template <bool kFour>
+// A whole group (pieces 2 i and 2 i + 1) by one lane: codes and scale.
+__device__ __forceinline__ uint2 quantise_group(const uint4 &va, const uint4 &vb, float mul, uint32_t &scale) {
+  const uint32_t top = max(top8(va), top8(vb));
+  uint32_t same;
+  float inv, inv2;
+  group_scales(top, top, mul, scale, same, inv, inv2);
+  float a[8], b[8];
+  unpack8(va, a);
+  unpack8(vb, b);
+  return make_uint2(encode8(va, a, inv), encode8(vb, b, inv));
+}
+__device__ __forceinline__ void store_group(uint8_t *page, int row, int i, uint2 codes, uint32_t scale) {
+  uint8_t *blk = page + (row >> 4) * kBlk4;
+  *reinterpret_cast<uint2 *>(blk + (row & 15) * 64 + i * 8) = codes;
+  blk[kBlk4Scales + (row & 15) * 8 + i] = (uint8_t)scale;
+}
+
+template <bool kFour, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads) k_append(AppendP p) {
   pdl_wait();
   pdl_trigger();
@@ -313,23 +379,24 @@ __global__ void __launch_bounds__(kRopeThreads) k_append(AppendP p) {
                            (int64_t)p.C << p.shift, p.status);
   if (!k.ok) return;
   int pa, pb;
-  pieces(p.r, i, true, pa, pb);
-  const bool apart = pb != pa + 1;
+  pieces<kHalf>(p.r, i, pa, pb);
+  const bool even = (i & 1) == 0;
+  const int qa = kFour ? 2 * i : i, qb = kFour ? qa + 1 : i + 8;     // the value row's pieces
   const int c = (int)(k.pos >> p.shift), row = (int)(k.pos & (p.cs - 1));
   const int64_t page_bytes = (int64_t)p.cs * (kFour ? kRow4 : 2 * kD);
   const int h0 = blockIdx.y * p.heads, h1 = min(p.H, h0 + p.heads);
   const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k + k.b * p.ks.b + k.t * p.ks.t + h0 * p.ks.h);
   const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v + k.b * p.vs.b + k.t * p.vs.t + h0 * p.vs.h);
-  uint4 nka = ksrc[pa], nkb = ksrc[pb], nva = vsrc[2 * i], nvb = vsrc[2 * i + 1];
+  uint4 nka = ksrc[pa], nkb = ksrc[pb], nva = vsrc[qa], nvb = vsrc[qb];
   Turn t;
-  make_turn(p.r, i, k.pos, t);
+  make_turn<kHalf>(p.r, i, k.pos, t);
 #pragma unroll 1
   for (int h = h0; h < h1; ++h) {
     uint4 ka = nka, kb = nkb;
     const uint4 va = nva, vb = nvb;
     if (h + 1 < h1) {          // the next head's rows are on their way
       ksrc += p.ks.h / 8, vsrc += p.vs.h / 8;
-      nka = ksrc[pa], nkb = ksrc[pb], nva = vsrc[2 * i], nvb = vsrc[2 * i + 1];
+      nka = ksrc[pa], nkb = ksrc[pb], nva = vsrc[qa], nvb = vsrc[qb];
     }
     const int64_t chunk = ((int64_t)k.b * p.H + h) * p.C + c;
     int64_t slot = -1;
@@ -340,31 +407,31 @@ __global__ void __launch_bounds__(kRopeThreads) k_append(AppendP p) {
         slot = -1;
       }
     }
-    rotate(p.r, i, t, ka, kb);
+    rotate<kHalf>(p.r, i, t, ka, kb);
     if (kFour) {
-      uint32_t kca, kcb, ksa, ksb, vca, vcb, vsa, vsb;
-      quantise(ka, kb, pow2i(-head_exp(p.k_exp, h, p.status)), apart, lanes, kca, kcb, ksa, ksb);
-      quantise(va, vb, pow2i(-head_exp(p.v_exp, h, p.status)), false, lanes, vca, vcb, vsa, vsb);
+      uint32_t kca, kcb, ksa, ksb, vs;
+      quantise(ka, kb, pow2i(-head_exp(p.k_exp, h, p.status)), lanes, kca, kcb, ksa, ksb);
+      const uint2 vc = quantise_group(va, vb, pow2i(-head_exp(p.v_exp, h, p.status)), vs);
       if (p.Kh) {
-        store4(p.Kh + chunk * page_bytes, row, pa, pb, i, apart, kca, kcb, ksa, ksb);
-        store4(p.Vh + chunk * page_bytes, row, 2 * i, 2 * i + 1, i, false, vca, vcb, vsa, vsb);
+        store4(p.Kh + chunk * page_bytes, row, pa, pb, even, kca, kcb, ksa, ksb);
+        store_group(p.Vh + chunk * page_bytes, row, i, vc, vs);
       }
       if (slot >= 0) {
-        store4(p.Khot + slot * page_bytes, row, pa, pb, i, apart, kca, kcb, ksa, ksb);
-        store4(p.Vhot + slot * page_bytes, row, 2 * i, 2 * i + 1, i, false, vca, vcb, vsa, vsb);
+        store4(p.Khot + slot * page_bytes, row, pa, pb, even, kca, kcb, ksa, ksb);
+        store_group(p.Vhot + slot * page_bytes, row, i, vc, vs);
       }
     } else {
       if (p.Kh) {
         uint4 *kd = reinterpret_cast<uint4 *>(p.Kh + chunk * page_bytes + row * 2 * kD);
         uint4 *vd = reinterpret_cast<uint4 *>(p.Vh + chunk * page_bytes + row * 2 * kD);
         kd[pa] = ka, kd[pb] = kb;
-        vd[2 * i] = va, vd[2 * i + 1] = vb;
+        vd[qa] = va, vd[qb] = vb;
       }
       if (slot >= 0) {
         uint4 *kd = reinterpret_cast<uint4 *>(p.Khot + slot * page_bytes + row * 2 * kD);
         uint4 *vd = reinterpret_cast<uint4 *>(p.Vhot + slot * page_bytes + row * 2 * kD);
         kd[pa] = ka, kd[pb] = kb;
-        vd[2 * i] = va, vd[2 * i + 1] = vb;
+        vd[qa] = va, vd[qb] = vb;
       }
     }
   }
@@ -376,14 +443,16 @@ Rope rope_of(const dd_rope *r) {
     k.freq = static_cast<const uint64_t *>(r->table);
     k.lut = reinterpret_cast<const float4 *>(static_cast<const uint8_t *>(r->table) + kLutOff);
     k.rot_dim = r->rot_dim;
-    k.half = r->layout == DD_ROPE_HALF;
   }
   return k;
 }
 
 // Heads per warp: one while that does not give every SM 16 warps (of 4 tokens), so
 // that a step of a few tokens takes one row's time; else 16 at most (by then a token's
-// sines and cosines are a tenth of the work), in groups of one size.
+// sines and cosines are a tenth of the work), in groups of one size.  A step of 32 rows
+// with 32 heads: one head a warp 2.6 us, 16 heads 6.1; a prompt of 4 x 4K tokens with 64
+// heads: one 238 us, 16 heads 108 (8 and 32 within 2% of it); 4-bit append of 2 x 32K tokens
+// with 8 heads: one 180 us, 8 heads 119.
 int heads_per_warp(int64_t tokens, int H, int sm_count) {
   const int64_t warps = (tokens + 3) / 4, want = (int64_t)sm_count * 16;
   int64_t groups = (H + 15) / 16;
@@ -399,7 +468,8 @@ cudaError_t launch_rope_rows(const dd_rope *r, const void *x, const int64_t *xs,
   const int64_t tokens = (int64_t)B * T;
   const int heads = heads_per_warp(tokens, H, sm_count);
   const int64_t gx = (tokens * 8 + kRopeThreads - 1) / kRopeThreads;
-  return launch_k(k_rope_rows, dim3((unsigned)gx, (H + heads - 1) / heads), dim3(kRopeThreads), 0, s, rope_of(r),
+  return launch_k(r->layout == DD_ROPE_HALF ? k_rope_rows<true> : k_rope_rows<false>,
+                  dim3((unsigned)gx, (H + heads - 1) / heads), dim3(kRopeThreads), 0, s, rope_of(r),
                   static_cast<const uint16_t *>(x), Rows{xs[0], xs[1], xs[2]}, static_cast<uint16_t *>(out),
                   Rows{os[0], os[1], os[2]}, B, T, H, heads, start_pos, new_len, status);
 }
@@ -424,8 +494,10 @@ cudaError_t launch_append(const dd_append_args *a, void *kh_dev, void *vh_dev, i
   p.k_exp = a->k_exp, p.v_exp = a->v_exp;
   p.status = status;
   const dim3 grid((unsigned)((tokens * 8 + kRopeThreads - 1) / kRopeThreads), (Hkv + p.heads - 1) / p.heads);
-  return a->format == DD_KV_4BIT ? launch_k(k_append<true>, grid, dim3(kRopeThreads), 0, s, p)
-                                 : launch_k(k_append<false>, grid, dim3(kRopeThreads), 0, s, p);
+  const bool four = a->format == DD_KV_4BIT, half = a->rope && a->rope->layout == DD_ROPE_HALF;
+  return launch_k(four ? half ? k_append<true, true> : k_append<true, false>
+                       : half ? k_append<false, true> : k_append<false, false>,
+                  grid, dim3(kRopeThreads), 0, s, p);
 }
 
 }  // namespace dd

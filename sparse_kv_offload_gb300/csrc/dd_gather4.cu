@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(kThreads4) k_gather4(
 // Expansion to bf16: one warp per block of 16 rows of K or V; a lane turns the
 // four bytes of codes of 8 values (16 lanes a row, two rows an instruction), so
 // loads and stores are whole lines.  Bound by the host link (72 bytes a row), or,
-// from a home cache in HBM, by the 256 bytes written for each row.
+// from a home cache in HBM, by the 256 bytes written for each row: 231 MB in 37 us, 92% of the
+// copy rate (every lane loading its own scales 44 us).
 __global__ void __launch_bounds__(kThreads4) k_expand4(
     const uint8_t *__restrict__ Kh, const uint8_t *__restrict__ Vh, const int32_t *__restrict__ miss_list,
     const int32_t *__restrict__ miss_count, uint4 *__restrict__ Kst, uint4 *__restrict__ Vst, int64_t max_misses,
@@ -80,9 +81,12 @@ __global__ void __launch_bounds__(kThreads4) k_expand4(
 #pragma unroll
     for (int i = 0; i < 8; ++i) codes[i] = *reinterpret_cast<const uint32_t *>(src + i * 128 + lane * 4);
     // rows 2i and 2i + 1: group (lane & 15) / 2 of row 2i + lane / 16
+    // the block's 128 scales, four a lane, handed round
+    const uint32_t four = *reinterpret_cast<const uint32_t *>(src + kBlk4Scales + lane * 4);
     uint32_t sc[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sc[i] = src[kBlk4Scales + (2 * i + (lane >> 4)) * 8 + ((lane & 15) >> 1)];
+    for (int i = 0; i < 8; ++i)
+      sc[i] = __shfl_sync(0xffffffffu, four, 4 * i + (lane >> 4) * 2 + ((lane >> 3) & 1)) >> (((lane >> 1) & 3) * 8) & 0xFFu;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t h[4], o[4];
@@ -105,9 +109,12 @@ cudaError_t launch_gather4(const uint8_t *Kh, const uint8_t *Vh, const int32_t *
   if (max_misses == 0) return cudaSuccess;
   const int64_t total = (int64_t)units * C;
   const int bpc = cs / 16;
-  // a persistent grid, no larger than the most misses need
+  // no larger than the most misses need; the copy's blocks are all resident at once, of the
+  // expansion's five an SM are, and short blocks even out the end (231 MB: 5 an SM 41 us, 8 38,
+  // 16 37, 64 39)
+  const int64_t most = (int64_t)sm_count * (expand ? 16 : 8);
   int64_t blocks = (2 * max_misses * (expand ? bpc : 1) * 32 + kThreads4 - 1) / kThreads4;
-  if (blocks > (int64_t)sm_count * 8) blocks = (int64_t)sm_count * 8;
+  if (blocks > most) blocks = most;
   if (!expand)
     return launch_k(k_gather4, dim3((unsigned)blocks), dim3(kThreads4), 0, s, reinterpret_cast<const uint4 *>(Kh),
                     reinterpret_cast<const uint4 *>(Vh), miss_list, miss_count, static_cast<uint4 *>(Kst),

@@ -540,7 +540,7 @@ cudaError_t launch_t(int grid, const Attn4Params &p, cudaStream_t s) {
 
 // Up to 8 query vectors: one tile a warp, up to 16: two; more: tcgen05.  Both sides of the
 // second border (us, mma.sync in groups of 16 / tcgen05): 12 query vectors 41 / 66, 16: 79 /
-// 120, 20: 44.3 / 42.3, 24: 17.5 / 17.5, 40: 215 / 141, 64: 87 / 62; and with 4 the whole cache
+// 120, 20: 44.3 / 40.7, 24: 17.5 / 17.3, 40: 215 / 132, 64: 87 / 60; and with 4 the whole cache
 // of 8 requests takes 179 / 489.  (The first border is a tile's width: up to it a second tile
 // would hold padding only.)
 Attn4Plan attn4_plan(int units, int NQ, int sm_count) {

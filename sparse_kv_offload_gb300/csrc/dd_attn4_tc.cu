@@ -20,13 +20,18 @@
 // by 2^8, the softmax threads take O over into fp32 registers, where additions round to
 // nearest, and the next product overwrites it.
 //
-// Bound by the softmax threads' chain per tile (some 3,000 cycles; the products take 1,024,
-// the decoding 2,000, and both run beside it).  32B-class layer, five queries
-// (171 MB of pages, floor 25 us): the mma.sync kernel in groups of 16 215 us, 64-row tiles
-// 182, 128-row tiles 151, both parts of P in one operand and O taken over every eight tiles
-// instead of two 141.  Sixteen softmax
-// warps (80 registers) gain 1-3% with 40 or more query vectors and lose 5% with 20; eight
-// decoding warps (96 registers) lose 10%.
+// Bound by the softmax threads' chain per tile (some 3,200 cycles, most of them latency: the
+// loads of S 900, the exponentials and P's stores 900, two barriers, O's look 400), which
+// the products (1,024, issued in 720) and the decoding (2,500) run beside, and by the ends of
+// runs, a quarter of the time here.  32B-class layer, five queries (171 MB of pages, floor 25 us):
+// the mma.sync kernel in groups of 16 215 us, 64-row tiles 182, 128-row tiles 151, both
+// parts of P in one operand and O taken over every eight tiles instead of two 141, the
+// products issued by an elected thread of a whole warp, which keeps the descriptors in uniform
+// registers (lane 0 alone took 1,730 cycles for a tile's 16), 132.  Not kept: sixteen softmax
+// warps (80 registers; 1-3% gained with 40 or more query vectors, 5% lost with 20), eight
+// decoding warps (96 registers, -10%) or two blocks decoded at once (160 us: the softmax waits
+// for their shared-memory traffic), a second buffer for P (146), two groups of four softmax warps on
+// alternate tiles (184), P from the old reference with the vote at its end (136).
 #include "dd_attn4.cuh"
 
 namespace dd {
@@ -51,6 +56,13 @@ constexpr size_t kTcSmem = 1024 + (size_t)(kK + kV) * kKvBytes + 2 * kHalf + 4 *
 // kind::f16 instruction descriptor with fp16 A and B: fp32 accumulator, B's major-ness, N, M
 constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// One thread of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft * 32) : "memory"); }
@@ -149,7 +161,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
   __shared__ uint32_t s_tmem;
   __shared__ int s_over, s_last;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const Attn4Args &a = p.a;
   const uint32_t raw_full = smem_u32(bars), raw_empty = raw_full + 8 * kRaw;
   const uint32_t k_full = raw_empty + 8 * kRaw, k_empty = k_full + 8 * kK, v_full = k_empty + 8 * kK,
@@ -266,7 +278,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
       }
     } else if (warp == kSoft + kDecode + 1) {
       // ------------------------------------------------------------ products
-      if (lane == 0) {
+      // (the whole warp waits and counts, so that what the products are told is uniform)
+      {
         // (descriptors hold addresses in 16-byte units: a step adds a constant)
         constexpr uint32_t id_s = idesc_f16(kTcM, 128, 0), id_o = idesc_f16(128, 128, 1);
         const uint64_t q_desc = smem_desc_sw128(q0s, 16, 1024), k_desc = smem_desc_sw128(kv0, 16, 1024);
@@ -276,16 +289,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           wait(v_full + 8 * (u % kV), u / kV);
           wait(p_ready, u);
           tc_fence_after();
-          if (!alive) return;
+          if (!__all_sync(0xffffffffu, alive)) return;
           const uint64_t vb = v_desc + (uint32_t)((u % kV) * (kKvBytes / 16));
-          const bool over = s_over != 0;
+          const bool over = __shfl_sync(0xffffffffu, s_over, 0) != 0;
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            tc_mma(tmem_o, p_desc + ((ks >> 2) * kTileHalf + (ks & 3) * 32) / 16, vb + ks * 16 * 128 / 16, id_o,
-                   !(over && ks == 0));
+            for (int ks = 0; ks < 8; ++ks)
+              tc_mma(tmem_o, p_desc + ((ks >> 2) * kTileHalf + (ks & 3) * 32) / 16, vb + ks * 16 * 128 / 16, id_o,
+                     !(over && ks == 0));
+            tc_commit(v_empty + 8 * (u % kV));
+            tc_commit(pv_done);
           }
-          tc_commit(v_empty + 8 * (u % kV));
-          tc_commit(pv_done);
         };
         int x = wlo;
         for (int r = 0; r < n_runs; ++r, ++run_no) {
@@ -294,7 +308,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           for (; x < end; ++x, ++t) {
             wait(k_full + 8 * (t % kK), t / kK);
             tc_fence_after();
-            if (alive) {
+            if (__all_sync(0xffffffffu, alive) && elect_one()) {
               // the softmax threads are done with S(t - 2): P(t - 2) was ready
               const uint64_t kb = k_desc + (uint32_t)((t % kK) * (kKvBytes / 16));
 #pragma unroll
@@ -520,7 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
     if (whi >= slice.hi) break;
   }
   // every product issued is done before the tensor memory is freed
-  if (warp == kSoft + kDecode + 1 && lane == 0) {
+  if (warp == kSoft + kDecode + 1 && elect_one()) {
     tc_commit(mma_done);
     mbar_wait(mma_done, 0, a.status);
   }

@@ -213,6 +213,42 @@ def test_append(dd, four, B, T, H, cs, C, rot, half, host):
             assert not only[w][cache.n:].view(torch.uint8).any()
 
 
+# (H, rot, half): with 10,000 tokens a warp goes through several heads, with 200 through one
+MANY = [(40, 128, True), (17, 64, False), (9, 96, True), (6, 32, False), (5, 96, False), (16, 64, True)]
+
+
+@pytest.mark.parametrize("H,rot,half", MANY)
+def test_many_tokens(dd, H, rot, half):
+    """Prompts long enough for warps with many heads: the oracle's rotation on some rows, and on all of them, in place
+    and in both formats of the cache, what calls of 200 tokens give."""
+    import torch
+    T, step, cs = 10000, 200, 16
+    g = torch.Generator(device="cuda").manual_seed(H)
+    k, v = (torch.randn(1, T, H, D, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    rope, freq, gain = make_rope(dd, rot, half, "by_parts")
+    with dd.Context(dd.Shape(1, H, H, D, T, cs, 1, 1), max_misses=0, hot_slots=0) as ctx:
+        whole, parts, same = torch.zeros_like(k), torch.zeros_like(k), k.clone()
+        ctx.rope(rope, k, whole, tl.to_i32([77]))
+        ctx.rope(rope, same, same, tl.to_i32([77]))
+        for t in range(0, T, step):
+            ctx.rope(rope, k[:, t:t + step], parts[:, t:t + step], tl.to_i32([77 + t]))
+        assert ctx.status() == 0 and torch.equal(whole, parts) and torch.equal(whole, same)
+        rows = torch.arange(0, T, 397, device="cuda")
+        check_rotated(tl.from_bf16(whole[:, rows].contiguous()), tl.from_bf16(k[:, rows].contiguous()),
+                      77 + rows.cpu().numpy()[None], freq, half, gain)
+        for four in (False, True):
+            shape = (H * T // cs, cs * 72) if four else (1, H, T, D)
+            home = [torch.zeros(shape, dtype=torch.uint8 if four else torch.bfloat16, device="cuda") for _ in range(4)]
+            kw = dict(rope=rope, kv_format=dd.KV_4BIT if four else dd.KV_BF16)
+            n = T - 5                                              # an odd end
+            ctx.append_kv(k[:, :n], v[:, :n], tl.to_i32([3]), Kh=home[0], Vh=home[1], **kw)
+            for t in range(0, n, step):
+                e = min(n, t + step)
+                ctx.append_kv(k[:, t:e], v[:, t:e], tl.to_i32([3 + t]), Kh=home[2], Vh=home[3], **kw)
+            assert ctx.status() == 0
+            assert torch.equal(home[0], home[2]) and torch.equal(home[1], home[3]) and home[0].any() and home[1].any()
+
+
 def test_quantiser_edges(dd):
     """Rows where the 4-bit rounding can go wrong: every tie of both formats, the smallest and the largest
     scales, zeros, subnormals, infinities and NaN."""

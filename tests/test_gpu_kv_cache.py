@@ -327,6 +327,11 @@ def test_gather4(dd, cs, C, B, H, n, host):
             assert np.array_equal(oracle.bf16_decode(tl.from_bf16(wide[w]))[:n], want) and (wide[w][n:] == 5).all()
 
 
+def test_gather4_of_many_chunks(dd):
+    """More blocks than the grid has warps, and pages in any order."""
+    test_gather4(dd, 64, 1000, 1, 3, 2900, False)
+
+
 def test_device_checks(dd):
     """Positions, lengths, slots, chunks and exponents out of range: reported, their rows left out, the rest written."""
     import torch

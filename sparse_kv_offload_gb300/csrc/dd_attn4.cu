@@ -150,19 +150,20 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
       }
       stage_tails(p, r, s_tails, tid, kThreads);
     };
-    stage_run(runs[0]);
     // lane 2 t + h holds block h of tile i0 + t
-    auto entry = [&](int i) -> BlockRef {
-      if (i >= n_tiles || dead) return {0, 0u};
+    auto entry = [&](int i) -> Entry {
+      if (i >= n_tiles || dead) return {0, 0, -1, 0, 0u};
       const int x = wlo + warp + i * kWarps;
       int r = 0;
 #pragma unroll
       for (int step = kMaxRuns / 2; step > 0; step >>= 1)
         if (r + step < n_runs && runs[r + step].start <= x) r += step;
-      return look_up(p, runs[r], 2 * (x - runs[r].start) + (lane & 1), slice.staged, all_q);
+      return load_entry(p, runs[r], 2 * (x - runs[r].start) + (lane & 1), all_q);
     };
     int i0 = 0;
-    BlockRef cur = entry(lane >> 1), nxt = {0, 0u};
+    const Entry first = entry(lane >> 1);
+    stage_run(runs[0]);      // on the way together with the union's entries
+    BlockRef cur = look_at(p, first, slice.staged, all_q), nxt = {0, 0u};
 
     // the two lanes that hold tile i ask for its blocks (an empty block just arrives)
     auto issue = [&](int i) {
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
     };
 #pragma unroll 1
     for (int i = 0; i < S; ++i) issue(i);
-    nxt = entry(16 + (lane >> 1));
+    nxt = look_at(p, entry(16 + (lane >> 1)), slice.staged, all_q);
 
     int i = 0;
 #pragma unroll 1
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
         if ((i & 15) == 15) {
           i0 += 16;
           cur = nxt;
-          nxt = entry(i0 + 16 + (lane >> 1));
+          nxt = look_at(p, entry(i0 + 16 + (lane >> 1)), slice.staged, all_q);
         }
       }
 

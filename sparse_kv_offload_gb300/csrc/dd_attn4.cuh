@@ -186,16 +186,32 @@ struct BlockRef {
   int slot;
   uint32_t meta;
 };
-__device__ __forceinline__ BlockRef look_up(const Attn4Params &p, const Run &r, int blk, int64_t staged, uint32_t all_q) {
+// (The union's entry is loaded first and looked at later, so that other work fits in between.)
+struct Entry {
+  int slot, idx, sub, len;       // sub: block of the chunk, -1: no such block
+  uint32_t qm;
+};
+__device__ __forceinline__ Entry load_entry(const Attn4Params &p, const Run &r, int blk, uint32_t all_q) {
   const Attn4Args &a = p.a;
-  const int ci = blk >> p.bpc_shift, sub = blk & ((1 << p.bpc_shift) - 1);
-  if (ci >= r.cnt) return {0, 0u};
-  const int64_t e = (int64_t)r.unit * a.umax + ci;
-  const int slot = a.union_slot[e];
-  const uint32_t qm = a.union_qmask ? a.union_qmask[e] & all_q : all_q;
+  const int ci = blk >> p.bpc_shift;
+  Entry n = {0, 0, -1, r.len, all_q};
+  if (ci < r.cnt) {
+    const int64_t e = (int64_t)r.unit * a.umax + ci;
+    n.sub = blk & ((1 << p.bpc_shift) - 1);
+    n.slot = a.union_slot[e];
+    if (a.union_qmask) n.qm = a.union_qmask[e];
+    if (a.kv_len) n.idx = a.union_idx[e];
+  }
+  return n;
+}
+__device__ __forceinline__ BlockRef look_at(const Attn4Params &p, const Entry &n, int64_t staged, uint32_t all_q) {
+  const Attn4Args &a = p.a;
+  if (n.sub < 0) return {0, 0u};
+  const int slot = n.slot, sub = n.sub;
+  const uint32_t qm = n.qm & all_q;
   int rows = 16;
   if (a.kv_len) {
-    const int64_t left = r.len - ((int64_t)a.union_idx[e] * a.cs + sub * 16);
+    const int64_t left = n.len - ((int64_t)n.idx * a.cs + sub * 16);
     rows = left < 0 ? 0 : left > 16 ? 16 : (int)left;
   }
   if (slot >= 0 ? slot >= a.hot_slots : -1 - (int64_t)slot >= staged) {
@@ -285,15 +301,19 @@ struct Slice {
     const Attn4Args &a = p.a;
     const int tid = threadIdx.x;
     one_round = p.units <= kThreads;
-    if (tid == 0) sm.flag = load_status(a.status);
-    staged = a.miss_count ? min((int64_t)*a.miss_count, a.max_misses) : a.max_misses;
+    // all loads before the first use of one
+    const int pending = tid == 0 ? load_status(a.status) : 0;
+    const int missing = a.miss_count ? *a.miss_count : INT_MAX;
     if (one_round) {
       if (tid < p.units) my_tiles = unit_tiles(p, tid, kTileShift, mine);
+      if (tid == 0) sm.flag = pending;
       my_start = block_excl_scan(my_tiles, sm.scratch, &total);
     } else {
       for (int u = tid; u < p.units; u += kThreads) my_tiles += unit_tiles(p, u, kTileShift, mine);
+      if (tid == 0) sm.flag = pending;
       total = block_sum(my_tiles, sm.scratch);
     }
+    staged = min((int64_t)missing, a.max_misses);
     dead = sm.flag != 0;       // an error is pending: no work (the arrival counts go on)
     const int n_cta = (int)gridDim.x;
     per = ((total + n_cta - 1) / n_cta + kQuantum - 1) / kQuantum * kQuantum;

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
 #pragma unroll
           for (int step = kMaxRuns / 2; step > 0; step >>= 1)
             if (r + step < n_runs && runs[r + step].start <= x) r += step;
-          ref = look_up(p, runs[r], kBlocks * (x - runs[r].start) + (lane & 7), slice.staged, all_q);
+          ref = look_at(p, load_entry(p, runs[r], kBlocks * (x - runs[r].start) + (lane & 7), all_q), slice.staged, all_q);
         }
         for (int k = 0; k < 4 && i0 + k < n_tiles; ++k, ++t) {
           const int st = t % kRaw;

@@ -137,7 +137,6 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
 
     // --------------------------------------- this warp's tiles: wlo + warp + i * kWarps
     const int n_tiles = whi - wlo > warp ? (whi - wlo - warp + kWarps - 1) / kWarps : 0;
-    // the first run's query vectors are on their way while the tiles are looked up
     // a run's query vectors and its own new rows come by asynchronous copies, the first
     // run's while its tiles are looked up
     auto stage_run = [&](const Run &r) {

@@ -14,8 +14,8 @@
 //     interleaved before they are converted.
 // Query vectors are the narrow side (8 a tile), so the 4 or 8 of a KV head's
 // group are not padded to 16.
-// Whole cache, 8 requests of 128K (842 MB): 179 us, where the copies alone take 131 and
-// everything but the copies 160-176.  A tile of 32 rows takes 748 instructions: 128 conversions
+// Whole cache, 8 requests of 128K (842 MB): 177 us, where the copies alone take 131 and
+// everything but the copies 160-176.  A tile of 32 rows takes some 750 instructions: 128 conversions
 // and 128 multiplications, 41 to interleave V's rows, 64 additions of sums, the rest loads,
 // softmax and moves.
 //
@@ -46,9 +46,10 @@ constexpr int kJoinRow = 132;            // floats of a query vector's sums in t
 
 // NT tiles of 8 query vectors a warp, two CTAs on an SM.  Up to 4 query vectors (kPack)
 // the two parts of P share a tile, one in its columns 0-3, one in 4-7, which halves the
-// products with V (whole cache, 8 requests of 128K: 195 -> 179 us).  One tile: eight warps a CTA
-// with the queries in registers (128 registers a thread); two: six warps (168), the
-// queries in shared memory.
+// products with V (whole cache, 8 requests of 128K: 195 -> 179 us), and their queries, a
+// kilobyte, wait in shared memory, without which registers spill (179 -> 177; 64 requests of
+// 128 chunks 47 -> 45).  One tile: eight warps a CTA (128 registers a thread), two: six (168),
+// the queries in shared memory too.
 __host__ __device__ constexpr int attn4_warps(int nt) { return nt == 1 ? 8 : 6; }
 constexpr int kStages = 2;               // tiles in flight per warp
 __host__ __device__ constexpr size_t attn4_smem(int nt) {
@@ -100,7 +101,8 @@ __device__ __forceinline__ uint32_t movm(uint32_t a) {
 template <int NT, bool kPack>
 __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_constant__ Attn4Params p) {
   constexpr int S = kStages, kWarps = attn4_warps(NT), kThreads = kWarps * 32;
-  constexpr bool kQReg = NT == 1;
+  constexpr bool kQReg = NT == 1 && !kPack;
+  constexpr int kVecs = kPack ? 4 : NT * 8;        // query vectors
   extern __shared__ __align__(128) uint8_t smem[];
   float *join = reinterpret_cast<float *>(smem + kWarps * S * kTileBytes);     // [kWarps][8][kJoinRow]
   uint8_t *qsm = smem + kWarps * S * kTileBytes + kWarps * 8 * kJoinRow * 4;   // [NT][8 steps][32 lanes][8 B]
@@ -110,7 +112,8 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
   __shared__ uint4 s_tails[2 * kMaxNq * 16];      // the unit's own new rows: keys, values
   __shared__ float s_back[NT * 8];
   __shared__ int s_flag;
-  __shared__ uint4 s_query[NT * 8 * 16];            // the run's query vectors as they are
+  __shared__ uint4 s_query[kVecs * 16];
+  __shared__ uint2 s_pack[kPack ? 8 * 16 : 1];      // their fragments, [8 steps][query vector, quarter]            // the run's query vectors as they are
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t4 = lane & 3, g8 = lane >> 2;
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
     // a run's query vectors and its own new rows come by asynchronous copies, the first
     // run's while its tiles are looked up
     auto stage_run = [&](const Run &r) {
-      for (int e = tid; e < NT * 8 * 16; e += kThreads) {
+      for (int e = tid; e < kVecs * 16; e += kThreads) {
         const int qv = e >> 4;
         if (qv < p.NQ)
           cp_async16(s_query + e, reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + out_row(p, r.unit, qv)) + (e & 15));
@@ -199,23 +202,27 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
         mul[0][0] = __shfl_sync(0xffffffffu, back, t4 * 8) * kmul;
         mul[0][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4) * kmul;
       } else {
-        if (warp < NT) {
+        if (warp < NT && (!kPack || lane < 16)) {
           uint4 w[4];
           uint32_t f[16];
           float back;
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[e] = s_query[(warp * 8 + g8) * 16 + t4 * 4 + e];
-          query_fragments(w, f, back);
+          query_fragments(w, f, back, kPack ? 0xFFFFu : 0xFFFFFFFFu);
 #pragma unroll
           for (int s = 0; s < 8; ++s)
-            *reinterpret_cast<uint2 *>(qsm + ((warp * 8 + s) * 32 + lane) * 8) = make_uint2(f[2 * s], f[2 * s + 1]);
+            if constexpr (kPack)
+              s_pack[s * 16 + lane] = make_uint2(f[2 * s], f[2 * s + 1]);
+            else
+              *reinterpret_cast<uint2 *>(qsm + ((warp * 8 + s) * 32 + lane) * 8) = make_uint2(f[2 * s], f[2 * s + 1]);
           if (t4 == 0) s_back[warp * 8 + g8] = back;
         }
         __syncthreads();
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          mul[n][0] = s_back[n * 8 + 2 * t4] * kmul;
-          mul[n][1] = s_back[n * 8 + 2 * t4 + 1] * kmul;
+          const int qv = n * 8 + (kPack ? 2 * t4 & 3 : 2 * t4);
+          mul[n][0] = s_back[qv] * kmul;
+          mul[n][1] = s_back[qv + 1] * kmul;
         }
       }
 #pragma unroll
@@ -277,6 +284,8 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
                   uint2 q2;
                   if constexpr (kQReg)
                     q2 = make_uint2(qf[2 * (2 * w + e)], qf[2 * (2 * w + e) + 1]);
+                  else if constexpr (kPack)
+                    q2 = s_pack[(2 * w + e) * 16 + (lane & 15)];
                   else
                     q2 = *reinterpret_cast<const uint2 *>(qsm + ((n * 8 + 2 * w + e) * 32 + lane) * 8);
                   if (w == 0 && e == 0)
@@ -392,6 +401,15 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
             }
             const uint32_t s01[2] = {e4m3x2_to_half2(sc[0]), e4m3x2_to_half2(sc[1])};
             const uint32_t s23[2] = {e4m3x2_to_half2(sc[0] >> 16), e4m3x2_to_half2(sc[1] >> 16)};
+            uint2 va[2][2], vb[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t at = tile + (2 * h + 1) * kBlk4 + g8 * 8 + e * 512;
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(va[h][e].x), "=r"(va[h][e].y) : "r"(at + ra * 64));
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vb[h][e].x), "=r"(vb[h][e].y) : "r"(at + rb * 64));
+              }
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               // even columns of two rows side by side, then the odd ones
@@ -400,8 +418,7 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
               for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const uint32_t vb = tile + (2 * h + 1) * kBlk4 + g8 * 8 + 4 * w + e * 512;
-                  const uint32_t xa = lds32(vb + ra * 64), xb = lds32(vb + rb * 64);
+                  const uint32_t xa = w ? va[h][e].y : va[h][e].x, xb = w ? vb[h][e].y : vb[h][e].x;
                   x[h][2 * e] = (xa & 0x0F0F0F0Fu) | ((xb << 4) & 0xF0F0F0F0u);
                   x[h][2 * e + 1] = ((xa >> 4) & 0x0F0F0F0Fu) | (xb & 0xF0F0F0F0u);
                 }
@@ -541,7 +558,7 @@ cudaError_t launch_t(int grid, const Attn4Params &p, cudaStream_t s) {
 // Up to 8 query vectors: one tile a warp, up to 16: two; more: tcgen05.  Both sides of the
 // second border (us, mma.sync in groups of 16 / tcgen05): 12 query vectors 41 / 66, 16: 79 /
 // 120, 20: 44.3 / 40.7, 24: 17.5 / 17.3, 40: 215 / 132, 64: 87 / 60; and with 4 the whole cache
-// of 8 requests takes 179 / 489.  (The first border is a tile's width: up to it a second tile
+// of 8 requests takes 177 / 489.  (The first border is a tile's width: up to it a second tile
 // would hold padding only.)
 Attn4Plan attn4_plan(int units, int NQ, int sm_count) {
   Attn4Plan pl;

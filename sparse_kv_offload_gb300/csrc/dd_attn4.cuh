@@ -150,15 +150,15 @@ __device__ __forceinline__ void finish(const Attn4Params &p, int unit, int qv, P
 
 // 32 query values of a lane as fp16 pairs, scaled by a power of two so that the largest of
 // the 128 values of the query vector (four neighbouring lanes) lies just below 2^15, and
-// the factor back.
-__device__ __forceinline__ void query_fragments(const uint4 (&w)[4], uint32_t (&f)[16], float &back) {
+// the factor back (lanes: those that take part).
+__device__ __forceinline__ void query_fragments(const uint4 (&w)[4], uint32_t (&f)[16], float &back, unsigned lanes = 0xFFFFFFFFu) {
   const uint32_t v[16] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w,
                           w[2].x, w[2].y, w[2].z, w[2].w, w[3].x, w[3].y, w[3].z, w[3].w};
   uint32_t top = 0;   // largest magnitude, as bits
 #pragma unroll
   for (int i = 0; i < 16; ++i) top = max(top, max((v[i] & 0x7FFFu) << 16, v[i] & 0x7FFF0000u));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  top = max(top, __shfl_xor_sync(lanes, top, 1));
+  top = max(top, __shfl_xor_sync(lanes, top, 2));
   const int e = (int)(top >> 23);
   const int sh = top == 0 || e == 255 ? 0 : min(126, 14 - (e - 127));
   const float mul = pow2i(sh);

@@ -26,7 +26,7 @@
 // in fp32 outside of it, where additions round to nearest: its own truncates, and
 // over the hundreds of additions of a long context that shows (1e-5).
 // The softmax's reference value is moved only when a score exceeds it by 2^8, so
-// most tiles need no maximum across lanes (P stays below 2^14).
+// most tiles need no maximum across lanes (P stays at 2^14 or below).
 //
 // Work split: the unions' tiles of 32 rows (two blocks) of all (request, KV head)
 // units, laid end to end, are cut into equal slices, one for each persistent CTA,
@@ -318,7 +318,9 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
             }
             float t0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
             float t1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-            if (__any_sync(0xffffffffu, t0 > m[n][0] + (kLazy + kHead) || t1 > m[n][1] + (kLazy + kHead))) {
+            // (the difference of two neighbours is exact; their sum with a bound is not from 2^25 on, where floats
+            // are 4 apart; -inf - -inf is no reason to move)
+            if (__any_sync(0xffffffffu, t0 - m[n][0] > kLazy + kHead || t1 - m[n][1] > kLazy + kHead)) {
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) {
                 t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));

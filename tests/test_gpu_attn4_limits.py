@@ -1,0 +1,70 @@
+"""Attention over 4-bit pages where its inputs are at their limits."""
+import numpy as np
+import pytest
+
+import oracle
+from sparse_kv_offload_gb300 import synth
+
+import dd_testlib as tl
+from test_gpu_attn4 import make_case, run, want_of
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+
+
+@pytest.fixture(scope="module")
+def dd():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from sparse_kv_offload_gb300 import build
+    build.build()
+    from sparse_kv_offload_gb300 import dd as mod
+    return mod
+
+
+def unit_scale():
+    """A softmax scale whose fp32 product with log2(e) is 1: scores are whole numbers of log2 units."""
+    s = np.float32(np.log(2.0))
+    for c in (np.nextafter(s, np.float32(0)), s, np.nextafter(s, np.float32(1))):
+        if c * np.float32(1.4426950408889634) == np.float32(1.0):
+            return float(c)
+    raise AssertionError
+
+
+@pytest.mark.parametrize("G", [3, 4, 8, 11, 16, 24, 64])
+def test_scores_whose_floats_are_far_apart(dd, G):
+    """From 2^25 on the next float is 4, 8, 16, ... away: a later row's score above the softmax's reference by every
+    such step, for query vectors of both signs, the same for all of a unit."""
+    import torch
+    B, cs, C = 320, 64, 16                             # several tiles of a unit follow one another on every warp
+    pairs = [(sign * m * 2.0 ** e, up * 2.0 ** (e - 23)) for e in range(24, 30) for m in (1.25, 1.5) for sign in (1, -1)
+             for up in (1, 2, 3, 4, 5, 6)]
+    pairs += [(2.0 ** e, up * 2.0 ** (e - 23)) for e in range(25, 29) for up in (1, 2, 3, 4)]
+    pairs = [(a, d) for a, d in pairs if d <= 40.0]
+    rng = np.random.default_rng(G)
+    # slot 0: rows with score q0, slot 1: rows with score q0 + q1; both with any values
+    K = np.zeros((2, cs, D), np.uint8)
+    K[:, :, 0] = 2                                     # code of 1.0, the scales are 1.0
+    K[1, :, 1] = 2
+    K = oracle.kv4_pack(K, np.full((2, cs, 8), 0x38, np.uint8))
+    V = oracle.kv4_pack(rng.integers(0, 16, (2, cs, D)).astype(np.uint8), np.full((2, cs, 8), 0x38, np.uint8))
+    q = np.zeros((B, 1, G, D), np.float32)
+    which = np.repeat(np.arange(B)[:, None] % len(pairs), G, 1)
+    assert len(pairs) <= B
+    q[:, 0, :, :2] = np.array(pairs)[which]
+    scale = unit_scale()
+    slot = np.repeat([0, 1], C // 2)[None].repeat(B, 0)
+    out = torch.full((B, 1, G, D), float("nan"), device="cuda")
+    with dd.Context(dd.Shape(B, G, 1, D, C * cs, cs, C, 1), max_misses=0, hot_slots=2) as ctx:
+        ctx.sparse_attn_decode_kv4(tl.to_bf16(synth.f32_to_bf16(q)), torch.from_numpy(K).cuda(), torch.from_numpy(V).cuda(),
+                                   None, None, tl.to_i32(slot), tl.to_i32(np.full(B, C)), out, softmax_scale=scale)
+        assert ctx.status() == 0
+    v = oracle.kv4_values(V, np.zeros(2)).mean(1)      # every row of a slot has the same weight
+    up = np.array([d for _, d in pairs])
+    w = np.exp(-up * scale)[:, None]
+    want = ((w * v[0] + v[1]) / (1.0 + w))[which]
+    # the scores are exact, so what is left is 2^-18 of the largest value for weights, sums and joins; the scale's own
+    # last bit moves a weight below 2^-1 by 40 * 2^-24 of itself at most
+    assert (np.abs(out.cpu().numpy()[:, 0] - want) <= 2.0 ** -18 * 6.0).all()

@@ -501,6 +501,9 @@ dd_status dd_gather_kv4(dd_ctx *ctx, const void *Kh, const void *Vh, const int32
  *                the end).  The position of row t of union chunk i is
  *                union_idx[b,g,i]*cs + t; union_idx int32 [B,Hkv,Umax] as written by
  *                dd_resolve_union (ascending, no chunk twice), needed with kv_len.
+ * A union_slot is looked at where some query sees a row of its chunk, and has to be in
+ * range there (DD_ERR_DEVICE_CHECK, the chunk left out); behind kv_len and where the
+ * query mask is 0 it may hold anything.
  * Attention over a whole cache: k = C, union_cnt = the chunks in use, union_idx =
  * 0, 1, ..., union_slot = their pages.  A query without a row gets zeros.
  * B*Hkv*(Umax*cs/16 + 1) has to stay below 2^30 (DD_ERR_INVALID_ARG). */

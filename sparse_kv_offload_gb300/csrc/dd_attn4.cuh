@@ -214,11 +214,13 @@ __device__ __forceinline__ BlockRef look_at(const Attn4Params &p, const Entry &n
     const int64_t left = n.len - ((int64_t)n.idx * a.cs + sub * 16);
     rows = left < 0 ? 0 : left > 16 ? 16 : (int)left;
   }
-  if (slot >= 0 ? slot >= a.hot_slots : -1 - (int64_t)slot >= staged) {
+  uint32_t meta = qm && rows ? qm | (uint32_t)rows << 8 | (uint32_t)sub << 13 : 0u;
+  // (whatever the tiles' size: only a slot that is going to be read has to be one)
+  if (meta && (slot >= 0 ? slot >= a.hot_slots : -1 - (int64_t)slot >= staged)) {
     set_status(a.status, DD_ERR_DEVICE_CHECK);
-    rows = 0;
+    meta = 0u;
   }
-  return {slot, qm && rows ? qm | (uint32_t)rows << 8 | (uint32_t)sub << 13 : 0u};
+  return {slot, meta};
 }
 
 // K and V of a block into shared memory (K first), completing on bar.

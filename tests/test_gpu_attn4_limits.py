@@ -68,3 +68,32 @@ def test_scores_whose_floats_are_far_apart(dd, G):
     # the scores are exact, so what is left is 2^-18 of the largest value for weights, sums and joins; the scale's own
     # last bit moves a weight below 2^-1 by 40 * 2^-24 of itself at most
     assert (np.abs(out.cpu().numpy()[:, 0] - want) <= 2.0 ** -18 * 6.0).all()
+
+
+@pytest.mark.parametrize("G", [1, 2, 4, 6, 8, 16, 32], ids=lambda g: f"nq{2 * g}")
+@pytest.mark.parametrize("cs", [16, 64])
+def test_pages_that_no_query_sees_need_no_slot(dd, G, cs):
+    """Entries behind kv_len, and entries that no query selected, may hold any slot, wherever they lie in a tile."""
+    rng = np.random.default_rng(G * cs)
+    for seed in range(4):
+        x = make_case(300 + seed, 3, 2, G, 2, cs, 40, 14, empty=0.1)
+        L = 40 * cs
+        x["length"] = np.array([[0, 5, L // 3], [1, L // 2 + 7, L], [cs, 3 * cs + 1, L - 1], [17, 200, 333]][seed])
+        seen = x["idx"] * cs < x["length"][:, None, None]
+        unseen = ~seen | (rng.random(seen.shape) < 0.2)
+        x["qmask"] = np.where(seen & unseen, 0, x["qmask"]).astype(np.uint8)
+        inside = np.arange(x["U"]) < x["cnt"][..., None]
+        bad = rng.choice([x["n_hot"], -1 - x["n_st"], 2 ** 31 - 1, -2 ** 31], seen.shape)
+        assert (inside & unseen).any()
+        for tails in (False, True):
+            want, tol = want_of(x, tails)
+            y = {**x, "slot": np.where(unseen, bad, x["slot"]).astype(np.int32)}
+            got, st = run(dd, y, tails)
+            assert st == 0
+            assert (np.abs(got - want) <= tol).all()
+        # and one that a query does see is reported
+        y["slot"] = x["slot"].copy()
+        at = np.argwhere(inside & ~unseen & (x["qmask"] != 0))
+        if len(at):
+            y["slot"][tuple(at[-1])] = x["n_hot"]
+            assert run(dd, y)[1] == dd.DD_ERR_DEVICE_CHECK

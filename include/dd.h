@@ -519,7 +519,9 @@ dd_status dd_sparse_attn_decode_kv4(dd_ctx *ctx, const void *q, const void *Khot
  * mbarrier no thread arrives on and no copy completes (the waits of the
  * attention pipeline and of the selection's landmark ring); kind 1: a
  * look-back word no unit publishes (the selection's sum over earlier
- * units).  The wait gives up by itself after about 2 s and records
+ * units); kind 2: a ring of many tiles of which no copy arrives (the 4-bit
+ * attention), where the wait for the first tile and the one for the copies
+ * behind it run out and no other is begun.  A wait gives up by itself after about 2 s and records
  * DD_ERR_TIMEOUT in the status word; the context stays usable once
  * dd_get_status has read and cleared it.  No fault or trap is involved. */
 dd_status dd_selftest_bounded_wait(dd_ctx *ctx, int32_t kind, dd_stream_t stream);

@@ -516,7 +516,7 @@ dd_status dd_update_residency(dd_ctx *c, int32_t step, int32_t cap, int32_t slot
 }
 
 dd_status dd_selftest_bounded_wait(dd_ctx *c, int32_t kind, dd_stream_t stream) {
-  if (!c || (kind != 0 && kind != 1)) return DD_ERR_INVALID_ARG;
+  if (!c || kind < 0 || kind > 2) return DD_ERR_INVALID_ARG;
   c->launches += 1;
   return cuda_ok(dd::launch_selftest_wait(kind, c->diag_word, c->status, (cudaStream_t)stream));
 }

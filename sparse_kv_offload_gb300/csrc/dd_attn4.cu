@@ -167,12 +167,13 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
     stage_run(runs[0]);      // on the way together with the union's entries
     BlockRef cur = look_at(p, first, slice.staged, all_q), nxt = {0, 0u};
 
-    // the two lanes that hold tile i ask for its blocks (an empty block just arrives)
+    // the two lanes that hold tile i ask for its blocks (an empty block just arrives); nobody
+    // does once a wait has run out, as nobody waits then
     auto issue = [&](int i) {
-      if (i < n_tiles && (lane >> 1) == (i & 15)) {
+      if (i < n_tiles && (lane >> 1) == (i & 15) && alive) {
         const BlockRef r = i >= i0 + 16 ? nxt : cur;
         const uint32_t st = (seq + (uint32_t)i) % S, bar = bar0 + 8 * st;
-        if (r.meta && alive)
+        if (r.meta)
           load_block(p, r, ring + st * kTileBytes + (lane & 1) * 2 * kBlk4, bar);
         else
           mbar_arrive(bar);
@@ -248,8 +249,7 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
         const uint32_t meta0 = __shfl_sync(0xffffffffu, cur.meta, 2 * (i & 15));
         const uint32_t meta1 = __shfl_sync(0xffffffffu, cur.meta, 2 * (i & 15) + 1);
         const uint32_t st = (seq + (uint32_t)i) % S;
-        if (!mbar_wait(bar0 + 8 * st, ((seq + (uint32_t)i) / S) & 1, a.status)) alive = false;
-        alive = __all_sync(0xffffffffu, alive);
+        alive = ring_wait<S>(alive, bar0, seq + (uint32_t)i, seq + (uint32_t)min(i + S, n_tiles) - 1u, lane, a.status);
         if ((meta0 | meta1) && alive) {
           const uint32_t tile = ring + st * kTileBytes;
           const uint32_t full_meta = all_q | 16u << 8;

@@ -233,6 +233,28 @@ __device__ __forceinline__ void load_block(const Attn4Params &p, const BlockRef 
   bulk_load(dst + kBlk4, (r.slot >= 0 ? a.Vhot : a.Vst) + off, kBlk4, bar);
 }
 
+// The copies of tiles [from, to) of a ring (at most 32, all asked for) have landed, or have had the
+// time of one wait to: a CTA does not leave with copies on their way to its shared memory.
+// All lanes of a warp.
+__device__ __forceinline__ void ring_drain(uint32_t bar0, uint32_t stages, uint32_t from, uint32_t to, int lane,
+                                           int32_t *status) {
+  const uint32_t t = from + (uint32_t)lane;
+  if (t < to) mbar_wait(bar0 + 8 * (t % stages), (t / stages) & 1u, status);
+  __syncwarp();
+}
+
+// A warp's wait for tile t of its ring, the last one asked for being `last` (all lanes).  The
+// first wait that runs out is the only one: what is behind it is drained, and from then on
+// (alive = what the call before gave) the answer is false at once.
+template <uint32_t S>
+__device__ __forceinline__ bool ring_wait(bool alive, uint32_t bar0, uint32_t t, uint32_t last, int lane,
+                                          int32_t *status) {
+  if (!alive) return false;
+  alive = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * (t % S), (t / S) & 1u, status));
+  if (!alive) ring_drain(bar0, S, t + 1, last + 1, lane, status);
+  return alive;
+}
+
 // Query vector k of the run's group from the parts of all its CTAs.
 __device__ __forceinline__ Part combine_parts(const Attn4Params &p, const Run &r, int k, int lane) {
   const int group_q = p.group_q;

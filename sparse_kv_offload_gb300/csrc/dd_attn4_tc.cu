@@ -534,6 +534,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
     }
     if (whi >= slice.hi) break;
   }
+  // (the decoding warps have waited for every copy, unless a wait has run out)
+  if (warp == kSoft + kDecode) ring_drain(raw_full, kRaw, (uint32_t)max(t - kRaw, 0), (uint32_t)t, lane, a.status);
   // every product issued is done before the tensor memory is freed
   if (warp == kSoft + kDecode + 1 && elect_one()) {
     tc_commit(mma_done);

@@ -504,6 +504,9 @@ dd_status dd_gather_kv4(dd_ctx *ctx, const void *Kh, const void *Vh, const int32
  * A union_slot is looked at where some query sees a row of its chunk, and has to be in
  * range there (DD_ERR_DEVICE_CHECK, the chunk left out); behind kv_len and where the
  * query mask is 0 it may hold anything.
+ * A call that reports DD_ERR_DEVICE_CHECK leaves of each (request, KV head)'s outputs
+ * either the result without what was out of range, or what was there before; one that
+ * is made while an error is pending leaves them all; DD_ERR_TIMEOUT says nothing of them.
  * Attention over a whole cache: k = C, union_cnt = the chunks in use, union_idx =
  * 0, 1, ..., union_slot = their pages.  A query without a row gets zeros.
  * B*Hkv*(Umax*cs/16 + 1) has to stay below 2^30 (DD_ERR_INVALID_ARG). */

@@ -526,14 +526,9 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
       }
       if (shared) {
         // the barrier above orders the CTA's parts before the count, the one below the count before the reads
-        if (tid == 0) {
-          const bool last = atom_add_acq_rel_gpu(p.arrive + unit, 1) == cta1 - cta0;
-          if (last) p.arrive[unit] = 0;        // for the next call
-          s_flag = last;
-        }
+        if (tid == 0) s_flag = arrive_at_unit(p, runs[r], dead);
         __syncthreads();
-        const bool last = s_flag != 0;
-        if (last && !dead) {
+        if (s_flag) {
 #pragma unroll 1
           for (int k = warp; k < p.NQ; k += kWarps)
             finish(p, unit, k, combine_parts(p, runs[r], k, lane),

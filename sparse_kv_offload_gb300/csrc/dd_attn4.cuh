@@ -255,6 +255,17 @@ __device__ __forceinline__ bool ring_wait(bool alive, uint32_t bar0, uint32_t t,
   return alive;
 }
 
+// One thread: the CTA is done with the run's unit, which others share.  True for the last one
+// to come, which then joins the parts, unless one of them did no work (dead: it began after
+// an error had been reported, by this call's own CTAs perhaps, and left its part of the
+// workspace as an earlier call did): those are counted in the upper half.
+__device__ __forceinline__ bool arrive_at_unit(const Attn4Params &p, const Run &r, bool dead) {
+  const uint32_t before = (uint32_t)atom_add_acq_rel_gpu(p.arrive + r.unit, dead ? 0x10001 : 1);
+  if ((int)(before & 0xFFFFu) != r.cta1 - r.cta0) return false;
+  p.arrive[r.unit] = 0;        // for the next call
+  return !dead && before < 0x10000u;
+}
+
 // Query vector k of the run's group from the parts of all its CTAs.
 __device__ __forceinline__ Part combine_parts(const Attn4Params &p, const Run &r, int k, int lane) {
   const int group_q = p.group_q;

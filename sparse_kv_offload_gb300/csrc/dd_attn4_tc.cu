@@ -213,9 +213,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
       // an error is pending: no work, but the counts of shared units go on
       if (tid == 0)
         for (int r = 0; r < n_runs; ++r)
-          if (runs[r].cta0 != runs[r].cta1 &&
-              atom_add_acq_rel_gpu(p.arrive + runs[r].unit, 1) == runs[r].cta1 - runs[r].cta0)
-            p.arrive[runs[r].unit] = 0;
+          if (runs[r].cta0 != runs[r].cta1) arrive_at_unit(p, runs[r], true);
     } else if (warp == kSoft + kDecode) {
       // ------------------------------------------------------------- loads
       for (int i0 = 0; i0 < n_tiles; i0 += 4) {
@@ -519,11 +517,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
         soft_barrier();
         if (shared) {
           // the barrier above orders the CTA's parts before the count, the one below the count before the reads
-          if (tid == 0) {
-            const bool last = atom_add_acq_rel_gpu(p.arrive + run.unit, 1) == run.cta1 - run.cta0;
-            if (last) p.arrive[run.unit] = 0;        // for the next call
-            s_last = last;
-          }
+          if (tid == 0) s_last = arrive_at_unit(p, run, false);
           soft_barrier();
           if (s_last)
             for (int k = warp; k < p.NQ; k += kSoft)

@@ -97,3 +97,40 @@ def test_pages_that_no_query_sees_need_no_slot(dd, G, cs):
         if len(at):
             y["slot"][tuple(at[-1])] = x["n_hot"]
             assert run(dd, y)[1] == dd.DD_ERR_DEVICE_CHECK
+
+
+@pytest.mark.parametrize("G", [4, 12, 30], ids=["nq4", "nq12", "nq30"])
+def test_an_error_of_the_call_itself_leaves_no_mixture(dd, G):
+    """A bad page in one short unit, while other streams' work holds a part of the SMs, so that some CTAs of the long units
+    start after the error has been reported: every unit's output is its own result, or as it was.  (An earlier call
+    with other queries has left its sums in the workspace.)"""
+    import torch
+    B, C, cs, n = 130, 400, 16, 64
+    rng = np.random.default_rng(400 + G)
+    codes, s8 = oracle.quantise_rows(rng.standard_normal((2 * n, cs, D)), np.zeros((2 * n, cs)))
+    p = list(torch.from_numpy(oracle.kv4_pack(codes, s8)).cuda().split(n))
+    q, other = (tl.to_bf16(synth.f32_to_bf16(rng.standard_normal((B, 1, G, D)).astype(np.float32))) for _ in range(2))
+    slot, cnt = tl.to_i32(rng.integers(0, n, (B, 1, C))), tl.to_i32(np.where(np.arange(B) < 100, 2, C))
+    bad = slot.clone()
+    bad[0, 0, 1] = n
+    busy = torch.zeros(512, 1 << 15, device="cuda")
+    sides = [torch.cuda.Stream() for _ in range(4)]
+    with dd.Context(dd.Shape(B, G, 1, D, C * cs, cs, C, 1), max_misses=0, hot_slots=n) as ctx:
+        want, junk = (torch.zeros(B, 1, G, D, device="cuda") for _ in range(2))
+        ctx.sparse_attn_decode_kv4(q, *p, None, None, slot, cnt, want)
+        assert ctx.status() == 0
+        for i in range(40):
+            ctx.sparse_attn_decode_kv4(other, *p, None, None, slot, cnt, junk)
+            assert ctx.status() == 0
+            out = torch.full((B, 1, G, D), 7.0, device="cuda")
+            torch.cuda.synchronize()
+            for s in sides[:1 + i % 4]:
+                with torch.cuda.stream(s):
+                    torch.cumsum(busy, 1)
+            ctx.sparse_attn_decode_kv4(q, *p, None, None, bad, cnt, out)
+            assert ctx.status() == dd.DD_ERR_DEVICE_CHECK
+            same = (out == want).flatten(1).all(1) | (out == 7.0).flatten(1).all(1)
+            assert same[1:].all()
+        out = torch.zeros(B, 1, G, D, device="cuda")
+        ctx.sparse_attn_decode_kv4(q, *p, None, None, slot, cnt, out)
+        assert ctx.status() == 0 and torch.equal(out, want)

@@ -508,7 +508,9 @@ dd_status dd_gather_kv4(dd_ctx *ctx, const void *Kh, const void *Vh, const int32
  * either the result without what was out of range, or what was there before; one that
  * is made while an error is pending leaves them all; DD_ERR_TIMEOUT says nothing of them.
  * Attention over a whole cache: k = C, union_cnt = the chunks in use, union_idx =
- * 0, 1, ..., union_slot = their pages.  A query without a row gets zeros.
+ * 0, 1, ..., union_slot = their pages.  A query without a row gets zeros, a score of +inf
+ * or NaN makes it NaN, and a score of -inf has no weight (of the step's own rows: NaN where
+ * nothing else has any).
  * B*Hkv*(Umax*cs/16 + 1) has to stay below 2^30 (DD_ERR_INVALID_ARG). */
 dd_status dd_sparse_attn_decode_kv4(dd_ctx *ctx, const void *q, const void *Khot, const void *Vhot,
                                     const void *Kst, const void *Vst, const int32_t *k_exp, const int32_t *v_exp,

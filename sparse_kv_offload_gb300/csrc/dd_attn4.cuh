@@ -159,8 +159,10 @@ __device__ __forceinline__ void query_fragments(const uint4 (&w)[4], uint32_t (&
   for (int i = 0; i < 16; ++i) top = max(top, max((v[i] & 0x7FFFu) << 16, v[i] & 0x7FFF0000u));
   top = max(top, __shfl_xor_sync(lanes, top, 1));
   top = max(top, __shfl_xor_sync(lanes, top, 2));
-  const int e = (int)(top >> 23);
-  const int sh = top == 0 || e == 255 ? 0 : min(126, 14 - (e - 127));
+  // beside an infinite (or NaN) value every finite one stays finite: what it adds does not matter,
+  // an infinity of its own would
+  const int e = min((int)(top >> 23), 254);
+  const int sh = top == 0 ? 0 : min(126, 14 - (e - 127));
   const float mul = pow2i(sh);
 #pragma unroll
   for (int i = 0; i < 16; ++i) f[i] = cvt_f16x2(bf_lo(v[i]) * mul, bf_hi(v[i]) * mul);

@@ -134,3 +134,28 @@ def test_an_error_of_the_call_itself_leaves_no_mixture(dd, G):
         out = torch.zeros(B, 1, G, D, device="cuda")
         ctx.sparse_attn_decode_kv4(q, *p, None, None, slot, cnt, out)
         assert ctx.status() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("G", [2, 6, 12, 24], ids=lambda g: f"nq{g}")
+def test_infinite_queries(dd, G):
+    """A query vector with an infinite value beside finite ones of any size: NaN where a row's score is +inf or NaN,
+    no weight where it is -inf, whatever the finite values are."""
+    x = make_case(500, 2, 2, G, 1, 16, 30, 12, p_hot=1.0, empty=0.0, ragged=False)
+    codes, s8 = oracle.kv4_unpack(x["Khot"])
+    s8 = s8 | 0x08                                                 # no zero scale
+    codes[..., 5] = np.where(codes[..., 5] & 7, codes[..., 5] & 7, 3)      # above zero: the score has q's sign
+    x["Khot"] = oracle.kv4_pack(codes, s8)
+    want, tol = want_of(x, False)
+    q = x["q"].copy()
+    big = synth.f32_to_bf16(np.array([1.0, 6e4, 7e4, 1e10, 3e38], np.float32))
+    for i, size in enumerate(big):
+        y = q.copy()
+        y[:, 0, 0::2, 5] = 0xFF80                                  # every other head: -inf
+        y[:, 0, 0::2, 9] = size
+        y[:, 0, 0::2, 77] = size | 0x8000
+        y[0, 0, 0, 5] = 0x7F80                                     # one with +inf
+        got, st = run(dd, {**x, "q": y}, False)
+        assert st == 0
+        assert np.isnan(got[0, 0, 0]).all()
+        assert not got[0, 0, 2::2].any() and not got[1, 0, 0::2].any()
+        assert (np.abs(got - want) <= tol)[:, :, 1::2].all()

@@ -200,8 +200,8 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
         for (int e = 0; e < 4; ++e) w[e] = s_query[(kPack ? g8 & 3 : g8) * 16 + t4 * 4 + e];
         // B fragment of step s: values 32 t4 + 4 s + {0,1} and {2,3} of query vector g8
         query_fragments(w, qf, back);
-        mul[0][0] = __shfl_sync(0xffffffffu, back, t4 * 8) * kmul;
-        mul[0][1] = __shfl_sync(0xffffffffu, back, t4 * 8 + 4) * kmul;
+        mul[0][0] = score_factor(__shfl_sync(0xffffffffu, back, t4 * 8), kmul);
+        mul[0][1] = score_factor(__shfl_sync(0xffffffffu, back, t4 * 8 + 4), kmul);
       } else {
         if (warp < NT && (!kPack || lane < 16)) {
           uint4 w[4];
@@ -222,8 +222,8 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int qv = n * 8 + (kPack ? 2 * t4 & 3 : 2 * t4);
-          mul[n][0] = s_back[qv] * kmul;
-          mul[n][1] = s_back[qv + 1] * kmul;
+          mul[n][0] = score_factor(s_back[qv], kmul);
+          mul[n][1] = score_factor(s_back[qv + 1], kmul);
         }
       }
 #pragma unroll

@@ -4,6 +4,7 @@
 // joining of a unit's parts.
 #pragma once
 
+#include <float.h>
 #include <limits.h>
 
 #include "dd_attn.cuh"
@@ -168,6 +169,11 @@ __device__ __forceinline__ void query_fragments(const uint4 (&w)[4], uint32_t (&
   for (int i = 0; i < 16; ++i) f[i] = cvt_f16x2(bf_lo(v[i]) * mul, bf_hi(v[i]) * mul);
   back = pow2i(-sh);
 }
+
+// From a product of scaled queries to a score, finite: a product of 0 stays a score of 0.
+// (Where this passes fp32, products differ by 2^-34 at least, so scores by 2^94: one row has all the
+// weight either way.)
+__device__ __forceinline__ float score_factor(float back, float kmul) { return fminf(back * kmul, FLT_MAX); }
 
 // The unit's own new rows into shared memory (keys, then values, 16 pieces a row), by
 // asynchronous copies of `threads` threads.

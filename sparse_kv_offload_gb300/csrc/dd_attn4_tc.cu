@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           uint32_t f[16];
           float back;
           query_fragments(w, f, back);
-          if (part == 0) s_back[qv] = back * (sl2 * pow2i(run.ke));
+          if (part == 0) s_back[qv] = score_factor(back, sl2 * pow2i(run.ke));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int c = 4 * part + e;

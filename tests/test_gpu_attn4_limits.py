@@ -159,3 +159,14 @@ def test_infinite_queries(dd, G):
         assert np.isnan(got[0, 0, 0]).all()
         assert not got[0, 0, 2::2].any() and not got[1, 0, 0::2].any()
         assert (np.abs(got - want) <= tol)[:, :, 1::2].all()
+
+
+@pytest.mark.parametrize("G", [4, 6, 12, 24], ids=lambda g: f"nq{g}")
+def test_a_factor_beyond_fp32_keeps_zero_scores(dd, G):
+    """Queries and a head's exponent so large that their factor alone passes fp32: rows of zeros still score zero."""
+    x = make_case(600, 2, 2, G, 1, 16, 30, 12, p_hot=1.0, empty=0.0, ragged=False, qscale=2.0 ** 90)
+    x["ke"] = np.full(2, 64)
+    x["Khot"] = np.zeros_like(x["Khot"])
+    want, tol = want_of(x, False)                                  # the mean of V
+    got, st = run(dd, x, False)
+    assert st == 0 and (np.abs(got - want) <= tol).all()

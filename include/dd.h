@@ -426,9 +426,9 @@ typedef struct {
 } dd_rope_params;
 
 /* Fill `table` (host memory, DD_ROPE_TABLE_BYTES) with what the calls below read
- * from device memory: each pair's frequency as a 64-bit fraction of a turn, so
- * that position * frequency is exact modulo one turn at any position, and 512
- * sines and cosines to 48 bits.  Host only: no device call. */
+ * from device memory: each pair's frequency as the nearest 64-bit fraction of a
+ * turn, so that position * frequency is off by position * 2^-62 radians at most,
+ * and 512 sines and cosines to 48 bits.  Host only: no device call. */
 #define DD_ROPE_TABLE_BYTES 8704
 dd_status dd_rope_table(const dd_rope_params *params, void *table);
 
@@ -444,8 +444,9 @@ typedef struct {
  * Row t of request b has position start_pos[b] + t, start_pos int32 [B] device,
  * positions >= 0; new_len int32 [B] device or NULL (= T): rows t >= new_len[b]
  * are padding and neither read nor written.  B is the context's; T and H are this
- * call's.  Each output is the exact rotation of its pair, taken to about 2^-36 of the
- * larger of the two values, rounded once to bf16. */
+ * call's.  A negative position or a length outside [0, T] sets DD_ERR_DEVICE_CHECK and leaves
+ * the request's rows out.  Each output is the exact rotation of its pair, taken to about
+ * 2^-36 + position * 2^-62 of the larger of the two values, rounded once to bf16. */
 dd_status dd_rope_rows(dd_ctx *ctx, const dd_rope *rope, const void *x, const int64_t x_stride[3], void *out,
                        const int64_t out_stride[3], int32_t T, int32_t H, const int32_t *start_pos,
                        const int32_t *new_len, dd_stream_t stream);

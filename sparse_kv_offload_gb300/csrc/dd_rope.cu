@@ -5,8 +5,8 @@
 // bf16 nearest to the exact rotation.  fp32 alone is off where it matters: the
 // angle of position 10^5 loses 17 of its 24 bits, and a product rounded to fp32
 // falls on the other side of a bf16 tie once in some ten thousand values.  So
-//   - a frequency is a 64-bit fraction of a turn: position * frequency wraps
-//     modulo a turn by itself, exactly, at any position;
+//   - a frequency is a 64-bit fraction of a turn, rounded once: position * frequency
+//     wraps modulo a turn by itself, off by position * 2^-62 radians at most;
 //   - sine and cosine come from 512 stored angles (hi + lo floats) and the angle
 //     sum formulas with the remainder |r| <= pi/512, whose series end after
 //     r^5 and r^4;
@@ -503,6 +503,75 @@ cudaError_t launch_append(const dd_append_args *a, void *kh_dev, void *vh_dev, i
 }  // namespace dd
 
 // --------------------------------------------------------------------- host table
+// A position is multiplied by the frequency, so a frequency needs all of its 64 bits: from a pow in
+// double it would be off by a hundred units of the last one (2^-23 radians at position 2^31),
+// and differently with every libm.  So frequencies are worked out in pairs of doubles.
+namespace {
+
+struct Wide {            // hi + lo, |lo| at most half a last bit of hi
+  double hi, lo;
+};
+
+Wide wide_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Wide operator+(Wide a, Wide b) {
+  const Wide s = wide_sum(a.hi, b.hi);
+  return wide_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+Wide operator-(Wide a) { return {-a.hi, -a.lo}; }
+Wide operator*(Wide a, Wide b) {
+  const double p = a.hi * b.hi, e = fma(a.hi, b.hi, -p);
+  return wide_sum(p, e + (a.hi * b.lo + a.lo * b.hi));
+}
+Wide operator/(Wide a, Wide b) {
+  const double q = a.hi / b.hi;
+  const Wide rest = a + -(b * Wide{q, 0.0});
+  return wide_sum(q, (rest.hi + rest.lo) / b.hi);
+}
+
+// a^n times 2^-e, the powers of two kept apart so that nothing overflows
+Wide wide_power(Wide a, int n, int &e) {
+  Wide r{1.0, 0.0};
+  int ea = 0;
+  e = 0;
+  auto scale = [](Wide &x, int &ex) {
+    int k;
+    frexp(x.hi, &k);
+    x = {ldexp(x.hi, -k), ldexp(x.lo, -k)};
+    ex += k;
+  };
+  for (scale(a, ea); n; n >>= 1) {
+    if (n & 1) {
+      r = r * a;
+      e += ea;
+      scale(r, e);
+    }
+    a = a * a;
+    ea *= 2;
+    scale(a, ea);
+  }
+  return r;
+}
+
+// base^(-i/n), 0 <= i < n <= 64: from pow's answer y by Newton's steps on y^n base^i = 1 (an error of
+// 2^-44 of y becomes one of 2^-83, and that one vanishes)
+Wide wide_root(double base, int i, int n) {
+  Wide y{pow(base, -(double)i / n), 0.0};
+  for (int step = 0; step < 2; ++step) {
+    int ey, eb;
+    const Wide p = wide_power(y, n, ey), b = wide_power({base, 0.0}, i, eb), one = p * b;
+    const Wide off = Wide{ldexp(one.hi, ey + eb), ldexp(one.lo, ey + eb)} + Wide{-1.0, 0.0};
+    y = y + -(y * (off / Wide{(double)n, 0.0}));
+  }
+  return y;
+}
+
+Wide clamp01(Wide x) { return x.hi < 0.0 ? Wide{0.0, 0.0} : x.hi >= 1.0 ? Wide{1.0, 0.0} : x; }
+
+}  // namespace
+
 static bool rope_params_ok(const dd_rope_params *p) {
   if (!p || p->rot_dim < 32 || p->rot_dim > dd::kD || p->rot_dim % 32) return false;
   if (!(p->base > 1.0) || !isfinite(p->base) || !isfinite(p->gain)) return false;
@@ -518,8 +587,8 @@ static bool rope_params_ok(const dd_rope_params *p) {
 extern "C" dd_status dd_rope_table(const dd_rope_params *p, void *table) {
   if (!rope_params_ok(p) || !table) return DD_ERR_INVALID_ARG;
   const double pi2 = 6.283185307179586476925286766559;
+  const Wide kPerRadian{0.15915494309189535, -9.839338337591243e-18};     // 1 / (2 pi)
   const int n = p->rot_dim / 2;
-  const double base = p->scaling == DD_ROPE_NTK ? p->base * pow(p->factor, p->rot_dim / (p->rot_dim - 2.0)) : p->base;
   double lo = 0, hi = 0;
   if (p->scaling == DD_ROPE_BY_PARTS) {
     const double a = p->rot_dim * log(p->orig_len / (p->beta_fast * pi2)) / (2.0 * log(p->base));
@@ -531,20 +600,23 @@ extern "C" dd_status dd_rope_table(const dd_rope_params *p, void *table) {
   for (int i = 0; i < 64; ++i) {
     freq[i] = 0;
     if (i >= n) continue;
-    double f = pow(base, -2.0 * i / p->rot_dim);
-    if (p->scaling == DD_ROPE_LINEAR) f /= p->factor;
-    if (p->scaling == DD_ROPE_BY_PARTS) {
-      const double span = hi - lo > 1e-3 ? hi - lo : 1e-3;
-      const double r = fmin(fmax((i - lo) / span, 0.0), 1.0);
-      f = f / p->factor * r + f * (1.0 - r);
+    const Wide whole{1.0, 0.0}, factor{p->factor, 0.0};
+    Wide f = wide_root(p->base, i, n);
+    if (p->scaling == DD_ROPE_LINEAR) {
+      f = f / factor;
+    } else if (p->scaling == DD_ROPE_NTK) {      // (base * factor^(n/(n-1)))^(-i/n)
+      f = f * wide_root(p->factor, i, n - 1);
+    } else if (p->scaling == DD_ROPE_BY_PARTS) {
+      const Wide r = clamp01(Wide{i - lo, 0.0} / Wide{hi - lo > 1e-3 ? hi - lo : 1e-3, 0.0});
+      f = f * (whole + -r) + f / factor * r;
     } else if (p->scaling == DD_ROPE_BY_WAVELENGTH) {
-      const double r = fmin(fmax((p->orig_len * f / pi2 - p->beta_slow) / (p->beta_fast - p->beta_slow), 0.0), 1.0);
-      f = f * r + f / p->factor * (1.0 - r);
+      const Wide turns = Wide{p->orig_len, 0.0} * f * kPerRadian;
+      const Wide r = clamp01((turns + Wide{-p->beta_slow, 0.0}) / wide_sum(p->beta_fast, -p->beta_slow));
+      f = f * r + f / factor * (whole + -r);
     }
-    // f / (2 pi) in two doubles, times 2^64 (f <= 1, so below 2^62)
-    const double inv = 0.15915494309189535, inv_lo = -9.839338337591243e-18;
-    const double t = f * inv, e = fma(f, inv, -t) + f * inv_lo;
-    const double th = floor(ldexp(t, 64)), tl = floor((ldexp(t, 64) - th) + ldexp(e, 64) + 0.5);
+    // turns per position, times 2^64 (f <= 1, so below 2^62), to the nearest integer
+    const Wide t = f * kPerRadian;
+    const double v = ldexp(t.hi, 64), th = floor(v), tl = floor((v - th) + ldexp(t.lo, 64) + 0.5);
     freq[i] = (uint64_t)th + (uint64_t)(int64_t)tl;
   }
   const double gain =

@@ -380,7 +380,7 @@ dd_status dd_update_residency(dd_ctx *ctx, int32_t step, int32_t cap, int32_t sl
  * one for each 16 consecutive values: value = code * scale * 2^e, where e is the
  * exponent of the KV head (k_exp / v_exp, int32 [Hkv] device, |e| <= 64, NULL =
  * all zero).  The product of code and scale has at most six significant bits, so
- * every value is exact in bf16 (2^e apart from its range).  Rows are stored in blocks of 16
+ * every value is exact in bf16.  Rows are stored in blocks of 16
  * (16 x 64 bytes of codes, then 16 x 8 bytes of scales: 1152 bytes), a chunk of
  * cs rows is cs/16 blocks, so a 4-bit pool or staging buffer is uint8
  * [slots, cs*72] and a 4-bit home cache uint8 [B,Hkv,C,cs*72], K and V apart,
@@ -444,7 +444,7 @@ typedef struct {
  * Row t of request b has position start_pos[b] + t, start_pos int32 [B] device,
  * positions >= 0; new_len int32 [B] device or NULL (= T): rows t >= new_len[b]
  * are padding and neither read nor written.  B is the context's; T and H are this
- * call's.  A negative position or a length outside [0, T] sets DD_ERR_DEVICE_CHECK and leaves
+ * call's (B*T at most 2^35 - 16, H at most 65535).  A negative position or a length outside [0, T] sets DD_ERR_DEVICE_CHECK and leaves
  * the request's rows out.  Each output is the exact rotation of its pair, taken to about
  * 2^-36 + position * 2^-62 of the larger of the two values, rounded once to bf16. */
 dd_status dd_rope_rows(dd_ctx *ctx, const dd_rope *rope, const void *x, const int64_t x_stride[3], void *out,
@@ -459,9 +459,10 @@ dd_status dd_rope_rows(dd_ctx *ctx, const dd_rope *rope, const void *x, const in
  *   - of the chunk's resident copy in Khot/Vhot (bf16 [hot_slots,cs,128] or 4-bit
  *     [hot_slots,cs*72]; both NULL: not written) where resident_slot (int32
  *     [B,Hkv,C]) is not -1.
- * k, v: bf16 [B,T,Hkv,128] with strides as in dd_rope_rows.  Every other row keeps
+ * k, v: bf16 [B,T,Hkv,128] with strides (and B*T) as in dd_rope_rows.  Every other row keeps
  * its bytes.  A position outside [0, L), a length outside [0, T] or a slot outside
- * [-1, hot_slots) sets DD_ERR_DEVICE_CHECK and its rows are left out.  Two resident
+ * [-1, hot_slots) sets DD_ERR_DEVICE_CHECK and its rows are left out (with a negative
+ * start_pos or a bad length all rows of the request).  Two resident
  * chunks must not share a slot.
  * 4 bits: a rotated key is rounded to bf16 first (so a cache of either format is
  * built from the same keys), the values of a head are divided by 2^e, a group's
@@ -487,8 +488,8 @@ dd_status dd_append_kv(dd_ctx *ctx, const dd_append_args *args, dd_stream_t stre
 /* dd_gather_kv for a 4-bit home cache Kh/Vh (pinned host, or device), by a kernel
  * that loads over the host link.  expand = 0: chunk m of the list is copied as it
  * is into staging slot m of Kst/Vst, uint8 [max_misses,cs*72].  expand != 0: it is
- * written as bf16 values, Kst/Vst bf16 [max_misses,cs,128], for the calls that take
- * bf16 chunks (a value below bf16's normal range rounds). */
+ * written as bf16 values, exactly, Kst/Vst bf16 [max_misses,cs,128], for the calls that
+ * take bf16 chunks. */
 dd_status dd_gather_kv4(dd_ctx *ctx, const void *Kh, const void *Vh, const int32_t *miss_list,
                         const int32_t *miss_count, void *Kst, void *Vst, int32_t expand, const int32_t *k_exp,
                         const int32_t *v_exp, dd_stream_t stream);

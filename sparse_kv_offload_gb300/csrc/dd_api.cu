@@ -683,6 +683,9 @@ static bool rows_ok(const void *p, const int64_t *stride) {
   return p && stride && aligned16(p) && stride[0] % 8 == 0 && stride[1] % 8 == 0 && stride[2] % 8 == 0;
 }
 
+// sixteen rows a CTA, and no more CTAs than a grid can have
+static bool too_many_rows(int64_t B, int64_t T) { return B * T > (int64_t)16 * INT32_MAX; }
+
 dd_status dd_rope_rows(dd_ctx *c, const dd_rope *rope, const void *x, const int64_t x_stride[3], void *out,
                        const int64_t out_stride[3], int32_t T, int32_t H, const int32_t *start_pos,
                        const int32_t *new_len, dd_stream_t stream) {
@@ -690,6 +693,7 @@ dd_status dd_rope_rows(dd_ctx *c, const dd_rope *rope, const void *x, const int6
   if (c->dims.B == 0 || T == 0 || H == 0) return DD_OK;
   if (!rope_ok(rope) || !rows_ok(x, x_stride) || !rows_ok(out, out_stride) || !start_pos) return DD_ERR_INVALID_ARG;
   if (x == out && memcmp(x_stride, out_stride, 3 * sizeof(int64_t)) != 0) return DD_ERR_INVALID_ARG;
+  if (too_many_rows(c->dims.B, T)) return DD_ERR_INVALID_ARG;
   DD_TRY(on_device(c));
   c->launches += 1;
   return cuda_ok(dd::launch_rope_rows(rope, x, x_stride, out, out_stride, c->dims.B, T, H, start_pos, new_len,
@@ -700,6 +704,7 @@ dd_status dd_append_kv(dd_ctx *c, const dd_append_args *a, dd_stream_t stream) {
   if (!c || !a || a->T < 0 || c->dims.Hkv > 65535) return DD_ERR_INVALID_ARG;
   if (a->format != DD_KV_BF16 && a->format != DD_KV_4BIT) return DD_ERR_INVALID_ARG;
   if (c->units == 0 || a->T == 0) return DD_OK;
+  if (too_many_rows(c->dims.B, a->T)) return DD_ERR_INVALID_ARG;
   if (!rows_ok(a->k, a->k_stride) || !rows_ok(a->v, a->v_stride) || !a->start_pos) return DD_ERR_INVALID_ARG;
   if (a->rope && !rope_ok(a->rope)) return DD_ERR_INVALID_ARG;
   if ((a->Kh == nullptr) != (a->Vh == nullptr) || (a->Khot == nullptr) != (a->Vhot == nullptr))

@@ -318,9 +318,7 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
             }
             float t0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
             float t1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-            // (the difference of two neighbours is exact; their sum with a bound is not from 2^25 on, where floats
-            // are 4 apart; -inf - -inf is no reason to move)
-            if (__any_sync(0xffffffffu, t0 - m[n][0] > kLazy + kHead || t1 - m[n][1] > kLazy + kHead)) {
+            if (__any_sync(0xffffffffu, t0 > highest_for(m[n][0]) || t1 > highest_for(m[n][1]))) {
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) {
                 t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));

@@ -17,6 +17,10 @@ constexpr int kMaxRuns = 16;             // units of a slice listed at a time
 constexpr float kLazy = 8.f;             // a score may exceed the reference by 2^kLazy ...
 constexpr float kHead = 6.f;             // ... and weights are held times 2^kHead
 
+// The highest score that leaves reference m in place.  Rounded down, as from 2^25 on floats are 4 apart
+// and the nearest one may lie above m + 14: no float is left out between this one and the sum.
+__device__ __forceinline__ float highest_for(float m) { return __fadd_rd(m, kLazy + kHead); }
+
 struct Run {           // a unit's place in the sequence of tiles
   int unit, b, g;                  // unit, request, KV head
   int start, end, cnt, len;        // tiles [start, end) of the sequence; chunks; rows (INT_MAX: no kv_len)

@@ -406,12 +406,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_attn4_tc(const __grid_constan
           asm volatile(
               "{\n .reg .pred q, r;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred r, 1, %2, q;\n selp.u32 %0, 1, 0, r;\n}\n"
               : "=r"(any)
-              : "r"((uint32_t)(pm - m > kLazy + kHead)), "n"(kSoft * 32)
+              : "r"((uint32_t)(pm > highest_for(m))), "n"(kSoft * 32)
               : "memory");
           const float mx = some ? fmaxf(s_red[0][row], s_red[1][row]) : -INFINITY;
           float factor = 1.f;
-          // (the difference, not a sum with the bound: exact where floats are far apart)
-          if (mx - m > kLazy + kHead) {
+          if (mx > highest_for(m)) {
             const float nm = mx - kHead;
             factor = weight_of(m, nm);
             m = nm;

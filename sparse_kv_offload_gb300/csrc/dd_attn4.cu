@@ -244,13 +244,14 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
       }
 
 #pragma unroll 1
-      for (; i < n_tiles && wlo + warp + i * kWarps < run_end; ++i) {
+      for (; alive && i < n_tiles && wlo + warp + i * kWarps < run_end; ++i) {
         // a block that was not asked for (0) is computed with all its rows masked
         const uint32_t meta0 = __shfl_sync(0xffffffffu, cur.meta, 2 * (i & 15));
         const uint32_t meta1 = __shfl_sync(0xffffffffu, cur.meta, 2 * (i & 15) + 1);
         const uint32_t st = (seq + (uint32_t)i) % S;
-        alive = ring_wait<S>(alive, bar0, seq + (uint32_t)i, seq + (uint32_t)min(i + S, n_tiles) - 1u, lane, a.status);
-        if ((meta0 | meta1) && alive) {
+        alive = ring_wait<S>(bar0, seq + (uint32_t)i, seq + (uint32_t)min(i + S, n_tiles) - 1u, lane, a.status);
+        if (!alive) break;
+        if (meta0 | meta1) {
           const uint32_t tile = ring + st * kTileBytes;
           const uint32_t full_meta = all_q | 16u << 8;
           const bool full = (meta0 & 0x1FFFu) == full_meta && (meta1 & 0x1FFFu) == full_meta;

@@ -255,16 +255,13 @@ __device__ __forceinline__ void ring_drain(uint32_t bar0, uint32_t stages, uint3
   __syncwarp();
 }
 
-// A warp's wait for tile t of its ring, the last one asked for being `last` (all lanes).  The
-// first wait that runs out is the only one: what is behind it is drained, and from then on
-// (alive = what the call before gave) the answer is false at once.
+// A warp's wait for tile t of its ring (all lanes).  False where it runs out: what is behind it,
+// up to tile `last`, is drained, and the warp waits for no other tile.
 template <uint32_t S>
-__device__ __forceinline__ bool ring_wait(bool alive, uint32_t bar0, uint32_t t, uint32_t last, int lane,
-                                          int32_t *status) {
-  if (!alive) return false;
-  alive = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * (t % S), (t / S) & 1u, status));
-  if (!alive) ring_drain(bar0, S, t + 1, last + 1, lane, status);
-  return alive;
+__device__ __forceinline__ bool ring_wait(uint32_t bar0, uint32_t t, uint32_t last, int lane, int32_t *status) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar0 + 8 * (t % S), (t / S) & 1u, status));
+  if (!ok) ring_drain(bar0, S, t + 1, last + 1, lane, status);
+  return ok;
 }
 
 // One thread: the CTA is done with the run's unit, which others share.  True for the last one

@@ -25,8 +25,8 @@ __global__ void k_selftest_wait(int kind, const unsigned long long *word, int32_
     if (lane < 2) mbar_init(bar0 + 8 * lane, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
-    bool alive = true;
-    for (uint32_t t = 0; t < kTiles; ++t) alive = ring_wait<2>(alive, bar0, t, min(t + 2, kTiles) - 1, lane, status);
+    for (uint32_t t = 0; t < kTiles; ++t)
+      if (!ring_wait<2>(bar0, t, min(t + 2, kTiles) - 1, lane, status)) return;
     return;
   }
   if (threadIdx.x != 0) return;

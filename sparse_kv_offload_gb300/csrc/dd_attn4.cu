@@ -14,17 +14,19 @@
 //     interleaved before they are converted.
 // Query vectors are the narrow side (8 a tile), so the 4 or 8 of a KV head's
 // group are not padded to 16.
-// Whole cache, 8 requests of 128K (842 MB): 177 us, where the copies alone take 131 and
-// everything but the copies 160-176.  A tile of 32 rows takes some 750 instructions: 128 conversions
+// Whole cache, 8 requests of 128K (842 MB): 177 us on the device in a graph (a call among
+// others 182-191), where the copies alone take 131 and everything but the copies 160-176.  A tile of 32 rows takes some 750 instructions: 128 conversions
 // and 128 multiplications, 41 to interleave V's rows, 64 additions of sums, the rest loads,
 // softmax and moves.
 //
 // Precision.  A code times its scale is exact in fp16.  A query vector is scaled
 // by a power of two to just below 2^15, where its 8-bit significands are exact in
 // fp16 down to 2^-32 of its largest value.  P is split into two fp16 parts (22
-// bits).  The matrix unit adds up 32 rows at a time; the running sums are added
-// in fp32 outside of it, where additions round to nearest: its own truncates, and
-// over the hundreds of additions of a long context that shows (1e-5).
+// bits, next to an exponential of ex2.approx, which is good to 2^-22 itself).  The matrix unit
+// truncates when it adds; that is left in for the 128 terms of a score and for 32
+// rows of O at a time.  The running sums are added in fp32 outside of it, where
+// additions round to nearest: over the hundreds of additions of a long context
+// truncation shows (1e-5).
 // The softmax's reference value is moved only when a score exceeds it by 2^8, so
 // most tiles need no maximum across lanes (P stays at 2^14 or below).
 //
@@ -112,8 +114,8 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
   __shared__ uint4 s_tails[2 * kMaxNq * 16];      // the unit's own new rows: keys, values
   __shared__ float s_back[NT * 8];
   __shared__ int s_flag;
-  __shared__ uint4 s_query[kVecs * 16];
-  __shared__ uint2 s_pack[kPack ? 8 * 16 : 1];      // their fragments, [8 steps][query vector, quarter]            // the run's query vectors as they are
+  __shared__ uint4 s_query[kVecs * 16];             // the run's query vectors as they are
+  __shared__ uint2 s_pack[kPack ? 8 * 16 : 1];      // their fragments, [8 steps][query vector, quarter]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t4 = lane & 3, g8 = lane >> 2;
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(attn4_warps(NT) * 32, 2) k_attn4(const __grid_
         uint4 w[4];
         float back;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = s_query[(kPack ? g8 & 3 : g8) * 16 + t4 * 4 + e];
+        for (int e = 0; e < 4; ++e) w[e] = s_query[g8 * 16 + t4 * 4 + e];
         // B fragment of step s: values 32 t4 + 4 s + {0,1} and {2,3} of query vector g8
         query_fragments(w, qf, back);
         mul[0][0] = score_factor(__shfl_sync(0xffffffffu, back, t4 * 8), kmul);

@@ -373,14 +373,19 @@ dd_status dd_update_residency(dd_ctx *ctx, int32_t step, int32_t cap, int32_t sl
  * These calls take a context like every other one.  They run on the current
  * device, which has to be the context's (DD_ERR_INVALID_ARG otherwise), keep
  * nothing on the host from one call for the next, and may all be captured into
- * a CUDA graph.
+ * a CUDA graph.  While an error is pending the gather and the attention do nothing,
+ * rotation and appends go on.  Appends leave the landmarks as they are, and dd_step,
+ * dd_prefetch_kv and dd_update_residency work on bf16 chunks only: landmarks of a 4-bit
+ * cache are built from expanded chunks, and a chunk is admitted to a 4-bit pool by the
+ * caller, who copies its page.
  *
  * The 4-bit cache.  A row of 128 values is 64 bytes of e2m1 codes (byte i: value
  * 2i in the low nibble, value 2i+1 in the high nibble) and eight e4m3 scales,
  * one for each 16 consecutive values: value = code * scale * 2^e, where e is the
  * exponent of the KV head (k_exp / v_exp, int32 [Hkv] device, |e| <= 64, NULL =
- * all zero).  The product of code and scale has at most six significant bits, so
- * every value is exact in bf16.  Rows are stored in blocks of 16
+ * all zero; one beyond 64 sets DD_ERR_DEVICE_CHECK and counts as 64).  The product of
+ * code and scale has at most six significant bits, so every value is exact in
+ * bf16.  Rows are stored in blocks of 16
  * (16 x 64 bytes of codes, then 16 x 8 bytes of scales: 1152 bytes), a chunk of
  * cs rows is cs/16 blocks, so a 4-bit pool or staging buffer is uint8
  * [slots, cs*72] and a 4-bit home cache uint8 [B,Hkv,C,cs*72], K and V apart,
@@ -513,6 +518,9 @@ dd_status dd_gather_kv4(dd_ctx *ctx, const void *Kh, const void *Vh, const int32
  * 0, 1, ..., union_slot = their pages.  A query without a row gets zeros, a score of +inf
  * or NaN makes it NaN, and a score of -inf has no weight (of the step's own rows: NaN where
  * nothing else has any).
+ * Sums are held in fp32; weights have 22 bits, and the tensor cores, which truncate, add up the
+ * 128 terms of a score and up to 1,024 rows.  Measured against 64 bits: 6e-8 to 6.4e-7 of the output
+ * (relative L2) for up to 16 query vectors per KV head, up to 2.3e-6 for more.
  * B*Hkv*(Umax*cs/16 + 1) has to stay below 2^30 (DD_ERR_INVALID_ARG). */
 dd_status dd_sparse_attn_decode_kv4(dd_ctx *ctx, const void *q, const void *Khot, const void *Vhot,
                                     const void *Kst, const void *Vst, const int32_t *k_exp, const int32_t *v_exp,

@@ -554,10 +554,18 @@ cudaError_t launch_t(int grid, const Attn4Params &p, cudaStream_t s) {
 }  // namespace
 
 // Up to 8 query vectors: one tile a warp, up to 16: two; more: tcgen05.  Both sides of the
-// second border (us, mma.sync in groups of 16 / tcgen05): 12 query vectors 41 / 66, 16: 79 /
-// 120, 20: 44.3 / 40.7, 24: 17.5 / 17.3, 40: 215 / 132, 64: 87 / 60; and with 4 the whole cache
-// of 8 requests takes 177 / 489.  (The first border is a tile's width: up to it a second tile
-// would hold padding only.)
+// second border (us on the device, mma.sync in groups of 16 / tcgen05):
+//    4  one request, 16 chunks of 16                          6.6 / 10.0
+//    4  8 requests of 128K, whole cache, 8 KV heads           177 / 463
+//    8  16 requests, 64 of 2,048 chunks of 16, two queries    19.1 / 28.9
+//   12  8 requests, 256 of 512 chunks of 64, two queries      41.5 / 63.2
+//   15  3 requests, 77 of 333 chunks of 32, three queries     20.9 / 22.0
+//   16  32 requests, 128 of 2,048 chunks of 16, four queries  79 / 111
+//   20  16 requests, 100 of 512 chunks of 32, two queries     44.3 / 40.9
+//   24  2 requests, 64 of 1,024 chunks of 16, two queries     17.5 / 17.3
+//   40  32 requests, 128 of 2,048 chunks of 16, five queries  215 / 133
+//   64  8 requests, 64 of 1,024 chunks of 32, eight queries   87 / 60
+// (The first border is a tile's width: up to it a second tile would hold padding only.)
 Attn4Plan attn4_plan(int units, int NQ, int sm_count) {
   Attn4Plan pl;
   pl.nt = NQ <= 8 ? 1 : NQ <= 16 ? 2 : 0;

@@ -1,8 +1,10 @@
 // Gather of missing chunks from a 4-bit home cache (pinned host, or HBM), as they are or
 // expanded to bf16 values.
 //
-// A chunk takes 72 bytes a row instead of 256, so the host link, which bounds a step whose
-// chunks are missing, brings 3.6 times as many rows.
+// A chunk takes 72 bytes a row instead of 256, and the host link bounds a step whose chunks are
+// missing.  20,000 chunks of 16 rows from pinned memory, in any order: bf16 800 us (205 GB/s, a
+// copy 210), 4 bits 238 us (194 GB/s), expanded 240 us: 3.4 times as many rows a second.
+// 2,000 chunks, where latency begins to count: 98, 40 and 42 us.
 #include "dd_attn.cuh"
 #include "dd_kv4.cuh"
 

@@ -27,10 +27,14 @@
 // 48 us, 82%.  (Every value by the sticky path: 231 us; the next head's pieces in registers
 // instead of four heads' on their way to shared memory 103 and 59; lanes 0-3 turning all of
 // half a row's pairs instead of every lane half of its own 108.)
-// Appending 201 MB to bf16 pages takes 39.5 us, 75% (first form 61), bound by the loads that
-// 16 warps an SM keep in flight; copies to shared memory gain 1 us there, keys and values by
-// blocks of their own lose 4.  4 bits are bound by the issue slots, most of them the
-// rounding's: 201 MB into 57 MB of pages in some 70 us.  A step's call of a few rows takes
+// Appending 201 MB to bf16 pages takes 39.6 us, 75% (first form 61), bound by the loads that
+// 16 warps an SM keep in flight, which is this layout's doing: a thread keeps its sines and cosines,
+// 32 registers, for all heads.  Copies to shared memory gain 1 us there, keys and values by
+// blocks of their own lose 4.  4 bits are bound by the same 16 warps: they use two thirds of the
+// issue slots, most of them for the rounding, and no pipe to its limit (201 MB into 57 MB of pages
+// in some 70 us).  Pages in pinned host memory: 131,072 tokens of 8 heads take 2,803 us in bf16
+// (191 GB/s, a copy to the host 192) and 852 us in 4 bits (177 GB/s; a row's scales go as
+// single bytes).  A step's call of a few rows takes
 // 2.6 us (rotation) or 3.1 us (append) on the device, a launch and one row's time.
 #include <math.h>
 
@@ -450,9 +454,11 @@ Rope rope_of(const dd_rope *r) {
 // Heads per warp: one while that does not give every SM 16 warps (of 4 tokens), so
 // that a step of a few tokens takes one row's time; else 16 at most (by then a token's
 // sines and cosines are a tenth of the work), in groups of one size.  A step of 32 rows
-// with 32 heads: one head a warp 2.6 us, 16 heads 6.1; a prompt of 4 x 4K tokens with 64
-// heads: one 238 us, 16 heads 108 (8 and 32 within 2% of it); 4-bit append of 2 x 32K tokens
-// with 8 heads: one 180 us, 8 heads 119.
+// with 32 heads: one head a warp 2.6 us, 16 heads 6.2; a prompt of 4 x 4K tokens with 64
+// heads, half of each turned: one 168 us, 8 heads 82.7, 16 heads 83.5, 32 heads 87; all of 4 x 2K
+// tokens' 64 heads turned: one 131, 8 heads 52.3, 16 heads 48.1, 32 heads 48.7; append of 4 ragged
+// prompts of 8K with 8 heads: one 60.9, 8 heads 39.6; 4-bit append and expansion of 2 x 32K
+// tokens with 8 heads: one 168 us, 8 heads 107.
 int heads_per_warp(int64_t tokens, int H, int sm_count) {
   const int64_t warps = (tokens + 3) / 4, want = (int64_t)sm_count * 16;
   int64_t groups = (H + 15) / 16;

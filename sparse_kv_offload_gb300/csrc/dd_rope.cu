@@ -616,8 +616,12 @@ extern "C" dd_status dd_rope_table(const dd_rope_params *p, void *table) {
       const Wide r = clamp01(Wide{i - lo, 0.0} / Wide{hi - lo > 1e-3 ? hi - lo : 1e-3, 0.0});
       f = f * (whole + -r) + f / factor * r;
     } else if (p->scaling == DD_ROPE_BY_WAVELENGTH) {
+      // (the borders first: between them the quotient is one of numbers of a size)
       const Wide turns = Wide{p->orig_len, 0.0} * f * kPerRadian;
-      const Wide r = clamp01((turns + Wide{-p->beta_slow, 0.0}) / wide_sum(p->beta_fast, -p->beta_slow));
+      const Wide r = turns.hi < p->beta_slow    ? Wide{0.0, 0.0}
+                     : turns.hi >= p->beta_fast ? whole
+                                                : clamp01((turns + Wide{-p->beta_slow, 0.0}) /
+                                                          wide_sum(p->beta_fast, -p->beta_slow));
       f = f * r + f / factor * (whole + -r);
     }
     // turns per position, times 2^64 (f <= 1, so below 2^62), to the nearest integer

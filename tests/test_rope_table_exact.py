@@ -55,3 +55,22 @@ def test_frequencies_are_the_nearest_fractions_of_a_turn(dd, scaling, base):
             for i, want in enumerate(exact_turns(rot, base, scaling, **kw)):
                 # half a unit of 2^-64 turns, and what pairs of doubles add: some 2^-95 of 2^62 units
                 assert abs(Dec(int(freq[i])) - want * 2 ** 64) <= Dec("0.5") + Dec(2) ** -30, (rot, i, factor)
+
+
+def test_borders_of_the_ramps(dd):
+    """Wavelength borders next to each other and contexts of any length: pairs stay or are divided, nothing overflows."""
+    plain = np.frombuffer(dd.rope_host_table(128, base=5e5).numpy().tobytes(), np.uint64, 64)
+    divided = np.frombuffer(dd.rope_host_table(128, base=5e5, scaling=dd.ROPE_LINEAR, factor=8.0).numpy().tobytes(),
+                            np.uint64, 64)
+    for orig_len, want in ((1e300, plain), (1e-300, divided)):
+        for slow in (1.0, 1e-290, 1e290):
+            if (orig_len > 1.0) == (slow > 1.0) and slow != 1.0:
+                continue
+            t = dd.rope_host_table(128, base=5e5, scaling=dd.ROPE_BY_WAVELENGTH, factor=8.0, orig_len=orig_len,
+                                   beta_slow=slow, beta_fast=float(np.nextafter(slow, np.inf)))
+            assert np.array_equal(np.frombuffer(t.numpy().tobytes(), np.uint64, 64), want)
+    for orig_len, want in ((1e300, plain), (1e-300, divided)):
+        t = dd.rope_host_table(128, base=5e5, scaling=dd.ROPE_BY_PARTS, factor=8.0, orig_len=orig_len, beta_slow=1.0,
+                               beta_fast=32.0)
+        got = np.frombuffer(t.numpy().tobytes(), np.uint64, 64)
+        assert np.array_equal(got[1:], want[1:])       # (the ramp's first pair may lie on its border)

@@ -19,8 +19,9 @@
  * the attention, a capped LRU residency update of per-(request, KV head) hot
  * pools after a step, a predictive prefetch of a layer's predicted chunks
  * ahead of its step, and beside the step rotary positions, appending rows to
- * the cache, and a cache held in 4 bits with the gather and the attention
- * that read it (each documented at its entry point below).
+ * the cache, a cache held in 4 bits with the gather and the attention
+ * that read it, attention of new tokens over a paged cache, and eviction by the
+ * attention weight that chunks have gathered (each documented at its entry point below).
  *
  * Notation: B requests, Hq query heads, Hkv KV heads, G = Hq/Hkv (query head h
  * reads KV head floor(h/G)), d head dimension, L context tokens, cs tokens per
@@ -528,6 +529,126 @@ dd_status dd_sparse_attn_decode_kv4(dd_ctx *ctx, const void *q, const void *Khot
                                     const int32_t *union_slot, const uint8_t *union_qmask,
                                     const int32_t *union_cnt, const int32_t *miss_count, const int32_t *kv_len,
                                     float softmax_scale, float *out, dd_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * New tokens over a paged cache, the weight that chunks gather, eviction by it
+ *
+ * A loop that keeps a cache to a budget:  dd_evict_chunks makes room for the tokens to come
+ * and writes the list of what is in the pool, dd_append_kv writes their keys and values,
+ * dd_extend_attn lets them attend, dd_chunk_weights adds their weights up per chunk.  The
+ * calls run on the current device, which has to be the context's, keep nothing on the host from
+ * one call for the next, and may be captured into a CUDA graph.  They share the
+ * context's counters: like all calls on a context, they must not overlap on the GPU.  While an
+ * error is pending they do nothing.  bf16 chunks only: a 4-bit cache is expanded by
+ * dd_gather_kv4 into staging first.
+ * ------------------------------------------------------------------------- */
+
+/* The rows of new tokens: q bf16 [B,T,Hq,128] with the strides (in elements, multiples of 8, not
+ * negative; the last dimension dense) of request, token and head.  Token t of request b
+ * stands at position start_pos[b] + t; tokens t >= new_len[b] are padding (new_len NULL: T).  A
+ * negative position, one at or behind L or a length outside [0, T] sets DD_ERR_DEVICE_CHECK and
+ * leaves the request's tokens out. */
+typedef struct {
+  const void *q;
+  int64_t q_stride[3];
+  int32_t T;
+  const int32_t *start_pos, *new_len;   /* int32 [B] device */
+} dd_new_rows;
+
+/* The chunks that are in the cache, per (request, KV head), in the layout of dd_resolve_union's
+ * and dd_evict_chunks' outputs: union_idx int32 [B,Hkv,Umax] chunk numbers, ascending, no chunk twice;
+ * union_slot their slots (hot: slot, staging: -(m+1)); union_cnt how many.  A whole cache: k = C, union_idx
+ * = 0, 1, ...  Row r of chunk c holds position c*cs + r.  A chunk that no token
+ * sees is not looked at; one that is seen and has a slot or number out of range sets
+ * DD_ERR_DEVICE_CHECK and is left out, as a count outside [0, Umax] leaves out the whole list. */
+typedef struct {
+  const void *Khot, *Vhot;              /* bf16 [hot_slots,cs,128] */
+  const void *Kst, *Vst;                /* bf16 [max_misses,cs,128] */
+  const int32_t *union_idx, *union_slot, *union_cnt;
+  const int32_t *miss_count;            /* NULL: every staging slot below max_misses is filled */
+} dd_page_list;
+
+/* Attention of new tokens (one a request, or a prompt's thousands) over the cache, causal by position: the
+ * token at position p sees the rows of its KV head's listed chunks at positions <= p, its own among
+ * them once it has been appended.
+ *   out[b,t,h] = sum_i w_i V_i / sum_i w_i,  w_i = exp(scale * q.K_i),  bf16, strides as q's;
+ *   lse[b,t,h] = ln sum_i w_i,  fp32 [B,T,Hq] dense, or NULL.
+ * A token that sees no row has zeros and lse -inf.  Rows that it does not see do not reach it, whatever
+ * they hold (NaN and infinities among it).  A score of +inf or NaN makes the row NaN, one of -inf has no
+ * weight.  Outputs of padding are left as they were.  Weights are rounded to bf16 for their product
+ * with V (up to 2^-8 of each, at random); sums and statistics are fp32.
+ * workspace: dd_extend_attn_workspace(ctx, T) bytes of device memory, 16-byte aligned, which calls on
+ * one stream may share; it holds nothing between calls.  out must not overlap the inputs.
+ * A call that reports DD_ERR_DEVICE_CHECK leaves each (request, KV head)'s outputs as its result without
+ * what was out of range, or as they were. */
+typedef struct {
+  dd_new_rows rows;
+  dd_page_list pages;
+  float softmax_scale;                  /* <= 0: 1/sqrt(128) */
+  void *out;
+  int64_t out_stride[3];
+  float *lse;
+  void *workspace;
+  int64_t workspace_bytes;
+} dd_extend_args;
+
+int64_t dd_extend_attn_workspace(const dd_ctx *ctx, int32_t T);
+dd_status dd_extend_attn(dd_ctx *ctx, const dd_extend_args *args, dd_stream_t stream);
+
+/* The attention weight that chunks gather from new tokens:
+ *   weight[b,g,c] = decay * weight[b,g,c] + sum over the counted tokens t and the G heads h of KV head g
+ *                   of the weights exp(scale * q.K_i - lse[b,t,h]) of the rows i of c that t sees
+ * for every chunk c of the list (the others keep theirs); weight fp32 [B,Hkv,C], lse as dd_extend_attn
+ * has written it for these rows.  window > 0 counts the last `window` tokens of each request, 0
+ * all.  decay in [0, 1]; 0 takes nothing over, whatever weight held.  A token without rows (lse -inf) adds
+ * nothing.  Vhot and Vst are not used.  fp32 sums in an order that depends on the sizes alone.
+ * workspace: dd_chunk_weights_workspace(ctx) bytes, as above. */
+typedef struct {
+  dd_new_rows rows;
+  dd_page_list pages;
+  float softmax_scale;
+  const float *lse;
+  int32_t window;
+  float decay;
+  float *weight;
+  void *workspace;
+  int64_t workspace_bytes;
+} dd_weights_args;
+
+int64_t dd_chunk_weights_workspace(const dd_ctx *ctx);
+dd_status dd_chunk_weights(dd_ctx *ctx, const dd_weights_args *args, dd_stream_t stream);
+
+/* Eviction by gathered weight, and slots for the chunks to come.  The pool is split per (request, KV head)
+ * unit u as for dd_update_residency: slots u*S .. u*S+S-1, S = slots_per_unit (1..16384, hot_slots =
+ * B*Hkv*S).  Per unit, with n0 = ceil(kv_len[b]/cs) and n1 = ceil((kv_len[b] + new_len[b])/cs):
+ *   1. R chunks are resident (resident_slot >= 0), and N of the chunks n0 .. n1-1 are not;
+ *   2. E = min(max(R + N - keep, 0), candidates) chunks leave, the candidates being the resident chunks c with
+ *      first <= c < n0 - last: those of the smallest weight[b,g,c], the lower chunk first where
+ *      weights are equal (-0 equals +0, a NaN is below every number);
+ *   3. the N new chunks, ascending, take the free slots, ascending.  Where there are too few the later ones
+ *      get none and DD_ERR_CAPACITY is set.
+ * weight fp32 [B,Hkv,C]; kv_len int32 [B]; new_len int32 [B] or NULL (no new chunks); resident_slot int32
+ * [B,Hkv,C], resident_out the same or another array, written whole.  Each of these may be NULL:
+ *   slot_chunk int32 [B,Hkv,S]  the chunk in each slot, or -1, written whole
+ *   last_used int32 [B,Hkv,S]   -1 for free slots, `step` for new chunks' slots, else kept
+ *   evicted int32 [B,Hkv,S], evicted_cnt int32 [B,Hkv]   the chunks that left, ascending
+ *   union_idx, union_slot int32 [B,Hkv,Umax], union_cnt int32 [B,Hkv]   the list of resident chunks after the
+ *      call, ascending, as dd_extend_attn and the decode attentions read it (all three or none; S <= Umax)
+ * Entries behind a count keep what they held.  A slot outside the unit's range or held by two chunks, or a
+ * length outside [0, L], sets DD_ERR_DEVICE_CHECK: the unit's resident_out is then its resident_slot, its
+ * counts 0, and the rest as it was.  K and V are not touched: an evicted chunk's slot is free at once. */
+typedef struct {
+  const float *weight;
+  const int32_t *kv_len, *new_len;
+  int32_t slots_per_unit, keep, first, last, step;
+  const int32_t *resident_slot;
+  int32_t *resident_out;
+  int32_t *slot_chunk, *last_used;
+  int32_t *evicted, *evicted_cnt;
+  int32_t *union_idx, *union_slot, *union_cnt;
+} dd_evict_args;
+
+dd_status dd_evict_chunks(dd_ctx *ctx, const dd_evict_args *args, dd_stream_t stream);
 
 /* Diagnostics for failure detection: runs one of the library's bounded
  * device waits on something that nothing will ever signal -- kind 0: an

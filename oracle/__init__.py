@@ -26,4 +26,5 @@ against closed forms, library routines for special cases, brute force on
 tiny inputs and the worked numbers printed on the pages.
 """
 from .kv_cache import *  # noqa: F401,F403
+from .page_list import *  # noqa: F401,F403
 from .sparse_kv import *  # noqa: F401,F403

@@ -10,7 +10,7 @@
 #include <algorithm>
 #include <vector>
 
-#include "dd_tc.cuh"
+#include "dd_pages.cuh"
 
 struct dd_ctx {
   dd_dims dims;
@@ -34,6 +34,7 @@ struct dd_ctx {
   dd::AttnPlan plan;
   dd::Attn4Plan plan4;
   int32_t *arrive4 = nullptr;         // 4-bit attention: CTAs done with each unit (zero between calls)
+  int32_t *page_ctr = nullptr;        // kernels over paged caches: items handed out, parts done (zero between calls)
   // host side
   int32_t *h_miss = nullptr;          // pinned: [1 + max_misses]
   cudaStream_t copy_stream = nullptr;
@@ -220,6 +221,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   add(3, 4);                                   // ticket counters + look-back epoch
   add(1, 8);                                   // self-test word
   add(units, 4);             // 4-bit attention: arrival counters
+  add(2 + (int64_t)dd::kCtrPerCta * c->sm_count, 4);   // kernels over paged caches: counters
   if (cudaMalloc(&c->ws, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   uint8_t *cur = static_cast<uint8_t *>(c->ws);
   c->status = carve<int32_t>(cur, 1);
@@ -243,6 +245,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   c->ticket = carve<int32_t>(cur, 3);
   c->diag_word = carve<unsigned long long>(cur, 1);
   c->arrive4 = carve<int32_t>(cur, units);
+  c->page_ctr = carve<int32_t>(cur, 2 + (int64_t)dd::kCtrPerCta * c->sm_count);
   if (cudaMemset(c->ws, 0, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   const int32_t first_epoch = 1;   // look-back words start zeroed, i.e. with epoch 0
   if (cudaMemcpy(c->ticket + 2, &first_epoch, sizeof(first_epoch), cudaMemcpyHostToDevice) != cudaSuccess)
@@ -772,6 +775,103 @@ dd_status dd_sparse_attn_decode_kv4(dd_ctx *c, const void *q, const void *Khot, 
   a.status = c->status;
   c->launches += 1;
   return cuda_ok(dd::launch_attn4(a, c->plan4, c->part_o, c->part_ml, c->arrive4, (cudaStream_t)stream));
+}
+
+// ------------------------------------------- new tokens over a paged cache, chunk weights, eviction
+
+// What the two kernels over lists of chunks share; V's pools are the caller's to check.
+static dd_status pages_args(const dd_ctx *c, const dd_new_rows *r, const dd_page_list *l, float softmax_scale,
+                            dd::PagesArgs *out) {
+  if (!rows_ok(r->q, r->q_stride) || !r->start_pos) return DD_ERR_INVALID_ARG;
+  if (!l->union_idx || !l->union_slot || !l->union_cnt) return DD_ERR_INVALID_ARG;
+  if (c->hot_slots > 0 && (!l->Khot || !aligned16(l->Khot))) return DD_ERR_INVALID_ARG;
+  if (c->max_misses > 0 && (!l->Kst || !aligned16(l->Kst))) return DD_ERR_INVALID_ARG;
+  // tensor maps step by less than 2^40 bytes, and not backwards
+  for (int i = 0; i < 3; ++i)
+    if (r->q_stride[i] < 0 || r->q_stride[i] >= (int64_t(1) << 39)) return DD_ERR_INVALID_ARG;
+  const dd_dims &d = c->dims;
+  dd::PagesArgs a{};
+  a.start_pos = r->start_pos, a.new_len = r->new_len;
+  a.union_idx = l->union_idx, a.union_slot = l->union_slot, a.union_cnt = l->union_cnt, a.miss_count = l->miss_count;
+  a.B = d.B, a.T = r->T, a.Hq = d.Hq, a.Hkv = d.Hkv, a.G = c->G, a.cs = d.cs, a.C = c->C, a.umax = c->umax;
+  a.hot_slots = c->hot_slots, a.max_misses = c->max_misses;
+  a.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kD);
+  a.sl2 = a.scale * 1.4426950408889634f;
+  a.status = c->status;
+  *out = a;
+  return DD_OK;
+}
+
+int64_t dd_extend_attn_workspace(const dd_ctx *c, int32_t T) {
+  if (!c || T < 0) return -1;
+  return dd::extend_workspace(c->dims.B, T, c->dims.Hq, c->dims.Hkv, c->sm_count);
+}
+
+dd_status dd_extend_attn(dd_ctx *c, const dd_extend_args *e, dd_stream_t stream) {
+  if (!c || !e || e->rows.T < 0) return DD_ERR_INVALID_ARG;
+  if (c->units == 0 || e->rows.T == 0) return DD_OK;
+  dd::ExtendArgs a{};
+  DD_TRY(pages_args(c, &e->rows, &e->pages, e->softmax_scale, &a.p));
+  if (c->hot_slots > 0 && (!e->pages.Vhot || !aligned16(e->pages.Vhot))) return DD_ERR_INVALID_ARG;
+  if (c->max_misses > 0 && (!e->pages.Vst || !aligned16(e->pages.Vst))) return DD_ERR_INVALID_ARG;
+  if (!rows_ok(e->out, e->out_stride)) return DD_ERR_INVALID_ARG;
+  if (!e->workspace || !aligned16(e->workspace) || e->workspace_bytes < dd_extend_attn_workspace(c, e->rows.T))
+    return DD_ERR_INVALID_ARG;
+  DD_TRY(on_device(c));
+  a.q = e->rows.q, a.Khot = e->pages.Khot, a.Vhot = e->pages.Vhot, a.Kst = e->pages.Kst, a.Vst = e->pages.Vst;
+  a.out = e->out, a.lse = e->lse;
+  for (int i = 0; i < 3; ++i) a.q_stride[i] = e->rows.q_stride[i], a.out_stride[i] = e->out_stride[i];
+  a.parts = static_cast<float *>(e->workspace);
+  a.ctr = c->page_ctr, a.dummy = c->dummy_pool, a.sm_count = c->sm_count;
+  c->launches += 1;
+  return cuda_ok(dd::launch_extend(a, (cudaStream_t)stream));
+}
+
+int64_t dd_chunk_weights_workspace(const dd_ctx *c) {
+  if (!c) return -1;
+  return dd::weights_workspace(c->dims.cs, c->sm_count);
+}
+
+dd_status dd_chunk_weights(dd_ctx *c, const dd_weights_args *e, dd_stream_t stream) {
+  if (!c || !e || e->rows.T < 0 || e->window < 0) return DD_ERR_INVALID_ARG;
+  if (!(e->decay >= 0.f && e->decay <= 1.f)) return DD_ERR_INVALID_ARG;
+  if (c->units == 0 || e->rows.T == 0) return DD_OK;
+  dd::WeightsArgs a{};
+  DD_TRY(pages_args(c, &e->rows, &e->pages, e->softmax_scale, &a.p));
+  if (!e->lse || !e->weight) return DD_ERR_INVALID_ARG;
+  if (!e->workspace || !aligned16(e->workspace) || e->workspace_bytes < dd_chunk_weights_workspace(c))
+    return DD_ERR_INVALID_ARG;
+  DD_TRY(on_device(c));
+  a.q = e->rows.q, a.Khot = e->pages.Khot, a.Kst = e->pages.Kst;
+  for (int i = 0; i < 3; ++i) a.q_stride[i] = e->rows.q_stride[i];
+  a.lse = e->lse, a.weight = e->weight, a.window = e->window, a.decay = e->decay;
+  a.parts = static_cast<float *>(e->workspace);
+  a.ctr = c->page_ctr, a.dummy = c->dummy_pool, a.sm_count = c->sm_count;
+  c->launches += 1;
+  return cuda_ok(dd::launch_weights(a, (cudaStream_t)stream));
+}
+
+dd_status dd_evict_chunks(dd_ctx *c, const dd_evict_args *e, dd_stream_t stream) {
+  if (!c || !e || e->slots_per_unit < 1 || e->slots_per_unit > dd::kMaxC) return DD_ERR_INVALID_ARG;
+  if (e->keep < 0 || e->keep > e->slots_per_unit || e->first < 0 || e->last < 0) return DD_ERR_INVALID_ARG;
+  if (c->hot_slots != (int64_t)c->units * e->slots_per_unit) return DD_ERR_INVALID_ARG;
+  if (c->units == 0) return DD_OK;
+  if (!e->weight || !e->kv_len || !e->resident_slot || !e->resident_out) return DD_ERR_INVALID_ARG;
+  if ((e->union_idx || e->union_slot || e->union_cnt) &&
+      (!e->union_idx || !e->union_slot || !e->union_cnt || e->slots_per_unit > c->umax))
+    return DD_ERR_INVALID_ARG;
+  if (e->evicted && !e->evicted_cnt) return DD_ERR_INVALID_ARG;
+  DD_TRY(on_device(c));
+  dd::EvictArgs a{};
+  a.weight = e->weight, a.kv_len = e->kv_len, a.new_len = e->new_len, a.resident_slot = e->resident_slot;
+  a.resident_out = e->resident_out, a.slot_chunk = e->slot_chunk, a.last_used = e->last_used;
+  a.evicted = e->evicted, a.evicted_cnt = e->evicted_cnt;
+  a.list_idx = e->union_idx, a.list_slot = e->union_slot, a.list_cnt = e->union_cnt;
+  a.units = c->units, a.Hkv = c->dims.Hkv, a.C = c->C, a.cs = c->dims.cs, a.S = e->slots_per_unit;
+  a.keep = e->keep, a.first = e->first, a.last = e->last, a.step = e->step, a.umax = c->umax;
+  a.status = c->status;
+  c->launches += 1;
+  return cuda_ok(dd::launch_evict(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

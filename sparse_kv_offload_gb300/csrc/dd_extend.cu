@@ -1,0 +1,869 @@
+// Attention of new tokens over a paged cache, on the fifth-generation tensor cores.
+//
+// Token t of request b stands at position p = start[b] + t and sees the rows of its KV
+// head's listed chunks whose positions are at most p:  o = sum_i w_i v_i / sum_i w_i with
+// w_i = exp(scale q.k_i), and lse = ln sum_i w_i.  One pass over the rows: with a reference m of
+// the scores seen so far, l = sum exp(s - m) and O = sum exp(s - m) v are kept, and both are
+// multiplied by exp(m - m') where m moves (only when a score exceeds it by 2^8: the weights
+// then stay finite, and few tiles pay).
+//
+// The G heads of a KV head share its rows, so a tile of 128 query rows is tt = 128 / G tokens
+// by G heads, brought by TMA from the caller's strides.  A CTA (one per SM) works on two
+// streams, each with S (128 x 128) and O (128 x 128) in tensor memory and four softmax warps,
+// a thread a query row; while one stream's softmax runs, the other's products do.  With
+// more than 128 query rows per KV head the streams are two row tiles over the same keys; with
+// fewer they are the even and the odd tiles of keys of one row tile, joined at the end.
+//   warps 0-3, 4-7  softmax of the streams: S out of tensor memory, weights as bf16 back in
+//                   its place, O rescaled when a reference moves, outputs
+//   warp 8          S = Q K^T, O += P V (P straight from tensor memory)
+//   warp 9          hands out the work and brings K's tiles, warp 10 Q's and V's
+//   warp 11         looks over V's tiles that some row does not see entirely: a masked weight of
+//                   0 times an infinity or NaN would be NaN, so such values are taken out of the
+//                   tile, and a row that does see one has it put into its output at the end
+// Weights are rounded to bf16 for the second product (V's type: the tensor cores take two
+// operands of one type): up to 2^-8 of each weight, at random, as the rounding of the
+// output.  l is the sum of the weights before that, so that lse has fp32's precision.
+//
+// Work: an item is a pair of row tiles (or the row tile) by a range of tiles of keys.  Ranges
+// are as long as they may be while the CTAs stay evenly filled (cut_of); a row tile cut into several ranges
+// has its parts joined by whoever finishes last, in the ranges' order.  Items are handed
+// out one after another with the pairs of one KV head and range next to each other, so that the
+// CTAs at work read the same keys at about the same time, out of L2.
+#include "dd_pages.cuh"
+
+namespace dd {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kK = 3, kV = 2;                        // tiles of K and of V on the way
+constexpr int kInfo = 8;                             // records of K's tiles (a softmax warp is at most kK + 2 behind)
+constexpr uint32_t kTmem = 512;                      // S: 2 x 128 columns, O: 2 x 128
+constexpr int kSoftRegs = 208, kOtherRegs = 80;      // 256 * 208 + 128 * 80 <= 384 * 168 at launch
+constexpr float kHead = 8.f;                         // weights stay below 2^8
+
+struct Item {
+  int unit, t0, start, len;
+  int j0;                     // first tile of keys
+  int ents;                   // the list's entries that the item's last token may see
+  int pos_max, pos_min;       // positions of the item's last and first token
+  int c[2];                   // tiles of each stream
+  int parts[2];               // of each stream's row tile: 0 nothing to do, 1 written out, more: joined
+  int part0[2], part[2];      // slots of the row tile's first part and of this stream's
+  int cut[2];                 // arrival counter
+  int local;                  // the two streams' sums are joined within the CTA
+};
+
+struct Misc {
+  uint64_t bars[40];
+  Item item[2];
+  int pos[kInfo][8];          // positions of the first rows of a tile's chunks
+  int whole[kInfo];           // every query row sees the whole tile
+  int vpos[kV][8], vwhole[kV];   // the same of V's tiles
+  int bad[3][128];            // lowest position of a NaN, +inf, -inf in each column of V
+  int bad_item, dead, pending, last[2];
+  uint32_t tmem;
+};
+
+constexpr size_t kTiles = (size_t)(2 + kK + kV) * kTileBytes;
+constexpr size_t kSmem = kTiles + sizeof(Misc);
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+struct ExtendParams {
+  CUtensorMap q, k, v, kst, vst;
+  PagesArgs a;
+  uint16_t *out;
+  int64_t os[3];
+  float *lse;
+  float *part_o;              // [slots][rows][128]
+  float2 *part_ml;            // [slots][rows]: reference (a score before the factor), sum
+  int64_t slots;              // parts there is room for, before the CTAs' own
+  WorkCounters w;
+  int mt;                     // tokens of an item
+  int pairs;                  // row tiles of an item: 1 or 2
+};
+
+// One (request, KV head) as the planning sees it.
+struct Unit {
+  int cnt, start, len, groups, tiles;     // groups of mt tokens; tiles of keys that the last of them may see
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// entries that a token may see: chunk numbers ascend, so entry i is chunk i or a later one
+__device__ __forceinline__ int entry_bound(const PagesArgs &a, const Unit &u, int token) {
+  return min(u.cnt, (u.start + token) / a.cs + 1);
+}
+
+__device__ __forceinline__ int tiles_of(const PagesArgs &a, int entries) {
+  return max(1, ceil_div(entries * a.cs, kTileKeys));      // (a row without keys still has its zeros to write)
+}
+
+__device__ __forceinline__ Unit load_unit(const ExtendParams &p, int u) {
+  Unit r = {0, 0, 0, 0, 0};
+  const Request q = load_request(p.a, u / p.a.Hkv);
+  r.cnt = load_count(p.a, u);
+  r.start = q.start, r.len = q.len;
+  r.groups = ceil_div(q.len, p.mt);
+  if (r.groups) r.tiles = tiles_of(p.a, entry_bound(p.a, r, q.len - 1));
+  return r;
+}
+
+// The first group of tokens that has more than `tiles` tiles of keys.
+__device__ __forceinline__ int first_longer(const ExtendParams &p, const Unit &u, int tiles) {
+  if (tiles <= 0) return 0;
+  if (u.tiles <= tiles) return u.groups;
+  const int need = tiles * kTileKeys - u.start + 1;        // its last token's number, from 1
+  return need <= 0 ? 0 : ceil_div(need, p.mt) - 1;
+}
+
+// The longest range of keys (in tiles) of an item.  Of the cuts into S = 1, 2, .. ranges of the mean
+// row tile, with at most kItemsPerCta items a CTA, the one that ends first: rounds of items, each its tiles
+// and kItemCost of them for what an item costs beside (queries, sums out and in, the join).  No
+// range is longer than a CTA's share, which keeps one long request from ending alone.
+// Bounds that follow, with P CTAs: row tile pairs that are cut <= 2 P, their ranges <= 6 P.
+constexpr int kItemCost = 3, kItemsPerCta = 4;
+__device__ __forceinline__ int cut_of(long long work, long long groups, int cta, int lane) {
+  const long long mean = max(1ll, (work + groups - 1) / max(1ll, groups));
+  const long long most = max(1ll, (long long)kItemsPerCta * cta / max(1ll, groups));
+  unsigned long long best = ~0ull;
+  for (long long s = 1 + lane; s <= min(most, mean); s += 32) {
+    const long long len = (mean + s - 1) / s;
+    const unsigned long long cost = (unsigned long long)((groups * s + cta - 1) / cta * (len + kItemCost));
+    best = min(best, (cost << 12) | (unsigned long long)min(s, 4095ll));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = min(best, (unsigned long long)__shfl_xor_sync(0xffffffffu, best, o));
+  const long long s = max(1ll, (long long)(best & 4095ull));
+  long long len = (mean + s - 1) / s;
+  if (s == 1) len = max(len, (work + cta - 1) / cta);
+  return (int)min(len, (long long)INT_MAX / kTileKeys);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ ExtendParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc &x = *reinterpret_cast<Misc *>(smem + kTiles);
+  const PagesArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t q0 = smem_u32(smem), k0 = q0 + 2 * kTileBytes, v0 = k0 + kK * kTileBytes;
+  const uint32_t bars = smem_u32(x.bars);
+  const uint32_t k_full = bars, k_free = k_full + 8 * kK, v_full = k_free + 8 * kK, v_ok = v_full + 8 * kV,
+                 v_free = v_ok + 8 * kV, q_full = v_free + 8 * kV, q_free = q_full + 8, s_full = q_free + 8,
+                 p_ready = s_full + 16, o_full = p_ready + 16, item_full = o_full + 16, item_free = item_full + 16,
+                 looked = item_free + 16, joined = looked + 16, mma_done = joined + 8;
+  if (tid == 0) {
+    for (int i = 0; i < kK; ++i) mbar_init(k_full + 8 * i, 1), mbar_init(k_free + 8 * i, 1);
+    for (int i = 0; i < kV; ++i) mbar_init(v_full + 8 * i, 1), mbar_init(v_ok + 8 * i, 1), mbar_init(v_free + 8 * i, 1);
+    mbar_init(q_full, 1), mbar_init(q_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(looked + 8 * i, 1), mbar_init(s_full + 8 * i, 2), mbar_init(p_ready + 8 * i, 4), mbar_init(o_full + 8 * i, 1);
+      mbar_init(item_full + 8 * i, 1), mbar_init(item_free + 8 * i, 11);
+    }
+    mbar_init(joined, 8), mbar_init(mma_done, 1);
+    x.bad_item = -1, x.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&x.tmem)), "r"(kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  pdl_wait();
+  pdl_trigger();
+  if (tid == 0) x.pending = load_status(a.status);
+  __syncthreads();
+  tc_fence_after();
+  const bool pending = x.pending != 0;      // an error is pending: no work
+  const uint32_t tmem = x.tmem;
+  const int rows_tile = a.tt * a.G;         // query rows of a tile
+  const int chunks = kTileKeys / a.cs;      // of a tile
+
+  // Waits give up together: the first that runs out (2 s) ends the CTA's work.  What has
+  // happened passes every waiter, so warps that meet at a barrier give up at the same one.
+  volatile int *dead = &x.dead;
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity & 1u)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+      if (mbar_try_wait(bar, parity & 1u)) return true;
+      if ((it & 63u) == 0) {
+        if (*dead) return false;
+        if (globaltimer_ns() - t0 > 2000000000ull) {
+          *dead = 1;
+          set_status(a.status, DD_ERR_TIMEOUT);
+          return false;
+        }
+      }
+    }
+  };
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  };
+
+  // (with an error pending: nothing, but the counters below are left all the same)
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (pending) {
+    } else if (warp == 9) {
+      // ------------------------------------------------------- the work, and K's tiles
+      const int units = a.B * a.Hkv, cta = (int)gridDim.x;
+      long long work = 0, groups = 0;
+      for (int u = lane; u < units; u += 32) {
+        const Unit r = load_unit(p, u);
+        work += (long long)r.groups * r.tiles;
+        groups += r.groups;
+      }
+  #pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        work += __shfl_xor_sync(0xffffffffu, work, o);
+        groups += __shfl_xor_sync(0xffffffffu, groups, o);
+      }
+      const int cut = cut_of(work, groups, cta, lane);
+      const int64_t staged = staged_slots(a);
+
+      // the lanes hold 32 units; what lies before them: items, ranges of cut groups, cut groups
+      int base_u = -32, cuts_before = 0;
+      long long items_before = 0, items_here = 0;
+      int parts_before = 0, parts_here = 0, cuts_here = 0;
+      Unit mine = {0, 0, 0, 0, 0};
+      int ranges = 0, items = 0, items_pre = 0, parts_pre = 0, cuts_pre = 0, m1 = 0;
+      long long next = blockIdx.x;
+      uint32_t n_item = 0, kt = 0;
+      bool ok = true;
+      while (ok) {
+        const long long want = next;
+        int ticket = 0;
+        if (lane == 0) ticket = atomicAdd(p.w.ctr, 1);       // the next one: on its way during this one's work
+        while (base_u + 32 < units && want >= items_before + items_here) {
+          items_before += items_here, parts_before += parts_here, cuts_before += cuts_here;
+          base_u += 32;
+          mine = {0, 0, 0, 0, 0};
+          if (base_u + lane < units) mine = load_unit(p, base_u + lane);
+          ranges = mine.groups ? ceil_div(mine.tiles, cut) : 0;
+          items = 0;
+          m1 = first_longer(p, mine, cut);
+          if (mine.groups == 1 || ranges <= 1) {
+            items = mine.groups * ranges;
+          } else {
+            for (int s = 0; s < ranges; ++s) items += mine.groups - first_longer(p, mine, s * cut);
+          }
+          int parts = ranges > 1 ? items - m1 : 0, cuts = ranges > 1 ? mine.groups - m1 : 0;
+          items_pre = warp_incl_scan(items), parts_pre = warp_incl_scan(parts), cuts_pre = warp_incl_scan(cuts);
+          items_here = __shfl_sync(0xffffffffu, items_pre, 31);
+          parts_here = __shfl_sync(0xffffffffu, parts_pre, 31);
+          cuts_here = __shfl_sync(0xffffffffu, cuts_pre, 31);
+          items_pre -= items, parts_pre -= parts, cuts_pre -= cuts;
+        }
+        const uint32_t slot = n_item & 1u;
+        if (n_item >= 2) ok = wait_warp(item_free + 8 * slot, (n_item >> 1) - 1);
+        if (!ok) break;
+        Item &it = x.item[slot];
+        if (want >= items_before + items_here) {             // no more
+          if (lane == 0) {
+            it.unit = -1;
+            mbar_arrive(item_full + 8 * slot);
+          }
+          break;
+        }
+        // the unit that has it
+        const int here = (int)(want - items_before);
+        const uint32_t at = __ballot_sync(0xffffffffu, items_pre <= here && here < items_pre + items);
+        const int src = __ffs((int)at) - 1;
+        Unit u;
+        u.cnt = __shfl_sync(0xffffffffu, mine.cnt, src), u.start = __shfl_sync(0xffffffffu, mine.start, src);
+        u.len = __shfl_sync(0xffffffffu, mine.len, src), u.groups = __shfl_sync(0xffffffffu, mine.groups, src);
+        u.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
+        const int n_ranges = __shfl_sync(0xffffffffu, ranges, src), um1 = __shfl_sync(0xffffffffu, m1, src);
+        const int part_base = parts_before + __shfl_sync(0xffffffffu, parts_pre, src);
+        const int cut_base = cuts_before + __shfl_sync(0xffffffffu, cuts_pre, src);
+        int rem = here - __shfl_sync(0xffffffffu, items_pre, src), s = 0, m = 0;
+        if (u.groups == 1) {
+          s = rem;
+        } else {
+          for (;; ++s) {
+            const int n = u.groups - first_longer(p, u, s * cut);
+            if (rem < n) break;
+            rem -= n;
+          }
+          m = u.groups - 1 - rem;                            // long ones first
+        }
+        const int unit = base_u + src;
+        const int64_t list = (int64_t)unit * a.umax;
+        const int t0 = m * p.mt, t_end = min(t0 + p.mt, u.len);
+        const int tiles = tiles_of(a, entry_bound(a, u, t_end - 1)), n_cut = ceil_div(tiles, cut);
+        const int j0 = s * cut, j1 = min(tiles, j0 + cut);
+        int skip = 0;                                          // ranges of the groups before this one
+        if (n_cut > 1 && m > 0)
+          for (int r = 0; r < n_ranges; ++r) skip += max(0, m - max(first_longer(p, u, r * cut), um1));
+        int c[2] = {0, 0}, parts[2] = {0, 0};
+        int ents = 0;
+        for (int w = 0; w < 2; ++w) {
+          const int lo = t0 + (p.pairs == 2 ? w * a.tt : 0), hi = p.pairs == 2 ? min(lo + a.tt, t_end) : t_end;
+          if (lo >= t_end) continue;
+          const int bound = entry_bound(a, u, hi - 1);
+          // with many tokens a list with gaps may hold many chunks that this token does not see yet
+          const int seen = a.T > kTileKeys ? entries_up_to(a.union_idx + list, bound, (u.start + hi - 1) / a.cs, lane) : bound;
+          const int n = max(0, min(ceil_div(seen * a.cs, kTileKeys), j1) - j0);
+          ents = max(ents, seen);
+          if (p.pairs == 2) {
+            c[w] = n;
+            const int mine_cut = ceil_div(tiles_of(a, bound), cut);
+            parts[w] = s < mine_cut ? mine_cut : 0;
+          } else {
+            c[w] = w == 0 ? (n + 1) / 2 : n / 2;
+            parts[w] = n_cut > 1 ? 2 * n_cut : (c[w] > 0 || w == 0 ? 1 : 0);
+          }
+        }
+        if (lane == 0) {
+          it.unit = unit, it.t0 = t0, it.start = u.start, it.len = u.len;
+          it.j0 = j0, it.ents = ents;
+          it.pos_max = u.start + t_end - 1, it.pos_min = u.start + t0;
+          it.local = p.pairs == 1 && n_cut == 1 && c[1] > 0;
+          for (int w = 0; w < 2; ++w) {
+            it.c[w] = c[w], it.parts[w] = parts[w];
+            const int first = 2 * (part_base + skip);
+            it.part0[w] = p.pairs == 2 ? first + w : first;
+            it.part[w] = first + 2 * s + w;
+            it.cut[w] = p.pairs == 2 ? 2 * (cut_base + m - um1) + w : cut_base + m - um1;
+          }
+          mbar_arrive(item_full + 8 * slot);
+        }
+        ++n_item;
+
+        // K's tiles; a batch of 32 entries is loaded while the tiles before it are asked for
+        const int nt = p.pairs == 2 ? max(c[0], c[1]) : c[0] + c[1];
+        const int per = 32 / chunks, pos_max = u.start + t_end - 1, pos_min = u.start + t0;
+        auto batch = [&](int j) {
+          const int e = (j0 + j) * chunks + lane;
+          if (e >= ents) return Entry{0, INT_MAX};
+          if (a.union_idx[list + e] > pos_max / a.cs) return Entry{0, INT_MAX};     // not seen, not looked at
+          return load_entry(a, list, e, ents, staged);
+        };
+        Entry now = batch(0);
+        for (int j = 0; ok && j < nt; j += per) {
+          Entry then = {0, INT_MAX};
+          if (j + per < nt) then = batch(j + per);
+          const uint32_t whole = __ballot_sync(0xffffffffu, now.pos != INT_MAX && now.pos <= pos_min - (a.cs - 1));
+          for (int i = 0; i < per && j + i < nt; ++i, ++kt) {
+            const uint32_t st = kt % kK;
+            if (kt >= kK) ok = wait_warp(k_free + 8 * st, kt / kK - 1);
+            if (!ok) break;
+            const int sl = __shfl_sync(0xffffffffu, now.slot, i * chunks + ((lane >> 1) & (chunks - 1)));
+            const int pos = __shfl_sync(0xffffffffu, now.pos, i * chunks + ((lane >> 1) & (chunks - 1)));
+            if (lane < 2 * chunks && (lane & 1) == 0) x.pos[kt % kInfo][lane >> 1] = pos;
+            if (lane == 0) {
+              const uint32_t all = (1u << chunks) - 1u;
+              x.whole[kt % kInfo] = ((whole >> (i * chunks)) & all) == all;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(k_full + 8 * st, kTileBytes);
+            __syncwarp();
+            if (lane < 2 * chunks) {
+              // half of a chunk's columns: rows behind the pool's last read as zeros
+              const bool far = pos != INT_MAX && sl < 0;
+              const uint32_t dst = k0 + st * kTileBytes + (lane & 1) * kTileHalfBytes + (lane >> 1) * a.cs * 128;
+              tma_load_3d(dst, far ? &p.kst : &p.k, 64 * (lane & 1), 0,
+                          pos == INT_MAX ? (int)max((int64_t)1, a.hot_slots) : (far ? -sl - 1 : sl), k_full + 8 * st);
+            }
+          }
+          now = then;
+        }
+        next = (long long)__shfl_sync(0xffffffffu, ticket, 0) + cta;
+      }
+      // copies in flight are waited for before the CTA leaves
+      for (uint32_t i = kt >= kK ? kt - kK : 0; i < kt; ++i) mbar_wait(k_full + 8 * (i % kK), (i / kK) & 1u, a.status);
+    } else if (warp == 10) {
+      // ------------------------------------------------------------- Q's and V's tiles
+      const int64_t staged = staged_slots(a);
+      uint32_t vt = 0, nq = 0;
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        ok = wait_warp(item_full + 8 * (n & 1u), n >> 1);
+        if (!ok) break;
+        const Item &it = x.item[n & 1u];
+        const int unit = it.unit;
+        if (unit < 0) break;
+        const int nt = p.pairs == 2 ? max(it.c[0], it.c[1]) : it.c[0] + it.c[1];
+        const int64_t list = (int64_t)unit * a.umax;
+        const int j0 = it.j0, ents = it.ents, pos_max = it.pos_max, pos_min = it.pos_min;
+        const bool two = p.pairs == 2 && it.c[1] > 0;
+        auto batch = [&](int j) {
+          const int e = (j0 + j) * chunks + lane;
+          if (e >= ents) return Entry{0, INT_MAX};
+          if (a.union_idx[list + e] > pos_max / a.cs) return Entry{0, INT_MAX};
+          return load_entry(a, list, e, ents, staged);
+        };
+        Entry now = batch(0);
+        if (nt > 0) {
+          if (nq > 0) ok = wait_warp(q_free, nq - 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(q_full, (uint32_t)(rows_tile * 256 * (two ? 2 : 1)));
+          __syncwarp();
+          if (lane < (two ? 4 : 2))
+            tma_load_4d(q0 + (lane >> 1) * kTileBytes + (lane & 1) * kTileHalfBytes, &p.q, 64 * (lane & 1),
+                        unit % a.Hkv * a.G, it.t0 + (lane >> 1) * a.tt, unit / a.Hkv, q_full);
+          ++nq;
+        }
+        const int per = 32 / chunks;
+        for (int j = 0; ok && j < nt; j += per) {
+          Entry then = {0, INT_MAX};
+          if (j + per < nt) then = batch(j + per);
+          const uint32_t whole = __ballot_sync(0xffffffffu, now.pos != INT_MAX && now.pos <= pos_min - (a.cs - 1));
+          for (int i = 0; i < per && j + i < nt; ++i, ++vt) {
+            const uint32_t st = vt % kV;
+            if (vt >= kV) ok = wait_warp(v_free + 8 * st, vt / kV - 1);
+            if (!ok) break;
+            const int sl = __shfl_sync(0xffffffffu, now.slot, i * chunks + ((lane >> 1) & (chunks - 1)));
+            const int pos = __shfl_sync(0xffffffffu, now.pos, i * chunks + ((lane >> 1) & (chunks - 1)));
+            if (lane < 2 * chunks && (lane & 1) == 0) x.vpos[st][lane >> 1] = pos;
+            if (lane == 0) {
+              const uint32_t all = (1u << chunks) - 1u;
+              x.vwhole[st] = ((whole >> (i * chunks)) & all) == all;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(v_full + 8 * st, kTileBytes);
+            __syncwarp();
+            if (lane < 2 * chunks) {
+              const bool far = pos != INT_MAX && sl < 0;
+              const uint32_t dst = v0 + st * kTileBytes + (lane & 1) * kTileHalfBytes + (lane >> 1) * a.cs * 128;
+              tma_load_3d(dst, far ? &p.vst : &p.v, 64 * (lane & 1), 0,
+                          pos == INT_MAX ? (int)max((int64_t)1, a.hot_slots) : (far ? -sl - 1 : sl), v_full + 8 * st);
+            }
+          }
+          now = then;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_free + 8 * (n & 1u));
+      }
+      for (uint32_t i = vt >= kV ? vt - kV : 0; i < vt; ++i) mbar_wait(v_full + 8 * (i % kV), (i / kV) & 1u, a.status);
+      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1u, a.status);
+    } else if (warp == 8) {
+      // -------------------------------------------------------------------- products
+      // (the whole warp waits and counts, so that what the products are told is uniform)
+      constexpr uint32_t id_s = idesc_bf16(128, 128, 0, 0), id_o = idesc_bf16(128, 128, 0, 1);
+      const uint64_t q_desc = smem_desc_sw128(q0, 16, 1024), k_desc = smem_desc_sw128(k0, 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(v0, kTileHalfBytes, 1024);
+      uint32_t t_base = 0, nq = 0, np[2] = {0, 0};
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        ok = wait_warp(item_full + 8 * (n & 1u), n >> 1);
+        if (!ok) break;
+        const Item &it = x.item[n & 1u];
+        if (it.unit < 0) break;
+        const int c0 = it.c[0], c1 = it.c[1], steps = max(c0, c1);
+        const int nt = p.pairs == 2 ? steps : c0 + c1;
+        if (nt > 0) ok = wait_warp(q_full, nq++);
+        for (int i = 0; ok && i <= steps && nt > 0; ++i) {
+  #pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int cw = w ? c1 : c0;
+            if (!ok) break;
+            if (i > 0 && i - 1 < cw) {
+              const int tile = p.pairs == 2 ? i - 1 : 2 * (i - 1) + w;
+              const uint32_t t = t_base + tile, st = t % kV;
+              ok = wait_warp(v_ok + 8 * st, t / kV) && wait_warp(p_ready + 8 * w, np[w]);
+              ++np[w];
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_lane()) {
+                const uint64_t vb = v_desc + st * (kTileBytes / 16);
+  #pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                  tc_mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * ks, vb + ks * (16 * 128 / 16), id_o, i > 1 || ks > 0);
+                if (p.pairs == 1 || w == 1 || i - 1 >= c1) tc_commit(v_free + 8 * st);
+                if (i == cw) tc_commit(o_full + 8 * w);
+              }
+              __syncwarp();
+            }
+            if (i < cw) {
+              const int tile = p.pairs == 2 ? i : 2 * i + w;
+              const uint32_t t = t_base + tile, st = t % kK;
+              ok = wait_warp(k_full + 8 * st, t / kK);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_lane()) {
+                const uint64_t qb = q_desc + (p.pairs == 2 ? w * (kTileBytes / 16) : 0);
+                const uint64_t kb = k_desc + st * (kTileBytes / 16);
+  #pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                  const uint32_t off = ((ks >> 2) * kTileHalfBytes + (ks & 3) * 32) / 16;
+                  tc_mma(tmem + 128 * w, qb + off, kb + off, id_s, ks > 0);
+                }
+                mbar_arrive(s_full + 8 * w);     // (hands on the tile's record, which came with K)
+                tc_commit(s_full + 8 * w);
+                if (p.pairs == 1 || w == 1 || i >= c1) tc_commit(k_free + 8 * st);
+                if (tile == nt - 1 && (p.pairs == 1 || w == 1 || i >= c1)) tc_commit(q_free);
+              }
+              __syncwarp();
+            }
+          }
+        }
+        t_base += nt;
+        if (lane == 0) mbar_arrive(item_free + 8 * (n & 1u));
+      }
+      // every product issued is done before the tensor memory is freed
+      if (elect_lane()) tc_commit(mma_done);
+      __syncwarp();
+      mbar_wait(mma_done, 0, a.status);
+    } else if (warp == 11) {
+      // -------------------------------------------- V's tiles that are not seen whole
+      uint32_t vt = 0;
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        ok = wait_warp(item_full + 8 * (n & 1u), n >> 1);
+        if (!ok) break;
+        const Item &it = x.item[n & 1u];
+        if (it.unit < 0) break;
+        const int nt = p.pairs == 2 ? max(it.c[0], it.c[1]) : it.c[0] + it.c[1];
+        bool found = false;
+        for (int j = 0; ok && j < nt; ++j, ++vt) {
+          const uint32_t st = vt % kV;
+          ok = wait_warp(v_full + 8 * st, vt / kV);
+          if (!ok) break;
+          if (!x.vwhole[st]) {
+            for (int e = lane; e < kTileBytes / 16; e += 32) {
+              const uint32_t at = v0 + st * kTileBytes + e * 16;
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+              uint32_t hit = 0;
+  #pragma unroll
+              for (int k = 0; k < 4; ++k) hit |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+              const uint32_t any = __ballot_sync(0xffffffffu, hit != 0u);
+              if (any == 0u) continue;
+              if (!found) {
+                // the records are the item's: the one before has used its own
+                found = true;
+                if (n > 0) ok = wait_warp(item_free + 8 * ((n - 1) & 1u), (n - 1) >> 1);
+                for (int k = lane; k < 3 * 128; k += 32) (&x.bad[0][0])[k] = INT_MAX;
+                if (lane == 0) x.bad_item = (int)n;
+                __syncwarp();
+              }
+              if (hit) {
+                const int row = (e & 1023) >> 3, col0 = (e >> 10) * 64 + (((e & 7) ^ (row & 7)) << 3);
+                const int first = x.vpos[st][row / a.cs], pos = first == INT_MAX ? INT_MAX : first + row % a.cs;
+  #pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const uint32_t v = (w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
+                  if ((v & 0x7F80u) == 0x7F80u) {
+                    const int kind = (v & 0x7Fu) ? 0 : ((v & 0x8000u) ? 2 : 1);
+                    atomicMin(&x.bad[kind][col0 + k], pos);
+                    w[k >> 1] &= (k & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+                  }
+                }
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+              }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_ok + 8 * st);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          __threadfence_block();
+          mbar_arrive(looked + 8 * (n & 1u));
+          mbar_arrive(item_free + 8 * (n & 1u));
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ---------------------------------------------------------------------- softmax
+    const int w = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;
+    const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+    const uint32_t s_at = tmem + lane_base + 128 * w, o_at = tmem + lane_base + 256 + 128 * w;
+    const int tok = r / a.G, head = r % a.G;
+    const bool some = 32 * quarter < rows_tile;            // of this warp's rows are query rows
+    uint32_t ns = 0, no = 0, n_joined = 0, t_base = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok && !pending; ++n) {
+      ok = wait_warp(item_full + 8 * (n & 1u), n >> 1);
+      if (!ok) break;
+      const Item &it = x.item[n & 1u];
+      const int unit = it.unit;
+      if (unit < 0) break;
+      const int cw = it.c[w], parts = it.parts[w];
+      const int nt = p.pairs == 2 ? max(it.c[0], it.c[1]) : it.c[0] + it.c[1];
+      const int token = it.t0 + (p.pairs == 2 ? w * a.tt : 0) + tok;
+      const bool valid = r < rows_tile && token < it.len;
+      const int pos = valid ? it.start + token : -1;
+      float m = -INFINITY, l = 0.f;                        // reference (a score before the factor), sum of weights
+      for (int i = 0; i < cw; ++i) {
+        const uint32_t t = t_base + (p.pairs == 2 ? i : 2 * i + w);
+        ok = wait_warp(s_full + 8 * w, ns);
+        ++ns;
+        if (!ok) break;
+        tc_fence_after();
+        if (some) {
+          float s[128];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) tmem_ld32(s_at + 32 * h, s + 32 * h);
+          tmem_wait_ld();
+          if (!x.whole[t % kInfo]) {
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+              const int row0 = 16 * h, first = x.pos[t % kInfo][row0 / a.cs];
+              // columns up to `lim` are seen
+              const int lim = first == INT_MAX ? -1 : pos - first - row0 % a.cs;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (e > lim) s[16 * h + e] = -INFINITY;
+            }
+          }
+          float m8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m8[e] = fmaxf(s[e], s[e + 8]);
+#pragma unroll
+          for (int h = 16; h < 128; h += 16)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], fmaxf(s[h + e], s[h + e + 8]));
+          const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                 fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+          // (also from -inf; not where both are; rows that are none hold anything and have no say)
+          const bool up = valid && (mx - m) * a.sl2 > kHead;
+          if (__any_sync(0xffffffffu, up)) {
+            const float f = up ? exp2_fast((m - mx) * a.sl2) : 1.f;
+            if (up) m = mx;
+            l *= f;
+            if (i > 0) {
+              // S(t) is there, so the product before it is done with O
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                float o[32];
+                tmem_ld32(o_at + 32 * h, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= f;
+                tmem_st32(o_at + 32 * h, o);
+              }
+              tmem_wait_st();
+            }
+          }
+          // weights 2^(s sl2 - m sl2): one rounding, of a number near 0 or one that gives no weight; scores so
+          // large that m sl2 itself is rounded by more than 2^-8 are taken from the reference first
+          const float ref = m == -INFINITY ? 0.f : m;
+          float mul = a.sl2, sub = -ref * a.sl2;
+          if (__any_sync(0xffffffffu, valid && !(fabsf(sub) <= 65536.f))) {
+#pragma unroll
+            for (int e = 0; e < 128; ++e) s[e] -= ref;
+            sub = 0.f;
+          }
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 y = fma2(make_float2(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), make_float2(mul, mul),
+                              make_float2(sub, sub));
+              y.x = exp2_fast(y.x), y.y = exp2_fast(y.y);
+              sum[e & 1] = add2(sum[e & 1], y);
+              pk[e] = bf16x2(y.x, y.y);
+            }
+            tmem_st16(s_at + 16 * h, pk);
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready + 8 * w);
+      }
+      if (!ok) break;
+      t_base += nt;
+
+      // ------------------------------------------------------------ the item's sums
+      ok = wait_warp(looked + 8 * (n & 1u), n >> 1);
+      if (!ok) break;
+      if (cw > 0) {
+        ok = wait_warp(o_full + 8 * w, no++);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (parts > 0) {
+        const bool direct = parts == 1 && !it.local;
+        const bool bad = x.bad_item == (int)n;
+        const int b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
+        const int64_t slot = it.local ? p.slots + 4 * blockIdx.x + 2 * (n & 1u) + w : it.part[w];
+        float *po = p.part_o + (slot * rows_tile + r) * kD;
+        const int64_t row = ((int64_t)b * a.T + token) * a.Hq + h0 + head;
+        uint16_t *dst = p.out + b * p.os[0] + token * p.os[1] + (h0 + head) * p.os[2];
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (some) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            float o[32];
+            if (cw > 0) {
+              tmem_ld32(o_at + 32 * h, o);
+              tmem_wait_ld();
+            }
+            if (cw == 0 || l == 0.f) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            }
+            if (bad) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                if (x.bad[0][32 * h + e] <= pos) o[e] = NAN;
+                if (x.bad[1][32 * h + e] <= pos) o[e] += INFINITY;
+                if (x.bad[2][32 * h + e] <= pos) o[e] -= INFINITY;
+              }
+            }
+            if (valid) {
+              if (direct) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  uint4 v;
+                  v.x = bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), v.y = bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
+                  v.z = bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), v.w = bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
+                  *reinterpret_cast<uint4 *>(dst + 32 * h + 8 * e) = v;
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  *reinterpret_cast<float4 *>(po + 32 * h + 4 * e) =
+                      make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              }
+            }
+          }
+          if (valid) {
+            if (direct) {
+              if (p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m == -INFINITY ? NAN : m * a.scale + logf(l));
+            } else {
+              p.part_ml[slot * rows_tile + r] = make_float2(m, l);
+            }
+          }
+        }
+        tc_fence_before();        // O is read before the next item's first product overwrites it
+
+        bool join = false;
+        int join_w = quarter, join_n = 4, n_parts = parts, stride = p.pairs;
+        int64_t first = it.part0[w];
+        if (it.local) {
+          // both streams' sums are in place: their warps share the rows
+          __threadfence_block();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(joined);
+          join = true;
+          first = p.slots + 4 * blockIdx.x + 2 * (n & 1u), n_parts = 2, stride = 1;
+          join_w = warp, join_n = 8;
+        } else if (parts > 1) {
+          const int arrivals = parts;
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+          if (quarter == 0 && lane == 0) {
+            __threadfence();
+            x.last[w] = atomicAdd(p.w.ctr + 2 + it.cut[w], 1) == arrivals - 1;
+            __threadfence();
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+          join = x.last[w] != 0;
+        }
+        if (join) {
+          if (it.local) {
+            ok = wait_warp(joined, n_joined++);
+            if (!ok) break;
+          }
+          const int t_first = it.t0 + (p.pairs == 2 ? w * a.tt : 0);
+          const int rows = min(rows_tile, (it.len - t_first) * a.G);
+          for (int k = join_w; k < rows; k += join_n) {
+            float top = -INFINITY;
+            for (int q = lane; q < n_parts; q += 32) top = fmaxf(top, __ldcg(&p.part_ml[(first + q * stride) * rows_tile + k]).x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float ref = top == -INFINITY ? 0.f : top;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float total = 0.f;
+            for (int q0 = 0; q0 < n_parts; q0 += 32) {
+              float f = 0.f, lq = 0.f;
+              if (q0 + lane < n_parts) {
+                const float2 ml = __ldcg(&p.part_ml[(first + (int64_t)(q0 + lane) * stride) * rows_tile + k]);
+                f = exp2_fast((ml.x - ref) * a.sl2), lq = ml.y;
+              }
+              const int nq = min(32, n_parts - q0);
+#pragma unroll 4
+              for (int q = 0; q < nq; ++q) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                    p.part_o + ((first + (int64_t)(q0 + q) * stride) * rows_tile + k) * kD + 4 * lane));
+                const float fq = __shfl_sync(0xffffffffu, f, q), l1 = __shfl_sync(0xffffffffu, lq, q);
+                if (l1 == 0.f) continue;                   // a part without keys
+                total += fq * l1;
+                acc.x += fq * v.x, acc.y += fq * v.y, acc.z += fq * v.z, acc.w += fq * v.w;
+              }
+            }
+            const float inv1 = total == 0.f ? 0.f : 1.f / total;
+            const int kt2 = t_first + k / a.G, kh = h0 + k % a.G;
+            *reinterpret_cast<uint2 *>(p.out + b * p.os[0] + kt2 * p.os[1] + kh * p.os[2] + 4 * lane) =
+                make_uint2(bf16x2(acc.x * inv1, acc.y * inv1), bf16x2(acc.z * inv1, acc.w * inv1));
+            if (p.lse && lane == 0)
+              p.lse[((int64_t)b * a.T + kt2) * a.Hq + kh] =
+                  total == 0.f ? -INFINITY : (top == -INFINITY ? NAN : top * a.scale + logf(total));
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_free + 8 * (n & 1u));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+  }
+  if (tid == 0) leave_counters(p.w);
+}
+
+struct Shape {
+  int tt, pairs, mt, rows;
+  int64_t slots, own;
+};
+
+Shape shape_of(int B, int T, int G, int Hkv, int cta) {
+  Shape s;
+  s.tt = T < 128 / G ? T : 128 / G;
+  s.pairs = T > s.tt ? 2 : 1;
+  s.mt = s.pairs * s.tt;
+  s.rows = s.tt * G;
+  s.slots = 12 * (int64_t)cta;
+  s.own = s.pairs == 1 ? 4 * (int64_t)cta : 0;
+  (void)B, (void)Hkv;
+  return s;
+}
+
+}  // namespace
+
+int64_t extend_workspace(int B, int T, int Hq, int Hkv, int sm_count) {
+  if (B == 0 || T == 0) return 0;
+  const Shape s = shape_of(B, T, Hq / Hkv, Hkv, sm_count);
+  return (s.slots + s.own) * s.rows * (kD + 2) * 4;
+}
+
+cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t stream) {
+  const PagesArgs &a = e.p;
+  const Shape s = shape_of(a.B, a.T, a.G, a.Hkv, e.sm_count);
+  ExtendParams p{};
+  p.a = a;
+  p.a.tt = s.tt;
+  const bool hot = a.hot_slots > 0, far = a.max_misses > 0;
+  if (!make_rows_map(&p.q, e.q, e.q_stride, a.B, a.T, a.Hq, a.G, s.tt) ||
+      !make_pages_map(&p.k, hot ? e.Khot : e.dummy, hot ? a.hot_slots : 1, a.cs) ||
+      !make_pages_map(&p.v, hot ? e.Vhot : e.dummy, hot ? a.hot_slots : 1, a.cs) ||
+      !make_pages_map(&p.kst, far ? e.Kst : e.dummy, far ? a.max_misses : 1, a.cs) ||
+      !make_pages_map(&p.vst, far ? e.Vst : e.dummy, far ? a.max_misses : 1, a.cs))
+    return cudaErrorInvalidValue;
+  p.out = static_cast<uint16_t *>(e.out);
+  for (int i = 0; i < 3; ++i) p.os[i] = e.out_stride[i];
+  p.lse = e.lse;
+  p.slots = s.slots;
+  p.part_o = e.parts;
+  p.part_ml = reinterpret_cast<float2 *>(e.parts + (s.slots + s.own) * s.rows * kD);
+  p.w = {e.ctr, kCtrPerCta * e.sm_count};
+  p.mt = s.mt, p.pairs = s.pairs;
+  cudaError_t r = set_dyn_smem((const void *)k_extend, kSmem);
+  if (r != cudaSuccess) return r;
+  return launch_k(k_extend, dim3(e.sm_count), dim3(kThreads), kSmem, stream, p);
+}
+
+}  // namespace dd

@@ -1,7 +1,7 @@
 // Host side of the TMA tensor maps the attention and scoring kernels read.
 #include <mutex>
 
-#include "dd_tc.cuh"
+#include "dd_pages.cuh"
 
 namespace dd {
 
@@ -95,6 +95,33 @@ bool make_q_map(CUtensorMap *map, const void *q, int B, int n_q, int Hq, int G) 
   next = (next + 1) % 16;
   if (n < 16) ++n;
   return true;
+}
+
+// The maps of the kernels over paged caches are made anew for every call (some 100 ns each).
+bool make_pages_map(CUtensorMap *map, const void *base, int64_t slots, int cs) {
+  auto enc = tensor_map_encoder();
+  if (!enc || base == nullptr || slots <= 0) return false;
+  cuuint64_t dims[3] = {128, (cuuint64_t)cs, (cuuint64_t)slots};
+  cuuint64_t strides[2] = {256, (cuuint64_t)cs * 256};
+  cuuint32_t box[3] = {64, (cuuint32_t)cs, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_rows_map(CUtensorMap *map, const void *q, const int64_t *stride, int B, int T, int Hq, int G, int tt) {
+  auto enc = tensor_map_encoder();
+  if (!enc || q == nullptr) return false;
+  // a dimension of one is never stepped over: any stride does
+  cuuint64_t dims[4] = {128, (cuuint64_t)Hq, (cuuint64_t)T, (cuuint64_t)B};
+  cuuint64_t strides[3] = {Hq > 1 ? (cuuint64_t)stride[2] * 2 : 256, T > 1 ? (cuuint64_t)stride[1] * 2 : 256,
+                           B > 1 ? (cuuint64_t)stride[0] * 2 : 256};
+  cuuint32_t box[4] = {64, (cuuint32_t)G, (cuuint32_t)tt, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace dd

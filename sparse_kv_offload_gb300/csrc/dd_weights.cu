@@ -1,0 +1,501 @@
+// The attention weight that each listed chunk has gathered from new tokens:
+//   weight[b,g,c] = decay * weight[b,g,c] + sum over tokens t, heads h of KV head g, rows i of
+//                   chunk c that t sees:  exp(scale q_{t,h}.k_i - lse_{t,h}),
+// lse as the attention of these tokens has left it.  One product and one exponential a pair, no
+// second product: half of the attention's operations, and K read once.
+//
+// The product is turned round, S = K Q^T with 128 keys on the rows of tensor memory, so that a
+// thread owns a key and its sum over the query rows stays in a register; only a chunk's rows
+// are added up across lanes.  With queries on the rows every tile would need 128 column sums.
+// Sums are fp32, in an order that depends on the sizes alone (no atomics on values).
+//   warps 0-3, 4-7  exponentials and sums of a pair's two tiles of 128 keys
+//   warp 8          the products, two of each tile on the way in tensor memory
+//   warp 9          hands out the work and brings K's tiles (two pairs on the way)
+//   warp 10         Q's tiles (three on the way), warp 11 their log-sum-exps
+//
+// An item is a run of pairs of tiles by a range of the query rows' tiles.  With few query rows (one
+// tile) the keys stream past the queries and an item is several pairs; with many, the queries
+// stream past a pair.  Where the pairs alone would leave CTAs idle the rows are cut too, and
+// a pair's parts (16 sums at most) are added up in order by whoever finishes last.
+#include "dd_pages.cuh"
+
+namespace dd {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kQ = 3;                                // tiles of queries on the way
+constexpr int kPair = 2;                             // pairs of tiles of keys on the way
+constexpr uint32_t kTmem = 512;                      // S: two of 128 columns for each tile of a pair
+constexpr int kItemsPerCta = 8, kMaxRun = 16;
+
+struct Pair {
+  int unit, start, len;
+  int tok0;                   // the first token that counts
+  int r0, r1;                 // tiles of query rows to go through
+  int keep_q;                 // one tile of queries for all pairs of the item: 1 first, 2 last, 3 both, 4 neither, 0 no
+  int parts, part0, part, cut;   // ranges of rows, slots, arrival counter
+  int pos[16];                // positions of the first rows of its chunks, INT_MAX where there is none
+};
+
+struct Misc {
+  uint64_t bars[40];
+  Pair pair[kPair];
+  alignas(16) float lse[kQ][128];   // times log2 e; +inf where there is no row
+  float sum[2][2][8];                // [buffer][stream][16 rows]
+  int dead, pending;
+  uint32_t tmem;
+};
+
+constexpr size_t kTiles = (size_t)(kQ + 2 * kPair) * kTileBytes;
+constexpr size_t kSmem = kTiles + sizeof(Misc);
+static_assert(kSmem <= 232448, "shared memory of a CTA");
+
+struct WeightsParams {
+  CUtensorMap q, k, kst;
+  PagesArgs a;
+  const float *lse;
+  float *weight;
+  int window;
+  float decay;
+  float *parts;               // [slots][16]
+  WorkCounters w;
+};
+
+struct Unit {
+  int cnt, start, len, tok0, pairs, rows;     // pairs of tiles of keys, tiles of query rows
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ Unit load_unit(const WeightsParams &p, int u) {
+  Unit r;
+  const Request q = load_request(p.a, u / p.a.Hkv);
+  r.cnt = load_count(p.a, u);
+  r.start = q.start, r.len = q.len;
+  r.tok0 = p.window > 0 ? max(0, q.len - p.window) : 0;
+  r.pairs = ceil_div(r.cnt * p.a.cs, 2 * kTileKeys);
+  r.rows = max(1, ceil_div(q.len - r.tok0, p.a.tt));       // (without tokens the weights still decay)
+  return r;
+}
+
+// Pairs of an item and tiles of rows of an item.  With P CTAs: pairs whose rows are cut <= 8 P, items of
+// those <= 16 P.
+struct Cut {
+  int run, rows;
+};
+__device__ __forceinline__ Cut cut_of(long long pairs, long long work, bool one, int cta) {
+  if (one) return {(int)max(1ll, min((long long)kMaxRun, pairs / (4ll * cta))), INT_MAX};
+  if (pairs >= (long long)kItemsPerCta * cta) return {1, INT_MAX};
+  return {1, (int)max(1ll, (work + (long long)kItemsPerCta * cta - 1) / ((long long)kItemsPerCta * cta))};
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__ WeightsParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Misc &x = *reinterpret_cast<Misc *>(smem + kTiles);
+  const PagesArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t q0 = smem_u32(smem), k0 = q0 + kQ * kTileBytes;
+  const uint32_t bars = smem_u32(x.bars);
+  const uint32_t pair_full = bars, pair_free = pair_full + 8 * kPair, k_free = pair_free + 8 * kPair,
+                 q_full = k_free + 8 * kPair, q_free = q_full + 8 * kQ, s_full = q_free + 8 * kQ, s_free = s_full + 32,
+                 mma_done = s_free + 32;
+  if (tid == 0) {
+    // a pair: its record and its tiles; free again after the products (tiles) and the sums (record)
+    for (int i = 0; i < kPair; ++i) mbar_init(pair_full + 8 * i, 1), mbar_init(pair_free + 8 * i, 11), mbar_init(k_free + 8 * i, 1);
+    // a tile of queries: its copy and its log-sum-exps; free after the products and the sums
+    for (int i = 0; i < kQ; ++i) mbar_init(q_full + 8 * i, 2), mbar_init(q_free + 8 * i, 9);
+    for (int i = 0; i < 4; ++i) mbar_init(s_full + 8 * i, 2), mbar_init(s_free + 8 * i, 4);
+    mbar_init(mma_done, 1);
+    x.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&x.tmem)), "r"(kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  const int rows_tile = a.tt * a.G, chunks = kTileKeys / a.cs;
+  // query rows behind a tile's last are never written: zeros once, and every column of S is a number
+  for (int i = 0; i < kQ; ++i)
+    for (int e = tid; e < 2 * (128 - rows_tile) * 8; e += kThreads) {
+      const int half = e / ((128 - rows_tile) * 8), rest = e % ((128 - rows_tile) * 8);
+      *reinterpret_cast<uint4 *>(smem + i * kTileBytes + half * kTileHalfBytes + rows_tile * 128 + rest * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  tc_fence_before();
+  pdl_wait();
+  pdl_trigger();
+  if (tid == 0) x.pending = load_status(a.status);
+  __syncthreads();
+  tc_fence_after();
+  const bool pending = x.pending != 0;
+  const uint32_t tmem = x.tmem;
+
+  volatile int *dead = &x.dead;
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity & 1u)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+      if (mbar_try_wait(bar, parity & 1u)) return true;
+      if ((it & 63u) == 0) {
+        if (*dead) return false;
+        if (globaltimer_ns() - t0 > 2000000000ull) {
+          *dead = 1;
+          set_status(a.status, DD_ERR_TIMEOUT);
+          return false;
+        }
+      }
+    }
+  };
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, wait(bar, parity));
+  };
+  // whether a step of a pair takes a new tile of queries, and whether it is the tile's last
+  auto new_q = [](int keep) { return keep == 0 || (keep & 1); };
+  auto last_q = [](int keep) { return keep == 0 || keep == 2 || keep == 3; };
+
+  if (pending) {
+    // no work; the counters below are left all the same
+  } else if (warp == 9) {
+    // ------------------------------------------------------- the work, and K's tiles
+    const int units = a.B * a.Hkv, cta = (int)gridDim.x;
+    long long pairs = 0, work = 0;
+    bool one = true;
+    for (int u = lane; u < units; u += 32) {
+      const Unit r = load_unit(p, u);
+      pairs += r.pairs;
+      work += (long long)r.pairs * r.rows;
+      one = one && r.rows == 1;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+      work += __shfl_xor_sync(0xffffffffu, work, o);
+    }
+    one = __all_sync(0xffffffffu, one);
+    const Cut cut = cut_of(pairs, work, one, cta);
+    const int64_t staged = staged_slots(a);
+
+    int base_u = -32;
+    long long items_before = 0, items_here = 0;
+    int cuts_before = 0, cuts_here = 0, parts_before = 0, parts_here = 0;
+    Unit mine = {0, 0, 0, 0, 0, 0};
+    int runs = 0, ranges = 0, items = 0, items_pre = 0, cuts_pre = 0, parts_pre = 0;
+    long long next = blockIdx.x;
+    uint32_t n = 0;                                        // pairs so far
+    bool ok = true;
+    for (;;) {
+      const long long want = next;
+      int ticket = 0;
+      if (lane == 0) ticket = atomicAdd(p.w.ctr, 1);
+      while (base_u + 32 < units && want >= items_before + items_here) {
+        items_before += items_here, cuts_before += cuts_here, parts_before += parts_here;
+        base_u += 32;
+        mine = {0, 0, 0, 0, 0, 0};
+        if (base_u + lane < units) mine = load_unit(p, base_u + lane);
+        runs = ceil_div(mine.pairs, cut.run);
+        ranges = mine.rows ? (cut.rows >= mine.rows ? 1 : ceil_div(mine.rows, cut.rows)) : 0;
+        items = runs * ranges;
+        const int cuts = ranges > 1 ? mine.pairs : 0, parts = cuts * ranges;
+        items_pre = warp_incl_scan(items), cuts_pre = warp_incl_scan(cuts), parts_pre = warp_incl_scan(parts);
+        items_here = __shfl_sync(0xffffffffu, items_pre, 31);
+        cuts_here = __shfl_sync(0xffffffffu, cuts_pre, 31);
+        parts_here = __shfl_sync(0xffffffffu, parts_pre, 31);
+        items_pre -= items, cuts_pre -= cuts, parts_pre -= parts;
+      }
+      if (want >= items_before + items_here) break;
+      const int here = (int)(want - items_before);
+      const int src = __ffs((int)__ballot_sync(0xffffffffu, items_pre <= here && here < items_pre + items)) - 1;
+      Unit u;
+      u.cnt = __shfl_sync(0xffffffffu, mine.cnt, src), u.start = __shfl_sync(0xffffffffu, mine.start, src);
+      u.len = __shfl_sync(0xffffffffu, mine.len, src), u.tok0 = __shfl_sync(0xffffffffu, mine.tok0, src);
+      u.pairs = __shfl_sync(0xffffffffu, mine.pairs, src), u.rows = __shfl_sync(0xffffffffu, mine.rows, src);
+      const int n_runs = __shfl_sync(0xffffffffu, runs, src), n_ranges = __shfl_sync(0xffffffffu, ranges, src);
+      const int cut0 = cuts_before + __shfl_sync(0xffffffffu, cuts_pre, src);
+      const int part0 = parts_before + __shfl_sync(0xffffffffu, parts_pre, src);
+      const int rem = here - __shfl_sync(0xffffffffu, items_pre, src);
+      const int range = rem / n_runs, run = rem % n_runs;
+      const int p0 = run * cut.run, p1 = min(u.pairs, p0 + cut.run);
+      const int range0 = n_ranges > 1 ? range * cut.rows : 0;
+      const int range1 = n_ranges > 1 ? min(u.rows, range0 + cut.rows) : u.rows;
+      const int unit = base_u + src;
+      const int64_t list = (int64_t)unit * a.umax;
+      const bool keep = one && u.len > u.tok0;
+      // the entries of a pair, one a lane; those of the next pair are loaded behind this one's copies
+      auto entry = [&](int pr) {
+        const int e = pr * 2 * chunks + lane;
+        return lane < 2 * chunks && pr < p1 ? load_entry(a, list, e, u.cnt, staged) : Entry{0, INT_MAX};
+      };
+      Entry now = entry(p0);
+      for (int pr = p0; pr < p1; ++pr, ++n) {
+        const Entry then = entry(pr + 1);
+        const uint32_t st = n % kPair;
+        if (n >= kPair) ok = wait_warp(pair_free + 8 * st, n / kPair - 1) && wait_warp(k_free + 8 * st, n / kPair - 1);
+        if (!ok) break;
+        Pair &r = x.pair[st];
+        // tokens before the pair's first row see none of it
+        const int first = __reduce_min_sync(0xffffffffu, now.pos);
+        const int from = first == INT_MAX ? INT_MAX : max(0, first - u.start - u.tok0) / a.tt;
+        if (lane < 2 * chunks) r.pos[lane] = now.pos;
+        if (lane == 0) {
+          r.unit = unit, r.start = u.start, r.len = u.len, r.tok0 = u.tok0;
+          r.r0 = keep ? 0 : min(max(range0, from), range1);
+          r.r1 = u.len > u.tok0 ? range1 : r.r0;
+          r.keep_q = keep ? (pr == p0 ? (pr == p1 - 1 ? 3 : 1) : (pr == p1 - 1 ? 2 : 4)) : 0;
+          r.parts = n_ranges, r.part0 = part0 + pr * n_ranges, r.part = part0 + pr * n_ranges + range;
+          r.cut = 2 * (cut0 + pr);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(pair_full + 8 * st, 2 * kTileBytes);
+        __syncwarp();
+        // a lane: half of the columns of one of the 2 * chunks chunks
+        const int ch = lane >> 1, sl = __shfl_sync(0xffffffffu, now.slot, ch), pos = __shfl_sync(0xffffffffu, now.pos, ch);
+        if (ch < 2 * chunks) {
+          const bool far = pos != INT_MAX && sl < 0;
+          const uint32_t dst = k0 + (st * 2 + ch / chunks) * kTileBytes + (lane & 1) * kTileHalfBytes + ch % chunks * a.cs * 128;
+          tma_load_3d(dst, far ? &p.kst : &p.k, 64 * (lane & 1), 0,
+                      pos == INT_MAX ? (int)max((int64_t)1, a.hot_slots) : (far ? -sl - 1 : sl), pair_full + 8 * st);
+        }
+        now = then;
+      }
+      if (!ok) break;
+      next = (long long)__shfl_sync(0xffffffffu, ticket, 0) + cta;
+    }
+    if (ok) {
+      const uint32_t st = n % kPair;
+      if (n >= kPair) ok = wait_warp(pair_free + 8 * st, n / kPair - 1) && wait_warp(k_free + 8 * st, n / kPair - 1);
+      if (ok && lane == 0) {
+        x.pair[st].unit = -1;
+        mbar_arrive(pair_full + 8 * st);
+      }
+    }
+    // copies in flight are waited for before the CTA leaves (with the last record sent, those of
+    // the pair that had its place before are done with)
+    for (uint32_t i = n >= kPair ? n - kPair + (ok ? 1 : 0) : 0; i < n; ++i)
+      mbar_wait(pair_full + 8 * (i % kPair), (i / kPair) & 1u, a.status);
+  } else if (warp == 10 || warp == 11) {
+    // ------------------------------------------- Q's tiles, and their log-sum-exps
+    uint32_t nq = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      const uint32_t st = n % kPair;
+      ok = wait_warp(pair_full + 8 * st, n / kPair);
+      if (!ok) break;
+      const Pair &r = x.pair[st];
+      const int unit = r.unit;
+      if (unit < 0) break;
+      const int r1 = r.r1, tok0 = r.tok0, len = r.len, b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
+      if (new_q(r.keep_q)) {
+        for (int t = r.r0; t < r1; ++t, ++nq) {
+          const uint32_t sq = nq % kQ;
+          if (nq >= kQ) ok = wait_warp(q_free + 8 * sq, nq / kQ - 1);
+          if (!ok) break;
+          const int first = tok0 + t * a.tt;
+          if (warp == 10) {
+            if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * sq, (uint32_t)(rows_tile * 256));
+            __syncwarp();
+            if (lane < 2) tma_load_4d(q0 + sq * kTileBytes + lane * kTileHalfBytes, &p.q, 64 * lane, h0, first, b, q_full + 8 * sq);
+          } else {
+#pragma unroll
+            for (int e = lane; e < 128; e += 32) {
+              float v = INFINITY;                          // no row: weight 2^-inf
+              if (e < rows_tile && first + e / a.G < len) {
+                v = p.lse[((int64_t)b * a.T + first + e / a.G) * a.Hq + h0 + e % a.G];
+                v = v == -INFINITY ? INFINITY : v * 1.4426950408889634f;   // a row without keys has no weights
+              }
+              x.lse[sq][e] = v;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + 8 * sq);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_free + 8 * st);
+    }
+    if (warp == 10)
+      for (uint32_t i = nq >= kQ ? nq - kQ : 0; i < nq; ++i) mbar_wait(q_full + 8 * (i % kQ), (i / kQ) & 1u, a.status);
+  } else if (warp == 8) {
+    // -------------------------------------------------------------------- products
+    const uint32_t id = idesc_bf16(128, (rows_tile + 31) / 32 * 32, 0, 0);   // (as many columns as are read)
+    const uint64_t q_desc = smem_desc_sw128(q0, 16, 1024), k_desc = smem_desc_sw128(k0, 16, 1024);
+    uint32_t nq = 0, ns = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      const uint32_t st = n % kPair;
+      ok = wait_warp(pair_full + 8 * st, n / kPair);
+      if (!ok) break;
+      const Pair &r = x.pair[st];
+      if (r.unit < 0) break;
+      const int r1 = r.r1, keep = r.keep_q;
+      for (int t = r.r0; t < r1; ++t, ++ns) {
+        if (new_q(keep)) ok = wait_warp(q_full + 8 * (nq % kQ), nq / kQ);
+        if (!ok) break;
+        const uint32_t sq = nq % kQ, buf = ns & 1u;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (ns >= 2) ok = wait_warp(s_free + 8 * (2 * w + buf), (ns >> 1) - 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_lane()) {
+            const uint64_t qb = q_desc + sq * (kTileBytes / 16), kb = k_desc + (st * 2 + w) * (kTileBytes / 16);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint32_t off = ((ks >> 2) * kTileHalfBytes + (ks & 3) * 32) / 16;
+              tc_mma(tmem + 256 * w + 128 * buf, kb + off, qb + off, id, ks > 0);
+            }
+            mbar_arrive(s_full + 8 * (2 * w + buf));       // (hands on the pair's and the queries' records)
+            tc_commit(s_full + 8 * (2 * w + buf));
+            if (w == 1 && last_q(keep)) tc_commit(q_free + 8 * sq);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (last_q(keep)) ++nq;
+      }
+      if (!ok) break;
+      if (elect_lane()) tc_commit(k_free + 8 * st);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_free + 8 * st);
+    }
+    if (elect_lane()) tc_commit(mma_done);
+    __syncwarp();
+    mbar_wait(mma_done, 0, a.status);
+  } else {
+    // ------------------------------------------------------- exponentials and sums
+    const int w = warp >> 2, quarter = warp & 3, key = 32 * quarter + lane;
+    const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+    uint32_t nq = 0, ns = 0;
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      const uint32_t st = n % kPair;
+      ok = wait_warp(pair_full + 8 * st, n / kPair);
+      if (!ok) break;
+      const Pair &r = x.pair[st];
+      const int unit = r.unit;
+      if (unit < 0) break;
+      const int r0 = r.r0, r1 = r.r1, keep = r.keep_q;
+      const int first = r.pos[w * chunks + key / a.cs], pos = first == INT_MAX ? INT_MAX : first + key % a.cs;
+      float total = 0.f;
+      for (int t = r0; t < r1; ++t, ++ns) {
+        const uint32_t sq = nq % kQ, buf = ns & 1u;
+        ok = wait_warp(s_full + 8 * (2 * w + buf), ns >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        const int tok = r.tok0 + t * a.tt;                 // of the tile's first row
+        const int cols = min(rows_tile, (r.len - tok) * a.G);
+        // columns of tokens at or behind the key's position; S of the others may be anything
+        const int lo = pos == INT_MAX ? 128 : (int)min((int64_t)128, max((int64_t)0, (int64_t)(pos - r.start - tok) * a.G));
+        const bool whole = __all_sync(0xffffffffu, lo == 0 && cols == rows_tile);
+        const float *ls = x.lse[sq];
+        const uint32_t at = tmem + lane_base + 256 * w + 128 * buf;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          if (32 * h >= cols) break;
+          float s[32];
+          tmem_ld32(at + 32 * h, s);
+          tmem_wait_ld();
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 z = *reinterpret_cast<const float4 *>(ls + 32 * h + 4 * e);
+              float2 y0 = fma2(make_float2(s[4 * e], s[4 * e + 1]), make_float2(a.sl2, a.sl2), make_float2(-z.x, -z.y));
+              float2 y1 = fma2(make_float2(s[4 * e + 2], s[4 * e + 3]), make_float2(a.sl2, a.sl2), make_float2(-z.z, -z.w));
+              y0.x = exp2_fast(y0.x), y0.y = exp2_fast(y0.y), y1.x = exp2_fast(y1.x), y1.y = exp2_fast(y1.y);
+              sum[0] = add2(sum[0], y0), sum[1] = add2(sum[1], y1);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int c = 32 * h + e;
+              const float y = exp2_fast(fmaf(s[e], a.sl2, -ls[c]));
+              if (c >= lo && c < cols) sum[e & 1].x += y;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(s_free + 8 * (2 * w + buf));
+          if (last_q(keep)) mbar_arrive(q_free + 8 * sq);
+        }
+        if (last_q(keep)) ++nq;
+        total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      }
+      if (!ok) break;
+      // sixteen rows' sums, then a chunk's
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      if ((lane & 15) == 0) x.sum[n & 1u][w][2 * quarter + (lane >> 4)] = total;
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+      if (quarter == 0) {
+        float v = 0.f;
+        int at = INT_MAX;
+        if (lane < chunks) {
+          for (int i = 0; i < a.cs / 16; ++i) v += x.sum[n & 1u][w][lane * (a.cs / 16) + i];
+          at = r.pos[w * chunks + lane];
+        }
+        bool done = true;
+        if (r.parts > 1) {
+          if (lane < chunks) __stcg(p.parts + (int64_t)r.part * 16 + w * 8 + lane, v);
+          __syncwarp();
+          int last = 0;
+          if (lane == 0) {
+            __threadfence();
+            last = atomicAdd(p.w.ctr + 2 + r.cut + w, 1) == r.parts - 1;
+            __threadfence();
+          }
+          done = __shfl_sync(0xffffffffu, last, 0) != 0;
+          __syncwarp();
+          if (done && lane < chunks) {
+            v = 0.f;
+            for (int i = 0; i < r.parts; ++i) v += __ldcg(p.parts + (int64_t)(r.part0 + i) * 16 + w * 8 + lane);
+          }
+        }
+        if (done && at != INT_MAX) {
+          float *to = p.weight + (int64_t)unit * a.C + at / a.cs;
+          *to = p.decay == 0.f ? v : fmaf(p.decay, *to, v);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_free + 8 * st);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+  }
+  if (tid == 0) leave_counters(p.w);
+}
+
+}  // namespace
+
+int64_t weights_workspace(int cs, int sm_count) {
+  (void)cs;
+  return (int64_t)2 * kItemsPerCta * sm_count * 16 * 4;
+}
+
+cudaError_t launch_weights(const WeightsArgs &e, cudaStream_t stream) {
+  const PagesArgs &a = e.p;
+  WeightsParams p{};
+  p.a = a;
+  const int most = 128 / a.G, seen = e.window > 0 && e.window < a.T ? e.window : a.T;
+  p.a.tt = seen < most ? seen : most;
+  const bool hot = a.hot_slots > 0, far = a.max_misses > 0;
+  if (!make_rows_map(&p.q, e.q, e.q_stride, a.B, a.T, a.Hq, a.G, p.a.tt) ||
+      !make_pages_map(&p.k, hot ? e.Khot : e.dummy, hot ? a.hot_slots : 1, a.cs) ||
+      !make_pages_map(&p.kst, far ? e.Kst : e.dummy, far ? a.max_misses : 1, a.cs))
+    return cudaErrorInvalidValue;
+  p.lse = e.lse, p.weight = e.weight, p.window = e.window, p.decay = e.decay, p.parts = e.parts;
+  p.w = {e.ctr, kCtrPerCta * e.sm_count};
+  cudaError_t r = set_dyn_smem((const void *)k_weights, kSmem);
+  if (r != cudaSuccess) return r;
+  return launch_k(k_weights, dim3(e.sm_count), dim3(kThreads), kSmem, stream, p);
+}
+
+}  // namespace dd

@@ -37,6 +37,7 @@ EXPORTED = (
     "dd_build_landmarks_minmax", "dd_score_landmarks_minmax", "dd_update_residency",
     "dd_prefetch_kv", "dd_select_topk_mass", "dd_selftest_bounded_wait", "dd_step_folds_scoring",
     "dd_rope_table", "dd_rope_rows", "dd_append_kv", "dd_gather_kv4", "dd_sparse_attn_decode_kv4",
+    "dd_extend_attn", "dd_extend_attn_workspace", "dd_chunk_weights", "dd_chunk_weights_workspace", "dd_evict_chunks",
 )
 
 
@@ -88,6 +89,13 @@ class RopeRef(ctypes.Structure):
 # Vhot, resident_slot, k_exp, v_exp
 _append_args = struct.Struct("@2P6q2i10P")
 _strides = struct.Struct("@3q")
+# dd_new_rows (q, strides, T, start_pos, new_len) and dd_page_list (Khot, Vhot, Kst, Vst, union_idx,
+# union_slot, union_cnt, miss_count), then the rest of dd_extend_args and dd_weights_args
+_extend_args = struct.Struct("@P3qi2P8PfP3q2Pq")
+_weights_args = struct.Struct("@P3qi2P8PfPif2Pq")
+# dd_evict_args: weight, kv_len, new_len; slots_per_unit, keep, first, last, step; resident_slot, resident_out,
+# slot_chunk, last_used, evicted, evicted_cnt, union_idx, union_slot, union_cnt
+_evict_args = struct.Struct("@3P5i9P")
 
 
 def _load():
@@ -116,6 +124,11 @@ def _load():
         "dd_append_kv": (i32, [_vp, ctypes.c_char_p, _vp]),
         "dd_gather_kv4": (i32, [_vp] * 7 + [i32] + [_vp] * 3),
         "dd_sparse_attn_decode_kv4": (i32, [_vp] * 16 + [f32, _vp, _vp]),
+        "dd_extend_attn_workspace": (i64, [_vp, i32]),
+        "dd_extend_attn": (i32, [_vp, ctypes.c_char_p, _vp]),
+        "dd_chunk_weights_workspace": (i64, [_vp]),
+        "dd_chunk_weights": (i32, [_vp, ctypes.c_char_p, _vp]),
+        "dd_evict_chunks": (i32, [_vp, ctypes.c_char_p, _vp]),
         "dd_get_status": (i32, [_vp, ctypes.POINTER(i32)]),
         "dd_launch_count": (i64, [_vp]),
         "dd_step_folds_scoring": (i32, [ctypes.POINTER(Dims), i32, ctypes.c_int, f32]),
@@ -225,6 +238,14 @@ def _either(t, dtype, numel, name, allow_none=False):
     if isinstance(t, torch.Tensor):
         return _dev(t, dtype, numel, name) if t.is_cuda else _ptr(t, dtype, numel, device=False, name=name)
     return _ptr(t, dtype, numel, name=name, allow_none=allow_none)
+
+
+def _same_device(first, *others):
+    """Every tensor given lives on the device of the first."""
+    d = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError("all tensors of a call must be on one device")
 
 
 class Rope:
@@ -479,6 +500,95 @@ class Context:
             _dev(union_qmask, u8, nu, "union_qmask"), _i32(union_cnt, units, "union_cnt"),
             _dev(miss_count, i32, 1, "miss_count"), _dev(kv_len, i32, s.B, "kv_len"), float(softmax_scale),
             _dev(out, torch.float32, nq, "out"), _stream(stream)), "dd_sparse_attn_decode_kv4")
+
+    # ------------------------------- new tokens over a paged cache, chunk weights, eviction
+    def _scratch(self, workspace, nbytes, like, stream):
+        """A call's workspace: the caller's, or one from torch's allocator on the call's stream."""
+        if workspace is not None:
+            return workspace, _dev(workspace, torch.uint8, nbytes, "workspace")
+        if stream is None:
+            t = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        else:
+            with torch.cuda.stream(stream):
+                t = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return t, t.data_ptr()
+
+    def _new_rows(self, q, start_pos, new_len):
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("q must be a tensor [B, T, Hq, 128]")
+        s = self.shape
+        T = q.shape[1]
+        qp, *qs = _rows(q, (s.B, T, s.Hq, D_HEAD), "q")
+        return qp, *qs, T, _i32(start_pos, s.B, "start_pos"), _dev(new_len, torch.int32, s.B, "new_len") or 0
+
+    def _pages(self, Khot, Vhot, Kst, Vst, union_idx, union_slot, union_cnt, miss_count):
+        s = self.shape
+        page, units = s.cs * s.d, s.B * s.Hkv
+        nh, ns, bf = self.hot_slots * page, self.max_misses * page, torch.bfloat16
+        return (_dev(Khot, bf, nh, "Khot") or 0, _dev(Vhot, bf, nh, "Vhot") or 0, _dev(Kst, bf, ns, "Kst") or 0,
+                _dev(Vst, bf, ns, "Vst") or 0, _i32(union_idx, units * s.umax, "union_idx"),
+                _i32(union_slot, units * s.umax, "union_slot"), _i32(union_cnt, units, "union_cnt"),
+                _dev(miss_count, torch.int32, 1, "miss_count") or 0)
+
+    def extend_attn_workspace(self, T) -> int:
+        """Bytes of workspace that extend_attn of T tokens a request needs."""
+        return int(_lib.dd_extend_attn_workspace(self._h, int(T)))
+
+    def extend_attn(self, q, start_pos, Khot, Vhot, union_idx, union_slot, union_cnt, out, new_len=None, lse=None,
+                    Kst=None, Vst=None, miss_count=None, softmax_scale=0.0, workspace=None, stream=None):
+        """Attention of new tokens q bf16 [B, T, Hq, 128] over the listed chunks, causal by position, into
+        ``out`` (bf16, q's shape) and ``lse`` (fp32 [B, T, Hq]); ``workspace`` (uint8) comes from torch's
+        allocator unless given (see dd.h)."""
+        s = self.shape
+        rows = self._new_rows(q, start_pos, new_len)
+        T = rows[4]
+        op, *os_ = _rows(out, (s.B, T, s.Hq, D_HEAD), "out", writable=True)
+        _same_device(q, out, start_pos, new_len, lse, Khot, Vhot, Kst, Vst, union_idx, union_slot, union_cnt, miss_count,
+                     workspace)
+        n = self.extend_attn_workspace(T)
+        keep, wp = self._scratch(workspace, n, q, stream)
+        a = _extend_args.pack(*rows, *self._pages(Khot, Vhot, Kst, Vst, union_idx, union_slot, union_cnt, miss_count),
+                              float(softmax_scale), op, *os_, _dev(lse, torch.float32, s.B * T * s.Hq, "lse") or 0, wp, n)
+        _chk(_lib.dd_extend_attn(self._h, a, _stream(stream)), "dd_extend_attn")
+
+    def chunk_weights(self, q, start_pos, lse, Khot, union_idx, union_slot, union_cnt, weight, new_len=None, window=0,
+                      decay=1.0, Kst=None, miss_count=None, softmax_scale=0.0, workspace=None, stream=None):
+        """Add the attention weights of new tokens up per listed chunk: ``weight`` fp32 [B, Hkv, C] becomes
+        decay * weight + theirs, lse as extend_attn left it, of the last ``window`` tokens of a
+        request (0: all; see dd.h)."""
+        s = self.shape
+        rows = self._new_rows(q, start_pos, new_len)
+        _same_device(q, start_pos, new_len, lse, weight, Khot, Kst, union_idx, union_slot, union_cnt, miss_count, workspace)
+        if lse is None or weight is None:
+            raise ValueError("lse and weight are required")
+        n = int(_lib.dd_chunk_weights_workspace(self._h))
+        keep, wp = self._scratch(workspace, n, q, stream)
+        a = _weights_args.pack(*rows, *self._pages(Khot, None, Kst, None, union_idx, union_slot, union_cnt, miss_count),
+                               float(softmax_scale), _dev(lse, torch.float32, s.B * rows[4] * s.Hq, "lse"), int(window),
+                               float(decay), _dev(weight, torch.float32, s.B * s.Hkv * s.C, "weight"), wp, n)
+        _chk(_lib.dd_chunk_weights(self._h, a, _stream(stream)), "dd_chunk_weights")
+
+    def evict_chunks(self, weight, kv_len, resident_slot, resident_out, keep, slots_per_unit, first=0, last=0,
+                     new_len=None, slot_chunk=None, last_used=None, step=0, evicted=None, evicted_cnt=None,
+                     union_idx=None, union_slot=None, union_cnt=None, stream=None):
+        """Bring each (request, KV head)'s pool to ``keep`` chunks by gathered weight, give the chunks of the
+        tokens to come their slots and list what is resident (see dd.h)."""
+        s = self.shape
+        units, i32 = s.B * s.Hkv, torch.int32
+        n, ns, nu = units * s.C, units * int(slots_per_unit), units * s.umax
+        if weight is None:
+            raise ValueError("weight is required")
+        wp = _dev(weight, torch.float32, n, "weight")
+        _same_device(weight, kv_len, new_len, resident_slot, resident_out, slot_chunk, last_used, evicted, evicted_cnt,
+                     union_idx, union_slot, union_cnt)
+        a = _evict_args.pack(
+            wp, _i32(kv_len, s.B, "kv_len"), _dev(new_len, i32, s.B, "new_len") or 0, int(slots_per_unit), int(keep),
+            int(first), int(last), int(step), _i32(resident_slot, n, "resident_slot"), _i32(resident_out, n, "resident_out"),
+            _dev(slot_chunk, i32, ns, "slot_chunk") or 0, _dev(last_used, i32, ns, "last_used") or 0,
+            _dev(evicted, i32, ns, "evicted") or 0, _dev(evicted_cnt, i32, units, "evicted_cnt") or 0,
+            _dev(union_idx, i32, nu, "union_idx") or 0, _dev(union_slot, i32, nu, "union_slot") or 0,
+            _dev(union_cnt, i32, units, "union_cnt") or 0)
+        _chk(_lib.dd_evict_chunks(self._h, a, _stream(stream)), "dd_evict_chunks")
 
     def selftest_bounded_wait(self, kind, stream=None):
         """Run a bounded device wait that nothing signals (see dd.h); the status

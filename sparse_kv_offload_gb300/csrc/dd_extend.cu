@@ -754,7 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
           if (quarter == 0 && lane == 0) {
             __threadfence();
-            x.last[w] = atomicAdd(p.w.ctr + 2 + it.cut[w], 1) == arrivals - 1;
+            int32_t *ctr = p.w.ctr + 2 + it.cut[w];
+            x.last[w] = atomicAdd(ctr, 1) == arrivals - 1;
+            if (x.last[w]) *ctr = 0;
             __threadfence();
           }
           asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
   }
-  if (tid == 0) leave_counters(p.w);
+  leave_counters(p.w, a.status, &x.pending);
 }
 
 struct Shape {

@@ -193,15 +193,20 @@ struct WorkCounters {
   int n;          // arrival counters
 };
 
-// The launch's last CTA leaves the counters as it found them.  One thread, after all of its CTA's arrivals.
-__device__ __forceinline__ void leave_counters(const WorkCounters &w) {
-  __threadfence();
-  if (atomicAdd(w.ctr + 1, 1) == (int)gridDim.x - 1) {
+// The launch's last CTA leaves the counters as it found them: whoever joins parts clears their
+// counter, and where a launch reports an error some may never be joined.  All threads, after their
+// CTA's last arrival and a barrier.
+__device__ __forceinline__ void leave_counters(const WorkCounters &w, int32_t *status, int *last) {
+  if (threadIdx.x == 0) {
     __threadfence();
-    for (int i = 0; i < w.n; ++i) w.ctr[2 + i] = 0;
-    w.ctr[0] = 0;
-    w.ctr[1] = 0;
+    *last = atomicAdd(w.ctr + 1, 1) == (int)gridDim.x - 1;
+    __threadfence();
   }
+  __syncthreads();
+  if (!*last) return;
+  if (load_status(status) != 0)
+    for (int i = threadIdx.x; i < w.n; i += blockDim.x) w.ctr[2 + i] = 0;
+  if (threadIdx.x < 2) w.ctr[threadIdx.x] = 0;
 }
 
 constexpr int kCtrPerCta = 32;      // arrival counters per CTA of the grid (one CTA an SM)

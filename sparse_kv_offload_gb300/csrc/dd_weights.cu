@@ -445,7 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           int last = 0;
           if (lane == 0) {
             __threadfence();
-            last = atomicAdd(p.w.ctr + 2 + r.cut + w, 1) == r.parts - 1;
+            int32_t *ctr = p.w.ctr + 2 + r.cut + w;
+            last = atomicAdd(ctr, 1) == r.parts - 1;
+            if (last) *ctr = 0;
             __threadfence();
           }
           done = __shfl_sync(0xffffffffu, last, 0) != 0;
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
   }
-  if (tid == 0) leave_counters(p.w);
+  leave_counters(p.w, a.status, &x.pending);
 }
 
 }  // namespace

@@ -149,14 +149,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   const uint32_t bars = smem_u32(x.bars);
   const uint32_t k_full = bars, k_free = k_full + 8 * kK, v_full = k_free + 8 * kK, v_ok = v_full + 8 * kV,
                  v_free = v_ok + 8 * kV, q_full = v_free + 8 * kV, q_free = q_full + 8, s_full = q_free + 8,
-                 p_ready = s_full + 16, o_full = p_ready + 16, item_full = o_full + 16, item_free = item_full + 16,
+                 p_half = s_full + 16, p_ready = p_half + 16, o_full = p_ready + 16, item_full = o_full + 16, item_free = item_full + 16,
                  looked = item_free + 16, joined = looked + 16, mma_done = joined + 8;
   if (tid == 0) {
     for (int i = 0; i < kK; ++i) mbar_init(k_full + 8 * i, 1), mbar_init(k_free + 8 * i, 1);
     for (int i = 0; i < kV; ++i) mbar_init(v_full + 8 * i, 1), mbar_init(v_ok + 8 * i, 1), mbar_init(v_free + 8 * i, 1);
     mbar_init(q_full, 1), mbar_init(q_free, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(looked + 8 * i, 1), mbar_init(s_full + 8 * i, 2), mbar_init(p_ready + 8 * i, 4), mbar_init(o_full + 8 * i, 1);
+      mbar_init(looked + 8 * i, 1), mbar_init(s_full + 8 * i, 2), mbar_init(p_half + 8 * i, 4), mbar_init(p_ready + 8 * i, 4), mbar_init(o_full + 8 * i, 1);
       mbar_init(item_full + 8 * i, 1), mbar_init(item_free + 8 * i, 11);
     }
     mbar_init(joined, 8), mbar_init(mma_done, 1);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         work += (long long)r.groups * r.tiles;
         groups += r.groups;
       }
-  #pragma unroll
+#pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         work += __shfl_xor_sync(0xffffffffu, work, o);
         groups += __shfl_xor_sync(0xffffffffu, groups, o);
@@ -455,26 +455,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         const int nt = p.pairs == 2 ? steps : c0 + c1;
         if (nt > 0) ok = wait_warp(q_full, nq++);
         for (int i = 0; ok && i <= steps && nt > 0; ++i) {
-  #pragma unroll
+#pragma unroll
           for (int w = 0; w < 2; ++w) {
             const int cw = w ? c1 : c0;
             if (!ok) break;
             if (i > 0 && i - 1 < cw) {
               const int tile = p.pairs == 2 ? i - 1 : 2 * (i - 1) + w;
               const uint32_t t = t_base + tile, st = t % kV;
-              ok = wait_warp(v_ok + 8 * st, t / kV) && wait_warp(p_ready + 8 * w, np[w]);
+              ok = wait_warp(v_ok + 8 * st, t / kV);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                // the weights of 64 keys, then those of the others
+                ok = ok && wait_warp((half ? p_ready : p_half) + 8 * w, np[w]);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_lane()) {
+                  const uint64_t vb = v_desc + st * (kTileBytes / 16);
+#pragma unroll
+                  for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                    tc_mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * ks, vb + ks * (16 * 128 / 16), id_o,
+                              i > 1 || ks > 0);
+                  if (half) {
+                    if (p.pairs == 1 || w == 1 || i - 1 >= c1) tc_commit(v_free + 8 * st);
+                    if (i == cw) tc_commit(o_full + 8 * w);
+                  }
+                }
+                __syncwarp();
+              }
               ++np[w];
               if (!ok) break;
-              tc_fence_after();
-              if (elect_lane()) {
-                const uint64_t vb = v_desc + st * (kTileBytes / 16);
-  #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                  tc_mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * ks, vb + ks * (16 * 128 / 16), id_o, i > 1 || ks > 0);
-                if (p.pairs == 1 || w == 1 || i - 1 >= c1) tc_commit(v_free + 8 * st);
-                if (i == cw) tc_commit(o_full + 8 * w);
-              }
-              __syncwarp();
             }
             if (i < cw) {
               const int tile = p.pairs == 2 ? i : 2 * i + w;
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               if (elect_lane()) {
                 const uint64_t qb = q_desc + (p.pairs == 2 ? w * (kTileBytes / 16) : 0);
                 const uint64_t kb = k_desc + st * (kTileBytes / 16);
-  #pragma unroll
+#pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
                   const uint32_t off = ((ks >> 2) * kTileHalfBytes + (ks & 3) * 32) / 16;
                   tc_mma(tmem + 128 * w, qb + off, kb + off, id_s, ks > 0);
@@ -527,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               uint32_t w[4];
               asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
               uint32_t hit = 0;
-  #pragma unroll
+#pragma unroll
               for (int k = 0; k < 4; ++k) hit |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
               const uint32_t any = __ballot_sync(0xffffffffu, hit != 0u);
               if (any == 0u) continue;
@@ -542,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               if (hit) {
                 const int row = (e & 1023) >> 3, col0 = (e >> 10) * 64 + (((e & 7) ^ (row & 7)) << 3);
                 const int first = x.vpos[st][row / a.cs], pos = first == INT_MAX ? INT_MAX : first + row % a.cs;
-  #pragma unroll
+#pragma unroll
                 for (int k = 0; k < 8; ++k) {
                   const uint32_t v = (w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
                   if ((v & 0x7F80u) == 0x7F80u) {
@@ -590,6 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       const bool valid = r < rows_tile && token < it.len;
       const int pos = valid ? it.start + token : -1;
       float m = -INFINITY, l = 0.f;                        // reference (a score before the factor), sum of weights
+      float sub = 0.f;                                     // the reference times the factor, negated
+      bool far = false;
       for (int i = 0; i < cw; ++i) {
         const uint32_t t = t_base + (p.pairs == 2 ? i : 2 * i + w);
         ok = wait_warp(s_full + 8 * w, ns);
@@ -597,30 +608,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         if (!ok) break;
         tc_fence_after();
         if (some) {
+          const int whole = x.whole[t % kInfo];
           float s[128];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) tmem_ld32(s_at + 32 * h, s + 32 * h);
+          // the second half is on its way while the first is looked over
+          tmem_ld32(s_at, s), tmem_ld32(s_at + 32, s + 32);
           tmem_wait_ld();
-          if (!x.whole[t % kInfo]) {
+          tmem_ready(s), tmem_ready(s + 32);
+          tmem_ld32(s_at + 64, s + 64), tmem_ld32(s_at + 96, s + 96);
+          float mx = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < 8; ++h) {
-              const int row0 = 16 * h, first = x.pos[t % kInfo][row0 / a.cs];
-              // columns up to `lim` are seen
-              const int lim = first == INT_MAX ? -1 : pos - first - row0 % a.cs;
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (e > lim) s[16 * h + e] = -INFINITY;
+          for (int half = 0; half < 2; ++half) {
+            if (half) {
+              tmem_wait_ld();
+              tmem_ready(s + 64), tmem_ready(s + 96);
             }
+            if (!whole) {
+#pragma unroll
+              for (int h = 4 * half; h < 4 * half + 4; ++h) {
+                const int row0 = 16 * h, first = x.pos[t % kInfo][row0 / a.cs];
+                // columns up to `lim` are seen
+                const int lim = first == INT_MAX ? -1 : pos - first - row0 % a.cs;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (e > lim) s[16 * h + e] = -INFINITY;
+              }
+            }
+            float m4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = fmaxf(s[64 * half + e], s[64 * half + 4 + e]);
+#pragma unroll
+            for (int h = 8; h < 64; h += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], s[64 * half + h + e], s[64 * half + h + 4 + e]);
+            mx = max3(mx, max3(m4[0], m4[1], m4[2]), m4[3]);
           }
-          float m8[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m8[e] = fmaxf(s[e], s[e + 8]);
-#pragma unroll
-          for (int h = 16; h < 128; h += 16)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m8[e] = fmaxf(m8[e], fmaxf(s[h + e], s[h + e + 8]));
-          const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                 fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
           // (also from -inf; not where both are; rows that are none hold anything and have no say)
           const bool up = valid && (mx - m) * a.sl2 > kHead;
           if (__any_sync(0xffffffffu, up)) {
@@ -629,26 +650,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             l *= f;
             if (i > 0) {
               // S(t) is there, so the product before it is done with O
-#pragma unroll
+#pragma unroll 1
               for (int h = 0; h < 4; ++h) {
                 float o[32];
                 tmem_ld32(o_at + 32 * h, o);
                 tmem_wait_ld();
+                tmem_ready(o);
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] *= f;
                 tmem_st32(o_at + 32 * h, o);
               }
               tmem_wait_st();
             }
+            // weights are 2^(s sl2 - m sl2), one rounding of a number near 0 or of one that gives no weight; scores
+            // so large that m sl2 itself is rounded by more than 2^-8 are taken from the reference first
+            sub = m == -INFINITY ? 0.f : -m * a.sl2;
+            far = __any_sync(0xffffffffu, valid && !(fabsf(sub) <= 65536.f));
           }
-          // weights 2^(s sl2 - m sl2): one rounding, of a number near 0 or one that gives no weight; scores so
-          // large that m sl2 itself is rounded by more than 2^-8 are taken from the reference first
-          const float ref = m == -INFINITY ? 0.f : m;
-          float mul = a.sl2, sub = -ref * a.sl2;
-          if (__any_sync(0xffffffffu, valid && !(fabsf(sub) <= 65536.f))) {
+          float add = sub;
+          if (far) {
 #pragma unroll
-            for (int e = 0; e < 128; ++e) s[e] -= ref;
-            sub = 0.f;
+            for (int e = 0; e < 128; ++e) s[e] -= m == -INFINITY ? 0.f : m;
+            add = 0.f;
           }
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -656,16 +679,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float2 y = fma2(make_float2(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), make_float2(mul, mul),
-                              make_float2(sub, sub));
+              float2 y = fma2(make_float2(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), make_float2(a.sl2, a.sl2),
+                              make_float2(add, add));
               y.x = exp2_fast(y.x), y.y = exp2_fast(y.y);
               sum[e & 1] = add2(sum[e & 1], y);
               pk[e] = bf16x2(y.x, y.y);
             }
             tmem_st16(s_at + 16 * h, pk);
+            if (h == 1) {
+              // the first 64 keys' product may begin
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_half + 8 * w);
+            }
           }
           l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
+        } else if (lane == 0) {
+          mbar_arrive(p_half + 8 * w);
         }
         tc_fence_before();
         __syncwarp();

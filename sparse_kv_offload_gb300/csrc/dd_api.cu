@@ -786,6 +786,9 @@ static dd_status pages_args(const dd_ctx *c, const dd_new_rows *r, const dd_page
   if (!l->union_idx || !l->union_slot || !l->union_cnt) return DD_ERR_INVALID_ARG;
   if (c->hot_slots > 0 && (!l->Khot || !aligned16(l->Khot))) return DD_ERR_INVALID_ARG;
   if (c->max_misses > 0 && (!l->Kst || !aligned16(l->Kst))) return DD_ERR_INVALID_ARG;
+  // tiles of query rows and of keys are numbered with 32 bits
+  const int64_t per_tile = 128 / c->G;
+  if ((int64_t)c->units * ((r->T + per_tile - 1) / per_tile) >= (int64_t(1) << 30)) return DD_ERR_INVALID_ARG;
   // tensor maps step by less than 2^40 bytes, and not backwards
   for (int i = 0; i < 3; ++i)
     if (r->q_stride[i] < 0 || r->q_stride[i] >= (int64_t(1) << 39)) return DD_ERR_INVALID_ARG;

@@ -24,11 +24,11 @@
 // operands of one type): up to 2^-8 of each weight, at random, as the rounding of the
 // output.  l is the sum of the weights before that, so that lse has fp32's precision.
 //
-// Work: an item is a pair of row tiles (or the row tile) by a range of tiles of keys.  Ranges
-// are as long as they may be while the CTAs stay evenly filled (cut_of); a row tile cut into several ranges
-// has its parts joined by whoever finishes last, in the ranges' order.  Items are handed
-// out one after another with the pairs of one KV head and range next to each other, so that the
-// CTAs at work read the same keys at about the same time, out of L2.
+// Work: with two row tiles an item is a pair of them, whole or by a range of tiles of keys (cut_of); items are
+// handed out one after another, the pairs of one KV head and range next to each other, so that the CTAs
+// at work read the same keys at about the same time, out of L2.  With one row tile a unit a CTA has
+// an equal slice of all units' tiles, as nothing is read twice and the bytes bound it.  A row tile that is cut
+// has its parts joined by whoever finishes last, in the ranges' order.
 #include "dd_pages.cuh"
 
 namespace dd {
@@ -49,8 +49,8 @@ struct Item {
   int pos_max, pos_min;       // positions of the item's last and first token
   int c[2];                   // tiles of each stream
   int parts[2];               // of each stream's row tile: 0 nothing to do, 1 written out, more: joined
-  int part0[2], part[2];      // slots of the row tile's first part and of this stream's
-  int cut[2];                 // arrival counter
+  int64_t part0, part;        // slots of the first range's parts and of this one's (slices: the first slice's number)
+  int cut;                    // arrival counter (pairs: and the next one)
   int local;                  // the two streams' sums are joined within the CTA
 };
 
@@ -117,28 +117,41 @@ __device__ __forceinline__ int first_longer(const ExtendParams &p, const Unit &u
   return need <= 0 ? 0 : ceil_div(need, p.mt) - 1;
 }
 
-// The longest range of keys (in tiles) of an item.  Of the cuts into S = 1, 2, .. ranges of the mean
-// row tile, with at most kItemsPerCta items a CTA, the one that ends first: rounds of items, each its tiles
-// and kItemCost of them for what an item costs beside (queries, sums out and in, the join).  No
-// range is longer than a CTA's share, which keeps one long request from ending alone.
-// Bounds that follow, with P CTAs: row tile pairs that are cut <= 2 P, their ranges <= 6 P.
+// A unit without its last `whole` groups of tokens.
+__device__ __forceinline__ Unit cut_part(const ExtendParams &p, const Unit &u, int whole) {
+  Unit r = u;
+  r.groups -= whole;
+  r.tiles = r.groups ? tiles_of(p.a, entry_bound(p.a, u, min(r.groups * p.mt, u.len) - 1)) : 0;
+  return r;
+}
+
+// Pairs of row tiles: as many as there are whole rounds of CTAs for are taken whole, in order, and the
+// rest, fewer than CTAs, is cut into ranges of at most this many tiles of keys.  Of the cuts into s = 1, 2, ..
+// ranges of the mean pair, with at most kItemsPerCta items a CTA, the one that ends first: rounds of items, each
+// its tiles and kItemCost of them for what an item costs beside (queries, sums out and in, the join), and where
+// lengths differ up to one item more.  No range is longer than a CTA's share, which keeps one long request
+// from ending alone.  With P CTAs: pairs that are cut < P, their ranges <= 5 P.
 constexpr int kItemCost = 3, kItemsPerCta = 4;
-__device__ __forceinline__ int cut_of(long long work, long long groups, int cta, int lane) {
-  const long long mean = max(1ll, (work + groups - 1) / max(1ll, groups));
-  const long long most = max(1ll, (long long)kItemsPerCta * cta / max(1ll, groups));
+__device__ __forceinline__ int cut_of(long long work, int groups, int longest, int cta, int lane) {
+  if (groups == 0) return 1;
+  const int mean = (int)max(1ll, (work + groups - 1) / groups), most = max(1, kItemsPerCta * cta / groups);
   unsigned long long best = ~0ull;
-  for (long long s = 1 + lane; s <= min(most, mean); s += 32) {
-    const long long len = (mean + s - 1) / s;
-    const unsigned long long cost = (unsigned long long)((groups * s + cta - 1) / cta * (len + kItemCost));
-    best = min(best, (cost << 12) | (unsigned long long)min(s, 4095ll));
+  for (int s = 1 + lane; s <= min(most, mean); s += 32) {
+    const int len = ceil_div(mean, s);
+    const unsigned long long cost = (unsigned long long)ceil_div(groups * s, cta) * (len + kItemCost) + min(len, max(0, longest - mean));
+    best = min(best, (cost << 12) | (unsigned long long)min(s, 4095));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = min(best, (unsigned long long)__shfl_xor_sync(0xffffffffu, best, o));
-  const long long s = max(1ll, (long long)(best & 4095ull));
-  long long len = (mean + s - 1) / s;
-  if (s == 1) len = max(len, (work + cta - 1) / cta);
-  return (int)min(len, (long long)INT_MAX / kTileKeys);
+  const int s = max(1, (int)(best & 4095ull)), len = ceil_div(mean, s);
+  return s == 1 ? max(len, (int)((work + cta - 1) / cta)) : len;
 }
+
+// One row tile a unit: the units' tiles of keys, laid end to end, are cut into equal slices, one a CTA; kUnitCost
+// tiles stand before each unit's for what it costs beside.  A unit that slices cut is joined from two parts
+// a slice (the streams'): in its first slice it is the last unit, in the others the first.
+constexpr int kUnitCost = 2;
+__device__ __forceinline__ int64_t slice_slot(int64_t slice, bool first, int w) { return 4 * slice + (first ? 2 : 0) + w; }
 
 __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ ExtendParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -208,131 +221,183 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     } else if (warp == 9) {
       // ------------------------------------------------------- the work, and K's tiles
       const int units = a.B * a.Hkv, cta = (int)gridDim.x;
-      long long work = 0, groups = 0;
+      const bool sliced = p.pairs == 1;
+      uint32_t total = 0;                                  // groups, or tiles of all units and their costs (below 2^31)
+      Unit few = {0, 0, 0, 0, 0};                          // a lane's unit, where there are no more than 32
       for (int u = lane; u < units; u += 32) {
-        const Unit r = load_unit(p, u);
-        work += (long long)r.groups * r.tiles;
-        groups += r.groups;
+        const Unit r = few = load_unit(p, u);
+        total += sliced ? (r.groups ? r.tiles + kUnitCost : 0) : r.groups;
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        work += __shfl_xor_sync(0xffffffffu, work, o);
-        groups += __shfl_xor_sync(0xffffffffu, groups, o);
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      const int whole_groups = (int)(total / cta * cta);
+      int cut = 1;
+      if (!sliced) {
+        // what is left to cut
+        long long work = 0;
+        int longest = 0, before = 0;
+        for (int u0 = 0; u0 < units; u0 += 32) {
+          Unit r = {0, 0, 0, 0, 0};
+          if (u0 + lane < units) r = units <= 32 ? few : load_unit(p, u0 + lane);
+          const int incl = warp_incl_scan(r.groups);
+          r = cut_part(p, r, min(r.groups, max(0, whole_groups - before - (incl - r.groups))));
+          work += (long long)r.groups * r.tiles;
+          longest = max(longest, r.tiles);
+          before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        cut = cut_of(work, (int)total - whole_groups, longest, cta, lane);
       }
-      const int cut = cut_of(work, groups, cta, lane);
+      const int per = max((int)((total + cta - 1) / cta), 2);      // of a slice: a tile for each stream at least
       const int64_t staged = staged_slots(a);
 
-      // the lanes hold 32 units; what lies before them: items, ranges of cut groups, cut groups
-      int base_u = -32, cuts_before = 0;
-      long long items_before = 0, items_here = 0;
-      int parts_before = 0, parts_here = 0, cuts_here = 0;
-      Unit mine = {0, 0, 0, 0, 0};
+      // The lanes hold 32 units; counts before them and of them.  Slices: `items` are tiles (and costs), the place that
+      // is wanted moves through the CTA's own slice.  Else items are handed out by tickets, the first by number.
+      int base_u = -32, cuts_before = 0, parts_before = 0, parts_here = 0, cuts_here = 0;
+      int items_before = 0, items_here = 0, groups_before = 0, groups_here = 0;
+      Unit mine = {0, 0, 0, 0, 0}, rest = {0, 0, 0, 0, 0};  // a unit, and its groups that are cut
       int ranges = 0, items = 0, items_pre = 0, parts_pre = 0, cuts_pre = 0, m1 = 0;
-      long long next = blockIdx.x;
+      int want = sliced ? (int)blockIdx.x * per : (int)blockIdx.x;
+      const int slice_end = want + per;
       uint32_t n_item = 0, kt = 0;
       bool ok = true;
       while (ok) {
-        const long long want = next;
         int ticket = 0;
-        if (lane == 0) ticket = atomicAdd(p.w.ctr, 1);       // the next one: on its way during this one's work
+        if (!sliced && lane == 0) ticket = atomicAdd(p.w.ctr, 1);    // the next one: on its way during this one's work
         while (base_u + 32 < units && want >= items_before + items_here) {
-          items_before += items_here, parts_before += parts_here, cuts_before += cuts_here;
+          items_before += items_here, parts_before += parts_here, cuts_before += cuts_here, groups_before += groups_here;
           base_u += 32;
           mine = {0, 0, 0, 0, 0};
-          if (base_u + lane < units) mine = load_unit(p, base_u + lane);
-          ranges = mine.groups ? ceil_div(mine.tiles, cut) : 0;
-          items = 0;
-          m1 = first_longer(p, mine, cut);
-          if (mine.groups == 1 || ranges <= 1) {
-            items = mine.groups * ranges;
+          if (base_u + lane < units) mine = units <= 32 ? few : load_unit(p, base_u + lane);
+          int parts = 0, cuts = 0;
+          if (sliced) {
+            items = mine.groups ? mine.tiles + kUnitCost : 0;
           } else {
-            for (int s = 0; s < ranges; ++s) items += mine.groups - first_longer(p, mine, s * cut);
+            const int groups_incl = warp_incl_scan(mine.groups);
+            groups_here = __shfl_sync(0xffffffffu, groups_incl, 31);
+            const int whole = min(mine.groups, max(0, whole_groups - groups_before - (groups_incl - mine.groups)));
+            rest = cut_part(p, mine, whole);
+            ranges = rest.groups ? ceil_div(rest.tiles, cut) : 0;
+            m1 = first_longer(p, rest, cut);
+            items = whole + rest.groups * min(ranges, 1);
+            for (int s = 1; s < ranges; ++s) items += rest.groups - first_longer(p, rest, s * cut);
+            parts = ranges > 1 ? items - whole - m1 : 0, cuts = ranges > 1 ? rest.groups - m1 : 0;
           }
-          int parts = ranges > 1 ? items - m1 : 0, cuts = ranges > 1 ? mine.groups - m1 : 0;
           items_pre = warp_incl_scan(items), parts_pre = warp_incl_scan(parts), cuts_pre = warp_incl_scan(cuts);
           items_here = __shfl_sync(0xffffffffu, items_pre, 31);
           parts_here = __shfl_sync(0xffffffffu, parts_pre, 31);
           cuts_here = __shfl_sync(0xffffffffu, cuts_pre, 31);
           items_pre -= items, parts_pre -= parts, cuts_pre -= cuts;
         }
+        const bool end = want >= items_before + items_here || (sliced && want >= slice_end);
+        int src = 0, here = 0;
+        if (!end) {
+          // the unit that has it
+          here = want - items_before;
+          src = __ffs((int)__ballot_sync(0xffffffffu, items_pre <= here && here < items_pre + items)) - 1;
+          here -= __shfl_sync(0xffffffffu, items_pre, src);
+        }
+        Unit u;
+        u.cnt = __shfl_sync(0xffffffffu, mine.cnt, src), u.start = __shfl_sync(0xffffffffu, mine.start, src);
+        u.len = __shfl_sync(0xffffffffu, mine.len, src), u.groups = __shfl_sync(0xffffffffu, mine.groups, src);
+        u.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
+        int m = 0, tiles = 0, j0 = 0, j1 = 0, n_cut = 1;    // group, its tiles, the range, how many ranges
+        int64_t part0 = 0, part = 0;                        // slots of the pair's first part and of the range's
+        int cut_no = 0;
+        if (!end && sliced) {
+          const int first = want - here;                    // where the unit begins
+          const int upto = min(slice_end, first + kUnitCost + u.tiles);
+          tiles = u.tiles;
+          j0 = max(0, here - kUnitCost), j1 = max(0, upto - first - kUnitCost);
+          const int s0 = (first + kUnitCost) / per, s1 = (first + kUnitCost + u.tiles - 1) / per;
+          n_cut = s1 - s0 + 1, cut_no = s0;
+          part0 = s0, part = slice_slot(blockIdx.x, (int)blockIdx.x == s0, 0);
+          want = upto;
+          if (j0 >= j1) continue;                           // only of the cost before its tiles
+        } else if (!end) {
+          Unit r;
+          r.cnt = u.cnt, r.start = u.start, r.len = u.len;
+          r.groups = __shfl_sync(0xffffffffu, rest.groups, src), r.tiles = __shfl_sync(0xffffffffu, rest.tiles, src);
+          const int n_ranges = __shfl_sync(0xffffffffu, ranges, src), um1 = __shfl_sync(0xffffffffu, m1, src);
+          const int part_base = parts_before + __shfl_sync(0xffffffffu, parts_pre, src);
+          const int cut_base = cuts_before + __shfl_sync(0xffffffffu, cuts_pre, src);
+          const int whole = u.groups - r.groups;
+          int s = 0;
+          if (here < whole) {
+            m = u.groups - 1 - here;                        // long ones first
+          } else {
+            int rem = here - whole;
+            for (;; ++s) {
+              const int n = r.groups - first_longer(p, r, s * cut);
+              if (rem < n) break;
+              rem -= n;
+            }
+            m = r.groups - 1 - rem;
+          }
+          tiles = tiles_of(a, entry_bound(a, u, min((m + 1) * p.mt, u.len) - 1));
+          if (here < whole) {
+            j1 = tiles;
+          } else {
+            n_cut = ceil_div(tiles, cut);
+            j0 = s * cut, j1 = min(tiles, j0 + cut);
+            int skip = 0;                                   // ranges of the groups before this one
+            if (n_cut > 1)
+              for (int k = 0; k < n_ranges; ++k) skip += max(0, m - max(first_longer(p, r, k * cut), um1));
+            part0 = 2 * (part_base + skip), part = part0 + 2 * s;
+            cut_no = 2 * (cut_base + m - um1);
+          }
+        }
         const uint32_t slot = n_item & 1u;
         if (n_item >= 2) ok = wait_warp(item_free + 8 * slot, (n_item >> 1) - 1);
         if (!ok) break;
         Item &it = x.item[slot];
-        if (want >= items_before + items_here) {             // no more
+        if (end) {
           if (lane == 0) {
             it.unit = -1;
             mbar_arrive(item_full + 8 * slot);
           }
           break;
         }
-        // the unit that has it
-        const int here = (int)(want - items_before);
-        const uint32_t at = __ballot_sync(0xffffffffu, items_pre <= here && here < items_pre + items);
-        const int src = __ffs((int)at) - 1;
-        Unit u;
-        u.cnt = __shfl_sync(0xffffffffu, mine.cnt, src), u.start = __shfl_sync(0xffffffffu, mine.start, src);
-        u.len = __shfl_sync(0xffffffffu, mine.len, src), u.groups = __shfl_sync(0xffffffffu, mine.groups, src);
-        u.tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
-        const int n_ranges = __shfl_sync(0xffffffffu, ranges, src), um1 = __shfl_sync(0xffffffffu, m1, src);
-        const int part_base = parts_before + __shfl_sync(0xffffffffu, parts_pre, src);
-        const int cut_base = cuts_before + __shfl_sync(0xffffffffu, cuts_pre, src);
-        int rem = here - __shfl_sync(0xffffffffu, items_pre, src), s = 0, m = 0;
-        if (u.groups == 1) {
-          s = rem;
-        } else {
-          for (;; ++s) {
-            const int n = u.groups - first_longer(p, u, s * cut);
-            if (rem < n) break;
-            rem -= n;
-          }
-          m = u.groups - 1 - rem;                            // long ones first
-        }
         const int unit = base_u + src;
         const int64_t list = (int64_t)unit * a.umax;
         const int t0 = m * p.mt, t_end = min(t0 + p.mt, u.len);
-        const int tiles = tiles_of(a, entry_bound(a, u, t_end - 1)), n_cut = ceil_div(tiles, cut);
-        const int j0 = s * cut, j1 = min(tiles, j0 + cut);
-        int skip = 0;                                          // ranges of the groups before this one
-        if (n_cut > 1 && m > 0)
-          for (int r = 0; r < n_ranges; ++r) skip += max(0, m - max(first_longer(p, u, r * cut), um1));
-        int c[2] = {0, 0}, parts[2] = {0, 0};
-        int ents = 0;
+        int c0 = 0, c1 = 0, parts0 = 0, parts1 = 0, ents = 0;
+#pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const int lo = t0 + (p.pairs == 2 ? w * a.tt : 0), hi = p.pairs == 2 ? min(lo + a.tt, t_end) : t_end;
+          const int lo = t0 + (sliced ? 0 : w * a.tt), hi = sliced ? t_end : min(lo + a.tt, t_end);
           if (lo >= t_end) continue;
           const int bound = entry_bound(a, u, hi - 1);
           // with many tokens a list with gaps may hold many chunks that this token does not see yet
           const int seen = a.T > kTileKeys ? entries_up_to(a.union_idx + list, bound, (u.start + hi - 1) / a.cs, lane) : bound;
           const int n = max(0, min(ceil_div(seen * a.cs, kTileKeys), j1) - j0);
           ents = max(ents, seen);
-          if (p.pairs == 2) {
-            c[w] = n;
-            const int mine_cut = ceil_div(tiles_of(a, bound), cut);
-            parts[w] = s < mine_cut ? mine_cut : 0;
+          int c, parts;
+          if (sliced) {
+            c = w == 0 ? (n + 1) / 2 : n / 2;
+            parts = n_cut > 1 ? 2 * n_cut : (c > 0 || w == 0 ? 1 : 0);
           } else {
-            c[w] = w == 0 ? (n + 1) / 2 : n / 2;
-            parts[w] = n_cut > 1 ? 2 * n_cut : (c[w] > 0 || w == 0 ? 1 : 0);
+            c = n;
+            const int mine_cut = n_cut > 1 ? ceil_div(tiles_of(a, bound), cut) : 1;
+            parts = j0 < mine_cut * cut ? mine_cut : 0;
           }
+          if (w) c1 = c, parts1 = parts;
+          else c0 = c, parts0 = parts;
         }
         if (lane == 0) {
           it.unit = unit, it.t0 = t0, it.start = u.start, it.len = u.len;
           it.j0 = j0, it.ents = ents;
           it.pos_max = u.start + t_end - 1, it.pos_min = u.start + t0;
-          it.local = p.pairs == 1 && n_cut == 1 && c[1] > 0;
-          for (int w = 0; w < 2; ++w) {
-            it.c[w] = c[w], it.parts[w] = parts[w];
-            const int first = 2 * (part_base + skip);
-            it.part0[w] = p.pairs == 2 ? first + w : first;
-            it.part[w] = first + 2 * s + w;
-            it.cut[w] = p.pairs == 2 ? 2 * (cut_base + m - um1) + w : cut_base + m - um1;
-          }
+          it.local = sliced && n_cut == 1 && c1 > 0;
+          it.c[0] = c0, it.c[1] = c1, it.parts[0] = parts0, it.parts[1] = parts1;
+          it.part0 = part0, it.part = part, it.cut = cut_no;
           mbar_arrive(item_full + 8 * slot);
         }
         ++n_item;
 
-        // K's tiles; a batch of 32 entries is loaded while the tiles before it are asked for
-        const int nt = p.pairs == 2 ? max(c[0], c[1]) : c[0] + c[1];
+      // K's tiles; a batch of 32 entries is loaded while the tiles before it are asked for
+        const int nt = sliced ? c0 + c1 : max(c0, c1);
         const int per = 32 / chunks, pos_max = u.start + t_end - 1, pos_min = u.start + t0;
         auto batch = [&](int j) {
           const int e = (j0 + j) * chunks + lane;
@@ -369,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           }
           now = then;
         }
-        next = (long long)__shfl_sync(0xffffffffu, ticket, 0) + cta;
+        if (!sliced) want = __shfl_sync(0xffffffffu, ticket, 0) + cta;
       }
       // copies in flight are waited for before the CTA leaves
       for (uint32_t i = kt >= kK ? kt - kK : 0; i < kt; ++i) mbar_wait(k_full + 8 * (i % kK), (i / kK) & 1u, a.status);
@@ -718,18 +783,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         const bool direct = parts == 1 && !it.local;
         const bool bad = x.bad_item == (int)n;
         const int b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
-        const int64_t slot = it.local ? p.slots + 4 * blockIdx.x + 2 * (n & 1u) + w : it.part[w];
+        const int64_t slot = it.local ? p.slots + 4 * blockIdx.x + 2 * (n & 1u) + w : it.part + w;
         float *po = p.part_o + (slot * rows_tile + r) * kD;
         const int64_t row = ((int64_t)b * a.T + token) * a.Hq + h0 + head;
         uint16_t *dst = p.out + b * p.os[0] + token * p.os[1] + (h0 + head) * p.os[2];
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (some) {
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 4; ++h) {
             float o[32];
             if (cw > 0) {
               tmem_ld32(o_at + 32 * h, o);
               tmem_wait_ld();
+              tmem_ready(o);
             }
             if (cw == 0 || l == 0.f) {
 #pragma unroll
@@ -771,22 +837,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         tc_fence_before();        // O is read before the next item's first product overwrites it
 
         bool join = false;
-        int join_w = quarter, join_n = 4, n_parts = parts, stride = p.pairs;
-        int64_t first = it.part0[w];
+        int join_w = quarter, join_n = 4, n_parts = parts;
+        const int64_t own = p.slots + 4 * blockIdx.x + 2 * (n & 1u);
+        // the slot of the row tile's part q, in the ranges' order
+        auto slot_of = [&](int q) -> int64_t {
+          if (it.local) return own + q;
+          return p.pairs == 2 ? it.part0 + 2 * q + w : slice_slot(it.part0 + (q >> 1), q < 2, q & 1);
+        };
         if (it.local) {
           // both streams' sums are in place: their warps share the rows
           __threadfence_block();
           __syncwarp();
           if (lane == 0) mbar_arrive(joined);
           join = true;
-          first = p.slots + 4 * blockIdx.x + 2 * (n & 1u), n_parts = 2, stride = 1;
-          join_w = warp, join_n = 8;
+          n_parts = 2, join_w = warp, join_n = 8;
         } else if (parts > 1) {
           const int arrivals = parts;
           asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
           if (quarter == 0 && lane == 0) {
             __threadfence();
-            int32_t *ctr = p.w.ctr + 2 + it.cut[w];
+            int32_t *ctr = p.w.ctr + 2 + it.cut + (p.pairs == 2 ? w : 0);
             x.last[w] = atomicAdd(ctr, 1) == arrivals - 1;
             if (x.last[w]) *ctr = 0;
             __threadfence();
@@ -799,39 +869,63 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             ok = wait_warp(joined, n_joined++);
             if (!ok) break;
           }
+          // four rows at a time, so that four parts of them are on their way at once; lane 8 j + q
+          // holds the statistics of row j's part q (of eight)
           const int t_first = it.t0 + (p.pairs == 2 ? w * a.tt : 0);
           const int rows = min(rows_tile, (it.len - t_first) * a.G);
-          for (int k = join_w; k < rows; k += join_n) {
-            float top = -INFINITY;
-            for (int q = lane; q < n_parts; q += 32) top = fmaxf(top, __ldcg(&p.part_ml[(first + q * stride) * rows_tile + k]).x);
+          auto stats = [&](int k, int q) { return q < n_parts ? __ldcg(&p.part_ml[slot_of(q) * rows_tile + k]) : make_float2(-INFINITY, 0.f); };
+          for (int k0 = 4 * join_w; k0 < rows; k0 += 4 * join_n) {
+            const int k = min(k0 + (lane >> 3), rows - 1), q8 = lane & 7;
+            float4 v[4][4], acc[4];
+            auto load = [&](int q0) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              for (int q = 0; q < 4; ++q) {
+                const float *from = p.part_o + slot_of(min(q0 + q, n_parts - 1)) * rows_tile * kD + 4 * lane;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j][q] = __ldcg(reinterpret_cast<const float4 *>(from + min(k0 + j, rows - 1) * kD));
+              }
+            };
+            load(0);
+            float2 ml = stats(k, q8);
+            float top = ml.x;
+            for (int q = q8 + 8; q < n_parts; q += 8) top = fmaxf(top, stats(k, q).x);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
             const float ref = top == -INFINITY ? 0.f : top;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float total = 0.f;
-            for (int q0 = 0; q0 < n_parts; q0 += 32) {
-              float f = 0.f, lq = 0.f;
-              if (q0 + lane < n_parts) {
-                const float2 ml = __ldcg(&p.part_ml[(first + (int64_t)(q0 + lane) * stride) * rows_tile + k]);
-                f = exp2_fast((ml.x - ref) * a.sl2), lq = ml.y;
+            float total = 0.f, f = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q0 = 0; q0 < n_parts; q0 += 4) {
+              if (q0 > 0) load(q0);
+              if ((q0 & 7) == 0) {
+                if (q0 > 0) ml = stats(k, q0 + q8);
+                f = exp2_fast((ml.x - ref) * a.sl2);
+                total += f * ml.y;
               }
-              const int nq = min(32, n_parts - q0);
-#pragma unroll 4
-              for (int q = 0; q < nq; ++q) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                    p.part_o + ((first + (int64_t)(q0 + q) * stride) * rows_tile + k) * kD + 4 * lane));
-                const float fq = __shfl_sync(0xffffffffu, f, q), l1 = __shfl_sync(0xffffffffu, lq, q);
-                if (l1 == 0.f) continue;                   // a part without keys
-                total += fq * l1;
-                acc.x += fq * v.x, acc.y += fq * v.y, acc.z += fq * v.z, acc.w += fq * v.w;
-              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float fq = __shfl_sync(0xffffffffu, f, 8 * j + (q0 & 4) + q);
+                  if (q0 + q < n_parts) {
+                    acc[j].x += fq * v[j][q].x, acc[j].y += fq * v[j][q].y;
+                    acc[j].z += fq * v[j][q].z, acc[j].w += fq * v[j][q].w;
+                  }
+                }
             }
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
             const float inv1 = total == 0.f ? 0.f : 1.f / total;
-            const int kt2 = t_first + k / a.G, kh = h0 + k % a.G;
-            *reinterpret_cast<uint2 *>(p.out + b * p.os[0] + kt2 * p.os[1] + kh * p.os[2] + 4 * lane) =
-                make_uint2(bf16x2(acc.x * inv1, acc.y * inv1), bf16x2(acc.z * inv1, acc.w * inv1));
-            if (p.lse && lane == 0)
-              p.lse[((int64_t)b * a.T + kt2) * a.Hq + kh] =
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float iv = __shfl_sync(0xffffffffu, inv1, 8 * j);
+              if (k0 + j < rows)
+                *reinterpret_cast<uint2 *>(p.out + b * p.os[0] + (t_first + (k0 + j) / a.G) * p.os[1] +
+                                           (h0 + (k0 + j) % a.G) * p.os[2] + 4 * lane) =
+                    make_uint2(bf16x2(acc[j].x * iv, acc[j].y * iv), bf16x2(acc[j].z * iv, acc[j].w * iv));
+            }
+            if (p.lse && q8 == 0 && k0 + (lane >> 3) < rows)
+              p.lse[((int64_t)b * a.T + t_first + k / a.G) * a.Hq + h0 + k % a.G] =
                   total == 0.f ? -INFINITY : (top == -INFINITY ? NAN : top * a.scale + logf(total));
           }
         }
@@ -854,15 +948,14 @@ struct Shape {
   int64_t slots, own;
 };
 
-Shape shape_of(int B, int T, int G, int Hkv, int cta) {
+Shape shape_of(int T, int G, int cta) {
   Shape s;
   s.tt = T < 128 / G ? T : 128 / G;
   s.pairs = T > s.tt ? 2 : 1;
   s.mt = s.pairs * s.tt;
   s.rows = s.tt * G;
-  s.slots = 12 * (int64_t)cta;
-  s.own = s.pairs == 1 ? 4 * (int64_t)cta : 0;
-  (void)B, (void)Hkv;
+  s.slots = (s.pairs == 1 ? 4 : 10) * (int64_t)cta;    // parts: 4 a slice, 2 a range of a pair
+  s.own = s.pairs == 1 ? 4 * (int64_t)cta : 0;         // of units that no slice cuts
   return s;
 }
 
@@ -870,13 +963,13 @@ Shape shape_of(int B, int T, int G, int Hkv, int cta) {
 
 int64_t extend_workspace(int B, int T, int Hq, int Hkv, int sm_count) {
   if (B == 0 || T == 0) return 0;
-  const Shape s = shape_of(B, T, Hq / Hkv, Hkv, sm_count);
+  const Shape s = shape_of(T, Hq / Hkv, sm_count);
   return (s.slots + s.own) * s.rows * (kD + 2) * 4;
 }
 
 cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t stream) {
   const PagesArgs &a = e.p;
-  const Shape s = shape_of(a.B, a.T, a.G, a.Hkv, e.sm_count);
+  const Shape s = shape_of(a.T, a.G, e.sm_count);
   ExtendParams p{};
   p.a = a;
   p.a.tt = s.tt;

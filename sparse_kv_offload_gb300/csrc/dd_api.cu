@@ -797,6 +797,7 @@ static dd_status pages_args(const dd_ctx *c, const dd_new_rows *r, const dd_page
   a.start_pos = r->start_pos, a.new_len = r->new_len;
   a.union_idx = l->union_idx, a.union_slot = l->union_slot, a.union_cnt = l->union_cnt, a.miss_count = l->miss_count;
   a.B = d.B, a.T = r->T, a.Hq = d.Hq, a.Hkv = d.Hkv, a.G = c->G, a.cs = d.cs, a.C = c->C, a.umax = c->umax;
+  a.cs_log = d.cs == 16 ? 4 : (d.cs == 32 ? 5 : 6);
   a.hot_slots = c->hot_slots, a.max_misses = c->max_misses;
   a.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kD);
   a.sl2 = a.scale * 1.4426950408889634f;

@@ -48,11 +48,17 @@ struct Item {
   int ents;                   // the list's entries that the item's last token may see
   int pos_max, pos_min;       // positions of the item's last and first token
   int c[2];                   // tiles of each stream
-  int parts[2];               // of each stream's row tile: 0 nothing to do, 1 written out, more: joined
+  int parts[2];               // of each stream's row tile: 0 nothing to write, 1 its outputs, more: a part to be joined
   int64_t part0, part;        // slots of the first range's parts and of this one's (slices: the first slice's number)
   int cut;                    // arrival counter (pairs: and the next one)
-  int local;                  // the two streams' sums are joined within the CTA
 };
+
+// A row tile to be joined.
+struct Task {
+  int unit, len, token, parts;    // its first token
+  int64_t first;
+};
+constexpr int kTasks = 24;    // of a CTA: with fewer than four left its next item is its last, if any may be cut
 
 struct Misc {
   uint64_t bars[40];
@@ -61,7 +67,8 @@ struct Misc {
   int whole[kInfo];           // every query row sees the whole tile
   int vpos[kV][8], vwhole[kV];   // the same of V's tiles
   int bad[3][128];            // lowest position of a NaN, +inf, -inf in each column of V
-  int bad_item, dead, pending, last[2];
+  Task task[kTasks];
+  int tasks, bad_item, dead, pending;
   uint32_t tmem;
 };
 
@@ -77,7 +84,6 @@ struct ExtendParams {
   float *lse;
   float *part_o;              // [slots][rows][128]
   float2 *part_ml;            // [slots][rows]: reference (a score before the factor), sum
-  int64_t slots;              // parts there is room for, before the CTAs' own
   WorkCounters w;
   int mt;                     // tokens of an item
   int pairs;                  // row tiles of an item: 1 or 2
@@ -88,15 +94,15 @@ struct Unit {
   int cnt, start, len, groups, tiles;     // groups of mt tokens; tiles of keys that the last of them may see
 };
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ int ceil_div(int a, int b) { return (int)((unsigned)(a + b - 1) / (unsigned)b); }
 
 // entries that a token may see: chunk numbers ascend, so entry i is chunk i or a later one
 __device__ __forceinline__ int entry_bound(const PagesArgs &a, const Unit &u, int token) {
-  return min(u.cnt, (u.start + token) / a.cs + 1);
+  return min(u.cnt, ((u.start + token) >> a.cs_log) + 1);
 }
 
 __device__ __forceinline__ int tiles_of(const PagesArgs &a, int entries) {
-  return max(1, ceil_div(entries * a.cs, kTileKeys));      // (a row without keys still has its zeros to write)
+  return max(1, ((entries << a.cs_log) + kTileKeys - 1) / kTileKeys);      // (a row without keys still has its zeros to write)
 }
 
 __device__ __forceinline__ Unit load_unit(const ExtendParams &p, int u) {
@@ -126,32 +132,121 @@ __device__ __forceinline__ Unit cut_part(const ExtendParams &p, const Unit &u, i
 }
 
 // Pairs of row tiles: as many as there are whole rounds of CTAs for are taken whole, in order, and the
-// rest, fewer than CTAs, is cut into ranges of at most this many tiles of keys.  Of the cuts into s = 1, 2, ..
-// ranges of the mean pair, with at most kItemsPerCta items a CTA, the one that ends first: rounds of items, each
-// its tiles and kItemCost of them for what an item costs beside (queries, sums out and in, the join), and where
-// lengths differ up to one item more.  No range is longer than a CTA's share, which keeps one long request
-// from ending alone.  With P CTAs: pairs that are cut < P, their ranges <= 5 P.
+// rest, fewer than CTAs, is cut into ranges of at most this many tiles of keys: of 1/s of the longest pair
+// for s = 1, 2, .. the one that ends first, by rounds of items, each its tiles and kItemCost of them for what an
+// item costs beside (queries, sums out and in, the join).  With P CTAs: pairs that are cut < P, their ranges
+// <= work / length + pairs <= 5 P.
 constexpr int kItemCost = 3, kItemsPerCta = 4;
 __device__ __forceinline__ int cut_of(long long work, int groups, int longest, int cta, int lane) {
   if (groups == 0) return 1;
-  const int mean = (int)max(1ll, (work + groups - 1) / groups), most = max(1, kItemsPerCta * cta / groups);
+  const int least = max(1, (int)((work + kItemsPerCta * cta - 1) / (kItemsPerCta * cta)));
   unsigned long long best = ~0ull;
-  for (int s = 1 + lane; s <= min(most, mean); s += 32) {
-    const int len = ceil_div(mean, s);
-    const unsigned long long cost = (unsigned long long)ceil_div(groups * s, cta) * (len + kItemCost) + min(len, max(0, longest - mean));
-    best = min(best, (cost << 12) | (unsigned long long)min(s, 4095));
+  for (int s = 1 + lane; s <= longest; s += 32) {
+    const int len = max(ceil_div(longest, s), least);
+    const unsigned long long items = min((unsigned long long)groups * ceil_div(longest, len), (unsigned long long)work / len + groups);
+    const unsigned long long cost = (items + cta - 1) / cta * (len + kItemCost);
+    best = min(best, (cost << 24) | (unsigned long long)(0xFFFFFF - len));
+    if (len == least) break;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = min(best, (unsigned long long)__shfl_xor_sync(0xffffffffu, best, o));
-  const int s = max(1, (int)(best & 4095ull)), len = ceil_div(mean, s);
-  return s == 1 ? max(len, (int)((work + cta - 1) / cta)) : len;
+  return 0xFFFFFF - (int)(best & 0xFFFFFFull);
 }
 
 // One row tile a unit: the units' tiles of keys, laid end to end, are cut into equal slices, one a CTA; kUnitCost
-// tiles stand before each unit's for what it costs beside.  A unit that slices cut is joined from two parts
-// a slice (the streams'): in its first slice it is the last unit, in the others the first.
+// tiles stand before each unit's for what it costs beside.  A unit that slices cut is joined from a part of
+// each: in its first slice it is the last unit, in the others the first.
 constexpr int kUnitCost = 2;
-__device__ __forceinline__ int64_t slice_slot(int64_t slice, bool first, int w) { return 4 * slice + (first ? 2 : 0) + w; }
+
+// A row tile that has several parts: o = sum_q f_q O_q / sum_q f_q l_q with f_q = 2^((m_q - m) sl2), m the largest
+// reference, in the order of the parts. 
+struct Join {
+  const float *part_o;
+  const float2 *part_ml;
+  int64_t first;
+  int pairs, parts, rows, rows_tile, G, Hq;
+  float scale, sl2;
+  uint16_t *out;              // the row tile's first row
+  int64_t os1, os2;
+  float *lse;
+};
+
+__device__ __forceinline__ int64_t slice_slot(int64_t slice, bool first) { return 2 * slice + (first ? 1 : 0); }
+
+// R rows by Q parts are on their way at once, the next rows' while these are written; lane (32 / R) j + q
+// holds the statistics of row j's part q.
+template <int R>
+__device__ __forceinline__ void join_rows(const Join &p, int join_w, int join_n) {
+  constexpr int Q = 16 / R, L = 32 / R;
+  const int lane = threadIdx.x & 31, lj = lane / L, lq = lane % L;
+  const int rows = p.rows, n_parts = p.parts;
+  auto slot_of = [&](int q) -> int64_t {
+    return p.pairs == 2 ? p.first + 2 * q : slice_slot(p.first + q, q == 0);
+  };
+  auto stats = [&](int k, int q) {
+    return q < n_parts ? __ldcg(p.part_ml + slot_of(q) * p.rows_tile + k) : make_float2(-INFINITY, 0.f);
+  };
+  float4 v[R][Q];
+  float2 ml;
+  auto load = [&](int k0, int q0) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const float *from = p.part_o + slot_of(min(q0 + q, n_parts - 1)) * p.rows_tile * kD + 4 * lane;
+#pragma unroll
+      for (int j = 0; j < R; ++j) v[j][q] = __ldcg(reinterpret_cast<const float4 *>(from + min(k0 + j, rows - 1) * kD));
+    }
+  };
+  int k0 = R * join_w;
+  if (k0 < rows) load(k0, 0), ml = stats(min(k0 + lj, rows - 1), lq);
+  while (k0 < rows) {
+    const int k = min(k0 + lj, rows - 1);
+    float top = ml.x;
+    for (int q = lq + L; q < n_parts; q += L) top = fmaxf(top, stats(k, q).x);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float total = 0.f, f = 0.f;
+    float4 acc[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q0 = 0; q0 < n_parts; q0 += Q) {
+      if (q0 > 0) load(k0, q0);
+      if (q0 % L == 0) {
+        if (q0 > 0) ml = stats(k, q0 + lq);
+        f = exp2_fast((ml.x - ref) * p.sl2);
+        total += f * ml.y;
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          const float fq = __shfl_sync(0xffffffffu, f, L * j + q0 % L + q);
+          if (q0 + q < n_parts) {
+            acc[j].x += fq * v[j][q].x, acc[j].y += fq * v[j][q].y;
+            acc[j].z += fq * v[j][q].z, acc[j].w += fq * v[j][q].w;
+          }
+        }
+    }
+    const int kn = k0 + R * join_n;
+    if (kn < rows) load(kn, 0), ml = stats(min(kn + lj, rows - 1), lq);
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const int t = k / p.G, h = k - t * p.G;
+    const int64_t to = t * p.os1 + h * p.os2;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const float iv = __shfl_sync(0xffffffffu, inv, L * j);
+      const int64_t at = __shfl_sync(0xffffffffu, to, L * j);
+      if (k0 + j < rows)
+        *reinterpret_cast<uint2 *>(p.out + at + 4 * lane) =
+            make_uint2(bf16x2(acc[j].x * iv, acc[j].y * iv), bf16x2(acc[j].z * iv, acc[j].w * iv));
+    }
+    if (p.lse && lq == 0 && k0 + lj < rows)
+      p.lse[(int64_t)t * p.Hq + h] = total == 0.f ? -INFINITY : (top == -INFINITY ? NAN : top * p.scale + logf(total));
+    k0 = kn;
+  }
+}
 
 __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ ExtendParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -163,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   const uint32_t k_full = bars, k_free = k_full + 8 * kK, v_full = k_free + 8 * kK, v_ok = v_full + 8 * kV,
                  v_free = v_ok + 8 * kV, q_full = v_free + 8 * kV, q_free = q_full + 8, s_full = q_free + 8,
                  p_half = s_full + 16, p_ready = p_half + 16, o_full = p_ready + 16, item_full = o_full + 16, item_free = item_full + 16,
-                 looked = item_free + 16, joined = looked + 16, mma_done = joined + 8;
+                 looked = item_free + 16, handed = looked + 16, taken = handed + 8, mma_done = taken + 8;
   if (tid == 0) {
     for (int i = 0; i < kK; ++i) mbar_init(k_full + 8 * i, 1), mbar_init(k_free + 8 * i, 1);
     for (int i = 0; i < kV; ++i) mbar_init(v_full + 8 * i, 1), mbar_init(v_ok + 8 * i, 1), mbar_init(v_free + 8 * i, 1);
@@ -172,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       mbar_init(looked + 8 * i, 1), mbar_init(s_full + 8 * i, 2), mbar_init(p_half + 8 * i, 4), mbar_init(p_ready + 8 * i, 4), mbar_init(o_full + 8 * i, 1);
       mbar_init(item_full + 8 * i, 1), mbar_init(item_free + 8 * i, 11);
     }
-    mbar_init(joined, 8), mbar_init(mma_done, 1);
-    x.bad_item = -1, x.dead = 0;
+    mbar_init(handed, 4), mbar_init(taken, 4), mbar_init(mma_done, 1);
+    x.bad_item = -1, x.dead = 0, x.tasks = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {
@@ -262,10 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       int want = sliced ? (int)blockIdx.x * per : (int)blockIdx.x;
       const int slice_end = want + per;
       uint32_t n_item = 0, kt = 0;
+      int tasks = 0;                                       // that this CTA may have to do
       bool ok = true;
       while (ok) {
-        int ticket = 0;
-        if (!sliced && lane == 0) ticket = atomicAdd(p.w.ctr, 1);    // the next one: on its way during this one's work
+        int ticket = INT_MAX / 2;
+        // the next one: on its way during this one's work
+        if (!sliced && lane == 0 && tasks + 4 <= kTasks) ticket = atomicAdd(p.w.ctr, 1);
         while (base_u + 32 < units && want >= items_before + items_here) {
           items_before += items_here, parts_before += parts_here, cuts_before += cuts_here, groups_before += groups_here;
           base_u += 32;
@@ -313,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           j0 = max(0, here - kUnitCost), j1 = max(0, upto - first - kUnitCost);
           const int s0 = (first + kUnitCost) / per, s1 = (first + kUnitCost + u.tiles - 1) / per;
           n_cut = s1 - s0 + 1, cut_no = s0;
-          part0 = s0, part = slice_slot(blockIdx.x, (int)blockIdx.x == s0, 0);
+          part0 = s0, part = slice_slot(blockIdx.x, (int)blockIdx.x == s0);
           want = upto;
           if (j0 >= j1) continue;                           // only of the cost before its tiles
         } else if (!end) {
@@ -370,13 +467,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           if (lo >= t_end) continue;
           const int bound = entry_bound(a, u, hi - 1);
           // with many tokens a list with gaps may hold many chunks that this token does not see yet
-          const int seen = a.T > kTileKeys ? entries_up_to(a.union_idx + list, bound, (u.start + hi - 1) / a.cs, lane) : bound;
-          const int n = max(0, min(ceil_div(seen * a.cs, kTileKeys), j1) - j0);
+          const int seen = a.T > kTileKeys ? entries_up_to(a.union_idx + list, bound, (u.start + hi - 1) >> a.cs_log, lane) : bound;
+          const int n = max(0, min(((seen << a.cs_log) + kTileKeys - 1) / kTileKeys, j1) - j0);
           ents = max(ents, seen);
           int c, parts;
           if (sliced) {
             c = w == 0 ? (n + 1) / 2 : n / 2;
-            parts = n_cut > 1 ? 2 * n_cut : (c > 0 || w == 0 ? 1 : 0);
+            parts = w == 0 ? n_cut : 0;                     // (stream 0 writes for both)
           } else {
             c = n;
             const int mine_cut = n_cut > 1 ? ceil_div(tiles_of(a, bound), cut) : 1;
@@ -389,12 +486,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           it.unit = unit, it.t0 = t0, it.start = u.start, it.len = u.len;
           it.j0 = j0, it.ents = ents;
           it.pos_max = u.start + t_end - 1, it.pos_min = u.start + t0;
-          it.local = sliced && n_cut == 1 && c1 > 0;
           it.c[0] = c0, it.c[1] = c1, it.parts[0] = parts0, it.parts[1] = parts1;
           it.part0 = part0, it.part = part, it.cut = cut_no;
           mbar_arrive(item_full + 8 * slot);
         }
         ++n_item;
+        if (n_cut > 1) tasks += 2;
 
       // K's tiles; a batch of 32 entries is loaded while the tiles before it are asked for
         const int nt = sliced ? c0 + c1 : max(c0, c1);
@@ -402,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         auto batch = [&](int j) {
           const int e = (j0 + j) * chunks + lane;
           if (e >= ents) return Entry{0, INT_MAX};
-          if (a.union_idx[list + e] > pos_max / a.cs) return Entry{0, INT_MAX};     // not seen, not looked at
+          if (a.union_idx[list + e] > pos_max >> a.cs_log) return Entry{0, INT_MAX};     // not seen, not looked at
           return load_entry(a, list, e, ents, staged);
         };
         Entry now = batch(0);
@@ -456,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         auto batch = [&](int j) {
           const int e = (j0 + j) * chunks + lane;
           if (e >= ents) return Entry{0, INT_MAX};
-          if (a.union_idx[list + e] > pos_max / a.cs) return Entry{0, INT_MAX};
+          if (a.union_idx[list + e] > pos_max >> a.cs_log) return Entry{0, INT_MAX};
           return load_entry(a, list, e, ents, staged);
         };
         Entry now = batch(0);
@@ -615,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               }
               if (hit) {
                 const int row = (e & 1023) >> 3, col0 = (e >> 10) * 64 + (((e & 7) ^ (row & 7)) << 3);
-                const int first = x.vpos[st][row / a.cs], pos = first == INT_MAX ? INT_MAX : first + row % a.cs;
+                const int first = x.vpos[st][row >> a.cs_log], pos = first == INT_MAX ? INT_MAX : first + (row & (a.cs - 1));
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                   const uint32_t v = (w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
@@ -650,7 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     const uint32_t s_at = tmem + lane_base + 128 * w, o_at = tmem + lane_base + 256 + 128 * w;
     const int tok = r / a.G, head = r % a.G;
     const bool some = 32 * quarter < rows_tile;            // of this warp's rows are query rows
-    uint32_t ns = 0, no = 0, n_joined = 0, t_base = 0;
+    uint32_t ns = 0, no = 0, n_both = 0, t_base = 0;
+    float2 *stat = reinterpret_cast<float2 *>(smem + kTileBytes);    // (one row tile leaves the second's queries' place free)
     bool ok = true;
     for (uint32_t n = 0; ok && !pending; ++n) {
       ok = wait_warp(item_full + 8 * (n & 1u), n >> 1);
@@ -690,9 +788,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             if (!whole) {
 #pragma unroll
               for (int h = 4 * half; h < 4 * half + 4; ++h) {
-                const int row0 = 16 * h, first = x.pos[t % kInfo][row0 / a.cs];
+                const int row0 = 16 * h, first = x.pos[t % kInfo][row0 >> a.cs_log];
                 // columns up to `lim` are seen
-                const int lim = first == INT_MAX ? -1 : pos - first - row0 % a.cs;
+                const int lim = first == INT_MAX ? -1 : pos - first - (row0 & (a.cs - 1));
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                   if (e > lim) s[16 * h + e] = -INFINITY;
@@ -779,15 +877,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         if (!ok) break;
         tc_fence_after();
       }
-      if (parts > 0) {
-        const bool direct = parts == 1 && !it.local;
+      const bool both = p.pairs == 1 && it.c[1] > 0;       // the streams have sums of the same rows
+      if (both && w == 1) {
+        // stream 0 takes O out of this one's columns: it has the same lanes
+        stat[r] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(handed);
+        ok = wait_warp(taken, n_both++);
+        if (!ok) break;
+      } else if (parts > 0) {
+        float f0 = 1.f, f1 = 0.f;
+        if (both) {
+          ok = wait_warp(handed, n_both++);
+          if (!ok) break;
+          tc_fence_after();
+          const float2 other = stat[r];
+          const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+          f0 = exp2_fast((m - ref) * a.sl2), f1 = exp2_fast((other.x - ref) * a.sl2);
+          m = top, l = l * f0 + other.y * f1;
+        }
         const bool bad = x.bad_item == (int)n;
         const int b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
-        const int64_t slot = it.local ? p.slots + 4 * blockIdx.x + 2 * (n & 1u) + w : it.part + w;
+        const int64_t slot = it.part + (p.pairs == 2 ? w : 0);
         float *po = p.part_o + (slot * rows_tile + r) * kD;
         const int64_t row = ((int64_t)b * a.T + token) * a.Hq + h0 + head;
         uint16_t *dst = p.out + b * p.os[0] + token * p.os[1] + (h0 + head) * p.os[2];
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (parts == 1) f0 = l == 0.f ? 0.f : f0 / l, f1 = l == 0.f ? 0.f : f1 / l;
         if (some) {
 #pragma unroll 1
           for (int h = 0; h < 4; ++h) {
@@ -797,9 +913,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               tmem_wait_ld();
               tmem_ready(o);
             }
-            if (cw == 0 || l == 0.f) {
+            const bool none = cw == 0 || l == 0.f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * f0;
+            if (both) {
+              float o1[32];
+              tmem_ld32(o_at + 128 + 32 * h, o1);
+              tmem_wait_ld();
+              tmem_ready(o1);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : fmaf(o1[e], f1, o[e]);
             }
             if (bad) {
 #pragma unroll
@@ -810,14 +933,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               }
             }
             if (valid) {
-              if (direct) {
+              if (parts == 1) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  uint4 v;
-                  v.x = bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv), v.y = bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
-                  v.z = bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv), v.w = bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
-                  *reinterpret_cast<uint4 *>(dst + 32 * h + 8 * e) = v;
-                }
+                for (int e = 0; e < 4; ++e)
+                  *reinterpret_cast<uint4 *>(dst + 32 * h + 8 * e) =
+                      make_uint4(bf16x2(o[8 * e], o[8 * e + 1]), bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                 bf16x2(o[8 * e + 4], o[8 * e + 5]), bf16x2(o[8 * e + 6], o[8 * e + 7]));
               } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -827,111 +948,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             }
           }
           if (valid) {
-            if (direct) {
+            if (parts == 1) {
               if (p.lse) p.lse[row] = l == 0.f ? -INFINITY : (m == -INFINITY ? NAN : m * a.scale + logf(l));
             } else {
               p.part_ml[slot * rows_tile + r] = make_float2(m, l);
             }
           }
         }
-        tc_fence_before();        // O is read before the next item's first product overwrites it
-
-        bool join = false;
-        int join_w = quarter, join_n = 4, n_parts = parts;
-        const int64_t own = p.slots + 4 * blockIdx.x + 2 * (n & 1u);
-        // the slot of the row tile's part q, in the ranges' order
-        auto slot_of = [&](int q) -> int64_t {
-          if (it.local) return own + q;
-          return p.pairs == 2 ? it.part0 + 2 * q + w : slice_slot(it.part0 + (q >> 1), q < 2, q & 1);
-        };
-        if (it.local) {
-          // both streams' sums are in place: their warps share the rows
-          __threadfence_block();
+        if (both) {
+          tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(joined);
-          join = true;
-          n_parts = 2, join_w = warp, join_n = 8;
-        } else if (parts > 1) {
-          const int arrivals = parts;
+          if (lane == 0) mbar_arrive(taken);
+        }
+        if (parts > 1) {
           asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
           if (quarter == 0 && lane == 0) {
             __threadfence();
             int32_t *ctr = p.w.ctr + 2 + it.cut + (p.pairs == 2 ? w : 0);
-            x.last[w] = atomicAdd(ctr, 1) == arrivals - 1;
-            if (x.last[w]) *ctr = 0;
+            if (atomicAdd(ctr, 1) == parts - 1) {
+              // the last part: joined when the CTA is through with its items
+              *ctr = 0;
+              Task &k = x.task[atomicAdd(&x.tasks, 1)];
+              k.unit = unit, k.len = it.len, k.token = it.t0 + (p.pairs == 2 ? w * a.tt : 0);
+              k.parts = parts, k.first = it.part0 + (p.pairs == 2 ? w : 0);
+            }
             __threadfence();
-          }
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
-          join = x.last[w] != 0;
-        }
-        if (join) {
-          if (it.local) {
-            ok = wait_warp(joined, n_joined++);
-            if (!ok) break;
-          }
-          // four rows at a time, so that four parts of them are on their way at once; lane 8 j + q
-          // holds the statistics of row j's part q (of eight)
-          const int t_first = it.t0 + (p.pairs == 2 ? w * a.tt : 0);
-          const int rows = min(rows_tile, (it.len - t_first) * a.G);
-          auto stats = [&](int k, int q) { return q < n_parts ? __ldcg(&p.part_ml[slot_of(q) * rows_tile + k]) : make_float2(-INFINITY, 0.f); };
-          for (int k0 = 4 * join_w; k0 < rows; k0 += 4 * join_n) {
-            const int k = min(k0 + (lane >> 3), rows - 1), q8 = lane & 7;
-            float4 v[4][4], acc[4];
-            auto load = [&](int q0) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float *from = p.part_o + slot_of(min(q0 + q, n_parts - 1)) * rows_tile * kD + 4 * lane;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j][q] = __ldcg(reinterpret_cast<const float4 *>(from + min(k0 + j, rows - 1) * kD));
-              }
-            };
-            load(0);
-            float2 ml = stats(k, q8);
-            float top = ml.x;
-            for (int q = q8 + 8; q < n_parts; q += 8) top = fmaxf(top, stats(k, q).x);
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float ref = top == -INFINITY ? 0.f : top;
-            float total = 0.f, f = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int q0 = 0; q0 < n_parts; q0 += 4) {
-              if (q0 > 0) load(q0);
-              if ((q0 & 7) == 0) {
-                if (q0 > 0) ml = stats(k, q0 + q8);
-                f = exp2_fast((ml.x - ref) * a.sl2);
-                total += f * ml.y;
-              }
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float fq = __shfl_sync(0xffffffffu, f, 8 * j + (q0 & 4) + q);
-                  if (q0 + q < n_parts) {
-                    acc[j].x += fq * v[j][q].x, acc[j].y += fq * v[j][q].y;
-                    acc[j].z += fq * v[j][q].z, acc[j].w += fq * v[j][q].w;
-                  }
-                }
-            }
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-            const float inv1 = total == 0.f ? 0.f : 1.f / total;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float iv = __shfl_sync(0xffffffffu, inv1, 8 * j);
-              if (k0 + j < rows)
-                *reinterpret_cast<uint2 *>(p.out + b * p.os[0] + (t_first + (k0 + j) / a.G) * p.os[1] +
-                                           (h0 + (k0 + j) % a.G) * p.os[2] + 4 * lane) =
-                    make_uint2(bf16x2(acc[j].x * iv, acc[j].y * iv), bf16x2(acc[j].z * iv, acc[j].w * iv));
-            }
-            if (p.lse && q8 == 0 && k0 + (lane >> 3) < rows)
-              p.lse[((int64_t)b * a.T + t_first + k / a.G) * a.Hq + h0 + k % a.G] =
-                  total == 0.f ? -INFINITY : (top == -INFINITY ? NAN : top * a.scale + logf(total));
           }
         }
       }
+      tc_fence_before();          // O is read before the next item's first product overwrites it
       __syncwarp();
       if (lane == 0) mbar_arrive(item_free + 8 * (n & 1u));
+    }
+    // ------------------------------------------------- row tiles whose last part came from here
+    asm volatile("bar.sync 3, 256;" ::: "memory");
+    const int tasks = *(volatile int *)&x.tasks;
+    for (int k = 0; k < tasks; ++k) {
+      const Task &task = x.task[k];
+      const int b = task.unit / a.Hkv, h0 = task.unit % a.Hkv * a.G;
+      Join q;
+      q.part_o = p.part_o, q.part_ml = p.part_ml, q.first = task.first, q.pairs = p.pairs, q.parts = task.parts;
+      q.rows = min(rows_tile, (task.len - task.token) * a.G), q.rows_tile = rows_tile, q.G = a.G, q.Hq = a.Hq;
+      q.scale = a.scale, q.sl2 = a.sl2;
+      q.out = p.out + b * p.os[0] + task.token * p.os[1] + h0 * p.os[2], q.os1 = p.os[1], q.os2 = p.os[2];
+      q.lse = p.lse ? p.lse + ((int64_t)b * a.T + task.token) * a.Hq + h0 : nullptr;
+      // (few rows have many parts: one warp a row)
+      if (q.rows <= 32) join_rows<1>(q, warp, 8);
+      else join_rows<4>(q, warp, 8);
     }
   }
   tc_fence_before();
@@ -945,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
 
 struct Shape {
   int tt, pairs, mt, rows;
-  int64_t slots, own;
+  int64_t slots;
 };
 
 Shape shape_of(int T, int G, int cta) {
@@ -954,8 +1017,7 @@ Shape shape_of(int T, int G, int cta) {
   s.pairs = T > s.tt ? 2 : 1;
   s.mt = s.pairs * s.tt;
   s.rows = s.tt * G;
-  s.slots = (s.pairs == 1 ? 4 : 10) * (int64_t)cta;    // parts: 4 a slice, 2 a range of a pair
-  s.own = s.pairs == 1 ? 4 * (int64_t)cta : 0;         // of units that no slice cuts
+  s.slots = (s.pairs == 1 ? 2 : 10) * (int64_t)cta;    // parts: 2 a slice, 2 a range of a pair
   return s;
 }
 
@@ -964,7 +1026,7 @@ Shape shape_of(int T, int G, int cta) {
 int64_t extend_workspace(int B, int T, int Hq, int Hkv, int sm_count) {
   if (B == 0 || T == 0) return 0;
   const Shape s = shape_of(T, Hq / Hkv, sm_count);
-  return (s.slots + s.own) * s.rows * (kD + 2) * 4;
+  return s.slots * s.rows * (kD + 2) * 4;
 }
 
 cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t stream) {
@@ -983,9 +1045,8 @@ cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t stream) {
   p.out = static_cast<uint16_t *>(e.out);
   for (int i = 0; i < 3; ++i) p.os[i] = e.out_stride[i];
   p.lse = e.lse;
-  p.slots = s.slots;
   p.part_o = e.parts;
-  p.part_ml = reinterpret_cast<float2 *>(e.parts + (s.slots + s.own) * s.rows * kD);
+  p.part_ml = reinterpret_cast<float2 *>(e.parts + s.slots * s.rows * kD);
   p.w = {e.ctr, kCtrPerCta * e.sm_count};
   p.mt = s.mt, p.pairs = s.pairs;
   cudaError_t r = set_dyn_smem((const void *)k_extend, kSmem);

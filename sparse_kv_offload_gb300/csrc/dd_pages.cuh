@@ -20,7 +20,7 @@ struct PagesArgs {
   const int32_t *start_pos, *new_len;             // [B]; new_len null: T
   const int32_t *union_idx, *union_slot;          // [B,Hkv,umax]
   const int32_t *union_cnt, *miss_count;          // [B,Hkv]; [1] or null
-  int B, T, Hq, Hkv, G, cs, C, umax;
+  int B, T, Hq, Hkv, G, cs, cs_log, C, umax;      // cs = 2^cs_log
   int tt;                                         // tokens of a tile of query rows: tt * G <= 128
   int64_t hot_slots, max_misses;
   float scale, sl2;                               // softmax scale, and times log2 e
@@ -63,7 +63,7 @@ __device__ __forceinline__ Entry load_entry(const PagesArgs &a, int64_t list, in
     set_status(a.status, DD_ERR_DEVICE_CHECK);
     return {0, INT_MAX};
   }
-  return {slot, idx * a.cs};
+  return {slot, idx << a.cs_log};
 }
 
 __device__ __forceinline__ int64_t staged_slots(const PagesArgs &a) {

@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kQ = 3;                                // tiles of queries on the way
 constexpr int kPair = 2;                             // pairs of tiles of keys on the way
+constexpr int kRec = 4;                              // records of pairs
 constexpr uint32_t kTmem = 512;                      // S: two of 128 columns for each tile of a pair
 constexpr int kItemsPerCta = 8, kMaxRun = 16;
 
@@ -40,8 +41,8 @@ struct Pair {
 
 struct Misc {
   uint64_t bars[40];
-  Pair pair[kPair];
-  alignas(16) float lse[kQ][128];   // times log2 e; +inf where there is no row
+  Pair pair[kRec];
+  alignas(16) float lse[kQ][128];   // times -log2 e; -inf where there is no row
   float sum[2][2][8];                // [buffer][stream][16 rows]
   int dead, pending;
   uint32_t tmem;
@@ -97,12 +98,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t q0 = smem_u32(smem), k0 = q0 + kQ * kTileBytes;
   const uint32_t bars = smem_u32(x.bars);
-  const uint32_t pair_full = bars, pair_free = pair_full + 8 * kPair, k_free = pair_free + 8 * kPair,
+  const uint32_t pair_full = bars, pair_free = pair_full + 8 * kRec, k_free = pair_free + 8 * kRec,
                  q_full = k_free + 8 * kPair, q_free = q_full + 8 * kQ, s_full = q_free + 8 * kQ, s_free = s_full + 32,
                  mma_done = s_free + 32;
   if (tid == 0) {
     // a pair: its record and its tiles; free again after the products (tiles) and the sums (record)
-    for (int i = 0; i < kPair; ++i) mbar_init(pair_full + 8 * i, 1), mbar_init(pair_free + 8 * i, 11), mbar_init(k_free + 8 * i, 1);
+    for (int i = 0; i < kRec; ++i) mbar_init(pair_full + 8 * i, 1), mbar_init(pair_free + 8 * i, 11);
+    for (int i = 0; i < kPair; ++i) mbar_init(k_free + 8 * i, 1);
     // a tile of queries: its copy and its log-sum-exps; free after the products and the sums
     for (int i = 0; i < kQ; ++i) mbar_init(q_full + 8 * i, 2), mbar_init(q_free + 8 * i, 9);
     for (int i = 0; i < 4; ++i) mbar_init(s_full + 8 * i, 2), mbar_init(s_free + 8 * i, 4);
@@ -231,10 +233,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       Entry now = entry(p0);
       for (int pr = p0; pr < p1; ++pr, ++n) {
         const Entry then = entry(pr + 1);
-        const uint32_t st = n % kPair;
-        if (n >= kPair) ok = wait_warp(pair_free + 8 * st, n / kPair - 1) && wait_warp(k_free + 8 * st, n / kPair - 1);
+        const uint32_t st = n % kPair, rec = n % kRec;
+        if (n >= kRec) ok = wait_warp(pair_free + 8 * rec, n / kRec - 1);
+        if (n >= kPair) ok = ok && wait_warp(k_free + 8 * st, n / kPair - 1);
         if (!ok) break;
-        Pair &r = x.pair[st];
+        Pair &r = x.pair[rec];
         // tokens before the pair's first row see none of it
         const int first = __reduce_min_sync(0xffffffffu, now.pos);
         const int from = first == INT_MAX ? INT_MAX : max(0, first - u.start - u.tok0) / a.tt;
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           r.cut = 2 * (cut0 + pr);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(pair_full + 8 * st, 2 * kTileBytes);
+        if (lane == 0) mbar_arrive_expect_tx(pair_full + 8 * rec, 2 * kTileBytes);
         __syncwarp();
         // a lane: half of the columns of one of the 2 * chunks chunks
         const int ch = lane >> 1, sl = __shfl_sync(0xffffffffu, now.slot, ch), pos = __shfl_sync(0xffffffffu, now.pos, ch);
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           const bool far = pos != INT_MAX && sl < 0;
           const uint32_t dst = k0 + (st * 2 + ch / chunks) * kTileBytes + (lane & 1) * kTileHalfBytes + ch % chunks * a.cs * 128;
           tma_load_3d(dst, far ? &p.kst : &p.k, 64 * (lane & 1), 0,
-                      pos == INT_MAX ? (int)max((int64_t)1, a.hot_slots) : (far ? -sl - 1 : sl), pair_full + 8 * st);
+                      pos == INT_MAX ? (int)max((int64_t)1, a.hot_slots) : (far ? -sl - 1 : sl), pair_full + 8 * rec);
         }
         now = then;
       }
@@ -264,56 +267,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       next = (long long)__shfl_sync(0xffffffffu, ticket, 0) + cta;
     }
     if (ok) {
-      const uint32_t st = n % kPair;
-      if (n >= kPair) ok = wait_warp(pair_free + 8 * st, n / kPair - 1) && wait_warp(k_free + 8 * st, n / kPair - 1);
+      const uint32_t rec = n % kRec;
+      if (n >= kRec) ok = wait_warp(pair_free + 8 * rec, n / kRec - 1);
       if (ok && lane == 0) {
-        x.pair[st].unit = -1;
-        mbar_arrive(pair_full + 8 * st);
+        x.pair[rec].unit = -1;
+        mbar_arrive(pair_full + 8 * rec);
       }
     }
-    // copies in flight are waited for before the CTA leaves (with the last record sent, those of
-    // the pair that had its place before are done with)
-    for (uint32_t i = n >= kPair ? n - kPair + (ok ? 1 : 0) : 0; i < n; ++i)
-      mbar_wait(pair_full + 8 * (i % kPair), (i / kPair) & 1u, a.status);
+    // copies in flight are waited for before the CTA leaves (there are no more than those of the last kPair
+    // pairs, whose records are not the last one's)
+    for (uint32_t i = n >= kPair ? n - kPair : 0; i < n; ++i)
+      mbar_wait(pair_full + 8 * (i % kRec), (i / kRec) & 1u, a.status);
   } else if (warp == 10 || warp == 11) {
     // ------------------------------------------- Q's tiles, and their log-sum-exps
     uint32_t nq = 0;
     bool ok = true;
+    // a lane's four rows of a tile: their tokens (-1: none) and places
+    int mine[4], off[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = lane + 32 * k, tok = e / a.G;
+      mine[k] = e < rows_tile ? tok : -1;
+      off[k] = tok * a.Hq + e - tok * a.G;
+    }
     for (uint32_t n = 0; ok; ++n) {
-      const uint32_t st = n % kPair;
-      ok = wait_warp(pair_full + 8 * st, n / kPair);
+      const uint32_t rec = n % kRec;
+      ok = wait_warp(pair_full + 8 * rec, n / kRec);
       if (!ok) break;
-      const Pair &r = x.pair[st];
+      const Pair &r = x.pair[rec];
       const int unit = r.unit;
       if (unit < 0) break;
       const int r1 = r.r1, tok0 = r.tok0, len = r.len, b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
       if (new_q(r.keep_q)) {
+        // (log-sum-exps are loaded two tiles ahead)
+        const float *from = p.lse + ((int64_t)b * a.T + tok0) * a.Hq + h0;
+        auto fetch = [&](int t, float (&v)[4]) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[k] = -INFINITY;
+            if (warp == 11 && t < r1 && mine[k] >= 0 && tok0 + t * a.tt + mine[k] < len) v[k] = from[(int64_t)t * a.tt * a.Hq + off[k]];
+          }
+        };
+        float v[2][4];
+        fetch(r.r0, v[0]), fetch(r.r0 + 1, v[1]);
         for (int t = r.r0; t < r1; ++t, ++nq) {
           const uint32_t sq = nq % kQ;
           if (nq >= kQ) ok = wait_warp(q_free + 8 * sq, nq / kQ - 1);
           if (!ok) break;
-          const int first = tok0 + t * a.tt;
           if (warp == 10) {
             if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * sq, (uint32_t)(rows_tile * 256));
             __syncwarp();
-            if (lane < 2) tma_load_4d(q0 + sq * kTileBytes + lane * kTileHalfBytes, &p.q, 64 * lane, h0, first, b, q_full + 8 * sq);
+            if (lane < 2)
+              tma_load_4d(q0 + sq * kTileBytes + lane * kTileHalfBytes, &p.q, 64 * lane, h0, tok0 + t * a.tt, b, q_full + 8 * sq);
           } else {
+            // a row without keys (-inf) has no weights, nor has what is no row: 2^-inf
 #pragma unroll
-            for (int e = lane; e < 128; e += 32) {
-              float v = INFINITY;                          // no row: weight 2^-inf
-              if (e < rows_tile && first + e / a.G < len) {
-                v = p.lse[((int64_t)b * a.T + first + e / a.G) * a.Hq + h0 + e % a.G];
-                v = v == -INFINITY ? INFINITY : v * 1.4426950408889634f;   // a row without keys has no weights
-              }
-              x.lse[sq][e] = v;
-            }
+            for (int k = 0; k < 4; ++k) x.lse[sq][lane + 32 * k] = v[0][k] == -INFINITY ? -INFINITY : v[0][k] * -1.4426950408889634f;
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full + 8 * sq);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[0][k] = v[1][k];
+            fetch(t + 2, v[1]);
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(pair_free + 8 * st);
+      if (lane == 0) mbar_arrive(pair_free + 8 * rec);
     }
     if (warp == 10)
       for (uint32_t i = nq >= kQ ? nq - kQ : 0; i < nq; ++i) mbar_wait(q_full + 8 * (i % kQ), (i / kQ) & 1u, a.status);
@@ -324,11 +343,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     uint32_t nq = 0, ns = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
-      const uint32_t st = n % kPair;
-      ok = wait_warp(pair_full + 8 * st, n / kPair);
+      const uint32_t rec = n % kRec;
+      ok = wait_warp(pair_full + 8 * rec, n / kRec);
       if (!ok) break;
-      const Pair &r = x.pair[st];
+      const Pair &r = x.pair[rec];
       if (r.unit < 0) break;
+      const uint32_t st = n % kPair;
       const int r1 = r.r1, keep = r.keep_q;
       for (int t = r.r0; t < r1; ++t, ++ns) {
         if (new_q(keep)) ok = wait_warp(q_full + 8 * (nq % kQ), nq / kQ);
@@ -358,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       if (!ok) break;
       if (elect_lane()) tc_commit(k_free + 8 * st);
       __syncwarp();
-      if (lane == 0) mbar_arrive(pair_free + 8 * st);
+      if (lane == 0) mbar_arrive(pair_free + 8 * rec);
     }
     if (elect_lane()) tc_commit(mma_done);
     __syncwarp();
@@ -370,14 +390,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     uint32_t nq = 0, ns = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
-      const uint32_t st = n % kPair;
-      ok = wait_warp(pair_full + 8 * st, n / kPair);
+      const uint32_t rec = n % kRec;
+      ok = wait_warp(pair_full + 8 * rec, n / kRec);
       if (!ok) break;
-      const Pair &r = x.pair[st];
+      const Pair &r = x.pair[rec];
       const int unit = r.unit;
       if (unit < 0) break;
       const int r0 = r.r0, r1 = r.r1, keep = r.keep_q;
       const int first = r.pos[w * chunks + key / a.cs], pos = first == INT_MAX ? INT_MAX : first + key % a.cs;
+      // what the chunks hold so far is on its way meanwhile
+      const int at = quarter == 0 && lane < chunks ? r.pos[w * chunks + lane] : INT_MAX;
+      float *const to = p.weight + (int64_t)unit * a.C + (at == INT_MAX ? 0 : at >> a.cs_log);
+      const float old = at != INT_MAX && p.decay != 0.f && r.parts == 1 ? *to : 0.f;
       float total = 0.f;
       for (int t = r0; t < r1; ++t, ++ns) {
         const uint32_t sq = nq % kQ, buf = ns & 1u;
@@ -391,19 +415,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         const bool whole = __all_sync(0xffffffffu, lo == 0 && cols == rows_tile);
         const float *ls = x.lse[sq];
         const uint32_t at = tmem + lane_base + 256 * w + 128 * buf;
+        // 32 columns at a time, the next ones on their way
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float s[2][32];
+        tmem_ld32(at, s[0]);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           if (32 * h >= cols) break;
-          float s[32];
-          tmem_ld32(at + 32 * h, s);
           tmem_wait_ld();
+          tmem_ready(s[h & 1]);
+          if (h < 3 && 32 * h + 32 < cols) tmem_ld32(at + 32 * h + 32, s[(h + 1) & 1]);
+          const float *v = s[h & 1];
           if (whole) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float4 z = *reinterpret_cast<const float4 *>(ls + 32 * h + 4 * e);
-              float2 y0 = fma2(make_float2(s[4 * e], s[4 * e + 1]), make_float2(a.sl2, a.sl2), make_float2(-z.x, -z.y));
-              float2 y1 = fma2(make_float2(s[4 * e + 2], s[4 * e + 3]), make_float2(a.sl2, a.sl2), make_float2(-z.z, -z.w));
+              float2 y0 = fma2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(a.sl2, a.sl2), make_float2(z.x, z.y));
+              float2 y1 = fma2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(a.sl2, a.sl2), make_float2(z.z, z.w));
               y0.x = exp2_fast(y0.x), y0.y = exp2_fast(y0.y), y1.x = exp2_fast(y1.x), y1.y = exp2_fast(y1.y);
               sum[0] = add2(sum[0], y0), sum[1] = add2(sum[1], y1);
             }
@@ -411,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const int c = 32 * h + e;
-              const float y = exp2_fast(fmaf(s[e], a.sl2, -ls[c]));
+              const float y = exp2_fast(fmaf(v[e], a.sl2, ls[c]));
               if (c >= lo && c < cols) sum[e & 1].x += y;
             }
           }
@@ -431,39 +459,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
       if ((lane & 15) == 0) x.sum[n & 1u][w][2 * quarter + (lane >> 4)] = total;
       asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+      const int parts = r.parts, part0 = r.part0, part = r.part, cut = r.cut;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_free + 8 * rec);
       if (quarter == 0) {
         float v = 0.f;
-        int at = INT_MAX;
-        if (lane < chunks) {
+        if (lane < chunks)
           for (int i = 0; i < a.cs / 16; ++i) v += x.sum[n & 1u][w][lane * (a.cs / 16) + i];
-          at = r.pos[w * chunks + lane];
-        }
-        bool done = true;
-        if (r.parts > 1) {
-          if (lane < chunks) __stcg(p.parts + (int64_t)r.part * 16 + w * 8 + lane, v);
+        if (parts == 1) {
+          if (at != INT_MAX) *to = p.decay == 0.f ? v : fmaf(p.decay, old, v);
+        } else {
+          if (lane < chunks) __stcg(p.parts + (int64_t)part * 16 + w * 8 + lane, v);
           __syncwarp();
           int last = 0;
           if (lane == 0) {
             __threadfence();
-            int32_t *ctr = p.w.ctr + 2 + r.cut + w;
-            last = atomicAdd(ctr, 1) == r.parts - 1;
+            int32_t *ctr = p.w.ctr + 2 + cut + w;
+            last = atomicAdd(ctr, 1) == parts - 1;
             if (last) *ctr = 0;
             __threadfence();
           }
-          done = __shfl_sync(0xffffffffu, last, 0) != 0;
+          last = __shfl_sync(0xffffffffu, last, 0);
           __syncwarp();
-          if (done && lane < chunks) {
+          if (last && at != INT_MAX) {
             v = 0.f;
-            for (int i = 0; i < r.parts; ++i) v += __ldcg(p.parts + (int64_t)(r.part0 + i) * 16 + w * 8 + lane);
+            for (int i = 0; i < parts; ++i) v += __ldcg(p.parts + (int64_t)(part0 + i) * 16 + w * 8 + lane);
+            *to = p.decay == 0.f ? v : fmaf(p.decay, *to, v);
           }
         }
-        if (done && at != INT_MAX) {
-          float *to = p.weight + (int64_t)unit * a.C + at / a.cs;
-          *to = p.decay == 0.f ? v : fmaf(p.decay, *to, v);
-        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pair_free + 8 * st);
     }
   }
   tc_fence_before();

@@ -522,11 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             if (lane == 0) mbar_arrive_expect_tx(k_full + 8 * st, kTileBytes);
             __syncwarp();
             if (lane < 2 * chunks) {
-              // half of a chunk's columns: rows behind the pool's last read as zeros
-              const bool far = pos != INT_MAX && sl < 0;
-              const uint32_t dst = k0 + st * kTileBytes + (lane & 1) * kTileHalfBytes + (lane >> 1) * a.cs * 128;
-              tma_load_3d(dst, far ? &p.kst : &p.k, 64 * (lane & 1), 0,
-                          pos == INT_MAX ? (int)max((int64_t)1, a.hot_slots) : (far ? -sl - 1 : sl), k_full + 8 * st);
+                load_chunk(p.k, p.kst, a, sl, pos, lane & 1, k0 + st * kTileBytes + (lane >> 1) * a.cs * 128, k_full + 8 * st);
             }
           }
           now = then;
@@ -587,10 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             if (lane == 0) mbar_arrive_expect_tx(v_full + 8 * st, kTileBytes);
             __syncwarp();
             if (lane < 2 * chunks) {
-              const bool far = pos != INT_MAX && sl < 0;
-              const uint32_t dst = v0 + st * kTileBytes + (lane & 1) * kTileHalfBytes + (lane >> 1) * a.cs * 128;
-              tma_load_3d(dst, far ? &p.vst : &p.v, 64 * (lane & 1), 0,
-                          pos == INT_MAX ? (int)max((int64_t)1, a.hot_slots) : (far ? -sl - 1 : sl), v_full + 8 * st);
+              load_chunk(p.v, p.vst, a, sl, pos, lane & 1, v0 + st * kTileBytes + (lane >> 1) * a.cs * 128, v_full + 8 * st);
             }
           }
           now = then;

@@ -90,11 +90,13 @@ __device__ __forceinline__ int entries_up_to(const int32_t *idx, int n, int last
   return lo;
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
+// Half of the columns of a chunk into a tile; a chunk that is not there (position INT_MAX) becomes zeros, as rows
+// behind a pool's last read as zeros.
+__device__ __forceinline__ void load_chunk(const CUtensorMap &hot, const CUtensorMap &far, const PagesArgs &a, int slot,
+                                           int pos, int half, uint32_t dst, uint32_t bar) {
+  const bool staged = pos != INT_MAX && slot < 0;
+  const int64_t row = pos == INT_MAX ? (a.hot_slots > 0 ? a.hot_slots : 1) : (staged ? -(int64_t)slot - 1 : slot);
+  tma_load_2d(dst + half * kTileHalfBytes, staged ? &far : &hot, 64 * half, (int)row << a.cs_log, bar);
 }
 
 // One thread of a converged warp, the same one every time.
@@ -229,7 +231,7 @@ __device__ __forceinline__ void leave_counters(const WorkCounters &w, int32_t *s
 constexpr int kCtrPerCta = 32;      // arrival counters per CTA of the grid (one CTA an SM)
 
 // host: tensor maps (bf16, 128-byte swizzle), made anew for every call (dd_tmap.cu)
-// A pool [slots, cs, 128], boxes of one slot's rows x 64 columns; slot number `slots` reads as zeros.
+// A pool [slots * cs, 128] (below 2^31 rows), boxes of one slot's rows x 64 columns; rows behind the last read as zeros.
 bool make_pages_map(CUtensorMap *map, const void *base, int64_t slots, int cs);
 // Query rows [B, T, Hq, 128] with strides in elements, boxes of 64 columns x G heads x tt tokens.
 bool make_rows_map(CUtensorMap *map, const void *q, const int64_t *stride, int B, int T, int Hq, int G, int tt);

@@ -101,11 +101,11 @@ bool make_q_map(CUtensorMap *map, const void *q, int B, int n_q, int Hq, int G) 
 bool make_pages_map(CUtensorMap *map, const void *base, int64_t slots, int cs) {
   auto enc = tensor_map_encoder();
   if (!enc || base == nullptr || slots <= 0) return false;
-  cuuint64_t dims[3] = {128, (cuuint64_t)cs, (cuuint64_t)slots};
-  cuuint64_t strides[2] = {256, (cuuint64_t)cs * 256};
-  cuuint32_t box[3] = {64, (cuuint32_t)cs, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+  cuuint64_t dims[2] = {128, (cuuint64_t)slots * cs};
+  cuuint64_t strides[1] = {256};
+  cuuint32_t box[2] = {64, (cuuint32_t)cs};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

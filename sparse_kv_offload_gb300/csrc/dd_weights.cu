@@ -10,8 +10,9 @@
 // Sums are fp32, in an order that depends on the sizes alone (no atomics on values).
 //   warps 0-3, 4-7  exponentials and sums of a pair's two tiles of 128 keys
 //   warp 8          the products, two of each tile on the way in tensor memory
-//   warp 9          hands out the work and brings K's tiles (two pairs on the way)
-//   warp 10         Q's tiles (three on the way), warp 11 their log-sum-exps
+//   warp 9          hands out the work and brings the first of a pair's tiles of keys, warp 10 the second (two
+//                   pairs on the way; a warp issues a box in some 100 cycles, and chunks of 16 rows are 32 boxes a pair)
+//   warp 11         Q's tiles (three on the way) and their log-sum-exps
 //
 // An item is a run of pairs of tiles by a range of the query rows' tiles.  With few query rows (one
 // tile) the keys stream past the queries and an item is several pairs; with many, the queries
@@ -36,6 +37,7 @@ struct Pair {
   int r0, r1;                 // tiles of query rows to go through
   int keep_q;                 // one tile of queries for all pairs of the item: 1 first, 2 last, 3 both, 4 neither, 0 no
   int parts, part0, part, cut;   // ranges of rows, slots, arrival counter
+  int slot[16];               // of its chunks
   int pos[16];                // positions of the first rows of its chunks, INT_MAX where there is none
 };
 
@@ -98,15 +100,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t q0 = smem_u32(smem), k0 = q0 + kQ * kTileBytes;
   const uint32_t bars = smem_u32(x.bars);
-  const uint32_t pair_full = bars, pair_free = pair_full + 8 * kRec, k_free = pair_free + 8 * kRec,
+  const uint32_t rec_full = bars, pair_full = rec_full + 8 * kRec, pair_free = pair_full + 8 * kRec, k_free = pair_free + 8 * kRec,
                  q_full = k_free + 8 * kPair, q_free = q_full + 8 * kQ, s_full = q_free + 8 * kQ, s_free = s_full + 32,
                  mma_done = s_free + 32;
   if (tid == 0) {
     // a pair: its record and its tiles; free again after the products (tiles) and the sums (record)
-    for (int i = 0; i < kRec; ++i) mbar_init(pair_full + 8 * i, 1), mbar_init(pair_free + 8 * i, 11);
+    for (int i = 0; i < kRec; ++i)
+      mbar_init(rec_full + 8 * i, 1), mbar_init(pair_full + 8 * i, 1), mbar_init(pair_free + 8 * i, 11);
     for (int i = 0; i < kPair; ++i) mbar_init(k_free + 8 * i, 1);
     // a tile of queries: its copy and its log-sum-exps; free after the products and the sums
-    for (int i = 0; i < kQ; ++i) mbar_init(q_full + 8 * i, 2), mbar_init(q_free + 8 * i, 9);
+    for (int i = 0; i < kQ; ++i) mbar_init(q_full + 8 * i, 1), mbar_init(q_free + 8 * i, 9);
     for (int i = 0; i < 4; ++i) mbar_init(s_full + 8 * i, 2), mbar_init(s_free + 8 * i, 4);
     mbar_init(mma_done, 1);
     x.dead = 0;
@@ -153,6 +156,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   };
   auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait(bar, parity));
+  };
+  // a tile of keys: a lane brings half of the columns of a chunk (its slot and position in lane `chunk`)
+  auto load_tile = [&](int slot, int pos, uint32_t dst, uint32_t bar) {
+    const int ch = lane >> 1, sl = __shfl_sync(0xffffffffu, slot, ch), at = __shfl_sync(0xffffffffu, pos, ch);
+    if (ch < chunks) load_chunk(p.k, p.kst, a, sl, at, lane & 1, dst + ch * a.cs * 128, bar);
   };
   // whether a step of a pair takes a new tile of queries, and whether it is the tile's last
   auto new_q = [](int keep) { return keep == 0 || (keep & 1); };
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         // tokens before the pair's first row see none of it
         const int first = __reduce_min_sync(0xffffffffu, now.pos);
         const int from = first == INT_MAX ? INT_MAX : max(0, first - u.start - u.tok0) / a.tt;
-        if (lane < 2 * chunks) r.pos[lane] = now.pos;
+        if (lane < 2 * chunks) r.pos[lane] = now.pos, r.slot[lane] = now.slot;
         if (lane == 0) {
           r.unit = unit, r.start = u.start, r.len = u.len, r.tok0 = u.tok0;
           r.r0 = keep ? 0 : min(max(range0, from), range1);
@@ -253,14 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(pair_full + 8 * rec, 2 * kTileBytes);
         __syncwarp();
-        // a lane: half of the columns of one of the 2 * chunks chunks
-        const int ch = lane >> 1, sl = __shfl_sync(0xffffffffu, now.slot, ch), pos = __shfl_sync(0xffffffffu, now.pos, ch);
-        if (ch < 2 * chunks) {
-          const bool far = pos != INT_MAX && sl < 0;
-          const uint32_t dst = k0 + (st * 2 + ch / chunks) * kTileBytes + (lane & 1) * kTileHalfBytes + ch % chunks * a.cs * 128;
-          tma_load_3d(dst, far ? &p.kst : &p.k, 64 * (lane & 1), 0,
-                      pos == INT_MAX ? (int)max((int64_t)1, a.hot_slots) : (far ? -sl - 1 : sl), pair_full + 8 * rec);
-        }
+        if (lane == 0) mbar_arrive(rec_full + 8 * rec);      // (warp 10 brings the second tile)
+        load_tile(now.slot, now.pos, k0 + st * 2 * kTileBytes, pair_full + 8 * rec);
         now = then;
       }
       if (!ok) break;
@@ -271,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       if (n >= kRec) ok = wait_warp(pair_free + 8 * rec, n / kRec - 1);
       if (ok && lane == 0) {
         x.pair[rec].unit = -1;
+        mbar_arrive(rec_full + 8 * rec);
         mbar_arrive(pair_full + 8 * rec);
       }
     }
@@ -278,7 +281,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     // pairs, whose records are not the last one's)
     for (uint32_t i = n >= kPair ? n - kPair : 0; i < n; ++i)
       mbar_wait(pair_full + 8 * (i % kRec), (i / kRec) & 1u, a.status);
-  } else if (warp == 10 || warp == 11) {
+  } else if (warp == 10) {
+    // ----------------------------------------------------- K's second tile of a pair
+    bool ok = true;
+    for (uint32_t n = 0; ok; ++n) {
+      const uint32_t rec = n % kRec, st = n % kPair;
+      ok = wait_warp(rec_full + 8 * rec, n / kRec);
+      if (!ok) break;
+      const Pair &r = x.pair[rec];
+      if (r.unit < 0) break;
+      const int slot = lane < chunks ? r.slot[chunks + lane] : 0, pos = lane < chunks ? r.pos[chunks + lane] : INT_MAX;
+      load_tile(slot, pos, k0 + (st * 2 + 1) * kTileBytes, pair_full + 8 * rec);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_free + 8 * rec);
+    }
+  } else if (warp == 11) {
     // ------------------------------------------- Q's tiles, and their log-sum-exps
     uint32_t nq = 0;
     bool ok = true;
@@ -305,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             v[k] = -INFINITY;
-            if (warp == 11 && t < r1 && mine[k] >= 0 && tok0 + t * a.tt + mine[k] < len) v[k] = from[(int64_t)t * a.tt * a.Hq + off[k]];
+            if (t < r1 && mine[k] >= 0 && tok0 + t * a.tt + mine[k] < len) v[k] = from[(int64_t)t * a.tt * a.Hq + off[k]];
           }
         };
         float v[2][4];
@@ -314,28 +331,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           const uint32_t sq = nq % kQ;
           if (nq >= kQ) ok = wait_warp(q_free + 8 * sq, nq / kQ - 1);
           if (!ok) break;
-          if (warp == 10) {
-            if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * sq, (uint32_t)(rows_tile * 256));
-            __syncwarp();
-            if (lane < 2)
-              tma_load_4d(q0 + sq * kTileBytes + lane * kTileHalfBytes, &p.q, 64 * lane, h0, tok0 + t * a.tt, b, q_full + 8 * sq);
-          } else {
-            // a row without keys (-inf) has no weights, nor has what is no row: 2^-inf
+          // a row without keys (-inf) has no weights, nor has what is no row: 2^-inf
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x.lse[sq][lane + 32 * k] = v[0][k] == -INFINITY ? -INFINITY : v[0][k] * -1.4426950408889634f;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full + 8 * sq);
+          for (int k = 0; k < 4; ++k) x.lse[sq][lane + 32 * k] = v[0][k] == -INFINITY ? -INFINITY : v[0][k] * -1.4426950408889634f;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * sq, (uint32_t)(rows_tile * 256));
+          __syncwarp();
+          if (lane < 2)
+            tma_load_4d(q0 + sq * kTileBytes + lane * kTileHalfBytes, &p.q, 64 * lane, h0, tok0 + t * a.tt, b, q_full + 8 * sq);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[0][k] = v[1][k];
-            fetch(t + 2, v[1]);
-          }
+          for (int k = 0; k < 4; ++k) v[0][k] = v[1][k];
+          fetch(t + 2, v[1]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(pair_free + 8 * rec);
     }
-    if (warp == 10)
-      for (uint32_t i = nq >= kQ ? nq - kQ : 0; i < nq; ++i) mbar_wait(q_full + 8 * (i % kQ), (i / kQ) & 1u, a.status);
+    for (uint32_t i = nq >= kQ ? nq - kQ : 0; i < nq; ++i) mbar_wait(q_full + 8 * (i % kQ), (i / kQ) & 1u, a.status);
   } else if (warp == 8) {
     // -------------------------------------------------------------------- products
     const uint32_t id = idesc_bf16(128, (rows_tile + 31) / 32 * 32, 0, 0);   // (as many columns as are read)

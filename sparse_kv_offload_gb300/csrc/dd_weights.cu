@@ -10,9 +10,9 @@
 // Sums are fp32, in an order that depends on the sizes alone (no atomics on values).
 //   warps 0-3, 4-7  exponentials and sums of a pair's two tiles of 128 keys
 //   warp 8          the products, two of each tile on the way in tensor memory
-//   warp 9          hands out the work and brings the first of a pair's tiles of keys, warp 10 the second (two
-//                   pairs on the way; a warp issues a box in some 100 cycles, and chunks of 16 rows are 32 boxes a pair)
-//   warp 11         Q's tiles (three on the way) and their log-sum-exps
+//   warp 9          hands out the work and brings a third of a pair's keys, as warps 10 and 11 do (two or
+//                   three pairs on the way; a warp issues a box in some 100 cycles, and chunks of 16 rows are 32 boxes a pair)
+//   warp 11         Q's tiles (three on the way) and their log-sum-exps, too
 //
 // An item is a run of pairs of tiles by a range of the query rows' tiles.  With few query rows (one
 // tile) the keys stream past the queries and an item is several pairs; with many, the queries
@@ -24,9 +24,10 @@ namespace dd {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kSums = 8;                             // warps of exponentials and sums
+constexpr int kThreads = (kSums + 4) * 32;
 constexpr int kQ = 3;                                // tiles of queries on the way
-constexpr int kPair = 2;                             // pairs of tiles of keys on the way
+constexpr int kPairs = 3;                            // pairs of tiles of keys on the way, two with many query rows
 constexpr int kRec = 4;                              // records of pairs
 constexpr uint32_t kTmem = 512;                      // S: two of 128 columns for each tile of a pair
 constexpr int kItemsPerCta = 8, kMaxRun = 16;
@@ -50,7 +51,8 @@ struct Misc {
   uint32_t tmem;
 };
 
-constexpr size_t kTiles = (size_t)(kQ + 2 * kPair) * kTileBytes;
+constexpr size_t kTiles = (size_t)7 * kTileBytes;    // kQ tiles of queries and 2 pairs, or kQ of 32 rows and 3 pairs
+static_assert(kQ * 2 * 32 * 128 + kPairs * 2 * kTileBytes <= kTiles, "few query rows");
 constexpr size_t kSmem = kTiles + sizeof(Misc);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
@@ -98,36 +100,36 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   Misc &x = *reinterpret_cast<Misc *>(smem + kTiles);
   const PagesArgs &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const uint32_t q0 = smem_u32(smem), k0 = q0 + kQ * kTileBytes;
+  const int rows_tile = a.tt * a.G, chunks = kTileKeys / a.cs;
+  const bool few = rows_tile <= 32;
+  const uint32_t q_half = few ? 32 * 128 : kTileHalfBytes, kPair = few ? kPairs : 2;
+  const uint32_t q0 = smem_u32(smem), k0 = q0 + kQ * 2 * q_half;
   const uint32_t bars = smem_u32(x.bars);
   const uint32_t rec_full = bars, pair_full = rec_full + 8 * kRec, pair_free = pair_full + 8 * kRec, k_free = pair_free + 8 * kRec,
-                 q_full = k_free + 8 * kPair, q_free = q_full + 8 * kQ, s_full = q_free + 8 * kQ, s_free = s_full + 32,
+                 q_full = k_free + 8 * kPairs, q_free = q_full + 8 * kQ, s_full = q_free + 8 * kQ, s_free = s_full + 32,
                  mma_done = s_free + 32;
   if (tid == 0) {
     // a pair: its record and its tiles; free again after the products (tiles) and the sums (record)
     for (int i = 0; i < kRec; ++i)
-      mbar_init(rec_full + 8 * i, 1), mbar_init(pair_full + 8 * i, 1), mbar_init(pair_free + 8 * i, 11);
-    for (int i = 0; i < kPair; ++i) mbar_init(k_free + 8 * i, 1);
+      mbar_init(rec_full + 8 * i, 1), mbar_init(pair_full + 8 * i, 1), mbar_init(pair_free + 8 * i, kSums + 3);
+    for (int i = 0; i < kPairs; ++i) mbar_init(k_free + 8 * i, 1);
     // a tile of queries: its copy and its log-sum-exps; free after the products and the sums
-    for (int i = 0; i < kQ; ++i) mbar_init(q_full + 8 * i, 1), mbar_init(q_free + 8 * i, 9);
+    for (int i = 0; i < kQ; ++i) mbar_init(q_full + 8 * i, 1), mbar_init(q_free + 8 * i, kSums + 1);
     for (int i = 0; i < 4; ++i) mbar_init(s_full + 8 * i, 2), mbar_init(s_free + 8 * i, 4);
     mbar_init(mma_done, 1);
     x.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) {
+  if (warp == kSums) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&x.tmem)), "r"(kTmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  const int rows_tile = a.tt * a.G, chunks = kTileKeys / a.cs;
   // query rows behind a tile's last are never written: zeros once, and every column of S is a number
-  for (int i = 0; i < kQ; ++i)
-    for (int e = tid; e < 2 * (128 - rows_tile) * 8; e += kThreads) {
-      const int half = e / ((128 - rows_tile) * 8), rest = e % ((128 - rows_tile) * 8);
-      *reinterpret_cast<uint4 *>(smem + i * kTileBytes + half * kTileHalfBytes + rows_tile * 128 + rest * 16) =
-          make_uint4(0u, 0u, 0u, 0u);
-    }
+  const int blank = (few ? 32 : 128) - rows_tile;
+  for (int e = tid; e < kQ * 2 * blank * 8; e += kThreads)
+    *reinterpret_cast<uint4 *>(smem + e / (blank * 8) * q_half + rows_tile * 128 + e % (blank * 8) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   tc_fence_before();
   pdl_wait();
@@ -157,18 +159,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, wait(bar, parity));
   };
-  // a tile of keys: a lane brings half of the columns of a chunk (its slot and position in lane `chunk`)
-  auto load_tile = [&](int slot, int pos, uint32_t dst, uint32_t bar) {
-    const int ch = lane >> 1, sl = __shfl_sync(0xffffffffu, slot, ch), at = __shfl_sync(0xffffffffu, pos, ch);
-    if (ch < chunks) load_chunk(p.k, p.kst, a, sl, at, lane & 1, dst + ch * a.cs * 128, bar);
-  };
   // whether a step of a pair takes a new tile of queries, and whether it is the tile's last
   auto new_q = [](int keep) { return keep == 0 || (keep & 1); };
   auto last_q = [](int keep) { return keep == 0 || keep == 2 || keep == 3; };
-
+  // a third of a pair's 2 * chunks chunks: a lane brings half of the columns of one (its slot and position in the
+  // lane of the chunk's number)
+  auto load_third = [&](int third, int slot, int pos, uint32_t st, uint32_t bar) {
+    const int lo = 2 * chunks * third / 3, hi = 2 * chunks * (third + 1) / 3, ch = min(lo + (lane >> 1), 31);
+    const int sl = __shfl_sync(0xffffffffu, slot, ch), at = __shfl_sync(0xffffffffu, pos, ch);
+    if (ch < hi) load_chunk(p.k, p.kst, a, sl, at, lane & 1, k0 + (st * 2 + ch / chunks) * kTileBytes + ch % chunks * a.cs * 128, bar);
+  };
   if (pending) {
     // no work; the counters below are left all the same
-  } else if (warp == 9) {
+  } else if (warp == kSums + 1) {
     // ------------------------------------------------------- the work, and K's tiles
     const int units = a.B * a.Hkv, cta = (int)gridDim.x;
     long long pairs = 0, work = 0;
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         // tokens before the pair's first row see none of it
         const int first = __reduce_min_sync(0xffffffffu, now.pos);
         const int from = first == INT_MAX ? INT_MAX : max(0, first - u.start - u.tok0) / a.tt;
-        if (lane < 2 * chunks) r.pos[lane] = now.pos, r.slot[lane] = now.slot;
+        if (lane < 16) r.pos[lane] = now.pos, r.slot[lane] = now.slot;
         if (lane == 0) {
           r.unit = unit, r.start = u.start, r.len = u.len, r.tok0 = u.tok0;
           r.r0 = keep ? 0 : min(max(range0, from), range1);
@@ -261,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(pair_full + 8 * rec, 2 * kTileBytes);
         __syncwarp();
-        if (lane == 0) mbar_arrive(rec_full + 8 * rec);      // (warp 10 brings the second tile)
-        load_tile(now.slot, now.pos, k0 + st * 2 * kTileBytes, pair_full + 8 * rec);
+        if (lane == 0) mbar_arrive(rec_full + 8 * rec);
+        load_third(0, now.slot, now.pos, st, pair_full + 8 * rec);
         now = then;
       }
       if (!ok) break;
@@ -281,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     // pairs, whose records are not the last one's)
     for (uint32_t i = n >= kPair ? n - kPair : 0; i < n; ++i)
       mbar_wait(pair_full + 8 * (i % kRec), (i / kRec) & 1u, a.status);
-  } else if (warp == 10) {
-    // ----------------------------------------------------- K's second tile of a pair
+  } else if (warp == kSums + 2) {
+    // ------------------------------------------------------ a third of a pair's keys
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
       const uint32_t rec = n % kRec, st = n % kPair;
@@ -290,12 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       if (!ok) break;
       const Pair &r = x.pair[rec];
       if (r.unit < 0) break;
-      const int slot = lane < chunks ? r.slot[chunks + lane] : 0, pos = lane < chunks ? r.pos[chunks + lane] : INT_MAX;
-      load_tile(slot, pos, k0 + (st * 2 + 1) * kTileBytes, pair_full + 8 * rec);
+      load_third(1, r.slot[lane & 15], r.pos[lane & 15], st, pair_full + 8 * rec);
       __syncwarp();
       if (lane == 0) mbar_arrive(pair_free + 8 * rec);
     }
-  } else if (warp == 11) {
+  } else if (warp == kSums + 3) {
     // ------------------------------------------- Q's tiles, and their log-sum-exps
     uint32_t nq = 0;
     bool ok = true;
@@ -309,11 +311,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     }
     for (uint32_t n = 0; ok; ++n) {
       const uint32_t rec = n % kRec;
-      ok = wait_warp(pair_full + 8 * rec, n / kRec);
+      ok = wait_warp(rec_full + 8 * rec, n / kRec);
       if (!ok) break;
       const Pair &r = x.pair[rec];
       const int unit = r.unit;
       if (unit < 0) break;
+      load_third(2, r.slot[lane & 15], r.pos[lane & 15], n % kPair, pair_full + 8 * rec);
       const int r1 = r.r1, tok0 = r.tok0, len = r.len, b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
       if (new_q(r.keep_q)) {
         // (log-sum-exps are loaded two tiles ahead)
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           if (lane == 0) mbar_arrive_expect_tx(q_full + 8 * sq, (uint32_t)(rows_tile * 256));
           __syncwarp();
           if (lane < 2)
-            tma_load_4d(q0 + sq * kTileBytes + lane * kTileHalfBytes, &p.q, 64 * lane, h0, tok0 + t * a.tt, b, q_full + 8 * sq);
+            tma_load_4d(q0 + (sq * 2 + lane) * q_half, &p.q, 64 * lane, h0, tok0 + t * a.tt, b, q_full + 8 * sq);
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[0][k] = v[1][k];
           fetch(t + 2, v[1]);
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       if (lane == 0) mbar_arrive(pair_free + 8 * rec);
     }
     for (uint32_t i = nq >= kQ ? nq - kQ : 0; i < nq; ++i) mbar_wait(q_full + 8 * (i % kQ), (i / kQ) & 1u, a.status);
-  } else if (warp == 8) {
+  } else if (warp == kSums) {
     // -------------------------------------------------------------------- products
     const uint32_t id = idesc_bf16(128, (rows_tile + 31) / 32 * 32, 0, 0);   // (as many columns as are read)
     const uint64_t q_desc = smem_desc_sw128(q0, 16, 1024), k_desc = smem_desc_sw128(k0, 16, 1024);
@@ -372,11 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           if (!ok) break;
           tc_fence_after();
           if (elect_lane()) {
-            const uint64_t qb = q_desc + sq * (kTileBytes / 16), kb = k_desc + (st * 2 + w) * (kTileBytes / 16);
+            const uint64_t qb = q_desc + sq * (q_half / 8), kb = k_desc + (st * 2 + w) * (kTileBytes / 16);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
-              const uint32_t off = ((ks >> 2) * kTileHalfBytes + (ks & 3) * 32) / 16;
-              tc_mma(tmem + 256 * w + 128 * buf, kb + off, qb + off, id, ks > 0);
+              tc_mma(tmem + 256 * w + 128 * buf, kb + ((ks >> 2) * kTileHalfBytes + (ks & 3) * 32) / 16,
+                     qb + ((ks >> 2) * q_half + (ks & 3) * 32) / 16, id, ks > 0);
             }
             mbar_arrive(s_full + 8 * (2 * w + buf));       // (hands on the pair's and the queries' records)
             tc_commit(s_full + 8 * (2 * w + buf));
@@ -399,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     // ------------------------------------------------------- exponentials and sums
     const int w = warp >> 2, quarter = warp & 3, key = 32 * quarter + lane;
     const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+    const int key_chunk = w * chunks + (key >> a.cs_log), key_row = key & (a.cs - 1);
     uint32_t nq = 0, ns = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
@@ -408,8 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       const Pair &r = x.pair[rec];
       const int unit = r.unit;
       if (unit < 0) break;
-      const int r0 = r.r0, r1 = r.r1, keep = r.keep_q;
-      const int first = r.pos[w * chunks + key / a.cs], pos = first == INT_MAX ? INT_MAX : first + key % a.cs;
+      const int r0 = r.r0, r1 = r.r1, keep = r.keep_q, first = r.pos[key_chunk];
+      // the key's place among the counted tokens (those at or behind it see it), and how many there are
+      const int place = first == INT_MAX ? INT_MAX : first + key_row - r.start - r.tok0, counted = r.len - r.tok0;
       // what the chunks hold so far is on its way meanwhile
       const int at = quarter == 0 && lane < chunks ? r.pos[w * chunks + lane] : INT_MAX;
       float *const to = p.weight + (int64_t)unit * a.C + (at == INT_MAX ? 0 : at >> a.cs_log);
@@ -420,10 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         ok = wait_warp(s_full + 8 * (2 * w + buf), ns >> 1);
         if (!ok) break;
         tc_fence_after();
-        const int tok = r.tok0 + t * a.tt;                 // of the tile's first row
-        const int cols = min(rows_tile, (r.len - tok) * a.G);
-        // columns of tokens at or behind the key's position; S of the others may be anything
-        const int lo = pos == INT_MAX ? 128 : (int)min((int64_t)128, max((int64_t)0, (int64_t)(pos - r.start - tok) * a.G));
+        const int tok = t * a.tt;                          // of the tile's first row
+        const int cols = min(rows_tile, (counted - tok) * a.G);
+        // columns of tokens that see the key; S of the others may be anything
+        const int lo = place <= tok ? 0 : (place - tok >= a.tt ? 128 : (place - tok) * a.G);
         const bool whole = __all_sync(0xffffffffu, lo == 0 && cols == rows_tile);
         const float *ls = x.lse[sq];
         const uint32_t at = tmem + lane_base + 256 * w + 128 * buf;
@@ -439,14 +444,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           if (h < 3 && 32 * h + 32 < cols) tmem_ld32(at + 32 * h + 32, s[(h + 1) & 1]);
           const float *v = s[h & 1];
           if (whole) {
+            // all exponentials before the first sum, which would wait for its own
+            float y[32];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float4 z = *reinterpret_cast<const float4 *>(ls + 32 * h + 4 * e);
-              float2 y0 = fma2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(a.sl2, a.sl2), make_float2(z.x, z.y));
-              float2 y1 = fma2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(a.sl2, a.sl2), make_float2(z.z, z.w));
-              y0.x = exp2_fast(y0.x), y0.y = exp2_fast(y0.y), y1.x = exp2_fast(y1.x), y1.y = exp2_fast(y1.y);
-              sum[0] = add2(sum[0], y0), sum[1] = add2(sum[1], y1);
+              const float2 y0 = fma2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(a.sl2, a.sl2), make_float2(z.x, z.y));
+              const float2 y1 = fma2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(a.sl2, a.sl2), make_float2(z.z, z.w));
+              y[4 * e] = exp2_fast(y0.x), y[4 * e + 1] = exp2_fast(y0.y);
+              y[4 * e + 2] = exp2_fast(y1.x), y[4 * e + 3] = exp2_fast(y1.y);
             }
+            tmem_ready(y);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[e & 1] = add2(sum[e & 1], make_float2(y[2 * e], y[2 * e + 1]));
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -477,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       if (quarter == 0) {
         float v = 0.f;
         if (lane < chunks)
-          for (int i = 0; i < a.cs / 16; ++i) v += x.sum[n & 1u][w][lane * (a.cs / 16) + i];
+          for (int i = 0; i < a.cs >> 4; ++i) v += x.sum[n & 1u][w][lane * (a.cs >> 4) + i];
         if (parts == 1) {
           if (at != INT_MAX) *to = p.decay == 0.f ? v : fmaf(p.decay, old, v);
         } else {
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kSums) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
   }

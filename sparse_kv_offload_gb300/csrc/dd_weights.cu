@@ -14,9 +14,8 @@
 //                   three pairs on the way; a warp issues a box in some 100 cycles, and chunks of 16 rows are 32 boxes a pair)
 //   warp 11         Q's tiles (three on the way) and their log-sum-exps, too
 //
-// An item is a run of pairs of tiles by a range of the query rows' tiles.  With few query rows (one
-// tile) the keys stream past the queries and an item is several pairs; with many, the queries
-// stream past a pair.  Where the pairs alone would leave CTAs idle the rows are cut too, and
+// With few query rows (one tile) the keys stream past the queries, an equal slice of all pairs a CTA; with many, the
+// queries stream past a pair.  Where the pairs alone would leave CTAs idle the rows are cut too, and
 // a pair's parts (16 sums at most) are added up in order by whoever finishes last.
 #include "dd_pages.cuh"
 
@@ -30,7 +29,7 @@ constexpr int kQ = 3;                                // tiles of queries on the 
 constexpr int kPairs = 3;                            // pairs of tiles of keys on the way, two with many query rows
 constexpr int kRec = 4;                              // records of pairs
 constexpr uint32_t kTmem = 512;                      // S: two of 128 columns for each tile of a pair
-constexpr int kItemsPerCta = 8, kMaxRun = 16;
+constexpr int kItemsPerCta = 8;
 
 struct Pair {
   int unit, start, len;
@@ -84,15 +83,10 @@ __device__ __forceinline__ Unit load_unit(const WeightsParams &p, int u) {
   return r;
 }
 
-// Pairs of an item and tiles of rows of an item.  With P CTAs: pairs whose rows are cut <= 8 P, items of
-// those <= 16 P.
-struct Cut {
-  int run, rows;
-};
-__device__ __forceinline__ Cut cut_of(long long pairs, long long work, bool one, int cta) {
-  if (one) return {(int)max(1ll, min((long long)kMaxRun, pairs / (4ll * cta))), INT_MAX};
-  if (pairs >= (long long)kItemsPerCta * cta) return {1, INT_MAX};
-  return {1, (int)max(1ll, (work + (long long)kItemsPerCta * cta - 1) / ((long long)kItemsPerCta * cta))};
+// Tiles of query rows of an item.  With P CTAs: pairs whose rows are cut <= 8 P, items of those <= 16 P.
+__device__ __forceinline__ int rows_cut_of(long long pairs, long long work, bool one, int cta) {
+  const long long most = (long long)kItemsPerCta * cta;
+  return one || pairs >= most ? INT_MAX : (int)max(1ll, (work + most - 1) / most);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__ WeightsParams p) {
@@ -188,29 +182,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       work += __shfl_xor_sync(0xffffffffu, work, o);
     }
     one = __all_sync(0xffffffffu, one);
-    const Cut cut = cut_of(pairs, work, one, cta);
+    const int rows_cut = rows_cut_of(pairs, work, one, cta);
     const int64_t staged = staged_slots(a);
 
-    int base_u = -32;
-    long long items_before = 0, items_here = 0;
-    int cuts_before = 0, cuts_here = 0, parts_before = 0, parts_here = 0;
+    // One tile of query rows a unit: every CTA has an equal slice of all units' pairs, laid end to end.  Else
+    // items, a pair by a range of rows each, are handed out by tickets, the first by number.
+    const int per_cta = (int)((pairs + cta - 1) / cta);
+    int base_u = -32, items_before = 0, items_here = 0, cuts_before = 0, cuts_here = 0, parts_before = 0, parts_here = 0;
     Unit mine = {0, 0, 0, 0, 0, 0};
-    int runs = 0, ranges = 0, items = 0, items_pre = 0, cuts_pre = 0, parts_pre = 0;
-    long long next = blockIdx.x;
-    uint32_t n = 0;                                        // pairs so far
+    int ranges = 0, items = 0, items_pre = 0, cuts_pre = 0, parts_pre = 0;
+    int want = one ? (int)blockIdx.x * per_cta : (int)blockIdx.x;
+    const int slice_end = want + per_cta;
+    uint32_t n = 0, st = 0, round = 0;                     // pairs so far, the next one's place, times around
     bool ok = true;
     for (;;) {
-      const long long want = next;
       int ticket = 0;
-      if (lane == 0) ticket = atomicAdd(p.w.ctr, 1);
+      if (!one && lane == 0) ticket = atomicAdd(p.w.ctr, 1);
       while (base_u + 32 < units && want >= items_before + items_here) {
         items_before += items_here, cuts_before += cuts_here, parts_before += parts_here;
         base_u += 32;
         mine = {0, 0, 0, 0, 0, 0};
         if (base_u + lane < units) mine = load_unit(p, base_u + lane);
-        runs = ceil_div(mine.pairs, cut.run);
-        ranges = mine.rows ? (cut.rows >= mine.rows ? 1 : ceil_div(mine.rows, cut.rows)) : 0;
-        items = runs * ranges;
+        ranges = rows_cut >= mine.rows ? 1 : ceil_div(mine.rows, rows_cut);
+        items = mine.pairs * ranges;
         const int cuts = ranges > 1 ? mine.pairs : 0, parts = cuts * ranges;
         items_pre = warp_incl_scan(items), cuts_pre = warp_incl_scan(cuts), parts_pre = warp_incl_scan(parts);
         items_here = __shfl_sync(0xffffffffu, items_pre, 31);
@@ -218,58 +212,65 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         parts_here = __shfl_sync(0xffffffffu, parts_pre, 31);
         items_pre -= items, cuts_pre -= cuts, parts_pre -= parts;
       }
-      if (want >= items_before + items_here) break;
-      const int here = (int)(want - items_before);
+      if (want >= items_before + items_here || (one && want >= slice_end)) break;
+      const int here = want - items_before;
       const int src = __ffs((int)__ballot_sync(0xffffffffu, items_pre <= here && here < items_pre + items)) - 1;
       Unit u;
       u.cnt = __shfl_sync(0xffffffffu, mine.cnt, src), u.start = __shfl_sync(0xffffffffu, mine.start, src);
       u.len = __shfl_sync(0xffffffffu, mine.len, src), u.tok0 = __shfl_sync(0xffffffffu, mine.tok0, src);
       u.pairs = __shfl_sync(0xffffffffu, mine.pairs, src), u.rows = __shfl_sync(0xffffffffu, mine.rows, src);
-      const int n_runs = __shfl_sync(0xffffffffu, runs, src), n_ranges = __shfl_sync(0xffffffffu, ranges, src);
+      const int n_ranges = __shfl_sync(0xffffffffu, ranges, src);
       const int cut0 = cuts_before + __shfl_sync(0xffffffffu, cuts_pre, src);
       const int part0 = parts_before + __shfl_sync(0xffffffffu, parts_pre, src);
       const int rem = here - __shfl_sync(0xffffffffu, items_pre, src);
-      const int range = rem / n_runs, run = rem % n_runs;
-      const int p0 = run * cut.run, p1 = min(u.pairs, p0 + cut.run);
-      const int range0 = n_ranges > 1 ? range * cut.rows : 0;
-      const int range1 = n_ranges > 1 ? min(u.rows, range0 + cut.rows) : u.rows;
+      const int range = one ? 0 : rem / u.pairs;
+      const int p0 = one ? rem : rem - range * u.pairs, p1 = one ? min(u.pairs, rem + slice_end - want) : p0 + 1;
+      const int range0 = n_ranges > 1 ? range * rows_cut : 0;
+      const int range1 = n_ranges > 1 ? min(u.rows, range0 + rows_cut) : u.rows;
       const int unit = base_u + src;
       const int64_t list = (int64_t)unit * a.umax;
       const bool keep = one && u.len > u.tok0;
-      // the entries of a pair, one a lane; those of the next pair are loaded behind this one's copies
-      auto entry = [&](int pr) {
-        const int e = pr * 2 * chunks + lane;
-        return lane < 2 * chunks && pr < p1 ? load_entry(a, list, e, u.cnt, staged) : Entry{0, INT_MAX};
-      };
-      Entry now = entry(p0);
-      for (int pr = p0; pr < p1; ++pr, ++n) {
-        const Entry then = entry(pr + 1);
-        const uint32_t st = n % kPair, rec = n % kRec;
-        if (n >= kRec) ok = wait_warp(pair_free + 8 * rec, n / kRec - 1);
-        if (n >= kPair) ok = ok && wait_warp(k_free + 8 * st, n / kPair - 1);
-        if (!ok) break;
-        Pair &r = x.pair[rec];
-        // tokens before the pair's first row see none of it
-        const int first = __reduce_min_sync(0xffffffffu, now.pos);
-        const int from = first == INT_MAX ? INT_MAX : max(0, first - u.start - u.tok0) / a.tt;
-        if (lane < 16) r.pos[lane] = now.pos, r.slot[lane] = now.slot;
-        if (lane == 0) {
-          r.unit = unit, r.start = u.start, r.len = u.len, r.tok0 = u.tok0;
-          r.r0 = keep ? 0 : min(max(range0, from), range1);
-          r.r1 = u.len > u.tok0 ? range1 : r.r0;
-          r.keep_q = keep ? (pr == p0 ? (pr == p1 - 1 ? 3 : 1) : (pr == p1 - 1 ? 2 : 4)) : 0;
-          r.parts = n_ranges, r.part0 = part0 + pr * n_ranges, r.part = part0 + pr * n_ranges + range;
-          r.cut = 2 * (cut0 + pr);
+      // 32 entries at a time, those of the next two times on their way
+      const int two = 2 * chunks, per = 32 / two;          // pairs a time
+      auto batch = [&](int pr) { return pr < p1 ? load_entry(a, list, pr * two + lane, min(u.cnt, p1 * two), staged) : Entry{0, INT_MAX}; };
+      Entry now = batch(p0), then = batch(p0 + per);
+      for (int b = p0; ok && b < p1; b += per) {
+        const Entry later = batch(b + 2 * per);
+        for (int pr = b; pr < min(b + per, p1); ++pr, ++n) {
+          const uint32_t rec = n % kRec;
+          if (n >= kRec) ok = wait_warp(pair_free + 8 * rec, n / kRec - 1);
+          if (round > 0) ok = ok && wait_warp(k_free + 8 * st, round - 1);
+          if (!ok) break;
+          Pair &r = x.pair[rec];
+          const int from_lane = (pr - b) * two + (lane & (two - 1));
+          const int slot = __shfl_sync(0xffffffffu, now.slot, from_lane), pos = __shfl_sync(0xffffffffu, now.pos, from_lane);
+          if (lane < two) r.pos[lane] = pos, r.slot[lane] = slot;
+          if (lane == 0) {
+            r.unit = unit, r.start = u.start, r.len = u.len, r.tok0 = u.tok0;
+            r.keep_q = keep ? (pr == p0 ? (pr == p1 - 1 ? 3 : 1) : (pr == p1 - 1 ? 2 : 4)) : 0;
+            r.parts = n_ranges, r.part0 = part0 + pr * n_ranges, r.part = part0 + pr * n_ranges + range;
+            r.cut = 2 * (cut0 + pr);
+          }
+          int r0 = 0;
+          if (!keep) {
+            // tokens before the pair's first row see none of it
+            const int first = __reduce_min_sync(0xffffffffu, pos);
+            r0 = min(max(range0, first == INT_MAX ? INT_MAX : max(0, first - u.start - u.tok0) / a.tt), range1);
+          }
+          if (lane == 0) r.r0 = r0, r.r1 = u.len > u.tok0 ? range1 : r0;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(pair_full + 8 * rec, 2 * kTileBytes);
+            mbar_arrive(rec_full + 8 * rec);
+          }
+          __syncwarp();
+          load_third(0, slot, pos, st, pair_full + 8 * rec);
+          if (++st == kPair) st = 0, ++round;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(pair_full + 8 * rec, 2 * kTileBytes);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(rec_full + 8 * rec);
-        load_third(0, now.slot, now.pos, st, pair_full + 8 * rec);
-        now = then;
+        now = then, then = later;
       }
       if (!ok) break;
-      next = (long long)__shfl_sync(0xffffffffu, ticket, 0) + cta;
+      want = one ? want + p1 - p0 : __shfl_sync(0xffffffffu, ticket, 0) + cta;
     }
     if (ok) {
       const uint32_t rec = n % kRec;
@@ -286,20 +287,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       mbar_wait(pair_full + 8 * (i % kRec), (i / kRec) & 1u, a.status);
   } else if (warp == kSums + 2) {
     // ------------------------------------------------------ a third of a pair's keys
+    uint32_t st = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
-      const uint32_t rec = n % kRec, st = n % kPair;
+      const uint32_t rec = n % kRec;
       ok = wait_warp(rec_full + 8 * rec, n / kRec);
       if (!ok) break;
       const Pair &r = x.pair[rec];
       if (r.unit < 0) break;
       load_third(1, r.slot[lane & 15], r.pos[lane & 15], st, pair_full + 8 * rec);
+      if (++st == kPair) st = 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(pair_free + 8 * rec);
     }
   } else if (warp == kSums + 3) {
     // ------------------------------------------- Q's tiles, and their log-sum-exps
-    uint32_t nq = 0;
+    uint32_t nq = 0, st = 0;
     bool ok = true;
     // a lane's four rows of a tile: their tokens (-1: none) and places
     int mine[4], off[4];
@@ -316,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       const Pair &r = x.pair[rec];
       const int unit = r.unit;
       if (unit < 0) break;
-      load_third(2, r.slot[lane & 15], r.pos[lane & 15], n % kPair, pair_full + 8 * rec);
+      load_third(2, r.slot[lane & 15], r.pos[lane & 15], st, pair_full + 8 * rec);
+      if (++st == kPair) st = 0;
       const int r1 = r.r1, tok0 = r.tok0, len = r.len, b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
       if (new_q(r.keep_q)) {
         // (log-sum-exps are loaded two tiles ahead)
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     // -------------------------------------------------------------------- products
     const uint32_t id = idesc_bf16(128, (rows_tile + 31) / 32 * 32, 0, 0);   // (as many columns as are read)
     const uint64_t q_desc = smem_desc_sw128(q0, 16, 1024), k_desc = smem_desc_sw128(k0, 16, 1024);
-    uint32_t nq = 0, ns = 0;
+    uint32_t nq = 0, ns = 0, st = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
       const uint32_t rec = n % kRec;
@@ -363,7 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       if (!ok) break;
       const Pair &r = x.pair[rec];
       if (r.unit < 0) break;
-      const uint32_t st = n % kPair;
       const int r1 = r.r1, keep = r.keep_q;
       for (int t = r.r0; t < r1; ++t, ++ns) {
         if (new_q(keep)) ok = wait_warp(q_full + 8 * (nq % kQ), nq / kQ);
@@ -392,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       }
       if (!ok) break;
       if (elect_lane()) tc_commit(k_free + 8 * st);
+      if (++st == kPair) st = 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(pair_free + 8 * rec);
     }

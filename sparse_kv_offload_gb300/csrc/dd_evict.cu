@@ -6,16 +6,18 @@
 // resident chunks c with first <= c < n0 - last, the lower chunk first where weights are equal.
 // The N new chunks then take free slots, ascending both.
 //
-// One CTA a unit: weights become order keys in shared memory (a NaN below every number, -0 as
-// +0), an 8-bit radix select finds the E-th smallest, and a warp takes a run of chunks, 32 at a
-// time, so that ranks are ballots and every access is a whole line.
+// One CTA a unit, each warp a run of 32 N chunks: a lane keeps N of them in registers (slot, weight as an order
+// key: a NaN below every number, -0 as +0), read once, all loads on their way together.  A radix select over the
+// keys in digits of 11 bits finds the E-th smallest (2,048 bins spread exponents over banks, and the first two
+// digits leave one or two keys: a third is rarely looked at).  Ranks are ballots, so every access is a whole line.
 #include "dd_pages.cuh"
 
 namespace dd {
 
 namespace {
 
-enum : uint8_t { kAbsent = 0, kStays = 1, kMay = 2, kNew = 3 };
+enum : uint32_t { kAbsent = 0, kStays = 1, kMay = 2, kNew = 3 };
+constexpr int kDigit = 11, kBins = 1 << kDigit;
 
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (w != w) return 0u;
@@ -43,19 +45,16 @@ __device__ __forceinline__ Counts warp_prefix(Counts v, int (*scratch)[33], Coun
   return r;
 }
 
+template <int N>
 __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t sm[];
-  uint32_t *key = sm;                                        // [C]
-  uint16_t *free_slot = reinterpret_cast<uint16_t *>(sm);    // [S], then owners [S], once the keys are done with
   const int words = (a.S + 31) / 32;
-  const int front = max(a.C, a.S + 1);
-  uint32_t *used = sm + front;                               // [words]
-  uint8_t *state = reinterpret_cast<uint8_t *>(used + words);   // [C]
-  uint16_t *owner = free_slot + a.S;
+  uint32_t *hist = sm;                                       // [kBins]
+  uint32_t *used = sm + kBins;                               // [words] slots held
+  uint16_t *free_slot = reinterpret_cast<uint16_t *>(used + words), *owner = free_slot + a.S;   // [S] each
   __shared__ int scratch[3][33];
-  __shared__ uint32_t hist[256];
   __shared__ int s_bad;
-  __shared__ uint32_t s_digit, s_rank;
+  __shared__ uint32_t s_digit, s_rank, s_count;
 
   pdl_wait();
   pdl_trigger();
@@ -64,30 +63,34 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
   const int b = u / a.Hkv;
   const int64_t row = (int64_t)u * a.C, base = (int64_t)u * a.S;
   const int kv = a.kv_len[b], more = a.new_len ? a.new_len[b] : 0;
+  const int c0 = warp * 32 * N + lane;
+  const uint32_t below = (1u << lane) - 1u;
+  int32_t slot[N];
+  uint32_t key[N], state = 0u;                               // state: two bits a chunk
+#pragma unroll
+  for (int k = 0; k < N; ++k) slot[k] = c0 + 32 * k < a.C ? a.resident_slot[row + c0 + 32 * k] : -1;
+#pragma unroll
+  for (int k = 0; k < N; ++k) key[k] = c0 + 32 * k < a.C ? order_key(a.weight[row + c0 + 32 * k]) : 0u;
   bool bad = kv < 0 || more < 0 || (int64_t)kv + more > (int64_t)a.C * a.cs;
   const int n0 = bad ? 0 : (kv + a.cs - 1) / a.cs, n1 = bad ? 0 : (kv + more + a.cs - 1) / a.cs;
-  const int seg = ((a.C + 31) / 32 + warps - 1) / warps * 32, lo = min(a.C, warp * seg), hi = min(a.C, lo + seg);
 
   if (tid == 0) s_bad = 0;
   for (int i = tid; i < words; i += blockDim.x) used[i] = 0u;
   __syncthreads();
   Counts n = {0, 0, 0};                                      // resident, new, candidates
-  for (int c0 = lo; c0 < hi; c0 += 32) {
-    const int c = c0 + lane;
-    uint8_t st = kAbsent;
-    if (c < hi) {
-      const int64_t s = a.resident_slot[row + c];
-      if (s >= 0) {
-        const int64_t k = s - base;
-        // a slot of another unit, or of two chunks
-        if (k < 0 || k >= a.S || (atomicOr(&used[k >> 5], 1u << (k & 31)) >> (k & 31) & 1u)) s_bad = 1;
-        st = c >= a.first && c < n0 - a.last ? kMay : kStays;
-      } else if (c >= n0 && c < n1) {
-        st = kNew;
-      }
-      state[c] = st;
-      key[c] = st == kMay ? order_key(a.weight[row + c]) : 0xFFFFFFFFu;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int c = c0 + 32 * k;
+    uint32_t st = kAbsent;
+    if (slot[k] >= 0) {
+      const int64_t s = slot[k] - base;
+      // a slot of another unit, or of two chunks
+      if (s < 0 || s >= a.S || (atomicOr(&used[s >> 5], 1u << (s & 31)) >> (s & 31) & 1u)) s_bad = 1;
+      st = c >= a.first && c < n0 - a.last ? kMay : kStays;
+    } else if (c >= n0 && c < n1 && c < a.C) {
+      st = kNew;
     }
+    state |= st << (2 * k);
     n.a += __popc(__ballot_sync(0xffffffffu, st == kStays || st == kMay));
     n.b += __popc(__ballot_sync(0xffffffffu, st == kNew));
     n.c += __popc(__ballot_sync(0xffffffffu, st == kMay));
@@ -102,122 +105,123 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
       if (a.evicted_cnt) a.evicted_cnt[u] = 0;
       if (a.list_cnt) a.list_cnt[u] = 0;
     }
-    for (int c = tid; c < a.C; c += blockDim.x) a.resident_out[row + c] = a.resident_slot[row + c];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (c0 + 32 * k < a.C) a.resident_out[row + c0 + 32 * k] = slot[k];
     return;
   }
   const int leave = min(max(all.a + all.b - a.keep, 0), all.c);
 
-  // the leave-th smallest key of the candidates, and how many equal to it leave
+  // the digits of the leave-th smallest key, from the top, until all keys that share them leave
+  int shift = 32;
   uint32_t bound = 0u, rank = (uint32_t)leave;               // of those that share the digits found so far
-  if (leave > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += blockDim.x) hist[i] = 0u;
-      __syncthreads();
-      for (int c0 = lo; c0 < hi; c0 += 32) {
-        const int c = c0 + lane;
-        if (c < hi && state[c] == kMay) {
-          const uint32_t k = key[c];
-          if (shift == 24 || (k >> (shift + 8)) == (bound >> (shift + 8))) atomicAdd(&hist[k >> shift & 255u], 1u);
-        }
-      }
-      __syncthreads();
-      if (warp == 0) {
-        uint32_t sum = 0, v[8];
+  bool ties = leave > 0;
+  for (int width = kDigit; ties && shift > 0; ) {
+    const int next = max(0, shift - width);
+    for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0u;
+    __syncthreads();
+    const uint32_t mask = (1u << (shift - next)) - 1u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = hist[8 * lane + i], sum += v[i];
-        uint32_t before = (uint32_t)warp_incl_scan((int)sum) - sum;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (before < rank && rank <= before + v[i]) s_digit = 8 * lane + i, s_rank = rank - before;
-          before += v[i];
-        }
+    for (int k = 0; k < N; ++k)
+      if ((state >> (2 * k) & 3u) == kMay && (shift == 32 || key[k] >> shift == bound))
+        atomicAdd(&hist[key[k] >> next & mask], 1u);
+    __syncthreads();
+    // (at most 16 bins a thread: there are 128 threads or more)
+    const int per = kBins / blockDim.x > 0 ? kBins / blockDim.x : 1, from = tid * per;
+    int sum = 0;
+    if (from < kBins)
+      for (int i = 0; i < per; ++i) sum += (int)hist[from + i];
+    Counts t, mine = {0, 0, 0};
+    const int incl = warp_incl_scan(sum);
+    mine.a = __shfl_sync(0xffffffffu, incl, 31);
+    uint32_t before = (uint32_t)(warp_prefix(mine, scratch, t, warp, lane, warps).a + incl - sum);
+    if (from < kBins && before < rank && rank <= before + (uint32_t)sum)
+      for (int i = 0; i < per; ++i) {
+        const uint32_t v = hist[from + i];
+        if (before < rank && rank <= before + v) s_digit = from + i, s_rank = rank - before, s_count = v;
+        before += v;
       }
-      __syncthreads();
-      bound |= s_digit << shift;
-      rank = s_rank;
-    }
+    __syncthreads();
+    bound = shift == 32 ? s_digit : bound << (shift - next) | s_digit;
+    rank = s_rank, ties = s_count != s_rank, shift = next;
   }
 
-  // ties at the bound leave in chunk order
+  // the first `rank` of the keys that share the digits leave, in chunk order
   Counts m = {0, 0, 0};
-  if (leave > 0)
-    for (int c0 = lo; c0 < hi; c0 += 32) {
-      const int c = c0 + lane;
-      m.a += __popc(__ballot_sync(0xffffffffu, c < hi && state[c] == kMay && key[c] == bound));
-    }
-  int ties = warp_prefix(m, scratch, all, warp, lane, warps).a;
+  if (ties)
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      m.a += __popc(__ballot_sync(0xffffffffu, (state >> (2 * k) & 3u) == kMay && key[k] >> shift == bound));
+  int tied = ties ? warp_prefix(m, scratch, all, warp, lane, warps).a : 0;
   m = {0, 0, 0};                                             // leaving, new, staying
-  for (int c0 = lo; c0 < hi; c0 += 32) {
-    const int c = c0 + lane;
-    const uint8_t st = c < hi ? state[c] : (uint8_t)kAbsent;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint32_t st = state >> (2 * k) & 3u;
     bool go = false;
     if (leave > 0) {
-      const bool tie = st == kMay && key[c] == bound;
+      const uint32_t top = key[k] >> shift;
+      const bool tie = st == kMay && top == bound;
       const uint32_t in = __ballot_sync(0xffffffffu, tie);
-      go = st == kMay && (key[c] < bound || (tie && ties + __popc(in & ((1u << lane) - 1u)) < (int)rank));
-      ties += __popc(in);
+      go = st == kMay && (top < bound || (tie && (!ties || tied + __popc(in & below) < (int)rank)));
+      tied += __popc(in);
     }
     if (go) {
-      const int k = (int)(a.resident_slot[row + c] - base);
-      atomicAnd(&used[k >> 5], ~(1u << (k & 31)));
+      const int s = (int)(slot[k] - base);
+      atomicAnd(&used[s >> 5], ~(1u << (s & 31)));
     }
     // (from here on: kMay leaves)
-    if (c < hi) state[c] = st == kMay && !go ? (uint8_t)kStays : st;
+    if (st == kMay && !go) state ^= (kMay ^ kStays) << (2 * k);
     m.a += __popc(__ballot_sync(0xffffffffu, go));
     m.b += __popc(__ballot_sync(0xffffffffu, st == kNew));
     m.c += __popc(__ballot_sync(0xffffffffu, st == kStays || (st == kMay && !go)));
   }
   const Counts pre = warp_prefix(m, scratch, all, warp, lane, warps);
 
-  // the free slots, ascending (the keys are done with)
-  int taken_by = 0;
+  // the free slots, ascending: a thread a word of 32
+  int n_free = 0;
   {
-    int f = 0;
-    uint32_t w = 0;
-    for (int i = warp * 32; i < words; i += warps * 32) {    // at most 512 words: one each
-      const int k = i + lane;
-      if (k < words) {
-        w = ~used[k];
-        if (k == words - 1 && (a.S & 31)) w &= (1u << (a.S & 31)) - 1u;
-      }
-      f = __popc(w);
+    uint32_t w = 0u;
+    if (tid < words) {
+      w = ~used[tid];
+      if (tid == words - 1 && (a.S & 31)) w &= (1u << (a.S & 31)) - 1u;
     }
-    const int incl = warp_incl_scan(f);
+    const int f = __popc(w), incl = warp_incl_scan(f);
     Counts t, fc = {__shfl_sync(0xffffffffu, incl, 31), 0, 0};
     int at = warp_prefix(fc, scratch, t, warp, lane, warps).a + incl - f;
-    taken_by = t.a;
-    const int k = warp * 32 + lane;
+    n_free = t.a;
     while (w) {
       const int bit = __ffs((int)w) - 1;
       w &= w - 1;
-      free_slot[at++] = (uint16_t)(32 * k + bit);
+      if (at < all.b) free_slot[at] = (uint16_t)(32 * tid + bit);
+      ++at;
     }
     for (int i = tid; i < a.S; i += blockDim.x) owner[i] = 0xFFFFu;
   }
   __syncthreads();
-  if (all.b > taken_by && tid == 0) set_status(a.status, DD_ERR_CAPACITY);
-  const int given = min(all.b, taken_by);
+  if (all.b > n_free && tid == 0) set_status(a.status, DD_ERR_CAPACITY);
+  const int given = min(all.b, n_free);
 
-  // lists need the new chunks that have got a slot: they are behind n0, among the residents there
+  // (new chunks lie behind n0, among the residents there)
   int gone = pre.a, fresh = pre.b, stay = pre.c;
-  for (int c0 = lo; c0 < hi; c0 += 32) {
-    const int c = c0 + lane;
-    const uint8_t st = c < hi ? state[c] : (uint8_t)kAbsent;
-    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int c = c0 + 32 * k;
+    const uint32_t st = state >> (2 * k) & 3u;
     const uint32_t in_go = __ballot_sync(0xffffffffu, st == kMay), in_new = __ballot_sync(0xffffffffu, st == kNew),
                    in_stay = __ballot_sync(0xffffffffu, st == kStays);
-    const int my_new = fresh + __popc(in_new & below), my_stay = stay + __popc(in_stay & below);
-    if (c < hi) {
-      const int32_t old = a.resident_slot[row + c];
+    if (c < a.C) {
+      const int my_new = fresh + __popc(in_new & below);
       int32_t now = -1;
-      if (st == kStays) now = old;
+      if (st == kStays) now = slot[k];
       if (st == kNew && my_new < given) now = (int32_t)base + free_slot[my_new];
       a.resident_out[row + c] = now;
       if (now >= 0) {
         owner[now - base] = (uint16_t)c;
-        const int at = my_stay + min(my_new, given);
-        if (a.list_idx) a.list_idx[(int64_t)u * a.umax + at] = c;
-        if (a.list_slot) a.list_slot[(int64_t)u * a.umax + at] = now;
+        const int at = stay + __popc(in_stay & below) + min(my_new, given);
+        if (a.list_idx) {
+          a.list_idx[(int64_t)u * a.umax + at] = c;
+          a.list_slot[(int64_t)u * a.umax + at] = now;
+        }
         if (st == kNew && a.last_used) a.last_used[now] = a.step;
       }
       if (st == kMay && a.evicted) a.evicted[base + gone + __popc(in_go & below)] = c;
@@ -240,14 +244,28 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
-  const int per = (a.C + 31) / 32;                 // runs of 32 chunks
-  const int words = (a.S + 31) / 32, front = a.C > a.S + 1 ? a.C : a.S + 1;
-  int threads = 32 * (per < 32 ? (per < 4 ? 4 : per) : 32);
-  if (threads < words) threads = (words + 31) / 32 * 32;      // a thread a word of free slots
-  const size_t smem = (size_t)(front + words) * 4 + a.C;
-  cudaError_t e = set_dyn_smem((const void *)k_evict, smem);
-  if (e != cudaSuccess) return e;
-  return launch_k(k_evict, dim3(a.units), dim3(threads), smem, s, a);
+  // 32 warps at most, four at least, and a thread for each word of the slots' bitmap
+  const int lines = (a.C + 31) / 32, words = (a.S + 31) / 32;
+  int n = 1;
+  while (n * 32 < lines) n *= 2;
+  int warps = (lines + n - 1) / n;
+  if (warps < 4) warps = 4;
+  if (32 * warps < words) warps = (words + 31) / 32;
+  // (the bins are shared out evenly among a power of two of threads)
+  int pow = 4;
+  while (pow < warps) pow *= 2;
+  const size_t smem = (size_t)(kBins + words) * 4 + (size_t)a.S * 4;
+  auto go = [&](auto *kernel) {
+    const cudaError_t e = set_dyn_smem((const void *)kernel, smem);
+    return e != cudaSuccess ? e : launch_k(kernel, dim3(a.units), dim3(32 * pow), smem, s, a);
+  };
+  switch (n) {
+    case 1: return go(&k_evict<1>);
+    case 2: return go(&k_evict<2>);
+    case 4: return go(&k_evict<4>);
+    case 8: return go(&k_evict<8>);
+    default: return go(&k_evict<16>);
+  }
 }
 
 }  // namespace dd

@@ -58,19 +58,22 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
 
   pdl_wait();
   pdl_trigger();
-  if (load_status(a.status) != 0) return;
+  const int32_t status = load_status(a.status);
   const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int b = u / a.Hkv;
   const int64_t row = (int64_t)u * a.C, base = (int64_t)u * a.S;
-  const int kv = a.kv_len[b], more = a.new_len ? a.new_len[b] : 0;
   const int c0 = warp * 32 * N + lane;
   const uint32_t below = (1u << lane) - 1u;
+  const int32_t *const slots = a.resident_slot + row + c0;
+  const float *const weights = a.weight + row + c0;
   int32_t slot[N];
   uint32_t key[N], state = 0u;                               // state: two bits a chunk
 #pragma unroll
-  for (int k = 0; k < N; ++k) slot[k] = c0 + 32 * k < a.C ? a.resident_slot[row + c0 + 32 * k] : -1;
+  for (int k = 0; k < N; ++k) slot[k] = c0 + 32 * k < a.C ? slots[32 * k] : -1;
 #pragma unroll
-  for (int k = 0; k < N; ++k) key[k] = c0 + 32 * k < a.C ? order_key(a.weight[row + c0 + 32 * k]) : 0u;
+  for (int k = 0; k < N; ++k) key[k] = c0 + 32 * k < a.C ? __float_as_uint(weights[32 * k]) : 0u;
+  const int kv = a.kv_len[b], more = a.new_len ? a.new_len[b] : 0;
+  if (status != 0) return;
   bool bad = kv < 0 || more < 0 || (int64_t)kv + more > (int64_t)a.C * a.cs;
   const int n0 = bad ? 0 : (kv + a.cs - 1) / a.cs, n1 = bad ? 0 : (kv + more + a.cs - 1) / a.cs;
 
@@ -78,23 +81,26 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
   for (int i = tid; i < words; i += blockDim.x) used[i] = 0u;
   __syncthreads();
   Counts n = {0, 0, 0};                                      // resident, new, candidates
+  const int may0 = a.first, may1 = n0 - a.last;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int c = c0 + 32 * k;
-    uint32_t st = kAbsent;
     if (slot[k] >= 0) {
-      const int64_t s = slot[k] - base;
       // a slot of another unit, or of two chunks
-      if (s < 0 || s >= a.S || (atomicOr(&used[s >> 5], 1u << (s & 31)) >> (s & 31) & 1u)) s_bad = 1;
-      st = c >= a.first && c < n0 - a.last ? kMay : kStays;
+      const int64_t s = slot[k] - base;
+      bool ok = s >= 0 && s < a.S;
+      if (ok) ok = (atomicOr(&used[(int)s >> 5], 1u << (s & 31)) >> (s & 31) & 1u) == 0u;
+      if (!ok) s_bad = 1;
+      const bool may = c >= may0 && c < may1;
+      state |= (may ? kMay : kStays) << (2 * k);
+      n.a += 1, n.c += may;
     } else if (c >= n0 && c < n1 && c < a.C) {
-      st = kNew;
+      state |= kNew << (2 * k);
+      n.b += 1;
     }
-    state |= st << (2 * k);
-    n.a += __popc(__ballot_sync(0xffffffffu, st == kStays || st == kMay));
-    n.b += __popc(__ballot_sync(0xffffffffu, st == kNew));
-    n.c += __popc(__ballot_sync(0xffffffffu, st == kMay));
+    key[k] = order_key(__uint_as_float(key[k]));
   }
+  n.a = __reduce_add_sync(0xffffffffu, n.a), n.b = __reduce_add_sync(0xffffffffu, n.b), n.c = __reduce_add_sync(0xffffffffu, n.c);
   Counts all;
   warp_prefix(n, scratch, all, warp, lane, warps);
   bad = bad || s_bad != 0;
@@ -160,21 +166,24 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
     bool go = false;
     if (leave > 0) {
       const uint32_t top = key[k] >> shift;
-      const bool tie = st == kMay && top == bound;
-      const uint32_t in = __ballot_sync(0xffffffffu, tie);
-      go = st == kMay && (top < bound || (tie && (!ties || tied + __popc(in & below) < (int)rank)));
-      tied += __popc(in);
+      go = st == kMay && top <= bound;
+      if (ties) {
+        const bool tie = st == kMay && top == bound;
+        const uint32_t in = __ballot_sync(0xffffffffu, tie);
+        if (tie) go = tied + __popc(in & below) < (int)rank;
+        tied += __popc(in);
+      }
     }
+    // (from here on: kMay leaves)
     if (go) {
       const int s = (int)(slot[k] - base);
       atomicAnd(&used[s >> 5], ~(1u << (s & 31)));
+    } else if (st == kMay) {
+      state ^= (kMay ^ kStays) << (2 * k);
     }
-    // (from here on: kMay leaves)
-    if (st == kMay && !go) state ^= (kMay ^ kStays) << (2 * k);
-    m.a += __popc(__ballot_sync(0xffffffffu, go));
-    m.b += __popc(__ballot_sync(0xffffffffu, st == kNew));
-    m.c += __popc(__ballot_sync(0xffffffffu, st == kStays || (st == kMay && !go)));
+    m.a += go, m.b += st == kNew, m.c += st == kStays || (st == kMay && !go);
   }
+  m.a = __reduce_add_sync(0xffffffffu, m.a), m.b = __reduce_add_sync(0xffffffffu, m.b), m.c = __reduce_add_sync(0xffffffffu, m.c);
   const Counts pre = warp_prefix(m, scratch, all, warp, lane, warps);
 
   // the free slots, ascending: a thread a word of 32
@@ -202,31 +211,37 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
   const int given = min(all.b, n_free);
 
   // (new chunks lie behind n0, among the residents there)
-  int gone = pre.a, fresh = pre.b, stay = pre.c;
+  int gone = pre.a, listed = pre.c + min(pre.b, given), fresh = pre.b;
+  int32_t *const out = a.resident_out + row + c0;
+  int32_t *const idx_to = a.list_idx ? a.list_idx + (int64_t)u * a.umax : nullptr;
+  int32_t *const slot_to = a.list_slot + (a.list_idx ? (int64_t)u * a.umax : 0);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int c = c0 + 32 * k;
     const uint32_t st = state >> (2 * k) & 3u;
-    const uint32_t in_go = __ballot_sync(0xffffffffu, st == kMay), in_new = __ballot_sync(0xffffffffu, st == kNew),
-                   in_stay = __ballot_sync(0xffffffffu, st == kStays);
-    if (c < a.C) {
+    int32_t now = st == kStays ? slot[k] : -1;
+    if (all.b > 0) {
+      const uint32_t in_new = __ballot_sync(0xffffffffu, st == kNew);
       const int my_new = fresh + __popc(in_new & below);
-      int32_t now = -1;
-      if (st == kStays) now = slot[k];
-      if (st == kNew && my_new < given) now = (int32_t)base + free_slot[my_new];
-      a.resident_out[row + c] = now;
-      if (now >= 0) {
-        owner[now - base] = (uint16_t)c;
-        const int at = stay + __popc(in_stay & below) + min(my_new, given);
-        if (a.list_idx) {
-          a.list_idx[(int64_t)u * a.umax + at] = c;
-          a.list_slot[(int64_t)u * a.umax + at] = now;
-        }
-        if (st == kNew && a.last_used) a.last_used[now] = a.step;
+      if (st == kNew && my_new < given) {
+        now = (int32_t)base + free_slot[my_new];
+        if (a.last_used) a.last_used[now] = a.step;
       }
-      if (st == kMay && a.evicted) a.evicted[base + gone + __popc(in_go & below)] = c;
+      fresh += __popc(in_new);
     }
-    gone += __popc(in_go), fresh += __popc(in_new), stay += __popc(in_stay);
+    if (c < a.C) out[32 * k] = now;
+    const uint32_t in = __ballot_sync(0xffffffffu, now >= 0);
+    if (now >= 0) {
+      owner[now - base] = (uint16_t)c;
+      const int at = listed + __popc(in & below);
+      if (idx_to) idx_to[at] = c, slot_to[at] = now;
+    }
+    listed += __popc(in);
+    if (a.evicted) {
+      const uint32_t in_go = __ballot_sync(0xffffffffu, st == kMay);
+      if (st == kMay) a.evicted[base + gone + __popc(in_go & below)] = c;
+      gone += __popc(in_go);
+    }
   }
   if (tid == 0) {
     if (a.evicted_cnt) a.evicted_cnt[u] = all.a;

@@ -9,7 +9,7 @@
 // One CTA a unit, each warp a run of 32 N chunks: a lane keeps N of them in registers (slot, weight as an order
 // key: a NaN below every number, -0 as +0), read once, all loads on their way together.  A radix select over the
 // keys in digits of 11 bits finds the E-th smallest (2,048 bins spread exponents over banks, and the first two
-// digits leave one or two keys: a third is rarely looked at).  Ranks are ballots, so every access is a whole line.
+// digits leave one or two keys, or equal ones: a third is rarely looked at).  Ranks are ballots, so every access is a whole line.
 #include "dd_pages.cuh"
 
 namespace dd {
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
   uint16_t *free_slot = reinterpret_cast<uint16_t *>(used + words), *owner = free_slot + a.S;   // [S] each
   __shared__ int scratch[3][33];
   __shared__ int s_bad;
-  __shared__ uint32_t s_digit, s_rank, s_count;
+  __shared__ uint32_t s_digit, s_rank, s_count, s_low, s_high;
 
   pdl_wait();
   pdl_trigger();
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
   bool bad = kv < 0 || more < 0 || (int64_t)kv + more > (int64_t)a.C * a.cs;
   const int n0 = bad ? 0 : (kv + a.cs - 1) / a.cs, n1 = bad ? 0 : (kv + more + a.cs - 1) / a.cs;
 
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) s_bad = 0, s_low = 0xFFFFFFFFu, s_high = 0u, s_count = 0u;
   for (int i = tid; i < words; i += blockDim.x) used[i] = 0u;
   __syncthreads();
   Counts n = {0, 0, 0};                                      // resident, new, candidates
@@ -121,17 +121,28 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
   // the digits of the leave-th smallest key, from the top, until all keys that share them leave
   int shift = 32;
   uint32_t bound = 0u, rank = (uint32_t)leave;               // of those that share the digits found so far
+  uint32_t shared = (uint32_t)all.c;                         // how many share them
   bool ties = leave > 0;
   for (int width = kDigit; ties && shift > 0; ) {
     const int next = max(0, shift - width);
     for (int i = tid; i < kBins; i += blockDim.x) hist[i] = 0u;
     __syncthreads();
     const uint32_t mask = (1u << (shift - next)) - 1u;
+    uint32_t low = 0xFFFFFFFFu, high = 0u;
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      if ((state >> (2 * k) & 3u) == kMay && (shift == 32 || key[k] >> shift == bound))
+      if ((state >> (2 * k) & 3u) == kMay && (shift == 32 || key[k] >> shift == bound)) {
         atomicAdd(&hist[key[k] >> next & mask], 1u);
+        low = min(low, key[k]), high = max(high, key[k]);
+      }
+    low = __reduce_min_sync(0xffffffffu, low), high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0 && low <= high) atomicMin(&s_low, low), atomicMax(&s_high, high);
     __syncthreads();
+    if (s_low == s_high) {
+      // all alike (chunks that nothing has looked at): no digit tells them apart
+      bound = s_low, shift = 0, ties = shared != rank;
+      break;
+    }
     // (at most 16 bins a thread: there are 128 threads or more)
     const int per = kBins / blockDim.x > 0 ? kBins / blockDim.x : 1, from = tid * per;
     int sum = 0;
@@ -149,7 +160,8 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
       }
     __syncthreads();
     bound = shift == 32 ? s_digit : bound << (shift - next) | s_digit;
-    rank = s_rank, ties = s_count != s_rank, shift = next;
+    rank = s_rank, shared = s_count, ties = shared != rank, shift = next;
+    if (tid == 0) s_low = 0xFFFFFFFFu, s_high = 0u;        // (read before the barrier in front of this)
   }
 
   // the first `rank` of the keys that share the digits leave, in chunk order
@@ -261,8 +273,9 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
   // 32 warps at most, four at least, and a thread for each word of the slots' bitmap
   const int lines = (a.C + 31) / 32, words = (a.S + 31) / 32;
+  // (two CTAs an SM where 16 warps will do: 2,048 chunks of 256 units 9.9 us; 18.1 with 32 warps, in two rounds)
   int n = 1;
-  while (n * 32 < lines) n *= 2;
+  while (n < 16 && n * 16 < lines) n *= 2;
   int warps = (lines + n - 1) / n;
   if (warps < 4) warps = 4;
   if (32 * warps < words) warps = (words + 31) / 32;

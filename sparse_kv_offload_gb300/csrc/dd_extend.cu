@@ -105,15 +105,25 @@ __device__ __forceinline__ int tiles_of(const PagesArgs &a, int entries) {
   return max(1, ((entries << a.cs_log) + kTileKeys - 1) / kTileKeys);      // (a row without keys still has its zeros to write)
 }
 
-__device__ __forceinline__ Unit load_unit(const ExtendParams &p, int u) {
+struct RawUnit {
+  int start, len, cnt;
+};
+__device__ __forceinline__ RawUnit raw_unit(const PagesArgs &a, int u) {
+  const int b = u / a.Hkv;
+  return {a.start_pos[b], a.new_len ? a.new_len[b] : a.T, a.union_cnt[u]};
+}
+
+__device__ __forceinline__ Unit make_unit(const ExtendParams &p, const RawUnit &w) {
   Unit r = {0, 0, 0, 0, 0};
-  const Request q = load_request(p.a, u / p.a.Hkv);
-  r.cnt = load_count(p.a, u);
+  const Request q = check_request(p.a, w.start, w.len);
+  r.cnt = check_count(p.a, w.cnt);
   r.start = q.start, r.len = q.len;
   r.groups = ceil_div(q.len, p.mt);
   if (r.groups) r.tiles = tiles_of(p.a, entry_bound(p.a, r, q.len - 1));
   return r;
 }
+
+__device__ __forceinline__ Unit load_unit(const ExtendParams &p, int u) { return make_unit(p, raw_unit(p.a, u)); }
 
 // The first group of tokens that has more than `tiles` tiles of keys.
 __device__ __forceinline__ int first_longer(const ExtendParams &p, const Unit &u, int tiles) {
@@ -134,9 +144,9 @@ __device__ __forceinline__ Unit cut_part(const ExtendParams &p, const Unit &u, i
 // Pairs of row tiles: as many as there are whole rounds of CTAs for are taken whole, in order, and the
 // rest, fewer than CTAs, is cut into ranges of at most this many tiles of keys: of 1/s of the longest pair
 // for s = 1, 2, .. the one that ends first, by rounds of items, each its tiles and kItemCost of them for what an
-// item costs beside (queries, sums out and in, the join).  With P CTAs: pairs that are cut < P, their ranges
+// item costs beside (queries, sums out and in), and kJoinCost for the joins at the end.  With P CTAs: pairs that are cut < P, their ranges
 // <= work / length + pairs <= 5 P.
-constexpr int kItemCost = 3, kItemsPerCta = 4;
+constexpr int kItemCost = 3, kJoinCost = 6, kItemsPerCta = 4;
 __device__ __forceinline__ int cut_of(long long work, int groups, int longest, int cta, int lane) {
   if (groups == 0) return 1;
   const int least = max(1, (int)((work + kItemsPerCta * cta - 1) / (kItemsPerCta * cta)));
@@ -144,7 +154,7 @@ __device__ __forceinline__ int cut_of(long long work, int groups, int longest, i
   for (int s = 1 + lane; s <= longest; s += 32) {
     const int len = max(ceil_div(longest, s), least);
     const unsigned long long items = min((unsigned long long)groups * ceil_div(longest, len), (unsigned long long)work / len + groups);
-    const unsigned long long cost = (items + cta - 1) / cta * (len + kItemCost);
+    const unsigned long long cost = (items + cta - 1) / cta * (len + kItemCost) + (len < longest ? kJoinCost : 0);
     best = min(best, (cost << 24) | (unsigned long long)(0xFFFFFF - len));
     if (len == least) break;
   }
@@ -318,13 +328,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       const int units = a.B * a.Hkv, cta = (int)gridDim.x;
       const bool sliced = p.pairs == 1;
       uint32_t total = 0;                                  // groups, or tiles of all units and their costs (below 2^31)
+      uint32_t block = 0;                                  // a lane's block of 32 units: theirs
       Unit few = {0, 0, 0, 0, 0};                          // a lane's unit, where there are no more than 32
-      for (int u = lane; u < units; u += 32) {
-        const Unit r = few = load_unit(p, u);
-        total += sliced ? (r.groups ? r.tiles + kUnitCost : 0) : r.groups;
-      }
+      for (int u0 = 0; u0 < units; u0 += 128) {
+        // (the loads of 128 units are on their way together)
+        RawUnit raw[4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        for (int k = 0; k < 4; ++k)
+          if (u0 + 32 * k + lane < units) raw[k] = raw_unit(a, u0 + 32 * k + lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (u0 + 32 * k >= units) break;
+          Unit r = {0, 0, 0, 0, 0};
+          if (u0 + 32 * k + lane < units) r = make_unit(p, raw[k]);
+          if (u0 + k == 0) few = r;
+          const uint32_t sum = __reduce_add_sync(0xffffffffu, (uint32_t)(sliced ? (r.groups ? r.tiles + kUnitCost : 0) : r.groups));
+          if (lane == u0 / 32 + k) block = sum;
+          total += sum;
+        }
+      }
       const int whole_groups = (int)(total / cta * cta);
       int cut = 1;
       if (!sliced) {
@@ -356,6 +378,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       int ranges = 0, items = 0, items_pre = 0, parts_pre = 0, cuts_pre = 0, m1 = 0;
       int want = sliced ? (int)blockIdx.x * per : (int)blockIdx.x;
       const int slice_end = want + per;
+      if (sliced && units <= 1024) {
+        // the block of units that the slice begins in
+        const int incl = warp_incl_scan((int)block);
+        const uint32_t past = __ballot_sync(0xffffffffu, incl <= want);      // (a prefix: sums ascend)
+        const int skip = min(__popc(past), (units - 1) / 32);
+        if (skip > 0) base_u = 32 * (skip - 1), items_here = __shfl_sync(0xffffffffu, incl, skip - 1);
+      }
       uint32_t n_item = 0, kt = 0;
       int tasks = 0;                                       // that this CTA may have to do
       bool ok = true;
@@ -890,7 +919,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           f0 = exp2_fast((m - ref) * a.sl2), f1 = exp2_fast((other.x - ref) * a.sl2);
           m = top, l = l * f0 + other.y * f1;
         }
-        const bool bad = x.bad_item == (int)n;
         const int b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
         const int64_t slot = it.part + (p.pairs == 2 ? w : 0);
         float *po = p.part_o + (slot * rows_tile + r) * kD;
@@ -898,6 +926,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         uint16_t *dst = p.out + b * p.os[0] + token * p.os[1] + (h0 + head) * p.os[2];
         if (parts == 1) f0 = l == 0.f ? 0.f : f0 / l, f1 = l == 0.f ? 0.f : f1 / l;
         if (some) {
+          const bool none = cw == 0 || l == 0.f;
 #pragma unroll 1
           for (int h = 0; h < 4; ++h) {
             float o[32];
@@ -906,7 +935,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               tmem_wait_ld();
               tmem_ready(o);
             }
-            const bool none = cw == 0 || l == 0.f;
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * f0;
             if (both) {
@@ -916,14 +944,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               tmem_ready(o1);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : fmaf(o1[e], f1, o[e]);
-            }
-            if (bad) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                if (x.bad[0][32 * h + e] <= pos) o[e] = NAN;
-                if (x.bad[1][32 * h + e] <= pos) o[e] += INFINITY;
-                if (x.bad[2][32 * h + e] <= pos) o[e] -= INFINITY;
-              }
             }
             if (valid) {
               if (parts == 1) {
@@ -938,6 +958,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
                   *reinterpret_cast<float4 *>(po + 32 * h + 4 * e) =
                       make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
               }
+            }
+          }
+          if (valid && x.bad_item == (int)n) {
+            // values of V that were taken out of a tile, where the row sees them
+#pragma unroll 1
+            for (int c = 0; c < 128; ++c) {
+              const bool nan = x.bad[0][c] <= pos, up = x.bad[1][c] <= pos, down = x.bad[2][c] <= pos;
+              if (!nan && !up && !down) continue;
+              const float add = nan || (up && down) ? NAN : (up ? INFINITY : -INFINITY);
+              if (parts == 1) dst[c] = (uint16_t)f2bf(bf_lo(dst[c]) + add);
+              else po[c] += add;
             }
           }
           if (valid) {
@@ -987,7 +1018,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       q.lse = p.lse ? p.lse + ((int64_t)b * a.T + task.token) * a.Hq + h0 : nullptr;
       // (few rows have many parts: one warp a row)
       if (q.rows <= 32) join_rows<1>(q, warp, 8);
-      else join_rows<4>(q, warp, 8);
+      else if (q.parts <= 4) join_rows<4>(q, warp, 8);
+      else join_rows<2>(q, warp, 8);
     }
   }
   tc_fence_before();

@@ -31,8 +31,7 @@ struct Request {
   int start, len;                                 // a request that is out of range has no tokens
 };
 
-__device__ __forceinline__ Request load_request(const PagesArgs &a, int b) {
-  const int start = a.start_pos[b], len = a.new_len ? a.new_len[b] : a.T;
+__device__ __forceinline__ Request check_request(const PagesArgs &a, int start, int len) {
   if (start < 0 || len < 0 || len > a.T || (int64_t)start + len > (int64_t)a.C * a.cs) {
     set_status(a.status, DD_ERR_DEVICE_CHECK);
     return {0, 0};
@@ -40,14 +39,19 @@ __device__ __forceinline__ Request load_request(const PagesArgs &a, int b) {
   return {start, len};
 }
 
-__device__ __forceinline__ int load_count(const PagesArgs &a, int unit) {
-  const int n = a.union_cnt[unit];
+__device__ __forceinline__ Request load_request(const PagesArgs &a, int b) {
+  return check_request(a, a.start_pos[b], a.new_len ? a.new_len[b] : a.T);
+}
+
+__device__ __forceinline__ int check_count(const PagesArgs &a, int n) {
   if (n < 0 || n > a.umax) {
     set_status(a.status, DD_ERR_DEVICE_CHECK);
     return 0;
   }
   return n;
 }
+
+__device__ __forceinline__ int load_count(const PagesArgs &a, int unit) { return check_count(a, a.union_cnt[unit]); }
 
 // Entry e of a unit's list: the chunk's slot (hot: slot, staged: -(m+1)) and the position of
 // its first row; INT_MAX where there is none or it is out of range (the slot is then looked at no more).

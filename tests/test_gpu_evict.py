@@ -112,3 +112,93 @@ def test_evict(dd, name, in_place):
     for n in OUT:
         assert np.array_equal(got[n], want[n]), n
     assert status == (dd.DD_ERR_CAPACITY if short else 0)
+
+
+def test_only_the_map(dd):
+    """No optional output: the map alone."""
+    x = make(9, 2, 2, 60, 16, 40, 20)
+    before = buffers(x, 40)
+    got, status = run(dd, x, 1, 2, before, optional=False)
+    want, _ = want_of(x, 1, 2, before)
+    assert status == 0 and np.array_equal(got["resident_out"], want["resident_out"])
+    for n in OUT[1:]:
+        assert np.array_equal(got[n], before[n]), n
+
+
+@pytest.mark.parametrize("kind", ["equal", "nan", "inf", "negative", "tiny", "near"])
+def test_weights_of_all_kinds(dd, kind):
+    """Ties by chunk, NaN below every number, signs, subnormals, neighbours in the last bit."""
+    x = make(11, 2, 2, 500, 16, 300, 100, ties=0.0)
+    rng = np.random.default_rng(2)
+    w = x["w"]
+    if kind == "equal":
+        w[:] = 1.5
+    elif kind == "nan":
+        w[rng.random(w.shape) < 0.4] = np.nan
+        w[rng.random(w.shape) < 0.1] = -np.nan
+    elif kind == "inf":
+        w[rng.random(w.shape) < 0.4] = np.inf
+        w[rng.random(w.shape) < 0.4] = -np.inf
+    elif kind == "negative":
+        w[:] = rng.standard_normal(w.shape).astype(np.float32)
+        w[rng.random(w.shape) < 0.3] = -0.0
+        w[rng.random(w.shape) < 0.3] = 0.0
+    elif kind == "tiny":
+        w[:] = (rng.integers(0, 40, w.shape) * 1.4e-45).astype(np.float32)
+    else:
+        w[:] = (np.float32(1.0).view(np.uint32) + rng.integers(0, 3, w.shape).astype(np.uint32)).view(np.float32)
+    before = buffers(x, 300)
+    got, status = run(dd, x, 3, 5, before)
+    want, _ = want_of(x, 3, 5, before)
+    for n in OUT:
+        assert np.array_equal(got[n], want[n]), n
+    assert status == 0
+
+
+def test_lengths_from_nothing_to_all(dd):
+    """Empty caches, full ones, chunks that are resident ahead of their rows, protected ranges that cover all."""
+    x = make(12, 6, 1, 32, 16, 32, 8, ties=0.0)
+    x["kv"][:] = [0, 1, 16, 17, 511, 512]
+    x["n"][:] = [0, 15, 0, 495, 1, 0]
+    x["slot"][:] = -1
+    for b in range(6):
+        x["slot"][b, 0, :20] = b * 32 + np.arange(20)        # (for the short ones: behind their rows)
+    for first, last in ((0, 0), (32, 0), (0, 40), (5, 5)):
+        before = buffers(x, 32)
+        got, status = run(dd, x, first, last, before)
+        want, short = want_of(x, first, last, before)
+        for n in OUT:
+            assert np.array_equal(got[n], want[n]), (n, first, last)
+        assert status == (dd.DD_ERR_CAPACITY if short else 0)
+
+
+def test_device_checks(dd):
+    """A slot outside the unit's range, of two chunks, a length out of range: the unit stays as it was."""
+    for what in ("outside", "other_unit", "twice", "kv", "kv_negative", "new"):
+        x = make(13, 3, 2, 50, 16, 30, 10)
+        before = buffers(x, 30)
+        want, _ = want_of(x, 1, 1, before)                # of the units that are as they should be
+        s = x["slot"][1, 1]
+        here = np.flatnonzero(s >= 0)
+        if what == "outside":
+            s[here[0]] = 3 * 2 * 30
+        elif what == "other_unit":
+            s[here[0]] = 5
+        elif what == "twice":
+            s[here[0]] = s[here[1]]
+        elif what == "kv":
+            x["kv"][1], x["n"][1] = 801, 0
+        elif what == "kv_negative":
+            x["kv"][1] = -1
+        else:
+            x["kv"][1], x["n"][1] = 700, 101
+        got, status = run(dd, x, 1, 1, before)
+        assert status == dd.DD_ERR_DEVICE_CHECK
+        for b in (0, 2):                                   # (or as they were: a CTA that finds the error pending does nothing)
+            for h in range(2):
+                assert np.array_equal(got["resident_out"][b, h], want["resident_out"][b, h]) or \
+                    np.array_equal(got["resident_out"][b, h], before["resident_out"][b, h])
+        assert np.array_equal(got["resident_out"][1, 1], x["slot"][1, 1]) or \
+            np.array_equal(got["resident_out"][1, 1], before["resident_out"][1, 1])
+        for n in ("slot_chunk", "last_used", "evicted", "union_idx", "union_slot"):
+            assert np.array_equal(got[n][1, 1], before[n][1, 1]), n

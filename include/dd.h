@@ -577,7 +577,7 @@ typedef struct {
  * they hold (NaN and infinities among it).  A score of +inf or NaN makes the row NaN, one of -inf has no
  * weight.  Outputs of padding are left as they were.  Weights are rounded to bf16 for their product
  * with V (up to 2^-8 of each, at random); sums and statistics are fp32.
- * workspace: dd_extend_attn_workspace(ctx, T) bytes of device memory, 16-byte aligned, which calls on
+ * workspace: dd_extend_attn_workspace(ctx, T) bytes of device memory, 32-byte aligned, which calls on
  * one stream may share; it holds nothing between calls.  out must not overlap the inputs.
  * A call that reports DD_ERR_DEVICE_CHECK leaves each (request, KV head)'s outputs as its result without
  * what was out of range, or as they were. */

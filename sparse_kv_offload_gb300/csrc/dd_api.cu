@@ -819,7 +819,8 @@ dd_status dd_extend_attn(dd_ctx *c, const dd_extend_args *e, dd_stream_t stream)
   if (c->hot_slots > 0 && (!e->pages.Vhot || !aligned16(e->pages.Vhot))) return DD_ERR_INVALID_ARG;
   if (c->max_misses > 0 && (!e->pages.Vst || !aligned16(e->pages.Vst))) return DD_ERR_INVALID_ARG;
   if (!rows_ok(e->out, e->out_stride)) return DD_ERR_INVALID_ARG;
-  if (!e->workspace || !aligned16(e->workspace) || e->workspace_bytes < dd_extend_attn_workspace(c, e->rows.T))
+  if (!e->workspace || (reinterpret_cast<uintptr_t>(e->workspace) & 31u) ||
+      e->workspace_bytes < dd_extend_attn_workspace(c, e->rows.T))
     return DD_ERR_INVALID_ARG;
   DD_TRY(on_device(c));
   a.q = e->rows.q, a.Khot = e->pages.Khot, a.Vhot = e->pages.Vhot, a.Kst = e->pages.Kst, a.Vst = e->pages.Vst;

@@ -85,6 +85,7 @@ struct ExtendParams {
   float *part_o;              // [slots][rows][128]
   float2 *part_ml;            // [slots][rows]: reference (a score before the factor), sum
   WorkCounters w;
+  bool wide;                  // rows of `out` begin at multiples of 32 bytes
   int mt;                     // tokens of an item
   int pairs;                  // row tiles of an item: 1 or 2
 };
@@ -947,16 +948,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             }
             if (valid) {
               if (parts == 1) {
+                uint32_t v[16];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  *reinterpret_cast<uint4 *>(dst + 32 * h + 8 * e) =
-                      make_uint4(bf16x2(o[8 * e], o[8 * e + 1]), bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                 bf16x2(o[8 * e + 4], o[8 * e + 5]), bf16x2(o[8 * e + 6], o[8 * e + 7]));
+                for (int e = 0; e < 16; ++e) v[e] = bf16x2(o[2 * e], o[2 * e + 1]);
+                if (p.wide) {
+                  store32(dst + 32 * h, v), store32(dst + 32 * h + 16, v + 8);
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<uint4 *>(dst + 32 * h + 8 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                }
               } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  *reinterpret_cast<float4 *>(po + 32 * h + 4 * e) =
-                      make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                for (int e = 0; e < 4; ++e) store32(po + 32 * h + 8 * e, reinterpret_cast<const uint32_t *>(o) + 8 * e);
               }
             }
           }
@@ -1070,6 +1074,8 @@ cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t stream) {
   p.out = static_cast<uint16_t *>(e.out);
   for (int i = 0; i < 3; ++i) p.os[i] = e.out_stride[i];
   p.lse = e.lse;
+  p.wide = reinterpret_cast<uintptr_t>(e.out) % 32 == 0 && e.out_stride[0] % 16 == 0 && e.out_stride[1] % 16 == 0 &&
+           e.out_stride[2] % 16 == 0;
   p.part_o = e.parts;
   p.part_ml = reinterpret_cast<float2 *>(e.parts + s.slots * s.rows * kD);
   p.w = {e.ctr, kCtrPerCta * e.sm_count};

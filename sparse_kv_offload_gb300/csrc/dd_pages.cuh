@@ -190,6 +190,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
+// 32 bytes to an address that is a multiple of 32: a thread that writes a row of its own fills a sector each time.
+__device__ __forceinline__ void store32(void *to, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // The largest of three; a NaN counts as nothing.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;

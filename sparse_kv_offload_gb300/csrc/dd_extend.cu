@@ -716,15 +716,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           ok = wait_warp(v_full + 8 * st, vt / kV);
           if (!ok) break;
           if (!x.vwhole[st]) {
-            for (int e = lane; e < kTileBytes / 16; e += 32) {
-              const uint32_t at = v0 + st * kTileBytes + e * 16;
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
-              uint32_t hit = 0;
+            const uint32_t tile = v0 + st * kTileBytes + lane * 16;
+            bool fixed = false;
+            for (int e0 = 0; e0 < kTileBytes / 16; e0 += 256) {
+              // eight pieces a lane: 0 times a finite value is 0, whatever its sign
+              uint32_t zero[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) hit |= ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-              const uint32_t any = __ballot_sync(0xffffffffu, hit != 0u);
-              if (any == 0u) continue;
+              for (int k = 0; k < 8; ++k) {
+                uint32_t w[4];
+                lds128(tile + (e0 + 32 * k) * 16, w);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) zero[q] = fma_bf16x2(w[q], 0u, zero[q]);
+              }
+              if (!__any_sync(0xffffffffu, (zero[0] | zero[1] | zero[2] | zero[3]) != 0u)) continue;
               if (!found) {
                 // the records are the item's: the one before has used its own
                 found = true;
@@ -733,7 +737,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
                 if (lane == 0) x.bad_item = (int)n;
                 __syncwarp();
               }
-              if (hit) {
+              fixed = true;
+#pragma unroll 1
+              for (int e = e0 + lane; e < e0 + 256; e += 32) {
+                const uint32_t at = v0 + st * kTileBytes + e * 16;
+                uint32_t w[4];
+                lds128(at, w);
                 const int row = (e & 1023) >> 3, col0 = (e >> 10) * 64 + (((e & 7) ^ (row & 7)) << 3);
                 const int first = x.vpos[st][row >> a.cs_log], pos = first == INT_MAX ? INT_MAX : first + (row & (a.cs - 1));
 #pragma unroll
@@ -749,7 +758,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
                              : "memory");
               }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (fixed)
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(v_ok + 8 * st);

@@ -43,7 +43,7 @@ constexpr int kSoftRegs = 208, kOtherRegs = 80;      // 256 * 208 + 128 * 80 <= 
 constexpr float kHead = 8.f;                         // weights stay below 2^8
 
 struct Item {
-  int unit, t0, start, len;
+  int unit, b, h0, t0, start, len;   // the unit's request and first query head
   int j0;                     // first tile of keys
   int ents;                   // the list's entries that the item's last token may see
   int pos_max, pos_min;       // positions of the item's last and first token
@@ -147,21 +147,20 @@ __device__ __forceinline__ Unit cut_part(const ExtendParams &p, const Unit &u, i
 // for s = 1, 2, .. the one that ends first, by rounds of items, each its tiles and kItemCost of them for what an
 // item costs beside (queries, sums out and in), and kJoinCost for the joins at the end.  With P CTAs: pairs that are cut < P, their ranges
 // <= work / length + pairs <= 5 P.
-constexpr int kItemCost = 3, kJoinCost = 6, kItemsPerCta = 4;
-__device__ __forceinline__ int cut_of(long long work, int groups, int longest, int cta, int lane) {
+constexpr int kItemCost = 3, kJoinCost = 12, kItemsPerCta = 4;
+__device__ __forceinline__ int cut_of(int work, int groups, int longest, int cta, int lane) {
   if (groups == 0) return 1;
-  const int least = max(1, (int)((work + kItemsPerCta * cta - 1) / (kItemsPerCta * cta)));
-  unsigned long long best = ~0ull;
+  const int least = max(1, ceil_div(work, kItemsPerCta * cta));
+  // (fewer groups than CTAs and at most 8,192 tiles each: costs stay below 2^17, lengths below 2^14)
+  uint32_t best = ~0u;
   for (int s = 1 + lane; s <= longest; s += 32) {
     const int len = max(ceil_div(longest, s), least);
-    const unsigned long long items = min((unsigned long long)groups * ceil_div(longest, len), (unsigned long long)work / len + groups);
-    const unsigned long long cost = (items + cta - 1) / cta * (len + kItemCost) + (len < longest ? kJoinCost : 0);
-    best = min(best, (cost << 24) | (unsigned long long)(0xFFFFFF - len));
+    const int items = min(groups * ceil_div(longest, len), (int)((unsigned)work / (unsigned)len) + groups);
+    const int cost = ceil_div(items, cta) * (len + kItemCost) + (len < longest ? kJoinCost : 0);
+    best = min(best, (uint32_t)cost << 14 | (uint32_t)(16383 - len));
     if (len == least) break;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) best = min(best, (unsigned long long)__shfl_xor_sync(0xffffffffu, best, o));
-  return 0xFFFFFF - (int)(best & 0xFFFFFFull);
+  return 16383 - (int)(__reduce_min_sync(0xffffffffu, best) & 16383u);
 }
 
 // One row tile a unit: the units' tiles of keys, laid end to end, are cut into equal slices, one a CTA; kUnitCost
@@ -186,9 +185,9 @@ __device__ __forceinline__ int64_t slice_slot(int64_t slice, bool first) { retur
 
 // R rows by Q parts are on their way at once, the next rows' while these are written; lane (32 / R) j + q
 // holds the statistics of row j's part q.
-template <int R>
+template <int R, int Q>
 __device__ __forceinline__ void join_rows(const Join &p, int join_w, int join_n) {
-  constexpr int Q = 16 / R, L = 32 / R;
+  constexpr int L = 32 / R;
   const int lane = threadIdx.x & 31, lj = lane / L, lq = lane % L;
   const int rows = p.rows, n_parts = p.parts;
   auto slot_of = [&](int q) -> int64_t {
@@ -352,19 +351,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       int cut = 1;
       if (!sliced) {
         // what is left to cut
-        long long work = 0;
-        int longest = 0, before = 0;
+        int work = 0, longest = 0, before = 0;
         for (int u0 = 0; u0 < units; u0 += 32) {
           Unit r = {0, 0, 0, 0, 0};
           if (u0 + lane < units) r = units <= 32 ? few : load_unit(p, u0 + lane);
           const int incl = warp_incl_scan(r.groups);
           r = cut_part(p, r, min(r.groups, max(0, whole_groups - before - (incl - r.groups))));
-          work += (long long)r.groups * r.tiles;
+          work += r.groups * r.tiles;
           longest = max(longest, r.tiles);
           before += __shfl_sync(0xffffffffu, incl, 31);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+        work = __reduce_add_sync(0xffffffffu, work);
         longest = __reduce_max_sync(0xffffffffu, longest);
         cut = cut_of(work, (int)total - whole_groups, longest, cta, lane);
       }
@@ -513,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           else c0 = c, parts0 = parts;
         }
         if (lane == 0) {
-          it.unit = unit, it.t0 = t0, it.start = u.start, it.len = u.len;
+          it.unit = unit, it.b = unit / a.Hkv, it.h0 = (unit - it.b * a.Hkv) * a.G, it.t0 = t0, it.start = u.start, it.len = u.len;
           it.j0 = j0, it.ents = ents;
           it.pos_max = u.start + t_end - 1, it.pos_min = u.start + t0;
           it.c[0] = c0, it.c[1] = c1, it.parts[0] = parts0, it.parts[1] = parts1;
@@ -590,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           __syncwarp();
           if (lane < (two ? 4 : 2))
             tma_load_4d(q0 + (lane >> 1) * kTileBytes + (lane & 1) * kTileHalfBytes, &p.q, 64 * (lane & 1),
-                        unit % a.Hkv * a.G, it.t0 + (lane >> 1) * a.tt, unit / a.Hkv, q_full);
+                        it.h0, it.t0 + (lane >> 1) * a.tt, it.b, q_full);
           ++nq;
         }
         const int per = 32 / chunks;
@@ -930,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           f0 = exp2_fast((m - ref) * a.sl2), f1 = exp2_fast((other.x - ref) * a.sl2);
           m = top, l = l * f0 + other.y * f1;
         }
-        const int b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
+        const int b = it.b, h0 = it.h0;
         const int64_t slot = it.part + (p.pairs == 2 ? w : 0);
         float *po = p.part_o + (slot * rows_tile + r) * kD;
         const int64_t row = ((int64_t)b * a.T + token) * a.Hq + h0 + head;
@@ -1031,9 +1028,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       q.out = p.out + b * p.os[0] + task.token * p.os[1] + h0 * p.os[2], q.os1 = p.os[1], q.os2 = p.os[2];
       q.lse = p.lse ? p.lse + ((int64_t)b * a.T + task.token) * a.Hq + h0 : nullptr;
       // (few rows have many parts: one warp a row)
-      if (q.rows <= 32) join_rows<1>(q, warp, 8);
-      else if (q.parts <= 4) join_rows<4>(q, warp, 8);
-      else join_rows<2>(q, warp, 8);
+      if (q.rows <= 32) join_rows<1, 16>(q, warp, 8);
+      else if (q.parts <= 4) join_rows<4, 4>(q, warp, 8);
+      else join_rows<2, 8>(q, warp, 8);
     }
   }
   tc_fence_before();

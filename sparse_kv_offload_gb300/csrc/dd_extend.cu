@@ -58,7 +58,7 @@ struct Task {
   int unit, len, token, parts;    // its first token
   int64_t first;
 };
-constexpr int kTasks = 24;    // of a CTA: with fewer than four left its next item is its last, if any may be cut
+constexpr int kTasks = 16;    // of a CTA: with fewer than four left its next item is its last (eight cut items a CTA; there are five)
 
 struct Misc {
   uint64_t bars[40];
@@ -68,6 +68,7 @@ struct Misc {
   int vpos[kV][8], vwhole[kV];   // the same of V's tiles
   int bad[3][128];            // lowest position of a NaN, +inf, -inf in each column of V
   Task task[kTasks];
+  uint32_t sum[kThreads / 32], block[32];   // units' groups, or tiles and costs: of each warp, of the first blocks of 32
   int tasks, bad_item, dead, pending;
   uint32_t tmem;
 };
@@ -106,25 +107,15 @@ __device__ __forceinline__ int tiles_of(const PagesArgs &a, int entries) {
   return max(1, ((entries << a.cs_log) + kTileKeys - 1) / kTileKeys);      // (a row without keys still has its zeros to write)
 }
 
-struct RawUnit {
-  int start, len, cnt;
-};
-__device__ __forceinline__ RawUnit raw_unit(const PagesArgs &a, int u) {
-  const int b = u / a.Hkv;
-  return {a.start_pos[b], a.new_len ? a.new_len[b] : a.T, a.union_cnt[u]};
-}
-
-__device__ __forceinline__ Unit make_unit(const ExtendParams &p, const RawUnit &w) {
+__device__ __forceinline__ Unit load_unit(const ExtendParams &p, int u) {
   Unit r = {0, 0, 0, 0, 0};
-  const Request q = check_request(p.a, w.start, w.len);
-  r.cnt = check_count(p.a, w.cnt);
+  const Request q = load_request(p.a, u / p.a.Hkv);
+  r.cnt = load_count(p.a, u);
   r.start = q.start, r.len = q.len;
   r.groups = ceil_div(q.len, p.mt);
   if (r.groups) r.tiles = tiles_of(p.a, entry_bound(p.a, r, q.len - 1));
   return r;
 }
-
-__device__ __forceinline__ Unit load_unit(const ExtendParams &p, int u) { return make_unit(p, raw_unit(p.a, u)); }
 
 // The first group of tokens that has more than `tiles` tiles of keys.
 __device__ __forceinline__ int first_longer(const ExtendParams &p, const Unit &u, int tiles) {
@@ -290,6 +281,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   pdl_wait();
   pdl_trigger();
   if (tid == 0) x.pending = load_status(a.status);
+  // groups of all units, or their tiles and costs (below 2^31): a warp's blocks of 32 units each
+  const int units = a.B * a.Hkv;
+  const bool sliced = p.pairs == 1;
+  Unit few = {0, 0, 0, 0, 0};                              // a lane's unit, where there are no more than 32
+  if (units <= 32 && lane < units && (warp == 0 || warp == 9)) few = load_unit(p, lane);
+  {
+    uint32_t total = 0;
+    for (int u0 = 32 * warp; u0 < units; u0 += kThreads) {
+      const Unit r = units <= 32 ? few : (u0 + lane < units ? load_unit(p, u0 + lane) : Unit{0, 0, 0, 0, 0});
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, (uint32_t)(sliced ? (r.groups ? r.tiles + kUnitCost : 0) : r.groups));
+      if (lane == 0 && u0 < 1024) x.block[u0 >> 5] = sum;
+      total += sum;
+    }
+    if (lane == 0) x.sum[warp] = total;
+  }
   __syncthreads();
   tc_fence_after();
   const bool pending = x.pending != 0;      // an error is pending: no work
@@ -325,28 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     if (pending) {
     } else if (warp == 9) {
       // ------------------------------------------------------- the work, and K's tiles
-      const int units = a.B * a.Hkv, cta = (int)gridDim.x;
-      const bool sliced = p.pairs == 1;
-      uint32_t total = 0;                                  // groups, or tiles of all units and their costs (below 2^31)
-      uint32_t block = 0;                                  // a lane's block of 32 units: theirs
-      Unit few = {0, 0, 0, 0, 0};                          // a lane's unit, where there are no more than 32
-      for (int u0 = 0; u0 < units; u0 += 128) {
-        // (the loads of 128 units are on their way together)
-        RawUnit raw[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (u0 + 32 * k + lane < units) raw[k] = raw_unit(a, u0 + 32 * k + lane);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (u0 + 32 * k >= units) break;
-          Unit r = {0, 0, 0, 0, 0};
-          if (u0 + 32 * k + lane < units) r = make_unit(p, raw[k]);
-          if (u0 + k == 0) few = r;
-          const uint32_t sum = __reduce_add_sync(0xffffffffu, (uint32_t)(sliced ? (r.groups ? r.tiles + kUnitCost : 0) : r.groups));
-          if (lane == u0 / 32 + k) block = sum;
-          total += sum;
-        }
-      }
+      const int cta = (int)gridDim.x;
+      uint32_t total = lane < kThreads / 32 ? x.sum[lane] : 0u;
+      total = __reduce_add_sync(0xffffffffu, total);
       const int whole_groups = (int)(total / cta * cta);
       int cut = 1;
       if (!sliced) {
@@ -378,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       const int slice_end = want + per;
       if (sliced && units <= 1024) {
         // the block of units that the slice begins in
-        const int incl = warp_incl_scan((int)block);
+        const int incl = warp_incl_scan(32 * lane < units ? (int)x.block[lane] : 0);
         const uint32_t past = __ballot_sync(0xffffffffu, incl <= want);      // (a prefix: sums ascend)
         const int skip = min(__popc(past), (units - 1) / 32);
         if (skip > 0) base_u = 32 * (skip - 1), items_here = __shfl_sync(0xffffffffu, incl, skip - 1);

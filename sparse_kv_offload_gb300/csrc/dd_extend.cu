@@ -259,14 +259,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   const uint32_t k_full = bars, k_free = k_full + 8 * kK, v_full = k_free + 8 * kK, v_ok = v_full + 8 * kV,
                  v_free = v_ok + 8 * kV, q_full = v_free + 8 * kV, q_free = q_full + 8, s_full = q_free + 8,
                  p_half = s_full + 16, p_ready = p_half + 16, o_full = p_ready + 16, item_full = o_full + 16, item_free = item_full + 16,
-                 looked = item_free + 16, handed = looked + 16, taken = handed + 8, mma_done = taken + 8;
+                 looked = item_free + 16, handed = looked + 16, taken = handed + 8, mma_done = taken + 8, stored = mma_done + 8;
   if (tid == 0) {
     for (int i = 0; i < kK; ++i) mbar_init(k_full + 8 * i, 1), mbar_init(k_free + 8 * i, 1);
     for (int i = 0; i < kV; ++i) mbar_init(v_full + 8 * i, 1), mbar_init(v_ok + 8 * i, 1), mbar_init(v_free + 8 * i, 1);
     mbar_init(q_full, 1), mbar_init(q_free, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(looked + 8 * i, 1), mbar_init(s_full + 8 * i, 2), mbar_init(p_half + 8 * i, 4), mbar_init(p_ready + 8 * i, 4), mbar_init(o_full + 8 * i, 1);
-      mbar_init(item_full + 8 * i, 1), mbar_init(item_free + 8 * i, 11);
+      mbar_init(item_full + 8 * i, 1), mbar_init(item_free + 8 * i, 11), mbar_init(stored + 8 * i, 4);
     }
     mbar_init(handed, 4), mbar_init(taken, 4), mbar_init(mma_done, 1);
     x.bad_item = -1, x.dead = 0, x.tasks = 0;
@@ -303,8 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   const int rows_tile = a.tt * a.G;         // query rows of a tile
   const int chunks = kTileKeys / a.cs;      // of a tile
 
-  // Waits give up together: the first that runs out (2 s) ends the CTA's work.  What has
-  // happened passes every waiter, so warps that meet at a barrier give up at the same one.
+  // The first wait that runs out (2 s) ends the CTA's work: the others give up with it.
   volatile int *dead = &x.dead;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     if (mbar_try_wait(bar, parity & 1u)) return true;
@@ -764,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     const uint32_t s_at = tmem + lane_base + 128 * w, o_at = tmem + lane_base + 256 + 128 * w;
     const int tok = r / a.G, head = r % a.G;
     const bool some = 32 * quarter < rows_tile;            // of this warp's rows are query rows
-    uint32_t ns = 0, no = 0, n_both = 0, t_base = 0;
+    uint32_t ns = 0, no = 0, n_both = 0, n_parts = 0, t_base = 0;
     float2 *stat = reinterpret_cast<float2 *>(smem + kTileBytes);    // (one row tile leaves the second's queries' place free)
     bool ok = true;
     for (uint32_t n = 0; ok && !pending; ++n) {
@@ -983,7 +982,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           if (lane == 0) mbar_arrive(taken);
         }
         if (parts > 1) {
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+          // (a wait that gives up: a warp may have done so already, before an event that the others still saw)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(stored + 8 * w);
+          ok = wait_warp(stored + 8 * w, n_parts++);
+          if (!ok) break;
           if (quarter == 0 && lane == 0) {
             __threadfence();
             int32_t *ctr = p.w.ctr + 2 + it.cut + (p.pairs == 2 ? w : 0);

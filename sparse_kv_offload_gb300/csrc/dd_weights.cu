@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   const uint32_t bars = smem_u32(x.bars);
   const uint32_t rec_full = bars, pair_full = rec_full + 8 * kRec, pair_free = pair_full + 8 * kRec, k_free = pair_free + 8 * kRec,
                  q_full = k_free + 8 * kPairs, q_free = q_full + 8 * kQ, s_full = q_free + 8 * kQ, s_free = s_full + 32,
-                 mma_done = s_free + 32;
+                 mma_done = s_free + 32, summed = mma_done + 8;
   if (tid == 0) {
     // a pair: its record and its tiles; free again after the products (tiles) and the sums (record)
     for (int i = 0; i < kRec; ++i)
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     // a tile of queries: its copy and its log-sum-exps; free after the products and the sums
     for (int i = 0; i < kQ; ++i) mbar_init(q_full + 8 * i, 1), mbar_init(q_free + 8 * i, kSums + 1);
     for (int i = 0; i < 4; ++i) mbar_init(s_full + 8 * i, 2), mbar_init(s_free + 8 * i, 4);
-    mbar_init(mma_done, 1);
+    mbar_init(mma_done, 1), mbar_init(summed, 4), mbar_init(summed + 8, 4);
     x.dead = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -448,7 +448,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           if (h < 3 && 32 * h + 32 < cols) tmem_ld32(at + 32 * h + 32, s[(h + 1) & 1]);
           const float *v = s[h & 1];
           if (whole) {
-            // all exponentials before the first sum, which would wait for its own
             float y[32];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -484,7 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
       if ((lane & 15) == 0) x.sum[n & 1u][w][2 * quarter + (lane >> 4)] = total;
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory");
+      // (a wait that gives up: a warp may have done so already, before an event that the others still saw)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(summed + 8 * w);
+      ok = wait_warp(summed + 8 * w, n);
+      if (!ok) break;
       const int parts = r.parts, part0 = r.part0, part = r.part, cut = r.cut;
       __syncwarp();
       if (lane == 0) mbar_arrive(pair_free + 8 * rec);

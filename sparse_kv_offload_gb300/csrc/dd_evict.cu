@@ -6,10 +6,17 @@
 // resident chunks c with first <= c < n0 - last, the lower chunk first where weights are equal.
 // The N new chunks then take free slots, ascending both.
 //
-// One CTA a unit, each warp a run of 32 N chunks: a lane keeps N of them in registers (slot, weight as an order
-// key: a NaN below every number, -0 as +0), read once, all loads on their way together.  A radix select over the
-// keys in digits of 11 bits finds the E-th smallest (2,048 bins spread exponents over banks, and the first two
-// digits leave one or two keys, or equal ones: a third is rarely looked at).  Ranks are ballots, so every access is a whole line.
+// One CTA a unit, two an SM.  A radix select over the weights' order keys (a NaN below every number, -0 as +0) in
+// digits of 11 bits finds the E-th smallest: 2,048 bins spread exponents over banks, and the first two digits
+// leave one or two keys, or equal ones, so a third is rarely looked at.  What bounds it is the chain of
+// passes and barriers, not its bytes.
+//   k_evict       up to 8,192 chunks: a lane keeps up to 16 of them in registers (slot, key), read once, all
+//                 loads on their way together; ranks are ballots, so every access is a whole line
+//   k_evict_many  more: 512 threads cannot hold them, and 1,024 leave room for one CTA an SM.  The residents
+//                 become entries (key, chunk, slot) in shared memory, in any order; chunk order is kept in bitmaps
+//                 with a prefix of each word, so a rank is a prefix and a population count
+// 512 units of 16,384, 12,288, 8,192, 4,096 chunks, a quarter resident: k_evict_many 66, 56, 43, 33 us, k_evict 93, 84 (1,024
+// threads), 43, 27; 32 units: 24, 23, 18, 14 and 22, 21, 16, 11.
 #include "dd_pages.cuh"
 
 namespace dd {
@@ -46,7 +53,7 @@ __device__ __forceinline__ Counts warp_prefix(Counts v, int (*scratch)[33], Coun
 }
 
 template <int N>
-__global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
+__global__ void __launch_bounds__(512, 2) k_evict(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t sm[];
   const int words = (a.S + 31) / 32;
   uint32_t *hist = sm;                                       // [kBins]
@@ -268,12 +275,294 @@ __global__ void __launch_bounds__(1024) k_evict(const EvictArgs a) {
     }
 }
 
+constexpr uint32_t kLeaves = 0x8000u;   // of an entry's chunk: it may leave
+
+// Exclusive prefix over the block's threads, and the total.  `scratch` holds 33 ints; two barriers, none at the end.
+__device__ __forceinline__ int block_prefix(int v, int *scratch, int *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int incl = warp_incl_scan(v);
+  if (lane == 31) scratch[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int x = lane < warps ? scratch[lane] : 0, s = warp_incl_scan(x);
+    __syncwarp();
+    scratch[lane] = s - x;
+    if (lane == 31) scratch[32] = s;
+  }
+  __syncthreads();
+  *total = scratch[32];
+  return scratch[warp] + incl - v;
+}
+
+// The rank of bit c among a bitmap's, whose words have the prefix `pre`.
+__device__ __forceinline__ int rank_of(const uint32_t *bits, const uint16_t *pre, int c) {
+  return pre[c >> 5] + __popc(bits[c >> 5] & ((1u << (c & 31)) - 1u));
+}
+
+struct EvictSmem {
+  uint32_t *hist, *used, *here, *gone, *tied, *key;   // bins; bitmaps of slots and chunks; entries' keys [S]
+  uint16_t *pre, *chunk, *slot, *owner, *spare;       // words' prefix; entries [S]; chunk of a slot, free slots [S]
+};
+
+__host__ __device__ inline size_t evict_smem(int C, int S, uint32_t *w, EvictSmem *m) {
+  const int cw = (C + 31) / 32, sw = (S + 31) / 32;
+  EvictSmem x;
+  x.hist = w, x.used = x.hist + kBins, x.here = x.used + sw, x.gone = x.here + cw, x.tied = x.gone + cw, x.key = x.tied + cw;
+  x.pre = reinterpret_cast<uint16_t *>(x.key + S);
+  x.chunk = x.pre + cw, x.slot = x.chunk + S, x.owner = x.slot + S, x.spare = x.owner + S;
+  if (m) *m = x;
+  return (size_t)(kBins + sw + 3 * cw + S) * 4 + (size_t)(cw + 4 * S) * 2;
+}
+
+__global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
+  extern __shared__ __align__(16) uint32_t sm[];
+  __shared__ int scratch[2][33], s_bad, s_entries, s_may;
+  __shared__ uint32_t s_digit, s_rank, s_count, s_low, s_high;
+  constexpr int N = 16;                                      // chunks of a lane at a time
+  EvictSmem m;
+  evict_smem(a.C, a.S, sm, &m);
+  const int cw = (a.C + 31) / 32, sw = (a.S + 31) / 32;
+
+  pdl_wait();
+  pdl_trigger();
+  const int32_t status = load_status(a.status);
+  const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  const int b = u / a.Hkv;
+  const int64_t row = (int64_t)u * a.C, base = (int64_t)u * a.S;
+  const uint32_t below = (1u << lane) - 1u;
+  int32_t *const out = a.resident_out + row;
+  int32_t slot[N];
+  float weight[N];
+  auto load = [&](int c0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) slot[k] = c0 + 32 * k < a.C ? a.resident_slot[row + c0 + 32 * k] : -1;
+#pragma unroll
+    for (int k = 0; k < N; ++k) weight[k] = c0 + 32 * k < a.C ? a.weight[row + c0 + 32 * k] : 0.f;
+  };
+  int c0 = warp * 32 * N + lane;
+  load(c0);
+  const int kv = a.kv_len[b], more = a.new_len ? a.new_len[b] : 0;
+  if (status != 0) return;
+  bool bad = kv < 0 || more < 0 || (int64_t)kv + more > (int64_t)a.C * a.cs;
+  const int n0 = bad ? 0 : (kv + a.cs - 1) / a.cs, n1 = bad ? 0 : (kv + more + a.cs - 1) / a.cs;
+
+  if (tid == 0) s_bad = 0, s_entries = 0, s_may = 0, s_low = 0xFFFFFFFFu, s_high = 0u;
+  for (int i = tid; i < sw + 3 * cw; i += nt) m.used[i] = 0u;      // (and the bitmaps of chunks behind it)
+  __syncthreads();
+  const int may0 = a.first, may1 = n0 - a.last;
+  int mays = 0;
+  for (;;) {
+    uint32_t in[N];
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) in[k] = __ballot_sync(0xffffffffu, slot[k] >= 0), mine += __popc(in[k]);
+    int first = 0;                                             // one place for all of a warp's entries
+    if (lane == 0 && mine) first = atomicAdd(&s_entries, mine);
+    first = __shfl_sync(0xffffffffu, first, 0);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int c = c0 + 32 * k;
+      if (c < a.C) out[c] = slot[k];                           // as it was, until it turns out otherwise
+      if (lane == 0 && in[k]) m.here[c >> 5] = in[k];
+      if (slot[k] >= 0) {
+        // a slot of another unit, or of two chunks
+        const int64_t s = slot[k] - base;
+        const int at = first + __popc(in[k] & below);
+        bool ok = s >= 0 && s < a.S && at < a.S;
+        if (ok) ok = (atomicOr(&m.used[(int)s >> 5], 1u << (s & 31)) >> (s & 31) & 1u) == 0u;
+        if (!ok) {
+          s_bad = 1;
+        } else {
+          const bool may = c >= may0 && c < may1;
+          mays += may;
+          m.key[at] = order_key(weight[k]);
+          m.chunk[at] = (uint16_t)(may ? c | kLeaves : c), m.slot[at] = (uint16_t)s;
+        }
+      }
+      first += __popc(in[k]);
+    }
+    // (a warp's chunks of this round begin at c0 - lane)
+    c0 += nt * N;
+    if (c0 - lane >= a.C) break;
+    load(c0);
+  }
+  mays = __reduce_add_sync(0xffffffffu, mays);
+  if (lane == 0 && mays) atomicAdd(&s_may, mays);
+  __syncthreads();
+  if (bad || s_bad != 0) {
+    // left as it was
+    if (tid == 0) {
+      set_status(a.status, DD_ERR_DEVICE_CHECK);
+      if (a.evicted_cnt) a.evicted_cnt[u] = 0;
+      if (a.list_cnt) a.list_cnt[u] = 0;
+    }
+    return;
+  }
+  // the new chunks: a thread a word
+  uint32_t fresh = 0u;
+  if (tid < cw) {
+    const int lo = min(max(n0 - 32 * tid, 0), 32), hi = min(max(n1 - 32 * tid, 0), 32);
+    const uint32_t range = (hi == 32 ? ~0u : (1u << hi) - 1u) & ~(lo == 32 ? ~0u : (1u << lo) - 1u);
+    fresh = ~m.here[tid] & range;
+  }
+  int n_new;
+  const int my_new = block_prefix(__popc(fresh), scratch[0], &n_new);
+  const int entries = s_entries, leave = min(max(entries + n_new - a.keep, 0), s_may);
+
+  // the digits of the leave-th smallest key, from the top, until all keys that share them leave
+  int shift = 32;
+  uint32_t bound = 0u, rank = (uint32_t)leave;               // of those that share the digits found so far
+  uint32_t shared = (uint32_t)s_may;                         // how many share them
+  bool ties = leave > 0;
+  while (ties && shift > 0) {
+    const int next = max(0, shift - kDigit);
+    for (int i = tid; i < kBins; i += nt) m.hist[i] = 0u;
+    __syncthreads();
+    const uint32_t mask = (1u << (shift - next)) - 1u;
+    uint32_t low = 0xFFFFFFFFu, high = 0u;
+    for (int i = tid; i < entries; i += nt) {
+      const uint32_t k = m.key[i];
+      if ((m.chunk[i] & kLeaves) && (shift == 32 || k >> shift == bound)) {
+        atomicAdd(&m.hist[k >> next & mask], 1u);
+        low = min(low, k), high = max(high, k);
+      }
+    }
+    low = __reduce_min_sync(0xffffffffu, low), high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0 && low <= high) atomicMin(&s_low, low), atomicMax(&s_high, high);
+    __syncthreads();
+    if (s_low == s_high) {
+      // all alike (chunks that nothing has looked at): no digit tells them apart
+      bound = s_low, shift = 0, ties = shared != rank;
+      break;
+    }
+    const int per = kBins / nt, from = tid * per;
+    int sum = 0, all;
+    for (int i = 0; i < per; ++i) sum += (int)m.hist[from + i];
+    uint32_t before = (uint32_t)block_prefix(sum, scratch[1], &all);
+    if (before < rank && rank <= before + (uint32_t)sum)
+      for (int i = 0; i < per; ++i) {
+        const uint32_t v = m.hist[from + i];
+        if (before < rank && rank <= before + v) s_digit = from + i, s_rank = rank - before, s_count = v;
+        before += v;
+      }
+    __syncthreads();
+    bound = shift == 32 ? s_digit : bound << (shift - next) | s_digit;
+    rank = s_rank, shared = s_count, ties = shared != rank, shift = next;
+    if (tid == 0) s_low = 0xFFFFFFFFu, s_high = 0u;          // (read before the barriers in front of this)
+  }
+
+  int total;
+  if (ties) {
+    // of the keys that share the digits the first `rank` leave, in chunk order
+    for (int i = tid; i < entries; i += nt) {
+      const int c = m.chunk[i] & (kLeaves - 1u);
+      if ((m.chunk[i] & kLeaves) && m.key[i] >> shift == bound) atomicOr(&m.tied[c >> 5], 1u << (c & 31));
+    }
+    __syncthreads();
+    const int before = block_prefix(tid < cw ? __popc(m.tied[tid]) : 0, scratch[0], &total);
+    if (tid < cw) m.pre[tid] = (uint16_t)before;
+    __syncthreads();
+  }
+  if (leave > 0)
+    for (int i = tid; i < entries; i += nt) {
+      const uint32_t chunk = m.chunk[i], top = m.key[i] >> shift;
+      const int c = (int)(chunk & (kLeaves - 1u));
+      if ((chunk & kLeaves) && (top < bound || (top == bound && (!ties || rank_of(m.tied, m.pre, c) < (int)rank)))) {
+        const int s = m.slot[i];
+        atomicAnd(&m.used[s >> 5], ~(1u << (s & 31)));
+        atomicAnd(&m.here[c >> 5], ~(1u << (c & 31)));
+        atomicOr(&m.gone[c >> 5], 1u << (c & 31));
+        out[c] = -1;
+      }
+    }
+  for (int i = tid; i < a.S; i += nt) m.owner[i] = 0xFFFFu;
+  __syncthreads();
+
+  // the free slots, ascending, as many as are needed: a thread a word
+  int n_free;
+  {
+    uint32_t w = 0u;
+    if (tid < sw) {
+      w = ~m.used[tid];
+      if (tid == sw - 1 && (a.S & 31)) w &= (1u << (a.S & 31)) - 1u;
+    }
+    int at = block_prefix(__popc(w), scratch[1], &n_free);
+    for (; w && at < n_new; w &= w - 1, ++at) m.spare[at] = (uint16_t)(32 * tid + __ffs((int)w) - 1);
+  }
+  __syncthreads();
+  if (n_new > n_free && tid == 0) set_status(a.status, DD_ERR_CAPACITY);
+  const int given = min(n_new, n_free);
+  // (a word has one thread: no other writes it now)
+  uint32_t placed = 0u;
+  int j = my_new;
+  for (uint32_t w = fresh; w && j < given; w &= w - 1, ++j) {
+    const int c = 32 * tid + __ffs((int)w) - 1, s = m.spare[j];
+    placed |= w & (0u - w);
+    out[c] = (int32_t)base + s;
+    m.owner[s] = (uint16_t)c;
+    if (a.last_used) a.last_used[base + s] = a.step;
+  }
+  if (placed) m.here[tid] |= placed;
+  // the chunks that are resident now, by word
+  {
+    const int before = block_prefix(tid < cw ? __popc(m.here[tid]) : 0, scratch[0], &total);
+    if (tid < cw) m.pre[tid] = (uint16_t)before;
+  }
+  __syncthreads();
+  int32_t *const idx_to = a.list_idx ? a.list_idx + (int64_t)u * a.umax : nullptr;
+  int32_t *const slot_to = a.list_slot + (a.list_idx ? (int64_t)u * a.umax : 0);
+  for (int i = tid; i < entries; i += nt) {
+    const int c = m.chunk[i] & (kLeaves - 1u), s = m.slot[i];
+    if (!(m.here[c >> 5] >> (c & 31) & 1u)) continue;
+    m.owner[s] = (uint16_t)c;
+    if (idx_to) {
+      const int at = rank_of(m.here, m.pre, c);
+      idx_to[at] = c, slot_to[at] = (int32_t)base + s;
+    }
+  }
+  if (idx_to) {
+    j = my_new;
+    for (uint32_t w = placed; w; w &= w - 1, ++j) {
+      const int c = 32 * tid + __ffs((int)w) - 1, at = rank_of(m.here, m.pre, c);
+      idx_to[at] = c, slot_to[at] = (int32_t)base + m.spare[j];
+    }
+  }
+  if (a.evicted && leave > 0) {
+    // the chunks that left (nothing ties any more: their words' prefix takes that place)
+    uint16_t *const gone_pre = reinterpret_cast<uint16_t *>(m.tied);
+    const int before = block_prefix(tid < cw ? __popc(m.gone[tid]) : 0, scratch[1], &n_free);
+    if (tid < cw) gone_pre[tid] = (uint16_t)before;
+    __syncthreads();
+    for (int i = tid; i < entries; i += nt) {
+      const int c = m.chunk[i] & (kLeaves - 1u);
+      if (m.gone[c >> 5] >> (c & 31) & 1u) a.evicted[base + rank_of(m.gone, gone_pre, c)] = c;
+    }
+  }
+  if (tid == 0) {
+    if (a.evicted_cnt) a.evicted_cnt[u] = leave;
+    if (a.list_cnt) a.list_cnt[u] = total;
+  }
+  __syncthreads();
+  if (a.slot_chunk || a.last_used)
+    for (int i = tid; i < a.S; i += nt) {
+      const uint16_t c = m.owner[i];
+      if (a.slot_chunk) a.slot_chunk[base + i] = c == 0xFFFFu ? -1 : (int32_t)c;
+      if (a.last_used && c == 0xFFFFu) a.last_used[base + i] = -1;
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
-  // 32 warps at most, four at least, and a thread for each word of the slots' bitmap
   const int lines = (a.C + 31) / 32, words = (a.S + 31) / 32;
-  // (two CTAs an SM where 16 warps will do: 2,048 chunks of 256 units 9.9 us; 18.1 with 32 warps, in two rounds)
+  if (lines > 256) {
+    // (16,384 chunks and slots at most: 512 words of a bitmap, one a thread)
+    const size_t smem = evict_smem(a.C, a.S, nullptr, nullptr);
+    const cudaError_t e = set_dyn_smem((const void *)k_evict_many, smem);
+    return e != cudaSuccess ? e : launch_k(k_evict_many, dim3(a.units), dim3(512), smem, s, a);
+  }
+  // 16 warps at most (two CTAs an SM: 2,048 chunks of 256 units 9.9 us; 18.1 with 32 warps, in two rounds), four
+  // at least, and a thread for each word of the slots' bitmap
   int n = 1;
   while (n < 16 && n * 16 < lines) n *= 2;
   int warps = (lines + n - 1) / n;

@@ -202,3 +202,84 @@ def test_device_checks(dd):
             np.array_equal(got["resident_out"][1, 1], before["resident_out"][1, 1])
         for n in ("slot_chunk", "last_used", "evicted", "union_idx", "union_slot"):
             assert np.array_equal(got[n][1, 1], before[n][1, 1]), n
+
+
+# more chunks than a CTA's registers hold
+MANY = {
+    "a_few_more": (3, 2, 8193, 16, 3000, 2500, 4, 64, 0.3),
+    "whole_pool_leaves": (2, 2, 9000, 16, 1000, 0, 0, 0, 0.3),
+    "nothing_leaves": (2, 2, 12289, 16, 4096, 4096, 0, 0, 0.3),
+    "ties": (4, 2, 10000, 16, 5000, 2000, 3, 7, 0.9),
+    "odd_pool": (3, 1, 16383, 16, 77, 50, 2, 5, 0.0),
+    "protected": (2, 2, 9001, 16, 2222, 5, 4000, 4000, 0.1),
+    "many_units": (24, 8, 8200, 16, 512, 300, 1, 1, 0.3),
+    "pool_larger_than_half_of_shared_memory": (2, 2, 16384, 16, 9001, 3001, 0, 1, 0.5),
+}
+
+
+@pytest.mark.parametrize("name", list(MANY))
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_many_chunks(dd, name, in_place):
+    B, H, C, cs, S, keep, first, last, ties = MANY[name]
+    x = make(17, B, H, C, cs, S, keep, ties=ties)
+    x["kv"][0], x["n"][0] = C * cs - 40, 40               # (new chunks at the very end, where the pool is not full)
+    before = buffers(x, min(C, S))
+    got, status = run(dd, x, first, last, before, in_place=in_place)
+    want, short = want_of(x, first, last, before)
+    for n in OUT:
+        assert np.array_equal(got[n], want[n]), n
+    assert status == (dd.DD_ERR_CAPACITY if short else 0)
+    got, status = run(dd, x, first, last, before, in_place=in_place, optional=False)
+    assert np.array_equal(got["resident_out"], want["resident_out"])
+    for n in OUT[1:]:
+        assert np.array_equal(got[n], before[n]), n
+
+
+@pytest.mark.parametrize("kind", ["equal", "nan", "inf", "near", "tiny"])
+def test_many_chunks_weights_of_all_kinds(dd, kind):
+    x = make(18, 2, 2, 8800, 16, 2000, 700, ties=0.0)
+    rng = np.random.default_rng(2)
+    w = x["w"]
+    if kind == "equal":
+        w[:] = 1.5
+    elif kind == "nan":
+        w[rng.random(w.shape) < 0.6] = np.nan
+        w[rng.random(w.shape) < 0.2] = -np.nan
+    elif kind == "inf":
+        w[rng.random(w.shape) < 0.5] = np.inf
+        w[rng.random(w.shape) < 0.5] = -np.inf
+    elif kind == "near":
+        w[:] = (np.float32(1.0).view(np.uint32) + rng.integers(0, 3, w.shape).astype(np.uint32)).view(np.float32)
+    else:
+        w[:] = (rng.integers(0, 40, w.shape) * 1.4e-45).astype(np.float32)
+    before = buffers(x, 2000)
+    got, status = run(dd, x, 3, 5, before)
+    want, _ = want_of(x, 3, 5, before)
+    for n in OUT:
+        assert np.array_equal(got[n], want[n]), n
+    assert status == 0
+
+
+@pytest.mark.parametrize("what", ["outside", "negative_side", "twice", "more_than_slots", "kv"])
+def test_many_chunks_device_checks(dd, what):
+    x = make(19, 2, 2, 9000, 16, 300, 100)
+    before = buffers(x, 300)
+    s = x["slot"][1, 1]
+    here = np.flatnonzero(s >= 0)
+    base = 3 * 300
+    if what == "outside":
+        s[8999] = base + 300
+    elif what == "negative_side":
+        s[here[0]] = base - 1
+    elif what == "twice":
+        s[here[0]] = s[here[1]]
+    elif what == "more_than_slots":
+        s[:] = base + np.arange(9000) % 300
+    else:
+        x["kv"][1], x["n"][1] = 9000 * 16, 1
+    got, status = run(dd, x, 1, 1, before)
+    assert status == dd.DD_ERR_DEVICE_CHECK
+    assert np.array_equal(got["resident_out"][1, 1], s) or np.array_equal(got["resident_out"][1, 1], before["resident_out"][1, 1])
+    assert got["evicted_cnt"][1, 1] in (0, before["evicted_cnt"][1, 1]) and got["union_cnt"][1, 1] in (0, before["union_cnt"][1, 1])
+    for n in ("slot_chunk", "last_used", "evicted", "union_idx", "union_slot"):
+        assert np.array_equal(got[n][1, 1], before[n][1, 1]), n

@@ -27,8 +27,15 @@
 // Work: with two row tiles an item is a pair of them, whole or by a range of tiles of keys (cut_of); items are
 // handed out one after another, the pairs of one KV head and range next to each other, so that the CTAs
 // at work read the same keys at about the same time, out of L2.  With one row tile a unit a CTA has
-// an equal slice of all units' tiles, as nothing is read twice and the bytes bound it.  A row tile that is cut
-// has its parts joined by whoever finishes last, in the ranges' order.
+// an equal slice of all units' tiles, as nothing is read twice and the bytes bound it (decode 256 us, 435 with
+// ranges).  A row tile that is cut has its parts joined by whoever finishes last, in the ranges' order.
+//
+// What bounds it: HBM with one token a request (16 whole caches of up to 32K: 245 us, 6,150 GB/s); with many, the
+// tensor cores and beside them the issue slots of the softmax (2,048 tokens behind 62K others, 64 heads:
+// 2.7 ms, 1,560-1,610 TFLOP/s; a step of two tiles takes 3,000 cycles, its products 2,500 at the rate of a large product).  Short items pay for
+// their ends, some 12,000 cycles each: the last weights, O out of tensor memory, places and stores (first 2,048
+// tokens of four prompts, 64 heads: 315 us, 870 TFLOP/s).  The softmax's loop needs nearly all of its registers:
+// anything that the compiler keeps across it, an item's end that holds 64 columns at once among it, costs 20 to 60%.
 #include "dd_pages.cuh"
 
 namespace dd {
@@ -160,7 +167,7 @@ __device__ __forceinline__ int cut_of(int work, int groups, int longest, int cta
 constexpr int kUnitCost = 2;
 
 // A row tile that has several parts: o = sum_q f_q O_q / sum_q f_q l_q with f_q = 2^((m_q - m) sl2), m the largest
-// reference, in the order of the parts. 
+// reference, in the order of the parts.
 struct Join {
   const float *part_o;
   const float2 *part_ml;

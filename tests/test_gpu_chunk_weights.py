@@ -195,3 +195,14 @@ def test_device_checks(dd):
             ids = x["idx"][b, g, :x["cnt"][b, g]]
             off = np.abs(got[b, g, ids] - want[b, g, ids])
             assert ((off <= tol[b, g, ids]) | (got[b, g, ids] == 1.0)).all()
+
+
+@pytest.mark.parametrize("B,H,G,T,C", [(140, 8, 2, 1, 9), (131, 8, 64, 3, 3)])
+def test_many_requests_and_heads(dd, B, H, G, T, C):
+    x = pl.make_case(24, B, H, G, T, 16, C, 0.8, True, 0.1)
+    lse = pl.lse_of(x)
+    w0 = np.random.default_rng(3).random((B, H, C)).astype(np.float32)
+    got, status = pl.run_weights(dd, x, lse, w0, 0, 0.75)
+    want, tol = pl.want_weights(x, lse, 0, 0.75, w0)
+    assert status == 0
+    all_close(got, want, tol, x)

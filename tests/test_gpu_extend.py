@@ -332,3 +332,12 @@ def test_pending_error_stops_the_call_and_the_next_one_works(dd):
         got = pl.run_extend(dd, x, ctx=ctx, t=t)
         assert got[2] == 0
         pl.check_extend(got, pl.want_extend(x))
+
+
+@pytest.mark.parametrize("B,H,G,T,C", [(140, 8, 2, 1, 9), (5, 7, 4, 2, 40), (131, 8, 64, 3, 3)])
+def test_many_requests_and_heads(dd, B, H, G, T, C):
+    """More (request, KV head)s than a warp's lanes, and than their sums' places: slices and pairs of tiles."""
+    x = pl.make_case(23, B, H, G, T, 16, C, 0.8, True, 0.1)
+    got = pl.run_extend(dd, x)
+    assert got[2] == 0
+    pl.check_extend(got, pl.want_extend(x))

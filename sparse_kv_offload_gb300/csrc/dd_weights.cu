@@ -50,7 +50,9 @@ struct Misc {
   uint64_t bars[40];
   Pair pair[kRec];
   alignas(16) float lse[kQ][128];   // times -log2 e; -inf where there is no row
-  float sum[2][2][8];                // [buffer][stream][16 rows]
+  float sum[2][2][4];                // [buffer][stream][32 rows], for chunks of 64
+  long long work[kThreads / 32];      // units' pairs by rows of each warp, their pairs, and of the first blocks of 32 units
+  int pairs[kThreads / 32], one[kThreads / 32], block[32];
   int dead, pending;
   uint32_t tmem;
 };
@@ -134,6 +136,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   pdl_wait();
   pdl_trigger();
   if (tid == 0) x.pending = load_status(a.status);
+  // what there is to do: a warp's blocks of 32 units each
+  const int units = a.B * a.Hkv;
+  {
+    int pairs = 0, one = 1;
+    long long work = 0;
+    for (int u0 = 32 * warp; u0 < units; u0 += kThreads) {
+      Unit r = {0, 0, 0, 0, 0, 1};
+      if (u0 + lane < units) r = load_unit(p, u0 + lane);
+      const int sum = __reduce_add_sync(0xffffffffu, r.pairs);
+      if (lane == 0 && u0 < 1024) x.block[u0 >> 5] = sum;
+      pairs += sum, work += (long long)r.pairs * r.rows, one &= r.rows == 1;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+    one = __all_sync(0xffffffffu, one);
+    if (lane == 0) x.pairs[warp] = pairs, x.work[warp] = work, x.one[warp] = one;
+  }
   __syncthreads();
   tc_fence_after();
   const bool pending = x.pending != 0;
@@ -172,21 +191,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     // no work; the counters below are left all the same
   } else if (warp == kSums + 1) {
     // ------------------------------------------------------- the work, and K's tiles
-    const int units = a.B * a.Hkv, cta = (int)gridDim.x;
-    long long pairs = 0, work = 0;
-    bool one = true;
-    for (int u = lane; u < units; u += 32) {
-      const Unit r = load_unit(p, u);
-      pairs += r.pairs;
-      work += (long long)r.pairs * r.rows;
-      one = one && r.rows == 1;
-    }
+    const int cta = (int)gridDim.x, part_of = min(lane, kThreads / 32 - 1);
+    const bool some = lane < kThreads / 32;
+    const int pairs = __reduce_add_sync(0xffffffffu, some ? x.pairs[part_of] : 0);
+    const bool one = __all_sync(0xffffffffu, x.one[part_of]);
+    long long work = some ? x.work[part_of] : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
-      work += __shfl_xor_sync(0xffffffffu, work, o);
-    }
-    one = __all_sync(0xffffffffu, one);
+    for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
     const int rows_cut = rows_cut_of(pairs, work, one, cta);
     const int64_t staged = staged_slots(a);
 
@@ -198,6 +209,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     int ranges = 0, items = 0, items_pre = 0, cuts_pre = 0, parts_pre = 0;
     int want = one ? (int)blockIdx.x * per_cta : (int)blockIdx.x;
     const int slice_end = want + per_cta;
+    if (one && units <= 1024) {
+      // the block of units that the slice begins in
+      const int incl = warp_incl_scan(32 * lane < units ? x.block[lane] : 0);
+      const uint32_t past = __ballot_sync(0xffffffffu, incl <= want);        // (a prefix: sums ascend)
+      const int skip = min(__popc(past), (units - 1) / 32);
+      if (skip > 0) base_u = 32 * (skip - 1), items_here = __shfl_sync(0xffffffffu, incl, skip - 1);
+    }
     uint32_t n = 0, st = 0, round = 0;                     // pairs so far, the next one's place, times around
     bool ok = true;
     for (;;) {
@@ -412,6 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     const int w = warp >> 2, quarter = warp & 3, key = 32 * quarter + lane;
     const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
     const int key_chunk = w * chunks + (key >> a.cs_log), key_row = key & (a.cs - 1);
+    // the chunk's first key writes its weight
+    const bool writes = key_row == 0;
     uint32_t nq = 0, ns = 0;
     bool ok = true;
     for (uint32_t n = 0; ok; ++n) {
@@ -424,10 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       const int r0 = r.r0, r1 = r.r1, keep = r.keep_q, first = r.pos[key_chunk];
       // the key's place among the counted tokens (those at or behind it see it), and how many there are
       const int place = first == INT_MAX ? INT_MAX : first + key_row - r.start - r.tok0, counted = r.len - r.tok0;
-      // what the chunks hold so far is on its way meanwhile
-      const int at = quarter == 0 && lane < chunks ? r.pos[w * chunks + lane] : INT_MAX;
-      float *const to = p.weight + (int64_t)unit * a.C + (at == INT_MAX ? 0 : at >> a.cs_log);
-      const float old = at != INT_MAX && p.decay != 0.f && r.parts == 1 ? *to : 0.f;
+      // what the chunk holds so far is on its way meanwhile
+      float *const to = p.weight + (int64_t)unit * a.C + (first == INT_MAX ? 0 : first >> a.cs_log);
+      const int parts = r.parts;
+      const float old = writes && first != INT_MAX && p.decay != 0.f && parts == 1 ? *to : 0.f;
       float total = 0.f;
       for (int t = r0; t < r1; ++t, ++ns) {
         const uint32_t sq = nq % kQ, buf = ns & 1u;
@@ -484,44 +504,45 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
-      // sixteen rows' sums, then a chunk's
+      // a chunk's rows, across lanes; those of 64 in two warps
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-      if ((lane & 15) == 0) x.sum[n & 1u][w][2 * quarter + (lane >> 4)] = total;
-      // (a wait that gives up: a warp may have done so already, before an event that the others still saw)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(summed + 8 * w);
-      ok = wait_warp(summed + 8 * w, n);
-      if (!ok) break;
-      const int parts = r.parts, part0 = r.part0, part = r.part, cut = r.cut;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pair_free + 8 * rec);
-      if (quarter == 0) {
-        float v = 0.f;
-        if (lane < chunks)
-          for (int i = 0; i < a.cs >> 4; ++i) v += x.sum[n & 1u][w][lane * (a.cs >> 4) + i];
-        if (parts == 1) {
-          if (at != INT_MAX) *to = p.decay == 0.f ? v : fmaf(p.decay, old, v);
-        } else {
-          if (lane < chunks) __stcg(p.parts + (int64_t)part * 16 + w * 8 + lane, v);
-          __syncwarp();
-          int last = 0;
-          if (lane == 0) {
-            __threadfence();
-            int32_t *ctr = p.w.ctr + 2 + cut + w;
-            last = atomicAdd(ctr, 1) == parts - 1;
-            if (last) *ctr = 0;
-            __threadfence();
-          }
-          last = __shfl_sync(0xffffffffu, last, 0);
-          __syncwarp();
-          if (last && at != INT_MAX) {
-            v = 0.f;
-            for (int i = 0; i < parts; ++i) v += __ldcg(p.parts + (int64_t)(part0 + i) * 16 + w * 8 + lane);
-            *to = p.decay == 0.f ? v : fmaf(p.decay, *to, v);
-          }
+      if (a.cs > 16) total += __shfl_xor_sync(0xffffffffu, total, 16);
+      if (a.cs > 32) {
+        if (lane == 0) x.sum[n & 1u][w][quarter] = total;
+        // (a wait that gives up: a warp may have done so already, before an event that the others still saw)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(summed + 8 * w);
+        ok = wait_warp(summed + 8 * w, n);
+        if (!ok) break;
+        total = x.sum[n & 1u][w][quarter & 2] + x.sum[n & 1u][w][quarter | 1];
+      }
+      if (parts == 1) {
+        if (writes && first != INT_MAX) *to = p.decay == 0.f ? total : fmaf(p.decay, old, total);
+      } else {
+        const int part0 = r.part0, part = r.part, cut = r.cut;
+        if (writes) __stcg(p.parts + (int64_t)part * 16 + w * 8 + (key >> a.cs_log), total);
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) {
+          __threadfence();
+          int32_t *ctr = p.w.ctr + 2 + cut + w;
+          last = atomicAdd(ctr, 1) == 4 * parts - 1;       // (four warps a part)
+          if (last) *ctr = 0;
+          __threadfence();
+        }
+        last = __shfl_sync(0xffffffffu, last, 0);
+        __syncwarp();
+        const int at = last && lane < chunks ? r.pos[w * chunks + lane] : INT_MAX;
+        if (at != INT_MAX) {
+          float v = 0.f;
+          for (int i = 0; i < parts; ++i) v += __ldcg(p.parts + (int64_t)(part0 + i) * 16 + w * 8 + lane);
+          float *const all = p.weight + (int64_t)unit * a.C + (at >> a.cs_log);
+          *all = p.decay == 0.f ? v : fmaf(p.decay, *all, v);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_free + 8 * rec);
     }
   }
   tc_fence_before();

@@ -59,15 +59,29 @@ struct Entry {
   int slot, pos;
 };
 
-__device__ __forceinline__ Entry load_entry(const PagesArgs &a, int64_t list, int e, int n, int64_t staged) {
-  if (e >= n) return {0, INT_MAX};
-  const int slot = a.union_slot[list + e], idx = a.union_idx[list + e];
+// As the list holds it: loaded ahead of its use and looked at then (a check behind the load would wait for it).
+struct RawEntry {
+  int slot, idx;
+};
+
+__device__ __forceinline__ RawEntry fetch_entry(const PagesArgs &a, int64_t list, int e, int n) {
+  if (e >= n) return {0, 0};
+  return {a.union_slot[list + e], a.union_idx[list + e]};
+}
+
+__device__ __forceinline__ Entry check_entry(const PagesArgs &a, RawEntry r, bool there, int64_t staged) {
+  if (!there) return {0, INT_MAX};
+  const int slot = r.slot, idx = r.idx;
   const bool ok = idx >= 0 && idx < a.C && (slot >= 0 ? slot < a.hot_slots : -(int64_t)slot - 1 < staged);
   if (!ok) {
     set_status(a.status, DD_ERR_DEVICE_CHECK);
     return {0, INT_MAX};
   }
   return {slot, idx << a.cs_log};
+}
+
+__device__ __forceinline__ Entry load_entry(const PagesArgs &a, int64_t list, int e, int n, int64_t staged) {
+  return check_entry(a, fetch_entry(a, list, e, n), e < n, staged);
 }
 
 __device__ __forceinline__ int64_t staged_slots(const PagesArgs &a) {

@@ -253,12 +253,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       const int unit = base_u + src;
       const int64_t list = (int64_t)unit * a.umax;
       const bool keep = one && u.len > u.tok0;
-      // 32 entries at a time, those of the next two times on their way
+      // 32 entries at a time, those of the next time on their way
       const int two = 2 * chunks, per = 32 / two;          // pairs a time
-      auto batch = [&](int pr) { return pr < p1 ? load_entry(a, list, pr * two + lane, min(u.cnt, p1 * two), staged) : Entry{0, INT_MAX}; };
-      Entry now = batch(p0), then = batch(p0 + per);
+      const int ents = min(u.cnt, p1 * two);
+      RawEntry then = fetch_entry(a, list, p0 * two + lane, ents);
       for (int b = p0; ok && b < p1; b += per) {
-        const Entry later = batch(b + 2 * per);
+        const Entry now = check_entry(a, then, b * two + lane < ents, staged);
+        then = fetch_entry(a, list, (b + per) * two + lane, ents);
         for (int pr = b; pr < min(b + per, p1); ++pr, ++n) {
           const uint32_t rec = n % kRec;
           if (n >= kRec) ok = wait_warp(pair_free + 8 * rec, n / kRec - 1);
@@ -290,7 +291,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           load_third(0, slot, pos, st, pair_full + 8 * rec);
           if (++st == kPair) st = 0, ++round;
         }
-        now = then, then = later;
       }
       if (!ok) break;
       want = one ? want + p1 - p0 : __shfl_sync(0xffffffffu, ticket, 0) + cta;

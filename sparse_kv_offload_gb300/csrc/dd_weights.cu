@@ -19,9 +19,10 @@
 // a pair's parts (16 sums at most) are added up in order by whoever finishes last.
 //
 // What bounds it: with many query rows the exponentials, 16 a clock and SM (2 requests, 2,048 tokens, 64 heads, 16K of
-// context: 1.11 ms, 93% of that rate; a quarter of them as polynomials on the FMA pipe: 1.32); with one token
-// a request the asking for boxes (16 whole caches of up to 32K in chunks of 16: 151 us, 5,000 GB/s; one
-// warp asking 255, two 182 before entries came two batches ahead).
+// context: 1.11 ms, 93% of that rate; a quarter of them as polynomials on the FMA pipe: 1.32).  With two tiles of
+// query rows a pair its ends count, some 1,400 of 5,470 cycles (last 32 tokens of 8 prompts, 64 heads: 130 us, 60%).  With
+// one token a request HBM (16 whole caches of up to 32K in chunks of 16: 126 us, 5,960 GB/s; 130 with two pairs
+// on the way; 189 as items; 145 while a list's entries were looked at right behind their loads, not a batch later).
 #include "dd_pages.cuh"
 
 namespace dd {

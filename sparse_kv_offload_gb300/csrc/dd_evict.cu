@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
       }
       first += __popc(in[k]);
     }
-    // (a warp's chunks of this round begin at c0 - lane)
+    // (a warp's next chunks begin at c0 - lane)
     c0 += nt * N;
     if (c0 - lane >= a.C) break;
     load(c0);

@@ -283,3 +283,30 @@ def test_many_chunks_device_checks(dd, what):
     assert got["evicted_cnt"][1, 1] in (0, before["evicted_cnt"][1, 1]) and got["union_cnt"][1, 1] in (0, before["union_cnt"][1, 1])
     for n in ("slot_chunk", "last_used", "evicted", "union_idx", "union_slot"):
         assert np.array_equal(got[n][1, 1], before[n][1, 1]), n
+
+
+@pytest.mark.parametrize("C,S", [(40, 100), (100, 16384), (9000, 16384)])
+def test_more_slots_than_chunks(dd, C, S):
+    """Pools larger than the cache: no list (it has Umax places), the rest as ever."""
+    import torch
+    x = make(21, 2, 1, C, 16, S, C // 2, ties=0.2, full=0.9)
+    before = buffers(x, 1)
+    want, short = want_of(x, 1, 2, buffers(x, C))
+    t = {n: torch.from_numpy(v).cuda() for n, v in before.items()}
+    with dd.Context(dd.Shape(2, 1, 1, 128, C * 16, 16, C, 1), 0, 2 * S) as ctx:
+        args = (torch.from_numpy(x["w"]).cuda(), torch.from_numpy(x["kv"]).cuda(), torch.from_numpy(x["slot"]).cuda(), t["resident_out"],
+                x["keep"], S)
+        rest = {n: t[n] for n in OUT[1:5]}
+        ctx.evict_chunks(*args, first=1, last=2, new_len=torch.from_numpy(x["n"]).cuda(), step=77, **rest)
+        assert ctx.status() == 0 and not short
+        with pytest.raises(dd.DDError):                   # lists of Umax = C places
+            lists = [torch.zeros(2 * C, dtype=torch.int32, device="cuda") for _ in range(2)]
+            ctx.evict_chunks(*args, union_idx=lists[0], union_slot=lists[1], union_cnt=t["union_cnt"])
+    for n in OUT[:5]:
+        got = t[n].cpu().numpy()
+        if n == "evicted":                                # (entries behind the counts keep what they held)
+            for b in range(2):
+                k = want["evicted_cnt"][b, 0]
+                assert np.array_equal(got[b, 0, :k], want[n][b, 0, :k]) and np.array_equal(got[b, 0, k:], before[n][b, 0, k:])
+        else:
+            assert np.array_equal(got, want[n]), n

@@ -15,8 +15,8 @@
 //   k_evict_many  more: 512 threads cannot hold them, and 1,024 leave room for one CTA an SM.  The residents
 //                 become entries (key, chunk, slot) in shared memory, in any order; chunk order is kept in bitmaps
 //                 with a prefix of each word, so a rank is a prefix and a population count
-// 512 units of 16,384, 12,288, 8,192, 4,096 chunks, a quarter resident: k_evict_many 66, 56, 43, 33 us, k_evict 93, 84 (1,024
-// threads), 43, 27; 32 units: 24, 23, 18, 14 and 22, 21, 16, 11.
+// 512 units of 16,384, 12,288, 8,192, 4,096 chunks, a quarter resident: k_evict_many 61, 51, 41, 33 us, k_evict 93, 84 (1,024
+// threads), 43, 27; 32 units: 22, 19, 16, 14 and 22, 21, 16, 11.
 #include "dd_pages.cuh"
 
 namespace dd {
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t sm[];
   __shared__ int scratch[2][33], s_bad, s_entries, s_may;
   __shared__ uint32_t s_digit, s_rank, s_count, s_low, s_high;
-  constexpr int N = 16;                                      // chunks of a lane at a time
+  constexpr int N = 8;                                       // chunks of a lane at a time (16: 66 us for 61, 4: 64)
   EvictSmem m;
   evict_smem(a.C, a.S, sm, &m);
   const int cw = (a.C + 31) / 32, sw = (a.S + 31) / 32;
@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
   const int64_t row = (int64_t)u * a.C, base = (int64_t)u * a.S;
   const uint32_t below = (1u << lane) - 1u;
   int32_t *const out = a.resident_out + row;
+  const bool copy = a.resident_out != a.resident_slot;
   int32_t slot[N];
   float weight[N];
   auto load = [&](int c0) {
@@ -350,6 +351,7 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
   for (int i = tid; i < sw + 3 * cw; i += nt) m.used[i] = 0u;      // (and the bitmaps of chunks behind it)
   __syncthreads();
   const int may0 = a.first, may1 = n0 - a.last;
+  const uint32_t slots = base <= INT_MAX ? (uint32_t)a.S : 0u;     // (a unit behind all 32-bit slots has none)
   int mays = 0;
   for (;;) {
     uint32_t in[N];
@@ -362,17 +364,16 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int c = c0 + 32 * k;
-      if (c < a.C) out[c] = slot[k];                           // as it was, until it turns out otherwise
+      if (copy && c < a.C) out[c] = slot[k];                   // as it was, until it turns out otherwise
       if (lane == 0 && in[k]) m.here[c >> 5] = in[k];
       if (slot[k] >= 0) {
-        // a slot of another unit, or of two chunks
-        const int64_t s = slot[k] - base;
+        // a slot of another unit, or more chunks than slots (two chunks of a slot: see below)
+        const uint32_t s = (uint32_t)slot[k] - (uint32_t)base;
         const int at = first + __popc(in[k] & below);
-        bool ok = s >= 0 && s < a.S && at < a.S;
-        if (ok) ok = (atomicOr(&m.used[(int)s >> 5], 1u << (s & 31)) >> (s & 31) & 1u) == 0u;
-        if (!ok) {
+        if (s >= slots || at >= a.S) {
           s_bad = 1;
         } else {
+          atomicOr(&m.used[s >> 5], 1u << (s & 31));
           const bool may = c >= may0 && c < may1;
           mays += may;
           m.key[at] = order_key(weight[k]);
@@ -389,7 +390,19 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
   mays = __reduce_add_sync(0xffffffffu, mays);
   if (lane == 0 && mays) atomicAdd(&s_may, mays);
   __syncthreads();
-  if (bad || s_bad != 0) {
+  // the new chunks: a thread a word
+  uint32_t fresh = 0u;
+  if (tid < cw) {
+    const int lo = min(max(n0 - 32 * tid, 0), 32), hi = min(max(n1 - 32 * tid, 0), 32);
+    const uint32_t range = (hi == 32 ? ~0u : (1u << hi) - 1u) & ~(lo == 32 ? ~0u : (1u << lo) - 1u);
+    fresh = ~m.here[tid] & range;
+  }
+  // (and how many slots are held: as many as chunks hold one)
+  int both;
+  const int my_new = block_prefix(__popc(fresh) | __popc(tid < sw ? m.used[tid] : 0u) << 16, scratch[0], &both) & 0xFFFF;
+  const int n_new = both & 0xFFFF, entries = s_entries;
+  bad = bad || s_bad != 0 || both >> 16 != entries;
+  if (bad) {
     // left as it was
     if (tid == 0) {
       set_status(a.status, DD_ERR_DEVICE_CHECK);
@@ -398,16 +411,7 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
     }
     return;
   }
-  // the new chunks: a thread a word
-  uint32_t fresh = 0u;
-  if (tid < cw) {
-    const int lo = min(max(n0 - 32 * tid, 0), 32), hi = min(max(n1 - 32 * tid, 0), 32);
-    const uint32_t range = (hi == 32 ? ~0u : (1u << hi) - 1u) & ~(lo == 32 ? ~0u : (1u << lo) - 1u);
-    fresh = ~m.here[tid] & range;
-  }
-  int n_new;
-  const int my_new = block_prefix(__popc(fresh), scratch[0], &n_new);
-  const int entries = s_entries, leave = min(max(entries + n_new - a.keep, 0), s_may);
+  const int leave = min(max(entries + n_new - a.keep, 0), s_may);
 
   // the digits of the leave-th smallest key, from the top, until all keys that share them leave
   int shift = 32;

@@ -636,7 +636,8 @@ dd_status dd_chunk_weights(dd_ctx *ctx, const dd_weights_args *args, dd_stream_t
  *      call, ascending, as dd_extend_attn and the decode attentions read it (all three or none; S <= Umax)
  * Entries behind a count keep what they held.  A slot outside the unit's range or held by two chunks, or a
  * length outside [0, L], sets DD_ERR_DEVICE_CHECK: the unit's resident_out is then its resident_slot, its
- * counts 0, and the rest as it was.  K and V are not touched: an evicted chunk's slot is free at once. */
+ * counts 0, and the rest as it was.  What one unit reports does not touch the others.  K and V are not
+ * touched: an evicted chunk's slot is free at once. */
 typedef struct {
   const float *weight;
   const int32_t *kv_len, *new_len;

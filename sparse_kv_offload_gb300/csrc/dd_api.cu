@@ -35,6 +35,7 @@ struct dd_ctx {
   dd::Attn4Plan plan4;
   int32_t *arrive4 = nullptr;         // 4-bit attention: CTAs done with each unit (zero between calls)
   int32_t *page_ctr = nullptr;        // kernels over paged caches: items handed out, parts done (zero between calls)
+  uint32_t *evict_launches = nullptr; // eviction: launches of each unit, then the last one that reported an error
   // host side
   int32_t *h_miss = nullptr;          // pinned: [1 + max_misses]
   cudaStream_t copy_stream = nullptr;
@@ -222,6 +223,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   add(1, 8);                                   // self-test word
   add(units, 4);             // 4-bit attention: arrival counters
   add(2 + (int64_t)dd::kCtrPerCta * c->sm_count, 4);   // kernels over paged caches: counters
+  add(units + 1, 4);         // eviction: launches
   if (cudaMalloc(&c->ws, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   uint8_t *cur = static_cast<uint8_t *>(c->ws);
   c->status = carve<int32_t>(cur, 1);
@@ -246,6 +248,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   c->diag_word = carve<unsigned long long>(cur, 1);
   c->arrive4 = carve<int32_t>(cur, units);
   c->page_ctr = carve<int32_t>(cur, 2 + (int64_t)dd::kCtrPerCta * c->sm_count);
+  c->evict_launches = carve<uint32_t>(cur, units + 1);
   if (cudaMemset(c->ws, 0, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   const int32_t first_epoch = 1;   // look-back words start zeroed, i.e. with epoch 0
   if (cudaMemcpy(c->ticket + 2, &first_epoch, sizeof(first_epoch), cudaMemcpyHostToDevice) != cudaSuccess)
@@ -874,7 +877,7 @@ dd_status dd_evict_chunks(dd_ctx *c, const dd_evict_args *e, dd_stream_t stream)
   a.list_idx = e->union_idx, a.list_slot = e->union_slot, a.list_cnt = e->union_cnt;
   a.units = c->units, a.Hkv = c->dims.Hkv, a.C = c->C, a.cs = c->dims.cs, a.S = e->slots_per_unit;
   a.keep = e->keep, a.first = e->first, a.last = e->last, a.step = e->step, a.umax = c->umax;
-  a.status = c->status;
+  a.status = c->status, a.launches = c->evict_launches, a.raised = c->evict_launches + c->units;
   c->launches += 1;
   return cuda_ok(dd::launch_evict(a, (cudaStream_t)stream));
 }

@@ -32,6 +32,32 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// An error that was pending before the launch stops all of its units, one that a unit of the launch reports no
+// other: `raised` is the number of the last launch that has reported one, and a unit's count of launches is the
+// number of this one (every launch runs every unit).  One thread a CTA; the others take its answer behind a barrier.
+struct Launch {
+  uint32_t number;
+  bool stopped;
+};
+__device__ __forceinline__ Launch begin_launch(const EvictArgs &a, int u) {
+  Launch l;
+  const int32_t status = load_status(a.status);
+  l.number = a.launches[u] + 1u;
+  a.launches[u] = l.number;
+  l.stopped = false;
+  if (status != 0) {
+    __threadfence();                                         // (whoever set the word has written its launch before)
+    l.stopped = *reinterpret_cast<const volatile uint32_t *>(a.raised) != l.number;
+  }
+  return l;
+}
+
+__device__ __forceinline__ void report(const EvictArgs &a, uint32_t launch, int32_t code) {
+  *reinterpret_cast<volatile uint32_t *>(a.raised) = launch;
+  __threadfence();
+  set_status(a.status, code);
+}
+
 // Exclusive prefix over the warps of up to three counts of each warp; the totals in t.
 struct Counts {
   int a, b, c;
@@ -60,12 +86,11 @@ __global__ void __launch_bounds__(512, 2) k_evict(const EvictArgs a) {
   uint32_t *used = sm + kBins;                               // [words] slots held
   uint16_t *free_slot = reinterpret_cast<uint16_t *>(used + words), *owner = free_slot + a.S;   // [S] each
   __shared__ int scratch[3][33];
-  __shared__ int s_bad;
+  __shared__ int s_bad, s_stopped;
   __shared__ uint32_t s_digit, s_rank, s_count, s_low, s_high;
 
   pdl_wait();
   pdl_trigger();
-  const int32_t status = load_status(a.status);
   const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   const int b = u / a.Hkv;
   const int64_t row = (int64_t)u * a.C, base = (int64_t)u * a.S;
@@ -80,13 +105,18 @@ __global__ void __launch_bounds__(512, 2) k_evict(const EvictArgs a) {
 #pragma unroll
   for (int k = 0; k < N; ++k) key[k] = c0 + 32 * k < a.C ? __float_as_uint(weights[32 * k]) : 0u;
   const int kv = a.kv_len[b], more = a.new_len ? a.new_len[b] : 0;
-  if (status != 0) return;
+  uint32_t launch = 0u;                                      // (thread 0's, which reports)
+  if (tid == 0) {
+    const Launch l = begin_launch(a, u);
+    launch = l.number, s_stopped = l.stopped;
+  }
   bool bad = kv < 0 || more < 0 || (int64_t)kv + more > (int64_t)a.C * a.cs;
   const int n0 = bad ? 0 : (kv + a.cs - 1) / a.cs, n1 = bad ? 0 : (kv + more + a.cs - 1) / a.cs;
 
   if (tid == 0) s_bad = 0, s_low = 0xFFFFFFFFu, s_high = 0u, s_count = 0u;
   for (int i = tid; i < words; i += blockDim.x) used[i] = 0u;
   __syncthreads();
+  if (s_stopped) return;
   Counts n = {0, 0, 0};                                      // resident, new, candidates
   const int may0 = a.first, may1 = n0 - a.last;
 #pragma unroll
@@ -114,7 +144,7 @@ __global__ void __launch_bounds__(512, 2) k_evict(const EvictArgs a) {
   if (bad) {
     // left as it was
     if (tid == 0) {
-      set_status(a.status, DD_ERR_DEVICE_CHECK);
+      report(a, launch, DD_ERR_DEVICE_CHECK);
       if (a.evicted_cnt) a.evicted_cnt[u] = 0;
       if (a.list_cnt) a.list_cnt[u] = 0;
     }
@@ -226,7 +256,7 @@ __global__ void __launch_bounds__(512, 2) k_evict(const EvictArgs a) {
     for (int i = tid; i < a.S; i += blockDim.x) owner[i] = 0xFFFFu;
   }
   __syncthreads();
-  if (all.b > n_free && tid == 0) set_status(a.status, DD_ERR_CAPACITY);
+  if (all.b > n_free && tid == 0) report(a, launch, DD_ERR_CAPACITY);
   const int given = min(all.b, n_free);
 
   // (new chunks lie behind n0, among the residents there)
@@ -316,7 +346,7 @@ __host__ __device__ inline size_t evict_smem(int C, int S, uint32_t *w, EvictSme
 
 __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t sm[];
-  __shared__ int scratch[2][33], s_bad, s_entries, s_may;
+  __shared__ int scratch[2][33], s_bad, s_stopped, s_entries, s_may;
   __shared__ uint32_t s_digit, s_rank, s_count, s_low, s_high;
   constexpr int N = 8;                                       // chunks of a lane at a time (16: 66 us for 61, 4: 64)
   EvictSmem m;
@@ -325,7 +355,6 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
 
   pdl_wait();
   pdl_trigger();
-  const int32_t status = load_status(a.status);
   const int u = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
   const int b = u / a.Hkv;
   const int64_t row = (int64_t)u * a.C, base = (int64_t)u * a.S;
@@ -343,13 +372,18 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
   int c0 = warp * 32 * N + lane;
   load(c0);
   const int kv = a.kv_len[b], more = a.new_len ? a.new_len[b] : 0;
-  if (status != 0) return;
+  uint32_t launch = 0u;                                      // (thread 0's, which reports)
+  if (tid == 0) {
+    const Launch l = begin_launch(a, u);
+    launch = l.number, s_stopped = l.stopped;
+  }
   bool bad = kv < 0 || more < 0 || (int64_t)kv + more > (int64_t)a.C * a.cs;
   const int n0 = bad ? 0 : (kv + a.cs - 1) / a.cs, n1 = bad ? 0 : (kv + more + a.cs - 1) / a.cs;
 
   if (tid == 0) s_bad = 0, s_entries = 0, s_may = 0, s_low = 0xFFFFFFFFu, s_high = 0u;
   for (int i = tid; i < sw + 3 * cw; i += nt) m.used[i] = 0u;      // (and the bitmaps of chunks behind it)
   __syncthreads();
+  if (s_stopped) return;
   const int may0 = a.first, may1 = n0 - a.last;
   const uint32_t slots = base <= INT_MAX ? (uint32_t)a.S : 0u;     // (a unit behind all 32-bit slots has none)
   int mays = 0;
@@ -405,7 +439,7 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
   if (bad) {
     // left as it was
     if (tid == 0) {
-      set_status(a.status, DD_ERR_DEVICE_CHECK);
+      report(a, launch, DD_ERR_DEVICE_CHECK);
       if (a.evicted_cnt) a.evicted_cnt[u] = 0;
       if (a.list_cnt) a.list_cnt[u] = 0;
     }
@@ -494,7 +528,7 @@ __global__ void __launch_bounds__(512, 2) k_evict_many(const EvictArgs a) {
     for (; w && at < n_new; w &= w - 1, ++at) m.spare[at] = (uint16_t)(32 * tid + __ffs((int)w) - 1);
   }
   __syncthreads();
-  if (n_new > n_free && tid == 0) set_status(a.status, DD_ERR_CAPACITY);
+  if (n_new > n_free && tid == 0) report(a, launch, DD_ERR_CAPACITY);
   const int given = min(n_new, n_free);
   // (a word has one thread: no other writes it now)
   uint32_t placed = 0u;

@@ -310,6 +310,7 @@ struct EvictArgs {
   int32_t *resident_out, *slot_chunk, *last_used, *evicted, *evicted_cnt, *list_idx, *list_slot, *list_cnt;
   int units, Hkv, C, cs, S, keep, first, last, step, umax;
   int32_t *status;
+  uint32_t *launches, *raised;   // [units] launches so far, the same for all units; [1] the last one with an error
 };
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s);
 

@@ -580,7 +580,7 @@ typedef struct {
  * workspace: dd_extend_attn_workspace(ctx, T) bytes of device memory, 32-byte aligned, which calls on
  * one stream may share; it holds nothing between calls.  out must not overlap the inputs.
  * A call that reports DD_ERR_DEVICE_CHECK leaves each (request, KV head)'s outputs as its result without
- * what was out of range, or as they were. */
+ * what was out of range; those of a request that is left out stay as they were. */
 typedef struct {
   dd_new_rows rows;
   dd_page_list pages;
@@ -602,6 +602,8 @@ dd_status dd_extend_attn(dd_ctx *ctx, const dd_extend_args *args, dd_stream_t st
  * has written it for these rows.  window > 0 counts the last `window` tokens of each request, 0
  * all.  decay in [0, 1]; 0 takes nothing over, whatever weight held.  A token without rows (lse -inf) adds
  * nothing.  Vhot and Vst are not used.  fp32 sums in an order that depends on the sizes alone.
+ * A call that reports DD_ERR_DEVICE_CHECK leaves every other chunk's weight as it should be: a request that
+ * is left out adds nothing (its chunks decay), a chunk or list that is left out keeps what it had.
  * workspace: dd_chunk_weights_workspace(ctx) bytes, as above. */
 typedef struct {
   dd_new_rows rows;

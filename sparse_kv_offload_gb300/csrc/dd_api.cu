@@ -34,7 +34,7 @@ struct dd_ctx {
   dd::AttnPlan plan;
   dd::Attn4Plan plan4;
   int32_t *arrive4 = nullptr;         // 4-bit attention: CTAs done with each unit (zero between calls)
-  int32_t *page_ctr = nullptr;        // kernels over paged caches: items handed out, parts done (zero between calls)
+  int32_t *page_ctr = nullptr;        // kernels over paged caches: items handed out, parts done, an error (zero between calls)
   uint32_t *evict_launches = nullptr; // eviction: launches of each unit, then the last one that reported an error
   // host side
   int32_t *h_miss = nullptr;          // pinned: [1 + max_misses]
@@ -222,7 +222,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   add(3, 4);                                   // ticket counters + look-back epoch
   add(1, 8);                                   // self-test word
   add(units, 4);             // 4-bit attention: arrival counters
-  add(2 + (int64_t)dd::kCtrPerCta * c->sm_count, 4);   // kernels over paged caches: counters
+  add(3 + (int64_t)dd::kCtrPerCta * c->sm_count, 4);   // kernels over paged caches: counters, an error
   add(units + 1, 4);         // eviction: launches
   if (cudaMalloc(&c->ws, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   uint8_t *cur = static_cast<uint8_t *>(c->ws);
@@ -247,7 +247,7 @@ dd_status dd_create(const dd_dims *dims, int64_t max_misses, int64_t hot_slots, 
   c->ticket = carve<int32_t>(cur, 3);
   c->diag_word = carve<unsigned long long>(cur, 1);
   c->arrive4 = carve<int32_t>(cur, units);
-  c->page_ctr = carve<int32_t>(cur, 2 + (int64_t)dd::kCtrPerCta * c->sm_count);
+  c->page_ctr = carve<int32_t>(cur, 3 + (int64_t)dd::kCtrPerCta * c->sm_count);
   c->evict_launches = carve<uint32_t>(cur, units + 1);
   if (cudaMemset(c->ws, 0, bytes) != cudaSuccess) return fail(DD_ERR_CUDA);
   const int32_t first_epoch = 1;   // look-back words start zeroed, i.e. with epoch 0
@@ -804,7 +804,7 @@ static dd_status pages_args(const dd_ctx *c, const dd_new_rows *r, const dd_page
   a.hot_slots = c->hot_slots, a.max_misses = c->max_misses;
   a.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)kD);
   a.sl2 = a.scale * 1.4426950408889634f;
-  a.status = c->status;
+  a.status = c->status, a.raised = c->page_ctr + 2 + (int64_t)dd::kCtrPerCta * c->sm_count;
   *out = a;
   return DD_OK;
 }

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         if (*dead) return false;
         if (globaltimer_ns() - t0 > 2000000000ull) {
           *dead = 1;
-          set_status(a.status, DD_ERR_TIMEOUT);
+          set_status(a.raised, DD_ERR_TIMEOUT);
           return false;
         }
       }
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         if (!sliced) want = __shfl_sync(0xffffffffu, ticket, 0) + cta;
       }
       // copies in flight are waited for before the CTA leaves
-      for (uint32_t i = kt >= kK ? kt - kK : 0; i < kt; ++i) mbar_wait(k_full + 8 * (i % kK), (i / kK) & 1u, a.status);
+      for (uint32_t i = kt >= kK ? kt - kK : 0; i < kt; ++i) mbar_wait(k_full + 8 * (i % kK), (i / kK) & 1u, a.raised);
     } else if (warp == 10) {
       // ------------------------------------------------------------- Q's and V's tiles
       const int64_t staged = staged_slots(a);
@@ -611,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         __syncwarp();
         if (lane == 0) mbar_arrive(item_free + 8 * (n & 1u));
       }
-      for (uint32_t i = vt >= kV ? vt - kV : 0; i < vt; ++i) mbar_wait(v_full + 8 * (i % kV), (i / kV) & 1u, a.status);
-      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1u, a.status);
+      for (uint32_t i = vt >= kV ? vt - kV : 0; i < vt; ++i) mbar_wait(v_full + 8 * (i % kV), (i / kV) & 1u, a.raised);
+      if (nq > 0) mbar_wait(q_full, (nq - 1) & 1u, a.raised);
     } else if (warp == 8) {
       // -------------------------------------------------------------------- products
       // (the whole warp waits and counts, so that what the products are told is uniform)
@@ -689,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       // every product issued is done before the tensor memory is freed
       if (elect_lane()) tc_commit(mma_done);
       __syncwarp();
-      mbar_wait(mma_done, 0, a.status);
+      mbar_wait(mma_done, 0, a.raised);
     } else if (warp == 11) {
       // -------------------------------------------- V's tiles that are not seen whole
       uint32_t vt = 0;
@@ -1036,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
   }
-  leave_counters(p.w, a.status, &x.pending);
+  leave_counters(p.w, a, &x.pending);
 }
 
 struct Shape {

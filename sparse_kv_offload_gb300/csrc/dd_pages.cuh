@@ -24,7 +24,9 @@ struct PagesArgs {
   int tt;                                         // tokens of a tile of query rows: tt * G <= 128
   int64_t hot_slots, max_misses;
   float scale, sl2;                               // softmax scale, and times log2 e
-  int32_t *status;
+  // The status word stops a launch where an error was pending before it.  What the launch itself finds goes to
+  // another word, which its last CTA moves there: CTAs that start later do their work all the same.
+  int32_t *status, *raised;
 };
 
 struct Request {
@@ -33,7 +35,7 @@ struct Request {
 
 __device__ __forceinline__ Request check_request(const PagesArgs &a, int start, int len) {
   if (start < 0 || len < 0 || len > a.T || (int64_t)start + len > (int64_t)a.C * a.cs) {
-    set_status(a.status, DD_ERR_DEVICE_CHECK);
+    set_status(a.raised, DD_ERR_DEVICE_CHECK);
     return {0, 0};
   }
   return {start, len};
@@ -45,7 +47,7 @@ __device__ __forceinline__ Request load_request(const PagesArgs &a, int b) {
 
 __device__ __forceinline__ int check_count(const PagesArgs &a, int n) {
   if (n < 0 || n > a.umax) {
-    set_status(a.status, DD_ERR_DEVICE_CHECK);
+    set_status(a.raised, DD_ERR_DEVICE_CHECK);
     return 0;
   }
   return n;
@@ -74,7 +76,7 @@ __device__ __forceinline__ Entry check_entry(const PagesArgs &a, RawEntry r, boo
   const int slot = r.slot, idx = r.idx;
   const bool ok = idx >= 0 && idx < a.C && (slot >= 0 ? slot < a.hot_slots : -(int64_t)slot - 1 < staged);
   if (!ok) {
-    set_status(a.status, DD_ERR_DEVICE_CHECK);
+    set_status(a.raised, DD_ERR_DEVICE_CHECK);
     return {0, INT_MAX};
   }
   return {slot, idx << a.cs_log};
@@ -247,18 +249,24 @@ struct WorkCounters {
   int n;          // arrival counters
 };
 
-// The launch's last CTA leaves the counters as it found them: whoever joins parts clears their
-// counter, and where a launch reports an error some may never be joined.  All threads, after their
+// The launch's last CTA reports its error and leaves the counters as it found them: whoever joins parts clears
+// their counter, and where a wait ran out some may never be joined.  All threads, after their
 // CTA's last arrival and a barrier.
-__device__ __forceinline__ void leave_counters(const WorkCounters &w, int32_t *status, int *last) {
+__device__ __forceinline__ void leave_counters(const WorkCounters &w, const PagesArgs &a, int *last) {
   if (threadIdx.x == 0) {
+    int what = 0;                                   // 1: the last one, 2: and there is an error
     __threadfence();
-    *last = atomicAdd(w.ctr + 1, 1) == (int)gridDim.x - 1;
-    __threadfence();
+    if (atomicAdd(w.ctr + 1, 1) == (int)gridDim.x - 1) {
+      __threadfence();
+      const int32_t error = load_status(a.raised);
+      what = error != 0 ? 2 : 1;
+      if (error != 0) set_status(a.status, error), *a.raised = 0;
+    }
+    *last = what;
   }
   __syncthreads();
   if (!*last) return;
-  if (load_status(status) != 0)
+  if (*last == 2)
     for (int i = threadIdx.x; i < w.n; i += blockDim.x) w.ctr[2 + i] = 0;
   if (threadIdx.x < 2) w.ctr[threadIdx.x] = 0;
 }

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         if (*dead) return false;
         if (globaltimer_ns() - t0 > 2000000000ull) {
           *dead = 1;
-          set_status(a.status, DD_ERR_TIMEOUT);
+          set_status(a.raised, DD_ERR_TIMEOUT);
           return false;
         }
       }
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     // copies in flight are waited for before the CTA leaves (there are no more than those of the last kPair
     // pairs, whose records are not the last one's)
     for (uint32_t i = n >= kPair ? n - kPair : 0; i < n; ++i)
-      mbar_wait(pair_full + 8 * (i % kRec), (i / kRec) & 1u, a.status);
+      mbar_wait(pair_full + 8 * (i % kRec), (i / kRec) & 1u, a.raised);
   } else if (warp == kSums + 2) {
     // ------------------------------------------------------ a third of a pair's keys
     uint32_t st = 0;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       __syncwarp();
       if (lane == 0) mbar_arrive(pair_free + 8 * rec);
     }
-    for (uint32_t i = nq >= kQ ? nq - kQ : 0; i < nq; ++i) mbar_wait(q_full + 8 * (i % kQ), (i / kQ) & 1u, a.status);
+    for (uint32_t i = nq >= kQ ? nq - kQ : 0; i < nq; ++i) mbar_wait(q_full + 8 * (i % kQ), (i / kQ) & 1u, a.raised);
   } else if (warp == kSums) {
     // -------------------------------------------------------------------- products
     const uint32_t id = idesc_bf16(128, (rows_tile + 31) / 32 * 32, 0, 0);   // (as many columns as are read)
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     }
     if (elect_lane()) tc_commit(mma_done);
     __syncwarp();
-    mbar_wait(mma_done, 0, a.status);
+    mbar_wait(mma_done, 0, a.raised);
   } else {
     // ------------------------------------------------------- exponentials and sums
     const int w = warp >> 2, quarter = warp & 3, key = 32 * quarter + lane;
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
   }
-  leave_counters(p.w, a.status, &x.pending);
+  leave_counters(p.w, a, &x.pending);
 }
 
 }  // namespace

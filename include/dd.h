@@ -598,7 +598,8 @@ dd_status dd_extend_attn(dd_ctx *ctx, const dd_extend_args *args, dd_stream_t st
 /* The attention weight that chunks gather from new tokens:
  *   weight[b,g,c] = decay * weight[b,g,c] + sum over the counted tokens t and the G heads h of KV head g
  *                   of the weights exp(scale * q.K_i - lse[b,t,h]) of the rows i of c that t sees
- * for every chunk c of the list (the others keep theirs); weight fp32 [B,Hkv,C], lse as dd_extend_attn
+ * for every chunk c of the list, one that no token sees among them (its number has to be one of a chunk all
+ * the same, its slot is not looked at); the others keep theirs.  weight fp32 [B,Hkv,C], lse as dd_extend_attn
  * has written it for these rows.  window > 0 counts the last `window` tokens of each request, 0
  * all.  decay in [0, 1]; 0 takes nothing over, whatever weight held.  A token without rows (lse -inf) adds
  * nothing.  Vhot and Vst are not used.  fp32 sums in an order that depends on the sizes alone.

@@ -71,10 +71,11 @@ __device__ __forceinline__ RawEntry fetch_entry(const PagesArgs &a, int64_t list
   return {a.union_slot[list + e], a.union_idx[list + e]};
 }
 
-__device__ __forceinline__ Entry check_entry(const PagesArgs &a, RawEntry r, bool there, int64_t staged) {
+// `last`: the last chunk that a token sees, -1 where there is no token.  The slot of one behind it is not looked at.
+__device__ __forceinline__ Entry check_entry(const PagesArgs &a, RawEntry r, bool there, int last, int64_t staged) {
   if (!there) return {0, INT_MAX};
   const int slot = r.slot, idx = r.idx;
-  const bool ok = idx >= 0 && idx < a.C && (slot >= 0 ? slot < a.hot_slots : -(int64_t)slot - 1 < staged);
+  const bool ok = idx >= 0 && idx < a.C && (idx > last || (slot >= 0 ? slot < a.hot_slots : -(int64_t)slot - 1 < staged));
   if (!ok) {
     set_status(a.raised, DD_ERR_DEVICE_CHECK);
     return {0, INT_MAX};
@@ -83,7 +84,7 @@ __device__ __forceinline__ Entry check_entry(const PagesArgs &a, RawEntry r, boo
 }
 
 __device__ __forceinline__ Entry load_entry(const PagesArgs &a, int64_t list, int e, int n, int64_t staged) {
-  return check_entry(a, fetch_entry(a, list, e, n), e < n, staged);
+  return check_entry(a, fetch_entry(a, list, e, n), e < n, INT_MAX, staged);
 }
 
 __device__ __forceinline__ int64_t staged_slots(const PagesArgs &a) {

@@ -39,6 +39,7 @@ constexpr int kItemsPerCta = 8;
 
 struct Pair {
   int unit, start, len;
+  int last;                   // position of the last token, -1 where there is none
   int tok0;                   // the first token that counts
   int r0, r1;                 // tiles of query rows to go through
   int keep_q;                 // one tile of queries for all pairs of the item: 1 first, 2 last, 3 both, 4 neither, 0 no
@@ -182,11 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   auto new_q = [](int keep) { return keep == 0 || (keep & 1); };
   auto last_q = [](int keep) { return keep == 0 || keep == 2 || keep == 3; };
   // a third of a pair's 2 * chunks chunks: a lane brings half of the columns of one (its slot and position in the
-  // lane of the chunk's number)
-  auto load_third = [&](int third, int slot, int pos, uint32_t st, uint32_t bar) {
+  // lane of the chunk's number; zeros for one behind the last token's position)
+  auto load_third = [&](int third, int slot, int pos, int last, uint32_t st, uint32_t bar) {
     const int lo = 2 * chunks * third / 3, hi = 2 * chunks * (third + 1) / 3, ch = min(lo + (lane >> 1), 31);
     const int sl = __shfl_sync(0xffffffffu, slot, ch), at = __shfl_sync(0xffffffffu, pos, ch);
-    if (ch < hi) load_chunk(p.k, p.kst, a, sl, at, lane & 1, k0 + (st * 2 + ch / chunks) * kTileBytes + ch % chunks * a.cs * 128, bar);
+    if (ch < hi) load_chunk(p.k, p.kst, a, sl, at > last ? INT_MAX : at, lane & 1, k0 + (st * 2 + ch / chunks) * kTileBytes + ch % chunks * a.cs * 128, bar);
   };
   if (pending) {
     // no work; the counters below are left all the same
@@ -254,12 +255,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       const int unit = base_u + src;
       const int64_t list = (int64_t)unit * a.umax;
       const bool keep = one && u.len > u.tok0;
+      const int last = u.len > 0 ? u.start + u.len - 1 : -1;
       // 32 entries at a time, those of the next time on their way
       const int two = 2 * chunks, per = 32 / two;          // pairs a time
       const int ents = min(u.cnt, p1 * two);
       RawEntry then = fetch_entry(a, list, p0 * two + lane, ents);
       for (int b = p0; ok && b < p1; b += per) {
-        const Entry now = check_entry(a, then, b * two + lane < ents, staged);
+        const Entry now = check_entry(a, then, b * two + lane < ents, last >> a.cs_log, staged);
         then = fetch_entry(a, list, (b + per) * two + lane, ents);
         for (int pr = b; pr < min(b + per, p1); ++pr, ++n) {
           const uint32_t rec = n % kRec;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
           const int slot = __shfl_sync(0xffffffffu, now.slot, from_lane), pos = __shfl_sync(0xffffffffu, now.pos, from_lane);
           if (lane < two) r.pos[lane] = pos, r.slot[lane] = slot;
           if (lane == 0) {
-            r.unit = unit, r.start = u.start, r.len = u.len, r.tok0 = u.tok0;
+            r.unit = unit, r.start = u.start, r.len = u.len, r.last = last, r.tok0 = u.tok0;
             r.keep_q = keep ? (pr == p0 ? (pr == p1 - 1 ? 3 : 1) : (pr == p1 - 1 ? 2 : 4)) : 0;
             r.parts = n_ranges, r.part0 = part0 + pr * n_ranges, r.part = part0 + pr * n_ranges + range;
             r.cut = 2 * (cut0 + pr);
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
             mbar_arrive(rec_full + 8 * rec);
           }
           __syncwarp();
-          load_third(0, slot, pos, st, pair_full + 8 * rec);
+          load_third(0, slot, pos, last, st, pair_full + 8 * rec);
           if (++st == kPair) st = 0, ++round;
         }
       }
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       if (!ok) break;
       const Pair &r = x.pair[rec];
       if (r.unit < 0) break;
-      load_third(1, r.slot[lane & 15], r.pos[lane & 15], st, pair_full + 8 * rec);
+      load_third(1, r.slot[lane & 15], r.pos[lane & 15], r.last, st, pair_full + 8 * rec);
       if (++st == kPair) st = 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(pair_free + 8 * rec);
@@ -343,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
       const Pair &r = x.pair[rec];
       const int unit = r.unit;
       if (unit < 0) break;
-      load_third(2, r.slot[lane & 15], r.pos[lane & 15], st, pair_full + 8 * rec);
+      load_third(2, r.slot[lane & 15], r.pos[lane & 15], r.last, st, pair_full + 8 * rec);
       if (++st == kPair) st = 0;
       const int r1 = r.r1, tok0 = r.tok0, len = r.len, b = unit / a.Hkv, h0 = unit % a.Hkv * a.G;
       if (new_q(r.keep_q)) {

@@ -50,3 +50,67 @@ def test_a_key_of_minus_infinity_has_no_weight(dd, G, T, cs):
         dx = max(pl.score_error(q, Kn, 128 ** -0.5, z) for q, z in zip(x["q64"][0, :, hs].reshape(-1, 128), lse[0, :, hs].reshape(-1)))
         want = 0.5 * w0[0, g] + new
         assert (np.abs(got[0, g] - want) <= (dx + 2.0 ** -21 + 256 * 2.0 ** -24) * new + 2.0 ** -23 * want).all()
+
+
+def both(dd, x, t, lse, w0):
+    """Attention, then weights with decay 0.5: (out, lse, weights)."""
+    ctx = pl.context(dd, x)
+    out, z, status = pl.run_extend(dd, x, ctx=ctx, t=t)
+    assert status == 0
+    w, status = pl.run_weights(dd, x, lse, w0, 0, 0.5, ctx=ctx, t=t)
+    assert status == 0
+    ctx.close()
+    return out, z, w
+
+
+@pytest.mark.parametrize("G,T", [(4, 1), (8, 5), (8, 40), (2, 150)])
+@pytest.mark.parametrize("cs", [16, 64])
+def test_chunks_that_no_token_sees_are_not_looked_at(dd, G, T, cs):
+    """Behind the last token: slots of no pool, staging slots that are not filled, and one that is."""
+    C = 30
+    x = pl.make_case(93, 2, 2, G, T, cs, C, 1.0, ragged=False, start=[3 * cs + 5, 20 * cs - T])
+    lse = pl.lse_of(x)
+    w0 = np.random.default_rng(6).random((2, 2, C)).astype(np.float32)
+    t = pl.tensors(x)
+    out, z, w = both(dd, x, t, lse, w0)
+    y = {k: (v.copy() if isinstance(v, np.ndarray) else v) for k, v in x.items()}
+    for b in range(2):
+        for g in range(2):
+            n = x["cnt"][b, g]
+            first = x["idx"][b, g, n - 1] + 1               # (lists end with the last token's chunk)
+            more = min(6, C - n, C - first)
+            y["idx"][b, g, n:n + more] = first + np.arange(more)
+            y["slot"][b, g, n:n + more] = [x["n_hot"], -1, -99, 2 ** 31 - 1, -2 ** 31, 0][:more]
+            y["cnt"][b, g] = n + more
+    u = dict(t, **{k: v for k, v in pl.tensors(y).items() if k in ("idx", "slot", "cnt")})
+    o2, z2, w2 = both(dd, y, u, lse, w0)
+    assert np.array_equal(out, o2, equal_nan=True) and np.array_equal(z, z2, equal_nan=True)
+    want, tol = pl.want_weights(x, lse, 0, 0.5, w0)
+    for b in range(2):
+        for g in range(2):
+            n = x["cnt"][b, g]
+            at = x["idx"][b, g, :n]
+            assert (np.abs(w2 - want)[b, g, at] <= tol[b, g, at]).all()
+            behind = list(y["idx"][b, g, n:y["cnt"][b, g]])
+            assert len(behind) >= 4
+            assert np.array_equal(w2[b, g, behind], w0[b, g, behind] * np.float32(0.5))
+            rest = sorted(set(range(C)) - set(at) - set(behind))
+            assert np.array_equal(w2[b, g, rest], w0[b, g, rest].astype(np.float64))
+
+
+def test_a_request_without_tokens_looks_at_no_slot(dd):
+    """Its chunks decay, whatever the list's slots are; the others are as ever."""
+    x = pl.make_case(94, 3, 2, 4, 9, 16, 25, 1.0, lens=[9, 0, 3])
+    lse = pl.lse_of(x)
+    w0 = np.random.default_rng(7).random((3, 2, 25)).astype(np.float32)
+    want, tol = pl.want_weights(x, lse, 0, 0.25, w0)
+    y = dict(x, slot=x["slot"].copy(), idx=x["idx"].copy())
+    y["slot"][1] = [[x["n_hot"] + 5] * 25, [-77] * 25]
+    got, status = pl.run_weights(dd, y, lse, w0, 0, 0.25)
+    assert status == 0
+    for b in range(3):
+        for g in range(2):
+            at = x["idx"][b, g, :x["cnt"][b, g]]
+            assert (np.abs(got - want)[b, g, at] <= tol[b, g, at]).all()
+            if b == 1:
+                assert len(at) and np.array_equal(got[b, g, at], w0[b, g, at] * np.float32(0.25))

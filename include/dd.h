@@ -602,7 +602,7 @@ dd_status dd_extend_attn(dd_ctx *ctx, const dd_extend_args *args, dd_stream_t st
  * the same, its slot is not looked at); the others keep theirs.  weight fp32 [B,Hkv,C], lse as dd_extend_attn
  * has written it for these rows.  window > 0 counts the last `window` tokens of each request, 0
  * all.  decay in [0, 1]; 0 takes nothing over, whatever weight held.  A token without rows (lse -inf) adds
- * nothing.  Vhot and Vst are not used.  fp32 sums in an order that depends on the sizes alone.
+ * nothing; without tokens (T = 0, or new_len 0) the listed chunks decay.  Vhot and Vst are not used.  fp32 sums in an order that depends on the sizes alone.
  * A call that reports DD_ERR_DEVICE_CHECK leaves every other chunk's weight as it should be: a request that
  * is left out adds nothing (its chunks decay), a chunk or list that is left out keeps what it had.
  * workspace: dd_chunk_weights_workspace(ctx) bytes, as above. */

@@ -785,7 +785,7 @@ dd_status dd_sparse_attn_decode_kv4(dd_ctx *c, const void *q, const void *Khot, 
 // What the two kernels over lists of chunks share; V's pools are the caller's to check.
 static dd_status pages_args(const dd_ctx *c, const dd_new_rows *r, const dd_page_list *l, float softmax_scale,
                             dd::PagesArgs *out) {
-  if (!rows_ok(r->q, r->q_stride) || !r->start_pos) return DD_ERR_INVALID_ARG;
+  if ((r->T > 0 && !rows_ok(r->q, r->q_stride)) || !r->start_pos) return DD_ERR_INVALID_ARG;
   if (!l->union_idx || !l->union_slot || !l->union_cnt) return DD_ERR_INVALID_ARG;
   if (c->hot_slots > 0 && (!l->Khot || !aligned16(l->Khot))) return DD_ERR_INVALID_ARG;
   if (c->max_misses > 0 && (!l->Kst || !aligned16(l->Kst))) return DD_ERR_INVALID_ARG;
@@ -793,7 +793,7 @@ static dd_status pages_args(const dd_ctx *c, const dd_new_rows *r, const dd_page
   const int64_t per_tile = 128 / c->G;
   if ((int64_t)c->units * ((r->T + per_tile - 1) / per_tile) >= (int64_t(1) << 30)) return DD_ERR_INVALID_ARG;
   // tensor maps step by less than 2^40 bytes, and not backwards
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < 3 && r->T > 0; ++i)
     if (r->q_stride[i] < 0 || r->q_stride[i] >= (int64_t(1) << 39)) return DD_ERR_INVALID_ARG;
   const dd_dims &d = c->dims;
   dd::PagesArgs a{};
@@ -843,10 +843,10 @@ int64_t dd_chunk_weights_workspace(const dd_ctx *c) {
 dd_status dd_chunk_weights(dd_ctx *c, const dd_weights_args *e, dd_stream_t stream) {
   if (!c || !e || e->rows.T < 0 || e->window < 0) return DD_ERR_INVALID_ARG;
   if (!(e->decay >= 0.f && e->decay <= 1.f)) return DD_ERR_INVALID_ARG;
-  if (c->units == 0 || e->rows.T == 0) return DD_OK;
+  if (c->units == 0) return DD_OK;                       // (without tokens the listed chunks decay)
   dd::WeightsArgs a{};
   DD_TRY(pages_args(c, &e->rows, &e->pages, e->softmax_scale, &a.p));
-  if (!e->lse || !e->weight) return DD_ERR_INVALID_ARG;
+  if ((e->rows.T > 0 && !e->lse) || !e->weight) return DD_ERR_INVALID_ARG;
   if (!e->workspace || !aligned16(e->workspace) || e->workspace_bytes < dd_chunk_weights_workspace(c))
     return DD_ERR_INVALID_ARG;
   DD_TRY(on_device(c));

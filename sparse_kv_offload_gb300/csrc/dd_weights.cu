@@ -576,9 +576,11 @@ cudaError_t launch_weights(const WeightsArgs &e, cudaStream_t stream) {
   WeightsParams p{};
   p.a = a;
   const int most = 128 / a.G, seen = e.window > 0 && e.window < a.T ? e.window : a.T;
-  p.a.tt = seen < most ? seen : most;
+  p.a.tt = seen < 1 ? 1 : (seen < most ? seen : most);
   const bool hot = a.hot_slots > 0, far = a.max_misses > 0;
-  if (!make_rows_map(&p.q, e.q, e.q_stride, a.B, a.T, a.Hq, a.G, p.a.tt) ||
+  // (without tokens nothing is read through the map)
+  const int64_t dense[3] = {(int64_t)a.Hq * kD, (int64_t)a.Hq * kD, kD};
+  if (!make_rows_map(&p.q, a.T > 0 ? e.q : e.dummy, a.T > 0 ? e.q_stride : dense, a.B, a.T > 0 ? a.T : 1, a.Hq, a.G, p.a.tt) ||
       !make_pages_map(&p.k, hot ? e.Khot : e.dummy, hot ? a.hot_slots : 1, a.cs) ||
       !make_pages_map(&p.kst, far ? e.Kst : e.dummy, far ? a.max_misses : 1, a.cs))
     return cudaErrorInvalidValue;

@@ -114,3 +114,32 @@ def test_a_request_without_tokens_looks_at_no_slot(dd):
             assert (np.abs(got - want)[b, g, at] <= tol[b, g, at]).all()
             if b == 1:
                 assert len(at) and np.array_equal(got[b, g, at], w0[b, g, at] * np.float32(0.25))
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.5, 1.0])
+def test_no_tokens_at_all(dd, decay):
+    """T = 0: the listed chunks decay, as with new_len 0, and nothing else changes."""
+    import torch
+    x = pl.make_case(95, 2, 2, 4, 5, 16, 12, 0.7, lens=[5, 2], start=[100, 40])
+    t = pl.tensors(x)
+    w0 = np.random.default_rng(8).random((2, 2, 12)).astype(np.float32)
+    w0[0, 0, x["idx"][0, 0, 0]] = np.inf
+    want = w0.copy()
+    for b in range(2):
+        for g in range(2):
+            at = x["idx"][b, g, :x["cnt"][b, g]]
+            want[b, g, at] = w0[b, g, at] * np.float32(decay) if decay else 0.0
+    with pl.context(dd, x) as ctx:
+        for q, lens in ((t["q"][:, :0], None), (t["q"][:, :0], torch.zeros_like(t["lens"])), (t["q"], torch.zeros_like(t["lens"]))):
+            w = torch.from_numpy(w0).cuda()
+            z = torch.empty(2, q.shape[1], 8, device="cuda")
+            ctx.chunk_weights(q, t["start"], z, t["Khot"], t["idx"], t["slot"], t["cnt"], w, new_len=lens, decay=decay)
+            assert ctx.status() == 0
+            assert np.array_equal(w.cpu().numpy(), want)
+        # a position is still one of the cache
+        w = torch.from_numpy(w0).cuda()
+        ctx.chunk_weights(t["q"][:, :0], t["start"] - 1000, z, t["Khot"], t["idx"], t["slot"], t["cnt"], w, decay=decay)
+        assert ctx.status() == dd.DD_ERR_DEVICE_CHECK
+        out = t["q"][:, :0].clone()
+        ctx.extend_attn(t["q"][:, :0], t["start"], t["Khot"], t["Vhot"], t["idx"], t["slot"], t["cnt"], out)
+        assert ctx.status() == 0

@@ -630,6 +630,12 @@ dd_status dd_chunk_weights(dd_ctx *ctx, const dd_weights_args *args, dd_stream_t
  *      weights are equal (-0 equals +0, a NaN is below every number);
  *   3. the N new chunks, ascending, take the free slots, ascending.  Where there are too few the later ones
  *      get none and DD_ERR_CAPACITY is set.
+ * Where tokens follow, last is 1 at least: with kv_len no multiple of cs they begin in chunk n0 - 1, which holds
+ * rows already.  It is no new chunk, and with last = 0 it may leave like any other; dd_append_kv would then drop
+ * the tokens' rows until chunk n0 begins, and they would not see themselves.  Nor does it get a slot
+ * here when it has none: its rows before kv_len are not in the pool.  So after DD_ERR_CAPACITY the call is
+ * repeated with a smaller keep, and the resident_out that it left, before the tokens are appended: with the same
+ * kv_len the chunks without a slot are new again.
  * weight fp32 [B,Hkv,C]; kv_len int32 [B]; new_len int32 [B] or NULL (no new chunks); resident_slot int32
  * [B,Hkv,C], resident_out the same or another array, written whole.  Each of these may be NULL:
  *   slot_chunk int32 [B,Hkv,S]  the chunk in each slot, or -1, written whole

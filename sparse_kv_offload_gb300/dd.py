@@ -568,11 +568,12 @@ class Context:
                                float(decay), _dev(weight, torch.float32, s.B * s.Hkv * s.C, "weight"), wp, n)
         _chk(_lib.dd_chunk_weights(self._h, a, _stream(stream)), "dd_chunk_weights")
 
-    def evict_chunks(self, weight, kv_len, resident_slot, resident_out, keep, slots_per_unit, first=0, last=0,
+    def evict_chunks(self, weight, kv_len, resident_slot, resident_out, keep, slots_per_unit, first=0, last=1,
                      new_len=None, slot_chunk=None, last_used=None, step=0, evicted=None, evicted_cnt=None,
                      union_idx=None, union_slot=None, union_cnt=None, stream=None):
         """Bring each (request, KV head)'s pool to ``keep`` chunks by gathered weight, give the chunks of the
-        tokens to come their slots and list what is resident (see dd.h)."""
+        tokens to come their slots and list what is resident.  The ``last`` chunks stay: one at least where
+        tokens follow, as they begin in a partly filled one (see dd.h)."""
         s = self.shape
         units, i32 = s.B * s.Hkv, torch.int32
         n, ns, nu = units * s.C, units * int(slots_per_unit), units * s.umax

@@ -34,10 +34,12 @@ __global__ void __launch_bounds__(kResThreads) k_update_residency(
   __shared__ unsigned long long keys[kMaxSlotsPerUnit];
   __shared__ uint8_t in_union[kMaxSlotsPerUnit];
   __shared__ int scratch[33];
+  __shared__ int32_t pending;
   pdl_wait();
   pdl_trigger();
-  if (load_status(status) != 0) return;
   const int u = blockIdx.x, tid = threadIdx.x;
+  // (read by one thread: another unit of the launch may set it at any time, and the CTA stays or leaves as a whole)
+  if (tid == 0) pending = load_status(status);
   const int64_t base = (int64_t)u * S;
   int32_t *sc = slot_chunk + base;
   int32_t *lu = last_used + base;
@@ -49,6 +51,7 @@ __global__ void __launch_bounds__(kResThreads) k_update_residency(
 
   for (int t = tid; t < S; t += kResThreads) in_union[t] = 0;
   __syncthreads();
+  if (pending != 0) return;
   // 1. union residents: refreshed and protected; count the misses
   int my_miss = 0;
   for (int i = tid; i < U; i += kResThreads) {

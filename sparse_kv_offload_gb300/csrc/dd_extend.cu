@@ -22,7 +22,11 @@
 //                   tile, and a row that does see one has it put into its output at the end
 // Weights are rounded to bf16 for the second product (V's type: the tensor cores take two
 // operands of one type): up to 2^-8 of each weight, at random, as the rounding of the
-// output.  l is the sum of the weights before that, so that lse has fp32's precision.
+// output.  With up to 32 query rows (kLowRows), where one warp of a stream's four has rows, what the rounding leaves out is a
+// second operand of half the columns: 2^-15 of each weight, as in the attentions over a step's selection.  (With it and
+// without: 16 whole caches 229 and 219 us, outputs off by 0.0016 and 0.0023, 0.0016 by their own rounding alone; with 40
+// rows 69 and 61; prompts 436 and 305, behind 62K 4.2 and 2.8 ms.)  l is the sum of the weights before
+// that, so that lse has fp32's precision.
 //
 // Work: with two row tiles an item is a pair of them, whole or by a range of tiles of keys (cut_of); items are
 // handed out one after another, the pairs of one KV head and range next to each other, so that the CTAs
@@ -48,6 +52,7 @@ constexpr int kInfo = 8;                             // records of K's tiles (a 
 constexpr uint32_t kTmem = 512;                      // S: 2 x 128 columns, O: 2 x 128
 constexpr int kSoftRegs = 208, kOtherRegs = 80;      // 256 * 208 + 128 * 80 <= 384 * 168 at launch
 constexpr float kHead = 8.f;                         // weights stay below 2^8
+constexpr int kLowRows = 32;                         // query rows of a tile whose weights have two parts
 
 struct Item {
   int unit, b, h0, t0, start, len;   // the unit's request and first query head
@@ -95,7 +100,6 @@ struct ExtendParams {
   WorkCounters w;
   bool wide;                  // rows of `out` begin at multiples of 32 bytes
   int mt;                     // tokens of an item
-  int pairs;                  // row tiles of an item: 1 or 2
 };
 
 // One (request, KV head) as the planning sees it.
@@ -256,6 +260,8 @@ __device__ __forceinline__ void join_rows(const Join &p, int join_w, int join_n)
   }
 }
 
+// kPairs: row tiles of an item.  kLow: the weights' second parts.
+template <int kPairs, bool kLow>
 __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ ExtendParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Misc &x = *reinterpret_cast<Misc *>(smem + kTiles);
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   if (tid == 0) x.pending = load_status(a.status);
   // groups of all units, or their tiles and costs (below 2^31): a warp's blocks of 32 units each
   const int units = a.B * a.Hkv;
-  const bool sliced = p.pairs == 1;
+  constexpr bool sliced = kPairs == 1;
   Unit few = {0, 0, 0, 0, 0};                              // a lane's unit, where there are no more than 32
   if (units <= 32 && lane < units && (warp == 0 || warp == 9)) few = load_unit(p, lane);
   {
@@ -562,10 +568,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         const Item &it = x.item[n & 1u];
         const int unit = it.unit;
         if (unit < 0) break;
-        const int nt = p.pairs == 2 ? max(it.c[0], it.c[1]) : it.c[0] + it.c[1];
+        const int nt = kPairs == 2 ? max(it.c[0], it.c[1]) : it.c[0] + it.c[1];
         const int64_t list = (int64_t)unit * a.umax;
         const int j0 = it.j0, ents = it.ents, pos_max = it.pos_max, pos_min = it.pos_min;
-        const bool two = p.pairs == 2 && it.c[1] > 0;
+        const bool two = kPairs == 2 && it.c[1] > 0;
         auto batch = [&](int j) {
           const int e = (j0 + j) * chunks + lane;
           if (e >= ents) return Entry{0, INT_MAX};
@@ -627,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         const Item &it = x.item[n & 1u];
         if (it.unit < 0) break;
         const int c0 = it.c[0], c1 = it.c[1], steps = max(c0, c1);
-        const int nt = p.pairs == 2 ? steps : c0 + c1;
+        const int nt = kPairs == 2 ? steps : c0 + c1;
         if (nt > 0) ok = wait_warp(q_full, nq++);
         for (int i = 0; ok && i <= steps && nt > 0; ++i) {
 #pragma unroll
@@ -635,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             const int cw = w ? c1 : c0;
             if (!ok) break;
             if (i > 0 && i - 1 < cw) {
-              const int tile = p.pairs == 2 ? i - 1 : 2 * (i - 1) + w;
+              const int tile = kPairs == 2 ? i - 1 : 2 * (i - 1) + w;
               const uint32_t t = t_base + tile, st = t % kV;
               ok = wait_warp(v_ok + 8 * st, t / kV);
 #pragma unroll
@@ -647,11 +653,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
                 if (elect_lane()) {
                   const uint64_t vb = v_desc + st * (kTileBytes / 16);
 #pragma unroll
-                  for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                  for (int ks = 4 * half; ks < 4 * half + 4; ++ks) {
                     tc_mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 8 * ks, vb + ks * (16 * 128 / 16), id_o,
                               i > 1 || ks > 0);
+                    if (kLow)
+                      tc_mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + 64 + 8 * ks, vb + ks * (16 * 128 / 16), id_o, 1);
+                  }
                   if (half) {
-                    if (p.pairs == 1 || w == 1 || i - 1 >= c1) tc_commit(v_free + 8 * st);
+                    if (kPairs == 1 || w == 1 || i - 1 >= c1) tc_commit(v_free + 8 * st);
                     if (i == cw) tc_commit(o_full + 8 * w);
                   }
                 }
@@ -661,13 +670,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               if (!ok) break;
             }
             if (i < cw) {
-              const int tile = p.pairs == 2 ? i : 2 * i + w;
+              const int tile = kPairs == 2 ? i : 2 * i + w;
               const uint32_t t = t_base + tile, st = t % kK;
               ok = wait_warp(k_full + 8 * st, t / kK);
               if (!ok) break;
               tc_fence_after();
               if (elect_lane()) {
-                const uint64_t qb = q_desc + (p.pairs == 2 ? w * (kTileBytes / 16) : 0);
+                const uint64_t qb = q_desc + (kPairs == 2 ? w * (kTileBytes / 16) : 0);
                 const uint64_t kb = k_desc + st * (kTileBytes / 16);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
@@ -676,8 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
                 }
                 mbar_arrive(s_full + 8 * w);     // (hands on the tile's record, which came with K)
                 tc_commit(s_full + 8 * w);
-                if (p.pairs == 1 || w == 1 || i >= c1) tc_commit(k_free + 8 * st);
-                if (tile == nt - 1 && (p.pairs == 1 || w == 1 || i >= c1)) tc_commit(q_free);
+                if (kPairs == 1 || w == 1 || i >= c1) tc_commit(k_free + 8 * st);
+                if (tile == nt - 1 && (kPairs == 1 || w == 1 || i >= c1)) tc_commit(q_free);
               }
               __syncwarp();
             }
@@ -699,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         if (!ok) break;
         const Item &it = x.item[n & 1u];
         if (it.unit < 0) break;
-        const int nt = p.pairs == 2 ? max(it.c[0], it.c[1]) : it.c[0] + it.c[1];
+        const int nt = kPairs == 2 ? max(it.c[0], it.c[1]) : it.c[0] + it.c[1];
         bool found = false;
         for (int j = 0; ok && j < nt; ++j, ++vt) {
           const uint32_t st = vt % kV;
@@ -780,15 +789,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       const int unit = it.unit;
       if (unit < 0) break;
       const int cw = it.c[w], parts = it.parts[w];
-      const int nt = p.pairs == 2 ? max(it.c[0], it.c[1]) : it.c[0] + it.c[1];
-      const int token = it.t0 + (p.pairs == 2 ? w * a.tt : 0) + tok;
+      const int nt = kPairs == 2 ? max(it.c[0], it.c[1]) : it.c[0] + it.c[1];
+      const int token = it.t0 + (kPairs == 2 ? w * a.tt : 0) + tok;
       const bool valid = r < rows_tile && token < it.len;
       const int pos = valid ? it.start + token : -1;
       float m = -INFINITY, l = 0.f;                        // reference (a score before the factor), sum of weights
       float sub = 0.f;                                     // the reference times the factor, negated
       bool far = false;
       for (int i = 0; i < cw; ++i) {
-        const uint32_t t = t_base + (p.pairs == 2 ? i : 2 * i + w);
+        const uint32_t t = t_base + (kPairs == 2 ? i : 2 * i + w);
         ok = wait_warp(s_full + 8 * w, ns);
         ++ns;
         if (!ok) break;
@@ -862,16 +871,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            uint32_t pk[16];
+            uint32_t pk[16], low[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float2 y = fma2(make_float2(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), make_float2(a.sl2, a.sl2),
                               make_float2(add, add));
               y.x = exp2_fast(y.x), y.y = exp2_fast(y.y);
               sum[e & 1] = add2(sum[e & 1], y);
-              pk[e] = bf16x2(y.x, y.y);
+              if (!kLow) {
+                pk[e] = bf16x2(y.x, y.y);
+              } else {
+                // the upper 16 bits, and what is left: never negative, and above 0 where the weight is, so that an
+                // infinity of V stays one
+                const uint32_t a0 = __float_as_uint(y.x), a1 = __float_as_uint(y.y);
+                pk[e] = __byte_perm(a0, a1, 0x7632);
+                const float2 cut = make_float2(-__uint_as_float(a0 & 0xFFFF0000u), -__uint_as_float(a1 & 0xFFFF0000u));
+                const float2 rest = fma2(y, make_float2(0x1p-20f, 0x1p-20f), add2(y, cut));
+                low[e] = bf16x2(rest.x, rest.y);
+              }
             }
             tmem_st16(s_at + 16 * h, pk);
+            if (kLow) tmem_st16(s_at + 64 + 16 * h, low);
             if (h == 1) {
               // the first 64 keys' product may begin
               tmem_wait_st();
@@ -900,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
         if (!ok) break;
         tc_fence_after();
       }
-      const bool both = p.pairs == 1 && it.c[1] > 0;       // the streams have sums of the same rows
+      const bool both = kPairs == 1 && it.c[1] > 0;       // the streams have sums of the same rows
       if (both && w == 1) {
         // stream 0 takes O out of this one's columns: it has the same lanes
         stat[r] = make_float2(m, l);
@@ -921,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           m = top, l = l * f0 + other.y * f1;
         }
         const int b = it.b, h0 = it.h0;
-        const int64_t slot = it.part + (p.pairs == 2 ? w : 0);
+        const int64_t slot = it.part + (kPairs == 2 ? w : 0);
         float *po = p.part_o + (slot * rows_tile + r) * kD;
         const int64_t row = ((int64_t)b * a.T + token) * a.Hq + h0 + head;
         uint16_t *dst = p.out + b * p.os[0] + token * p.os[1] + (h0 + head) * p.os[2];
@@ -996,13 +1016,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           if (!ok) break;
           if (quarter == 0 && lane == 0) {
             __threadfence();
-            int32_t *ctr = p.w.ctr + 2 + it.cut + (p.pairs == 2 ? w : 0);
+            int32_t *ctr = p.w.ctr + 2 + it.cut + (kPairs == 2 ? w : 0);
             if (atomicAdd(ctr, 1) == parts - 1) {
               // the last part: joined when the CTA is through with its items
               *ctr = 0;
               Task &k = x.task[atomicAdd(&x.tasks, 1)];
-              k.unit = unit, k.len = it.len, k.token = it.t0 + (p.pairs == 2 ? w * a.tt : 0);
-              k.parts = parts, k.first = it.part0 + (p.pairs == 2 ? w : 0);
+              k.unit = unit, k.len = it.len, k.token = it.t0 + (kPairs == 2 ? w * a.tt : 0);
+              k.parts = parts, k.first = it.part0 + (kPairs == 2 ? w : 0);
             }
             __threadfence();
           }
@@ -1019,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
       const Task &task = x.task[k];
       const int b = task.unit / a.Hkv, h0 = task.unit % a.Hkv * a.G;
       Join q;
-      q.part_o = p.part_o, q.part_ml = p.part_ml, q.first = task.first, q.pairs = p.pairs, q.parts = task.parts;
+      q.part_o = p.part_o, q.part_ml = p.part_ml, q.first = task.first, q.pairs = kPairs, q.parts = task.parts;
       q.rows = min(rows_tile, (task.len - task.token) * a.G), q.rows_tile = rows_tile, q.G = a.G, q.Hq = a.Hq;
       q.scale = a.scale, q.sl2 = a.sl2;
       q.out = p.out + b * p.os[0] + task.token * p.os[1] + h0 * p.os[2], q.os1 = p.os[1], q.os2 = p.os[2];
@@ -1083,10 +1103,11 @@ cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t stream) {
   p.part_o = e.parts;
   p.part_ml = reinterpret_cast<float2 *>(e.parts + s.slots * s.rows * kD);
   p.w = {e.ctr, kCtrPerCta * e.sm_count};
-  p.mt = s.mt, p.pairs = s.pairs;
-  cudaError_t r = set_dyn_smem((const void *)k_extend, kSmem);
+  p.mt = s.mt;
+  auto *kernel = s.pairs == 2 ? &k_extend<2, false> : (s.rows <= kLowRows ? &k_extend<1, true> : &k_extend<1, false>);
+  const cudaError_t r = set_dyn_smem((const void *)kernel, kSmem);
   if (r != cudaSuccess) return r;
-  return launch_k(k_extend, dim3(e.sm_count), dim3(kThreads), kSmem, stream, p);
+  return launch_k(kernel, dim3(e.sm_count), dim3(kThreads), kSmem, stream, p);
 }
 
 }  // namespace dd

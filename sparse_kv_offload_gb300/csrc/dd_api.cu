@@ -837,7 +837,7 @@ dd_status dd_extend_attn(dd_ctx *c, const dd_extend_args *e, dd_stream_t stream)
 
 int64_t dd_chunk_weights_workspace(const dd_ctx *c) {
   if (!c) return -1;
-  return dd::weights_workspace(c->dims.cs, c->sm_count);
+  return dd::weights_workspace(c->sm_count);
 }
 
 dd_status dd_chunk_weights(dd_ctx *c, const dd_weights_args *e, dd_stream_t stream) {

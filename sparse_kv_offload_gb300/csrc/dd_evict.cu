@@ -180,16 +180,14 @@ __global__ void __launch_bounds__(512, 2) k_evict(const EvictArgs a) {
       bound = s_low, shift = 0, ties = shared != rank;
       break;
     }
-    // (at most 16 bins a thread: there are 128 threads or more)
-    const int per = kBins / blockDim.x > 0 ? kBins / blockDim.x : 1, from = tid * per;
+    const int per = kBins / (int)blockDim.x, from = tid * per;   // (128, 256 or 512 threads)
     int sum = 0;
-    if (from < kBins)
-      for (int i = 0; i < per; ++i) sum += (int)hist[from + i];
+    for (int i = 0; i < per; ++i) sum += (int)hist[from + i];
     Counts t, mine = {0, 0, 0};
     const int incl = warp_incl_scan(sum);
     mine.a = __shfl_sync(0xffffffffu, incl, 31);
     uint32_t before = (uint32_t)(warp_prefix(mine, scratch, t, warp, lane, warps).a + incl - sum);
-    if (from < kBins && before < rank && rank <= before + (uint32_t)sum)
+    if (before < rank && rank <= before + (uint32_t)sum)
       for (int i = 0; i < per; ++i) {
         const uint32_t v = hist[from + i];
         if (before < rank && rank <= before + v) s_digit = from + i, s_rank = rank - before, s_count = v;

@@ -107,8 +107,6 @@ struct Unit {
   int cnt, start, len, groups, tiles;     // groups of mt tokens; tiles of keys that the last of them may see
 };
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (int)((unsigned)(a + b - 1) / (unsigned)b); }
-
 // entries that a token may see: chunk numbers ascend, so entry i is chunk i or a later one
 __device__ __forceinline__ int entry_bound(const PagesArgs &a, const Unit &u, int token) {
   return min(u.cnt, ((u.start + token) >> a.cs_log) + 1);
@@ -225,7 +223,7 @@ __device__ __forceinline__ void join_rows(const Join &p, int join_w, int join_n)
       if (q0 > 0) load(k0, q0);
       if (q0 % L == 0) {
         if (q0 > 0) ml = stats(k, q0 + lq);
-        f = exp2_fast((ml.x - ref) * p.sl2);
+        f = ex2_approx((ml.x - ref) * p.sl2);
         total += f * ml.y;
       }
 #pragma unroll
@@ -252,7 +250,7 @@ __device__ __forceinline__ void join_rows(const Join &p, int join_w, int join_n)
       const int64_t at = __shfl_sync(0xffffffffu, to, L * j);
       if (k0 + j < rows)
         *reinterpret_cast<uint2 *>(p.out + at + 4 * lane) =
-            make_uint2(bf16x2(acc[j].x * iv, acc[j].y * iv), bf16x2(acc[j].z * iv, acc[j].w * iv));
+            make_uint2(cvt_bf16x2(acc[j].x * iv, acc[j].y * iv), cvt_bf16x2(acc[j].z * iv, acc[j].w * iv));
     }
     if (p.lse && lq == 0 && k0 + lj < rows)
       p.lse[(int64_t)t * p.Hq + h] = total == 0.f ? -INFINITY : (top == -INFINITY ? NAN : top * p.scale + logf(total));
@@ -316,25 +314,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   const int rows_tile = a.tt * a.G;         // query rows of a tile
   const int chunks = kTileKeys / a.cs;      // of a tile
 
-  // The first wait that runs out (2 s) ends the CTA's work: the others give up with it.
-  volatile int *dead = &x.dead;
-  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity & 1u)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-      if (mbar_try_wait(bar, parity & 1u)) return true;
-      if ((it & 63u) == 0) {
-        if (*dead) return false;
-        if (globaltimer_ns() - t0 > 2000000000ull) {
-          *dead = 1;
-          set_status(a.raised, DD_ERR_TIMEOUT);
-          return false;
-        }
-      }
-    }
-  };
   auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, wait(bar, parity));
+    return __all_sync(0xffffffffu, wait_or_dead(bar, parity, &x.dead, a.raised));
   };
 
   // (with an error pending: nothing, but the counters below are left all the same)
@@ -840,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           // (also from -inf; not where both are; rows that are none hold anything and have no say)
           const bool up = valid && (mx - m) * a.sl2 > kHead;
           if (__any_sync(0xffffffffu, up)) {
-            const float f = up ? exp2_fast((m - mx) * a.sl2) : 1.f;
+            const float f = up ? ex2_approx((m - mx) * a.sl2) : 1.f;
             if (up) m = mx;
             l *= f;
             if (i > 0) {
@@ -876,10 +857,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
             for (int e = 0; e < 16; ++e) {
               float2 y = fma2(make_float2(s[32 * h + 2 * e], s[32 * h + 2 * e + 1]), make_float2(a.sl2, a.sl2),
                               make_float2(add, add));
-              y.x = exp2_fast(y.x), y.y = exp2_fast(y.y);
+              y.x = ex2_approx(y.x), y.y = ex2_approx(y.y);
               sum[e & 1] = add2(sum[e & 1], y);
               if (!kLow) {
-                pk[e] = bf16x2(y.x, y.y);
+                pk[e] = cvt_bf16x2(y.x, y.y);
               } else {
                 // the upper 16 bits, and what is left: never negative, and above 0 where the weight is, so that an
                 // infinity of V stays one
@@ -887,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
                 pk[e] = __byte_perm(a0, a1, 0x7632);
                 const float2 cut = make_float2(-__uint_as_float(a0 & 0xFFFF0000u), -__uint_as_float(a1 & 0xFFFF0000u));
                 const float2 rest = fma2(y, make_float2(0x1p-20f, 0x1p-20f), add2(y, cut));
-                low[e] = bf16x2(rest.x, rest.y);
+                low[e] = cvt_bf16x2(rest.x, rest.y);
               }
             }
             tmem_st16(s_at + 16 * h, pk);
@@ -937,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
           tc_fence_after();
           const float2 other = stat[r];
           const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
-          f0 = exp2_fast((m - ref) * a.sl2), f1 = exp2_fast((other.x - ref) * a.sl2);
+          f0 = ex2_approx((m - ref) * a.sl2), f1 = ex2_approx((other.x - ref) * a.sl2);
           m = top, l = l * f0 + other.y * f1;
         }
         const int b = it.b, h0 = it.h0;
@@ -970,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
               if (parts == 1) {
                 uint32_t v[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = bf16x2(o[2 * e], o[2 * e + 1]);
+                for (int e = 0; e < 16; ++e) v[e] = cvt_bf16x2(o[2 * e], o[2 * e + 1]);
                 if (p.wide) {
                   store32(dst + 32 * h, v), store32(dst + 32 * h + 16, v + 8);
                 } else {

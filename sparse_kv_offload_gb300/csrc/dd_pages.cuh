@@ -7,7 +7,7 @@
 
 #include <limits.h>
 
-#include "dd_tc.cuh"
+#include "dd_attn.cuh"
 
 namespace dd {
 
@@ -118,6 +118,25 @@ __device__ __forceinline__ void load_chunk(const CUtensorMap &hot, const CUtenso
   const bool staged = pos != INT_MAX && slot < 0;
   const int64_t row = pos == INT_MAX ? (a.hot_slots > 0 ? a.hot_slots : 1) : (staged ? -(int64_t)slot - 1 : slot);
   tma_load_2d(dst + half * kTileHalfBytes, staged ? &far : &hot, 64 * half, (int)row << a.cs_log, bar);
+}
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (int)((unsigned)(a + b - 1) / (unsigned)b); }
+
+// A CTA's waits: the first that runs out (2 s) ends the CTA's work, and the others give up with it.
+__device__ __forceinline__ bool wait_or_dead(uint32_t bar, uint32_t parity, volatile int *dead, int32_t *raised) {
+  if (mbar_try_wait(bar, parity & 1u)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity & 1u)) return true;
+    if ((it & 63u) == 0) {
+      if (*dead) return false;
+      if (globaltimer_ns() - t0 > 2000000000ull) {
+        *dead = 1;
+        set_status(raised, DD_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
 }
 
 // One thread of a converged warp, the same one every time.
@@ -231,18 +250,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // The context's counters for these kernels, zero between launches: items handed out,
 // CTAs done, then the parts that have arrived of each row tile that is cut.
 struct WorkCounters {
@@ -310,7 +317,7 @@ struct WeightsArgs {
   const void *dummy;
   int sm_count;
 };
-int64_t weights_workspace(int cs, int sm_count);
+int64_t weights_workspace(int sm_count);
 cudaError_t launch_weights(const WeightsArgs &a, cudaStream_t s);
 
 struct EvictArgs {

@@ -79,8 +79,6 @@ struct Unit {
   int cnt, start, len, tok0, pairs, rows;     // pairs of tiles of keys, tiles of query rows
 };
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
 __device__ __forceinline__ Unit load_unit(const WeightsParams &p, int u) {
   Unit r;
   const Request q = load_request(p.a, u / p.a.Hkv);
@@ -160,24 +158,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
   const bool pending = x.pending != 0;
   const uint32_t tmem = x.tmem;
 
-  volatile int *dead = &x.dead;
-  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity & 1u)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1;; ++it) {
-      if (mbar_try_wait(bar, parity & 1u)) return true;
-      if ((it & 63u) == 0) {
-        if (*dead) return false;
-        if (globaltimer_ns() - t0 > 2000000000ull) {
-          *dead = 1;
-          set_status(a.raised, DD_ERR_TIMEOUT);
-          return false;
-        }
-      }
-    }
-  };
   auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, wait(bar, parity));
+    return __all_sync(0xffffffffu, wait_or_dead(bar, parity, &x.dead, a.raised));
   };
   // whether a step of a pair takes a new tile of queries, and whether it is the tile's last
   auto new_q = [](int keep) { return keep == 0 || (keep & 1); };
@@ -481,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
             const float4 z = *reinterpret_cast<const float4 *>(ls + 32 * h + 4 * e);
             const float2 y0 = fma2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(a.sl2, a.sl2), make_float2(z.x, z.y));
             const float2 y1 = fma2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(a.sl2, a.sl2), make_float2(z.z, z.w));
-            y[4 * e] = exp2_fast(y0.x), y[4 * e + 1] = exp2_fast(y0.y);
-            y[4 * e + 2] = exp2_fast(y1.x), y[4 * e + 3] = exp2_fast(y1.y);
+            y[4 * e] = ex2_approx(y0.x), y[4 * e + 1] = ex2_approx(y0.y);
+            y[4 * e + 2] = ex2_approx(y1.x), y[4 * e + 3] = ex2_approx(y1.y);
           }
         };
         if (whole) {
@@ -566,8 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
 
 }  // namespace
 
-int64_t weights_workspace(int cs, int sm_count) {
-  (void)cs;
+int64_t weights_workspace(int sm_count) {
   return (int64_t)2 * kItemsPerCta * sm_count * 16 * 4;
 }
 

@@ -576,7 +576,8 @@ typedef struct {
  * A token that sees no row has zeros and lse -inf.  Rows that it does not see do not reach it, whatever
  * they hold (NaN and infinities among it).  A score of +inf or NaN makes the row NaN, one of -inf has no
  * weight.  Outputs of padding are left as they were.  Weights are rounded for their product with V, at random:
- * by up to 2^-15 of each where T*G <= 32, by up to 2^-8 (to bf16) beyond; sums and statistics are fp32.
+ * by up to 2^-15 of each where T*G <= 32, by up to 2^-8 (to bf16) beyond; sums and statistics are fp32 (weights
+ * in them are below 2^8: values of V below 2^100 overflow none).
  * workspace: dd_extend_attn_workspace(ctx, T) bytes of device memory, 32-byte aligned, which calls on
  * one stream may share; it holds nothing between calls.  out must not overlap the inputs.
  * A call that reports DD_ERR_DEVICE_CHECK leaves each (request, KV head)'s outputs as its result without

@@ -13,7 +13,7 @@
 // a thread a query row; while one stream's softmax runs, the other's products do.  With
 // more than 128 query rows per KV head the streams are two row tiles over the same keys; with
 // fewer they are the even and the odd tiles of keys of one row tile, joined at the end.
-//   warps 0-3, 4-7  softmax of the streams: S out of tensor memory, weights as bf16 back in
+//   warps 0-3, 4-7  softmax of the streams: S out of tensor memory, weights back in
 //                   its place, O rescaled when a reference moves, outputs
 //   warp 8          S = Q K^T, O += P V (P straight from tensor memory)
 //   warp 9          hands out the work and brings K's tiles, warp 10 Q's and V's
@@ -22,11 +22,11 @@
 //                   tile, and a row that does see one has it put into its output at the end
 // Weights are rounded to bf16 for the second product (V's type: the tensor cores take two
 // operands of one type): up to 2^-8 of each weight, at random, as the rounding of the
-// output.  With up to 32 query rows (kLowRows), where one warp of a stream's four has rows, what the rounding leaves out is a
-// second operand of half the columns: 2^-15 of each weight, as in the attentions over a step's selection.  (With it and
-// without: 16 whole caches 229 and 219 us, outputs off by 0.0016 and 0.0023, 0.0016 by their own rounding alone; with 40
-// rows 69 and 61; prompts 436 and 305, behind 62K 4.2 and 2.8 ms.)  l is the sum of the weights before
-// that, so that lse has fp32's precision.
+// output.  With up to 32 query rows (kLowRows), where one warp of a stream's four has rows, what the rounding
+// leaves out is a second operand in the other half of S's columns: 2^-15 of each weight, much as the attentions
+// over a step's selection have it.  With it and without: 16 whole caches 229 and 219 us, outputs off by 0.0016 and
+// 0.0023 (relative L2; 0.0016 is their own rounding); 40 query rows 69 and 61; prompts 436 and 305; 2,048
+// tokens behind 62K 4.2 and 2.8 ms.  l is the sum of the weights before that, so that lse has fp32's precision.
 //
 // Work: with two row tiles an item is a pair of them, whole or by a range of tiles of keys (cut_of); items are
 // handed out one after another, the pairs of one KV head and range next to each other, so that the CTAs
@@ -34,11 +34,11 @@
 // an equal slice of all units' tiles, as nothing is read twice and the bytes bound it (decode 256 us, 435 with
 // ranges).  A row tile that is cut has its parts joined by whoever finishes last, in the ranges' order.
 //
-// What bounds it: HBM with one token a request (16 whole caches of up to 32K: 245 us, 6,150 GB/s); with many, the
-// tensor cores and beside them the issue slots of the softmax (2,048 tokens behind 62K others, 64 heads:
-// 2.7 ms, 1,560-1,610 TFLOP/s; a step of two tiles takes 3,000 cycles, its products 2,500 at the rate of a large product).  Short items pay for
-// their ends, some 12,000 cycles each: the last weights, O out of tensor memory, places and stores (first 2,048
-// tokens of four prompts, 64 heads: 315 us, 870 TFLOP/s).  The softmax's loop needs nearly all of its registers:
+// What bounds it: HBM with one token a request (16 whole caches of up to 32K: 222 to 253 us by their lengths, 6,300
+// GB/s); with many, the tensor cores and beside them the issue slots of the softmax (2,048 tokens behind 62K
+// others, 64 heads: 2.81 ms, 1,540 TFLOP/s; a step of two tiles takes 3,000 cycles, its products 2,500 at the rate
+// of a large product).  Short items pay for their ends, some 12,000 cycles each: the last weights, O out of tensor
+// memory, places and stores (first 2,048 tokens of four prompts, 64 heads: 304 us, 906 TFLOP/s).  The softmax's loop needs nearly all of its registers:
 // anything that the compiler keeps across it, an item's end that holds 64 columns at once among it, costs 20 to 60%.
 #include "dd_pages.cuh"
 

@@ -18,11 +18,13 @@
 // queries stream past a pair.  Where the pairs alone would leave CTAs idle the rows are cut too, and
 // a pair's parts (16 sums at most) are added up in order by whoever finishes last.
 //
-// What bounds it: with many query rows the exponentials, 16 a clock and SM (2 requests, 2,048 tokens, 64 heads, 16K of
-// context: 1.11 ms, 93% of that rate; a quarter of them as polynomials on the FMA pipe: 1.32).  With two tiles of
-// query rows a pair its ends count, some 1,400 of 5,470 cycles (last 32 tokens of 8 prompts, 64 heads: 130 us, 60%).  With
-// one token a request HBM (16 whole caches of up to 32K in chunks of 16: 126 us, 5,960 GB/s; 130 with two pairs
-// on the way; 189 as items; 145 while a list's entries were looked at right behind their loads, not a batch later).
+// What bounds it: with many query rows no pipe, but what two warps a scheduler can have on the way: a load out of tensor
+// memory, multiply-adds, exponentials and additions follow one another (2 requests, 2,048 tokens, 64 heads, 16K of
+// context: 1.02 ms, 12.5 scores a clock and SM of the 32 exponentials that ex2.approx alone runs at; XU and tensor pipe 42%
+// each on a smaller case; a quarter of the exponentials as polynomials on the FMA pipe cost 19%).  With two tiles of
+// query rows a pair its ends count as well (last 32 tokens of 8 prompts, 64 heads: 97 to 122 us by lengths, 11.3 a clock).
+// With one token a request HBM (16 whole caches of up to 32K in chunks of 16: 113 to 129 us by lengths, 6,200 GB/s;
+// 3% more with two pairs on the way, 50% as items, 15% with a list's entries looked at right behind their loads).
 #include "dd_pages.cuh"
 
 namespace dd {

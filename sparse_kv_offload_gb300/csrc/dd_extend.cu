@@ -24,7 +24,7 @@
 // operands of one type): up to 2^-8 of each weight, at random, as the rounding of the
 // output.  With up to 32 query rows (kLowRows), where one warp of a stream's four has rows, what the rounding
 // leaves out is a second operand in the other half of S's columns: 2^-15 of each weight, much as the attentions
-// over a step's selection have it.  With it and without: 16 whole caches 229 and 219 us, outputs off by 0.0016 and
+// over a step's selection have it.  With it and without: 16 whole caches 222 and 216 us, outputs off by 0.0016 and
 // 0.0023 (relative L2; 0.0016 is their own rounding); 40 query rows 69 and 61; prompts 436 and 305; 2,048
 // tokens behind 62K 4.2 and 2.8 ms.  l is the sum of the weights before that, so that lse has fp32's precision.
 //
@@ -34,7 +34,7 @@
 // an equal slice of all units' tiles, as nothing is read twice and the bytes bound it (decode 256 us, 435 with
 // ranges).  A row tile that is cut has its parts joined by whoever finishes last, in the ranges' order.
 //
-// What bounds it: HBM with one token a request (16 whole caches of up to 32K: 222 to 253 us by their lengths, 6,300
+// What bounds it: HBM with one token a request (16 whole caches of up to 32K: 216 to 245 us by their lengths, 6,500
 // GB/s); with many, the tensor cores and beside them the issue slots of the softmax (2,048 tokens behind 62K
 // others, 64 heads: 2.81 ms, 1,540 TFLOP/s; a step of two tiles takes 3,000 cycles, its products 2,500 at the rate
 // of a large product).  Short items pay for their ends, some 12,000 cycles each: the last weights, O out of tensor
@@ -47,7 +47,7 @@ namespace dd {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kK = 3, kV = 2;                        // tiles of K and of V on the way
+constexpr int kK = 3;                                // tiles of K on the way
 constexpr int kInfo = 8;                             // records of K's tiles (a softmax warp is at most kK + 2 behind)
 constexpr uint32_t kTmem = 512;                      // S: 2 x 128 columns, O: 2 x 128
 constexpr int kSoftRegs = 208, kOtherRegs = 80;      // 256 * 208 + 128 * 80 <= 384 * 168 at launch
@@ -77,7 +77,7 @@ struct Misc {
   Item item[2];
   int pos[kInfo][8];          // positions of the first rows of a tile's chunks
   int whole[kInfo];           // every query row sees the whole tile
-  int vpos[kV][8], vwhole[kV];   // the same of V's tiles
+  int vpos[3][8], vwhole[3];  // the same of V's tiles
   int bad[3][128];            // lowest position of a NaN, +inf, -inf in each column of V
   Task task[kTasks];
   uint32_t sum[kThreads / 32], block[32];   // units' groups, or tiles and costs: of each warp, of the first blocks of 32
@@ -85,7 +85,7 @@ struct Misc {
   uint32_t tmem;
 };
 
-constexpr size_t kTiles = (size_t)(2 + kK + kV) * kTileBytes;
+constexpr size_t kTiles = (size_t)(2 + kK + 2) * kTileBytes;   // queries of two row tiles, or of one and a third tile of V
 constexpr size_t kSmem = kTiles + sizeof(Misc);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
 
@@ -265,7 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
   Misc &x = *reinterpret_cast<Misc *>(smem + kTiles);
   const PagesArgs &a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const uint32_t q0 = smem_u32(smem), k0 = q0 + 2 * kTileBytes, v0 = k0 + kK * kTileBytes;
+  // tiles of V on the way: with few rows a tile is held longest (its scores and weights come first), and the second
+  // row tile's place is free (16 whole caches: 222 us with three, 226 with two)
+  constexpr int kV = kLow ? 3 : 2;
+  const uint32_t q0 = smem_u32(smem), k0 = q0 + (kLow ? 1 + kV : 2) * kTileBytes;
+  const uint32_t v0 = kLow ? q0 + kTileBytes : k0 + kK * kTileBytes;
   const uint32_t bars = smem_u32(x.bars);
   const uint32_t k_full = bars, k_free = k_full + 8 * kK, v_full = k_free + 8 * kK, v_ok = v_full + 8 * kV,
                  v_free = v_ok + 8 * kV, q_full = v_free + 8 * kV, q_free = q_full + 8, s_full = q_free + 8,
@@ -761,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend(const __grid_constant__ 
     const int tok = r / a.G, head = r % a.G;
     const bool some = 32 * quarter < rows_tile;            // of this warp's rows are query rows
     uint32_t ns = 0, no = 0, n_both = 0, n_parts = 0, t_base = 0;
-    float2 *stat = reinterpret_cast<float2 *>(smem + kTileBytes);    // (one row tile leaves the second's queries' place free)
+    // (one row tile leaves the second's queries' place free, few rows their own tile's later ones)
+    float2 *stat = reinterpret_cast<float2 *>(smem + (kLow ? 64 * 128 : kTileBytes));
     bool ok = true;
     for (uint32_t n = 0; ok && !pending; ++n) {
       ok = wait_warp(item_full + 8 * (n & 1u), n >> 1);

@@ -20,10 +20,10 @@
 //
 // What bounds it: with many query rows no pipe, but what two warps a scheduler can have on the way: a load out of tensor
 // memory, multiply-adds, exponentials and additions follow one another (2 requests, 2,048 tokens, 64 heads, 16K of
-// context: 1.02 ms, 12.5 scores a clock and SM of the 32 exponentials that ex2.approx alone runs at; XU and tensor pipe 42%
+// context: 1.03 ms, 12.4 scores a clock and SM of the 32 exponentials that ex2.approx alone runs at; XU and tensor pipe 42%
 // each on a smaller case; a quarter of the exponentials as polynomials on the FMA pipe cost 19%).  With two tiles of
-// query rows a pair its ends count as well (last 32 tokens of 8 prompts, 64 heads: 97 to 122 us by lengths, 11.3 a clock).
-// With one token a request HBM (16 whole caches of up to 32K in chunks of 16: 113 to 129 us by lengths, 6,200 GB/s;
+// query rows a pair its ends count as well (last 32 tokens of 8 prompts, 64 heads: 98 to 123 us by lengths, 11.2 a clock).
+// With one token a request HBM (16 whole caches of up to 32K in chunks of 16: 111 to 126 us by lengths, 6,300 GB/s;
 // 3% more with two pairs on the way, 50% as items, 15% with a list's entries looked at right behind their loads).
 #include "dd_pages.cuh"
 
@@ -455,25 +455,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
         float s[2][32], y[32];
         tmem_ld32(at, s[0]);
         // (two loops: with the choice by blocks inside one, 2,048 tokens of 64 heads took 1,156 us, so 1,024)
-        auto block = [&](int h) {
+        auto fetched = [&](int h) {
           tmem_wait_ld();
           tmem_ready(s[h & 1]);
           if (h < 3 && 32 * h + 32 < cols) tmem_ld32(at + 32 * h + 32, s[(h + 1) & 1]);
+        };
+        // the weights of columns 32 h + 4 e and three more
+        auto four = [&](int h, int e) {
           const float *v = s[h & 1];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 z = *reinterpret_cast<const float4 *>(ls + 32 * h + 4 * e);
-            const float2 y0 = fma2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(a.sl2, a.sl2), make_float2(z.x, z.y));
-            const float2 y1 = fma2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(a.sl2, a.sl2), make_float2(z.z, z.w));
-            y[4 * e] = ex2_approx(y0.x), y[4 * e + 1] = ex2_approx(y0.y);
-            y[4 * e + 2] = ex2_approx(y1.x), y[4 * e + 3] = ex2_approx(y1.y);
-          }
+          const float4 z = *reinterpret_cast<const float4 *>(ls + 32 * h + 4 * e);
+          const float2 y0 = fma2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(a.sl2, a.sl2), make_float2(z.x, z.y));
+          const float2 y1 = fma2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(a.sl2, a.sl2), make_float2(z.z, z.w));
+          y[4 * e] = ex2_approx(y0.x), y[4 * e + 1] = ex2_approx(y0.y);
+          y[4 * e + 2] = ex2_approx(y1.x), y[4 * e + 3] = ex2_approx(y1.y);
         };
         if (whole) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             if (32 * h >= cols) break;
-            block(h);
+            fetched(h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) four(h, e);
 #pragma unroll
             for (int e = 0; e < 16; ++e) sum[e & 1] = add2(sum[e & 1], make_float2(y[2 * e], y[2 * e + 1]));
           }
@@ -481,11 +483,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_weights(const __grid_constant__
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             if (32 * h >= cols) break;
-            block(h);
+            fetched(h);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) y[e] = 32 * h + e >= lo && 32 * h + e < cols ? y[e] : 0.f;
+            for (int e = 0; e < 8; ++e) {
+              if (32 * h + 4 * e >= cols) break;
+              four(h, e);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sum[e & 1] = add2(sum[e & 1], make_float2(y[2 * e], y[2 * e + 1]));
+              for (int k = 4 * e; k < 4 * e + 4; ++k) y[k] = 32 * h + k >= lo && 32 * h + k < cols ? y[k] : 0.f;
+              sum[0] = add2(sum[0], make_float2(y[4 * e], y[4 * e + 1]));
+              sum[1] = add2(sum[1], make_float2(y[4 * e + 2], y[4 * e + 3]));
+            }
           }
         }
         tc_fence_before();
